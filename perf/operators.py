@@ -1,0 +1,480 @@
+"""Cases of the 8-bit paged KV cache: appending with position rotation, single-token attention and causal
+attention of many new tokens, both with an optional sliding window and visible first tokens.
+
+``own`` false: the operators in plain torch operations; true: the library's calls (online_kv_cache_02_gb300.tq).
+A page holds 16 tokens; a block is one KV head of one page, e4m3 codes with a power-of-two scale.
+"""
+
+import functools
+import math
+
+import torch
+
+own = False
+
+PAGE = 16
+E_MIN, E_MAX = -100, 119
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ---------------------------------------------------------------------------
+# cases
+# ---------------------------------------------------------------------------
+def _case(op, dtype, batch, heads, kv_heads, d, n_new, len_lo, len_hi, **more):
+    c = dict(op=op, dtype=dtype, batch=batch, heads=heads, kv_heads=kv_heads, d=d, n_new=n_new, len_lo=len_lo,
+             len_hi=len_hi)
+    if op == "append":
+        c.update(rot=d, axes=1, interleaved=False, fused=True, ragged=False)
+    else:
+        c.update(window=0, sinks=0, ragged=False)
+    c.update(more)
+    return c
+
+
+def listed():
+    return [
+        # a decode step's new tokens: 16 sequences in mid page, K, V and Q as slices of one fused projection
+        dict(_case("append", "bf16", 16, 32, 8, 128, 1, 900, 5100), name="append_step"),
+        # a prefill's tokens, eight prompts at once
+        dict(_case("append", "bf16", 8, 32, 8, 128, 4096, 0, 0), name="append_prefill"),
+        # image and text tokens with three-axis positions, fp32 activations, prompts of different lengths
+        # appended behind earlier ones
+        dict(_case("append", "f32", 3, 28, 4, 128, 777, 5, 100, axes=3, ragged=True, fused=False), name="append_axes"),
+        # one short conversation: the latency of the call
+        dict(_case("decode", "bf16", 1, 32, 8, 128, 1, 1000, 1000), name="decode_single"),
+        # a long-context batch: bandwidth
+        dict(_case("decode", "bf16", 16, 32, 8, 128, 1, 32768, 32768), name="decode_long"),
+        # continuous batching: many sequences of different lengths
+        dict(_case("decode", "bf16", 64, 28, 4, 128, 1, 1024, 8192), name="decode_ragged"),
+        # a sliding-window layer at the same context, four first tokens visible
+        dict(_case("decode", "bf16", 16, 32, 8, 128, 1, 32768, 32768, window=4096, sinks=4), name="decode_window"),
+        # fp32 activations, a small head dimension, odd lengths
+        dict(_case("decode", "f32", 7, 16, 8, 64, 1, 3001, 9001), name="decode_f32"),
+        # verification of five drafted tokens per sequence
+        dict(_case("causal", "bf16", 16, 32, 8, 128, 5, 2000, 8000), name="causal_draft"),
+        # a whole prompt
+        dict(_case("causal", "bf16", 1, 32, 8, 128, 8192, 0, 0), name="causal_prompt"),
+        # a chunk of a long prompt behind what is cached
+        dict(_case("causal", "bf16", 2, 32, 8, 128, 1024, 15000, 30000, ragged=True), name="causal_chunk"),
+        # prompts of different lengths through a sliding-window layer
+        dict(_case("causal", "bf16", 3, 28, 4, 128, 4000, 0, 700, window=1024, sinks=16, ragged=True),
+             name="causal_window"),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["append", "decode", "causal"])
+    dtype = rng.choice(["bf16", "bf16", "bf16", "f32"])
+    heads, kv_heads = rng.choice([(32, 8), (28, 4), (8, 1), (16, 8), (12, 12), (40, 8)])
+    d = rng.choice([128, 128, 128, 64, 256])
+    per = kv_heads * d
+    if op == "append":
+        n_new = _log_int(rng, 1, 4096)
+        batch = min(_log_int(rng, 1, 64), max(1, (8 * 4096 * 48 * 128) // (n_new * (heads + 2 * kv_heads) * d)))
+        rot = rng.choice([d, d, d // 2])
+        lo = rng.randrange(0, 3000)
+        return _case("append", dtype, batch, heads, kv_heads, d, n_new, lo, lo + rng.randrange(0, 200), rot=rot,
+                     axes=rng.choice([1, 1, 2, 3]), interleaved=rng.random() < 0.3, fused=rng.random() < 0.5,
+                     ragged=rng.random() < 0.5)
+    windowed = rng.random() < 0.4
+    more = dict(window=_log_int(rng, 64, 4096), sinks=rng.choice([0, 4, 17])) if windowed else {}
+    if op == "decode":
+        hi = _log_int(rng, 100, 60000)
+        batch = min(_log_int(rng, 1, 64), max(1, (16 * 32768 * 8 * 128) // (hi * per)))
+        return _case("decode", dtype, batch, heads, kv_heads, d, 1, max(1, hi // rng.choice([1, 2, 8])), hi, **more)
+    n_new = _log_int(rng, 2, 4000)
+    most = (1 << 27) if dtype == "bf16" else (1 << 25)     # (query, key) pairs times heads times d / 128
+    room = max(16, most * 128 // (n_new * heads * d))
+    batch = min(_log_int(rng, 1, 16), max(1, room // (n_new + 64)))
+    hi = min(_log_int(rng, 16, 20000), max(16, room // batch))
+    return _case("causal", dtype, batch, heads, kv_heads, d, n_new, hi // rng.choice([1, 3]), hi,
+                 ragged=rng.random() < 0.5, **more)
+
+
+def _lengths(case):
+    """Cached tokens before the call (for decode: with the query's own token) and new tokens, per sequence."""
+    n = case["batch"]
+    lo, hi = case["len_lo"], case["len_hi"]
+    order = [(5 * i + 3) % n if n % 5 else i for i in range(n)]
+    cached = [lo + (hi - lo) * i // max(1, n - 1) if n > 1 else hi for i in order]
+    new = [case["n_new"]] * n
+    if case["ragged"]:
+        new = [max(1, case["n_new"] - (case["n_new"] * b) // (2 * n)) for b in range(n)]
+    return cached, new
+
+
+def _visible(p, case):
+    """Keys that the query at position p sees."""
+    w, s = case["window"], case["sinks"]
+    return p + 1 if not w or p < w else w + min(s, p + 1 - w)
+
+
+def work(case):
+    d, hq, h = case["d"], case["heads"], case["kv_heads"]
+    e = 2 if case["dtype"] == "bf16" else 4
+    cached, new = _lengths(case)
+    if case["op"] == "append":
+        n = sum(new)
+        pages = sum((c + t + PAGE - 1) // PAGE - c // PAGE for c, t in zip(cached, new))
+        return {"bytes": n * (d * (hq + 2 * h) * e + d * (2 * h + hq * e) + 4 * case["rot"]) + 8 * h * pages,
+                "flops": 3 * n * case["rot"] * (hq + h) + 2 * n * 2 * h * d}
+    if case["op"] == "decode":
+        keys = sum(_visible(c - 1, case) for c in cached)
+        pairs, rows = keys, len(cached)
+    else:
+        pairs = keys = rows = 0
+        for c, t in zip(cached, new):
+            if not case["window"]:
+                pairs += t * c + t * (t + 1) // 2
+                keys += c + t
+            else:
+                pairs += sum(_visible(p, case) for p in range(c, c + t))
+                first = max(0, c + 1 - case["window"])
+                keys += c + t - first + min(first, case["sinks"])
+            rows += t
+    return {"bytes": 2 * keys * h * d + 8 * h * keys // PAGE + 2 * rows * hq * d * e, "flops": 4 * pairs * hq * d}
+
+
+# ---------------------------------------------------------------------------
+# inputs
+# ---------------------------------------------------------------------------
+def _block_exponent(amax):
+    """Smallest e with amax <= 448 * 2^e, kept in [E_MIN, E_MAX]."""
+    m, x = torch.frexp(amax)
+    e = x - 9 + (m > 0.875).int()
+    return torch.where(amax > 0, e, torch.full_like(e, E_MIN)).clamp(E_MIN, E_MAX)
+
+
+def _round_e4m3(x):
+    """fp64 values to the nearest e4m3 value (ties to even), at most 448 in size."""
+    _, ex = torch.frexp(x)
+    step = torch.exp2((ex - 1).clamp(min=-6).double() - 3)
+    return (torch.round(x / step) * step).clamp(-448.0, 448.0)
+
+
+def _cached_pages(gen, pages, h, d, outliers):
+    """A pool of filled blocks: codes [pages][h][16][d] and scales [pages][h]."""
+    codes = torch.empty(pages, h, PAGE, d, dtype=torch.float8_e4m3fn, device="cuda")
+    scale = torch.empty(pages, h, device="cuda")
+    for p in range(0, pages, 16384):
+        n = min(16384, pages - p)
+        x = torch.randn(n, h, PAGE, d, generator=gen, device="cuda")
+        x *= torch.exp2(torch.randint(-2, 2, (n, h, 1, 1), generator=gen, device="cuda").float())
+        x[..., :outliers] *= 4
+        e = _block_exponent(x.abs().amax(dim=(2, 3)))
+        s = torch.exp2(e.float())
+        codes[p:p + n] = (x / s[..., None, None]).to(torch.float8_e4m3fn)
+        scale[p:p + n] = s
+    return codes, scale
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    dt, d, hq, h = DTYPES[case["dtype"]], case["d"], case["heads"], case["kv_heads"]
+    b, n = case["batch"], case["n_new"]
+    cached, new = _lengths(case)
+    total = [c + (t if case["op"] != "decode" else 0) for c, t in zip(cached, new)]
+    maxp = max(1, (max(total) + PAGE - 1) // PAGE)
+    need = [(t + PAGE - 1) // PAGE for t in total]
+    pool = sum(need) + 3
+    ids = torch.randperm(pool, generator=gen, device="cuda").int()
+    table = torch.zeros(b, maxp, dtype=torch.int32, device="cuda")
+    at = 0
+    for i, k in enumerate(need):
+        table[i, :k] = ids[at:at + k]
+        at += k
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    kc, ks = _cached_pages(gen, pool, h, d, 4)
+    vc, vs = _cached_pages(gen, pool, h, d, 0)
+    st = dict(case=case, dtype=dt, kc=kc, vc=vc, ks=ks, vs=vs, table=table, pool=pool, maxp=maxp, max_len=max(total),
+              cached=ints(cached), new=ints(new))
+    if case["op"] == "append":
+        if case["fused"]:
+            qkv = torch.randn(b, n, (hq + 2 * h) * d, generator=gen, device="cuda").to(dt)
+            q, k, v = (x.unflatten(-1, (-1, d)) for x in qkv.split([hq * d, h * d, h * d], dim=-1))
+        else:
+            q, k, v = (torch.randn(b, n, x, d, generator=gen, device="cuda").to(dt) for x in (hq, h, h))
+        k[..., :4] *= 4
+        pairs, axes = case["rot"] // 2, case["axes"]
+        sections = [pairs // axes + (1 if a < pairs % axes else 0) for a in range(axes)]
+        pos = st["cached"][:, None] + torch.arange(n, device="cuda", dtype=torch.int32)[None]
+        if axes > 1:      # time advances slowly, height and width run over a grid
+            pos = torch.stack([pos // 64 if a == 0 else pos // 8 % 8 if a == 1 else pos % 8 for a in range(axes)])
+        max_pos = max(total) + 8
+        freq = 500000.0 ** (-torch.arange(pairs, device="cuda", dtype=torch.float64) / pairs)
+        ang = torch.arange(max_pos, device="cuda", dtype=torch.float64)[:, None] * freq
+        st.update(q=q, k=k, v=v, sections=sections, pos=pos.int().contiguous() if axes > 1 else None, max_pos=max_pos,
+                  table_cs=torch.cat([ang.cos(), ang.sin()], dim=1).float(),
+                  q_out=torch.zeros(b, n, hq, d, dtype=dt, device="cuda"))
+        return st
+    shape = (b, hq, d) if case["op"] == "decode" else (b, n, hq, d)
+    st["q"] = torch.randn(shape, generator=gen, device="cuda").to(dt)
+    st["out"] = torch.zeros(shape, dtype=dt, device="cuda")
+    return st
+
+
+# ---------------------------------------------------------------------------
+# the library's calls
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=None)
+def _handle(d):
+    from online_kv_cache_02_gb300 import tq
+    return tq, tq.tq_create(d, 3, 128, 0)
+
+
+def _plan(st):
+    """What a program keeps beside its cache: the library's descriptors and a workspace."""
+    if "plan" not in st:
+        c = st["case"]
+        tq, ctx = _handle(c["d"])
+        code = tq.TQ_BF16 if c["dtype"] == "bf16" else tq.TQ_F32
+        cache = tq.make_kv8_cache(st["kc"], st["vc"], st["ks"], st["vs"], st["table"], st["maxp"], st["pool"],
+                                  c["kv_heads"])
+        rope, ws, size = None, None, 0
+        if c["op"] == "append":
+            rope = tq.make_rope(st["table_cs"], st["max_pos"], c["rot"], c["interleaved"], st["sections"], st["pos"])
+        else:
+            size = tq.tq_kv8_workspace_size(ctx, c["batch"], c["n_new"], c["heads"], c["kv_heads"], st["max_len"])
+            ws = torch.empty(max(1, size), dtype=torch.uint8, device="cuda")
+        st["plan"] = (tq, ctx, code, cache, rope, ws, size)
+    return st["plan"]
+
+
+def _run_own(st):
+    c = st["case"]
+    tq, ctx, code, cache, rope, ws, size = _plan(st)
+    stream = torch.cuda.current_stream()
+    new = st["new"] if c["ragged"] else None
+    if c["op"] == "append":
+        tq.tq_kv8_append(ctx, cache, st["k"], st["v"], st["q"], code, c["batch"], c["n_new"], c["heads"],
+                         st["cached"], new, rope, st["q_out"], st["k"].stride(1), st["v"].stride(1),
+                         st["q"].stride(1), stream)
+        return {"k": st["kc"], "v": st["vc"], "k_scale": st["ks"], "v_scale": st["vs"], "q": st["q_out"]}
+    scale = 1.0 / math.sqrt(c["d"])
+    if c["op"] == "decode":
+        tq.tq_kv8_decode_attention(ctx, cache, st["q"], code, c["batch"], c["heads"], st["cached"], st["max_len"],
+                                   c["window"], c["sinks"], scale, st["out"], ws, size, stream)
+    else:
+        tq.tq_kv8_causal_attention(ctx, cache, st["q"], code, c["batch"], c["n_new"], c["heads"], st["cached"], new,
+                                   st["max_len"], c["window"], c["sinks"], scale, st["out"], ws, size, stream)
+    return st["out"]
+
+
+# ---------------------------------------------------------------------------
+# the plain form
+# ---------------------------------------------------------------------------
+def _rotated(x, st):
+    """x [b][n][heads][d] in fp64 with its pairs turned by the table's angles (in 64 bits: values next to a
+    rounding border of the 8-bit type decide a code)."""
+    c = st["case"]
+    rot, pairs = c["rot"], c["rot"] // 2
+    n = x.shape[1]
+    if c["axes"] == 1:
+        pos = (st["cached"][:, None] + torch.arange(n, device=x.device)).clamp(max=st["max_pos"] - 1)
+        cs = st["table_cs"][pos]                                       # [b][n][rot]
+    else:
+        axis = torch.repeat_interleave(torch.arange(c["axes"], device=x.device),
+                                       torch.tensor(st["sections"], device=x.device))
+        at = st["pos"].long()[axis].permute(1, 2, 0)                   # [b][n][pairs]
+        at = at.reshape(-1, pairs)
+        cs = torch.cat([torch.gather(st["table_cs"][:, :pairs], 0, at),
+                        torch.gather(st["table_cs"][:, pairs:], 0, at)], dim=1).view(*x.shape[:2], rot)
+    co, si = cs[..., None, :pairs].double(), cs[..., None, pairs:].double()
+    y = x.double()
+    r = y[..., :rot].unflatten(-1, (pairs, 2)) if c["interleaved"] else y[..., :rot].unflatten(-1, (2, pairs)).mT
+    a, b = r[..., 0], r[..., 1]
+    t = torch.stack([a * co - b * si, b * co + a * si], dim=-1)
+    t = t.flatten(-2) if c["interleaved"] else t.mT.flatten(-2)
+    return torch.cat([t, y[..., rot:]], dim=-1)
+
+
+def _append_blocks(x, codes, scale, st):
+    """Writes x [b][n][h][d] (fp64) into the blocks of its positions, page by page."""
+    b, n, h, d = x.shape
+    start, new = st["cached"].long(), st["new"].long()
+    np_ = (n + 2 * PAGE - 2) // PAGE
+    page = (start // PAGE)[:, None] + torch.arange(np_, device=x.device)                   # [b][np]
+    pos = page[..., None] * PAGE + torch.arange(PAGE, device=x.device)                     # [b][np][16]
+    t = pos - start[:, None, None]
+    fresh = (t >= 0) & (t < new[:, None, None])
+    bi, pi = torch.nonzero(fresh.any(-1), as_tuple=True)                                   # pages that are written
+    ids = st["table"].long()[bi, page[bi, pi]]
+    t, fresh = t[bi, pi], fresh[bi, pi]                                                    # [pages][16]
+    val = x[bi[:, None], t.clamp(0, n - 1)].permute(0, 2, 1, 3)                            # [pages][h][16][d]
+    is_new = fresh[:, None, :, None]
+    is_old = (t < 0)[:, None, :, None]
+    e = _block_exponent(torch.where(is_new, val.abs(), torch.zeros((), dtype=val.dtype, device=x.device)).amax((2, 3)))
+    e_old = torch.log2(scale[ids]).round().int()
+    e = torch.where(is_old.any(2)[..., 0], torch.maximum(e, e_old), e)
+    old = codes[ids]
+    again = _round_e4m3(old.double() * torch.exp2((e_old - e).double())[..., None, None])
+    put = _round_e4m3(val * torch.exp2(-e.double())[..., None, None])
+    put = torch.where(is_new, put, torch.where(is_old, again, old.double()))
+    codes.view(torch.uint8)[ids] = put.to(torch.float8_e4m3fn).view(torch.uint8)
+    scale[ids] = torch.exp2(e.float())
+
+
+def _run_append(st):
+    _append_blocks(_rotated(st["k"], st), st["kc"], st["ks"], st)
+    _append_blocks(st["v"].double(), st["vc"], st["vs"], st)
+    q = _rotated(st["q"], st).to(st["dtype"])
+    if st["case"]["ragged"]:
+        real = torch.arange(q.shape[1], device=q.device) < st["new"][:, None]
+        q = torch.where(real[..., None, None], q, st["q_out"])
+    st["q_out"].copy_(q)
+    return {"k": st["kc"], "v": st["vc"], "k_scale": st["ks"], "v_scale": st["vs"], "q": st["q_out"]}
+
+
+def _gathered(codes, scale, table):
+    """[b][h][tokens][d] fp32 values of the sequences' pages."""
+    t = table.long()
+    x = codes.view(torch.uint8)[t].view(torch.float8_e4m3fn).float() * scale[t][..., None, None]
+    return x.permute(0, 2, 1, 3, 4).flatten(2, 3)
+
+
+def _run_attention(st):
+    c = st["case"]
+    decode = c["op"] == "decode"
+    q = st["q"][:, None] if decode else st["q"]
+    b, n, hq, d = q.shape
+    h = c["kv_heads"]
+    k, v = _gathered(st["kc"], st["ks"], st["table"]), _gathered(st["vc"], st["vs"], st["table"])
+    p = st["cached"][:, None] + (-1 if decode else torch.arange(n, device=q.device)[None])    # [b][n] positions
+    j = torch.arange(k.shape[2], device=q.device)
+    seen = j <= p[..., None]
+    if c["window"]:
+        seen &= (j > p[..., None] - c["window"]) | (j < c["sinks"])
+    rows = q.float().view(b, n, h, hq // h, d).permute(0, 2, 1, 3, 4).reshape(b, h, n * (hq // h), d)
+    s = (rows @ k.mT).view(b, h, n, hq // h, -1) * (1.0 / math.sqrt(d))
+    s = s.masked_fill_(~seen[:, None, :, None, :], float("-inf"))
+    s -= s.amax(-1, keepdim=True)
+    s = s.exp_()
+    total = s.sum(-1, keepdim=True)
+    o = (s.view(b, h, n * (hq // h), -1) @ v).view(b, h, n, hq // h, d) / total
+    o = o.permute(0, 2, 1, 3, 4).reshape(b, n, hq, d).to(st["dtype"])
+    if decode:
+        return o[:, 0]
+    if c["ragged"]:
+        real = torch.arange(n, device=q.device) < st["new"][:, None]
+        o = torch.where(real[..., None, None], o, st["out"])
+    return o
+
+
+def run(state):
+    if own:
+        return _run_own(state)
+    return _run_append(state) if state["case"]["op"] == "append" else _run_attention(state)
+
+
+# ---------------------------------------------------------------------------
+# 64 bits, from the definition
+# ---------------------------------------------------------------------------
+def _nearest_code(x):
+    """Nearest e4m3 value of each x, by the distance to the two neighbours in the sorted list of all values."""
+    grid = torch.arange(127, dtype=torch.uint8, device=x.device).view(torch.float8_e4m3fn).double()   # 0 .. 448
+    a = x.abs().clamp(max=448.0)
+    hi = torch.searchsorted(grid, a).clamp(1, 126)
+    lo = hi - 1
+    dl, dh = a - grid[lo], grid[hi] - a
+    up = (dh < dl) | ((dh == dl) & (hi % 2 == 0))
+    return torch.copysign(grid[torch.where(up, hi, lo)], x)
+
+
+def _exact_append(case, seed):
+    st = prepare(case, seed)
+    cached, new = _lengths(case)
+    rot, pairs, d = case["rot"], case["rot"] // 2, case["d"]
+    axis = [a for a, s in enumerate(st["sections"]) for _ in range(s)]
+    first = list(range(0, rot, 2)) if case["interleaved"] else list(range(pairs))
+    second = [i + 1 for i in first] if case["interleaved"] else [i + pairs for i in first]
+    cos, sin = st["table_cs"][:, :pairs].double(), st["table_cs"][:, pairs:].double()
+    lane = torch.arange(pairs, device="cuda")
+    out = {"k": st["kc"].double(), "v": st["vc"].double(), "k_scale": st["ks"].double(), "v_scale": st["vs"].double(),
+           "q": st["q_out"].double()}
+    for b, (c0, n) in enumerate(zip(cached, new)):
+        at = torch.arange(c0, c0 + n, device="cuda")
+        if case["axes"] == 1:
+            at = at[:, None].expand(n, pairs)
+        else:
+            at = st["pos"][axis, b, :n].long().T
+        co, si = cos[at, lane][:, None], sin[at, lane][:, None]
+
+        def turn(x):
+            y = x[b, :n].double().clone()
+            a, z = y[..., first], y[..., second]
+            y[..., first], y[..., second] = a * co - z * si, z * co + a * si
+            return y
+
+        out["q"][b, :n] = turn(st["q"])
+        for name, val in (("k", turn(st["k"])), ("v", st["v"][b, :n].double())):
+            codes, scale = out[name], out[name + "_scale"]
+            # whole pages at once, the first one (which may hold older tokens) alone
+            head = min(n, -c0 % PAGE)
+            parts = ([(0, head)] if head else []) + [(head, n)] * (n > head)
+            for lo, hi in parts:
+                slot0 = (c0 + lo) % PAGE
+                m = 0 if slot0 else -(hi - lo) % PAGE
+                x = val[lo:hi]
+                ids = st["table"][b, (c0 + lo) // PAGE:(c0 + hi + PAGE - 1) // PAGE].long()
+                if slot0:
+                    amax = x.abs().amax(dim=(0, 2))                                       # [h]
+                    s_new = _exact_scale(amax)
+                    s_old = scale[ids[0]]
+                    s = torch.maximum(s_new, s_old)
+                    kept = codes[ids[0], :, :slot0] * (s_old / s)[:, None, None]
+                    codes[ids[0], :, :slot0] = torch.where((s > s_old)[:, None, None], _nearest_code(kept), kept)
+                    codes[ids[0], :, slot0:slot0 + hi - lo] = _nearest_code((x / s[None, :, None]).transpose(0, 1))
+                    scale[ids[0]] = s
+                else:
+                    pad = torch.cat([x, torch.zeros(m, *x.shape[1:], dtype=x.dtype, device="cuda")]) if m else x
+                    blocks = pad.view(-1, PAGE, *x.shape[1:]).transpose(1, 2)             # [pages][h][16][d]
+                    s = _exact_scale(blocks.abs().amax(dim=(2, 3)))
+                    q = _nearest_code(blocks / s[..., None, None])
+                    if m:
+                        q[-1, :, PAGE - m:] = codes[ids[-1], :, PAGE - m:]
+                    codes[ids], scale[ids] = q, s
+    return out
+
+
+def _exact_scale(amax):
+    e = torch.ceil(torch.log2(amax.clamp(min=2.0 ** -120) / 448.0))
+    for step in (-1, 1):      # a logarithm that rounded across a border
+        fits = amax <= 448.0 * torch.exp2(e + min(step, 0))
+        e = torch.where(fits if step < 0 else ~(amax <= 448.0 * torch.exp2(e)), e + step, e)
+    return torch.exp2(e.clamp(E_MIN, E_MAX))
+
+
+def _exact_attention(case, seed):
+    st = prepare(case, seed)
+    cached, new = _lengths(case)
+    decode = case["op"] == "decode"
+    h, g, d = case["kv_heads"], case["heads"] // case["kv_heads"], case["d"]
+    out = st["out"].double()
+    for b, (c0, n) in enumerate(zip(cached, new)):
+        first, total = (c0 - 1, c0) if decode else (c0, c0 + n)
+        ids = st["table"][b, :(total + PAGE - 1) // PAGE].long()
+        p = torch.arange(first, total, device="cuda")[:, None]
+        j = torch.arange(total, device="cuda")[None]
+        hidden = j > p
+        if case["window"]:
+            hidden = hidden | ((j <= p - case["window"]) & (j >= case["sinks"]))
+        for i in range(h):
+            k = (st["kc"][ids, i].double() * st["ks"][ids, i].double()[:, None, None]).reshape(-1, d)[:total]
+            v = (st["vc"][ids, i].double() * st["vs"][ids, i].double()[:, None, None]).reshape(-1, d)[:total]
+            for a in range(i * g, (i + 1) * g):
+                q = (st["q"][b, a][None] if decode else st["q"][b, :n, a]).double()
+                s = (q @ k.T) / math.sqrt(d)
+                o = torch.softmax(s.masked_fill(hidden, float("-inf")), dim=-1) @ v
+                if decode:
+                    out[b, a] = o[0]
+                else:
+                    out[b, :n, a] = o
+    return out
+
+
+def exact(case, seed):
+    return _exact_append(case, seed) if case["op"] == "append" else _exact_attention(case, seed)
