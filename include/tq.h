@@ -294,7 +294,8 @@ tq_status tq_causal_attention(const tq_ctx* ctx, const void* q, tq_dtype dtype, 
  * 1 = page id out of range, 2 = position beyond the block table,
  * 4 = sequence length beyond max_seq_len or the block table, 8 = a bounded
  * wait inside a kernel gave up (that launch's results are incomplete),
- * 16 = a kernel's shared-memory layout did not fit (it did no work). */
+ * 16 = a kernel's shared-memory layout did not fit (it did no work),
+ * 32 and 64: see tq_kv8_append. */
 tq_status tq_check_device_status(const tq_ctx* ctx, uint32_t* flags);
 
 /* Counters of the decisions the quantize kernels took again exactly (fp64 or
@@ -351,6 +352,100 @@ tq_status tq_search(const tq_ctx* ctx, const void* q, tq_dtype dtype, int nq, co
 tq_status tq_search_scores(const tq_ctx* ctx, const void* q, tq_dtype dtype, int nq, const void* k_cache,
                            const int32_t* block_table, int num_pages, int n_db, int k_top, float* scores,
                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- 8-bit paged cache -------------------------------------------------------
+ * A cache next to the 2-4 bit one for layers (or recent tokens) that want more
+ * precision, in the same 16-token pages and block tables ([P4] §3.1).  A block
+ * is one KV head of one page: e4m3 codes [16][d] and one fp32 scale, a power of
+ * two 2^e with e in [-100, 119]; the value of a code is code * scale.  Head
+ * dimension: the context's d, one of 64, 128, 256 (else TQ_ERR_UNSUPPORTED).
+ * Codes are 16-byte aligned; the pages' contents need no initialisation. */
+typedef struct {
+  void* k_codes;                /* device [num_pages][num_kv_heads][16][d] e4m3 */
+  void* v_codes;
+  float* k_scale;               /* device [num_pages][num_kv_heads] */
+  float* v_scale;
+  const int32_t* block_table;   /* device [batch][max_pages_per_seq] */
+  int max_pages_per_seq, num_pages, num_kv_heads;
+} tq_kv8_cache;
+
+/* Bytes of one page's codes and of its scales, for K and for V alike. */
+tq_status tq_kv8_cache_layout(const tq_ctx* ctx, int num_kv_heads, size_t* page_code_bytes, size_t* page_scale_bytes);
+
+/* Rotation by position.  Pair i of the first rot_dim channels of a head turns
+ * by the angle whose cosine and sine stand at cos_sin[p][i] and
+ * cos_sin[p][rot_dim/2 + i], (x1, x2) -> (x1 c - x2 s, x2 c + x1 s), with
+ * (x1, x2) = channels (i, i + rot_dim/2), or (2i, 2i + 1) when interleaved.
+ * Positions have num_axes axes (1 to 4; say time, height, width): pairs
+ * [0, section[0]) take axis 0's position, the next section[1] axis 1's, and so
+ * on (the sections add up to rot_dim/2; with one axis they are not read).
+ * pos NULL (one axis only): the token's position in the sequence.  rot_dim is
+ * a multiple of 16; the other channels stay as they are. */
+typedef struct {
+  const float* cos_sin;         /* device fp32 [max_pos][rot_dim], 16-byte aligned */
+  int max_pos, rot_dim, interleaved, num_axes;
+  int section[4];
+  const int32_t* pos;           /* device [num_axes][batch][n_new] or NULL */
+} tq_rope;
+
+/* Append to the 8-bit cache, rotating on the way.  k, v: [batch][n_new] tokens
+ * of [num_kv_heads][d], q: of [num_q_heads][d], in `dtype`; consecutive tokens
+ * are k_stride, v_stride, q_stride elements apart (0: dense), so that slices of
+ * one fused projection can be passed.  Any of k, v, q may be NULL.  Token t of
+ * sequence b goes to position start_pos[b] + t; of a padded batch, only the
+ * first new_lens[b] (device int32; NULL: n_new) tokens are read, and the rest
+ * of q_out and of the cache stays as it was.  Keys and queries are rotated
+ * (rope NULL: not); q_out (device [batch][n_new][num_q_heads][d] in `dtype`,
+ * dense) may be q itself when q is dense.
+ * A block's scale is the smallest 2^e with |x| <= 448 * 2^e for the tokens
+ * written to it so far: the call that writes slot 0 starts a block anew; a
+ * later call keeps the scale or raises it, and then rounds the earlier slots'
+ * codes again (exact but for the smallest).  Codes are the nearest (ties to
+ * even) to the exactly rotated values, whatever the launch.  After a rollback
+ * of a sequence, appending at a smaller position is the way to go on.
+ * Every block is written by one sequence: two that share a page must not both
+ * append to it.  Values that are not finite in fp32 set device status bit 32
+ * and are stored as 0 (NaN) or as the block's largest code (infinite), without
+ * counting for its scale.  Bit 2: a position beyond the block table (the page
+ * is skipped) or outside the cos_sin table (the token is skipped).  Bit 64: an
+ * earlier token's block had no power of two in range as its scale (taken as
+ * 2^-100).  Errors as tq_quantize. */
+tq_status tq_kv8_append(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* k, const void* v, const void* q,
+                        tq_dtype dtype, int batch, int n_new, int num_q_heads, const int32_t* start_pos,
+                        const int32_t* new_lens, const tq_rope* rope, void* q_out, long long k_stride,
+                        long long v_stride, long long q_stride, void* stream);
+
+/* Workspace bytes of the two attention calls below (decode: n_new = 1). */
+tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_new, int num_q_heads, int num_kv_heads,
+                                int max_seq_len, size_t* bytes);
+
+/* Decode attention over the 8-bit cache: tq_decode_attention's contract with
+ * scores <q, k> over the cached values, and a mask: the query, at position
+ * p = seq_lens[b] - 1, sees key j <= p if window = 0, or j > p - window, or
+ * j < sinks (the first tokens stay visible).  Only visible pages are read.
+ * q, out: [batch][num_q_heads][d] in `dtype` (bf16 or fp32; sums, maxima and
+ * weights' sums in fp32).  A sequence of length 0 gives zeros.  What lies in a
+ * page behind the sequence's end, or outside every query's window, may hold
+ * any bytes.  Any number of query heads per KV head.  The split of the work
+ * follows the lengths on the device; results do not depend on the run.
+ * Accuracy at every softmax_scale: fp32 products of exact codes; for fp32 the
+ * query and the weights keep 22 bits, for bf16 the query is exact and the
+ * weights keep 11.  q, out and workspace are 16-byte aligned. */
+tq_status tq_kv8_decode_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* q, tq_dtype dtype, int batch,
+                                  int num_q_heads, const int32_t* seq_lens, int max_seq_len, int window, int sinks,
+                                  float softmax_scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Causal attention of n_new tokens per sequence over the 8-bit cache (prompts,
+ * chunks of prompts, drafted tokens): q, out [batch][n_new][num_q_heads][d] in
+ * `dtype`; query t of sequence b stands at p = start_pos[b] + t and sees keys by
+ * the rule above; the cache already holds positions up to the last query's.  Of
+ * a padded batch only the first new_lens[b] (NULL: n_new) queries are answered
+ * and the other rows of `out` stay as they were.  start_pos[b] + new_lens[b]
+ * <= max_seq_len. */
+tq_status tq_kv8_causal_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* q, tq_dtype dtype, int batch,
+                                  int n_new, int num_q_heads, const int32_t* start_pos, const int32_t* new_lens,
+                                  int max_seq_len, int window, int sinks, float softmax_scale, void* out,
+                                  void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,5 +1,6 @@
 // C ABI entry points: context creation, argument checks, launches, status.
 #include "tq_internal.h"
+#include "tq_kv8.h"
 
 #include <cuda_runtime.h>
 
@@ -897,4 +898,187 @@ extern "C" tq_status tq_search_scores(const tq_ctx* ctx, const void* q, tq_dtype
   if (search_tc_supported(ctx->kl, ctx->cfg.m, k_top))
     return cuda_status(launch_search_tc(a, kc, block_table, num_pages, n_db, 1, nullptr, nullptr, scores, nullptr, s));
   return cuda_status(launch_search(a, kc, block_table, num_pages, n_db, 1, nullptr, nullptr, scores, s));
+}
+
+// ---------------------------------------------------------------------------
+// the 8-bit paged cache
+// ---------------------------------------------------------------------------
+namespace {
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+// The cache descriptor, for calls that touch K and V (or only one of them).
+tq_status kv8_check(const tq_ctx* ctx, const tq_kv8_cache* c, bool need_k, bool need_v) {
+  if (!ctx || !c) return TQ_ERR_INVALID_ARG;
+  if (!kv8_head_dim(ctx->cfg.d)) return TQ_ERR_UNSUPPORTED;
+  if (c->num_kv_heads < 1 || c->max_pages_per_seq < 1 || c->num_pages < 1 || !c->block_table) return TQ_ERR_INVALID_ARG;
+  if (need_k && (!c->k_codes || !c->k_scale || misaligned(c->k_codes))) return TQ_ERR_INVALID_ARG;
+  if (need_v && (!c->v_codes || !c->v_scale || misaligned(c->v_codes))) return TQ_ERR_INVALID_ARG;
+  return static_cast<long long>(c->num_pages) * c->num_kv_heads > 0x7FFFFFFFLL ? TQ_ERR_UNSUPPORTED : TQ_OK;
+}
+
+// The last check before a launch: the context's device is the current one.
+tq_status on_device(const tq_ctx* ctx) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return dev == ctx->device ? TQ_OK : TQ_ERR_INVALID_ARG;
+}
+
+// A rotation: its table, the axes' sections and the positions.
+tq_status rope_check(const tq_rope* r, int d) {
+  if (!r->cos_sin || misaligned(r->cos_sin) || r->max_pos < 1) return TQ_ERR_INVALID_ARG;
+  if (r->rot_dim < 16 || r->rot_dim > d || r->rot_dim % 16 || (d - r->rot_dim) % 16) return TQ_ERR_INVALID_ARG;
+  if (r->interleaved != 0 && r->interleaved != 1) return TQ_ERR_INVALID_ARG;
+  if (r->num_axes < 1 || r->num_axes > 4 || (r->num_axes > 1 && !r->pos)) return TQ_ERR_INVALID_ARG;
+  int sum = 0;
+  for (int i = 0; i < r->num_axes; ++i) {
+    if (r->section[i] < 0 || r->section[i] > d) return TQ_ERR_INVALID_ARG;
+    sum += r->section[i];
+  }
+  return r->num_axes == 1 || sum == r->rot_dim / 2 ? TQ_OK : TQ_ERR_INVALID_ARG;
+}
+
+tq_status kv8_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* q, tq_dtype dtype, int batch, int n_new,
+                        int Hq, const int32_t* lens, const int32_t* new_lens, bool decode, int max_seq_len, int window,
+                        int sinks, float softmax_scale, void* out, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  tq_status st = kv8_check(ctx, cache, true, true);
+  if (st != TQ_OK) return st;
+  const int H = cache->num_kv_heads;
+  if (batch < 0 || n_new < 1 || Hq < 1 || Hq % H || max_seq_len < 0 || window < 0 || sinks < 0) return TQ_ERR_INVALID_ARG;
+  if (dtype != TQ_BF16 && dtype != TQ_F32) return TQ_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale)) return TQ_ERR_INVALID_ARG;
+  if (batch == 0) return TQ_OK;
+  if (!q || !lens || !out || !workspace || misaligned(q) || misaligned(out) || misaligned(workspace))
+    return TQ_ERR_INVALID_ARG;
+  if (static_cast<long long>(batch) * n_new * Hq > 0x7FFFFFFFLL / 16) return TQ_ERR_UNSUPPORTED;
+  size_t need = 0;
+  st = tq_kv8_workspace_size(ctx, batch, n_new, Hq, H, max_seq_len, &need);
+  if (st != TQ_OK) return st;
+  if (workspace_bytes < need) return TQ_ERR_WORKSPACE;
+  st = on_device(ctx);
+  if (st != TQ_OK) return st;
+  Kv8Attn a{};
+  a.q = q;
+  a.out = out;
+  a.B = batch;
+  a.T = n_new;
+  a.Hq = Hq;
+  a.H = H;
+  a.G = Hq / H;
+  a.lens = lens;
+  a.new_lens = new_lens;
+  a.decode = decode ? 1 : 0;
+  a.max_seq_len = max_seq_len;
+  a.bt = cache->block_table;
+  a.maxp = cache->max_pages_per_seq;
+  a.num_pages = cache->num_pages;
+  a.kc = static_cast<const uint8_t*>(cache->k_codes);
+  a.vc = static_cast<const uint8_t*>(cache->v_codes);
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.part = static_cast<float*>(workspace);
+  a.err = ctx->tab.err;
+  return cuda_status(launch_kv8_rows(a, ctx->cfg.d, dtype == TQ_F32, static_cast<cudaStream_t>(stream)));
+}
+}  // namespace
+
+extern "C" tq_status tq_kv8_cache_layout(const tq_ctx* ctx, int num_kv_heads, size_t* page_code_bytes,
+                                         size_t* page_scale_bytes) {
+  if (!ctx || num_kv_heads < 1 || (!page_code_bytes && !page_scale_bytes)) return TQ_ERR_INVALID_ARG;
+  if (!kv8_head_dim(ctx->cfg.d)) return TQ_ERR_UNSUPPORTED;
+  if (page_code_bytes) *page_code_bytes = static_cast<size_t>(num_kv_heads) * kPage * ctx->cfg.d;
+  if (page_scale_bytes) *page_scale_bytes = static_cast<size_t>(num_kv_heads) * sizeof(float);
+  return TQ_OK;
+}
+
+extern "C" tq_status tq_kv8_append(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* k, const void* v,
+                                   const void* q, tq_dtype dtype, int batch, int n_new, int Hq,
+                                   const int32_t* start_pos, const int32_t* new_lens, const tq_rope* rope, void* q_out,
+                                   long long k_stride, long long v_stride, long long q_stride, void* stream) {
+  tq_status st = kv8_check(ctx, cache, k != nullptr, v != nullptr);
+  if (st != TQ_OK) return st;
+  const int d = ctx->cfg.d, H = cache->num_kv_heads;
+  if ((!k && !v && !q) || batch < 0 || n_new < 0) return TQ_ERR_INVALID_ARG;
+  if (dtype != TQ_BF16 && dtype != TQ_F32) return TQ_ERR_INVALID_ARG;
+  if (q && (Hq < 1 || !q_out || misaligned(q_out))) return TQ_ERR_INVALID_ARG;
+  const long long dk = static_cast<long long>(H) * d, dq = static_cast<long long>(q ? Hq : 0) * d;
+  if ((k && k_stride != 0 && k_stride < dk) || (v && v_stride != 0 && v_stride < dk) ||
+      (q && q_stride != 0 && q_stride < dq))
+    return TQ_ERR_INVALID_ARG;
+  if (rope) {
+    st = rope_check(rope, d);
+    if (st != TQ_OK) return st;
+  }
+  if (batch == 0 || n_new == 0) return TQ_OK;
+  if (!start_pos) return TQ_ERR_INVALID_ARG;
+  const uintptr_t elem = dtype == TQ_F32 ? 3 : 1;
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(q)) & elem)
+    return TQ_ERR_INVALID_ARG;
+  if (static_cast<long long>(batch) * n_new > 0x7FFFFFFFLL || H > 65535 || Hq > 65535) return TQ_ERR_UNSUPPORTED;
+  st = on_device(ctx);
+  if (st != TQ_OK) return st;
+  Kv8Append a{};
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.q_out = q_out;
+  a.batch = batch;
+  a.n_new = n_new;
+  a.Hq = q ? Hq : 0;
+  a.H = H;
+  a.k_stride = k_stride ? k_stride : dk;
+  a.v_stride = v_stride ? v_stride : dk;
+  a.q_stride = q_stride ? q_stride : dq;
+  a.start_pos = start_pos;
+  a.new_lens = new_lens;
+  a.kc = static_cast<uint8_t*>(cache->k_codes);
+  a.vc = static_cast<uint8_t*>(cache->v_codes);
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  a.bt = cache->block_table;
+  a.maxp = cache->max_pages_per_seq;
+  a.num_pages = cache->num_pages;
+  a.axes = 1;
+  if (rope) {
+    a.cs = rope->cos_sin;
+    a.max_pos = rope->max_pos;
+    a.rot = rope->rot_dim;
+    a.interleaved = rope->interleaved;
+    a.axes = rope->num_axes;
+    a.pos = rope->pos;
+    int end = 0;
+    for (int i = 0; i < a.axes; ++i) a.sec_end[i] = end += rope->section[i];
+  }
+  a.err = ctx->tab.err;
+  return cuda_status(launch_kv8_append(a, d, dtype == TQ_F32, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_new, int Hq, int H, int max_seq_len,
+                                           size_t* bytes) {
+  if (!ctx || !bytes || batch < 0 || n_new < 1 || Hq < 1 || H < 1 || Hq % H || max_seq_len < 0)
+    return TQ_ERR_INVALID_ARG;
+  if (!kv8_head_dim(ctx->cfg.d)) return TQ_ERR_UNSUPPORTED;
+  *bytes = kv8_rows_workspace(batch, n_new, Hq / H, H, ctx->cfg.d);
+  return TQ_OK;
+}
+
+extern "C" tq_status tq_kv8_decode_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* q, tq_dtype dtype,
+                                             int batch, int Hq, const int32_t* seq_lens, int max_seq_len, int window,
+                                             int sinks, float softmax_scale, void* out, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  return kv8_attention(ctx, cache, q, dtype, batch, 1, Hq, seq_lens, nullptr, true, max_seq_len, window, sinks,
+                       softmax_scale, out, workspace, workspace_bytes, stream);
+}
+
+extern "C" tq_status tq_kv8_causal_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* q, tq_dtype dtype,
+                                             int batch, int n_new, int Hq, const int32_t* start_pos,
+                                             const int32_t* new_lens, int max_seq_len, int window, int sinks,
+                                             float softmax_scale, void* out, void* workspace, size_t workspace_bytes,
+                                             void* stream) {
+  return kv8_attention(ctx, cache, q, dtype, batch, n_new, Hq, start_pos, new_lens, false, max_seq_len, window, sinks,
+                       softmax_scale, out, workspace, workspace_bytes, stream);
 }

@@ -1,0 +1,635 @@
+// Attention over the 8-bit paged cache for few query rows (decode, drafted
+// tokens), for fp32 queries and for every head dimension: mma.sync on e4m3
+// codes turned into fp16, which is exact.
+//
+// An item is (sequence, block of R = 8 NT query rows, KV head); its keys are
+// taken a page of 16 tokens at a time:
+//   S^T[16 tokens][R] = Kc Q^T        Kc codes, Q scaled per row by a power of two
+//                                     (fp16 exact for bf16 input; fp32 input as hi + lo)
+//   x = scale log2(e) 2^ek 2^-row S   log2 of the weight, -inf where hidden
+//   w = 2^(x + ev - M)                M = running max of x + ev over the keys: the
+//                                     page's value scale goes into the weight's exponent,
+//                                     so w <= 1 whatever the scales are
+//   O^T[d][R] += Vc^T w,  l += w 2^-ev,  out = O / l.
+// The transposed product uses all 8 columns of the MMA for 8 query rows.
+//
+// All pages of all items form one list, cut into equal spans, one per CTA
+// (whatever the sequences' lengths); a CTA's warps take the pages of its span
+// in turn and join their (M, l, O) in shared memory at an item's end.  Items
+// that cross spans leave partials for a second kernel.
+
+#include "tq_kv8.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+namespace tq {
+namespace {
+
+constexpr int kRWarps = 4;
+constexpr int kMinSpan = 8;               // pages a CTA takes at least (two per warp)
+constexpr int kMaxEntries = 2048;         // (sequence, row block) pairs that the split form lists
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t half2_of(uint32_t two) {     // two e4m3 codes (low 16 bits) -> f16x2
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(two)));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {            // relative error about 2^-22; 0 for -inf
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack(__half lo, __half hi) {
+  const __half2 h = __halves2half2(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 ldg128(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ldg64(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+// Channels: a lane's K words (four channels each) and V words, in panels of 128.
+template <int D> struct Lay {
+  static constexpr int KW = D / 16;       // words of one key row per lane (its quarter of the channels)
+  static constexpr int VW = D / 32;       // words of one value row per lane (its eighth)
+  static constexpr int MT = D / 16;       // 16-channel tiles of the value product
+  static constexpr int PAN = D >= 128 ? D / 128 : 1;
+  static constexpr int KP = KW / PAN, VP = VW / PAN;   // words per panel
+  __device__ static __forceinline__ int k_ch(int t, int j) { return 128 * (j / KP) + 4 * KP * t + 4 * (j % KP); }
+  __device__ static __forceinline__ int v_ch(int g, int w) { return 128 * (w / VP) + 4 * VP * g + 4 * (w % VP); }
+};
+
+struct Item {
+  int b, rb, h;
+  int p0, n;                              // the sequence's first query position and queries
+  int pmin, pmax;                         // positions of the block's first and last row
+  Kv8Range r;
+  int pages;
+};
+
+__device__ __forceinline__ int block_pages(const Kv8Attn& a, const Kv8Seq& s, int rb, int R, int& pmin, int& pmax,
+                                           Kv8Range& r) {
+  const long long rows = static_cast<long long>(s.n) * a.G, r0 = static_cast<long long>(rb) * R;
+  if (r0 >= rows) return 0;
+  const long long r1 = r0 + R < rows ? r0 + R : rows;
+  pmin = s.p0 + static_cast<int>(r0 / a.G);
+  pmax = s.p0 + static_cast<int>((r1 - 1) / a.G);
+  r = kv8_range(a.window, a.sinks, pmin, pmax);
+  return r.ns + r.nw;
+}
+
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(32 * kRWarps) kv8_rows_kernel(const __grid_constant__ Kv8Attn a, int nrb, int split) {
+  using Y = Lay<D>;
+  constexpr int R = 8 * NT, HL = F32 ? 2 : 1;
+  extern __shared__ __align__(16) float sm[];                    // [warps][R][D] joins; then the list's prefix sums
+  __shared__ float s_ml[kRWarps][R][2];
+  __shared__ int s_scan[32 * kRWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  pdl_wait();
+  pdl_trigger();
+  const int entries = a.B * nrb;
+  int* prefix = reinterpret_cast<int*>(sm + kRWarps * R * D);    // split form: pages of one head before entry i
+
+  long long u0 = 0, u1 = 0;                                      // this CTA's span of the list (pages)
+  int entry = 0;
+  long long item_at = 0;                                         // list position of the current item's first page
+  Item it{};
+  auto load_entry = [&](int e) {
+    it.b = e / nrb;
+    it.rb = e % nrb;
+    const Kv8Seq s = kv8_seq(a, it.b);
+    it.p0 = s.p0;
+    it.n = s.n;
+    it.pmin = it.pmax = 0;
+    it.pages = block_pages(a, s, it.rb, R, it.pmin, it.pmax, it.r);
+  };
+  if (split) {
+    // pages per entry, scanned: a run of entries per thread, then the threads' sums
+    const int per = (entries + 32 * kRWarps - 1) / (32 * kRWarps);
+    int sum = 0;
+    for (int i = 0; i < per; ++i) {
+      const int e = tid * per + i;
+      if (e >= entries) break;
+      int x0, x1;
+      Kv8Range r;
+      const int c = block_pages(a, kv8_seq(a, e / nrb), e % nrb, R, x0, x1, r);
+      prefix[e] = sum;
+      sum += c;
+    }
+    s_scan[tid] = sum;
+    __syncthreads();
+    for (int o = 1; o < 32 * kRWarps; o <<= 1) {
+      const int v = tid >= o ? s_scan[tid - o] : 0;
+      __syncthreads();
+      s_scan[tid] += v;
+      __syncthreads();
+    }
+    const int before = tid ? s_scan[tid - 1] : 0;
+    for (int i = 0; i < per; ++i) {
+      const int e = tid * per + i;
+      if (e < entries) prefix[e] += before;
+    }
+    const int total = s_scan[32 * kRWarps - 1];
+    __syncthreads();
+    const long long units = static_cast<long long>(total) * a.H;
+    long long span = (units + gridDim.x - 1) / gridDim.x;
+    span = span < kMinSpan ? kMinSpan : span;
+    u0 = span * blockIdx.x;
+    u1 = u0 + span < units ? u0 + span : units;
+    if (u0 >= u1 && blockIdx.x) return;
+    if (blockIdx.x == 0) {                                       // decode rows that see nothing: zeros
+      for (int e = 0; e < entries; ++e) {
+        const int c = (e + 1 < entries ? prefix[e + 1] : total) - prefix[e];
+        if (c == 0 && a.decode) {
+          for (int i = tid; i < a.H * R * D; i += 32 * kRWarps) {
+            const int row = (e % nrb) * R + i / D % R;
+            if (row < a.G) {
+              const long long o = (static_cast<long long>(e / nrb) * a.Hq + i / (D * R) * a.G + row) * D + i % D;
+              if (F32) static_cast<float*>(a.out)[o] = 0.0f;
+              else static_cast<unsigned short*>(a.out)[o] = 0;
+            }
+          }
+        }
+      }
+      if (u0 >= u1) return;
+    }
+    int lo = 0, hi = entries - 1;                                // the entry that holds u0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (static_cast<long long>(prefix[mid]) * a.H <= u0) lo = mid;
+      else hi = mid - 1;
+    }
+    entry = lo;
+    load_entry(entry);
+    const long long base = static_cast<long long>(prefix[entry]) * a.H;
+    it.h = static_cast<int>((u0 - base) / it.pages);
+    item_at = base + static_cast<long long>(it.h) * it.pages;
+  }
+
+  long long whole = blockIdx.x;                                  // whole form: items in turn
+  const long long items = static_cast<long long>(entries) * a.H;
+  for (;;) {
+    int c0, c1;                                                  // pages of the item that are this CTA's
+    bool complete;
+    int slot = 0;
+    if (split) {
+      if (u0 >= u1) break;
+      c0 = static_cast<int>(u0 - item_at);
+      c1 = static_cast<int>((u1 < item_at + it.pages ? u1 : item_at + it.pages) - item_at);
+      complete = c0 == 0 && c1 == it.pages;
+      slot = 2 * blockIdx.x + (c0 > 0 ? 0 : 1);
+    } else {
+      if (whole >= items) break;
+      it.h = static_cast<int>(whole % a.H);
+      load_entry(static_cast<int>(entries - 1 - whole / a.H));   // the longest rows of a prompt first
+      c0 = 0;
+      c1 = it.pages;
+      complete = true;
+    }
+    const int rows = min(R, static_cast<int>(min(static_cast<long long>(R), static_cast<long long>(it.n) * a.G -
+                                                                             static_cast<long long>(it.rb) * R)));
+    if (rows > 0) {
+      // ---- the block's queries as MMA operands ---------------------------------------
+      uint32_t qf[NT][HL][Y::KW][2];
+      float rf[NT][2];                                           // score factor of columns 2t, 2t + 1
+      int pr[NT][2];                                             // their positions
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = 8 * nt + g;
+        const long long gr = static_cast<long long>(it.rb) * R + row;
+        const int tok = static_cast<int>(gr / a.G), hq = it.h * a.G + static_cast<int>(gr % a.G);
+        float v[4 * Y::KW];
+        float mx = 0.0f;
+        const long long base = row < rows ? ((static_cast<long long>(it.b) * a.T + tok) * a.Hq + hq) * D : 0;
+#pragma unroll
+        for (int j = 0; j < Y::KW; ++j) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (row < rows) {
+            if (F32) {
+              const float* q = static_cast<const float*>(a.q) + base + Y::k_ch(t, j);
+              x = make_float4(q[0], q[1], q[2], q[3]);
+            } else {
+              const unsigned short* q = static_cast<const unsigned short*>(a.q) + base + Y::k_ch(t, j);
+              x = make_float4(__uint_as_float(q[0] << 16), __uint_as_float(q[1] << 16), __uint_as_float(q[2] << 16),
+                              __uint_as_float(q[3] << 16));
+            }
+          }
+          v[4 * j] = x.x, v[4 * j + 1] = x.y, v[4 * j + 2] = x.z, v[4 * j + 3] = x.w;
+          mx = fmaxf(fmaxf(fmaxf(mx, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(x.z))), fabsf(x.w));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // the row's largest value into [2^14, 2^15): fp16 then holds bf16 values exactly down to 2^-29 of it
+        int e = 14 - (static_cast<int>(__float_as_uint(mx) >> 23) - 127);
+        e = mx > 0.0f && mx <= 3.4028234e38f ? (e > 120 ? 120 : e) : 0;
+        const float up = __int_as_float((e + 127) << 23), down = __int_as_float((127 - e) << 23);
+#pragma unroll
+        for (int j = 0; j < Y::KW; ++j) {
+          __half hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = v[4 * j + i] * up;
+            hi[i] = __float2half_rn(x);
+            lo[i] = __float2half_rn(x - __half2float(hi[i]));
+          }
+          qf[nt][0][j][0] = pack(hi[0], hi[1]);
+          qf[nt][0][j][1] = pack(hi[2], hi[3]);
+          if (F32) {
+            qf[nt][HL - 1][j][0] = pack(lo[0], lo[1]);
+            qf[nt][HL - 1][j][1] = pack(lo[2], lo[3]);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          rf[nt][c] = a.scale_log2 * __shfl_sync(0xffffffffu, down, 4 * (2 * t + c));
+          const long long r = static_cast<long long>(it.rb) * R + 8 * nt + 2 * t + c;
+          pr[nt][c] = it.p0 + static_cast<int>(r / a.G);
+        }
+      }
+      float o[NT][Y::MT][4], m[NT][2], l[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < Y::MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.0f;
+      }
+      const int* table = a.bt + static_cast<long long>(it.b) * a.maxp;
+
+      for (int c = c0 + warp; c < c1; c += kRWarps) {
+        const int page = c < it.r.ns ? c : c - it.r.ns + it.r.w0;
+        const int pid = table[page];
+        if (pid < 0 || pid >= a.num_pages) {
+          if (lane == 0) atomicOr(a.err, kErrPage);
+          continue;
+        }
+        const long long blk = static_cast<long long>(pid) * a.H + it.h;
+        const uint8_t* kp = a.kc + blk * (kPage * D);
+        const uint8_t* vp = a.vc + blk * (kPage * D);
+        uint32_t kw[2][Y::KW], vw[4][Y::VW];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < Y::KW; j += 4) {
+            const uint4 x = ldg128(kp + (g + 8 * r) * D + Y::k_ch(t, j));
+            kw[r][j] = x.x, kw[r][j + 1] = x.y, kw[r][j + 2] = x.z, kw[r][j + 3] = x.w;
+          }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint8_t* row = vp + (2 * t + (r & 1) + 8 * (r >> 1)) * D;
+          if (Y::VP == 2) {
+            const uint2 x = ldg64(row + Y::v_ch(g, 0));
+            vw[r][0] = x.x, vw[r][1] = x.y;
+          } else {
+#pragma unroll
+            for (int w = 0; w < Y::VW; w += 4) {
+              const uint4 x = ldg128(row + Y::v_ch(g, w));
+              vw[r][w] = x.x, vw[r][w + 1] = x.y, vw[r][(w + 2) % Y::VW] = x.z, vw[r][(w + 3) % Y::VW] = x.w;
+            }
+          }
+        }
+        const float kscale = a.ks[blk];
+        const int ev = static_cast<int>((__float_as_uint(a.vs[blk]) >> 23) & 0xFF) - 127;
+        const float evf = static_cast<float>(ev), vinv = exp2f(-evf);
+
+        // ---- scores ----
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < Y::KW; ++j) {
+          const uint32_t a0 = half2_of(kw[0][j]), a2 = half2_of(kw[0][j] >> 16);
+          const uint32_t a1 = half2_of(kw[1][j]), a3 = half2_of(kw[1][j] >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int hl = 0; hl < HL; ++hl) mma16816(s[nt], a0, a1, a2, a3, qf[nt][hl][j][0], qf[nt][hl][j][1]);
+        }
+        const int j0 = 16 * page;
+        // does every row see the whole page?
+        const bool full = j0 + 15 <= it.pmin && (!a.window || j0 > it.pmax - a.window || j0 + 15 < a.sinks);
+        uint32_t live = 0xFFFFu;                                 // tokens that some row sees
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nt][i] = s[nt][i] * kscale * rf[nt][i & 1];
+        if (!full) {
+          live = 0u;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int j = j0 + k;
+            if (j <= it.pmax && (!a.window || j > it.pmin - a.window || j < a.sinks)) live |= 1u << k;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = j0 + g + 8 * (i >> 1), p = pr[nt][i & 1];
+              if (!(j <= p && (!a.window || j > p - a.window || j < a.sinks))) s[nt][i] = -INFINITY;
+            }
+        }
+        // ---- weights ----
+        uint32_t pf[NT][HL][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int cidx = 0; cidx < 2; ++cidx) {
+            float mx = fmaxf(s[nt][cidx], s[nt][2 + cidx]) + evf;
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float mn = fmaxf(m[nt][cidx], mx);
+            if (mn > m[nt][cidx]) {
+              const float al = exp2_fast(m[nt][cidx] - mn);
+              l[nt][cidx] *= al;
+#pragma unroll
+              for (int i = 0; i < Y::MT; ++i) {
+                o[nt][i][cidx] *= al;
+                o[nt][i][2 + cidx] *= al;
+              }
+              m[nt][cidx] = mn;
+            }
+            // weights up to 2^15, so that fp16 keeps 11 bits of them down to 2^-29
+            const float base = mn == -INFINITY ? 0.0f : mn - evf - 15.0f;
+            w[cidx] = exp2_fast(s[nt][cidx] - base);
+            w[2 + cidx] = exp2_fast(s[nt][2 + cidx] - base);
+            l[nt][cidx] += (w[cidx] + w[2 + cidx]) * vinv;
+          }
+          __half hh[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) hh[i] = __float2half_rn(w[i]);
+          pf[nt][0][0] = transpose8(pack(hh[0], hh[1]));
+          pf[nt][0][1] = transpose8(pack(hh[2], hh[3]));
+          if (F32) {
+            __half ll[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ll[i] = __float2half_rn(w[i] - __half2float(hh[i]));
+            pf[nt][HL - 1][0] = transpose8(pack(ll[0], ll[1]));
+            pf[nt][HL - 1][1] = transpose8(pack(ll[2], ll[3]));
+          }
+        }
+        // ---- values ----
+        if (live != 0xFFFFu) {                                   // what no row sees may hold anything
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (!((live >> (2 * t + (r & 1) + 8 * (r >> 1))) & 1u))
+#pragma unroll
+              for (int w = 0; w < Y::VW; ++w) vw[r][w] = 0u;
+        }
+#pragma unroll
+        for (int w = 0; w < Y::VW; ++w) {
+          const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), x1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+          const uint32_t y0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), y1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+          const uint32_t a0 = half2_of(x0), a1 = half2_of(x0 >> 16), a2 = half2_of(y0), a3 = half2_of(y0 >> 16);
+          const uint32_t b0 = half2_of(x1), b1 = half2_of(x1 >> 16), b2 = half2_of(y1), b3 = half2_of(y1 >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int hl = 0; hl < HL; ++hl) {
+              mma16816(o[nt][2 * w], a0, a1, a2, a3, pf[nt][hl][0], pf[nt][hl][1]);
+              mma16816(o[nt][2 * w + 1], b0, b1, b2, b3, pf[nt][hl][0], pf[nt][hl][1]);
+            }
+        }
+      }
+
+      // ---- join the warps ----------------------------------------------------------------
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float sum = l[nt][c];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          const int row = 8 * nt + 2 * t + c;
+          if (g == 0) {
+            s_ml[warp][row][0] = m[nt][c];
+            s_ml[warp][row][1] = sum;
+          }
+#pragma unroll
+          for (int w = 0; w < Y::VW; ++w)
+            *reinterpret_cast<float4*>(sm + (warp * R + row) * D + Y::v_ch(g, w)) =
+                make_float4(o[nt][2 * w][c], o[nt][2 * w][2 + c], o[nt][2 * w + 1][c], o[nt][2 * w + 1][2 + c]);
+        }
+      __syncthreads();
+      for (int i = tid; i < R * D / 4; i += 32 * kRWarps) {
+        const int row = i / (D / 4), ch = 4 * (i % (D / 4));
+        if (row >= rows) continue;
+        float M = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kRWarps; ++w) M = fmaxf(M, s_ml[w][row][0]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (M == -INFINITY) {                                    // no key, or scores that are all NaN: L is 0 or NaN
+#pragma unroll
+          for (int w = 0; w < kRWarps; ++w) L += s_ml[w][row][1];
+        } else {
+#pragma unroll
+          for (int w = 0; w < kRWarps; ++w) {
+            const float f = exp2_fast(s_ml[w][row][0] - M);
+            L += f * s_ml[w][row][1];
+            const float4 x = *reinterpret_cast<const float4*>(sm + (w * R + row) * D + ch);
+            acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+          }
+        }
+        if (complete) {
+          const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
+          const long long gr = static_cast<long long>(it.rb) * R + row;
+          const long long at =
+              ((static_cast<long long>(it.b) * a.T + gr / a.G) * a.Hq + it.h * a.G + gr % a.G) * D + ch;
+          if (F32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) =
+                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          } else {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                                 y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+            *reinterpret_cast<uint2*>(static_cast<unsigned short*>(a.out) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+          }
+        } else {
+          float* p = a.part + (static_cast<long long>(slot) * R + row) * (D + 4);
+          *reinterpret_cast<float4*>(p + 4 + ch) = acc;
+          if (ch == 0) {
+            p[0] = M;
+            p[1] = L;
+          }
+        }
+      }
+      __syncthreads();
+    } else if (a.decode && !split && tid < 32) {                 // an empty sequence: zeros
+      const int dr = min(R, a.G - it.rb * R);
+      for (int i = lane; i < dr * D; i += 32) {
+        const long long at = (static_cast<long long>(it.b) * a.Hq + it.h * a.G + it.rb * R + i / D) * D + i % D;
+        if (F32) static_cast<float*>(a.out)[at] = 0.0f;
+        else static_cast<unsigned short*>(a.out)[at] = 0;
+      }
+    }
+    if (!split) {
+      whole += gridDim.x;
+      continue;
+    }
+    u0 = item_at + c1;
+    if (u0 >= u1) break;
+    item_at += it.pages;
+    if (++it.h == a.H) {
+      it.h = 0;
+      do load_entry(++entry);
+      while (it.pages == 0);
+    }
+  }
+}
+
+// Joins the partials of the items that cross spans: one block per (entry, head, row).
+template <int D, bool F32>
+__global__ void __launch_bounds__(128) kv8_join_kernel(const __grid_constant__ Kv8Attn a, int nrb, int R, int grid) {
+  __shared__ int s_sum[2][4];
+  __shared__ float4 s_acc[4][D / 4];
+  __shared__ float s_l[4];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int row = blockIdx.x % R, h = (blockIdx.x / R) % a.H, e = blockIdx.x / R / a.H;
+  pdl_wait();
+  pdl_trigger();
+  const Kv8Seq s = kv8_seq(a, e / nrb);
+  const long long gr = static_cast<long long>(e % nrb) * R + row;
+  if (gr >= static_cast<long long>(s.n) * a.G) return;
+  int before = 0, total = 0, x0, x1;
+  Kv8Range r;
+  for (int i = tid; i < a.B * nrb; i += 128) {
+    const int c = block_pages(a, kv8_seq(a, i / nrb), i % nrb, R, x0, x1, r);
+    total += c;
+    before += i < e ? c : 0;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if (lane == 0) s_sum[0][warp] = before, s_sum[1][warp] = total;
+  __syncthreads();
+  before = s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3];
+  total = s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3];
+  const int pages = block_pages(a, s, e % nrb, R, x0, x1, r);
+  long long span = (static_cast<long long>(total) * a.H + grid - 1) / grid;
+  span = span < kMinSpan ? kMinSpan : span;
+  const long long at = static_cast<long long>(before) * a.H + static_cast<long long>(h) * pages;
+  const int first = static_cast<int>(at / span), last = static_cast<int>((at + pages - 1) / span);
+  if (first == last) return;                                     // one CTA had it all and wrote it
+  auto part = [&](int c) {                                       // CTA c's partial of this row
+    return a.part + (static_cast<long long>(2 * c + (c == first ? 1 : 0)) * R + row) * (D + 4);
+  };
+  float M = -INFINITY;
+  for (int c = first + lane; c <= last; c += 32) M = fmaxf(M, part(c)[0]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.0f;
+  float4 acc[(D + 127) / 128];
+#pragma unroll
+  for (int i = 0; i < (D + 127) / 128; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (M == -INFINITY) {
+    for (int c = first + warp; c <= last; c += 4) L += part(c)[1];
+  } else {
+    for (int c = first + warp; c <= last; c += 4) {
+      const float* p = part(c);
+      const float f = exp2_fast(p[0] - M);
+      L += f * p[1];
+#pragma unroll
+      for (int i = 0; i < (D + 127) / 128; ++i) {
+        if (128 * i + 4 * lane >= D) continue;
+        const float4 x = *reinterpret_cast<const float4*>(p + 4 + 128 * i + 4 * lane);
+        acc[i].x += f * x.x, acc[i].y += f * x.y, acc[i].z += f * x.z, acc[i].w += f * x.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < (D + 127) / 128; ++i)
+    if (128 * i + 4 * lane < D) s_acc[warp][32 * i + lane] = acc[i];
+  if (lane == 0) s_l[warp] = L;
+  __syncthreads();
+  L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+  const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
+  const long long o = ((static_cast<long long>(e / nrb) * a.T + gr / a.G) * a.Hq + h * a.G + gr % a.G) * D;
+  for (int i = tid; i < D; i += 128) {
+    const float y = (reinterpret_cast<const float*>(s_acc[0])[i] + reinterpret_cast<const float*>(s_acc[1])[i] +
+                     reinterpret_cast<const float*>(s_acc[2])[i] + reinterpret_cast<const float*>(s_acc[3])[i]) * inv;
+    if (F32) static_cast<float*>(a.out)[o + i] = y;
+    else static_cast<__nv_bfloat16*>(a.out)[o + i] = __float2bfloat16(y);
+  }
+}
+
+// Query rows per block: 16 where a KV head has more than 8 (d = 256: its accumulators fill the registers at 8).
+int rows_per_block(int T, int G, int d) { return static_cast<long long>(T) * G > 8 && d <= 128 ? 16 : 8; }
+int row_blocks(int T, int G, int R) { return static_cast<int>((static_cast<long long>(T) * G + R - 1) / R); }
+
+int sm_count() {
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+constexpr int kCtasPerSm = 4;
+
+template <int D, int NT, bool F32>
+cudaError_t launch_t(const Kv8Attn& a, cudaStream_t s) {
+  constexpr int R = 8 * NT;
+  const long long nrb = row_blocks(a.T, a.G, R);
+  const long long entries = a.B * nrb, items = entries * a.H;
+  if (items > 0x7FFFFFFFLL || items * R > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  const int grid = kCtasPerSm * sm_count();
+  // spans across items while the list is short; with four items or more per CTA whole items balance as well
+  const bool split = entries <= kMaxEntries && items < 4LL * grid;
+  const size_t smem = sizeof(float) * kRWarps * R * D + (split ? sizeof(int) * entries : 0);
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = smem_attr_once(kv8_rows_kernel<D, NT, F32>,
+                                 static_cast<int>(sizeof(float) * kRWarps * R * D + sizeof(int) * kMaxEntries), configured);
+  if (e != cudaSuccess) return e;
+  const long long ctas = split ? grid : (items < 0x7FFFFFFF ? items : 0x7FFFFFFF);
+  e = launch_pdl(kv8_rows_kernel<D, NT, F32>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kRWarps), smem, s, a,
+                 static_cast<int>(nrb), split ? 1 : 0);
+  if (e != cudaSuccess || !split) return e;
+  return launch_pdl(kv8_join_kernel<D, F32>, dim3(static_cast<unsigned>(items * R)), dim3(128), 0, s, a,
+                    static_cast<int>(nrb), R, grid);
+}
+
+template <int D>
+cudaError_t launch_d(const Kv8Attn& a, bool f32, cudaStream_t s) {
+  if constexpr (D <= 128) {
+    if (rows_per_block(a.T, a.G, D) == 16) return f32 ? launch_t<D, 2, true>(a, s) : launch_t<D, 2, false>(a, s);
+  }
+  return f32 ? launch_t<D, 1, true>(a, s) : launch_t<D, 1, false>(a, s);
+}
+
+}  // namespace
+
+bool kv8_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
+
+size_t kv8_rows_workspace(int B, int T, int G, int H, int d) {
+  (void)B;
+  (void)H;
+  return sizeof(float) * 2 * kCtasPerSm * static_cast<size_t>(sm_count()) * rows_per_block(T, G, d) * (d + 4);
+}
+
+cudaError_t launch_kv8_rows(const Kv8Attn& a, int d, bool f32, cudaStream_t s) {
+  switch (d) {
+    case 64: return launch_d<64>(a, f32, s);
+    case 128: return launch_d<128>(a, f32, s);
+    case 256: return launch_d<256>(a, f32, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace tq

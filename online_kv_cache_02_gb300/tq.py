@@ -40,6 +40,18 @@ class TQConfig(ctypes.Structure):
                 ("k_qjl", ctypes.c_int), ("seed", ctypes.c_uint64), ("codebook", ctypes.c_int)]
 
 
+class TQKv8Cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("max_pages_per_seq", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("num_kv_heads", ctypes.c_int)]
+
+
+class TQRope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("num_axes", ctypes.c_int), ("section", ctypes.c_int * 4),
+                ("pos", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libtq.so is not built ({LIB_PATH}); run __graft_entry__.build() first")
@@ -83,6 +95,14 @@ EXPORTS = {
     "tq_causal_workspace_size": ([_P, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)], _S),
     "tq_causal_attention": ([_P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _I, _I, _P, _P, _I, ctypes.c_float, _P, _P, _SZ,
                              _P], _S),
+    "tq_kv8_cache_layout": ([_P, _I, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)], _S),
+    "tq_kv8_append": ([_P, ctypes.POINTER(TQKv8Cache), _P, _P, _P, _I, _I, _I, _I, _P, _P, ctypes.POINTER(TQRope), _P,
+                       ctypes.c_longlong, ctypes.c_longlong, ctypes.c_longlong, _P], _S),
+    "tq_kv8_workspace_size": ([_P, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)], _S),
+    "tq_kv8_decode_attention": ([_P, ctypes.POINTER(TQKv8Cache), _P, _I, _I, _I, _P, _I, _I, _I, ctypes.c_float, _P, _P,
+                                 _SZ, _P], _S),
+    "tq_kv8_causal_attention": ([_P, ctypes.POINTER(TQKv8Cache), _P, _I, _I, _I, _I, _P, _P, _I, _I, _I, ctypes.c_float,
+                                 _P, _P, _SZ, _P], _S),
     "tq_check_device_status": ([_P, ctypes.POINTER(ctypes.c_uint32)], _S),
     "tq_refine_counters": ([_P, ctypes.POINTER(ctypes.c_ulonglong), _I], _S),
     "tq_status_string": ([_S], ctypes.c_char_p),
@@ -319,3 +339,60 @@ def tq_search_scores(ctx, q, dtype, nq, k_cache, block_table, num_pages, n_db, k
     _check("tq_search_scores", _lib.tq_search_scores(ctx, _ptr(q), dtype, nq, _ptr(k_cache), _ptr(block_table),
                                                      num_pages, n_db, k_top, _ptr(scores), _ptr(workspace),
                                                      workspace_bytes, _stream(stream)))
+
+
+def make_kv8_cache(k_codes, v_codes, k_scale, v_scale, block_table, max_pages_per_seq, num_pages, num_kv_heads):
+    """Descriptor of an 8-bit paged cache (tq_kv8_cache).  Build it once and keep it with the buffers it points to:
+    it holds them alive."""
+    c = TQKv8Cache(_ptr(k_codes), _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), max_pages_per_seq,
+                   num_pages, num_kv_heads)
+    c.buffers = (k_codes, v_codes, k_scale, v_scale, block_table)
+    return c
+
+
+def make_rope(cos_sin, max_pos, rot_dim, interleaved=False, sections=None, pos=None):
+    """Rotation by position (tq_rope): sections, the pairs of each axis (None: one axis for all)."""
+    sections = [rot_dim // 2] if sections is None else list(sections)
+    if not 1 <= len(sections) <= 4:
+        raise ValueError("one to four axes")
+    r = TQRope(_ptr(cos_sin), max_pos, rot_dim, int(interleaved), len(sections), (ctypes.c_int * 4)(*sections), _ptr(pos))
+    r.buffers = (cos_sin, pos)
+    return r
+
+
+def tq_kv8_cache_layout(ctx, num_kv_heads):
+    """Bytes of one page's codes and of its scales (K and V alike)."""
+    c, s = _SZ(), _SZ()
+    _check("tq_kv8_cache_layout", _lib.tq_kv8_cache_layout(ctx, num_kv_heads, ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+def tq_kv8_append(ctx, cache, k, v, q, dtype, batch, n_new, num_q_heads, start_pos, new_lens=None, rope=None, q_out=None,
+                  k_stride=0, v_stride=0, q_stride=0, stream=None):
+    """Append to the 8-bit cache, keys and queries rotated on the way (see tq.h); strides in elements per token."""
+    _check("tq_kv8_append", _lib.tq_kv8_append(
+        ctx, cache, _ptr(k), _ptr(v), _ptr(q), dtype, batch, n_new, num_q_heads, _ptr(start_pos), _ptr(new_lens), rope,
+        _ptr(q_out), k_stride, v_stride, q_stride, _stream(stream)))
+
+
+def tq_kv8_workspace_size(ctx, batch, n_new, num_q_heads, num_kv_heads, max_seq_len):
+    n = _SZ()
+    _check("tq_kv8_workspace_size", _lib.tq_kv8_workspace_size(ctx, batch, n_new, num_q_heads, num_kv_heads, max_seq_len,
+                                                               ctypes.byref(n)))
+    return n.value
+
+
+def tq_kv8_decode_attention(ctx, cache, q, dtype, batch, num_q_heads, seq_lens, max_seq_len, window, sinks,
+                            softmax_scale, out, workspace, workspace_bytes, stream=None):
+    """Decode attention over the 8-bit cache with an optional sliding window and visible first tokens (see tq.h)."""
+    _check("tq_kv8_decode_attention", _lib.tq_kv8_decode_attention(
+        ctx, cache, _ptr(q), dtype, batch, num_q_heads, _ptr(seq_lens), max_seq_len, window, sinks, softmax_scale,
+        _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def tq_kv8_causal_attention(ctx, cache, q, dtype, batch, n_new, num_q_heads, start_pos, new_lens, max_seq_len, window,
+                            sinks, softmax_scale, out, workspace, workspace_bytes, stream=None):
+    """Causal attention of n_new tokens per sequence over the 8-bit cache (see tq.h)."""
+    _check("tq_kv8_causal_attention", _lib.tq_kv8_causal_attention(
+        ctx, cache, _ptr(q), dtype, batch, n_new, num_q_heads, _ptr(start_pos), _ptr(new_lens), max_seq_len, window,
+        sinks, softmax_scale, _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))

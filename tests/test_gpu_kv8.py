@@ -1,0 +1,651 @@
+"""The 8-bit paged cache on the GPU against the fp64 oracle: appended codes and scales bit for bit, attention within
+bounds that count each rounding.
+
+Attention's bounds, per output element, with A = sum_j p_j |v_j| and the seen keys n:
+  - the output's own rounding: half a step of its type, finfo.eps / 2 of the value;
+  - the weights as fp16 (2^-11 of each; fp32 input: hi + lo, 2^-22);
+  - a logit's error: fp32 sums of exact products over d channels in the tensor core, at most d/16 + 1 steps
+    each off by 2^-23 of the running size, times scale * sum |q k|; its scaling and the exponential: 2^-21 of
+    its own size and 2^-21 more; a logit off by x moves the weights' share by at most 2 x A;
+  - the sums over keys: n/16 steps in the value product and the joins, each off by 2^-23 of A.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import kv8
+
+from .gpu_common import DEV, th, to_dev, torch, tq, wl
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": (torch.bfloat16, tq.TQ_BF16), "f32": (torch.float32, tq.TQ_F32)}
+_CTX = {}
+
+
+def ctx_for(d):
+    if d not in _CTX:
+        _CTX[d] = tq.tq_create_ex(tq.make_config(d=d, k_split=d // 64 * 32, v_split=d // 64 * 32))
+    return _CTX[d]
+
+
+def values(rng, dtype, *shape):
+    x = rng.standard_normal(shape).astype(np.float32)
+    return wl.bf16_round(x) if dtype == "bf16" else x
+
+
+class Cache:
+    """A pool on both sides, filled alike: random codes (NaN codes among them where nobody may look) and scales."""
+
+    def __init__(self, rng, pages, h, d, batch, maxp, spread=3, nan=True):
+        self.h, self.d, self.pages, self.maxp = h, d, pages, maxp
+        self.codes, self.scales = {}, {}
+        for kind in "kv":
+            c = rng.integers(0, 256, (pages, h, 16, d)).astype(np.uint8)
+            if not nan:
+                c[(c & 127) == 127] = 0
+            self.codes[kind] = c
+            self.scales[kind] = np.exp2(rng.integers(-6 - spread, -5 + spread, (pages, h))).astype(np.float32)
+        self.table = rng.permutation(pages)[:batch * maxp].reshape(batch, maxp).astype(np.int32)
+        self.dev = None
+
+    def clean(self, rng, b, positions):
+        """Plain random values (no NaN codes) at the given positions of sequence b."""
+        pos = np.asarray(positions)
+        for kind in "kv":
+            x = rng.standard_normal((pos.size, self.h, self.d)) * 60
+            self.codes[kind][self.table[b, pos // 16], :, pos % 16] = kv8.e4m3_encode(x)
+
+    def to_device(self):
+        t = {k: to_dev(v) for k, v in (("kc", self.codes["k"]), ("vc", self.codes["v"]), ("ks", self.scales["k"]),
+                                       ("vs", self.scales["v"]), ("bt", self.table))}
+        self.dev = t
+        self.desc = tq.make_kv8_cache(t["kc"], t["vc"], t["ks"], t["vs"], t["bt"], self.maxp, self.pages, self.h)
+        return self.desc
+
+    def same_as_device(self):
+        for kind in "kv":
+            got, want = self.dev[kind + "c"].cpu().numpy(), self.codes[kind]
+            bad = np.argwhere(got != want)
+            assert bad.size == 0, (kind, len(bad), bad[:4].tolist(), [(int(got[tuple(i)]), int(want[tuple(i)])) for i in bad[:4]])
+            assert np.array_equal(self.dev[kind + "s"].cpu().numpy(), self.scales[kind]), kind
+
+
+# ---------------------------------------------------------------------------
+# append
+# ---------------------------------------------------------------------------
+def _table(rng, max_pos, rot):
+    ang = np.arange(max_pos)[:, None] * 10000.0 ** (-np.arange(rot // 2) / (rot // 2))
+    return np.concatenate([np.cos(ang), np.sin(ang)], axis=1).astype(np.float32)
+
+
+def _append_case(rng, dtype, d, h, hq, starts, n_new, lens=None, rot=None, interleaved=False, sections=None, fused=False,
+                 kinds="kvq", x=None, inplace=False, flags=0):
+    b = len(starts)
+    rot = d if rot is None else rot
+    maxp = (max(starts) + n_new + 15) // 16 + 1
+    c = Cache(rng, b * maxp + 2, h, d, b, maxp, nan=False)
+    dt, code = DT[dtype]
+    hosts = x or {"k": values(rng, dtype, b, n_new, h, d) * 5, "v": values(rng, dtype, b, n_new, h, d),
+                  "q": values(rng, dtype, b, n_new, hq, d)}
+    if dtype == "bf16":
+        hosts = {k: wl.bf16_round(v) for k, v in hosts.items()}
+    max_pos = max(starts) + n_new + 3
+    cs = _table(rng, max_pos, rot) if rot else None
+    pos = None
+    if rot and sections:
+        pos = rng.integers(0, max_pos, (len(sections), b, n_new)).astype(np.int32)
+    desc = c.to_device()
+    dev, strides = {}, {"k": 0, "v": 0, "q": 0}
+    if fused:
+        row = torch.cat([to_dev(hosts[k]).to(dt).flatten(2) for k in "qkv"], dim=-1).contiguous()
+        at = 0
+        for k, heads in (("q", hq), ("k", h), ("v", h)):
+            dev[k] = row[..., at * d:(at + heads) * d]
+            strides[k] = row.stride(1)
+            at += heads
+    else:
+        dev = {k: to_dev(hosts[k]).to(dt) for k in "kvq"}
+    q_out = dev["q"] if inplace else torch.full((b, n_new, hq, d), -7.0, dtype=dt, device=DEV)
+    rope = tq.make_rope(to_dev(cs), max_pos, rot, interleaved, sections, None if pos is None else to_dev(pos)) if rot else None
+    ctx = ctx_for(d)
+    get = lambda k: dev[k] if k in kinds else None  # noqa: E731
+    tq.tq_kv8_append(ctx, desc, get("k"), get("v"), get("q"), code, b, n_new, hq, to_dev(np.asarray(starts, np.int32)),
+                     None if lens is None else to_dev(np.asarray(lens, np.int32)), rope, q_out if "q" in kinds else None,
+                     strides["k"], strides["v"], strides["q"])
+    torch.cuda.synchronize()
+    assert tq.tq_check_device_status(ctx) == flags
+
+    def turned(y, s, t):      # one token's heads, as fp64
+        if not rot:
+            return y.astype(np.float64)
+        p = [starts[s] + t] if pos is None else pos[:, s, t]
+        axis = np.repeat(np.arange(len(sections)), sections) if pos is not None else np.zeros(rot // 2, int)
+        at = np.asarray(p)[axis]
+        i = np.arange(rot // 2)
+        return kv8.rotate(y.astype(np.float64), cs[at, i].astype(np.float64), cs[at, rot // 2 + i].astype(np.float64),
+                          interleaved)
+
+    got_q = q_out.float().cpu().numpy()
+    for s in range(b):
+        n = n_new if lens is None else lens[s]
+        if n and "k" in kinds:
+            kv8.append(c.codes["k"], c.scales["k"], c.table[s], starts[s],
+                       np.stack([turned(hosts["k"][s, t], s, t) for t in range(n)]))
+        if n and "v" in kinds:
+            kv8.append(c.codes["v"], c.scales["v"], c.table[s], starts[s], hosts["v"][s, :n].astype(np.float64))
+        if "q" in kinds:
+            for t in range(n):
+                want = turned(hosts["q"][s, t], s, t)
+                # one rounding to the type, and fp32's two products and one sum before it
+                size = np.abs(hosts["q"][s, t]).max(axis=-1, keepdims=True)
+                tol = np.abs(want) * torch.finfo(dt).eps / 2 + 2.0 ** -22 * size
+                assert np.all(np.abs(got_q[s, t] - want) <= tol), (s, t)
+            if not inplace:
+                assert np.all(got_q[s, n:] == -7.0)
+    c.same_as_device()
+    return c
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("h,hq,starts,n_new,fused", [(2, 8, [0, 5, 16, 31], 1, False), (3, 3, [7], 1, True),
+                                                     (1, 16, [0, 3, 15], 37, True), (8, 8, [33, 0], 16, False)])
+def test_append(dtype, d, h, hq, starts, n_new, fused):
+    rng = np.random.default_rng(3)
+    _append_case(rng, dtype, d, h, hq, starts, n_new, fused=fused)
+
+
+@pytest.mark.parametrize("d,rot,interleaved,sections", [(128, 128, True, None), (128, 64, False, None), (128, 32, True, None),
+                                                        (128, 0, False, None), (128, 128, False, [16, 24, 24]),
+                                                        (128, 128, False, [13, 50, 1]), (64, 32, True, [5, 11]),
+                                                        (256, 240, False, [100, 0, 19, 1]), (64, 64, False, [32])])
+def test_append_rotations(d, rot, interleaved, sections):
+    rng = np.random.default_rng(4)
+    _append_case(rng, "bf16", d, 2, 6, [4, 18], 21, rot=rot, interleaved=interleaved, sections=sections)
+    _append_case(rng, "f32", d, 2, 6, [4, 18], 5, rot=rot, interleaved=interleaved, sections=sections, fused=True)
+
+
+@pytest.mark.parametrize("kinds", ["k", "v", "q", "kv", "kq"])
+def test_append_parts(kinds):
+    _append_case(np.random.default_rng(5), "bf16", 128, 4, 8, [9, 0], 20, kinds=kinds)
+
+
+def test_append_padded_batch_and_queries_in_place():
+    rng = np.random.default_rng(6)
+    _append_case(rng, "bf16", 128, 2, 4, [3, 16, 40, 0], 35, lens=[35, 0, 1, 17])
+    _append_case(rng, "f32", 64, 2, 4, [3, 16], 35, inplace=True)
+
+
+def test_append_unaligned_rows():
+    """Token strides that are no multiple of 16 bytes, and a base that is not 16-byte aligned."""
+    rng = np.random.default_rng(7)
+    for dtype in ("bf16", "f32"):
+        dt, code = DT[dtype]
+        h, d, n = 2, 128, 19
+        c = Cache(rng, 6, h, d, 1, 3, nan=False)
+        desc = c.to_device()
+        x = values(rng, dtype, 1, n, 1, h * d + 3)[:, :, 0]
+        dev = to_dev(x).to(dt)
+        k = dev[..., 1:1 + h * d]
+        tq.tq_kv8_append(ctx_for(d), desc, k, k, None, code, 1, n, 0, to_dev(np.asarray([5], np.int32)), None, None, None,
+                         k.stride(1), k.stride(1), 0)
+        torch.cuda.synchronize()
+        y = x[0, :, 1:1 + h * d].reshape(n, h, d).astype(np.float64)
+        for kind in "kv":
+            kv8.append(c.codes[kind], c.scales[kind], c.table[0], 5, y)
+        c.same_as_device()
+
+
+def test_append_ties_and_scale_borders():
+    """Values half way between codes, maxima on a border (448 * 2^e exactly, and one step of the type above), and
+    rotations whose exact results stand on ties (cosine 1/2, sine 1/2 in binary)."""
+    rng = np.random.default_rng(8)
+    h, d, n = 4, 128, 16
+    ties = (kv8.VALUES[:126] + kv8.VALUES[1:127]) / 2
+    x = rng.choice(np.concatenate([ties, -ties]), (1, n, h, d)).astype(np.float32)
+    x[..., 5] = 448.0
+    x[:, :, 1, 5] = 450.0                          # bf16 just above the border: the next scale
+    x[:, :, 2] /= 2.0 ** 40
+    x[:, :, 3] *= 2.0 ** 30
+    c = Cache(rng, 4, h, d, 1, 2, nan=False)
+    cs = np.full((64, d), 0.5, np.float32)
+    desc = c.to_device()
+    ctx = ctx_for(d)
+    for dtype in ("f32", "bf16"):
+        dt, code = DT[dtype]
+        y = wl.bf16_round(x) if dtype == "bf16" else x
+        dev = to_dev(y).to(dt)
+        tq.tq_kv8_append(ctx, desc, dev, dev, None, code, 1, n, 0, to_dev(np.asarray([16], np.int32)), None,
+                         tq.make_rope(to_dev(cs), 64, d), None)
+        torch.cuda.synchronize()
+        assert tq.tq_check_device_status(ctx) == 0
+        half = np.full(d // 2, 0.5)
+        kv8.append(c.codes["k"], c.scales["k"], c.table[0], 16, kv8.rotate(y[0].astype(np.float64), half, half, False))
+        kv8.append(c.codes["v"], c.scales["v"], c.table[0], 16, y[0].astype(np.float64))
+        c.same_as_device()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64), ("bf16", 256)])
+def test_append_token_by_token_with_growth_rollback_and_reuse(dtype, d):
+    """One token at a time, sizes up and down by 2^20 (blocks grow, old codes go down into the subnormals), then a
+    rollback into the middle of a page, then the pages again for another sequence."""
+    rng = np.random.default_rng(9)
+    h = 2
+    c = Cache(rng, 5, h, d, 1, 3, nan=False)
+    desc = c.to_device()
+    ctx = ctx_for(d)
+    dt, code = DT[dtype]
+    steps = list(range(0, 21)) + list(range(9, 24)) + list(range(0, 5))
+    for p in steps:
+        x = values(rng, dtype, 1, 1, h, d) * np.float32(2.0 ** rng.integers(-10, 11))
+        dev = to_dev(x).to(dt)
+        tq.tq_kv8_append(ctx, desc, dev, dev, None, code, 1, 1, 0, to_dev(np.asarray([p], np.int32)))
+        torch.cuda.synchronize()
+        for kind in "kv":
+            kv8.append(c.codes[kind], c.scales[kind], c.table[0], p, x[0].astype(np.float64))
+        c.same_as_device()
+    assert tq.tq_check_device_status(ctx) == 0
+
+
+def test_append_values_that_are_not_finite():
+    rng = np.random.default_rng(10)
+    h, d = 2, 128
+    x = {"k": values(rng, "f32", 1, 20, h, d), "v": values(rng, "f32", 1, 20, h, d), "q": values(rng, "f32", 1, 20, 2, d)}
+    x["v"][0, 3, 0, 7] = np.nan
+    x["v"][0, 4, 0, 9] = np.inf
+    x["v"][0, 17, 1, 100] = -np.inf
+    x["v"][0, 18, 1, 1] = 3.3e38
+    x["k"][0, 2, 1, 70] = np.nan                    # without a rotation: one channel
+    _append_case(rng, "f32", d, h, 2, [6], 20, x=x, rot=0, flags=32)
+    x["k"][0, 2, 1, 70] = 1e30
+    x["v"] = values(rng, "f32", 1, 20, h, d) * 0    # blocks of zeros take the smallest scale
+    _append_case(rng, "f32", d, h, 2, [6], 20, x=x, rot=0)
+    x["k"][0, 5, 0, 3] = np.inf                     # with one: both of the pair
+    c = _append_nonfinite_rotated(rng, x["k"])
+    assert not np.isnan(kv8.VALUES[c]).any()
+
+
+def _append_nonfinite_rotated(rng, k):
+    h, d = k.shape[2:]
+    c = Cache(rng, 4, h, d, 1, 2, nan=False)
+    for kind in "kv":
+        c.codes[kind][:] = 0
+    desc = c.to_device()
+    tq.tq_kv8_append(ctx_for(d), desc, to_dev(k), None, None, tq.TQ_F32, 1, 20, 0, to_dev(np.asarray([6], np.int32)), None,
+                     tq.make_rope(to_dev(_table(rng, 64, d)), 64, d))
+    torch.cuda.synchronize()
+    assert tq.tq_check_device_status(ctx_for(d)) == 32
+    return c.dev["kc"].cpu().numpy()
+
+
+def test_append_skips_and_flags_what_is_out_of_range():
+    rng = np.random.default_rng(11)
+    h, d, dt = 2, 128, torch.bfloat16
+    ctx = ctx_for(d)
+    x = values(rng, "bf16", 3, 20, h, d)
+    dev = to_dev(x).to(dt)
+    c = Cache(rng, 8, h, d, 3, 2, nan=False)
+    c.table[0, 1] = 8                               # no such page
+    c.table[2, 0] = -1
+    desc = c.to_device()
+    tq.tq_kv8_append(ctx, desc, dev, dev, None, tq.TQ_BF16, 3, 20, 0, to_dev(np.asarray([0, 25, 12], np.int32)))
+    torch.cuda.synchronize()
+    assert tq.tq_check_device_status(ctx) == 1 | 2  # bad pages; positions 32 .. 44 behind the table
+    for kind in "kv":
+        kv8.append(c.codes[kind], c.scales[kind], c.table[0], 0, x[0, :16].astype(np.float64))
+        kv8.append(c.codes[kind], c.scales[kind], c.table[1], 25, x[1, :7].astype(np.float64))
+        kv8.append(c.codes[kind], c.scales[kind], c.table[2], 16, x[2, 4:20].astype(np.float64))
+    c.same_as_device()
+    # positions outside the cosines' table: those tokens are skipped, queries among them
+    q_out = torch.full((1, 4, 2, d), -7.0, dtype=dt, device=DEV)
+    pos = to_dev(np.asarray([[[0, 9, -1, 3]]], np.int32))
+    before = c.dev["kc"].clone()
+    tq.tq_kv8_append(ctx, desc, dev[:1, :4].contiguous(), None, dev[:1, :4].contiguous(), tq.TQ_BF16, 1, 4, 2,
+                     to_dev(np.asarray([0], np.int32)), None, tq.make_rope(to_dev(_table(rng, 9, d)), 9, d, pos=pos), q_out)
+    torch.cuda.synchronize()
+    assert tq.tq_check_device_status(ctx) == 2
+    after = c.dev["kc"]
+    page = int(c.table[0, 0])
+    assert torch.equal(before[page, :, 1:3], after[page, :, 1:3]) and not torch.equal(before[page, :, 0], after[page, :, 0])
+    assert bool((q_out[0, 1:3] == -7).all()) and not bool((q_out[0, 0] == -7).all())
+    # a start before the sequence and too many tokens
+    tq.tq_kv8_append(ctx, desc, dev, dev, None, tq.TQ_BF16, 3, 20, 0, to_dev(np.asarray([-1, -30, -2], np.int32)))
+    torch.cuda.synchronize()
+    assert tq.tq_check_device_status(ctx) == 4
+    assert torch.equal(after, c.dev["kc"])
+    # an earlier block whose scale is none: taken as the smallest
+    c.dev["ks"][c.table[0, 0].item()] = 3.0
+    tq.tq_kv8_append(ctx, desc, dev[:1, :1].contiguous(), None, None, tq.TQ_BF16, 1, 1, 0,
+                     to_dev(np.asarray([2], np.int32)))
+    torch.cuda.synchronize()
+    assert tq.tq_check_device_status(ctx) == 64
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+def _attend(c, q, dtype, causal, starts, lens=None, window=0, sinks=0, scale=None, max_len=None, stream=None, out=None):
+    """starts: cached tokens with the query's own (decode) or before the queries (causal)."""
+    dt, code = DT[dtype]
+    d = c.d
+    b, hq = q.shape[0], q.shape[-2]
+    n_new = q.shape[1] if causal else 1
+    scale = 1.0 / np.sqrt(d) if scale is None else scale
+    max_len = c.maxp * 16 if max_len is None else max_len
+    ctx = ctx_for(d)
+    n = tq.tq_kv8_workspace_size(ctx, b, n_new, hq, c.h, max_len)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+    out = torch.full(q.shape, -7.0, dtype=dt, device=DEV) if out is None else out
+    qd, ld = to_dev(q).to(dt), to_dev(np.asarray(starts, np.int32))
+    if causal:
+        tq.tq_kv8_causal_attention(ctx, c.desc, qd, code, b, n_new, hq, ld,
+                                   None if lens is None else to_dev(np.asarray(lens, np.int32)), max_len, window, sinks,
+                                   scale, out, ws, n, stream)
+    else:
+        tq.tq_kv8_decode_attention(ctx, c.desc, qd, code, b, hq, ld, max_len, window, sinks, scale, out, ws, n, stream)
+    torch.cuda.synchronize()
+    return out.float().cpu().numpy()
+
+
+def _bound(dtype, want, mag, dots, n, d, scale, extra_logit=0.0):
+    eps = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    w = 2.0 ** -11 if dtype == "bf16" else 2.0 ** -21
+    logit = abs(scale) * dots * ((d / 16 + 1) * 2.0 ** -23 + 2.0 ** -21 + extra_logit) + 2.0 ** -21
+    return np.abs(want) * eps + mag * (w + 2 * logit[:, None] + (n / 16 + 40) * 2.0 ** -23) * (1 + eps) + 1e-38
+
+
+def _check(c, got, q, dtype, causal, starts, lens=None, window=0, sinks=0, scale=None, rows=None, hidden=None,
+           extra_logit=0.0):
+    d = c.d
+    scale = 1.0 / np.sqrt(d) if scale is None else scale
+    for b, s in enumerate(starts):
+        n = (q.shape[1] if lens is None else lens[b]) if causal else 1
+        for t in range(n):
+            if rows is not None and (b, t) not in rows:
+                continue
+            p = s + t if causal else s - 1
+            x = q[b, t] if causal else q[b]
+            want, mag, dots, keys = kv8.attention(x, c.codes["k"], c.scales["k"], c.codes["v"], c.scales["v"], c.table[b], p,
+                                                  window, sinks, scale, () if hidden is None else hidden.get(b, ()))
+            y = got[b, t] if causal else got[b]
+            tol = _bound(dtype, want, mag, dots, keys, d, scale, extra_logit)
+            err = np.abs(y - want)
+            assert np.all(err <= tol), (b, t, keys, float(np.nanmax(err / tol)), int(np.isnan(y).sum()))
+        if causal:
+            assert np.all(got[b, n:] == -7.0), b
+
+
+def _seen(p, window, sinks):
+    j = np.arange(p + 1)
+    return j[kv8.visible(p, j, window, sinks)]
+
+
+def _decode_case(rng, dtype, d, h, hq, lens, window=0, sinks=0, scale=None, spread=3, extra=1):
+    b = len(lens)
+    maxp = max(1, (max(lens) + 15) // 16 + extra)
+    c = Cache(rng, b * maxp + 1, h, d, b, maxp, spread)
+    for i, n in enumerate(lens):
+        if n:
+            c.clean(rng, i, _seen(n - 1, window, sinks))
+    c.to_device()
+    q = values(rng, dtype, b, hq, d)
+    got = _attend(c, q, dtype, False, lens, window=window, sinks=sinks, scale=scale)
+    assert tq.tq_check_device_status(ctx_for(d)) == 0
+    _check(c, got, q, dtype, False, lens, window=window, sinks=sinks, scale=scale)
+    return c, q, got
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,h,hq", [(128, 2, 8), (64, 3, 3), (256, 1, 5), (128, 1, 16), (128, 4, 28), (64, 1, 40), (256, 2, 24)])
+def test_decode(dtype, d, h, hq):
+    _decode_case(np.random.default_rng(20), dtype, d, h, hq, [1, 0, 15, 16, 17, 130, 301, 64])
+
+
+@pytest.mark.parametrize("dtype,window,sinks", [("bf16", 1, 0), ("bf16", 16, 1), ("bf16", 17, 16), ("f32", 40, 20),
+                                                ("bf16", 1000, 4), ("f32", 100, 0), ("bf16", 33, 300), ("bf16", 0, 5)])
+def test_decode_window_and_sinks(dtype, window, sinks):
+    """Everything outside the window and the first tokens holds NaN codes."""
+    _decode_case(np.random.default_rng(21), dtype, 128, 2, 8, [1, 2, 16, 17, 18, 100, 333, 48], window, sinks)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.1, 0.5, 3.0])
+def test_decode_softmax_scales(dtype, scale):
+    _decode_case(np.random.default_rng(22), dtype, 128, 2, 6, [70, 333], scale=scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_block_scales_far_apart(dtype):
+    """Scales from 2^-60 to 2^60 across pages: the value scale rides in the weights' exponents."""
+    rng = np.random.default_rng(23)
+    c = Cache(rng, 24, 2, 128, 1, 20)
+    c.clean(rng, 0, range(310))
+    c.scales["v"][:] = np.exp2(rng.integers(-60, 61, c.scales["v"].shape))
+    c.scales["k"][:] = np.exp2(rng.integers(-40, -4, c.scales["k"].shape))
+    c.to_device()
+    q = values(rng, dtype, 1, 4, 128)
+    q[0, 1] *= 2.0 ** -100
+    q[0, 2] *= 2.0 ** 20
+    q[0, 3] = 0
+    _check(c, _attend(c, q, dtype, False, [310]), q, dtype, False, [310])
+
+
+@pytest.mark.parametrize("dtype,d,h,hq,lens", [("bf16", 128, 8, 32, [9000]), ("f32", 128, 1, 4, [40000]),
+                                               ("bf16", 64, 2, 4, [5000, 1, 12000]), ("bf16", 256, 2, 4, [20001])])
+def test_decode_split_over_the_context(dtype, d, h, hq, lens):
+    _decode_case(np.random.default_rng(24), dtype, d, h, hq, lens)
+
+
+def test_decode_many_short_sequences():
+    rng = np.random.default_rng(25)
+    _decode_case(rng, "bf16", 128, 8, 16, [int(x) for x in rng.integers(0, 40, 420)])
+    _decode_case(rng, "bf16", 64, 1, 2, [int(x) for x in rng.integers(0, 20, 2100)])
+
+
+def test_decode_query_that_is_not_finite_spoils_only_its_row():
+    rng = np.random.default_rng(26)
+    c = Cache(rng, 9, 1, 128, 1, 8)
+    c.clean(rng, 0, range(100))
+    c.to_device()
+    q = values(rng, "f32", 1, 4, 128)
+    q[0, 1, 5] = np.nan
+    q[0, 2, 5] = np.inf
+    got = _attend(c, q, "f32", False, [100])
+    assert np.isnan(got[0, 1]).all() and np.isnan(got[0, 2]).all()
+    keep = [0, 3]
+    _check(c, got[:, keep], q[:, keep], "f32", False, [100])
+
+
+def test_decode_bad_pages_and_lengths():
+    rng = np.random.default_rng(27)
+    lens = [100, 40, 16]
+    c = Cache(rng, 30, 2, 128, 3, 8)
+    for i, n in enumerate(lens):
+        c.clean(rng, i, range(n))
+    c.table[0, 2], c.table[0, 5], c.table[2, 0] = 30, -1, 1 << 30
+    c.to_device()
+    q = values(rng, "bf16", 3, 4, 128)
+    got = _attend(c, q, "bf16", False, lens)
+    ctx = ctx_for(128)
+    assert tq.tq_check_device_status(ctx) == 1
+    _check(c, got, q, "bf16", False, lens, hidden={0: [*range(32, 48), *range(80, 96)], 2: range(16)})
+    assert np.all(got[2] == 0)
+    # lengths: negative counts as empty, beyond max_seq_len or the table as cut
+    got = _attend(c, q, "bf16", False, [-5, 41, 16], max_len=40)
+    assert tq.tq_check_device_status(ctx) == 4 | 1
+    assert np.all(got[0] == 0)
+    want, mag, dots, n = kv8.attention(q[1], c.codes["k"], c.scales["k"], c.codes["v"], c.scales["v"], c.table[1], 39, 0, 0,
+                                       1 / np.sqrt(128))
+    assert np.all(np.abs(got[1] - want) <= _bound("bf16", want, mag, dots, n, 128, 1 / np.sqrt(128)))
+
+
+def _causal_case(rng, dtype, d, h, hq, starts, n_new, lens=None, window=0, sinks=0, scale=None, rows=None, extra_logit=0.0):
+    b = len(starts)
+    real = [n_new] * b if lens is None else lens
+    maxp = max(1, (max(s + n for s, n in zip(starts, real)) + 15) // 16 + 1)
+    c = Cache(rng, b * maxp + 1, h, d, b, maxp)
+    for i, (s, n) in enumerate(zip(starts, real)):
+        if n:
+            see = sorted(set().union(*[set(_seen(p, window, sinks).tolist()) for p in range(s, s + n)])) if window else range(s + n)
+            c.clean(rng, i, list(see))
+    c.to_device()
+    q = values(rng, dtype, b, n_new, hq, d)
+    got = _attend(c, q, dtype, True, starts, lens, window, sinks, scale)
+    assert tq.tq_check_device_status(ctx_for(d)) == 0
+    if rows is not None:
+        rows = {(b_, int(t)) for b_ in range(b) for t in rng.integers(0, max(1, real[b_]), rows) if real[b_]}
+        rows |= {(b_, t) for b_ in range(b) for t in (0, real[b_] - 1) if real[b_]}
+    _check(c, got, q, dtype, True, starts, lens, window, sinks, scale, rows, extra_logit=extra_logit)
+    return c, q, got
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,h,hq,starts,n_new,lens", [(128, 2, 8, [0, 17, 100], 5, None), (128, 1, 4, [0, 31], 1, None),
+                                                      (64, 2, 2, [3, 0, 50, 9], 33, [33, 0, 1, 20]),
+                                                      (256, 1, 6, [10], 9, None), (128, 4, 28, [64, 0], 7, [7, 2]),
+                                                      (128, 1, 12, [200], 3, None)])
+def test_causal_few_rows(dtype, d, h, hq, starts, n_new, lens):
+    _causal_case(np.random.default_rng(30), dtype, d, h, hq, starts, n_new, lens)
+
+
+@pytest.mark.parametrize("dtype,window,sinks", [("bf16", 1, 0), ("f32", 7, 3), ("bf16", 24, 16), ("bf16", 200, 4), ("bf16", 16, 40)])
+def test_causal_few_rows_window(dtype, window, sinks):
+    _causal_case(np.random.default_rng(31), dtype, 128, 2, 6, [0, 40, 150], 5, None, window, sinks)
+
+
+@pytest.mark.parametrize("dtype,d,h,hq,starts,n_new,lens,window,sinks", [
+    ("bf16", 128, 2, 8, [0], 300, None, 0, 0), ("bf16", 128, 1, 4, [1000, 0], 200, [200, 77], 0, 0),
+    ("bf16", 128, 2, 14, [130, 5, 0], 257, [257, 1, 128], 64, 4), ("bf16", 128, 1, 1, [31], 700, None, 100, 0),
+    ("bf16", 128, 1, 4, [20000], 130, None, 0, 0), ("bf16", 128, 1, 5, [9], 513, None, 1, 1),
+    ("f32", 128, 2, 4, [50], 200, None, 90, 3), ("bf16", 64, 1, 8, [77], 150, None, 0, 0),
+    ("f32", 256, 1, 2, [3], 100, None, 0, 0), ("bf16", 128, 8, 32, [0, 300], 160, None, 128, 17)])
+def test_causal_many_rows(dtype, d, h, hq, starts, n_new, lens, window, sinks):
+    _causal_case(np.random.default_rng(32), dtype, d, h, hq, starts, n_new, lens, window, sinks, rows=40)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.08, 0.7])
+def test_causal_softmax_scales(scale):
+    _causal_case(np.random.default_rng(33), "bf16", 128, 2, 8, [60], 140, scale=scale, rows=40)
+
+
+def test_causal_bad_pages_and_lengths():
+    rng = np.random.default_rng(34)
+    c = Cache(rng, 40, 2, 128, 2, 16)
+    c.clean(rng, 0, range(230))
+    c.clean(rng, 1, range(200))
+    c.table[0, 3] = -7
+    c.to_device()
+    q = values(rng, "bf16", 2, 100, 8, 128)
+    ctx = ctx_for(128)
+    got = _attend(c, q, "bf16", True, [130, 100])
+    assert tq.tq_check_device_status(ctx) == 1
+    _check(c, got, q, "bf16", True, [130, 100], hidden={0: range(48, 64)}, rows={(0, 0), (0, 57), (0, 99), (1, 0), (1, 99)})
+    # queries beyond max_seq_len and a padded count that is none are cut; rows that are not answered stay
+    got = _attend(c, q, "bf16", True, [130, -3], lens=[1000, 5], max_len=200)
+    assert tq.tq_check_device_status(ctx) == 4 | 1
+    assert np.all(got[0, 70:] == -7) and np.all(got[1] == -7) and not np.any(np.all(got[0, :70] == -7, axis=-1))
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+def _steps(dtype, d, h, hq, window, sinks, graph=False):
+    """A prompt of each sequence, then single tokens, then five drafted ones: append + attention on one stream."""
+    rng = np.random.default_rng(40)
+    b, dt, code = 3, DT[dtype][0], DT[dtype][1]
+    ctx = ctx_for(d)
+    maxp = 14
+    c = Cache(rng, b * maxp, h, d, b, maxp)
+    desc = c.to_device()
+    cs = _table(rng, 300, d)
+    rope = tq.make_rope(to_dev(cs), 300, d)
+    lens = np.asarray([0, 0, 0], np.int32)
+    stream = torch.cuda.Stream()
+    for n_new, new in ((150, [150, 97, 16]), (1, [1, 1, 1]), (1, [1, 1, 1]), (5, [5, 5, 5]), (1, [1, 1, 1])):
+        x = {k: values(rng, dtype, b, n_new, hh, d) for k, hh in (("k", h), ("v", h), ("q", hq))}
+        dev = {k: to_dev(v).to(dt) for k, v in x.items()}
+        n = tq.tq_kv8_workspace_size(ctx, b, n_new, hq, h, 16 * maxp)
+        ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+        q_rot = torch.zeros(b, n_new, hq, d, dtype=dt, device=DEV)
+        out = torch.full((b, n_new, hq, d), -7.0, dtype=dt, device=DEV)
+        start, cnt, after = to_dev(lens), to_dev(np.asarray(new, np.int32)), to_dev(lens + np.asarray(new, np.int32))
+        torch.cuda.synchronize()
+
+        def call(st):
+            tq.tq_kv8_append(ctx, desc, dev["k"], dev["v"], dev["q"], code, b, n_new, hq, start, cnt, rope, q_rot, stream=st)
+            if n_new == 1:
+                tq.tq_kv8_decode_attention(ctx, desc, q_rot, code, b, hq, after, 16 * maxp, window, sinks, d ** -0.5, out, ws,
+                                           n, st)
+            else:
+                tq.tq_kv8_causal_attention(ctx, desc, q_rot, code, b, n_new, hq, start, cnt, 16 * maxp, window, sinks,
+                                           d ** -0.5, out, ws, n, st)
+
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                call(torch.cuda.current_stream())
+            out.fill_(-7.0)
+            torch.cuda.synchronize()
+            g.replay()
+            g.replay()                      # a step again: the same positions, the same bytes
+        else:
+            call(stream)
+        torch.cuda.synchronize()
+        assert tq.tq_check_device_status(ctx) == 0
+        got, q_got = out.float().cpu().numpy(), q_rot.float().cpu().numpy()
+        for s in range(b):
+            p0 = int(lens[s])
+            ks = np.stack([kv8.rotate(x["k"][s, t].astype(np.float64), cs[p0 + t, :d // 2].astype(np.float64),
+                                      cs[p0 + t, d // 2:].astype(np.float64), False) for t in range(new[s])])
+            kv8.append(c.codes["k"], c.scales["k"], c.table[s], p0, ks)
+            kv8.append(c.codes["v"], c.scales["v"], c.table[s], p0, x["v"][s, :new[s]].astype(np.float64))
+        c.same_as_device()
+        _check(c, got, q_got, dtype, True, [int(v) for v in lens], new, window, sinks)
+        lens = lens + np.asarray(new, np.int32)
+
+
+@pytest.mark.parametrize("dtype,d,h,hq,window,sinks", [("bf16", 128, 2, 8, 0, 0), ("bf16", 128, 1, 4, 40, 4),
+                                                       ("f32", 64, 2, 4, 0, 0), ("bf16", 256, 1, 3, 33, 16)])
+def test_prompt_then_steps_then_drafts(dtype, d, h, hq, window, sinks):
+    _steps(dtype, d, h, hq, window, sinks)
+
+
+def test_prompt_then_steps_then_drafts_captured():
+    _steps("bf16", 128, 2, 8, 0, 0, graph=True)
+
+
+def test_results_repeat_bit_for_bit():
+    rng = np.random.default_rng(41)
+    c = Cache(rng, 700, 2, 128, 2, 300)
+    c.clean(rng, 0, range(4700))
+    c.clean(rng, 1, range(900))
+    c.to_device()
+    q = values(rng, "bf16", 2, 70, 8, 128)
+    a = _attend(c, q, "bf16", True, [4600, 800])
+    b = _attend(c, q, "bf16", True, [4600, 800])
+    assert np.array_equal(a, b)
+    a = _attend(c, q[:, 0], "bf16", False, [4700, 900])
+    assert np.array_equal(a, _attend(c, q[:, 0], "bf16", False, [4700, 900]))
+
+
+def test_two_streams_at_once():
+    """Two calls that overlap on the GPU, each with its own workspace."""
+    rng = np.random.default_rng(42)
+    c = Cache(rng, 600, 4, 128, 1, 550)
+    c.clean(rng, 0, range(8700))
+    c.to_device()
+    q = values(rng, "bf16", 1, 16, 128)
+    want = _attend(c, q, "bf16", False, [8700])
+    ctx, dt = ctx_for(128), torch.bfloat16
+    n = tq.tq_kv8_workspace_size(ctx, 1, 1, 16, 4, 8800)
+    qd, ld = to_dev(q).to(dt), to_dev(np.asarray([8700], np.int32))
+    runs = [(torch.cuda.Stream(), torch.empty(n, dtype=torch.uint8, device=DEV), torch.empty(1, 16, 128, dtype=dt, device=DEV))
+            for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, ws, out in runs:
+            tq.tq_kv8_decode_attention(ctx, c.desc, qd, tq.TQ_BF16, 1, 16, ld, 8800, 0, 0, 128 ** -0.5, out, ws, n, st)
+    torch.cuda.synchronize()
+    for _, _, out in runs:
+        assert np.array_equal(out.float().cpu().numpy(), want)
