@@ -250,9 +250,9 @@ def _run_own(st):
     stream = torch.cuda.current_stream()
     new = st["new"] if c["ragged"] else None
     if c["op"] == "append":
+        row = (c["heads"] + 2 * c["kv_heads"]) * c["d"] if c["fused"] else 0      # elements from token to token
         tq.tq_kv8_append(ctx, cache, st["k"], st["v"], st["q"], code, c["batch"], c["n_new"], c["heads"],
-                         st["cached"], new, rope, st["q_out"], st["k"].stride(1), st["v"].stride(1),
-                         st["q"].stride(1), stream)
+                         st["cached"], new, rope, st["q_out"], row, row, row, stream)
         return {"k": st["kc"], "v": st["vc"], "k_scale": st["ks"], "v_scale": st["vs"], "q": st["q_out"]}
     scale = 1.0 / math.sqrt(c["d"])
     if c["op"] == "decode":
