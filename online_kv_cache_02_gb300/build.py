@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libtq.so")
 SOURCES = ["tq_api.cu", "tq_quantize.cu", "tq_quantize_tc.cu", "tq_quantize_pipe.cu", "tq_decode.cu", "tq_decode_lut.cu", "tq_noalloc.cu", "tq_search.cu", "tq_search_tc.cu", "tq_causal_tc.cu",
-           "tq_generic.cu", "tq_kv8_append.cu", "tq_kv8_rows.cu",
+           "tq_generic.cu", "tq_kv8_append.cu", "tq_kv8_rows.cu", "tq_kv8_tc.cu",
            "tq_host.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]

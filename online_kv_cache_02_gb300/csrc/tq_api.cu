@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -952,6 +953,9 @@ tq_status kv8_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void
   if (!q || !lens || !out || !workspace || misaligned(q) || misaligned(out) || misaligned(workspace))
     return TQ_ERR_INVALID_ARG;
   if (static_cast<long long>(batch) * n_new * Hq > 0x7FFFFFFFLL / 16) return TQ_ERR_UNSUPPORTED;
+  // positions lie below both: a window or sinks beyond them change nothing (and the kernels' sums stay in 32 bits)
+  const long long cap = std::min<long long>(max_seq_len, static_cast<long long>(kPage) * cache->max_pages_per_seq);
+  if (cap > (1LL << 29)) return TQ_ERR_UNSUPPORTED;
   size_t need = 0;
   st = tq_kv8_workspace_size(ctx, batch, n_new, Hq, H, max_seq_len, &need);
   if (st != TQ_OK) return st;
@@ -977,12 +981,15 @@ tq_status kv8_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void
   a.vc = static_cast<const uint8_t*>(cache->v_codes);
   a.ks = cache->k_scale;
   a.vs = cache->v_scale;
-  a.window = window;
-  a.sinks = sinks;
+  a.window = window < cap ? window : 0;
+  a.sinks = static_cast<int>(std::min<long long>(sinks, cap));
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.part = static_cast<float*>(workspace);
   a.err = ctx->tab.err;
-  return cuda_status(launch_kv8_rows(a, ctx->cfg.d, dtype == TQ_F32, static_cast<cudaStream_t>(stream)));
+  const bool f32 = dtype == TQ_F32;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (kv8_tc_takes(n_new, a.G, ctx->cfg.d, f32, softmax_scale)) return cuda_status(launch_kv8_tc(a, s));
+  return cuda_status(launch_kv8_rows(a, ctx->cfg.d, f32, s));
 }
 }  // namespace
 
@@ -1062,7 +1069,8 @@ extern "C" tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_n
   if (!ctx || !bytes || batch < 0 || n_new < 1 || Hq < 1 || H < 1 || Hq % H || max_seq_len < 0)
     return TQ_ERR_INVALID_ARG;
   if (!kv8_head_dim(ctx->cfg.d)) return TQ_ERR_UNSUPPORTED;
-  *bytes = kv8_rows_workspace(batch, n_new, Hq / H, H, ctx->cfg.d);
+  *bytes = std::max(kv8_rows_workspace(batch, n_new, Hq / H, H, ctx->cfg.d),
+                    ctx->cfg.d == kD ? kv8_tc_workspace(batch, n_new, Hq / H, H, max_seq_len) : 0);
   return TQ_OK;
 }
 

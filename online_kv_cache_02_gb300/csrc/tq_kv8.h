@@ -86,6 +86,11 @@ bool kv8_head_dim(int d);
 cudaError_t launch_kv8_append(const Kv8Append& a, int d, bool f32, cudaStream_t s);
 size_t kv8_rows_workspace(int B, int T, int G, int H, int d);
 cudaError_t launch_kv8_rows(const Kv8Attn& a, int d, bool f32, cudaStream_t s);
+// Many query rows on the tensor cores (tq_kv8_tc.cu): whether the call takes
+// that form, its workspace and its launch.
+bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale);
+size_t kv8_tc_workspace(int B, int T, int G, int H, int max_seq_len);
+cudaError_t launch_kv8_tc(const Kv8Attn& a, cudaStream_t s);
 
 }  // namespace tq
 

@@ -1,0 +1,704 @@
+// Causal attention of many query rows over the 8-bit paged cache on the tensor
+// cores (tcgen05), bf16 queries, d = 128.
+//
+// An item is (sequence, KV head, block of 256 query rows r = t G + g, chunk of
+// its pages); keys go by in tiles of 128 tokens (8 pages):
+//   S = (Qh + Ql) Kc^T    kind::f8f6f4 straight from the cache's codes, which TMA
+//                         puts in place: no conversion of K.  A query row, scaled
+//                         by a power of two, is the sum of two e4m3 parts: exact
+//                         for bf16 down to 2^-10 of the row's largest value, off
+//                         by at most 2^-17 of it below;
+//   w = 2^(f S + ev - M)  f = scale log2(e) 2^ek 2^-row per page, ev the page's
+//                         value exponent, M the row's running maximum (moved only
+//                         when passed by 2^8): block scales cost no instruction
+//                         beyond the softmax's own multiply-add;
+//   O += w Vc             w as fp16 in tensor memory, Vc as fp16 (exact), turned
+//                         from codes by four warps, token rows read MN-major;
+//   l += w 2^-ev,  out = O / l.
+//
+// Two 128-row halves A and B of the block take turns: while the softmax of one
+// runs, the tensor cores work on the other.  Tensor memory: S of A and B (each
+// overlaid by its weights), O of A and B, 512 columns.  Warps 0-3 and 4-7: the
+// softmax of A and B (thread = row), which also split the queries and write the
+// results; 8-11: values to fp16; 12: items, pages and TMA; 13: MMA issue.
+// Every wait is bounded; a wait that gives up sets the device error word.
+
+#include "tq_kv8.h"
+#include "tq_tc.cuh"
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+namespace tq {
+namespace {
+
+using namespace tcx;
+
+constexpr int kTD = 128;                  // head dimension
+constexpr int kTRows = 256;               // query rows per item
+constexpr int kTTok = 128;                // tokens per tile
+constexpr int kTPg = kTTok / kPage;       // pages per tile
+constexpr int kTThreads = 512;
+constexpr int kKSt = 3, kVSt = 2;         // raw K and V stages
+constexpr int kDescs = 8;
+constexpr float kMNone = -1.0e30f;
+constexpr float kSlack = 8.0f, kLift = 7.0f;   // weights lie below 2^15, the newest maximum's at 2^7 or above
+constexpr int kPartRow = kTD + 4;
+constexpr int kNoPage = 1 << 30;          // first position of a page that is not there: no query sees it
+
+struct TileDesc {                         // one tile of the stream, by page
+  float fac[kTPg];                        // scale log2(e) 2^ek
+  float ev[kTPg];                         // value exponent
+  float vinv[kTPg];                       // 2^-ev
+  int j0[kTPg];                           // first position
+  int full, pad[3];                       // every row of the block sees every token
+};
+
+// shared memory, from a 1024-byte boundary
+constexpr int kOffQ = 0;                              // [A, B][hi, lo][128 rows][128 B]
+constexpr int kOffK = kOffQ + 4 * 16384;              // [stage][128 tokens][128 B]
+constexpr int kOffVr = kOffK + kKSt * 16384;          // [stage][128 tokens][128 B]
+constexpr int kOffV = kOffVr + kVSt * 16384;          // [buffer][2 halves of 64 channels][128 tokens][128 B]
+constexpr int kOffDesc = kOffV + 2 * 32768;
+constexpr int kOffItem = kOffDesc + kDescs * static_cast<int>(sizeof(TileDesc));
+constexpr int kOffBar = kOffItem + kDescs * 8;
+enum Bar {
+  bKFull = 0, bKEmpty = bKFull + kKSt, bVFull = bKEmpty + kKSt, bVEmpty = bVFull + kVSt, bVReady = bVEmpty + kVSt,
+  bVFree = bVReady + 2, bSFull = bVFree + 2, bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2,
+  bItem = bQReady + 2, bDesc = bItem + kDescs, bDrain = bDesc + kDescs, bCount
+};
+constexpr int kOffTmem = kOffBar + 8 * bCount;
+constexpr int kTSmem = kOffTmem + 16 + 1024;
+static_assert(kTSmem <= 232448, "shared memory per block");
+// tensor-memory columns of half X
+__device__ __forceinline__ constexpr uint32_t col_s(int X) { return 128u * X; }
+__device__ __forceinline__ constexpr uint32_t col_o(int X) { return 256u + 128u * X; }
+
+__device__ __forceinline__ void mma_f8_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// kind::f8f6f4, fp32 accumulate, e4m3 A and B, K-major, M = 128, N = 128
+constexpr uint32_t kIdF8 = (1u << 4) | (static_cast<uint32_t>(kTTok >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+constexpr uint32_t kIdPV = idesc_f16(kTD) | (1u << 16);          // B MN-major
+// MN-major operand, 128-byte swizzle: token rows of 64 channels, 8-row groups 1024 B apart, channel halves 16 KB apart
+__device__ __forceinline__ uint64_t vdesc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16384 >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap* map, int blk, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(blk), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes_to_half2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(two)));
+  return r;
+}
+__device__ __forceinline__ uint32_t to_codes(float lo, float hi) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+struct TItem {
+  int b, h, qb, chunk;
+  int p0, rows;                           // first query position, query rows of the block (<= 256)
+  int pmin, pmax;
+  Kv8Range r;
+  int c0, c1;                             // pages of the list
+};
+__device__ __forceinline__ bool tc_item(const Kv8Attn& a, int idx, int nqb, int nch, TItem& it) {
+  it.chunk = idx % nch;
+  int rest = idx / nch;
+  it.h = rest % a.H;
+  rest = a.B * nqb - 1 - rest / a.H;      // the longest rows first
+  it.qb = rest / a.B;
+  it.b = rest % a.B;
+  const Kv8Seq s = kv8_seq(a, it.b);
+  const long long rows = static_cast<long long>(s.n) * a.G, r0 = static_cast<long long>(it.qb) * kTRows;
+  it.p0 = s.p0;
+  if (r0 >= rows) return false;
+  it.rows = static_cast<int>(rows - r0 < kTRows ? rows - r0 : kTRows);
+  it.pmin = s.p0 + static_cast<int>(r0 / a.G);
+  it.pmax = s.p0 + static_cast<int>((r0 + it.rows - 1) / a.G);
+  it.r = kv8_range(a.window, a.sinks, it.pmin, it.pmax);
+  const int pages = it.r.ns + it.r.nw, tiles = (pages + kTPg - 1) / kTPg, per = (tiles + nch - 1) / nch;
+  it.c0 = it.chunk * per * kTPg;
+  it.c1 = min(pages, it.c0 + per * kTPg);
+  return it.c0 < it.c1;
+}
+
+__global__ void __launch_bounds__(kTThreads, 1)
+    kv8_tc_kernel(const __grid_constant__ Kv8Attn a, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, int nqb, int nch, int items) {
+  extern __shared__ __align__(1024) unsigned char sm_raw[];
+  unsigned char* sm = sm_raw + ((0u - su32(sm_raw)) & 1023u);
+  const uint32_t sb = su32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto bar = [&](int i) { return sb + kOffBar + 8u * static_cast<uint32_t>(i); };
+  TileDesc* descs = reinterpret_cast<TileDesc*>(sm + kOffDesc);
+  int* item_ring = reinterpret_cast<int*>(sm + kOffItem);
+
+  if (tid == 0) {
+    for (int i = 0; i < kKSt; ++i) {
+      bar_init(bar(bKFull + i), 1);
+      bar_init(bar(bKEmpty + i), 1);
+    }
+    for (int i = 0; i < kVSt; ++i) {
+      bar_init(bar(bVFull + i), 1);
+      bar_init(bar(bVEmpty + i), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bar(bVReady + i), 4);
+      bar_init(bar(bVFree + i), 1);
+      bar_init(bar(bSFull + i), 1);
+      bar_init(bar(bPFull + i), 4);
+      bar_init(bar(bODone + i), 1);
+      bar_init(bar(bQReady + i), 4);
+    }
+    for (int i = 0; i < kDescs; ++i) {
+      bar_init(bar(bItem + i), 1);
+      bar_init(bar(bDesc + i), 1);
+    }
+    bar_init(bar(bDrain), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 13) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kOffTmem), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_trigger();
+  fence_async_smem();
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + kOffTmem);
+  bool failed = false;
+  // a warp's wait for phase `phase` of a barrier; once one gave up, every later one returns at once
+  auto wait = [&](int i, int phase) {
+    if (__all_sync(0xffffffffu, bar_wait(bar(i), phase & 1, failed))) return true;
+    failed = true;
+    return false;
+  };
+  // the n-th item of this CTA (-1: no more), from the ring
+  auto next_item = [&](int n) {
+    if (!wait(bItem + n % kDescs, n / kDescs)) return -1;
+    return *reinterpret_cast<volatile int*>(item_ring + n % kDescs);
+  };
+
+  if (warp < 8) {
+    // ---- softmax of half X (thread = row), the queries' split, the results ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    const int X = warp >> 2, wq = warp & 3, r = 32 * wq + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * wq) << 16);
+    const uint32_t ts = trow + col_s(X), to = trow + col_o(X);
+    const float sgn = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
+    int seq = 0, nS = 0, nO = 0;                       // tiles seen, phases of S and of the final O
+    for (int n = 0;; ++n) {
+      const int idx = next_item(n);
+      if (idx < 0) break;
+      TItem it;
+      tc_item(a, idx, nqb, nch, it);
+      const int ntile = (it.c1 - it.c0 + kTPg - 1) / kTPg;
+      if (128 * X >= it.rows) {                        // this half is empty
+        seq += ntile;
+        continue;
+      }
+      const int rr = 128 * X + r;                      // row of the block
+      const long long gr = static_cast<long long>(it.qb) * kTRows + rr;
+      const int tok = static_cast<int>(gr / a.G);
+      const bool live = rr < it.rows;
+      const int p = live ? it.p0 + tok : -1;           // an absent row sees nothing
+      const long long at = ((static_cast<long long>(it.b) * a.T + tok) * a.Hq + it.h * a.G + static_cast<int>(gr % a.G)) * kTD;
+      float rowf;
+      {
+        // the row as two e4m3 parts, scaled so that its largest value lies in [128, 256).  The last QK MMA of the
+        // item before has run: its scores were read.
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+        uint4 w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+        uint32_t mx = 0u;                              // largest magnitude: bf16 bits order as integers
+#pragma unroll
+        for (int i = 0; i < 64; ++i) mx = max(mx, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
+        int e = 7 - (static_cast<int>(mx >> 7) - 127);
+        e = mx && mx < 0x7F80u ? min(e, 120) : 0;
+        const float up = __int_as_float((e + 127) << 23) * sgn;
+        rowf = __int_as_float((127 - e) << 23);
+        const uint32_t qh = sb + kOffQ + X * 32768 + r * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t u0 = u[8 * c + 2 * k], u1 = u[8 * c + 2 * k + 1];
+            const float v0 = __uint_as_float(u0 << 16) * up, v1 = __uint_as_float(u0 & 0xFFFF0000u) * up;
+            const float v2 = __uint_as_float(u1 << 16) * up, v3 = __uint_as_float(u1 & 0xFFFF0000u) * up;
+            const uint32_t h01 = to_codes(v0, v1), h23 = to_codes(v2, v3);
+            const uint32_t f01 = codes_to_half2(h01), f23 = codes_to_half2(h23);
+            const float2 g01 = __half22float2(*reinterpret_cast<const __half2*>(&f01));
+            const float2 g23 = __half22float2(*reinterpret_cast<const __half2*>(&f23));
+            hi[k] = h01 | (h23 << 16);
+            lo[k] = to_codes(v0 - g01.x, v1 - g01.y) | (to_codes(v2 - g23.x, v3 - g23.y) << 16);
+          }
+          const uint32_t off = static_cast<uint32_t>((c ^ (r & 7)) << 4);
+          sts128(qh + off, hi[0], hi[1], hi[2], hi[3]);
+          sts128(qh + 16384 + off, lo[0], lo[1], lo[2], lo[3]);
+        }
+        // a row that is not finite: every score NaN, and so the result
+        if (mx >= 0x7F80u) rowf = __int_as_float(0x7FC00000);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(bQReady + X));
+      }
+      float m = kMNone, l = 0.0f;
+      for (int t = 0; t < ntile; ++t, ++seq) {
+        if (!wait(bDesc + seq % kDescs, seq / kDescs) || !wait(bSFull + X, nS)) break;
+        ++nS;
+        tc_after();
+        const TileDesc& d = descs[seq % kDescs];
+        float x[kTTok];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tld32(ts + 32u * c, *reinterpret_cast<float(*)[32]>(x + 32 * c));
+        if (!d.full) {
+#pragma unroll
+          for (int pg = 0; pg < kTPg; ++pg) {
+            const int j0 = d.j0[pg], hi = p - j0;                  // slots up to hi
+            uint32_t see = hi < 0 ? 0u : hi >= 15 ? 0xFFFFu : (2u << hi) - 1u;
+            if (a.window) {
+              const int lo = hi - a.window + 1, sk = a.sinks - j0; // from lo on, or below sk
+              const uint32_t win = lo <= 0 ? 0xFFFFu : lo > 15 ? 0u : 0xFFFFu << lo;
+              const uint32_t snk = sk <= 0 ? 0u : sk > 15 ? 0xFFFFu : (1u << sk) - 1u;
+              see &= win | snk;
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[16 * pg + k] = (see >> k) & 1u ? x[16 * pg + k] : -INFINITY;
+          }
+        }
+        float f[kTPg], mx = -INFINITY;
+#pragma unroll
+        for (int pg = 0; pg < kTPg; ++pg) {
+          f[pg] = fmaxf(d.fac[pg] * rowf, 1.2e-38f) + (rowf - rowf);   // never zero (hidden scores stay -inf); NaN stays
+          float mp = x[16 * pg];
+#pragma unroll
+          for (int k = 1; k < 16; ++k) mp = fmaxf(mp, x[16 * pg + k]);
+          mx = fmaxf(mx, fmaf(mp, f[pg], d.ev[pg]));
+        }
+        const bool moved = mx > m + kSlack;
+        if (__any_sync(0xffffffffu, moved)) {
+          const float alpha = moved ? ex2(m - mx) : 1.0f;
+          if (moved) {
+            m = mx;
+            l *= alpha;
+          }
+          if (t > 0) {                                 // O of the tiles before (their MMAs have run: S came after)
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              float o[16];
+              uint32_t u[16];
+              tld16(to + 16u * c, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * alpha);
+              tst16(to + 16u * c, u);
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int pg = 2 * c + q;
+            const float base = d.ev[pg] - m + kLift;
+            float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float w0 = ex2(fmaf(x[16 * pg + 2 * k], f[pg], base));
+              const float w1 = ex2(fmaf(x[16 * pg + 2 * k + 1], f[pg], base));
+              s0 += w0;
+              s1 += w1;
+              w[8 * q + k] = half2_bits(w0, w1);
+            }
+            l = fmaf(s0 + s1, d.vinv[pg], l);
+          }
+          tst16(ts + 16u * c, w);
+        }
+        tst_wait();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(bPFull + X));
+      }
+      if (failed) break;
+      // ---- the row's result (or partial) ----
+      if (!wait(bODone + X, nO)) break;
+      ++nO;
+      tc_after();
+      const float inv = l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
+      float* part = a.part + ((static_cast<long long>((it.b * a.H + it.h)) * nqb + it.qb) * nch + it.chunk) *
+                                 (static_cast<long long>(kTRows) * kPartRow) + static_cast<long long>(rr) * kPartRow;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        tld32(to + 32u * c, o);
+        if (!live) continue;
+        if (nch == 1) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
+            w[k] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        } else {
+          float4* dst = reinterpret_cast<float4*>(part + 4 + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          if (c == 0) *reinterpret_cast<float2*>(part) = make_float2(m, l);
+        }
+      }
+      tc_before();                                     // O is read before the next item's first P is announced
+    }
+  } else if (warp < 12) {
+    // ---- values to fp16: thread = token of the tile ----------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    const int t = tid - 256, pg = t >> 4;
+    int seq = 0;
+    for (int n = 0;; ++n) {
+      const int idx = next_item(n);
+      if (idx < 0) break;
+      TItem it;
+      tc_item(a, idx, nqb, nch, it);
+      const int ntile = (it.c1 - it.c0 + kTPg - 1) / kTPg;
+      for (int i = 0; i < ntile; ++i, ++seq) {
+        if (!wait(bVFull + seq % kVSt, seq / kVSt)) break;
+        if (seq >= 2 && !wait(bVFree + (seq & 1), (seq - 2) >> 1)) break;
+        const int j = descs[seq % kDescs].j0[pg] + (t & 15);
+        // what no row sees may hold anything: zeros instead
+        const bool see = j <= it.pmax && (!a.window || j > it.pmin - a.window || j < a.sinks);
+        const uint32_t src = sb + kOffVr + (seq % kVSt) * 16384 + t * 128;
+        const uint32_t dst = sb + kOffV + (seq & 1) * 32768 + t * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint4 w = lds128(src + static_cast<uint32_t>((c ^ (t & 7)) << 4));
+          if (!see) w = make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t o0 = static_cast<uint32_t>((((2 * c) & 7) ^ (t & 7)) << 4),
+                         o1 = static_cast<uint32_t>((((2 * c + 1) & 7) ^ (t & 7)) << 4);
+          const uint32_t half = dst + (c >> 2) * 16384;
+          sts128(half + o0, codes_to_half2(w.x), codes_to_half2(w.x >> 16), codes_to_half2(w.y), codes_to_half2(w.y >> 16));
+          sts128(half + o1, codes_to_half2(w.z), codes_to_half2(w.z >> 16), codes_to_half2(w.w), codes_to_half2(w.w >> 16));
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(bar(bVReady + (seq & 1)));
+          bar_arrive(bar(bVEmpty + seq % kVSt));
+        }
+      }
+      if (failed) break;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 12) {
+      // ---- items, pages, TMA ----------------------------------------------------------------
+      int seq = 0, n = 0, nk = 0, nv = 0;              // tiles, and copies issued
+      auto publish = [&](int idx) {
+        if (lane == 0) {
+          *reinterpret_cast<volatile int*>(item_ring + n % kDescs) = idx;
+          bar_arrive(bar(bItem + n % kDescs));
+        }
+        ++n;
+      };
+      const int grid = gridDim.x;
+      for (int k = 0;; ++k) {                          // back and forth over the list, longest items first
+        const int idx = k * grid + ((k & 1) ? grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
+        if (k * grid >= items) break;
+        if (idx >= items) continue;
+        TItem it;
+        if (!tc_item(a, idx, nqb, nch, it)) continue;
+        publish(idx);
+        const int* table = a.bt + static_cast<long long>(it.b) * a.maxp;
+        for (int c = it.c0; c < it.c1; c += kTPg, ++seq) {
+          // lane p < 8: page p of the tile
+          const int ci = c + lane;
+          int blk = -1, j0 = kNoPage;
+          float ks = 1.0f;
+          int ev = 0;
+          if (lane < kTPg && ci < it.c1) {
+            const int page = ci < it.r.ns ? ci : ci - it.r.ns + it.r.w0;
+            const int pid = table[page];
+            if (pid >= 0 && pid < a.num_pages) {
+              blk = pid * a.H + it.h;
+              j0 = kPage * page;
+              ks = a.ks[blk];
+              ev = static_cast<int>((__float_as_uint(a.vs[blk]) >> 23) & 0xFF) - 127;
+            } else {
+              atomicOr(a.err, kErrPage);
+            }
+          }
+          const bool seen = j0 + 15 <= it.pmin && (!a.window || j0 > it.pmax - a.window || j0 + 15 < a.sinks);
+          const bool full = (__ballot_sync(0xffffffffu, seen) & 0xFFu) == 0xFFu;
+          const uint32_t mask = __ballot_sync(0xffffffffu, blk >= 0);
+          if (seq >= kKSt && !wait(bKEmpty + seq % kKSt, seq / kKSt - 1)) break;
+          TileDesc& d = descs[seq % kDescs];
+          if (lane < kTPg) {
+            d.fac[lane] = fabsf(a.scale_log2) * ks;
+            d.ev[lane] = static_cast<float>(ev);
+            d.vinv[lane] = exp2f(static_cast<float>(-ev));
+            d.j0[lane] = j0;
+            if (lane == 0) d.full = full ? 1 : 0;
+          }
+          __syncwarp();
+          const uint32_t bytes = static_cast<uint32_t>(__popc(mask)) * kPage * kTD;
+          if (lane == 0) {
+            bar_arrive(bar(bDesc + seq % kDescs));
+            if (bytes) bar_arrive_tx(bar(bKFull + seq % kKSt), bytes);
+            else bar_arrive(bar(bKFull + seq % kKSt));
+          }
+          __syncwarp();
+          ++nk;
+          if (blk >= 0) tma_block(sb + kOffK + (seq % kKSt) * 16384 + lane * kPage * kTD, &mk, blk, bar(bKFull + seq % kKSt));
+          if (seq >= kVSt && !wait(bVEmpty + seq % kVSt, seq / kVSt - 1)) break;
+          if (lane == 0) {
+            if (bytes) bar_arrive_tx(bar(bVFull + seq % kVSt), bytes);
+            else bar_arrive(bar(bVFull + seq % kVSt));
+          }
+          __syncwarp();
+          ++nv;
+          if (blk >= 0) tma_block(sb + kOffVr + (seq % kVSt) * 16384 + lane * kPage * kTD, &mv, blk, bar(bVFull + seq % kVSt));
+        }
+        if (failed) break;
+      }
+      publish(-1);
+      // copies still in flight land before the CTA ends
+      bool f2 = false;
+      for (int s = nk >= kKSt ? nk - kKSt : 0; s < nk; ++s) (void)bar_wait(bar(bKFull + s % kKSt), (s / kKSt) & 1, f2);
+      for (int s = nv >= kVSt ? nv - kVSt : 0; s < nv; ++s) (void)bar_wait(bar(bVFull + s % kVSt), (s / kVSt) & 1, f2);
+    } else if (warp == 13) {
+      // ---- MMA issue, the warp converged ------------------------------------------------------
+      auto qk = [&](int X, int s) {
+        const uint32_t q = sb + kOffQ + X * 32768, k = sb + kOffK + (s % kKSt) * 16384;
+        tc_after();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma_f8_warp(tmem + col_s(X), sdesc(q + 32 * j), sdesc(k + 32 * j), kIdF8, j > 0 ? 1u : 0u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma_f8_warp(tmem + col_s(X), sdesc(q + 16384 + 32 * j), sdesc(k + 32 * j), kIdF8, 1u);
+        mma_commit_warp(bar(bSFull + X));
+      };
+      auto pv = [&](int X, int s, bool first) {
+        const uint32_t v = sb + kOffV + (s & 1) * 32768;
+        tc_after();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          mma_ts_warp(tmem + col_o(X), tmem + col_s(X) + 8u * j, vdesc(v + 2048u * j), kIdPV, first && j == 0 ? 0u : 1u);
+      };
+      int seq = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+      // tile seq + 1's scores are issued before the MMA warp turns to tile seq's other half
+      int n = 0, idx = next_item(n);
+      TItem it;
+      int tiles = 0, halves = 0;
+      auto open_item = [&]() {
+        tc_item(a, idx, nqb, nch, it);
+        tiles = (it.c1 - it.c0 + kTPg - 1) / kTPg;
+        halves = it.rows > 128 ? 2 : 1;
+      };
+      // scores of half X of tile s (the first of an item waits for its queries)
+      auto scores = [&](int X, int s, bool first) {
+        if (first) {
+          if (!wait(bQReady + X, nq[X])) return false;
+          ++nq[X];
+        }
+        if (!wait(bKFull + s % kKSt, s / kKSt)) return false;
+        qk(X, s);
+        return true;
+      };
+      bool ok = idx >= 0;
+      if (ok) {
+        open_item();
+        for (int X = 0; X < halves && ok; ++X) ok = scores(X, 0, true);
+        if (ok) mma_commit_warp(bar(bKEmpty));
+      }
+      while (ok && idx >= 0) {
+        const int my_tiles = tiles, my_halves = halves;
+        for (int t = 0; t < my_tiles && ok; ++t, ++seq) {
+          const bool last = t == my_tiles - 1;
+          int nhalves = my_halves;
+          if (last) {                                  // what comes after this item
+            idx = next_item(++n);
+            if (failed) ok = false;
+            nhalves = 0;
+            if (idx >= 0) {
+              open_item();
+              nhalves = halves;
+            }
+          }
+          if (!ok) break;
+          ok = wait(bVReady + (seq & 1), seq >> 1);
+          for (int X = 0; X < 2 && ok; ++X) {
+            if (X < my_halves) {
+              ok = wait(bPFull + X, np[X]);
+              if (!ok) break;
+              ++np[X];
+              pv(X, seq, t == 0);
+              if (X == my_halves - 1) mma_commit_warp(bar(bVFree + (seq & 1)));
+              if (last) mma_commit_warp(bar(bODone + X));
+            }
+            if (X < nhalves) {
+              ok = scores(X, seq + 1, last);
+              if (ok && X == nhalves - 1) mma_commit_warp(bar(bKEmpty + (seq + 1) % kKSt));
+            }
+          }
+        }
+      }
+      mma_commit_warp(bar(bDrain));                    // every MMA issued completes before the CTA ends
+      bool f2 = false;
+      (void)bar_wait(bar(bDrain), 0, f2);
+      __syncwarp();
+    }
+  }
+  if (failed && lane == 0) atomicOr(a.err, kErrTimeout);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// Joins the chunks of an item's rows: a warp per row.
+__global__ void __launch_bounds__(256) kv8_tc_join_kernel(const __grid_constant__ Kv8Attn a, int nqb, int nch) {
+  const int lane = threadIdx.x & 31;
+  const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int rr = static_cast<int>(w % kTRows);
+  const long long blk = w / kTRows;                    // (b H + h) nqb + qb
+  pdl_wait();
+  pdl_trigger();
+  const int qb = static_cast<int>(blk % nqb), h = static_cast<int>(blk / nqb % a.H), b = static_cast<int>(blk / nqb / a.H);
+  if (b >= a.B) return;
+  const Kv8Seq s = kv8_seq(a, b);
+  const long long gr = static_cast<long long>(qb) * kTRows + rr;
+  if (gr >= static_cast<long long>(s.n) * a.G) return;
+  // chunks that had pages: the same cut as the items'
+  const long long r0 = static_cast<long long>(qb) * kTRows, rows = static_cast<long long>(s.n) * a.G;
+  const int last = static_cast<int>((r0 + kTRows < rows ? r0 + kTRows : rows) - 1);
+  const Kv8Range r = kv8_range(a.window, a.sinks, s.p0 + static_cast<int>(r0 / a.G), s.p0 + last / a.G);
+  const int tiles = (r.ns + r.nw + kTPg - 1) / kTPg, per = (tiles + nch - 1) / nch, used = (tiles + per - 1) / per;
+  const float* p = a.part + blk * nch * (static_cast<long long>(kTRows) * kPartRow) + static_cast<long long>(rr) * kPartRow;
+  const long long step = static_cast<long long>(kTRows) * kPartRow;
+  float M = kMNone;
+  for (int c = 0; c < used; ++c) M = fmaxf(M, p[c * step]);
+  float L = 0.0f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < used; ++c) {
+    const float f = ex2(p[c * step] - M);
+    L = fmaf(f, p[c * step + 1], L);
+    const float4 x = *reinterpret_cast<const float4*>(p + c * step + 4 + 4 * lane);
+    acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y), acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
+  }
+  const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
+  const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  const long long at = ((static_cast<long long>(b) * a.T + gr / a.G) * a.Hq + h * a.G + gr % a.G) * kTD + 4 * lane;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+}
+
+int sm_count() {
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+int query_blocks(int T, int G) { return static_cast<int>((static_cast<long long>(T) * G + kTRows - 1) / kTRows); }
+
+// Chunks per item: one where the items alone fill the SMs; else as many as give each SM an item, of four tiles
+// at least (the partials are written and read once more).
+int chunks_for(long long items, int max_seq_len) {
+  const int sms = sm_count();
+  if (items >= sms) return 1;
+  const long long tiles = (max_seq_len + kTTok - 1) / kTTok;
+  long long n = sms / items;
+  n = n < tiles / 4 ? n : tiles / 4;
+  return n < 1 ? 1 : static_cast<int>(n);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {        // from the driver, looked up once
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+}  // namespace
+
+bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const int row = d < 128 ? d : 128;                   // 128-byte panels
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), kPage, static_cast<cuuint64_t>(blocks)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(d) * kPage};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(row), kPage, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale) {
+  return d == kTD && !f32 && static_cast<long long>(T) * G > 32 && softmax_scale != 0.0f &&
+         std::fabs(static_cast<double>(softmax_scale)) <= (1.0 + 1e-6) / std::sqrt(static_cast<double>(kTD));
+}
+
+size_t kv8_tc_workspace(int B, int T, int G, int H, int max_seq_len) {
+  const long long items = static_cast<long long>(B) * H * query_blocks(T, G);
+  const int nch = items > 0 ? chunks_for(items, max_seq_len) : 1;
+  return nch == 1 ? 16 : sizeof(float) * static_cast<size_t>(items) * nch * kTRows * kPartRow;
+}
+
+cudaError_t launch_kv8_tc(const Kv8Attn& a, cudaStream_t s) {
+  const int nqb = query_blocks(a.T, a.G);
+  const long long items1 = static_cast<long long>(a.B) * a.H * nqb;
+  const int nch = chunks_for(items1, a.max_seq_len);
+  const long long items = items1 * nch;
+  if (items > (1LL << 30)) return cudaErrorInvalidConfiguration;
+  CUtensorMap mk, mv;
+  const long long blocks = static_cast<long long>(a.num_pages) * a.H;
+  if (!kv8_block_map(&mk, a.kc, blocks, kTD) || !kv8_block_map(&mv, a.vc, blocks, kTD)) return cudaErrorInvalidValue;
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = smem_attr_once(kv8_tc_kernel, kTSmem, configured);
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  e = launch_pdl(kv8_tc_kernel, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kTThreads), kTSmem, s, a, mk, mv,
+                 nqb, nch, static_cast<int>(items));
+  if (e != cudaSuccess || nch == 1) return e;
+  return launch_pdl(kv8_tc_join_kernel, dim3(static_cast<unsigned>(items1 * (kTRows / 8))), dim3(256), 0, s, a, nqb, nch);
+}
+
+}  // namespace tq

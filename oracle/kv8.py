@@ -93,7 +93,8 @@ def visible(p, j, window, sinks):
 
 
 def attention(q, codes_k, scale_k, codes_v, scale_v, row, p, window, sinks, softmax_scale, hidden=()):
-    """q [hq][d] of one query at position p: (out, sum of weight * |value|, largest sum |q k| over the seen keys, seen).
+    """q [hq][d] of one query at position p: (out, sum of weight * |value|, and over the seen keys the largest sum |q k|,
+    the largest sum |k|, and their number).
     `hidden`: positions that are not there."""
     hq, d = q.shape
     h = codes_k.shape[1]
@@ -101,9 +102,9 @@ def attention(q, codes_k, scale_k, codes_v, scale_v, row, p, window, sinks, soft
     j = np.arange(p + 1)
     seen = visible(p, j, window, sinks) & ~np.isin(j, list(hidden))
     j = j[seen]
-    out, mag, dots = np.zeros((hq, d)), np.zeros((hq, d)), np.zeros(hq)
+    out, mag, dots, ksum = np.zeros((hq, d)), np.zeros((hq, d)), np.zeros(hq), np.zeros(hq)
     if j.size == 0:
-        return out, mag, dots, 0
+        return out, mag, dots, ksum, 0
     pg, sl = np.asarray(row)[j // PAGE], j % PAGE
     for kv in range(h):
         k = VALUES[codes_k[pg, kv, sl]] * scale_k[pg, kv].astype(np.float64)[:, None]
@@ -114,4 +115,5 @@ def attention(q, codes_k, scale_k, codes_v, scale_v, row, p, window, sinks, soft
             w /= w.sum()
             out[a], mag[a] = w @ v, w @ np.abs(v)
             dots[a] = (np.abs(k) @ np.abs(q[a].astype(np.float64))).max()
-    return out, mag, dots, j.size
+            ksum[a] = np.abs(k).sum(axis=1).max()
+    return out, mag, dots, ksum, j.size
