@@ -20,7 +20,7 @@
 // runs, the tensor cores work on the other.  Tensor memory: S of A and B (each
 // overlaid by its weights), O of A and B, 512 columns.  Warps 0-3 and 4-7: the
 // softmax of A and B (thread = row), which also split the queries and write the
-// results; 8-11: values to fp16; 12: items, pages and TMA; 13: MMA issue.
+// results; 8-11: values to fp16; 12: items, pages and TMA; 13, 14: MMA issue of A and B.
 // Every wait is bounded; a wait that gives up sets the device error word.
 
 #include "tq_kv8.h"
@@ -47,7 +47,9 @@ constexpr int kTThreads = 512;
 constexpr int kKSt = 3, kVSt = 2;         // raw K and V stages
 constexpr int kDescs = 8;
 constexpr float kMNone = -1.0e30f;
-constexpr float kSlack = 8.0f, kLift = 7.0f;   // weights lie below 2^15, the newest maximum's at 2^7 or above
+// Weights lie below 2^(kLift + kSlack) = 2^15 (fp16 ends at 2^16); M is set kHead above the largest score met, so that
+// it seldom moves again: the largest weight is then 2^3 at least, and fp16 keeps 11 bits down to 2^-17 of it.
+constexpr float kSlack = 8.0f, kLift = 7.0f, kHead = 4.0f;
 constexpr int kPartRow = kTD + 4;
 constexpr int kNoPage = 1 << 30;          // first position of a page that is not there: no query sees it
 
@@ -70,7 +72,7 @@ constexpr int kOffBar = kOffItem + kDescs * 8;
 enum Bar {
   bKFull = 0, bKEmpty = bKFull + kKSt, bVFull = bKEmpty + kKSt, bVEmpty = bVFull + kVSt, bVReady = bVEmpty + kVSt,
   bVFree = bVReady + 2, bSFull = bVFree + 2, bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2,
-  bItem = bQReady + 2, bDesc = bItem + kDescs, bDrain = bDesc + kDescs, bCount
+  bItem = bQReady + 2, bDesc = bItem + kDescs, bDrain = bDesc + kDescs, bCount = bDrain + 2
 };
 constexpr int kOffTmem = kOffBar + 8 * bCount;
 constexpr int kTSmem = kOffTmem + 16 + 1024;
@@ -122,6 +124,47 @@ __device__ __forceinline__ uint32_t to_codes(float lo, float hi) {
   return r;
 }
 
+// Pairs of fp32 in one 64-bit register (Blackwell's packed fp32 arithmetic).
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 128 columns of this thread's lane: four loads in flight, one wait.  The values pass through an empty statement
+// behind the wait, so that nothing uses them before it.
+__device__ __forceinline__ void tld32_start(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void pin8(float* v) {
+  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]));
+}
+__device__ __forceinline__ void tld32x4(uint32_t taddr, float (&v)[128]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tld32_start(taddr + 32u * i, v + 32 * i);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) pin8(v + 8 * i);
+}
 struct TItem {
   int b, h, qb, chunk;
   int p0, rows;                           // first query position, query rows of the block (<= 256)
@@ -164,7 +207,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kKSt; ++i) {
       bar_init(bar(bKFull + i), 1);
-      bar_init(bar(bKEmpty + i), 1);
+      bar_init(bar(bKEmpty + i), 2);
     }
     for (int i = 0; i < kVSt; ++i) {
       bar_init(bar(bVFull + i), 1);
@@ -172,17 +215,17 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(bar(bVReady + i), 4);
-      bar_init(bar(bVFree + i), 1);
+      bar_init(bar(bVFree + i), 2);
       bar_init(bar(bSFull + i), 1);
       bar_init(bar(bPFull + i), 4);
       bar_init(bar(bODone + i), 1);
       bar_init(bar(bQReady + i), 4);
+      bar_init(bar(bDrain + i), 1);
     }
     for (int i = 0; i < kDescs; ++i) {
       bar_init(bar(bItem + i), 1);
       bar_init(bar(bDesc + i), 1);
     }
-    bar_init(bar(bDrain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 13) {
@@ -282,71 +325,118 @@ __global__ void __launch_bounds__(kTThreads, 1)
         ++nS;
         tc_after();
         const TileDesc& d = descs[seq % kDescs];
-        float x[kTTok];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tld32(ts + 32u * c, *reinterpret_cast<float(*)[32]>(x + 32 * c));
-        if (!d.full) {
+        // never zero (a hidden score stays -inf), and NaN stays NaN
+        auto factor = [&](int pg) { return fmaxf(d.fac[pg] * rowf, 1.2e-38f) + (rowf - rowf); };
+        // The tile as it mostly is: every token seen and no score far above the maximum so far.  Weights by the old
+        // maximum while the new one is found out; stored only if it holds.
+        bool done = false;
+        if (d.full && t > 0) {
+          float x[kTTok];
+          uint32_t w[kTTok / 2];
+          tld32x4(ts, x);
+          float mx = -INFINITY, lt = l;
 #pragma unroll
           for (int pg = 0; pg < kTPg; ++pg) {
-            const int j0 = d.j0[pg], hi = p - j0;                  // slots up to hi
-            uint32_t see = hi < 0 ? 0u : hi >= 15 ? 0xFFFFu : (2u << hi) - 1u;
-            if (a.window) {
-              const int lo = hi - a.window + 1, sk = a.sinks - j0; // from lo on, or below sk
-              const uint32_t win = lo <= 0 ? 0xFFFFu : lo > 15 ? 0u : 0xFFFFu << lo;
-              const uint32_t snk = sk <= 0 ? 0u : sk > 15 ? 0xFFFFu : (1u << sk) - 1u;
-              see &= win | snk;
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[16 * pg + k] = (see >> k) & 1u ? x[16 * pg + k] : -INFINITY;
-          }
-        }
-        float f[kTPg], mx = -INFINITY;
-#pragma unroll
-        for (int pg = 0; pg < kTPg; ++pg) {
-          f[pg] = fmaxf(d.fac[pg] * rowf, 1.2e-38f) + (rowf - rowf);   // never zero (hidden scores stay -inf); NaN stays
-          float mp = x[16 * pg];
-#pragma unroll
-          for (int k = 1; k < 16; ++k) mp = fmaxf(mp, x[16 * pg + k]);
-          mx = fmaxf(mx, fmaf(mp, f[pg], d.ev[pg]));
-        }
-        const bool moved = mx > m + kSlack;
-        if (__any_sync(0xffffffffu, moved)) {
-          const float alpha = moved ? ex2(m - mx) : 1.0f;
-          if (moved) {
-            m = mx;
-            l *= alpha;
-          }
-          if (t > 0) {                                 // O of the tiles before (their MMAs have run: S came after)
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              float o[16];
-              uint32_t u[16];
-              tld16(to + 16u * c, o);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * alpha);
-              tst16(to + 16u * c, u);
-            }
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int pg = 2 * c + q;
-            const float base = d.ev[pg] - m + kLift;
-            float s0 = 0.0f, s1 = 0.0f;
+            const float f = factor(pg), base = d.ev[pg] - m + kLift;
+            const uint64_t f2 = pack2(f, f), b2 = pack2(base, base);
+            uint64_t s2 = 0ull;
+            float mp = x[16 * pg];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const float w0 = ex2(fmaf(x[16 * pg + 2 * k], f[pg], base));
-              const float w1 = ex2(fmaf(x[16 * pg + 2 * k + 1], f[pg], base));
-              s0 += w0;
-              s1 += w1;
-              w[8 * q + k] = half2_bits(w0, w1);
+              const float x0 = x[16 * pg + 2 * k], x1 = x[16 * pg + 2 * k + 1];
+              mp = fmaxf(fmaxf(mp, x0), x1);
+              float y0, y1;
+              unpack2(fma2(pack2(x0, x1), f2, b2), y0, y1);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              s2 = add2(s2, pack2(y0, y1));
+              w[8 * pg + k] = half2_bits(y0, y1);
             }
-            l = fmaf(s0 + s1, d.vinv[pg], l);
+            mx = fmaxf(mx, fmaf(mp, f, d.ev[pg]));
+            float s0, s1;
+            unpack2(s2, s0, s1);
+            lt = fmaf(s0 + s1, d.vinv[pg], lt);
           }
-          tst16(ts + 16u * c, w);
+          if (!__any_sync(0xffffffffu, mx > m + kSlack)) {
+            l = lt;
+            tst32(ts, *reinterpret_cast<uint32_t(*)[32]>(w));
+            tst32(ts + 32u, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
+            done = true;
+          }
+        }
+        if (!done) {                                   // page by page, scores read twice: the maximum first
+          auto scores = [&](int c, float (&x)[32]) {   // pages 2c, 2c + 1
+            tld32(ts + 32u * c, x);
+            if (d.full) return;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int j0 = d.j0[2 * c + q], hi = p - j0;           // slots up to hi
+              uint32_t see = hi < 0 ? 0u : hi >= 15 ? 0xFFFFu : (2u << hi) - 1u;
+              if (a.window) {
+                const int lo = hi - a.window + 1, sk = a.sinks - j0; // from lo on, or below sk
+                const uint32_t win = lo <= 0 ? 0xFFFFu : lo > 15 ? 0u : 0xFFFFu << lo;
+                const uint32_t snk = sk <= 0 ? 0u : sk > 15 ? 0xFFFFu : (1u << sk) - 1u;
+                see &= win | snk;
+              }
+#pragma unroll
+              for (int k = 0; k < 16; ++k) x[16 * q + k] = (see >> k) & 1u ? x[16 * q + k] : -INFINITY;
+            }
+          };
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float x[32];
+            scores(c, x);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              float m0 = x[16 * q], m1 = x[16 * q + 1];
+#pragma unroll
+              for (int k = 2; k < 16; k += 2) {
+                m0 = fmaxf(m0, x[16 * q + k]);
+                m1 = fmaxf(m1, x[16 * q + k + 1]);
+              }
+              mx = fmaxf(mx, fmaf(fmaxf(m0, m1), factor(2 * c + q), d.ev[2 * c + q]));
+            }
+          }
+          const bool moved = mx > m + kSlack;
+          if (__any_sync(0xffffffffu, moved)) {
+            const float alpha = moved ? ex2(m - (mx + kHead)) : 1.0f;
+            if (moved) {
+              m = mx + kHead;
+              l *= alpha;
+            }
+            if (t > 0) {                               // O of the tiles before (their MMAs have run: S came after)
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                float o[16];
+                uint32_t u[16];
+                tld16(to + 16u * c, o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * alpha);
+                tst16(to + 16u * c, u);
+              }
+            }
+          }
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {                // the weights overlay scores that were read
+            float x[32];
+            uint32_t w[16];
+            scores(c, x);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float f = factor(2 * c + q), base = d.ev[2 * c + q] - m + kLift;
+              float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float w0 = ex2(fmaf(x[16 * q + 2 * k], f, base)), w1 = ex2(fmaf(x[16 * q + 2 * k + 1], f, base));
+                s0 += w0;
+                s1 += w1;
+                w[8 * q + k] = half2_bits(w0, w1);
+              }
+              l = fmaf(s0 + s1, d.vinv[2 * c + q], l);
+            }
+            tst16(ts + 16u * c, w);
+          }
         }
         tst_wait();
         tc_before();
@@ -500,85 +590,75 @@ __global__ void __launch_bounds__(kTThreads, 1)
       bool f2 = false;
       for (int s = nk >= kKSt ? nk - kKSt : 0; s < nk; ++s) (void)bar_wait(bar(bKFull + s % kKSt), (s / kKSt) & 1, f2);
       for (int s = nv >= kVSt ? nv - kVSt : 0; s < nv; ++s) (void)bar_wait(bar(bVFull + s % kVSt), (s / kVSt) & 1, f2);
-    } else if (warp == 13) {
-      // ---- MMA issue, the warp converged ------------------------------------------------------
-      auto qk = [&](int X, int s) {
-        const uint32_t q = sb + kOffQ + X * 32768, k = sb + kOffK + (s % kKSt) * 16384;
-        tc_after();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mma_f8_warp(tmem + col_s(X), sdesc(q + 32 * j), sdesc(k + 32 * j), kIdF8, j > 0 ? 1u : 0u);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mma_f8_warp(tmem + col_s(X), sdesc(q + 16384 + 32 * j), sdesc(k + 32 * j), kIdF8, 1u);
-        mma_commit_warp(bar(bSFull + X));
-      };
-      auto pv = [&](int X, int s, bool first) {
-        const uint32_t v = sb + kOffV + (s & 1) * 32768;
-        tc_after();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          mma_ts_warp(tmem + col_o(X), tmem + col_s(X) + 8u * j, vdesc(v + 2048u * j), kIdPV, first && j == 0 ? 0u : 1u);
-      };
-      int seq = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-      // tile seq + 1's scores are issued before the MMA warp turns to tile seq's other half
-      int n = 0, idx = next_item(n);
+    } else if (warp < 15) {
+      // ---- MMA issue: warp 13 for half A, 14 for half B, each converged.  An issue waits for room in the tensor
+      // pipe's queue, and a barrier's wait takes some hundred cycles: two warps keep the pipe fed over each other's
+      // waits.  O += w V of a tile, then the next tile's scores. ---------------------------------------------------
+      const int X = warp - 13;
+      int seq = 0, nq = 0, np = 0;
+      int n = 0, idx = next_item(0);
       TItem it;
-      int tiles = 0, halves = 0;
+      bool mine = false, ok = idx >= 0;
+      int tiles = 0;
       auto open_item = [&]() {
         tc_item(a, idx, nqb, nch, it);
         tiles = (it.c1 - it.c0 + kTPg - 1) / kTPg;
-        halves = it.rows > 128 ? 2 : 1;
+        mine = it.rows > 128 * X;                      // does the item have rows in this half
       };
-      // scores of half X of tile s (the first of an item waits for its queries)
-      auto scores = [&](int X, int s, bool first) {
-        if (first) {
-          if (!wait(bQReady + X, nq[X])) return false;
-          ++nq[X];
-        }
+      // both halves release a stage: a half without rows arrives by hand
+      auto release = [&](int i, bool used) {
+        if (used) mma_commit_warp(bar(i));
+        else if (lane == 0) bar_arrive(bar(i));
+      };
+      auto scores = [&](int s, bool first) {           // of tile s (the first of an item waits for its queries)
         if (!wait(bKFull + s % kKSt, s / kKSt)) return false;
-        qk(X, s);
+        if (mine) {
+          if (first && !wait(bQReady + X, nq++)) return false;
+          const uint32_t q = sb + kOffQ + X * 32768, k = sb + kOffK + (s % kKSt) * 16384;
+          tc_after();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f8_warp(tmem + col_s(X), sdesc(q + 32 * j), sdesc(k + 32 * j), kIdF8, j > 0 ? 1u : 0u);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f8_warp(tmem + col_s(X), sdesc(q + 16384 + 32 * j), sdesc(k + 32 * j), kIdF8, 1u);
+          mma_commit_warp(bar(bSFull + X));
+        }
+        release(bKEmpty + s % kKSt, mine);
         return true;
       };
-      bool ok = idx >= 0;
       if (ok) {
         open_item();
-        for (int X = 0; X < halves && ok; ++X) ok = scores(X, 0, true);
-        if (ok) mma_commit_warp(bar(bKEmpty));
+        ok = scores(0, true);
       }
       while (ok && idx >= 0) {
-        const int my_tiles = tiles, my_halves = halves;
+        const int my_tiles = tiles;
+        const bool was_mine = mine;
         for (int t = 0; t < my_tiles && ok; ++t, ++seq) {
           const bool last = t == my_tiles - 1;
-          int nhalves = my_halves;
+          ok = wait(bVReady + (seq & 1), seq >> 1);
+          if (ok && was_mine) ok = wait(bPFull + X, np++);
+          if (!ok) break;
+          if (was_mine) {
+            const uint32_t v = sb + kOffV + (seq & 1) * 32768;
+            tc_after();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              mma_ts_warp(tmem + col_o(X), tmem + col_s(X) + 8u * j, vdesc(v + 2048u * j), kIdPV, t == 0 && j == 0 ? 0u : 1u);
+            if (last) mma_commit_warp(bar(bODone + X));
+          }
+          release(bVFree + (seq & 1), was_mine);
           if (last) {                                  // what comes after this item
             idx = next_item(++n);
             if (failed) ok = false;
-            nhalves = 0;
-            if (idx >= 0) {
-              open_item();
-              nhalves = halves;
-            }
+            if (idx >= 0) open_item();
           }
-          if (!ok) break;
-          ok = wait(bVReady + (seq & 1), seq >> 1);
-          for (int X = 0; X < 2 && ok; ++X) {
-            if (X < my_halves) {
-              ok = wait(bPFull + X, np[X]);
-              if (!ok) break;
-              ++np[X];
-              pv(X, seq, t == 0);
-              if (X == my_halves - 1) mma_commit_warp(bar(bVFree + (seq & 1)));
-              if (last) mma_commit_warp(bar(bODone + X));
-            }
-            if (X < nhalves) {
-              ok = scores(X, seq + 1, last);
-              if (ok && X == nhalves - 1) mma_commit_warp(bar(bKEmpty + (seq + 1) % kKSt));
-            }
-          }
+          if (ok && idx >= 0) ok = scores(seq + 1, last);
         }
       }
-      mma_commit_warp(bar(bDrain));                    // every MMA issued completes before the CTA ends
+      mma_commit_warp(bar(bDrain + X));                // every MMA issued completes before the CTA ends
       bool f2 = false;
-      (void)bar_wait(bar(bDrain), 0, f2);
+      (void)bar_wait(bar(bDrain + X), 0, f2);
       __syncwarp();
     }
   }
