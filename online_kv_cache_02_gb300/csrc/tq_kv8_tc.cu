@@ -72,7 +72,7 @@ constexpr int kOffBar = kOffItem + kDescs * 8;
 enum Bar {
   bKFull = 0, bKEmpty = bKFull + kKSt, bVFull = bKEmpty + kKSt, bVEmpty = bVFull + kVSt, bVReady = bVEmpty + kVSt,
   bVFree = bVReady + 2, bSFull = bVFree + 2, bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2,
-  bItem = bQReady + 2, bDesc = bItem + kDescs, bDrain = bDesc + kDescs, bCount = bDrain + 2
+  bItem = bQReady + 2, bDesc = bItem + kDescs, bDrain = bDesc + kDescs, bTurn = bDrain + 2, bCount = bTurn + 2
 };
 constexpr int kOffTmem = kOffBar + 8 * bCount;
 constexpr int kTSmem = kOffTmem + 16 + 1024;
@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       bar_init(bar(bODone + i), 1);
       bar_init(bar(bQReady + i), 4);
       bar_init(bar(bDrain + i), 1);
+      bar_init(bar(bTurn + i), 1);
     }
     for (int i = 0; i < kDescs; ++i) {
       bar_init(bar(bItem + i), 1);
@@ -591,9 +592,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
       for (int s = nk >= kKSt ? nk - kKSt : 0; s < nk; ++s) (void)bar_wait(bar(bKFull + s % kKSt), (s / kKSt) & 1, f2);
       for (int s = nv >= kVSt ? nv - kVSt : 0; s < nv; ++s) (void)bar_wait(bar(bVFull + s % kVSt), (s / kVSt) & 1, f2);
     } else if (warp < 15) {
-      // ---- MMA issue: warp 13 for half A, 14 for half B, each converged.  An issue waits for room in the tensor
-      // pipe's queue, and a barrier's wait takes some hundred cycles: two warps keep the pipe fed over each other's
-      // waits.  O += w V of a tile, then the next tile's scores. ---------------------------------------------------
+      // ---- MMA issue: warp 13 for half A, 14 for half B, each converged: O += w V of a tile, then the next tile's
+      // scores.  An issue waits for room in the tensor pipe's queue, and a barrier's wait takes some hundred cycles:
+      // two warps do their waits while the other issues.  They take strict turns: left to mix, both halves' MMAs end
+      // together, both softmaxes run together, and neither overlaps the other (4,370 cycles a tile). -----------------
       const int X = warp - 13;
       int seq = 0, nq = 0, np = 0;
       int n = 0, idx = next_item(0);
@@ -638,6 +640,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
           const bool last = t == my_tiles - 1;
           ok = wait(bVReady + (seq & 1), seq >> 1);
           if (ok && was_mine) ok = wait(bPFull + X, np++);
+          if (ok && !last) ok = wait(bKFull + (seq + 1) % kKSt, (seq + 1) / kKSt);
+          if (ok && (X == 1 || seq > 0)) ok = wait(bTurn + X, X == 1 ? seq : seq - 1);
           if (!ok) break;
           if (was_mine) {
             const uint32_t v = sb + kOffV + (seq & 1) * 32768;
@@ -653,7 +657,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
             if (failed) ok = false;
             if (idx >= 0) open_item();
           }
+          if (last && lane == 0) bar_arrive(bar(bTurn + 1 - X));   // the next item's first scores wait for its queries
           if (ok && idx >= 0) ok = scores(seq + 1, last);
+          if (!last && lane == 0) bar_arrive(bar(bTurn + 1 - X));
         }
       }
       mma_commit_warp(bar(bDrain + X));                // every MMA issued completes before the CTA ends
