@@ -81,11 +81,45 @@ static_assert(kTSmem <= 232448, "shared memory per block");
 __device__ __forceinline__ constexpr uint32_t col_s(int X) { return 128u * X; }
 __device__ __forceinline__ constexpr uint32_t col_o(int X) { return 256u + 128u * X; }
 
-__device__ __forceinline__ void mma_f8_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Eight MMAs in one statement, one elected lane: the issuing warps share their schedulers with the softmax, so that
+// every instruction between two MMAs counts.  S = Qh Kc^T + Ql Kc^T: four steps of 32 channels (32 B, 2 descriptor
+// units) each.
+__device__ __forceinline__ void mma8_scores(uint32_t d, uint64_t qh, uint64_t ql, uint64_t k, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred e, t, f;\n .reg .b64 h1, h2, h3, l1, l2, l3, k1, k2, k3;\n"
+      " add.u64 h1, %1, 2;\n add.u64 h2, %1, 4;\n add.u64 h3, %1, 6;\n"
+      " add.u64 l1, %2, 2;\n add.u64 l2, %2, 4;\n add.u64 l3, %2, 6;\n"
+      " add.u64 k1, %3, 2;\n add.u64 k2, %3, 4;\n add.u64 k3, %3, 6;\n"
+      " setp.ne.b32 t, 1, 0;\n setp.ne.b32 f, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %3, %4, f;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], h1, k1, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], h2, k2, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], h3, k3, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %2, %3, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], l1, k1, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], l2, k2, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], l3, k3, %4, t;\n}\n" ::"r"(d),
+      "l"(qh), "l"(ql), "l"(k), "r"(idesc)
+      : "memory");
+}
+// O (+)= w V: eight steps of 16 tokens (8 columns of weights, 2048 B or 128 descriptor units of values).
+__device__ __forceinline__ void mma8_values(uint32_t d, uint32_t w, uint64_t v, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred e, t, p;\n .reg .b32 w1, w2, w3, w4, w5, w6, w7;\n .reg .b64 v1, v2, v3, v4, v5, v6, v7;\n"
+      " add.u32 w1, %1, 8;\n add.u32 w2, %1, 16;\n add.u32 w3, %1, 24;\n add.u32 w4, %1, 32;\n add.u32 w5, %1, 40;\n"
+      " add.u32 w6, %1, 48;\n add.u32 w7, %1, 56;\n"
+      " add.u64 v1, %2, 128;\n add.u64 v2, %2, 256;\n add.u64 v3, %2, 384;\n add.u64 v4, %2, 512;\n"
+      " add.u64 v5, %2, 640;\n add.u64 v6, %2, 768;\n add.u64 v7, %2, 896;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.ne.b32 t, 1, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [w1], v1, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [w2], v2, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [w3], v3, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [w4], v4, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [w5], v5, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [w6], v6, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [w7], v7, %3, t;\n}\n" ::"r"(d),
+      "r"(w), "l"(v), "r"(idesc), "r"(acc)
       : "memory");
 }
 // kind::f8f6f4, fp32 accumulate, e4m3 A and B, K-major, M = 128, N = 128
@@ -165,6 +199,12 @@ __device__ __forceinline__ void tld32x4(uint32_t taddr, float (&v)[128]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) pin8(v + 8 * i);
 }
+// A value that is the same in the whole warp, by a reduction: its result is a uniform register, and so is what follows
+// from it (the MMAs' operands, so that no issue waits for moves).
+__device__ __forceinline__ int uniform(int v) {       // v >= 0
+  return static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(v)));
+}
+
 struct TItem {
   int b, h, qb, chunk;
   int p0, rows;                           // first query position, query rows of the block (<= 256)
@@ -199,7 +239,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   extern __shared__ __align__(1024) unsigned char sm_raw[];
   unsigned char* sm = sm_raw + ((0u - su32(sm_raw)) & 1023u);
   const uint32_t sb = su32(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   auto bar = [&](int i) { return sb + kOffBar + 8u * static_cast<uint32_t>(i); };
   TileDesc* descs = reinterpret_cast<TileDesc*>(sm + kOffDesc);
   int* item_ring = reinterpret_cast<int*>(sm + kOffItem);
@@ -251,7 +291,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   // the n-th item of this CTA (-1: no more), from the ring
   auto next_item = [&](int n) {
     if (!wait(bItem + n % kDescs, n / kDescs)) return -1;
-    return *reinterpret_cast<volatile int*>(item_ring + n % kDescs);
+    return uniform(*reinterpret_cast<volatile int*>(item_ring + n % kDescs) + 1) - 1;
   };
 
   if (warp < 8) {
@@ -535,54 +575,67 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (!tc_item(a, idx, nqb, nch, it)) continue;
         publish(idx);
         const int* table = a.bt + static_cast<long long>(it.b) * a.maxp;
-        for (int c = it.c0; c < it.c1; c += kTPg, ++seq) {
-          // lane p < 8: page p of the tile
-          const int ci = c + lane;
-          int blk = -1, j0 = kNoPage;
-          float ks = 1.0f;
-          int ev = 0;
-          if (lane < kTPg && ci < it.c1) {
+        // lane i holds page i of four tiles (lanes 8k .. 8k + 7: tile k); the next four tiles' ids and scales are on
+        // their way meanwhile (two dependent loads are as long as a tile)
+        struct PageInfo {
+          int blk, j0, ev;
+          float ks;
+        };
+        auto fetch = [&](int ci) {
+          PageInfo x{-1, kNoPage, 0, 1.0f};
+          if (ci < it.c1) {
             const int page = ci < it.r.ns ? ci : ci - it.r.ns + it.r.w0;
             const int pid = table[page];
             if (pid >= 0 && pid < a.num_pages) {
-              blk = pid * a.H + it.h;
-              j0 = kPage * page;
-              ks = a.ks[blk];
-              ev = static_cast<int>((__float_as_uint(a.vs[blk]) >> 23) & 0xFF) - 127;
+              x.blk = pid * a.H + it.h;
+              x.j0 = kPage * page;
+              x.ks = a.ks[x.blk];
+              x.ev = static_cast<int>((__float_as_uint(a.vs[x.blk]) >> 23) & 0xFF) - 127;
             } else {
               atomicOr(a.err, kErrPage);
             }
           }
-          const bool seen = j0 + 15 <= it.pmin && (!a.window || j0 > it.pmax - a.window || j0 + 15 < a.sinks);
-          const bool full = (__ballot_sync(0xffffffffu, seen) & 0xFFu) == 0xFFu;
-          const uint32_t mask = __ballot_sync(0xffffffffu, blk >= 0);
-          if (seq >= kKSt && !wait(bKEmpty + seq % kKSt, seq / kKSt - 1)) break;
-          TileDesc& d = descs[seq % kDescs];
-          if (lane < kTPg) {
-            d.fac[lane] = fabsf(a.scale_log2) * ks;
-            d.ev[lane] = static_cast<float>(ev);
-            d.vinv[lane] = exp2f(static_cast<float>(-ev));
-            d.j0[lane] = j0;
-            if (lane == 0) d.full = full ? 1 : 0;
+          return x;
+        };
+        PageInfo cur = fetch(it.c0 + lane);
+        for (int c4 = it.c0; c4 < it.c1 && !failed; c4 += 4 * kTPg) {
+          const PageInfo nxt = fetch(c4 + 4 * kTPg + lane);
+          const bool seen = cur.j0 + 15 <= it.pmin && (!a.window || cur.j0 > it.pmax - a.window || cur.j0 + 15 < a.sinks);
+          const uint32_t seen4 = __ballot_sync(0xffffffffu, seen), there4 = __ballot_sync(0xffffffffu, cur.blk >= 0);
+          for (int k = 0; k < 4 && c4 + k * kTPg < it.c1; ++k, ++seq) {
+            const bool on = (lane >> 3) == k;
+            const int pg = lane & 7;
+            const uint32_t bytes = static_cast<uint32_t>(__popc((there4 >> (8 * k)) & 0xFFu)) * kPage * kTD;
+            if (seq >= kKSt && !wait(bKEmpty + seq % kKSt, seq / kKSt - 1)) break;
+            TileDesc& d = descs[seq % kDescs];
+            if (on) {
+              d.fac[pg] = fabsf(a.scale_log2) * cur.ks;
+              d.ev[pg] = static_cast<float>(cur.ev);
+              d.vinv[pg] = exp2f(static_cast<float>(-cur.ev));
+              d.j0[pg] = cur.j0;
+              if (pg == 0) d.full = ((seen4 >> (8 * k)) & 0xFFu) == 0xFFu ? 1 : 0;
+            }
+            __syncwarp();
+            if (lane == 0) {
+              bar_arrive(bar(bDesc + seq % kDescs));
+              if (bytes) bar_arrive_tx(bar(bKFull + seq % kKSt), bytes);
+              else bar_arrive(bar(bKFull + seq % kKSt));
+            }
+            __syncwarp();
+            ++nk;
+            if (on && cur.blk >= 0)
+              tma_block(sb + kOffK + (seq % kKSt) * 16384 + pg * kPage * kTD, &mk, cur.blk, bar(bKFull + seq % kKSt));
+            if (seq >= kVSt && !wait(bVEmpty + seq % kVSt, seq / kVSt - 1)) break;
+            if (lane == 0) {
+              if (bytes) bar_arrive_tx(bar(bVFull + seq % kVSt), bytes);
+              else bar_arrive(bar(bVFull + seq % kVSt));
+            }
+            __syncwarp();
+            ++nv;
+            if (on && cur.blk >= 0)
+              tma_block(sb + kOffVr + (seq % kVSt) * 16384 + pg * kPage * kTD, &mv, cur.blk, bar(bVFull + seq % kVSt));
           }
-          __syncwarp();
-          const uint32_t bytes = static_cast<uint32_t>(__popc(mask)) * kPage * kTD;
-          if (lane == 0) {
-            bar_arrive(bar(bDesc + seq % kDescs));
-            if (bytes) bar_arrive_tx(bar(bKFull + seq % kKSt), bytes);
-            else bar_arrive(bar(bKFull + seq % kKSt));
-          }
-          __syncwarp();
-          ++nk;
-          if (blk >= 0) tma_block(sb + kOffK + (seq % kKSt) * 16384 + lane * kPage * kTD, &mk, blk, bar(bKFull + seq % kKSt));
-          if (seq >= kVSt && !wait(bVEmpty + seq % kVSt, seq / kVSt - 1)) break;
-          if (lane == 0) {
-            if (bytes) bar_arrive_tx(bar(bVFull + seq % kVSt), bytes);
-            else bar_arrive(bar(bVFull + seq % kVSt));
-          }
-          __syncwarp();
-          ++nv;
-          if (blk >= 0) tma_block(sb + kOffVr + (seq % kVSt) * 16384 + lane * kPage * kTD, &mv, blk, bar(bVFull + seq % kVSt));
+          cur = nxt;
         }
         if (failed) break;
       }
@@ -604,8 +657,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
       int tiles = 0;
       auto open_item = [&]() {
         tc_item(a, idx, nqb, nch, it);
-        tiles = (it.c1 - it.c0 + kTPg - 1) / kTPg;
-        mine = it.rows > 128 * X;                      // does the item have rows in this half
+        tiles = uniform((it.c1 - it.c0 + kTPg - 1) / kTPg);
+        mine = __all_sync(0xffffffffu, it.rows > 128 * X);   // does the item have rows in this half
       };
       // both halves release a stage: a half without rows arrives by hand
       auto release = [&](int i, bool used) {
@@ -613,17 +666,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
         else if (lane == 0) bar_arrive(bar(i));
       };
       auto scores = [&](int s, bool first) {           // of tile s (the first of an item waits for its queries)
-        if (!wait(bKFull + s % kKSt, s / kKSt)) return false;
+        if (first && !wait(bKFull + s % kKSt, s / kKSt)) return false;   // else waited for before the turn
         if (mine) {
           if (first && !wait(bQReady + X, nq++)) return false;
           const uint32_t q = sb + kOffQ + X * 32768, k = sb + kOffK + (s % kKSt) * 16384;
           tc_after();
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f8_warp(tmem + col_s(X), sdesc(q + 32 * j), sdesc(k + 32 * j), kIdF8, j > 0 ? 1u : 0u);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f8_warp(tmem + col_s(X), sdesc(q + 16384 + 32 * j), sdesc(k + 32 * j), kIdF8, 1u);
+          mma8_scores(tmem + col_s(X), sdesc(q), sdesc(q + 16384), sdesc(k), kIdF8);
           mma_commit_warp(bar(bSFull + X));
         }
         release(bKEmpty + s % kKSt, mine);
@@ -646,9 +694,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if (was_mine) {
             const uint32_t v = sb + kOffV + (seq & 1) * 32768;
             tc_after();
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              mma_ts_warp(tmem + col_o(X), tmem + col_s(X) + 8u * j, vdesc(v + 2048u * j), kIdPV, t == 0 && j == 0 ? 0u : 1u);
+            mma8_values(tmem + col_o(X), tmem + col_s(X), vdesc(v), kIdPV, t == 0 ? 0u : 1u);
             if (last) mma_commit_warp(bar(bODone + X));
           }
           release(bVFree + (seq & 1), was_mine);
