@@ -20,7 +20,7 @@
 // runs, the tensor cores work on the other.  Tensor memory: S of A and B (each
 // overlaid by its weights), O of A and B, 512 columns.  Warps 0-3 and 4-7: the
 // softmax of A and B (thread = row), which also split the queries and write the
-// results; 8-11: values to fp16; 12: items, pages and TMA; 13, 14: MMA issue of A and B.
+// results; 8-11: values to fp16; 12: items, pages and TMA; 13: MMA issue.
 // Every wait is bounded; a wait that gives up sets the device error word.
 
 #include "tq_kv8.h"
@@ -72,14 +72,14 @@ constexpr int kOffBar = kOffItem + kDescs * 8;
 enum Bar {
   bKFull = 0, bKEmpty = bKFull + kKSt, bVFull = bKEmpty + kKSt, bVEmpty = bVFull + kVSt, bVReady = bVEmpty + kVSt,
   bVFree = bVReady + 2, bSFull = bVFree + 2, bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2,
-  bItem = bQReady + 2, bDesc = bItem + kDescs, bDrain = bDesc + kDescs, bTurn = bDrain + 2, bCount = bTurn + 2
+  bItem = bQReady + 2, bDesc = bItem + kDescs, bDrain = bDesc + kDescs, bCount
 };
 constexpr int kOffTmem = kOffBar + 8 * bCount;
 constexpr int kTSmem = kOffTmem + 16 + 1024;
 static_assert(kTSmem <= 232448, "shared memory per block");
 // tensor-memory columns of half X
-__device__ __forceinline__ constexpr uint32_t col_s(int X) { return 128u * X; }
-__device__ __forceinline__ constexpr uint32_t col_o(int X) { return 256u + 128u * X; }
+__device__ __forceinline__ constexpr uint32_t col_s(uint32_t X) { return 128u * X; }
+__device__ __forceinline__ constexpr uint32_t col_o(uint32_t X) { return 256u + 128u * X; }
 
 // Eight MMAs in one statement, one elected lane: the issuing warps share their schedulers with the softmax, so that
 // every instruction between two MMAs counts.  S = Qh Kc^T + Ql Kc^T: four steps of 32 channels (32 B, 2 descriptor
@@ -199,6 +199,20 @@ __device__ __forceinline__ void tld32x4(uint32_t taddr, float (&v)[128]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) pin8(v + 8 * i);
 }
+// A bounded wait in few instructions, for the issuing warp: the tensor pipe's queue is short, and between two batches
+// of MMAs every instruction of the wait is a gap in it.
+__device__ __forceinline__ uint32_t wait_short(uint32_t b, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, %3;\n"
+      "W%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra D%=;\n"
+      " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra W%=;\nD%=:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(b), "r"(parity), "n"(kWaitS)
+      : "memory");
+  return done;
+}
+
 // A value that is the same in the whole warp, by a reduction: its result is a uniform register, and so is what follows
 // from it (the MMAs' operands, so that no issue waits for moves).
 __device__ __forceinline__ int uniform(int v) {       // v >= 0
@@ -247,7 +261,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kKSt; ++i) {
       bar_init(bar(bKFull + i), 1);
-      bar_init(bar(bKEmpty + i), 2);
+      bar_init(bar(bKEmpty + i), 1);
     }
     for (int i = 0; i < kVSt; ++i) {
       bar_init(bar(bVFull + i), 1);
@@ -255,18 +269,17 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(bar(bVReady + i), 4);
-      bar_init(bar(bVFree + i), 2);
+      bar_init(bar(bVFree + i), 1);
       bar_init(bar(bSFull + i), 1);
       bar_init(bar(bPFull + i), 4);
       bar_init(bar(bODone + i), 1);
       bar_init(bar(bQReady + i), 4);
-      bar_init(bar(bDrain + i), 1);
-      bar_init(bar(bTurn + i), 1);
     }
     for (int i = 0; i < kDescs; ++i) {
       bar_init(bar(bItem + i), 1);
       bar_init(bar(bDesc + i), 1);
     }
+    bar_init(bar(bDrain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 13) {
@@ -644,73 +657,85 @@ __global__ void __launch_bounds__(kTThreads, 1)
       bool f2 = false;
       for (int s = nk >= kKSt ? nk - kKSt : 0; s < nk; ++s) (void)bar_wait(bar(bKFull + s % kKSt), (s / kKSt) & 1, f2);
       for (int s = nv >= kVSt ? nv - kVSt : 0; s < nv; ++s) (void)bar_wait(bar(bVFull + s % kVSt), (s / kVSt) & 1, f2);
-    } else if (warp < 15) {
-      // ---- MMA issue: warp 13 for half A, 14 for half B, each converged: O += w V of a tile, then the next tile's
-      // scores.  An issue waits for room in the tensor pipe's queue, and a barrier's wait takes some hundred cycles:
-      // two warps do their waits while the other issues.  They take strict turns: left to mix, both halves' MMAs end
-      // together, both softmaxes run together, and neither overlaps the other (4,370 cycles a tile). -----------------
-      const int X = warp - 13;
-      int seq = 0, nq = 0, np = 0;
-      int n = 0, idx = next_item(0);
-      TItem it;
-      bool mine = false, ok = idx >= 0;
+    } else if (warp == 13) {
+      // ---- MMA issue, the warp converged: O += w V of a tile and the next tile's scores, half A, then half B.  The
+      // order is strict: left to mix, both halves' MMAs end together, both softmaxes run together and neither overlaps
+      // the other (4,370 cycles a tile). ---------------------------------------------------------------------------
+      auto ready = [&](int i, int phase) {             // wait() in few instructions
+        if (__all_sync(0xffffffffu, wait_short(bar(i), phase & 1))) return true;
+        failed = true;
+        return false;
+      };
+      int seq = 0, n = 0, idx = next_item(0);
+      int nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;          // phases of the queries and of the weights
       int tiles = 0;
+      bool two = false;                                // rows in half B
+      TItem it;
       auto open_item = [&]() {
         tc_item(a, idx, nqb, nch, it);
         tiles = uniform((it.c1 - it.c0 + kTPg - 1) / kTPg);
-        mine = __all_sync(0xffffffffu, it.rows > 128 * X);   // does the item have rows in this half
+        two = __all_sync(0xffffffffu, it.rows > 128);
       };
-      // both halves release a stage: a half without rows arrives by hand
-      auto release = [&](int i, bool used) {
-        if (used) mma_commit_warp(bar(i));
-        else if (lane == 0) bar_arrive(bar(i));
+      auto scores = [&](uint32_t X, int s) {
+        const uint32_t q = sb + kOffQ + X * 32768, k = sb + kOffK + (s % kKSt) * 16384;
+        mma8_scores(tmem + col_s(X), sdesc(q), sdesc(q + 16384), sdesc(k), kIdF8);
+        mma_commit_warp(bar(bSFull + X));
       };
-      auto scores = [&](int s, bool first) {           // of tile s (the first of an item waits for its queries)
-        if (first && !wait(bKFull + s % kKSt, s / kKSt)) return false;   // else waited for before the turn
-        if (mine) {
-          if (first && !wait(bQReady + X, nq++)) return false;
-          const uint32_t q = sb + kOffQ + X * 32768, k = sb + kOffK + (s % kKSt) * 16384;
+      auto values = [&](uint32_t X, int s, bool first) {
+        mma8_values(tmem + col_o(X), tmem + col_s(X), vdesc(sb + kOffV + (s & 1) * 32768), kIdPV, first ? 0u : 1u);
+      };
+      // the first tile of an item: its keys and its queries
+      auto first_scores = [&](int s) {
+        if (!ready(bKFull + s % kKSt, s / kKSt) || !ready(bQReady, nq0++)) return false;
+        tc_after();
+        scores(0, s);
+        if (two) {
+          if (!ready(bQReady + 1, nq1++)) return false;
           tc_after();
-          mma8_scores(tmem + col_s(X), sdesc(q), sdesc(q + 16384), sdesc(k), kIdF8);
-          mma_commit_warp(bar(bSFull + X));
+          scores(1, s);
         }
-        release(bKEmpty + s % kKSt, mine);
+        mma_commit_warp(bar(bKEmpty + s % kKSt));
         return true;
       };
+      bool ok = idx >= 0;
       if (ok) {
         open_item();
-        ok = scores(0, true);
+        ok = first_scores(0);
       }
       while (ok && idx >= 0) {
         const int my_tiles = tiles;
-        const bool was_mine = mine;
-        for (int t = 0; t < my_tiles && ok; ++t, ++seq) {
+        const bool my_two = two;
+        for (int t = 0; t < my_tiles; ++t, ++seq) {
           const bool last = t == my_tiles - 1;
-          ok = wait(bVReady + (seq & 1), seq >> 1);
-          if (ok && was_mine) ok = wait(bPFull + X, np++);
-          if (ok && !last) ok = wait(bKFull + (seq + 1) % kKSt, (seq + 1) / kKSt);
-          if (ok && (X == 1 || seq > 0)) ok = wait(bTurn + X, X == 1 ? seq : seq - 1);
+          ok = ready(bVReady + (seq & 1), seq >> 1) && (last || ready(bKFull + (seq + 1) % kKSt, (seq + 1) / kKSt)) &&
+               ready(bPFull, np0++);
           if (!ok) break;
-          if (was_mine) {
-            const uint32_t v = sb + kOffV + (seq & 1) * 32768;
+          tc_after();
+          values(0, seq, t == 0);
+          if (last) mma_commit_warp(bar(bODone));
+          else scores(0, seq + 1);
+          if (my_two) {
+            ok = ready(bPFull + 1, np1++);
+            if (!ok) break;
             tc_after();
-            mma8_values(tmem + col_o(X), tmem + col_s(X), vdesc(v), kIdPV, t == 0 ? 0u : 1u);
-            if (last) mma_commit_warp(bar(bODone + X));
+            values(1, seq, t == 0);
+            if (last) mma_commit_warp(bar(bODone + 1));
+            else scores(1, seq + 1);
           }
-          release(bVFree + (seq & 1), was_mine);
-          if (last) {                                  // what comes after this item
-            idx = next_item(++n);
-            if (failed) ok = false;
-            if (idx >= 0) open_item();
-          }
-          if (last && lane == 0) bar_arrive(bar(bTurn + 1 - X));   // the next item's first scores wait for its queries
-          if (ok && idx >= 0) ok = scores(seq + 1, last);
-          if (!last && lane == 0) bar_arrive(bar(bTurn + 1 - X));
+          mma_commit_warp(bar(bVFree + (seq & 1)));
+          if (!last) mma_commit_warp(bar(bKEmpty + (seq + 1) % kKSt));
+        }
+        if (!ok) break;
+        idx = next_item(++n);
+        if (failed) ok = false;
+        if (idx >= 0) {
+          open_item();
+          ok = first_scores(seq);
         }
       }
-      mma_commit_warp(bar(bDrain + X));                // every MMA issued completes before the CTA ends
+      mma_commit_warp(bar(bDrain));                    // every MMA issued completes before the CTA ends
       bool f2 = false;
-      (void)bar_wait(bar(bDrain + X), 0, f2);
+      (void)bar_wait(bar(bDrain), 0, f2);
       __syncwarp();
     }
   }
