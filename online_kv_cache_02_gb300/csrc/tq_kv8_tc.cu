@@ -69,10 +69,11 @@ constexpr int kOffV = kOffVr + kVSt * 16384;          // [buffer][2 halves of 64
 constexpr int kOffDesc = kOffV + 2 * 32768;
 constexpr int kOffItem = kOffDesc + kDescs * static_cast<int>(sizeof(TileDesc));
 constexpr int kOffBar = kOffItem + kDescs * 8;
+constexpr int kDoneRing = 4;
 enum Bar {
-  bKFull = 0, bKEmpty = bKFull + kKSt, bVFull = bKEmpty + kKSt, bVEmpty = bVFull + kVSt, bVReady = bVEmpty + kVSt,
-  bVFree = bVReady + 2, bSFull = bVFree + 2, bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2,
-  bItem = bQReady + 2, bDesc = bItem + kDescs, bDrain = bDesc + kDescs, bCount
+  bKFull = 0, bVFull = bKFull + kKSt, bVEmpty = bVFull + kVSt, bReady = bVEmpty + kVSt, bSFull = bReady + 2,
+  bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2, bItem = bQReady + 2, bDesc = bItem + kDescs,
+  bDone = bDesc + kDescs, bDrain = bDone + kDoneRing, bCount
 };
 constexpr int kOffTmem = kOffBar + 8 * bCount;
 constexpr int kTSmem = kOffTmem + 16 + 1024;
@@ -259,22 +260,19 @@ __global__ void __launch_bounds__(kTThreads, 1)
   int* item_ring = reinterpret_cast<int*>(sm + kOffItem);
 
   if (tid == 0) {
-    for (int i = 0; i < kKSt; ++i) {
-      bar_init(bar(bKFull + i), 1);
-      bar_init(bar(bKEmpty + i), 1);
-    }
+    for (int i = 0; i < kKSt; ++i) bar_init(bar(bKFull + i), 1);
     for (int i = 0; i < kVSt; ++i) {
       bar_init(bar(bVFull + i), 1);
       bar_init(bar(bVEmpty + i), 4);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(bar(bVReady + i), 4);
-      bar_init(bar(bVFree + i), 1);
+      bar_init(bar(bReady + i), 4);
       bar_init(bar(bSFull + i), 1);
       bar_init(bar(bPFull + i), 4);
       bar_init(bar(bODone + i), 1);
       bar_init(bar(bQReady + i), 4);
     }
+    for (int i = 0; i < kDoneRing; ++i) bar_init(bar(bDone + i), 1);
     for (int i = 0; i < kDescs; ++i) {
       bar_init(bar(bItem + i), 1);
       bar_init(bar(bDesc + i), 1);
@@ -418,13 +416,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
             done = true;
           }
         }
-        if (!done) {                                   // page by page, scores read twice: the maximum first
-          auto scores = [&](int c, float (&x)[32]) {   // pages 2c, 2c + 1
-            tld32(ts + 32u * c, x);
-            if (d.full) return;
+        if (!done) {                                   // an edge, an item's first tile, or a maximum that moves
+          float x[kTTok];
+          tld32x4(ts, x);
+          if (!d.full) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int j0 = d.j0[2 * c + q], hi = p - j0;           // slots up to hi
+            for (int pg = 0; pg < kTPg; ++pg) {
+              const int j0 = d.j0[pg], hi = p - j0;                  // slots up to hi
               uint32_t see = hi < 0 ? 0u : hi >= 15 ? 0xFFFFu : (2u << hi) - 1u;
               if (a.window) {
                 const int lo = hi - a.window + 1, sk = a.sinks - j0; // from lo on, or below sk
@@ -433,24 +431,19 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 see &= win | snk;
               }
 #pragma unroll
-              for (int k = 0; k < 16; ++k) x[16 * q + k] = (see >> k) & 1u ? x[16 * q + k] : -INFINITY;
+              for (int k = 0; k < 16; ++k) x[16 * pg + k] = (see >> k) & 1u ? x[16 * pg + k] : -INFINITY;
             }
-          };
+          }
           float mx = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float x[32];
-            scores(c, x);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              float m0 = x[16 * q], m1 = x[16 * q + 1];
+          for (int pg = 0; pg < kTPg; ++pg) {
+            float m0 = x[16 * pg], m1 = x[16 * pg + 1];
 #pragma unroll
-              for (int k = 2; k < 16; k += 2) {
-                m0 = fmaxf(m0, x[16 * q + k]);
-                m1 = fmaxf(m1, x[16 * q + k + 1]);
-              }
-              mx = fmaxf(mx, fmaf(fmaxf(m0, m1), factor(2 * c + q), d.ev[2 * c + q]));
+            for (int k = 2; k < 16; k += 2) {
+              m0 = fmaxf(m0, x[16 * pg + k]);
+              m1 = fmaxf(m1, x[16 * pg + k + 1]);
             }
+            mx = fmaxf(mx, fmaf(fmaxf(m0, m1), factor(pg), d.ev[pg]));
           }
           const bool moved = mx > m + kSlack;
           if (__any_sync(0xffffffffu, moved)) {
@@ -471,23 +464,27 @@ __global__ void __launch_bounds__(kTThreads, 1)
               }
             }
           }
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {                // the weights overlay scores that were read
-            float x[32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {                // the weights overlay the scores
             uint32_t w[16];
-            scores(c, x);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const float f = factor(2 * c + q), base = d.ev[2 * c + q] - m + kLift;
-              float s0 = 0.0f, s1 = 0.0f;
+              const int pg = 2 * c + q;
+              const float f = factor(pg), base = d.ev[pg] - m + kLift;
+              const uint64_t f2 = pack2(f, f), b2 = pack2(base, base);
+              uint64_t s2 = 0ull;
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const float w0 = ex2(fmaf(x[16 * q + 2 * k], f, base)), w1 = ex2(fmaf(x[16 * q + 2 * k + 1], f, base));
-                s0 += w0;
-                s1 += w1;
-                w[8 * q + k] = half2_bits(w0, w1);
+                float y0, y1;
+                unpack2(fma2(pack2(x[16 * pg + 2 * k], x[16 * pg + 2 * k + 1]), f2, b2), y0, y1);
+                y0 = ex2(y0);
+                y1 = ex2(y1);
+                s2 = add2(s2, pack2(y0, y1));
+                w[8 * q + k] = half2_bits(y0, y1);
               }
-              l = fmaf(s0 + s1, d.vinv[2 * c + q], l);
+              float s0, s1;
+              unpack2(s2, s0, s1);
+              l = fmaf(s0 + s1, d.vinv[pg], l);
             }
             tst16(ts + 16u * c, w);
           }
@@ -542,7 +539,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const int ntile = (it.c1 - it.c0 + kTPg - 1) / kTPg;
       for (int i = 0; i < ntile; ++i, ++seq) {
         if (!wait(bVFull + seq % kVSt, seq / kVSt)) break;
-        if (seq >= 2 && !wait(bVFree + (seq & 1), (seq - 2) >> 1)) break;
+        if (seq >= 2 && !wait(bDone + (seq - 2) % kDoneRing, (seq - 2) / kDoneRing)) break;
         const int j = descs[seq % kDescs].j0[pg] + (t & 15);
         // what no row sees may hold anything: zeros instead
         const bool see = j <= it.pmax && (!a.window || j > it.pmin - a.window || j < a.sinks);
@@ -560,10 +557,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          bar_arrive(bar(bVReady + (seq & 1)));
-          bar_arrive(bar(bVEmpty + seq % kVSt));
-        }
+        if (lane == 0) bar_arrive(bar(bVEmpty + seq % kVSt));
+        // the issuing warp's one wait for a tile covers the next tile's keys
+        if (i + 1 < ntile && !wait(bKFull + (seq + 1) % kKSt, (seq + 1) / kKSt)) break;
+        if (lane == 0) bar_arrive(bar(bReady + (seq & 1)));
       }
       if (failed) break;
     }
@@ -619,7 +616,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const bool on = (lane >> 3) == k;
             const int pg = lane & 7;
             const uint32_t bytes = static_cast<uint32_t>(__popc((there4 >> (8 * k)) & 0xFFu)) * kPage * kTD;
-            if (seq >= kKSt && !wait(bKEmpty + seq % kKSt, seq / kKSt - 1)) break;
+            if (seq >= kKSt && !wait(bDone + (seq - kKSt) % kDoneRing, (seq - kKSt) / kDoneRing)) break;
             TileDesc& d = descs[seq % kDescs];
             if (on) {
               d.fac[pg] = fabsf(a.scale_log2) * cur.ks;
@@ -694,7 +691,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
           tc_after();
           scores(1, s);
         }
-        mma_commit_warp(bar(bKEmpty + s % kKSt));
         return true;
       };
       bool ok = idx >= 0;
@@ -707,8 +703,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const bool my_two = two;
         for (int t = 0; t < my_tiles; ++t, ++seq) {
           const bool last = t == my_tiles - 1;
-          ok = ready(bVReady + (seq & 1), seq >> 1) && (last || ready(bKFull + (seq + 1) % kKSt, (seq + 1) / kKSt)) &&
-               ready(bPFull, np0++);
+          ok = ready(bReady + (seq & 1), seq >> 1) && ready(bPFull, np0++);
           if (!ok) break;
           tc_after();
           values(0, seq, t == 0);
@@ -722,8 +717,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             if (last) mma_commit_warp(bar(bODone + 1));
             else scores(1, seq + 1);
           }
-          mma_commit_warp(bar(bVFree + (seq & 1)));
-          if (!last) mma_commit_warp(bar(bKEmpty + (seq + 1) % kKSt));
+          mma_commit_warp(bar(bDone + seq % kDoneRing));   // the tile's keys and values have been read
         }
         if (!ok) break;
         idx = next_item(++n);
