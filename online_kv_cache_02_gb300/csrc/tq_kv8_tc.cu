@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   bool failed = false;
   // a warp's wait for phase `phase` of a barrier; once one gave up, every later one returns at once
   auto wait = [&](int i, int phase) {
-    if (__all_sync(0xffffffffu, bar_wait(bar(i), phase & 1, failed))) return true;
+    if (!failed && __all_sync(0xffffffffu, wait_short(bar(i), phase & 1))) return true;
     failed = true;
     return false;
   };
@@ -545,15 +545,19 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const bool see = j <= it.pmax && (!a.window || j > it.pmin - a.window || j < a.sinks);
         const uint32_t src = sb + kOffVr + (seq % kVSt) * 16384 + t * 128;
         const uint32_t dst = sb + kOffV + (seq & 1) * 32768 + t * 128;
+        uint4 w[8];                                    // every load ahead of the stores
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = lds128(src + static_cast<uint32_t>((c ^ (t & 7)) << 4));
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          uint4 w = lds128(src + static_cast<uint32_t>((c ^ (t & 7)) << 4));
-          if (!see) w = make_uint4(0u, 0u, 0u, 0u);
+          if (!see) w[c] = make_uint4(0u, 0u, 0u, 0u);
           const uint32_t o0 = static_cast<uint32_t>((((2 * c) & 7) ^ (t & 7)) << 4),
                          o1 = static_cast<uint32_t>((((2 * c + 1) & 7) ^ (t & 7)) << 4);
           const uint32_t half = dst + (c >> 2) * 16384;
-          sts128(half + o0, codes_to_half2(w.x), codes_to_half2(w.x >> 16), codes_to_half2(w.y), codes_to_half2(w.y >> 16));
-          sts128(half + o1, codes_to_half2(w.z), codes_to_half2(w.z >> 16), codes_to_half2(w.w), codes_to_half2(w.w >> 16));
+          sts128(half + o0, codes_to_half2(w[c].x), codes_to_half2(w[c].x >> 16), codes_to_half2(w[c].y),
+                 codes_to_half2(w[c].y >> 16));
+          sts128(half + o1, codes_to_half2(w[c].z), codes_to_half2(w[c].z >> 16), codes_to_half2(w[c].w),
+                 codes_to_half2(w[c].w >> 16));
         }
         fence_async_smem();
         __syncwarp();
