@@ -47,9 +47,10 @@ constexpr int kTThreads = 512;
 constexpr int kKSt = 3, kVSt = 2;         // raw K and V stages
 constexpr int kDescs = 8;
 constexpr float kMNone = -1.0e30f;
-// Weights lie below 2^(kLift + kSlack) = 2^15 (fp16 ends at 2^16); M is set kHead above the largest score met, so that
-// it seldom moves again: the largest weight is then 2^3 at least, and fp16 keeps 11 bits down to 2^-17 of it.
-constexpr float kSlack = 8.0f, kLift = 7.0f, kHead = 4.0f;
+// Weights are 2^(kLift + score - M).  M is set kHead above the largest score met, so that it seldom moves again: the
+// largest weight is then 2^3, and fp16 keeps 11 bits down to 2^-17 of it.  M moves when a page's 16 weights sum to more
+// than kFull, below the end of fp16: the largest of them is then 2^11.9 at least, a score above M + kSlack.
+constexpr float kSlack = 4.5f, kLift = 7.0f, kHead = 4.0f, kFull = 61000.0f;
 constexpr int kPartRow = kTD + 4;
 constexpr int kNoPage = 1 << 30;          // first position of a page that is not there: no query sees it
 
@@ -379,37 +380,35 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const TileDesc& d = descs[seq % kDescs];
         // never zero (a hidden score stays -inf), and NaN stays NaN
         auto factor = [&](int pg) { return fmaxf(d.fac[pg] * rowf, 1.2e-38f) + (rowf - rowf); };
-        // The tile as it mostly is: every token seen and no score far above the maximum so far.  Weights by the old
-        // maximum while the new one is found out; stored only if it holds.
+        // The tile as it mostly is: every token seen and no score far above the maximum so far.  The weights by the
+        // old maximum tell by themselves: a page's sum below kFull means that each fits fp16.  No maximum is taken.
         bool done = false;
         if (d.full && t > 0) {
           float x[kTTok];
           uint32_t w[kTTok / 2];
           tld32x4(ts, x);
-          float mx = -INFINITY, lt = l;
+          float most = 0.0f, lt = l;
 #pragma unroll
           for (int pg = 0; pg < kTPg; ++pg) {
             const float f = factor(pg), base = d.ev[pg] - m + kLift;
             const uint64_t f2 = pack2(f, f), b2 = pack2(base, base);
             uint64_t s2 = 0ull;
-            float mp = x[16 * pg];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const float x0 = x[16 * pg + 2 * k], x1 = x[16 * pg + 2 * k + 1];
-              mp = fmaxf(fmaxf(mp, x0), x1);
               float y0, y1;
-              unpack2(fma2(pack2(x0, x1), f2, b2), y0, y1);
+              unpack2(fma2(pack2(x[16 * pg + 2 * k], x[16 * pg + 2 * k + 1]), f2, b2), y0, y1);
               y0 = ex2(y0);
               y1 = ex2(y1);
               s2 = add2(s2, pack2(y0, y1));
               w[8 * pg + k] = half2_bits(y0, y1);
             }
-            mx = fmaxf(mx, fmaf(mp, f, d.ev[pg]));
             float s0, s1;
             unpack2(s2, s0, s1);
-            lt = fmaf(s0 + s1, d.vinv[pg], lt);
+            s0 += s1;
+            most = fmaxf(most, s0);
+            lt = fmaf(s0, d.vinv[pg], lt);
           }
-          if (!__any_sync(0xffffffffu, mx > m + kSlack)) {
+          if (!__any_sync(0xffffffffu, most > kFull)) {
             l = lt;
             tst32(ts, *reinterpret_cast<uint32_t(*)[32]>(w));
             tst32(ts + 32u, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
