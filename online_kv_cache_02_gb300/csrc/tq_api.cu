@@ -952,7 +952,7 @@ tq_status kv8_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void
   if (batch == 0) return TQ_OK;
   if (!q || !lens || !out || !workspace || misaligned(q) || misaligned(out) || misaligned(workspace))
     return TQ_ERR_INVALID_ARG;
-  if (static_cast<long long>(batch) * n_new * Hq > 0x7FFFFFFFLL / 16) return TQ_ERR_UNSUPPORTED;
+  if (static_cast<long long>(batch) * n_new * Hq >= (1LL << 27)) return TQ_ERR_UNSUPPORTED;
   // positions lie below both: a window or sinks beyond them change nothing (and the kernels' sums stay in 32 bits)
   const long long cap = std::min<long long>(max_seq_len, static_cast<long long>(kPage) * cache->max_pages_per_seq);
   if (cap > (1LL << 29)) return TQ_ERR_UNSUPPORTED;

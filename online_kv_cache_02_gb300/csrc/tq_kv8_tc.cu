@@ -1,8 +1,10 @@
 // Causal attention of many query rows over the 8-bit paged cache on the tensor
 // cores (tcgen05), bf16 queries, d = 128.
 //
-// An item is (sequence, KV head, block of 256 query rows r = t G + g, chunk of
-// its pages); keys go by in tiles of 128 tokens (8 pages):
+// An item is (sequence, KV head, block of 256 query rows r = t G + g); keys go by in
+// tiles of 128 tokens (8 pages).  All items' tiles form one list that is cut into
+// equal spans, one per CTA; the parts of an item that crosses spans are joined by a
+// second kernel.  Per tile:
 //   S = (Qh + Ql) Kc^T    kind::f8f6f4 straight from the cache's codes, which TMA
 //                         puts in place: no conversion of K.  A query row, scaled
 //                         by a power of two, is the sum of two e4m3 parts: exact
@@ -52,6 +54,9 @@ constexpr float kMNone = -1.0e30f;
 // than kFull, below the end of fp16: the largest of them is then 2^11.9 at least, a score above M + kSlack.
 constexpr float kSlack = 4.5f, kLift = 7.0f, kHead = 4.0f, kFull = 61000.0f;
 constexpr int kPartRow = kTD + 4;
+constexpr int kMaxBlocks = 2048;          // (sequence, query block) pairs that the split form lists
+constexpr int kItemCost = 5;              // an item's start and end, in tiles' time
+constexpr int kMinSpan = 2 + kItemCost;   // a CTA's share of the list at least
 constexpr int kNoPage = 1 << 30;          // first position of a page that is not there: no query sees it
 
 struct TileDesc {                         // one tile of the stream, by page
@@ -69,7 +74,8 @@ constexpr int kOffVr = kOffK + kKSt * 16384;          // [stage][128 tokens][128
 constexpr int kOffV = kOffVr + kVSt * 16384;          // [buffer][2 halves of 64 channels][128 tokens][128 B]
 constexpr int kOffDesc = kOffV + 2 * 32768;
 constexpr int kOffItem = kOffDesc + kDescs * static_cast<int>(sizeof(TileDesc));
-constexpr int kOffBar = kOffItem + kDescs * 8;
+constexpr int kItemMsg = 48;
+constexpr int kOffBar = kOffItem + kDescs * kItemMsg;
 constexpr int kDoneRing = 4;
 enum Bar {
   bKFull = 0, bVFull = bKFull + kKSt, bVEmpty = bVFull + kVSt, bReady = bVEmpty + kVSt, bSFull = bReady + 2,
@@ -154,10 +160,14 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(two)));
   return r;
 }
-__device__ __forceinline__ uint32_t to_codes(float lo, float hi) {
+__device__ __forceinline__ uint32_t half2_to_codes(uint32_t h2) {
   unsigned short r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
   return r;
+}
+__device__ __forceinline__ uint32_t sub_half2(uint32_t x, uint32_t y) {
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&d);
 }
 
 // Pairs of fp32 in one 64-bit register (Blackwell's packed fp32 arithmetic).
@@ -221,44 +231,57 @@ __device__ __forceinline__ int uniform(int v) {       // v >= 0
   return static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(v)));
 }
 
-struct TItem {
-  int b, h, qb, chunk;
-  int p0, rows;                           // first query position, query rows of the block (<= 256)
+__device__ __forceinline__ void stg256(void* p, const uint32_t* v) {   // 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// A block of query rows of one sequence, and the pages that it sees.
+struct TBlock {
+  int b, qb, p0, rows;                    // sequence, block, the sequence's first query position, rows (<= 256)
   int pmin, pmax;
   Kv8Range r;
-  int c0, c1;                             // pages of the list
+  int pages;
 };
-__device__ __forceinline__ bool tc_item(const Kv8Attn& a, int idx, int nqb, int nch, TItem& it) {
-  it.chunk = idx % nch;
-  int rest = idx / nch;
-  it.h = rest % a.H;
-  rest = a.B * nqb - 1 - rest / a.H;      // the longest rows first
-  it.qb = rest / a.B;
-  it.b = rest % a.B;
-  const Kv8Seq s = kv8_seq(a, it.b);
-  const long long rows = static_cast<long long>(s.n) * a.G, r0 = static_cast<long long>(it.qb) * kTRows;
-  it.p0 = s.p0;
-  if (r0 >= rows) return false;
-  it.rows = static_cast<int>(rows - r0 < kTRows ? rows - r0 : kTRows);
-  it.pmin = s.p0 + static_cast<int>(r0 / a.G);
-  it.pmax = s.p0 + static_cast<int>((r0 + it.rows - 1) / a.G);
-  it.r = kv8_range(a.window, a.sinks, it.pmin, it.pmax);
-  const int pages = it.r.ns + it.r.nw, tiles = (pages + kTPg - 1) / kTPg, per = (tiles + nch - 1) / nch;
-  it.c0 = it.chunk * per * kTPg;
-  it.c1 = min(pages, it.c0 + per * kTPg);
-  return it.c0 < it.c1;
+// Block `e` of the list (sequence by sequence); its tiles, 0 if there is nothing to do.  In the list an item takes
+// kItemCost units, then one per tile.
+__device__ __forceinline__ int tc_block(const Kv8Attn& a, int e, int nqb, TBlock& k) {
+  k.b = e / nqb;
+  k.qb = e - k.b * nqb;
+  const Kv8Seq s = kv8_seq(a, k.b);
+  const int rows = s.n * a.G, r0 = k.qb * kTRows;      // the host keeps batch T Hq below 2^27
+  k.p0 = s.p0;
+  k.rows = min(rows - r0, kTRows);
+  k.pages = 0;
+  if (k.rows <= 0) return 0;
+  k.pmin = s.p0 + r0 / a.G;
+  k.pmax = s.p0 + (r0 + k.rows - 1) / a.G;
+  k.r = kv8_range(a.window, a.sinks, k.pmin, k.pmax);
+  k.pages = k.r.ns + k.r.nw;
+  return (k.pages + kTPg - 1) / kTPg;
 }
+// What the load warp tells the others of an item: a block, a KV head, and a run of its tiles.
+struct alignas(16) ItemMsg {
+  int valid, b, h, qb;
+  int p0, rows, pmin, pmax;
+  int ntile, slot, pad[2];                // slot: of the workspace for a part of the tiles; -1 for all of them
+};
+// A split item's first part ends the span of one CTA; the join finds the others by it.
+struct TSplit {
+  int valid, b, h, qb, p0, rows, last, pad;            // last: the CTA that holds the item's end
+};
 
 __global__ void __launch_bounds__(kTThreads, 1)
     kv8_tc_kernel(const __grid_constant__ Kv8Attn a, const __grid_constant__ CUtensorMap mk,
-                  const __grid_constant__ CUtensorMap mv, int nqb, int nch, int items) {
+                  const __grid_constant__ CUtensorMap mv, int nqb, int split) {
   extern __shared__ __align__(1024) unsigned char sm_raw[];
   unsigned char* sm = sm_raw + ((0u - su32(sm_raw)) & 1023u);
   const uint32_t sb = su32(sm);
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   auto bar = [&](int i) { return sb + kOffBar + 8u * static_cast<uint32_t>(i); };
   TileDesc* descs = reinterpret_cast<TileDesc*>(sm + kOffDesc);
-  int* item_ring = reinterpret_cast<int*>(sm + kOffItem);
+  ItemMsg* item_ring = reinterpret_cast<ItemMsg*>(sm + kOffItem);
 
   if (tid == 0) {
     for (int i = 0; i < kKSt; ++i) bar_init(bar(bKFull + i), 1);
@@ -288,11 +311,57 @@ __global__ void __launch_bounds__(kTThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
+  // the list, cut into equal spans: units before each block (of one head), by a scan in the queries' room
+  const int entries = a.B * nqb;
+  long long u0 = 0, u1 = 0, span = 1;
+  int entry0 = 0, before0 = 0;
+  if (split) {
+    int* prefix = reinterpret_cast<int*>(sm + kOffQ);
+    int* warp_sum = prefix + kMaxBlocks;
+    const int per = (entries + kTThreads - 1) / kTThreads;
+    TBlock k;
+    int sum = 0;
+    for (int i = 0; i < per && tid * per + i < entries; ++i) {
+      prefix[tid * per + i] = sum;
+      const int tiles = tc_block(a, tid * per + i, nqb, k);
+      sum += tiles ? tiles + kItemCost : 0;
+    }
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      run += lane >= o ? v : 0;
+    }
+    if (lane == 31) warp_sum[tid >> 5] = run;
+    __syncthreads();
+    int base = run - sum, total = 0;
+    for (int w = 0; w < kTThreads / 32; ++w) {
+      base += w < (tid >> 5) ? warp_sum[w] : 0;
+      total += warp_sum[w];
+    }
+    for (int i = 0; i < per && tid * per + i < entries; ++i) prefix[tid * per + i] += base;
+    __syncthreads();
+    const long long units = static_cast<long long>(total) * a.H;
+    span = (units + gridDim.x - 1) / gridDim.x;
+    span = span < kMinSpan ? kMinSpan : span;
+    u0 = span * blockIdx.x < units ? span * blockIdx.x : units;
+    u1 = u0 + span < units ? u0 + span : units;
+    int lo = 0, hi = entries - 1;                      // the block that holds u0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (static_cast<long long>(prefix[mid]) * a.H <= u0) lo = mid;
+      else hi = mid - 1;
+    }
+    entry0 = lo;
+    before0 = prefix[lo];
+  }
   fence_async_smem();
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + kOffTmem);
+  TSplit* splits = reinterpret_cast<TSplit*>(a.part);              // one per CTA, then the partials' slots
+  float* parts = a.part + static_cast<size_t>(gridDim.x) * (sizeof(TSplit) / sizeof(float));
   bool failed = false;
   // a warp's wait for phase `phase` of a barrier; once one gave up, every later one returns at once
   auto wait = [&](int i, int phase) {
@@ -300,10 +369,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
     failed = true;
     return false;
   };
-  // the n-th item of this CTA (-1: no more), from the ring
+  // the n-th item of this CTA, from the ring
   auto next_item = [&](int n) {
-    if (!wait(bItem + n % kDescs, n / kDescs)) return -1;
-    return uniform(*reinterpret_cast<volatile int*>(item_ring + n % kDescs) + 1) - 1;
+    ItemMsg x{};
+    if (wait(bItem + n % kDescs, n / kDescs)) x = item_ring[n % kDescs];
+    return x;
   };
 
   if (warp < 8) {
@@ -313,65 +383,95 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * wq) << 16);
     const uint32_t ts = trow + col_s(X), to = trow + col_o(X);
     const float sgn = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // whole sectors per store
     int seq = 0, nS = 0, nO = 0;                       // tiles seen, phases of S and of the final O
-    for (int n = 0;; ++n) {
-      const int idx = next_item(n);
-      if (idx < 0) break;
-      TItem it;
-      tc_item(a, idx, nqb, nch, it);
-      const int ntile = (it.c1 - it.c0 + kTPg - 1) / kTPg;
-      if (128 * X >= it.rows) {                        // this half is empty
+    // The row of an item that is this thread's.
+    struct Row {
+      bool live;
+      int p;                                           // position; -1: an absent row sees nothing
+      long long at;                                    // its element of q and out
+      float rowf;
+    };
+    auto mine = [&](const ItemMsg& x) { return x.valid && 128 * X < x.rows; };
+    // Loads the row and leaves it in shared memory as two e4m3 parts, scaled so that its largest value lies in
+    // [128, 256).  The item before has no score MMA left: its last scores were read.
+    auto queries = [&](const ItemMsg& x) {
+      Row w;
+      const unsigned gr = static_cast<unsigned>(x.qb * kTRows + 128 * X + r), tok = gr / static_cast<unsigned>(a.G);
+      w.live = 128 * X + r < x.rows;
+      w.p = w.live ? x.p0 + static_cast<int>(tok) : -1;
+      w.at = ((static_cast<long long>(x.b) * a.T + tok) * a.Hq + x.h * a.G + (gr - tok * a.G)) * kTD;
+      // The warp's 32 rows, half a warp per row (a lane per row would ask for 32 lines with each load); the raw 16-byte
+      // pieces 2c and 2c + 1 of a row wait where the parts of its channels 16c .. 16c + 15 will stand.
+      const uint32_t qw = sb + kOffQ + X * 32768 + 32 * wq * 128, qh = qw + lane * 128;
+      {
+        const long long where = w.live ? w.at : -1;
+        const int piece = lane & 15;
+        uint4 v4[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const long long at = __shfl_sync(0xffffffffu, where, 2 * i + (lane >> 4));
+          v4[i] = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at)[piece]
+                          : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int rw = 2 * i + (lane >> 4);
+          sts128(qw + rw * 128 + (piece & 1) * 16384 + (((piece >> 1) ^ (rw & 7)) << 4), v4[i].x, v4[i].y, v4[i].z, v4[i].w);
+        }
+      }
+      __syncwarp();
+      uint32_t mx2 = 0u;                               // largest magnitudes: bf16 bits order as integers
+#pragma unroll 8
+      for (int i = 0; i < 16; ++i) {
+        const uint4 v = lds128(qh + (i & 1) * 16384 + (((i >> 1) ^ (r & 7)) << 4));
+        mx2 = __vmaxu2(__vmaxu2(mx2, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
+        mx2 = __vmaxu2(__vmaxu2(mx2, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
+      }
+      const uint32_t mx = max(mx2 & 0xFFFFu, mx2 >> 16);
+      int e = 7 - (static_cast<int>(mx >> 7) - 127);
+      e = mx && mx < 0x7F80u ? min(e, 120) : 0;
+      const float up = __int_as_float((e + 127) << 23) * sgn;
+      w.rowf = __int_as_float((127 - e) << 23);
+      // rolled: a loop that runs once an item, out of the instruction cache otherwise (3.6 us unrolled)
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t pos = qh + static_cast<uint32_t>((c ^ (r & 7)) << 4);
+        const uint4 ua = lds128(pos), ub = lds128(pos + 16384);
+        const uint32_t u[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {                  // fp16 holds the scaled bf16 values and their remainders exactly
+          const uint32_t a0 = u[2 * k], a1 = u[2 * k + 1];
+          const uint32_t f0 = half2_bits(__uint_as_float(a0 << 16) * up, __uint_as_float(a0 & 0xFFFF0000u) * up);
+          const uint32_t f1 = half2_bits(__uint_as_float(a1 << 16) * up, __uint_as_float(a1 & 0xFFFF0000u) * up);
+          const uint32_t h0 = half2_to_codes(f0), h1 = half2_to_codes(f1);
+          hi[k] = h0 | (h1 << 16);
+          lo[k] = half2_to_codes(sub_half2(f0, codes_to_half2(h0))) | (half2_to_codes(sub_half2(f1, codes_to_half2(h1))) << 16);
+        }
+        sts128(pos, hi[0], hi[1], hi[2], hi[3]);
+        sts128(pos + 16384, lo[0], lo[1], lo[2], lo[3]);
+      }
+      // a row that is not finite: every score NaN, and so the result
+      if (mx >= 0x7F80u) w.rowf = __int_as_float(0x7FC00000);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(bQReady + X));
+      return w;
+    };
+    ItemMsg it = next_item(0);
+    Row row{};
+    if (mine(it)) row = queries(it);
+    for (int n = 0; it.valid; ++n) {
+      const int ntile = it.ntile;
+      if (!mine(it)) {                                 // this half is empty
         seq += ntile;
+        it = next_item(n + 1);
+        if (mine(it)) row = queries(it);
         continue;
       }
-      const int rr = 128 * X + r;                      // row of the block
-      const long long gr = static_cast<long long>(it.qb) * kTRows + rr;
-      const int tok = static_cast<int>(gr / a.G);
-      const bool live = rr < it.rows;
-      const int p = live ? it.p0 + tok : -1;           // an absent row sees nothing
-      const long long at = ((static_cast<long long>(it.b) * a.T + tok) * a.Hq + it.h * a.G + static_cast<int>(gr % a.G)) * kTD;
-      float rowf;
-      {
-        // the row as two e4m3 parts, scaled so that its largest value lies in [128, 256).  The last QK MMA of the
-        // item before has run: its scores were read.
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
-        uint4 w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = live ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
-        uint32_t mx = 0u;                              // largest magnitude: bf16 bits order as integers
-#pragma unroll
-        for (int i = 0; i < 64; ++i) mx = max(mx, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
-        int e = 7 - (static_cast<int>(mx >> 7) - 127);
-        e = mx && mx < 0x7F80u ? min(e, 120) : 0;
-        const float up = __int_as_float((e + 127) << 23) * sgn;
-        rowf = __int_as_float((127 - e) << 23);
-        const uint32_t qh = sb + kOffQ + X * 32768 + r * 128;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t u0 = u[8 * c + 2 * k], u1 = u[8 * c + 2 * k + 1];
-            const float v0 = __uint_as_float(u0 << 16) * up, v1 = __uint_as_float(u0 & 0xFFFF0000u) * up;
-            const float v2 = __uint_as_float(u1 << 16) * up, v3 = __uint_as_float(u1 & 0xFFFF0000u) * up;
-            const uint32_t h01 = to_codes(v0, v1), h23 = to_codes(v2, v3);
-            const uint32_t f01 = codes_to_half2(h01), f23 = codes_to_half2(h23);
-            const float2 g01 = __half22float2(*reinterpret_cast<const __half2*>(&f01));
-            const float2 g23 = __half22float2(*reinterpret_cast<const __half2*>(&f23));
-            hi[k] = h01 | (h23 << 16);
-            lo[k] = to_codes(v0 - g01.x, v1 - g01.y) | (to_codes(v2 - g23.x, v3 - g23.y) << 16);
-          }
-          const uint32_t off = static_cast<uint32_t>((c ^ (r & 7)) << 4);
-          sts128(qh + off, hi[0], hi[1], hi[2], hi[3]);
-          sts128(qh + 16384 + off, lo[0], lo[1], lo[2], lo[3]);
-        }
-        // a row that is not finite: every score NaN, and so the result
-        if (mx >= 0x7F80u) rowf = __int_as_float(0x7FC00000);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) bar_arrive(bar(bQReady + X));
-      }
+      const float rowf = row.rowf;
+      const int p = row.p;
       float m = kMNone, l = 0.0f;
       for (int t = 0; t < ntile; ++t, ++seq) {
         if (!wait(bDesc + seq % kDescs, seq / kDescs) || !wait(bSFull + X, nS)) break;
@@ -494,28 +594,38 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (lane == 0) bar_arrive(bar(bPFull + X));
       }
       if (failed) break;
+      // the next item's queries first: its scores then run beside what is left of this one
+      const ItemMsg done_item = it;
+      const Row done_row = row;
+      it = next_item(n + 1);
+      if (mine(it)) row = queries(it);
       // ---- the row's result (or partial) ----
       if (!wait(bODone + X, nO)) break;
       ++nO;
       tc_after();
       const float inv = l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
-      float* part = a.part + ((static_cast<long long>((it.b * a.H + it.h)) * nqb + it.qb) * nch + it.chunk) *
-                                 (static_cast<long long>(kTRows) * kPartRow) + static_cast<long long>(rr) * kPartRow;
+      float* part = parts + (static_cast<long long>(done_item.slot) * kTRows + 128 * X + r) * kPartRow;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         float o[32];
         tld32(to + 32u * c, o);
-        if (!live) continue;
-        if (nch == 1) {
+        if (!done_row.live) continue;
+        if (done_item.slot < 0) {
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
             w[k] = *reinterpret_cast<const uint32_t*>(&y);
           }
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at + 32 * c);
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + done_row.at + 32 * c;
+          if (wide) {
+            stg256(dst, w);
+            stg256(dst + 16, w + 8);
+          } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            for (int k = 0; k < 4; ++k)
+              reinterpret_cast<uint4*>(dst)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          }
         } else {
           float4* dst = reinterpret_cast<float4*>(part + 4 + 32 * c);
 #pragma unroll
@@ -531,11 +641,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const int t = tid - 256, pg = t >> 4;
     int seq = 0;
     for (int n = 0;; ++n) {
-      const int idx = next_item(n);
-      if (idx < 0) break;
-      TItem it;
-      tc_item(a, idx, nqb, nch, it);
-      const int ntile = (it.c1 - it.c0 + kTPg - 1) / kTPg;
+      const ItemMsg it = next_item(n);
+      if (!it.valid) break;
+      const int ntile = it.ntile;
       for (int i = 0; i < ntile; ++i, ++seq) {
         if (!wait(bVFull + seq % kVSt, seq / kVSt)) break;
         if (seq >= 2 && !wait(bDone + (seq - 2) % kDoneRing, (seq - 2) / kDoneRing)) break;
@@ -572,21 +680,52 @@ __global__ void __launch_bounds__(kTThreads, 1)
     if (warp == 12) {
       // ---- items, pages, TMA ----------------------------------------------------------------
       int seq = 0, n = 0, nk = 0, nv = 0;              // tiles, and copies issued
-      auto publish = [&](int idx) {
+      auto publish = [&](const ItemMsg& x) {
         if (lane == 0) {
-          *reinterpret_cast<volatile int*>(item_ring + n % kDescs) = idx;
+          item_ring[n % kDescs] = x;
           bar_arrive(bar(bItem + n % kDescs));
         }
         ++n;
       };
-      const int grid = gridDim.x;
-      for (int k = 0;; ++k) {                          // back and forth over the list, longest items first
-        const int idx = k * grid + ((k & 1) ? grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
-        if (k * grid >= items) break;
-        if (idx >= items) continue;
-        TItem it;
-        if (!tc_item(a, idx, nqb, nch, it)) continue;
-        publish(idx);
+      TBlock it;
+      TSplit cut{};
+      int e = entry0, h = 0, tiles = split && u0 < u1 ? tc_block(a, e, nqb, it) : 0;
+      long long at = static_cast<long long>(before0) * a.H;          // the item's first unit in the list
+      if (tiles) {
+        h = static_cast<int>((u0 - at) / (tiles + kItemCost));
+        at += static_cast<long long>(h) * (tiles + kItemCost);
+      }
+      long long whole = blockIdx.x;                    // not split: whole items in turn, the longest rows first
+      const long long items = static_cast<long long>(entries) * a.H;
+      for (;;) {
+        int t0 = 0, t1 = 0;                            // the item's tiles that are this CTA's
+        if (split) {
+          if (u0 >= u1) break;
+          t0 = max(0, static_cast<int>(u0 - at) - kItemCost);
+          t1 = static_cast<int>(min(u1 - at - kItemCost, static_cast<long long>(tiles)));
+          if (t1 <= t0) break;                         // the span ends before the item's first tile
+          if (t0 == 0 && t1 < tiles) {
+            cut = TSplit{1, it.b, h, it.qb, it.p0, it.rows, static_cast<int>((at + kItemCost + tiles - 1) / span), 0};
+          }
+        } else {
+          if (whole >= items) break;
+          h = static_cast<int>(whole % a.H);
+          t1 = tiles = tc_block(a, entries - 1 - static_cast<int>(whole / a.H), nqb, it);
+          whole += gridDim.x;
+          if (!tiles) continue;
+        }
+        const int slot = t0 == 0 && t1 == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 ? 0 : 1);
+        publish(ItemMsg{1, it.b, h, it.qb, it.p0, it.rows, it.pmin, it.pmax, t1 - t0, slot, {0, 0}});
+        {                                              // the item's queries on their way to L2, token by token
+          const unsigned first = static_cast<unsigned>(it.qb * kTRows) / a.G,
+                         end = static_cast<unsigned>(it.qb * kTRows + it.rows - 1) / a.G + 1;
+          for (unsigned t = first + lane; t < end; t += 32) {
+            const char* q = static_cast<const char*>(a.q) +
+                            2 * ((static_cast<long long>(it.b) * a.T + t) * a.Hq + h * a.G) * kTD;
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q), "r"(2 * kTD * a.G));
+          }
+        }
+        const int c0 = t0 * kTPg, c1 = min(it.pages, t1 * kTPg);
         const int* table = a.bt + static_cast<long long>(it.b) * a.maxp;
         // lane i holds page i of four tiles (lanes 8k .. 8k + 7: tile k); the next four tiles' ids and scales are on
         // their way meanwhile (two dependent loads are as long as a tile)
@@ -596,11 +735,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
         };
         auto fetch = [&](int ci) {
           PageInfo x{-1, kNoPage, 0, 1.0f};
-          if (ci < it.c1) {
+          if (ci < c1) {
             const int page = ci < it.r.ns ? ci : ci - it.r.ns + it.r.w0;
             const int pid = table[page];
             if (pid >= 0 && pid < a.num_pages) {
-              x.blk = pid * a.H + it.h;
+              x.blk = pid * a.H + h;
               x.j0 = kPage * page;
               x.ks = a.ks[x.blk];
               x.ev = static_cast<int>((__float_as_uint(a.vs[x.blk]) >> 23) & 0xFF) - 127;
@@ -610,12 +749,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
           }
           return x;
         };
-        PageInfo cur = fetch(it.c0 + lane);
-        for (int c4 = it.c0; c4 < it.c1 && !failed; c4 += 4 * kTPg) {
+        PageInfo cur = fetch(c0 + lane);
+        for (int c4 = c0; c4 < c1 && !failed; c4 += 4 * kTPg) {
           const PageInfo nxt = fetch(c4 + 4 * kTPg + lane);
           const bool seen = cur.j0 + 15 <= it.pmin && (!a.window || cur.j0 > it.pmax - a.window || cur.j0 + 15 < a.sinks);
           const uint32_t seen4 = __ballot_sync(0xffffffffu, seen), there4 = __ballot_sync(0xffffffffu, cur.blk >= 0);
-          for (int k = 0; k < 4 && c4 + k * kTPg < it.c1; ++k, ++seq) {
+          for (int k = 0; k < 4 && c4 + k * kTPg < c1; ++k, ++seq) {
             const bool on = (lane >> 3) == k;
             const int pg = lane & 7;
             const uint32_t bytes = static_cast<uint32_t>(__popc((there4 >> (8 * k)) & 0xFFu)) * kPage * kTD;
@@ -651,8 +790,19 @@ __global__ void __launch_bounds__(kTThreads, 1)
           cur = nxt;
         }
         if (failed) break;
+        if (split) {
+          at += kItemCost + tiles;
+          u0 = at;
+          if (u0 >= u1) break;
+          if (++h == a.H) {
+            h = 0;
+            do tiles = tc_block(a, ++e, nqb, it);
+            while (!tiles);
+          }
+        }
       }
-      publish(-1);
+      publish(ItemMsg{});
+      if (split && lane == 0) splits[blockIdx.x] = cut;
       // copies still in flight land before the CTA ends
       bool f2 = false;
       for (int s = nk >= kKSt ? nk - kKSt : 0; s < nk; ++s) (void)bar_wait(bar(bKFull + s % kKSt), (s / kKSt) & 1, f2);
@@ -666,14 +816,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
         failed = true;
         return false;
       };
-      int seq = 0, n = 0, idx = next_item(0);
+      int seq = 0, n = 0;
+      ItemMsg it = next_item(0);
       int nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;          // phases of the queries and of the weights
       int tiles = 0;
       bool two = false;                                // rows in half B
-      TItem it;
       auto open_item = [&]() {
-        tc_item(a, idx, nqb, nch, it);
-        tiles = uniform((it.c1 - it.c0 + kTPg - 1) / kTPg);
+        tiles = uniform(it.ntile);
         two = __all_sync(0xffffffffu, it.rows > 128);
       };
       auto scores = [&](uint32_t X, int s) {
@@ -696,12 +845,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         return true;
       };
-      bool ok = idx >= 0;
+      bool ok = __all_sync(0xffffffffu, it.valid);
+      bool open = ok;
       if (ok) {
         open_item();
         ok = first_scores(0);
       }
-      while (ok && idx >= 0) {
+      while (ok && open) {
         const int my_tiles = tiles;
         const bool my_two = two;
         for (int t = 0; t < my_tiles; ++t, ++seq) {
@@ -723,9 +873,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
           mma_commit_warp(bar(bDone + seq % kDoneRing));   // the tile's keys and values have been read
         }
         if (!ok) break;
-        idx = next_item(++n);
+        it = next_item(++n);
+        open = __all_sync(0xffffffffu, it.valid);
         if (failed) ok = false;
-        if (idx >= 0) {
+        if (ok && open) {
           open_item();
           ok = first_scores(seq);
         }
@@ -743,41 +894,43 @@ __global__ void __launch_bounds__(kTThreads, 1)
   if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-// Joins the chunks of an item's rows: a warp per row.
-__global__ void __launch_bounds__(256) kv8_tc_join_kernel(const __grid_constant__ Kv8Attn a, int nqb, int nch) {
-  const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int rr = static_cast<int>(w % kTRows);
-  const long long blk = w / kTRows;                    // (b H + h) nqb + qb
+// Joins the parts of the items that cross spans: 32 rows a block, a warp per row.
+__global__ void __launch_bounds__(256) kv8_tc_join_kernel(const __grid_constant__ Kv8Attn a, int ctas) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
   pdl_wait();
   pdl_trigger();
-  const int qb = static_cast<int>(blk % nqb), h = static_cast<int>(blk / nqb % a.H), b = static_cast<int>(blk / nqb / a.H);
-  if (b >= a.B) return;
-  const Kv8Seq s = kv8_seq(a, b);
-  const long long gr = static_cast<long long>(qb) * kTRows + rr;
-  if (gr >= static_cast<long long>(s.n) * a.G) return;
-  // chunks that had pages: the same cut as the items'
-  const long long r0 = static_cast<long long>(qb) * kTRows, rows = static_cast<long long>(s.n) * a.G;
-  const int last = static_cast<int>((r0 + kTRows < rows ? r0 + kTRows : rows) - 1);
-  const Kv8Range r = kv8_range(a.window, a.sinks, s.p0 + static_cast<int>(r0 / a.G), s.p0 + last / a.G);
-  const int tiles = (r.ns + r.nw + kTPg - 1) / kTPg, per = (tiles + nch - 1) / nch, used = (tiles + per - 1) / per;
-  const float* p = a.part + blk * nch * (static_cast<long long>(kTRows) * kPartRow) + static_cast<long long>(rr) * kPartRow;
+  const TSplit cut = reinterpret_cast<const TSplit*>(a.part)[c];
+  if (!cut.valid) return;
+  const float* parts = a.part + static_cast<size_t>(ctas) * (sizeof(TSplit) / sizeof(float));
   const long long step = static_cast<long long>(kTRows) * kPartRow;
-  float M = kMNone;
-  for (int c = 0; c < used; ++c) M = fmaxf(M, p[c * step]);
-  float L = 0.0f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = 0; c < used; ++c) {
-    const float f = ex2(p[c * step] - M);
-    L = fmaf(f, p[c * step + 1], L);
-    const float4 x = *reinterpret_cast<const float4*>(p + c * step + 4 + 4 * lane);
-    acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y), acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const int rr = 32 * blockIdx.y + 8 * i + warp;
+    if (rr >= cut.rows) return;
+    // the first part is in its CTA's second slot, the others in their CTAs' first
+    auto part = [&](int k) { return parts + (2LL * k + (k == c ? 1 : 0)) * step + static_cast<long long>(rr) * kPartRow; };
+    float M = kMNone;
+    for (int k = c + lane; k <= cut.last; k += 32) M = fmaxf(M, part(k)[0]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.0f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = c; k <= cut.last; ++k) {
+      const float* p = part(k);
+      const float f = ex2(p[0] - M);
+      L = fmaf(f, p[1], L);
+      const float4 x = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
+      acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y), acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
+    }
+    const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
+    const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                         y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    const unsigned gr = static_cast<unsigned>(cut.qb * kTRows + rr), tok = gr / static_cast<unsigned>(a.G);
+    const long long at = ((static_cast<long long>(cut.b) * a.T + tok) * a.Hq + cut.h * a.G + (gr - tok * a.G)) * kTD + 4 * lane;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
   }
-  const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
-  const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  const long long at = ((static_cast<long long>(b) * a.T + gr / a.G) * a.Hq + h * a.G + gr % a.G) * kTD + 4 * lane;
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
 }
 
 int sm_count() {
@@ -787,16 +940,14 @@ int sm_count() {
 }
 int query_blocks(int T, int G) { return static_cast<int>((static_cast<long long>(T) * G + kTRows - 1) / kTRows); }
 
-// Chunks per item: one where the items alone fill the SMs; else as many as give each SM an item, of four tiles
-// at least (the partials are written and read once more).
-int chunks_for(long long items, int max_seq_len) {
+// CTAs of a call: one per SM, fewer where the list of tiles cannot be that long.
+int ctas_for(int B, int H, int nqb, int max_seq_len) {
+  const long long most = static_cast<long long>(B) * H * nqb * ((max_seq_len + kTTok - 1) / kTTok + 1);
+  const long long n = (most * (1 + kItemCost) + kMinSpan - 1) / kMinSpan;
   const int sms = sm_count();
-  if (items >= sms) return 1;
-  const long long tiles = (max_seq_len + kTTok - 1) / kTTok;
-  long long n = sms / items;
-  n = n < tiles / 4 ? n : tiles / 4;
-  return n < 1 ? 1 : static_cast<int>(n);
+  return static_cast<int>(n < sms ? (n < 1 ? 1 : n) : sms);
 }
+bool splits(int B, int nqb) { return static_cast<long long>(B) * nqb <= kMaxBlocks; }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {        // from the driver, looked up once
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -831,28 +982,25 @@ bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale) {
 }
 
 size_t kv8_tc_workspace(int B, int T, int G, int H, int max_seq_len) {
-  const long long items = static_cast<long long>(B) * H * query_blocks(T, G);
-  const int nch = items > 0 ? chunks_for(items, max_seq_len) : 1;
-  return nch == 1 ? 16 : sizeof(float) * static_cast<size_t>(items) * nch * kTRows * kPartRow;
+  const int nqb = query_blocks(T, G);
+  if (!splits(B, nqb)) return 16;
+  return static_cast<size_t>(ctas_for(B, H, nqb, max_seq_len)) *
+         (sizeof(TSplit) + 2 * sizeof(float) * static_cast<size_t>(kTRows) * kPartRow);
 }
 
 cudaError_t launch_kv8_tc(const Kv8Attn& a, cudaStream_t s) {
   const int nqb = query_blocks(a.T, a.G);
-  const long long items1 = static_cast<long long>(a.B) * a.H * nqb;
-  const int nch = chunks_for(items1, a.max_seq_len);
-  const long long items = items1 * nch;
-  if (items > (1LL << 30)) return cudaErrorInvalidConfiguration;
   CUtensorMap mk, mv;
   const long long blocks = static_cast<long long>(a.num_pages) * a.H;
   if (!kv8_block_map(&mk, a.kc, blocks, kTD) || !kv8_block_map(&mv, a.vc, blocks, kTD)) return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = smem_attr_once(kv8_tc_kernel, kTSmem, configured);
   if (e != cudaSuccess) return e;
-  const int sms = sm_count();
-  e = launch_pdl(kv8_tc_kernel, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(kTThreads), kTSmem, s, a, mk, mv,
-                 nqb, nch, static_cast<int>(items));
-  if (e != cudaSuccess || nch == 1) return e;
-  return launch_pdl(kv8_tc_join_kernel, dim3(static_cast<unsigned>(items1 * (kTRows / 8))), dim3(256), 0, s, a, nqb, nch);
+  const int ctas = ctas_for(a.B, a.H, nqb, a.max_seq_len);
+  const bool split = splits(a.B, nqb);
+  e = launch_pdl(kv8_tc_kernel, dim3(ctas), dim3(kTThreads), kTSmem, s, a, mk, mv, nqb, split ? 1 : 0);
+  if (e != cudaSuccess || !split) return e;
+  return launch_pdl(kv8_tc_join_kernel, dim3(ctas, kTRows / 32), dim3(256), 0, s, a, ctas);
 }
 
 }  // namespace tq
