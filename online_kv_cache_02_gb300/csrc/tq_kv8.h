@@ -4,6 +4,8 @@
 
 #include "tq_internal.h"
 
+#include <cuda.h>
+
 namespace tq {
 
 constexpr int kE8Min = -100, kE8Max = 119;   // exponents of a block's scale
@@ -86,6 +88,8 @@ bool kv8_head_dim(int d);
 cudaError_t launch_kv8_append(const Kv8Append& a, int d, bool f32, cudaStream_t s);
 size_t kv8_rows_workspace(int B, int T, int G, int H, int d);
 cudaError_t launch_kv8_rows(const Kv8Attn& a, int d, bool f32, cudaStream_t s);
+// TMA map of a cache's blocks: coordinates (channel, token, block), boxes of one block's 128-channel panel.
+bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d);
 // Many query rows on the tensor cores (tq_kv8_tc.cu): whether the call takes
 // that form, its workspace and its launch.
 bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale);

@@ -19,7 +19,9 @@
 // that cross spans leave partials for a second kernel.
 
 #include "tq_kv8.h"
+#include "tq_tc.cuh"
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -27,9 +29,16 @@
 namespace tq {
 namespace {
 
+using tcx::bar_arrive_tx;
+using tcx::bar_init;
+using tcx::bar_wait;
+using tcx::lds128;
+using tcx::lds64;
+using tcx::su32;
+
 constexpr int kRWarps = 4;
 constexpr int kMinSpan = 8;               // pages a CTA takes at least (two per warp)
-constexpr int kMaxEntries = 2048;         // (sequence, row block) pairs that the split form lists
+constexpr int kMaxEntries = 4096;         // (sequence, row block) pairs that the split form lists
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -57,16 +66,16 @@ __device__ __forceinline__ uint32_t pack(__half lo, __half hi) {
   const __half2 h = __halves2half2(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint4 ldg128(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+__device__ __forceinline__ void tma_panel(uint32_t dst, const CUtensorMap* map, int x, int blk, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(blk), "r"(bar)
+      : "memory");
 }
-__device__ __forceinline__ uint2 ldg64(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
+
+// CTAs per SM, as shared memory (the rings, the joins and a list of usual length) and registers allow.
+__host__ __device__ constexpr int ctas_per_sm(int d, int R) { return d <= 128 && R == 8 ? 3 : 2; }
 
 // Channels: a lane's K words (four channels each) and V words, in panels of 128.
 template <int D> struct Lay {
@@ -75,6 +84,12 @@ template <int D> struct Lay {
   static constexpr int MT = D / 16;       // 16-channel tiles of the value product
   static constexpr int PAN = D >= 128 ? D / 128 : 1;
   static constexpr int KP = KW / PAN, VP = VW / PAN;   // words per panel
+  // a warp's ring of pages: a K and a V block each, in panels of 16 rows x 128 bytes (64 at d = 64), swizzled by TMA
+  static constexpr int ROW = D >= 128 ? 128 : 64, PANEL = kPage * ROW, BLOCK = kPage * D, STAGE = 2 * BLOCK;
+  static constexpr int ST = D == 64 ? 6 : D == 128 ? 3 : 2;
+  __device__ static __forceinline__ uint32_t at(int row, int chunk) {      // 16-byte piece `chunk` of a panel's row
+    return static_cast<uint32_t>(row * ROW + ((chunk ^ (ROW == 128 ? row & 7 : (row >> 1) & 3)) << 4));
+  }
   __device__ static __forceinline__ int k_ch(int t, int j) { return 128 * (j / KP) + 4 * KP * t + 4 * (j % KP); }
   __device__ static __forceinline__ int v_ch(int g, int w) { return 128 * (w / VP) + 4 * VP * g + 4 * (w % VP); }
 };
@@ -99,19 +114,30 @@ __device__ __forceinline__ int block_pages(const Kv8Attn& a, const Kv8Seq& s, in
 }
 
 template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(32 * kRWarps) kv8_rows_kernel(const __grid_constant__ Kv8Attn a, int nrb, int split) {
+__global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows_kernel(const __grid_constant__ Kv8Attn a, const __grid_constant__ CUtensorMap mk,
+                                                                const __grid_constant__ CUtensorMap mv, int nrb, int split) {
   using Y = Lay<D>;
   constexpr int R = 8 * NT, HL = F32 ? 2 : 1;
-  extern __shared__ __align__(16) float sm[];                    // [warps][R][D] joins; then the list's prefix sums
+  // [warps][stages] pages; [warps][R][D] joins; the list's prefix sums
+  extern __shared__ __align__(1024) unsigned char sm_raw[];
+  unsigned char* ring = sm_raw + ((0u - su32(sm_raw)) & 1023u);
+  float* sm = reinterpret_cast<float*>(ring + kRWarps * Y::ST * Y::STAGE);
+  __shared__ uint64_t s_bar[kRWarps][Y::ST];
   __shared__ float s_ml[kRWarps][R][2];
   __shared__ int s_scan[32 * kRWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t my_ring = su32(ring) + warp * Y::ST * Y::STAGE, my_bar = su32(&s_bar[warp][0]);
+  if (lane == 0)
+    for (int i = 0; i < Y::ST; ++i) bar_init(my_bar + 8 * i, 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncwarp();
+  bool failed = false;
   pdl_wait();
   pdl_trigger();
   const int entries = a.B * nrb;
   int* prefix = reinterpret_cast<int*>(sm + kRWarps * R * D);    // split form: pages of one head before entry i
 
-  long long u0 = 0, u1 = 0;                                      // this CTA's span of the list (pages)
+  long long u0 = 0, u1 = 0, u0_first = 0;                        // this CTA's span of the list (pages)
   int entry = 0;
   long long item_at = 0;                                         // list position of the current item's first page
   Item it{};
@@ -182,10 +208,87 @@ __global__ void __launch_bounds__(32 * kRWarps) kv8_rows_kernel(const __grid_con
     }
     entry = lo;
     load_entry(entry);
+    u0_first = u0;
     const long long base = static_cast<long long>(prefix[entry]) * a.H;
     it.h = static_cast<int>((u0 - base) / it.pages);
     item_at = base + static_cast<long long>(it.h) * it.pages;
   }
+
+  // The warp's pages: every kRWarps-th of the CTA's span (whole form: of an item), counted by k.  A lane looks up one of
+  // 32 of them: its block, place in the sequence and scales.
+  struct PageInfo {
+    int blk, page;
+    float ks, ev;
+  };
+  auto fetch = [&](int k0) {
+    PageInfo x{-1, 0, 0.0f, 0.0f};
+    const long long u = u0_first + warp + static_cast<long long>(kRWarps) * (k0 + lane);
+    if (u >= u1) return x;
+    int c, h, b;
+    Kv8Range r;
+    if (split) {
+      int lo = 0, hi = entries - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (static_cast<long long>(prefix[mid]) * a.H <= u) lo = mid;
+        else hi = mid - 1;
+      }
+      int x0, x1;
+      b = lo / nrb;
+      const int pages = block_pages(a, kv8_seq(a, b), lo % nrb, R, x0, x1, r);
+      const int rem = static_cast<int>(u - static_cast<long long>(prefix[lo]) * a.H);
+      h = rem / pages;
+      c = rem - h * pages;
+    } else {
+      c = static_cast<int>(u);
+      h = it.h;
+      b = it.b;
+      r = it.r;
+    }
+    x.page = c < r.ns ? c : c - r.ns + r.w0;
+    const int pid = a.bt[static_cast<long long>(b) * a.maxp + x.page];
+    if (pid < 0 || pid >= a.num_pages) {
+      atomicOr(a.err, kErrPage);
+      return x;
+    }
+    x.blk = pid * a.H + h;
+    x.ks = a.ks[x.blk];
+    x.ev = static_cast<float>(static_cast<int>((__float_as_uint(a.vs[x.blk]) >> 23) & 0xFF) - 127);
+    return x;
+  };
+  PageInfo cur{-1, 0, 0.0f, 0.0f}, nxt = cur;
+  int k = 0, nk = 0;                                             // the warp's pages used, and how many there are
+  uint32_t used = 0;                                             // stages filled so far, by this warp, over all items
+  // page k + ahead of the warp into its ring slot (a page that is not there arrives with no bytes)
+  auto issue = [&](int ahead) {
+    if (k + ahead >= nk) return;
+    const int j = (k & 31) + ahead;
+    const bool far = j >= 32;
+    if (lane == (j & 31)) {
+      const int blk = far ? nxt.blk : cur.blk;
+      const uint32_t st = (used + ahead) % Y::ST, bar = my_bar + 8 * st, dst = my_ring + st * Y::STAGE;
+      if (blk >= 0) {
+        bar_arrive_tx(bar, Y::STAGE);
+#pragma unroll
+        for (int p = 0; p < Y::PAN; ++p) {
+          tma_panel(dst + p * Y::PANEL, &mk, 128 * p, blk, bar);
+          tma_panel(dst + Y::BLOCK + p * Y::PANEL, &mv, 128 * p, blk, bar);
+        }
+      } else {
+        tcx::bar_arrive(bar);
+      }
+    }
+    __syncwarp();
+  };
+  auto start = [&]() {                                           // a new run of pages
+    const long long n = u1 - u0_first - warp;
+    k = 0;
+    nk = n > 0 ? static_cast<int>((n + kRWarps - 1) / kRWarps) : 0;
+    cur = fetch(0);
+    nxt = nk > 32 ? fetch(32) : cur;
+    for (int i = 0; i < Y::ST; ++i) issue(i);
+  };
+  if (split) start();
 
   long long whole = blockIdx.x;                                  // whole form: items in turn
   const long long items = static_cast<long long>(entries) * a.H;
@@ -206,6 +309,8 @@ __global__ void __launch_bounds__(32 * kRWarps) kv8_rows_kernel(const __grid_con
       c0 = 0;
       c1 = it.pages;
       complete = true;
+      u1 = it.pages;
+      start();
     }
     const int rows = min(R, static_cast<int>(min(static_cast<long long>(R), static_cast<long long>(it.n) * a.G -
                                                                              static_cast<long long>(it.rb) * R)));
@@ -275,48 +380,37 @@ __global__ void __launch_bounds__(32 * kRWarps) kv8_rows_kernel(const __grid_con
         m[nt][0] = m[nt][1] = -INFINITY;
         l[nt][0] = l[nt][1] = 0.0f;
       }
-      const int* table = a.bt + static_cast<long long>(it.b) * a.maxp;
-
-      for (int c = c0 + warp; c < c1; c += kRWarps) {
-        const int page = c < it.r.ns ? c : c - it.r.ns + it.r.w0;
-        const int pid = table[page];
-        if (pid < 0 || pid >= a.num_pages) {
-          if (lane == 0) atomicOr(a.err, kErrPage);
+      // list position of the warp's next page, and of the item's end
+      const long long seg_end = split ? item_at + c1 : c1;
+      while (k < nk && u0_first + warp + static_cast<long long>(kRWarps) * k < seg_end) {
+        const int from = k & 31;
+        const int page = __shfl_sync(0xffffffffu, cur.page, from), blk = __shfl_sync(0xffffffffu, cur.blk, from);
+        const float kscale = __shfl_sync(0xffffffffu, cur.ks, from), evf = __shfl_sync(0xffffffffu, cur.ev, from);
+        const uint32_t st = used % Y::ST, kb = my_ring + st * Y::STAGE, vb = kb + Y::BLOCK;
+        if (!__all_sync(0xffffffffu, bar_wait(my_bar + 8 * st, (used / Y::ST) & 1, failed))) failed = true;
+        if (blk < 0 || failed) {                                 // flagged already: the page's tokens are not there
+          issue(Y::ST);
+          ++used;
+          if ((++k & 31) == 0) {
+            cur = nxt;
+            nxt = fetch(k + 32);
+          }
           continue;
         }
-        const long long blk = static_cast<long long>(pid) * a.H + it.h;
-        const uint8_t* kp = a.kc + blk * (kPage * D);
-        const uint8_t* vp = a.vc + blk * (kPage * D);
-        uint32_t kw[2][Y::KW], vw[4][Y::VW];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int j = 0; j < Y::KW; j += 4) {
-            const uint4 x = ldg128(kp + (g + 8 * r) * D + Y::k_ch(t, j));
-            kw[r][j] = x.x, kw[r][j + 1] = x.y, kw[r][j + 2] = x.z, kw[r][j + 3] = x.w;
-          }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint8_t* row = vp + (2 * t + (r & 1) + 8 * (r >> 1)) * D;
-          if (Y::VP == 2) {
-            const uint2 x = ldg64(row + Y::v_ch(g, 0));
-            vw[r][0] = x.x, vw[r][1] = x.y;
-          } else {
-#pragma unroll
-            for (int w = 0; w < Y::VW; w += 4) {
-              const uint4 x = ldg128(row + Y::v_ch(g, w));
-              vw[r][w] = x.x, vw[r][w + 1] = x.y, vw[r][(w + 2) % Y::VW] = x.z, vw[r][(w + 3) % Y::VW] = x.w;
-            }
-          }
-        }
-        const float kscale = a.ks[blk];
-        const int ev = static_cast<int>((__float_as_uint(a.vs[blk]) >> 23) & 0xFF) - 127;
-        const float evf = static_cast<float>(ev), vinv = exp2f(-evf);
+        const float vinv = exp2_fast(-evf);
 
         // ---- scores ----
         float s[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+        uint32_t kw[2][Y::KW];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < Y::KW; j += 4) {
+            const uint4 x = lds128(kb + (j / Y::KP) * Y::PANEL + Y::at(g + 8 * r, (Y::KP / 4) * t + (j % Y::KP) / 4));
+            kw[r][j] = x.x, kw[r][j + 1] = x.y, kw[r][j + 2] = x.z, kw[r][j + 3] = x.w;
+          }
 #pragma unroll
         for (int j = 0; j < Y::KW; ++j) {
           const uint32_t a0 = half2_of(kw[0][j]), a2 = half2_of(kw[0][j] >> 16);
@@ -390,6 +484,28 @@ __global__ void __launch_bounds__(32 * kRWarps) kv8_rows_kernel(const __grid_con
           }
         }
         // ---- values ----
+        uint32_t vw[4][Y::VW];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 2 * t + (r & 1) + 8 * (r >> 1);
+          if (Y::VP == 2) {
+            const uint2 x = lds64(vb + Y::at(row, g >> 1) + 8 * (g & 1));
+            vw[r][0] = x.x, vw[r][1] = x.y;
+          } else {
+#pragma unroll
+            for (int w = 0; w < Y::VW; w += 4) {
+              const uint4 x = lds128(vb + (w / Y::VP) * Y::PANEL + Y::at(row, g));
+              vw[r][w] = x.x, vw[r][w + 1] = x.y, vw[r][(w + 2) % Y::VW] = x.z, vw[r][(w + 3) % Y::VW] = x.w;
+            }
+          }
+        }
+        __syncwarp();                                            // the slot has been read: the next page into it
+        issue(Y::ST);
+        ++used;
+        if ((++k & 31) == 0) {
+          cur = nxt;
+          nxt = fetch(k + 32);
+        }
         if (live != 0xFFFFu) {                                   // what no row sees may hold anything
 #pragma unroll
           for (int r = 0; r < 4; ++r)
@@ -496,6 +612,12 @@ __global__ void __launch_bounds__(32 * kRWarps) kv8_rows_kernel(const __grid_con
       while (it.pages == 0);
     }
   }
+  // after a wait that gave up, copies may still be on their way: they land before the CTA ends
+  if (failed) {
+    if (lane == 0) atomicOr(a.err, kErrTimeout);
+    bool f2 = false;
+    for (int i = 0; i < Y::ST; ++i) (void)bar_wait(my_bar + 8 * ((used + i) % Y::ST), ((used + i) / Y::ST) & 1, f2);
+  }
 }
 
 // Joins the partials of the items that cross spans: one block per (entry, head, row).
@@ -581,7 +703,7 @@ int sm_count() {
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   return sms;
 }
-constexpr int kCtasPerSm = 4;
+
 
 template <int D, int NT, bool F32>
 cudaError_t launch_t(const Kv8Attn& a, cudaStream_t s) {
@@ -589,16 +711,20 @@ cudaError_t launch_t(const Kv8Attn& a, cudaStream_t s) {
   const long long nrb = row_blocks(a.T, a.G, R);
   const long long entries = a.B * nrb, items = entries * a.H;
   if (items > 0x7FFFFFFFLL || items * R > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  const int grid = kCtasPerSm * sm_count();
-  // spans across items while the list is short; with four items or more per CTA whole items balance as well
-  const bool split = entries <= kMaxEntries && items < 4LL * grid;
-  const size_t smem = sizeof(float) * kRWarps * R * D + (split ? sizeof(int) * entries : 0);
+  const int grid = ctas_per_sm(D, R) * sm_count();
+  const bool split = entries <= kMaxEntries;           // else whole items: as many balance by themselves
+  using Y = Lay<D>;
+  const size_t fixed = 1024 + kRWarps * (Y::ST * Y::STAGE + sizeof(float) * R * D);
+  const size_t smem = fixed + (split ? sizeof(int) * entries : 0);
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = smem_attr_once(kv8_rows_kernel<D, NT, F32>,
-                                 static_cast<int>(sizeof(float) * kRWarps * R * D + sizeof(int) * kMaxEntries), configured);
+                                 static_cast<int>(fixed + sizeof(int) * kMaxEntries), configured);
   if (e != cudaSuccess) return e;
+  CUtensorMap mk, mv;
+  const long long blocks = static_cast<long long>(a.num_pages) * a.H;
+  if (!kv8_block_map(&mk, a.kc, blocks, D) || !kv8_block_map(&mv, a.vc, blocks, D)) return cudaErrorInvalidValue;
   const long long ctas = split ? grid : (items < 0x7FFFFFFF ? items : 0x7FFFFFFF);
-  e = launch_pdl(kv8_rows_kernel<D, NT, F32>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kRWarps), smem, s, a,
+  e = launch_pdl(kv8_rows_kernel<D, NT, F32>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kRWarps), smem, s, a, mk, mv,
                  static_cast<int>(nrb), split ? 1 : 0);
   if (e != cudaSuccess || !split) return e;
   return launch_pdl(kv8_join_kernel<D, F32>, dim3(static_cast<unsigned>(items * R)), dim3(128), 0, s, a,
@@ -620,7 +746,8 @@ bool kv8_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
 size_t kv8_rows_workspace(int B, int T, int G, int H, int d) {
   (void)B;
   (void)H;
-  return sizeof(float) * 2 * kCtasPerSm * static_cast<size_t>(sm_count()) * rows_per_block(T, G, d) * (d + 4);
+  const int R = rows_per_block(T, G, d);
+  return sizeof(float) * 2 * ctas_per_sm(d, R) * static_cast<size_t>(sm_count()) * R * (d + 4);
 }
 
 cudaError_t launch_kv8_rows(const Kv8Attn& a, int d, bool f32, cudaStream_t s) {
