@@ -85,6 +85,7 @@ __device__ __forceinline__ Kv8Range kv8_range(int window, int sinks, int pmin, i
 }
 
 bool kv8_head_dim(int d);
+int kv8_sm_count();                      // of the current device
 cudaError_t launch_kv8_append(const Kv8Append& a, int d, bool f32, cudaStream_t s);
 size_t kv8_rows_workspace(int B, int T, int G, int H, int d);
 cudaError_t launch_kv8_rows(const Kv8Attn& a, int d, bool f32, cudaStream_t s);

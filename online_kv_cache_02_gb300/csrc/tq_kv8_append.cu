@@ -136,7 +136,6 @@ __global__ void __launch_bounds__(32 * kAWarps) kv8_append_kernel(const __grid_c
   const int npg = (a.n_new + 2 * kPage - 2) / kPage;
   const int b = blockIdx.x / npg, ip = blockIdx.x % npg;
   pdl_wait();
-  pdl_trigger();
   const int start = a.start_pos[b];
   int n = a.new_lens ? a.new_lens[b] : a.n_new;
   if (start < 0 || n < 0 || n > a.n_new) {

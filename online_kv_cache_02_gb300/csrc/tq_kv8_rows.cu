@@ -37,7 +37,7 @@ using tcx::lds64;
 using tcx::su32;
 
 constexpr int kRWarps = 4;
-constexpr int kMinSpan = 8;               // pages a CTA takes at least (two per warp)
+constexpr int kMinSpan = 4;               // pages a CTA takes at least (one per warp)
 constexpr int kMaxEntries = 4096;         // (sequence, row block) pairs that the split form lists
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -94,6 +94,11 @@ template <int D> struct Lay {
   __device__ static __forceinline__ int v_ch(int g, int w) { return 128 * (w / VP) + 4 * VP * g + 4 * (w % VP); }
 };
 
+// An item's first part ends the span of one CTA; the join finds the others by it.
+struct RSplit {
+  int valid, b, rb, h, n, last, pad[2];   // n: the sequence's queries; last: the CTA that holds the item's end
+};
+
 struct Item {
   int b, rb, h;
   int p0, n;                              // the sequence's first query position and queries
@@ -124,7 +129,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   float* sm = reinterpret_cast<float*>(ring + kRWarps * Y::ST * Y::STAGE);
   __shared__ uint64_t s_bar[kRWarps][Y::ST];
   __shared__ float s_ml[kRWarps][R][2];
-  __shared__ int s_scan[32 * kRWarps];
+  __shared__ int s_scan[kRWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const uint32_t my_ring = su32(ring) + warp * Y::ST * Y::STAGE, my_bar = su32(&s_bar[warp][0]);
   if (lane == 0)
@@ -133,11 +138,14 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   __syncwarp();
   bool failed = false;
   pdl_wait();
-  pdl_trigger();
+  pdl_trigger();                                                 // the join's launch, beside the work
+  RSplit* records = reinterpret_cast<RSplit*>(a.part);            // one per CTA, then the partials' slots
+  float* parts = a.part + static_cast<size_t>(gridDim.x) * (sizeof(RSplit) / sizeof(float));
+  RSplit cut{};
   const int entries = a.B * nrb;
   int* prefix = reinterpret_cast<int*>(sm + kRWarps * R * D);    // split form: pages of one head before entry i
 
-  long long u0 = 0, u1 = 0, u0_first = 0;                        // this CTA's span of the list (pages)
+  long long u0 = 0, u1 = 0, u0_first = 0, span = 1;              // this CTA's span of the list (pages)
   int entry = 0;
   long long item_at = 0;                                         // list position of the current item's first page
   Item it{};
@@ -163,42 +171,43 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
       prefix[e] = sum;
       sum += c;
     }
-    s_scan[tid] = sum;
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      run += lane >= o ? v : 0;
+    }
+    if (lane == 31) s_scan[warp] = run;
     __syncthreads();
-    for (int o = 1; o < 32 * kRWarps; o <<= 1) {
-      const int v = tid >= o ? s_scan[tid - o] : 0;
-      __syncthreads();
-      s_scan[tid] += v;
-      __syncthreads();
+    int before = run - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kRWarps; ++w) {
+      before += w < warp ? s_scan[w] : 0;
+      total += s_scan[w];
     }
-    const int before = tid ? s_scan[tid - 1] : 0;
-    for (int i = 0; i < per; ++i) {
-      const int e = tid * per + i;
-      if (e < entries) prefix[e] += before;
-    }
-    const int total = s_scan[32 * kRWarps - 1];
+    for (int i = 0; i < per && tid * per + i < entries; ++i) prefix[tid * per + i] += before;
     __syncthreads();
     const long long units = static_cast<long long>(total) * a.H;
-    long long span = (units + gridDim.x - 1) / gridDim.x;
+    span = (units + gridDim.x - 1) / gridDim.x;
     span = span < kMinSpan ? kMinSpan : span;
     u0 = span * blockIdx.x;
     u1 = u0 + span < units ? u0 + span : units;
-    if (u0 >= u1 && blockIdx.x) return;
-    if (blockIdx.x == 0) {                                       // decode rows that see nothing: zeros
-      for (int e = 0; e < entries; ++e) {
-        const int c = (e + 1 < entries ? prefix[e + 1] : total) - prefix[e];
-        if (c == 0 && a.decode) {
-          for (int i = tid; i < a.H * R * D; i += 32 * kRWarps) {
-            const int row = (e % nrb) * R + i / D % R;
-            if (row < a.G) {
-              const long long o = (static_cast<long long>(e / nrb) * a.Hq + i / (D * R) * a.G + row) * D + i % D;
-              if (F32) static_cast<float*>(a.out)[o] = 0.0f;
-              else static_cast<unsigned short*>(a.out)[o] = 0;
-            }
+    if (a.decode) {                                              // rows that see nothing: zeros
+      for (int e = blockIdx.x; e < entries; e += gridDim.x) {
+        if ((e + 1 < entries ? prefix[e + 1] : total) != prefix[e]) continue;
+        for (int i = tid; i < a.H * R * D; i += 32 * kRWarps) {
+          const int row = (e % nrb) * R + i / D % R;
+          if (row < a.G) {
+            const long long o = (static_cast<long long>(e / nrb) * a.Hq + i / (D * R) * a.G + row) * D + i % D;
+            if (F32) static_cast<float*>(a.out)[o] = 0.0f;
+            else static_cast<unsigned short*>(a.out)[o] = 0;
           }
         }
       }
-      if (u0 >= u1) return;
+    }
+    if (u0 >= u1) {
+      if (tid == 0) records[blockIdx.x].valid = 0;
+      return;
     }
     int lo = 0, hi = entries - 1;                                // the entry that holds u0
     while (lo < hi) {
@@ -218,7 +227,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   // 32 of them: its block, place in the sequence and scales.
   struct PageInfo {
     int blk, page;
-    float ks, ev;
+    float ks, vs;
   };
   auto fetch = [&](int k0) {
     PageInfo x{-1, 0, 0.0f, 0.0f};
@@ -253,7 +262,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
     }
     x.blk = pid * a.H + h;
     x.ks = a.ks[x.blk];
-    x.ev = static_cast<float>(static_cast<int>((__float_as_uint(a.vs[x.blk]) >> 23) & 0xFF) - 127);
+    x.vs = a.vs[x.blk];
     return x;
   };
   PageInfo cur{-1, 0, 0.0f, 0.0f}, nxt = cur;
@@ -302,6 +311,8 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
       c1 = static_cast<int>((u1 < item_at + it.pages ? u1 : item_at + it.pages) - item_at);
       complete = c0 == 0 && c1 == it.pages;
       slot = 2 * blockIdx.x + (c0 > 0 ? 0 : 1);
+      if (c0 == 0 && !complete)
+        cut = RSplit{1, it.b, it.rb, it.h, it.n, static_cast<int>((item_at + it.pages - 1) / span), {0, 0}};
     } else {
       if (whole >= items) break;
       it.h = static_cast<int>(whole % a.H);
@@ -385,7 +396,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
       while (k < nk && u0_first + warp + static_cast<long long>(kRWarps) * k < seg_end) {
         const int from = k & 31;
         const int page = __shfl_sync(0xffffffffu, cur.page, from), blk = __shfl_sync(0xffffffffu, cur.blk, from);
-        const float kscale = __shfl_sync(0xffffffffu, cur.ks, from), evf = __shfl_sync(0xffffffffu, cur.ev, from);
+        const float kscale = __shfl_sync(0xffffffffu, cur.ks, from), vscale = __shfl_sync(0xffffffffu, cur.vs, from);
         const uint32_t st = used % Y::ST, kb = my_ring + st * Y::STAGE, vb = kb + Y::BLOCK;
         if (!__all_sync(0xffffffffu, bar_wait(my_bar + 8 * st, (used / Y::ST) & 1, failed))) failed = true;
         if (blk < 0 || failed) {                                 // flagged already: the page's tokens are not there
@@ -397,6 +408,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
           }
           continue;
         }
+        const float evf = static_cast<float>(static_cast<int>((__float_as_uint(vscale) >> 23) & 0xFF) - 127);
         const float vinv = exp2_fast(-evf);
 
         // ---- scores ----
@@ -582,7 +594,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
                 make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
           }
         } else {
-          float* p = a.part + (static_cast<long long>(slot) * R + row) * (D + 4);
+          float* p = parts + (static_cast<long long>(slot) * R + row) * (D + 4);
           *reinterpret_cast<float4*>(p + 4 + ch) = acc;
           if (ch == 0) {
             p[0] = M;
@@ -612,6 +624,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
       while (it.pages == 0);
     }
   }
+  if (split && tid == 0) records[blockIdx.x] = cut;
   // after a wait that gave up, copies may still be on their way: they land before the CTA ends
   if (failed) {
     if (lane == 0) atomicOr(a.err, kErrTimeout);
@@ -620,77 +633,75 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   }
 }
 
-// Joins the partials of the items that cross spans: one block per (entry, head, row).
-template <int D, bool F32>
-__global__ void __launch_bounds__(128) kv8_join_kernel(const __grid_constant__ Kv8Attn a, int nrb, int R, int grid) {
-  __shared__ int s_sum[2][4];
-  __shared__ float4 s_acc[4][D / 4];
-  __shared__ float s_l[4];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row = blockIdx.x % R, h = (blockIdx.x / R) % a.H, e = blockIdx.x / R / a.H;
+// Joins the parts of the items that cross spans: a block per CTA of the first kernel, 16 / R warps per row.
+template <int D, int R, bool F32>
+__global__ void __launch_bounds__(512) kv8_join_kernel(const __grid_constant__ Kv8Attn a, int ctas) {
+  constexpr int kPer = 16 / R, kV = D >= 128 ? D / 128 : 1;      // warps per row, float4 per lane
+  __shared__ float4 s_acc[16][D / 4];
+  __shared__ float s_l[16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = warp / kPer, part_of = warp % kPer, c = blockIdx.x;
   pdl_wait();
-  pdl_trigger();
-  const Kv8Seq s = kv8_seq(a, e / nrb);
-  const long long gr = static_cast<long long>(e % nrb) * R + row;
-  if (gr >= static_cast<long long>(s.n) * a.G) return;
-  int before = 0, total = 0, x0, x1;
-  Kv8Range r;
-  for (int i = tid; i < a.B * nrb; i += 128) {
-    const int c = block_pages(a, kv8_seq(a, i / nrb), i % nrb, R, x0, x1, r);
-    total += c;
-    before += i < e ? c : 0;
-  }
-  before = __reduce_add_sync(0xffffffffu, before);
-  total = __reduce_add_sync(0xffffffffu, total);
-  if (lane == 0) s_sum[0][warp] = before, s_sum[1][warp] = total;
-  __syncthreads();
-  before = s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3];
-  total = s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3];
-  const int pages = block_pages(a, s, e % nrb, R, x0, x1, r);
-  long long span = (static_cast<long long>(total) * a.H + grid - 1) / grid;
-  span = span < kMinSpan ? kMinSpan : span;
-  const long long at = static_cast<long long>(before) * a.H + static_cast<long long>(h) * pages;
-  const int first = static_cast<int>(at / span), last = static_cast<int>((at + pages - 1) / span);
-  if (first == last) return;                                     // one CTA had it all and wrote it
-  auto part = [&](int c) {                                       // CTA c's partial of this row
-    return a.part + (static_cast<long long>(2 * c + (c == first ? 1 : 0)) * R + row) * (D + 4);
-  };
-  float M = -INFINITY;
-  for (int c = first + lane; c <= last; c += 32) M = fmaxf(M, part(c)[0]);
+  const RSplit cut = reinterpret_cast<const RSplit*>(a.part)[c];
+  if (!cut.valid) return;
+  const float* parts = a.part + static_cast<size_t>(ctas) * (sizeof(RSplit) / sizeof(float));
+  const int gr = cut.rb * R + row;
+  const bool live = gr < cut.n * a.G;
+  // the first part is in its CTA's second slot, the others in their CTAs' first
+  auto part = [&](int k) { return parts + ((2LL * k + (k == c ? 1 : 0)) * R + row) * (D + 4); };
+  float M = -INFINITY, L = 0.0f;
+  float4 acc[kV];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.0f;
-  float4 acc[(D + 127) / 128];
+  for (int i = 0; i < kV; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
+    for (int k = c + lane; k <= cut.last; k += 32) M = fmaxf(M, part(k)[0]);
 #pragma unroll
-  for (int i = 0; i < (D + 127) / 128; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (M == -INFINITY) {
-    for (int c = first + warp; c <= last; c += 4) L += part(c)[1];
-  } else {
-    for (int c = first + warp; c <= last; c += 4) {
-      const float* p = part(c);
-      const float f = exp2_fast(p[0] - M);
-      L += f * p[1];
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == -INFINITY ? 0.0f : M;                 // no key, or scores that are all NaN: sums of 0 or NaN
+#pragma unroll 8
+    for (int k = c + part_of; k <= cut.last; k += kPer) {
+      const float* p = part(k);
+      const float f = exp2_fast(p[0] - ref);
+      L += M == -INFINITY ? p[1] : f * p[1];
 #pragma unroll
-      for (int i = 0; i < (D + 127) / 128; ++i) {
+      for (int i = 0; i < kV; ++i) {
         if (128 * i + 4 * lane >= D) continue;
         const float4 x = *reinterpret_cast<const float4*>(p + 4 + 128 * i + 4 * lane);
         acc[i].x += f * x.x, acc[i].y += f * x.y, acc[i].z += f * x.z, acc[i].w += f * x.w;
       }
     }
   }
+  if (kPer > 1) {
 #pragma unroll
-  for (int i = 0; i < (D + 127) / 128; ++i)
-    if (128 * i + 4 * lane < D) s_acc[warp][32 * i + lane] = acc[i];
-  if (lane == 0) s_l[warp] = L;
-  __syncthreads();
-  L = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+    for (int i = 0; i < kV; ++i)
+      if (128 * i + 4 * lane < D) s_acc[warp][32 * i + lane] = acc[i];
+    if (lane == 0) s_l[warp] = L;
+    __syncthreads();
+    if (part_of != 0) return;
+    for (int w = 1; w < kPer; ++w) {
+      L += s_l[warp + w];
+#pragma unroll
+      for (int i = 0; i < kV; ++i)
+        if (128 * i + 4 * lane < D) {
+          const float4 x = s_acc[warp + w][32 * i + lane];
+          acc[i].x += x.x, acc[i].y += x.y, acc[i].z += x.z, acc[i].w += x.w;
+        }
+    }
+  }
+  if (!live) return;
   const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
-  const long long o = ((static_cast<long long>(e / nrb) * a.T + gr / a.G) * a.Hq + h * a.G + gr % a.G) * D;
-  for (int i = tid; i < D; i += 128) {
-    const float y = (reinterpret_cast<const float*>(s_acc[0])[i] + reinterpret_cast<const float*>(s_acc[1])[i] +
-                     reinterpret_cast<const float*>(s_acc[2])[i] + reinterpret_cast<const float*>(s_acc[3])[i]) * inv;
-    if (F32) static_cast<float*>(a.out)[o + i] = y;
-    else static_cast<__nv_bfloat16*>(a.out)[o + i] = __float2bfloat16(y);
+  const long long o = ((static_cast<long long>(cut.b) * a.T + gr / a.G) * a.Hq + cut.h * a.G + gr % a.G) * D;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    if (128 * i + 4 * lane >= D) continue;
+    const float4 y = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
+    const long long at = o + 128 * i + 4 * lane;
+    if (F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = y;
+    } else {
+      const __nv_bfloat162 p0 = __floats2bfloat162_rn(y.x, y.y), p1 = __floats2bfloat162_rn(y.z, y.w);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&p0), *reinterpret_cast<const uint32_t*>(&p1));
+    }
   }
 }
 
@@ -698,11 +709,6 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const __grid_constant__ K
 int rows_per_block(int T, int G, int d) { return static_cast<long long>(T) * G > 8 && d <= 128 ? 16 : 8; }
 int row_blocks(int T, int G, int R) { return static_cast<int>((static_cast<long long>(T) * G + R - 1) / R); }
 
-int sm_count() {
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
 
 
 template <int D, int NT, bool F32>
@@ -711,7 +717,7 @@ cudaError_t launch_t(const Kv8Attn& a, cudaStream_t s) {
   const long long nrb = row_blocks(a.T, a.G, R);
   const long long entries = a.B * nrb, items = entries * a.H;
   if (items > 0x7FFFFFFFLL || items * R > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  const int grid = ctas_per_sm(D, R) * sm_count();
+  const int grid = ctas_per_sm(D, R) * kv8_sm_count();
   const bool split = entries <= kMaxEntries;           // else whole items: as many balance by themselves
   using Y = Lay<D>;
   const size_t fixed = 1024 + kRWarps * (Y::ST * Y::STAGE + sizeof(float) * R * D);
@@ -727,8 +733,7 @@ cudaError_t launch_t(const Kv8Attn& a, cudaStream_t s) {
   e = launch_pdl(kv8_rows_kernel<D, NT, F32>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kRWarps), smem, s, a, mk, mv,
                  static_cast<int>(nrb), split ? 1 : 0);
   if (e != cudaSuccess || !split) return e;
-  return launch_pdl(kv8_join_kernel<D, F32>, dim3(static_cast<unsigned>(items * R)), dim3(128), 0, s, a,
-                    static_cast<int>(nrb), R, grid);
+  return launch_pdl(kv8_join_kernel<D, R, F32>, dim3(grid), dim3(512), 0, s, a, grid);
 }
 
 template <int D>
@@ -747,7 +752,7 @@ size_t kv8_rows_workspace(int B, int T, int G, int H, int d) {
   (void)B;
   (void)H;
   const int R = rows_per_block(T, G, d);
-  return sizeof(float) * 2 * ctas_per_sm(d, R) * static_cast<size_t>(sm_count()) * R * (d + 4);
+  return static_cast<size_t>(ctas_per_sm(d, R)) * kv8_sm_count() * (sizeof(RSplit) + 2 * sizeof(float) * R * (d + 4));
 }
 
 cudaError_t launch_kv8_rows(const Kv8Attn& a, int d, bool f32, cudaStream_t s) {

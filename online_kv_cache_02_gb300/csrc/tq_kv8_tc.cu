@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  pdl_trigger();
+  pdl_trigger();                                       // the join's launch
   // the list, cut into equal spans: units before each block (of one head), by a scan in the queries' room
   const int entries = a.B * nqb;
   long long u0 = 0, u1 = 0, span = 1;
@@ -898,7 +898,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
 __global__ void __launch_bounds__(256) kv8_tc_join_kernel(const __grid_constant__ Kv8Attn a, int ctas) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
   pdl_wait();
-  pdl_trigger();
   const TSplit cut = reinterpret_cast<const TSplit*>(a.part)[c];
   if (!cut.valid) return;
   const float* parts = a.part + static_cast<size_t>(ctas) * (sizeof(TSplit) / sizeof(float));
@@ -933,18 +932,13 @@ __global__ void __launch_bounds__(256) kv8_tc_join_kernel(const __grid_constant_
   }
 }
 
-int sm_count() {
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
 int query_blocks(int T, int G) { return static_cast<int>((static_cast<long long>(T) * G + kTRows - 1) / kTRows); }
 
 // CTAs of a call: one per SM, fewer where the list of tiles cannot be that long.
 int ctas_for(int B, int H, int nqb, int max_seq_len) {
   const long long most = static_cast<long long>(B) * H * nqb * ((max_seq_len + kTTok - 1) / kTTok + 1);
   const long long n = (most * (1 + kItemCost) + kMinSpan - 1) / kMinSpan;
-  const int sms = sm_count();
+  const int sms = kv8_sm_count();
   return static_cast<int>(n < sms ? (n < 1 ? 1 : n) : sms);
 }
 bool splits(int B, int nqb) { return static_cast<long long>(B) * nqb <= kMaxBlocks; }
@@ -962,6 +956,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {        // from the driver, looke
 }
 
 }  // namespace
+
+int kv8_sm_count() {
+  static std::atomic<int> known[64];                   // per device: the query costs as much as a launch
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 152;
+  int sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (sms > 0) return sms;
+  sms = 152;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && dev < 64)
+    known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
 
 bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d) {
   auto fn = encode_fn();
