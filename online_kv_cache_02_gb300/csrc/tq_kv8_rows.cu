@@ -13,10 +13,14 @@
 //   O^T[d][R] += Vc^T w,  l += w 2^-ev,  out = O / l.
 // The transposed product uses all 8 columns of the MMA for 8 query rows.
 //
-// All pages of all items form one list, cut into equal spans, one per CTA
-// (whatever the sequences' lengths); a CTA's warps take the pages of its span
-// in turn and join their (M, l, O) in shared memory at an item's end.  Items
-// that cross spans leave partials for a second kernel.
+// A CTA's warps take its pages in turn and join their (M, l, O) in shared memory
+// at an item's end.  How the pages come to the CTAs:
+//   direct  few pages per item: an item per cluster of 1 to 8 CTAs, joined through
+//           distributed shared memory, one launch;
+//   split   all pages of all items form one list, cut into equal spans, one per CTA
+//           (whatever the sequences' lengths); items that cross spans leave partials
+//           for a second kernel;
+//   whole   too many sequences to list: items in turn.
 
 #include "tq_kv8.h"
 #include "tq_tc.cuh"
@@ -25,6 +29,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 namespace tq {
 namespace {
@@ -38,7 +44,9 @@ using tcx::su32;
 
 constexpr int kRWarps = 4;
 constexpr int kMinSpan = 4;               // pages a CTA takes at least (one per warp)
-constexpr int kMaxEntries = 4096;         // (sequence, row block) pairs that the split form lists
+constexpr int kMaxEntries = 2048;         // (sequence, row block) pairs that the split form lists
+constexpr int kDirectPages = 32;          // pages per CTA up to which the direct form is taken
+enum Mode { kWhole = 0, kSplit = 1, kDirect = 2 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -72,6 +80,26 @@ __device__ __forceinline__ void tma_panel(uint32_t dst, const CUtensorMap* map, 
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(blk), "r"(bar)
       : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared-memory address `p` of the cluster's CTA `rank`, and loads from it.
+__device__ __forceinline__ uint32_t map_cluster(uint32_t p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(p), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t p) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(p));
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t p) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p));
+  return v;
 }
 
 // CTAs per SM, as shared memory (the rings, the joins and a list of usual length) and registers allow.
@@ -120,7 +148,8 @@ __device__ __forceinline__ int block_pages(const Kv8Attn& a, const Kv8Seq& s, in
 
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows_kernel(const __grid_constant__ Kv8Attn a, const __grid_constant__ CUtensorMap mk,
-                                                                const __grid_constant__ CUtensorMap mv, int nrb, int split) {
+                                                                const __grid_constant__ CUtensorMap mv, int nrb, int mode,
+                                                                int cluster) {
   using Y = Lay<D>;
   constexpr int R = 8 * NT, HL = F32 ? 2 : 1;
   // [warps][stages] pages; [warps][R][D] joins; the list's prefix sums
@@ -137,6 +166,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
   bool failed = false;
+  const bool split = mode == kSplit;
   pdl_wait();
   pdl_trigger();                                                 // the join's launch, beside the work
   RSplit* records = reinterpret_cast<RSplit*>(a.part);            // one per CTA, then the partials' slots
@@ -144,6 +174,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   RSplit cut{};
   const int entries = a.B * nrb;
   int* prefix = reinterpret_cast<int*>(sm + kRWarps * R * D);    // split form: pages of one head before entry i
+  Kv8Seq* seqs = reinterpret_cast<Kv8Seq*>(prefix + ((entries + 1) & ~1));   // and its sequence's queries
 
   long long u0 = 0, u1 = 0, u0_first = 0, span = 1;              // this CTA's span of the list (pages)
   int entry = 0;
@@ -152,7 +183,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   auto load_entry = [&](int e) {
     it.b = e / nrb;
     it.rb = e % nrb;
-    const Kv8Seq s = kv8_seq(a, it.b);
+    const Kv8Seq s = split ? seqs[e] : kv8_seq(a, it.b);
     it.p0 = s.p0;
     it.n = s.n;
     it.pmin = it.pmax = 0;
@@ -167,7 +198,9 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
       if (e >= entries) break;
       int x0, x1;
       Kv8Range r;
-      const int c = block_pages(a, kv8_seq(a, e / nrb), e % nrb, R, x0, x1, r);
+      const Kv8Seq s = kv8_seq(a, e / nrb);
+      const int c = block_pages(a, s, e % nrb, R, x0, x1, r);
+      seqs[e] = s;
       prefix[e] = sum;
       sum += c;
     }
@@ -219,11 +252,12 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
     load_entry(entry);
     u0_first = u0;
     const long long base = static_cast<long long>(prefix[entry]) * a.H;
-    it.h = static_cast<int>((u0 - base) / it.pages);
+    it.h = static_cast<int>(u0 - base) / it.pages;
     item_at = base + static_cast<long long>(it.h) * it.pages;
   }
 
-  // The warp's pages: every kRWarps-th of the CTA's span (whole form: of an item), counted by k.  A lane looks up one of
+  const int step = mode == kDirect ? kRWarps * cluster : kRWarps;
+  // The warp's pages: every step-th of the CTA's span (whole and direct form: of an item), counted by k.  A lane looks up one of
   // 32 of them: its block, place in the sequence and scales.
   struct PageInfo {
     int blk, page;
@@ -231,7 +265,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   };
   auto fetch = [&](int k0) {
     PageInfo x{-1, 0, 0.0f, 0.0f};
-    const long long u = u0_first + warp + static_cast<long long>(kRWarps) * (k0 + lane);
+    const long long u = u0_first + warp + static_cast<long long>(step) * (k0 + lane);
     if (u >= u1) return x;
     int c, h, b;
     Kv8Range r;
@@ -244,8 +278,8 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
       }
       int x0, x1;
       b = lo / nrb;
-      const int pages = block_pages(a, kv8_seq(a, b), lo % nrb, R, x0, x1, r);
-      const int rem = static_cast<int>(u - static_cast<long long>(prefix[lo]) * a.H);
+      const int pages = block_pages(a, seqs[lo], lo % nrb, R, x0, x1, r);
+      const int rem = static_cast<int>(u - static_cast<long long>(prefix[lo]) * a.H);   // below pages H: the host bounds it
       h = rem / pages;
       c = rem - h * pages;
     } else {
@@ -292,14 +326,15 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   auto start = [&]() {                                           // a new run of pages
     const long long n = u1 - u0_first - warp;
     k = 0;
-    nk = n > 0 ? static_cast<int>((n + kRWarps - 1) / kRWarps) : 0;
+    nk = n > 0 ? static_cast<int>((n + step - 1) / step) : 0;
     cur = fetch(0);
     nxt = nk > 32 ? fetch(32) : cur;
     for (int i = 0; i < Y::ST; ++i) issue(i);
   };
   if (split) start();
 
-  long long whole = blockIdx.x;                                  // whole form: items in turn
+  const int rank = mode == kDirect ? static_cast<int>(blockIdx.x) % cluster : 0;
+  long long whole = mode == kDirect ? blockIdx.x / cluster : blockIdx.x;   // the item; whole form: items in turn
   const long long items = static_cast<long long>(entries) * a.H;
   for (;;) {
     int c0, c1;                                                  // pages of the item that are this CTA's
@@ -319,7 +354,8 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
       load_entry(static_cast<int>(entries - 1 - whole / a.H));   // the longest rows of a prompt first
       c0 = 0;
       c1 = it.pages;
-      complete = true;
+      complete = mode == kWhole || cluster == 1;
+      u0_first = kRWarps * rank;
       u1 = it.pages;
       start();
     }
@@ -339,20 +375,25 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
         float mx = 0.0f;
         const long long base = row < rows ? ((static_cast<long long>(it.b) * a.T + tok) * a.Hq + hq) * D : 0;
 #pragma unroll
-        for (int j = 0; j < Y::KW; ++j) {
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < Y::KW; j += 2) {                     // eight channels
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
           if (row < rows) {
             if (F32) {
-              const float* q = static_cast<const float*>(a.q) + base + Y::k_ch(t, j);
-              x = make_float4(q[0], q[1], q[2], q[3]);
+              const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + base + Y::k_ch(t, j));
+              x = q[0];
+              y = q[1];
             } else {
-              const unsigned short* q = static_cast<const unsigned short*>(a.q) + base + Y::k_ch(t, j);
-              x = make_float4(__uint_as_float(q[0] << 16), __uint_as_float(q[1] << 16), __uint_as_float(q[2] << 16),
-                              __uint_as_float(q[3] << 16));
+              const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(a.q) + base + Y::k_ch(t, j));
+              x = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                              __uint_as_float(w.y & 0xFFFF0000u));
+              y = make_float4(__uint_as_float(w.z << 16), __uint_as_float(w.z & 0xFFFF0000u), __uint_as_float(w.w << 16),
+                              __uint_as_float(w.w & 0xFFFF0000u));
             }
           }
           v[4 * j] = x.x, v[4 * j + 1] = x.y, v[4 * j + 2] = x.z, v[4 * j + 3] = x.w;
+          v[4 * j + 4] = y.x, v[4 * j + 5] = y.y, v[4 * j + 6] = y.z, v[4 * j + 7] = y.w;
           mx = fmaxf(fmaxf(fmaxf(mx, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(x.z))), fabsf(x.w));
+          mx = fmaxf(fmaxf(fmaxf(mx, fabsf(y.x)), fmaxf(fabsf(y.y), fabsf(y.z))), fabsf(y.w));
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -393,7 +434,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
       }
       // list position of the warp's next page, and of the item's end
       const long long seg_end = split ? item_at + c1 : c1;
-      while (k < nk && u0_first + warp + static_cast<long long>(kRWarps) * k < seg_end) {
+      while (k < nk && u0_first + warp + static_cast<long long>(step) * k < seg_end) {
         const int from = k & 31;
         const int page = __shfl_sync(0xffffffffu, cur.page, from), blk = __shfl_sync(0xffffffffu, cur.blk, from);
         const float kscale = __shfl_sync(0xffffffffu, cur.ks, from), vscale = __shfl_sync(0xffffffffu, cur.vs, from);
@@ -560,6 +601,21 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
                 make_float4(o[nt][2 * w][c], o[nt][2 * w][2 + c], o[nt][2 * w + 1][c], o[nt][2 * w + 1][2 + c]);
         }
       __syncthreads();
+      // four channels of one row's result
+      auto store_row = [&](int row, int ch, float4 acc, float L) {
+        const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
+        const int gr = it.rb * R + row, tok = gr / a.G;
+        const long long at = ((static_cast<long long>(it.b) * a.T + tok) * a.Hq + it.h * a.G + (gr - tok * a.G)) * D + ch;
+        if (F32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) =
+              make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        } else {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                               y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+          *reinterpret_cast<uint2*>(static_cast<unsigned short*>(a.out) + at) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+        }
+      };
       for (int i = tid; i < R * D / 4; i += 32 * kRWarps) {
         const int row = i / (D / 4), ch = 4 * (i % (D / 4));
         if (row >= rows) continue;
@@ -580,21 +636,11 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
           }
         }
         if (complete) {
-          const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
-          const long long gr = static_cast<long long>(it.rb) * R + row;
-          const long long at =
-              ((static_cast<long long>(it.b) * a.T + gr / a.G) * a.Hq + it.h * a.G + gr % a.G) * D + ch;
-          if (F32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) =
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-          } else {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
-                                 y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(static_cast<unsigned short*>(a.out) + at) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-          }
+          store_row(row, ch, acc, L);
         } else {
-          float* p = parts + (static_cast<long long>(slot) * R + row) * (D + 4);
+          // the pages' room serves the direct form (its pages have been read), the workspace the split one
+          float* p = mode == kDirect ? reinterpret_cast<float*>(ring) + row * (D + 4)
+                                     : parts + (static_cast<long long>(slot) * R + row) * (D + 4);
           *reinterpret_cast<float4*>(p + 4 + ch) = acc;
           if (ch == 0) {
             p[0] = M;
@@ -603,6 +649,29 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
         }
       }
       __syncthreads();
+      if (!complete && mode == kDirect) {
+        // ---- join the cluster's CTAs: each takes a share of the rows' channels ------------
+        cluster_sync();
+        for (int i = rank * 32 * kRWarps + tid; i < rows * D / 4; i += 32 * kRWarps * cluster) {
+          const int row = i / (D / 4), ch = 4 * (i % (D / 4));
+          const uint32_t p = su32(ring) + row * (D + 4) * 4;
+          float M = -INFINITY, L = 0.0f;
+          for (int r = 0; r < cluster; ++r) M = fmaxf(M, ld_cluster(map_cluster(p, r)));
+          const float ref = M == -INFINITY ? 0.0f : M;           // no key, or scores that are all NaN: sums of 0 or NaN
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int r = 0; r < cluster; ++r) {
+            const uint32_t q = map_cluster(p, r);
+            const float f = M == -INFINITY ? 1.0f : exp2_fast(ld_cluster(q) - ref);
+            L += f * ld_cluster(q + 4);
+            const float4 x = ld_cluster4(q + 16 + 4 * ch);
+            acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+          }
+          store_row(row, ch, acc, L);
+        }
+        cluster_sync();                                          // nobody leaves before its sums were read
+      }
+    } else if (mode == kDirect && rank > 0) {
+      // (an empty sequence: the cluster's first CTA writes)
     } else if (a.decode && !split && tid < 32) {                 // an empty sequence: zeros
       const int dr = min(R, a.G - it.rb * R);
       for (int i = lane; i < dr * D; i += 32) {
@@ -611,6 +680,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
         else static_cast<unsigned short*>(a.out)[at] = 0;
       }
     }
+    if (mode == kDirect) break;
     if (!split) {
       whole += gridDim.x;
       continue;
@@ -711,29 +781,60 @@ int row_blocks(int T, int G, int R) { return static_cast<int>((static_cast<long 
 
 
 
+// launch_pdl with thread-block clusters.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster,
+                           Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 template <int D, int NT, bool F32>
 cudaError_t launch_t(const Kv8Attn& a, cudaStream_t s) {
   constexpr int R = 8 * NT;
   const long long nrb = row_blocks(a.T, a.G, R);
   const long long entries = a.B * nrb, items = entries * a.H;
   if (items > 0x7FFFFFFFLL || items * R > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  const int grid = ctas_per_sm(D, R) * kv8_sm_count();
-  const bool split = entries <= kMaxEntries;           // else whole items: as many balance by themselves
   using Y = Lay<D>;
+  const int slots = ctas_per_sm(D, R) * kv8_sm_count();
+  // Pages that an item can have, and the CTAs per item that fill the card.  Up to kDirectPages pages a CTA the direct
+  // form saves the list, the partials and the second launch; beyond, equal spans use the card better.
+  const long long span = a.window ? static_cast<long long>(a.window) + a.T + a.sinks + 2 * kPage : a.max_seq_len;
+  const long long pages = (std::min<long long>(span, a.max_seq_len) + kPage - 1) / kPage;
+  int cluster = 8;
+  while (cluster > 1 && (items * cluster > slots || pages <= cluster / 2 * kRWarps)) cluster /= 2;
+  const bool direct = pages <= static_cast<long long>(kDirectPages) * cluster;
+  const Mode mode = direct ? kDirect : entries <= kMaxEntries ? kSplit : kWhole;
   const size_t fixed = 1024 + kRWarps * (Y::ST * Y::STAGE + sizeof(float) * R * D);
-  const size_t smem = fixed + (split ? sizeof(int) * entries : 0);
+  const size_t list = sizeof(Kv8Seq) + sizeof(int);
+  const size_t smem = fixed + (mode == kSplit ? list * (entries + 1) : 0);
   static std::atomic<unsigned long long> configured{0};
-  cudaError_t e = smem_attr_once(kv8_rows_kernel<D, NT, F32>,
-                                 static_cast<int>(fixed + sizeof(int) * kMaxEntries), configured);
+  cudaError_t e = smem_attr_once(kv8_rows_kernel<D, NT, F32>, static_cast<int>(fixed + list * (kMaxEntries + 1)), configured);
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
   const long long blocks = static_cast<long long>(a.num_pages) * a.H;
   if (!kv8_block_map(&mk, a.kc, blocks, D) || !kv8_block_map(&mv, a.vc, blocks, D)) return cudaErrorInvalidValue;
-  const long long ctas = split ? grid : (items < 0x7FFFFFFF ? items : 0x7FFFFFFF);
-  e = launch_pdl(kv8_rows_kernel<D, NT, F32>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kRWarps), smem, s, a, mk, mv,
-                 static_cast<int>(nrb), split ? 1 : 0);
-  if (e != cudaSuccess || !split) return e;
-  return launch_pdl(kv8_join_kernel<D, R, F32>, dim3(grid), dim3(512), 0, s, a, grid);
+  if (mode != kSplit) {
+    const unsigned ctas = static_cast<unsigned>(direct ? items * cluster : items);
+    return launch_cluster(kv8_rows_kernel<D, NT, F32>, dim3(ctas), dim3(32 * kRWarps), smem, s, direct ? cluster : 1, a, mk, mv,
+                          static_cast<int>(nrb), static_cast<int>(mode), cluster);
+  }
+  e = launch_pdl(kv8_rows_kernel<D, NT, F32>, dim3(slots), dim3(32 * kRWarps), smem, s, a, mk, mv, static_cast<int>(nrb),
+                 static_cast<int>(mode), 1);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv8_join_kernel<D, R, F32>, dim3(slots), dim3(512), 0, s, a, slots);
 }
 
 template <int D>

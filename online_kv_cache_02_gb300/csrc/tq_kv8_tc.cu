@@ -983,7 +983,7 @@ bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d)
 }
 
 bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale) {
-  return d == kTD && !f32 && static_cast<long long>(T) * G > 32 && softmax_scale != 0.0f &&
+  return d == kTD && !f32 && static_cast<long long>(T) * G > 16 && softmax_scale != 0.0f &&
          std::fabs(static_cast<double>(softmax_scale)) <= (1.0 + 1e-6) / std::sqrt(static_cast<double>(kTD));
 }
 

@@ -7,7 +7,7 @@ Attention's bounds, per output element, with A = sum_j p_j |v_j| and the seen ke
   - a logit's error: fp32 sums of exact products over d channels in the tensor core, at most d/16 + 1 steps
     each off by 2^-23 of the running size, times scale * sum |q k|; its scaling and the exponential: 2^-21 of
     its own size and 2^-21 more; a logit off by x moves the weights' share by at most 2 x A;
-  - bf16, d = 128, more than 32 rows per KV head: the query as two e4m3 parts, off by at most 2^-17 of the row's
+  - bf16, d = 128, more than 16 rows per KV head: the query as two e4m3 parts, off by at most 2^-17 of the row's
     largest value per channel: scale * 2^-17 * max |q| * sum |k| on a logit;
   - the sums over keys: n/16 steps in the value product and the joins, each off by 2^-23 of A.
 """
@@ -371,7 +371,7 @@ def _check(c, got, q, dtype, causal, starts, lens=None, window=0, sinks=0, scale
                                                         c.table[b], p, window, sinks, scale,
                                                         () if hidden is None else hidden.get(b, ()))
             y = got[b, t] if causal else got[b]
-            two_parts = dtype == "bf16" and d == 128 and causal and q.shape[1] * (q.shape[2] // c.h) > 32
+            two_parts = dtype == "bf16" and d == 128 and causal and q.shape[1] * (q.shape[2] // c.h) > 16
             tol = _bound(dtype, want, mag, dots, keys, d, scale,
                          2.0 ** -17 * np.abs(x).max(axis=-1) * ksum if two_parts else 0.0)
             err = np.abs(y - want)
