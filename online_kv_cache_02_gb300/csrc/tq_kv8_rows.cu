@@ -45,7 +45,11 @@ using tcx::su32;
 constexpr int kRWarps = 4;
 constexpr int kMinSpan = 4;               // pages a CTA takes at least (one per warp)
 constexpr int kMaxEntries = 2048;         // (sequence, row block) pairs that the split form lists
-constexpr int kDirectPages = 32;          // pages per CTA up to which the direct form is taken
+// Pages per CTA up to which the direct form is taken (measured against the split form, bf16, d = 128, 32 / 8 heads):
+//   a CTA per item, 64: 200 sequences of 100 .. 1000 tokens 57 us (split 86), 64 of 1024 .. 8192 125 us (split 64);
+//   clusters that leave two thirds of the card free, 48: 1 of 6000 16.5 us (18.7), 2 of 3000 12.7 us (16.9);
+//   clusters that fill it, 32: 16 of 1000 15.4 us (16.5), 7 of 6000 36 us (27).
+constexpr int kDirectOne = 64, kDirectFew = 48, kDirectMany = 32;
 enum Mode { kWhole = 0, kSplit = 1, kDirect = 2 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -103,7 +107,7 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t p) {
 }
 
 // CTAs per SM, as shared memory (the rings, the joins and a list of usual length) and registers allow.
-__host__ __device__ constexpr int ctas_per_sm(int d, int R) { return d <= 128 && R == 8 ? 3 : 2; }
+__host__ __device__ constexpr int ctas_per_sm(int d, int R) { return R == 16 || d > 128 ? 2 : d == 128 ? 3 : 4; }
 
 // Channels: a lane's K words (four channels each) and V words, in panels of 128.
 template <int D> struct Lay {
@@ -114,7 +118,7 @@ template <int D> struct Lay {
   static constexpr int KP = KW / PAN, VP = VW / PAN;   // words per panel
   // a warp's ring of pages: a K and a V block each, in panels of 16 rows x 128 bytes (64 at d = 64), swizzled by TMA
   static constexpr int ROW = D >= 128 ? 128 : 64, PANEL = kPage * ROW, BLOCK = kPage * D, STAGE = 2 * BLOCK;
-  static constexpr int ST = D == 64 ? 6 : D == 128 ? 3 : 2;
+  static constexpr int ST = D == 64 ? 4 : D == 128 ? 3 : 2;
   __device__ static __forceinline__ uint32_t at(int row, int chunk) {      // 16-byte piece `chunk` of a panel's row
     return static_cast<uint32_t>(row * ROW + ((chunk ^ (ROW == 128 ? row & 7 : (row >> 1) & 3)) << 4));
   }
@@ -809,13 +813,13 @@ cudaError_t launch_t(const Kv8Attn& a, cudaStream_t s) {
   if (items > 0x7FFFFFFFLL || items * R > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
   using Y = Lay<D>;
   const int slots = ctas_per_sm(D, R) * kv8_sm_count();
-  // Pages that an item can have, and the CTAs per item that fill the card.  Up to kDirectPages pages a CTA the direct
-  // form saves the list, the partials and the second launch; beyond, equal spans use the card better.
+  // Pages that an item can have, and the CTAs per item that fill the card.
   const long long span = a.window ? static_cast<long long>(a.window) + a.T + a.sinks + 2 * kPage : a.max_seq_len;
   const long long pages = (std::min<long long>(span, a.max_seq_len) + kPage - 1) / kPage;
   int cluster = 8;
   while (cluster > 1 && (items * cluster > slots || pages <= cluster / 2 * kRWarps)) cluster /= 2;
-  const bool direct = pages <= static_cast<long long>(kDirectPages) * cluster;
+  const int most = cluster == 1 ? kDirectOne : 3 * items * cluster <= slots ? kDirectFew : kDirectMany;
+  const bool direct = pages <= static_cast<long long>(most) * cluster;
   const Mode mode = direct ? kDirect : entries <= kMaxEntries ? kSplit : kWhole;
   const size_t fixed = 1024 + kRWarps * (Y::ST * Y::STAGE + sizeof(float) * R * D);
   const size_t list = sizeof(Kv8Seq) + sizeof(int);

@@ -445,6 +445,21 @@ def test_decode_many_short_sequences():
     rng = np.random.default_rng(25)
     _decode_case(rng, "bf16", 128, 8, 16, [int(x) for x in rng.integers(0, 40, 420)])
     _decode_case(rng, "bf16", 64, 1, 2, [int(x) for x in rng.integers(0, 20, 2100)])
+    # more sequences than a list holds, with one long context among them
+    lens = [int(x) for x in rng.integers(0, 6, 2060)]
+    lens[1234] = 2100
+    b = len(lens)
+    c = Cache(rng, b + 140, 1, 64, 1, 140, nan=False)
+    c.table = np.zeros((b, 140), np.int32)
+    c.table[:, 0] = np.arange(b)
+    c.table[1234] = b + np.arange(140)
+    c.maxp = 140
+    for i, n in enumerate(lens):
+        if n:
+            c.clean(rng, i, range(n))
+    c.to_device()
+    q = values(rng, "bf16", b, 2, 64)
+    _check(c, _attend(c, q, "bf16", False, lens), q, "bf16", False, lens)
 
 
 def test_decode_query_that_is_not_finite_spoils_only_its_row():
