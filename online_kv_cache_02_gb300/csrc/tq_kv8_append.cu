@@ -13,10 +13,13 @@
 //
 // A CTA takes one page of one sequence and a group of its heads: the page's
 // cosines and sines go to shared memory once, with every pair's axis resolved,
-// and each warp takes whole (page, head) blocks, all 16 tokens in registers, so
-// that the maximum and the codes come from one read of the input.
+// and each warp takes whole (page, head) blocks: its 16 tokens by asynchronous
+// copies into shared memory, the next block's while this one is worked on, then
+// one pass for the maximum and one for the codes.  (Held in registers instead, a
+// block left room for eight warps an SM.)
 
 #include "tq_kv8.h"
+#include "tq_tc.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -55,44 +58,17 @@ __device__ __forceinline__ int block_exp64(double amax) {
   return e < kE8Min ? kE8Min : e > kE8Max ? kE8Max : e;
 }
 
-// Sixteen channels of one token: chunks A and B of eight, as they lie in memory.
+// Sixteen channels of one token: chunks A and B of eight.
 template <bool F32>
 struct Chunk2 {
   uint4 w[F32 ? 4 : 2];
-  __device__ __forceinline__ void load(const void* base, long long elem, int ca, int cb, bool aligned) {
-    if (F32) {
-      const float* p = static_cast<const float*>(base) + elem;
-      if (aligned) {
-        w[0] = *reinterpret_cast<const uint4*>(p + 8 * ca);
-        w[1] = *reinterpret_cast<const uint4*>(p + 8 * ca + 4);
-        w[2 * (F32 ? 1 : 0)] = *reinterpret_cast<const uint4*>(p + 8 * cb);
-        w[F32 ? 3 : 0] = *reinterpret_cast<const uint4*>(p + 8 * cb + 4);
-      } else {
-        uint32_t* o = reinterpret_cast<uint32_t*>(w);
+  __device__ __forceinline__ void load(uint32_t row, int ca, int cb) {   // from the token's row in shared memory
+    constexpr int kB = F32 ? 32 : 16;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i] = __float_as_uint(p[8 * ca + i]);
-          o[F32 ? 8 + i : 0] = __float_as_uint(p[8 * cb + i]);
-        }
-      }
-    } else {
-      const unsigned short* p = static_cast<const unsigned short*>(base) + elem;
-      if (aligned) {
-        w[0] = *reinterpret_cast<const uint4*>(p + 8 * ca);
-        w[1] = *reinterpret_cast<const uint4*>(p + 8 * cb);
-      } else {
-        uint32_t* o = reinterpret_cast<uint32_t*>(w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o[i] = p[8 * ca + 2 * i] | (static_cast<uint32_t>(p[8 * ca + 2 * i + 1]) << 16);
-          o[4 + i] = p[8 * cb + 2 * i] | (static_cast<uint32_t>(p[8 * cb + 2 * i + 1]) << 16);
-        }
-      }
+    for (int i = 0; i < kB / 16; ++i) {
+      w[i] = tcx::lds128(row + kB * ca + 16 * i);
+      w[kB / 16 + i] = tcx::lds128(row + kB * cb + 16 * i);
     }
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < (F32 ? 4 : 2); ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
   }
   // channel i (0 .. 15: chunk A, then chunk B)
   __device__ __forceinline__ float get(int i) const {
@@ -125,14 +101,22 @@ __device__ __forceinline__ void tame(float& r, float& b) {
   }
 }
 
+// Bytes of a block's input, and blocks in flight per warp.
+template <int D, bool F32>
+struct Stage {
+  static constexpr int ROW = D * (F32 ? 4 : 2), BYTES = kPage * ROW, N = BYTES <= 4096 ? 2 : 1;
+};
+
 template <int D, bool F32, bool INTER>
-__global__ void __launch_bounds__(32 * kAWarps) kv8_append_kernel(const __grid_constant__ Kv8Append a, int tasks_per_cta) {
+__global__ void __launch_bounds__(32 * kAWarps, 2) kv8_append_kernel(const __grid_constant__ Kv8Append a, int tasks_per_cta) {
+  using S = Stage<D, F32>;
   constexpr int kLanes = D / 16;                 // lanes per token, sixteen channels each
   constexpr int kTok = 32 / kLanes;              // tokens per step of a warp
-  constexpr int kSteps = kPage / kTok;
-  extern __shared__ float cs_sm[];               // [16][rot]
+  extern __shared__ __align__(16) unsigned char sm_raw[];
+  float* cs_sm = reinterpret_cast<float*>(sm_raw + kAWarps * S::N * S::BYTES);   // [16][rot]
   __shared__ int tok_ok[kPage];                  // the token is there and its position in the table
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t stages = tcx::su32(sm_raw) + warp * S::N * S::BYTES;
   const int npg = (a.n_new + 2 * kPage - 2) / kPage;
   const int b = blockIdx.x / npg, ip = blockIdx.x % npg;
   pdl_wait();
@@ -148,6 +132,31 @@ __global__ void __launch_bounds__(32 * kAWarps) kv8_append_kernel(const __grid_c
   const int nt = min(kPage - slot0, n - t0);               // tokens of this page
   if (nt <= 0) return;
   const int half = a.rot / 2;
+  const int nk = a.k ? a.H : 0, nv = a.v ? a.H : 0, nq = a.q ? a.Hq : 0;
+  const int task0 = blockIdx.y * tasks_per_cta, task1 = min(nk + nv + nq, task0 + tasks_per_cta);
+
+  // a block's tokens into the warp's stage
+  auto fetch = [&](int task, uint32_t dst) {
+    const int kind = task < nk ? 0 : task < nk + nv ? 1 : 2;
+    const int h = kind == 0 ? task : kind == 1 ? task - nk : task - nk - nv;
+    const long long stride = (kind == 0 ? a.k_stride : kind == 1 ? a.v_stride : a.q_stride) * (F32 ? 4 : 2);
+    const char* src = static_cast<const char*>(kind == 0 ? a.k : kind == 1 ? a.v : a.q) +
+                      (static_cast<long long>(b) * a.n_new + t0) * stride + static_cast<long long>(h) * S::ROW;
+    if (((reinterpret_cast<uintptr_t>(src) | static_cast<uintptr_t>(stride)) & 15) == 0) {
+      for (int i = lane; i < nt * (S::ROW / 16); i += 32)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * i),
+                     "l"(src + (i / (S::ROW / 16)) * stride + 16 * (i % (S::ROW / 16))));
+    } else {                                     // rows off the 16-byte grid, element by element
+      for (int i = lane; i < nt * D; i += 32) {
+        const char* p = src + (i / D) * stride + (i % D) * (F32 ? 4 : 2);
+        if (F32) asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 4 * i), "r"(*reinterpret_cast<const uint32_t*>(p)) : "memory");
+        else asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + 2 * i), "h"(*reinterpret_cast<const unsigned short*>(p)) : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (task0 + warp < task1) fetch(task0 + warp, stages);
+
   // ---- the page's cosines and sines, one row per token -------------------------------
   if (tid < kPage) tok_ok[tid] = 1;
   __syncthreads();
@@ -181,64 +190,63 @@ __global__ void __launch_bounds__(32 * kAWarps) kv8_append_kernel(const __grid_c
   const int cb = turns ? li + rch : ca + 1;
   // the lane's pairs: eight in a row, or four of chunk A and four of chunk B
   const int pa = INTER ? 4 * ca : 8 * li, pb = INTER ? 4 * cb : 8 * li + 4;
-
-  const int nk = a.k ? a.H : 0, nv = a.v ? a.H : 0, nq = a.q ? a.Hq : 0;
-  const int task0 = blockIdx.y * tasks_per_cta, task1 = min(nk + nv + nq, task0 + tasks_per_cta);
   const long long page_pos = (static_cast<long long>(start) + t0) / kPage;
+  const int steps = (nt + kTok - 1) / kTok;
+
+  int buf = 0;
   for (int task = task0 + warp; task < task1; task += kAWarps) {
     const int kind = task < nk ? 0 : task < nk + nv ? 1 : 2;
     const int h = kind == 0 ? task : kind == 1 ? task - nk : task - nk - nv;
-    const void* src = kind == 0 ? a.k : kind == 1 ? a.v : a.q;
-    const long long stride = kind == 0 ? a.k_stride : kind == 1 ? a.v_stride : a.q_stride;
     const bool rot = turns && kind != 1;
-    const bool aligned = ((reinterpret_cast<uintptr_t>(src) | static_cast<uintptr_t>(stride * (F32 ? 4 : 2))) & 15) == 0;
-    Chunk2<F32> x[kSteps];
-    bool have[kSteps];
-#pragma unroll
-    for (int st = 0; st < kSteps; ++st) {
-      const int t = st * kTok + sub;
-      have[st] = t < nt && tok_ok[t];
-      if (have[st])
-        x[st].load(src, (static_cast<long long>(b) * a.n_new + t0 + t) * stride + static_cast<long long>(h) * D, ca, cb,
-                   aligned);
-      else
-        x[st].zero();
+    const uint32_t in = stages + buf * S::BYTES;
+    if (S::N == 2 && task + kAWarps < task1) {
+      __syncwarp();                              // the stage's last block has been read
+      fetch(task + kAWarps, stages + (buf ^ 1) * S::BYTES);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
-    // the eight pairs of a step's channels `y`, turned: f(first, second channel of the sixteen, Turned, cos, sin).
+    __syncwarp();
+    // the eight pairs of a step's token, turned: f(first, second channel of the sixteen, Turned, x1, x2, cos, sin).
     // INTER is a template argument so that register indices stay static.
-    auto turned = [&](int st, bool there, const Chunk2<F32>& y, auto&& f) {
-      float c[8], s[8];
-      if (rot && there) {
-        const float* row = cs_sm + (st * kTok + sub) * a.rot;
+    auto pairs = [&](int t, auto&& f) {
+      Chunk2<F32> x;
+      x.load(in + t * S::ROW, ca, cb);
+      if (rot) {
+        float c[8], s[8];
+        const float* row = cs_sm + t * a.rot;
         *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(row + pa);
         *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(row + pb);
         *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(row + half + pa);
         *reinterpret_cast<float4*>(s + 4) = *reinterpret_cast<const float4*>(row + half + pb);
-      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i1 = INTER ? 2 * j : j, i2 = INTER ? 2 * j + 1 : 8 + j;
-        const float x1 = y.get(i1), x2 = y.get(i2);
-        if (rot && there) f(i1, i2, turn(x1, x2, c[j], s[j]), c[j], s[j]);
-        else f(i1, i2, Turned{x1, x2, 0.0f, 0.0f}, 1.0f, 0.0f);
+        for (int j = 0; j < 8; ++j) {
+          const int i1 = INTER ? 2 * j : j, i2 = INTER ? 2 * j + 1 : 8 + j;
+          const float x1 = x.get(i1), x2 = x.get(i2);
+          f(i1, i2, turn(x1, x2, c[j], s[j]), x1, x2, c[j], s[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i1 = INTER ? 2 * j : j, i2 = INTER ? 2 * j + 1 : 8 + j;
+          const float x1 = x.get(i1), x2 = x.get(i2);
+          f(i1, i2, Turned{x1, x2, 0.0f, 0.0f}, x1, x2, 1.0f, 0.0f);
+        }
       }
     };
-    auto pairs = [&](int st, auto&& f) { turned(st, have[st], x[st], f); };
-    auto token_elem = [&](int st) {
-      return (static_cast<long long>(b) * a.n_new + t0 + st * kTok + sub) * stride + static_cast<long long>(h) * D;
-    };
+    auto there = [&](int t) { return t < nt && tok_ok[t]; };
 
     if (kind == 2) {                             // queries: turned and rounded once
-#pragma unroll
-      for (int st = 0; st < kSteps; ++st) {
-        if (!have[st]) continue;
+#pragma unroll 1
+      for (int st = 0; st < steps; ++st) {
+        const int t = st * kTok + sub;
+        if (!there(t)) continue;
         float y[16];
-        pairs(st, [&](int i1, int i2, const Turned& t, float, float) {
-          y[i1] = t.r1;
-          y[i2] = t.r2;
+        pairs(t, [&](int i1, int i2, const Turned& r, float, float, float, float) {
+          y[i1] = r.r1;
+          y[i2] = r.r2;
         });
-        const long long at =
-            ((static_cast<long long>(b) * a.n_new + t0 + st * kTok + sub) * a.Hq + h) * D;
+        const long long at = ((static_cast<long long>(b) * a.n_new + t0 + t) * a.Hq + h) * D;
         if (F32) {
           float* o = static_cast<float*>(a.q_out) + at;
 #pragma unroll
@@ -259,131 +267,145 @@ __global__ void __launch_bounds__(32 * kAWarps) kv8_append_kernel(const __grid_c
           *reinterpret_cast<uint4*>(o + 8 * cb) = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
-      continue;
-    }
-
-    // ---- a block of keys or values ----------------------------------------------------
-    int pid = -1;
-    if (page_pos < a.maxp) {
-      pid = a.bt[static_cast<long long>(b) * a.maxp + page_pos];
-      if (pid < 0 || pid >= a.num_pages) {
-        if (lane == 0) atomicOr(a.err, kErrPage);
-        pid = -1;
+    } else {
+      // ---- a block of keys or values --------------------------------------------------
+      int pid = -1;
+      if (page_pos < a.maxp) {
+        pid = a.bt[static_cast<long long>(b) * a.maxp + page_pos];
+        if (pid < 0 || pid >= a.num_pages) {
+          if (lane == 0) atomicOr(a.err, kErrPage);
+          pid = -1;
+        }
+      } else if (lane == 0) {
+        atomicOr(a.err, kErrBlock);
       }
-    } else if (lane == 0) {
-      atomicOr(a.err, kErrBlock);
-    }
-    if (pid < 0) continue;                       // warp-uniform
-    const long long blk = static_cast<long long>(pid) * a.H + h;
-    uint8_t* codes = (kind == 0 ? a.kc : a.vc) + blk * (kPage * D);
-    float* scale = (kind == 0 ? a.ks : a.vs) + blk;
+      if (pid >= 0) {                            // warp-uniform
+        const long long blk = static_cast<long long>(pid) * a.H + h;
+        uint8_t* codes = (kind == 0 ? a.kc : a.vc) + blk * (kPage * D);
+        float* scale = (kind == 0 ? a.ks : a.vs) + blk;
 
-    // largest value of the block's new tokens, and the largest bound on an error
-    float amax = 0.0f, bmax = 0.0f;
-    bool odd = false;                            // a value that is not finite
-#pragma unroll
-    for (int st = 0; st < kSteps; ++st)
-      pairs(st, [&](int, int, const Turned& t, float, float) {
-        const float m1 = fabsf(t.r1), m2 = fabsf(t.r2);
-        const bool f1 = finite32(m1), f2 = finite32(m2);
-        odd |= !f1 || !f2;
-        amax = fmaxf(amax, fmaxf(f1 ? m1 : 0.0f, f2 ? m2 : 0.0f));
-        bmax = fmaxf(bmax, fmaxf(f1 ? t.b1 : 0.0f, f2 ? t.b2 : 0.0f));
-      });
-    // non-negative floats order as their bits
-    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-    bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
-    if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(a.err, kErrNonFinite);
-    int e = block_exp(amax);
-    if (bmax > 0.0f && block_exp(fmaxf(amax - bmax, 0.0f)) != block_exp(fminf(amax + bmax, 3.4028234e38f))) {
-      double m = 0.0;                            // next to a border: the maximum in fp64, from the input again
+        // largest value of the block's new tokens, and the largest bound on an error
+        float amax = 0.0f, bmax = 0.0f;
+        bool odd = false;                        // a value that is not finite
 #pragma unroll 1
-      for (int st = 0; st < kSteps; ++st) {
-        const int t = st * kTok + sub;
-        if (!(t < nt && tok_ok[t])) continue;
-        Chunk2<F32> y;
-        y.load(src, token_elem(st), ca, cb, aligned);
-        turned(st, true, y, [&](int i1, int i2, const Turned& t, float c, float s) {
-          const double x1 = y.get(i1), x2 = y.get(i2);
-          if (finite32(t.r1)) m = fmax(m, fabs(x1 * c - x2 * s));
-          if (finite32(t.r2)) m = fmax(m, fabs(x2 * c + x1 * s));
-        });
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-      e = block_exp64(m);
-    }
-    if (slot0 > 0) {                             // earlier tokens keep at least the block's scale
-      const uint32_t sb = __float_as_uint(*scale);
-      int e_old = static_cast<int>(sb >> 23) - 127;
-      if ((sb & 0x7FFFFFu) || e_old < kE8Min || e_old > kE8Max) {
-        if (lane == 0) atomicOr(a.err, kErrScale);
-        e_old = kE8Min;
-      }
-      if (e > e_old) {                           // their codes move down by an exact factor, rounded once more
-        // below 2^-126 every code rounds to zero all the same
-        const float f = pow2f(e_old - e < -126 ? -126 : e_old - e);
-        for (int i = lane; i < slot0 * D / 4; i += 32) {
-          uint32_t w = reinterpret_cast<const uint32_t*>(codes)[i];
-          float v0, v1, v2, v3;
-          e4m3x2_to_float(w & 0xFFFFu, v0, v1);
-          e4m3x2_to_float(w >> 16, v2, v3);
-          reinterpret_cast<uint32_t*>(codes)[i] = cvt_e4m3x2(v1 * f, v0 * f) | (cvt_e4m3x2(v3 * f, v2 * f) << 16);
+        for (int st = 0; st < steps; ++st) {
+          const int t = st * kTok + sub;
+          if (!there(t)) continue;
+          pairs(t, [&](int, int, const Turned& r, float, float, float, float) {
+            const float m1 = fabsf(r.r1), m2 = fabsf(r.r2);
+            const bool f1 = finite32(m1), f2 = finite32(m2);
+            odd |= !f1 || !f2;
+            amax = fmaxf(amax, fmaxf(f1 ? m1 : 0.0f, f2 ? m2 : 0.0f));
+            bmax = fmaxf(bmax, fmaxf(f1 ? r.b1 : 0.0f, f2 ? r.b2 : 0.0f));
+          });
         }
-      } else {
-        e = e_old;
-      }
-    }
-    if (lane == 0) *scale = pow2f(e);
-    const float inv = pow2f(-e);
-#pragma unroll
-    for (int st = 0; st < kSteps; ++st) {
-      if (!have[st]) continue;
-      // codes of value +- bound agree: that is the code
-      uint32_t lo[8], hi[8];                     // [pair]: code of the first channel | second << 8
-      uint32_t open = 0u;
-      pairs(st, [&](int i1, int i2, const Turned& t, float, float) {
-        float r1 = t.r1, r2 = t.r2, b1 = t.b1, b2 = t.b2;
-        tame(r1, b1);
-        tame(r2, b2);
-        const int j = INTER ? i1 / 2 : i1;
-        lo[j] = cvt_e4m3x2((r2 - b2) * inv, (r1 - b1) * inv);
-        hi[j] = cvt_e4m3x2((r2 + b2) * inv, (r1 + b1) * inv);
-        // (a zero's two codes may differ too: exact values have no bound)
-        if (lo[j] != hi[j] && (b1 > 0.0f || b2 > 0.0f)) open |= 1u << j;
-      });
-      if (open) {
-        pairs(st, [&](int i1, int i2, const Turned& t, float c, float s) {
-          const int j = INTER ? i1 / 2 : i1;
-          if ((open >> j) & 1u) {
-            const double x1 = x[st].get(i1), x2 = x[st].get(i2);
-            // the nearest e4m3 of the fp64 value: rounded to fp32 towards odd, which keeps ties apart
-            auto code = [&](double y) {
-              float f = __double2float_rz(y * inv);
-              if (static_cast<double>(f) != y * inv) f = __uint_as_float(__float_as_uint(f) | 1u);
-              return cvt_e4m3x2(0.0f, f) & 0xFFu;
-            };
-            // an infinite half of the pair keeps its code
-            if (finite32(t.r1)) lo[j] = (lo[j] & 0xFF00u) | code(x1 * c - x2 * s);
-            if (finite32(t.r2)) lo[j] = (lo[j] & 0x00FFu) | (code(x2 * c + x1 * s) << 8);
+        // non-negative floats order as their bits
+        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+        bmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(bmax)));
+        if (__any_sync(0xffffffffu, odd) && lane == 0) atomicOr(a.err, kErrNonFinite);
+        int e = block_exp(amax);
+        if (bmax > 0.0f && block_exp(fmaxf(amax - bmax, 0.0f)) != block_exp(fminf(amax + bmax, 3.4028234e38f))) {
+          double m = 0.0;                        // next to a border: the maximum in fp64
+#pragma unroll 1
+          for (int st = 0; st < steps; ++st) {
+            const int t = st * kTok + sub;
+            if (!there(t)) continue;
+            pairs(t, [&](int, int, const Turned& r, double x1, double x2, double c, double s) {
+              if (finite32(r.r1)) m = fmax(m, fabs(x1 * c - x2 * s));
+              if (finite32(r.r2)) m = fmax(m, fabs(x2 * c + x1 * s));
+            });
           }
-        });
-      }
-      uint32_t w[4];                             // the sixteen codes in channel order
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (INTER) {
-          w[i] = lo[2 * i] | (lo[2 * i + 1] << 16);
-        } else {
-          const int j = 4 * (i & 1), sh = i < 2 ? 0 : 8;
-          w[i] = ((lo[j] >> sh) & 0xFFu) | (((lo[j + 1] >> sh) & 0xFFu) << 8) | (((lo[j + 2] >> sh) & 0xFFu) << 16) |
-                 (((lo[j + 3] >> sh) & 0xFFu) << 24);
+          for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+          e = block_exp64(m);
+        }
+        if (slot0 > 0) {                         // earlier tokens keep at least the block's scale
+          const uint32_t sb = __float_as_uint(*scale);
+          int e_old = static_cast<int>(sb >> 23) - 127;
+          if ((sb & 0x7FFFFFu) || e_old < kE8Min || e_old > kE8Max) {
+            if (lane == 0) atomicOr(a.err, kErrScale);
+            e_old = kE8Min;
+          }
+          if (e > e_old) {                       // their codes move down by an exact factor, rounded once more
+            // below 2^-126 every code rounds to zero all the same
+            const float f = pow2f(e_old - e < -126 ? -126 : e_old - e);
+            for (int i = lane; i < slot0 * D / 4; i += 32) {
+              const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[i];
+              float v0, v1, v2, v3;
+              e4m3x2_to_float(w & 0xFFFFu, v0, v1);
+              e4m3x2_to_float(w >> 16, v2, v3);
+              reinterpret_cast<uint32_t*>(codes)[i] = cvt_e4m3x2(v1 * f, v0 * f) | (cvt_e4m3x2(v3 * f, v2 * f) << 16);
+            }
+          } else {
+            e = e_old;
+          }
+          __syncwarp();                          // every lane has read the scale
+        }
+        if (lane == 0) *scale = pow2f(e);
+        const float inv = pow2f(-e);
+#pragma unroll 1
+        for (int st = 0; st < steps; ++st) {
+          const int t = st * kTok + sub;
+          if (!there(t)) continue;
+          uint32_t lo[8];                        // [pair]: code of the first channel | second << 8
+          uint32_t open = 0u;
+          if (kind == 0) {
+            // codes of value +- bound agree: that is the code
+            pairs(t, [&](int i1, int, const Turned& r, float, float, float, float) {
+              float r1 = r.r1, r2 = r.r2, b1 = r.b1, b2 = r.b2;
+              tame(r1, b1);
+              tame(r2, b2);
+              const int j = INTER ? i1 / 2 : i1;
+              lo[j] = cvt_e4m3x2((r2 - b2) * inv, (r1 - b1) * inv);
+              // (a zero's two codes may differ too: exact values have no bound)
+              if (lo[j] != cvt_e4m3x2((r2 + b2) * inv, (r1 + b1) * inv) && (b1 > 0.0f || b2 > 0.0f)) open |= 1u << j;
+            });
+            if (open) {
+              pairs(t, [&](int i1, int, const Turned& r, double x1, double x2, double c, double s) {
+                const int j = INTER ? i1 / 2 : i1;
+                if ((open >> j) & 1u) {
+                  // the nearest e4m3 of the fp64 value: rounded to fp32 towards odd, which keeps ties apart
+                  auto code = [&](double y) {
+                    float f = __double2float_rz(y * inv);
+                    if (static_cast<double>(f) != y * inv) f = __uint_as_float(__float_as_uint(f) | 1u);
+                    return cvt_e4m3x2(0.0f, f) & 0xFFu;
+                  };
+                  // an infinite half of the pair keeps its code
+                  if (finite32(r.r1)) lo[j] = (lo[j] & 0xFF00u) | code(x1 * c - x2 * s);
+                  if (finite32(r.r2)) lo[j] = (lo[j] & 0x00FFu) | (code(x2 * c + x1 * s) << 8);
+                }
+              });
+            }
+          } else {                               // values as they are
+            pairs(t, [&](int i1, int, const Turned& r, float, float, float, float) {
+              float r1 = r.r1, r2 = r.r2, b1 = 0.0f;
+              tame(r1, b1);
+              tame(r2, b1);
+              lo[INTER ? i1 / 2 : i1] = cvt_e4m3x2(r2 * inv, r1 * inv);
+            });
+          }
+          uint32_t w[4];                         // the sixteen codes in channel order
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (INTER) {
+              w[i] = lo[2 * i] | (lo[2 * i + 1] << 16);
+            } else {                             // bytes 0 of four pairs, then their bytes 1
+              const int j = 4 * (i & 1);
+              const uint32_t sel = i < 2 ? 0x0040u : 0x0051u;
+              w[i] = __byte_perm(__byte_perm(lo[j], lo[j + 1], sel), __byte_perm(lo[j + 2], lo[j + 3], sel), 0x5410u);
+            }
+          }
+          uint8_t* row = codes + (slot0 + t) * D;
+          *reinterpret_cast<uint2*>(row + 8 * ca) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2*>(row + 8 * cb) = make_uint2(w[2], w[3]);
         }
       }
-      uint8_t* row = codes + (slot0 + st * kTok + sub) * D;
-      *reinterpret_cast<uint2*>(row + 8 * ca) = make_uint2(w[0], w[1]);
-      *reinterpret_cast<uint2*>(row + 8 * cb) = make_uint2(w[2], w[3]);
     }
+    if (S::N == 1 && task + kAWarps < task1) {
+      __syncwarp();
+      fetch(task + kAWarps, stages);
+    }
+    buf ^= S::N - 1;
   }
 }
 
@@ -398,7 +420,13 @@ cudaError_t launch_t(const Kv8Append& a, cudaStream_t s) {
   while (per < 4 && pages * ((groups + per - 1) / per) > 4096) per *= 2;
   const int tpc = per * kAWarps;
   if (pages > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  const size_t smem = sizeof(float) * kPage * static_cast<size_t>(a.rot);
+  using S = Stage<D, F32>;
+  constexpr int kStages = kAWarps * S::N * S::BYTES;
+  const size_t smem = kStages + sizeof(float) * kPage * static_cast<size_t>(a.rot);
+  static std::atomic<unsigned long long> configured{0};
+  const cudaError_t e = smem_attr_once(kv8_append_kernel<D, F32, INTER>, kStages + static_cast<int>(sizeof(float)) * kPage * D,
+                                       configured);
+  if (e != cudaSuccess) return e;
   return launch_pdl(kv8_append_kernel<D, F32, INTER>, dim3(static_cast<unsigned>(pages), (tasks + tpc - 1) / tpc),
                     dim3(32 * kAWarps), smem, s, a, tpc);
 }
