@@ -108,7 +108,7 @@ struct Stage {
 };
 
 template <int D, bool F32, bool INTER>
-__global__ void __launch_bounds__(32 * kAWarps, 2) kv8_append_kernel(const __grid_constant__ Kv8Append a, int tasks_per_cta) {
+__global__ void __launch_bounds__(32 * kAWarps, D == 256 ? (F32 ? 1 : 2) : 3) kv8_append_kernel(const __grid_constant__ Kv8Append a, int tasks_per_cta) {
   using S = Stage<D, F32>;
   constexpr int kLanes = D / 16;                 // lanes per token, sixteen channels each
   constexpr int kTok = 32 / kLanes;              // tokens per step of a warp
@@ -414,10 +414,10 @@ cudaError_t launch_t(const Kv8Append& a, cudaStream_t s) {
   const int npg = (a.n_new + 2 * kPage - 2) / kPage;
   const long long pages = static_cast<long long>(a.batch) * npg;
   const int tasks = (a.k ? a.H : 0) + (a.v ? a.H : 0) + (a.q ? a.Hq : 0);
-  // one block per warp while that fills the card; more per CTA (fewer copies of the cosines) beyond
+  // a block per warp while one wave of CTAs holds them; more per warp beyond, whose copies overlap the work
   int groups = (tasks + kAWarps - 1) / kAWarps;
   int per = 1;
-  while (per < 4 && pages * ((groups + per - 1) / per) > 4096) per *= 2;
+  while (per < 8 && pages * ((groups + per - 1) / per) > 3LL * kv8_sm_count()) per *= 2;
   const int tpc = per * kAWarps;
   if (pages > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
   using S = Stage<D, F32>;
