@@ -17,8 +17,8 @@
 // at an item's end.  How the pages come to the CTAs:
 //   direct  few pages per item: an item per cluster of 1 to 8 CTAs, joined through
 //           distributed shared memory, one launch;
-//   split   all pages of all items form one list, cut into equal spans, one per CTA
-//           (whatever the sequences' lengths); items that cross spans leave partials
+//   split   all pages of all items form one list, cut into spans of equal cost, one
+//           per CTA (whatever the sequences' lengths); items that cross spans leave partials
 //           for a second kernel;
 //   whole   too many sequences to list: items in turn.
 
@@ -43,8 +43,12 @@ using tcx::lds64;
 using tcx::su32;
 
 constexpr int kRWarps = 4;
-constexpr int kMinSpan = 4;               // pages a CTA takes at least (one per warp)
-constexpr int kMaxEntries = 2048;         // (sequence, row block) pairs that the split form lists
+// An item's start and end (its queries, the join) in pages of a CTA's time: 3.3 us against 0.23 us a page.  Spans are
+// equal in pages and items weighed so: short rows of a prompt would otherwise pile up in the first CTAs (2,048 tokens,
+// d = 64: 0.91 ms, 0.28 so).
+constexpr int kItemCost = 12;
+constexpr int kMinSpan = 4 + kItemCost;   // a CTA's share at least (a page per warp)
+constexpr int kMaxEntries = 1024;         // (sequence, row block) pairs that the split form lists
 // Pages per CTA up to which the direct form is taken (measured against the split form, bf16, d = 128, 32 / 8 heads):
 //   a CTA per item, 64: 200 sequences of 100 .. 1000 tokens 57 us (split 86), 64 of 1024 .. 8192 125 us (split 64);
 //   clusters that leave two thirds of the card free, 48: 1 of 6000 16.5 us (18.7), 2 of 3000 12.7 us (16.9);
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   float* sm = reinterpret_cast<float*>(ring + kRWarps * Y::ST * Y::STAGE);
   __shared__ uint64_t s_bar[kRWarps][Y::ST];
   __shared__ float s_ml[kRWarps][R][2];
-  __shared__ int s_scan[kRWarps];
+  __shared__ int s_scan[2][kRWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const uint32_t my_ring = su32(ring) + warp * Y::ST * Y::STAGE, my_bar = su32(&s_bar[warp][0]);
   if (lane == 0)
@@ -177,8 +181,10 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   float* parts = a.part + static_cast<size_t>(gridDim.x) * (sizeof(RSplit) / sizeof(float));
   RSplit cut{};
   const int entries = a.B * nrb;
-  int* prefix = reinterpret_cast<int*>(sm + kRWarps * R * D);    // split form: pages of one head before entry i
-  Kv8Seq* seqs = reinterpret_cast<Kv8Seq*>(prefix + ((entries + 1) & ~1));   // and its sequence's queries
+  // split form: pages of one head before entry i, the items among those entries, and the entry's sequence
+  int* prefix = reinterpret_cast<int*>(sm + kRWarps * R * D);
+  int* some = prefix + entries;
+  Kv8Seq* seqs = reinterpret_cast<Kv8Seq*>(some + entries);
 
   long long u0 = 0, u1 = 0, u0_first = 0, span = 1;              // this CTA's span of the list (pages)
   int entry = 0;
@@ -196,7 +202,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   if (split) {
     // pages per entry, scanned: a run of entries per thread, then the threads' sums
     const int per = (entries + 32 * kRWarps - 1) / (32 * kRWarps);
-    int sum = 0;
+    int sum = 0, cnt = 0;
     for (int i = 0; i < per; ++i) {
       const int e = tid * per + i;
       if (e >= entries) break;
@@ -206,29 +212,53 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
       const int c = block_pages(a, s, e % nrb, R, x0, x1, r);
       seqs[e] = s;
       prefix[e] = sum;
+      some[e] = cnt;
       sum += c;
+      cnt += c ? 1 : 0;
     }
-    int run = sum;
+    int run = sum, runc = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      const int v = __shfl_up_sync(0xffffffffu, run, o), vc = __shfl_up_sync(0xffffffffu, runc, o);
       run += lane >= o ? v : 0;
+      runc += lane >= o ? vc : 0;
     }
-    if (lane == 31) s_scan[warp] = run;
+    if (lane == 31) s_scan[0][warp] = run, s_scan[1][warp] = runc;
     __syncthreads();
-    int before = run - sum, total = 0;
+    int before = run - sum, beforec = runc - cnt, total = 0, totalc = 0;
 #pragma unroll
     for (int w = 0; w < kRWarps; ++w) {
-      before += w < warp ? s_scan[w] : 0;
-      total += s_scan[w];
+      before += w < warp ? s_scan[0][w] : 0;
+      beforec += w < warp ? s_scan[1][w] : 0;
+      total += s_scan[0][w];
+      totalc += s_scan[1][w];
     }
-    for (int i = 0; i < per && tid * per + i < entries; ++i) prefix[tid * per + i] += before;
+    for (int i = 0; i < per && tid * per + i < entries; ++i) {
+      prefix[tid * per + i] += before;
+      some[tid * per + i] += beforec;
+    }
     __syncthreads();
-    const long long units = static_cast<long long>(total) * a.H;
-    span = (units + gridDim.x - 1) / gridDim.x;
+    // Spans of equal cost, an item's pages behind its kItemCost: the first page at or behind cost x
+    auto cost_before = [&](int e) { return (prefix[e] + static_cast<long long>(kItemCost) * some[e]) * a.H; };
+    const long long pages_all = static_cast<long long>(total) * a.H,
+                    cost_all = pages_all + static_cast<long long>(kItemCost) * totalc * a.H;
+    span = (cost_all + gridDim.x - 1) / gridDim.x;
     span = span < kMinSpan ? kMinSpan : span;
-    u0 = span * blockIdx.x;
-    u1 = u0 + span < units ? u0 + span : units;
+    auto page_at = [&](long long x) {
+      if (x >= cost_all) return pages_all;
+      int lo = 0, hi = entries - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (cost_before(mid) <= x) lo = mid;
+        else hi = mid - 1;
+      }
+      const int pages = (lo + 1 < entries ? prefix[lo + 1] : total) - prefix[lo];
+      const int rem = static_cast<int>(x - cost_before(lo)), h = rem / (pages + kItemCost);
+      return static_cast<long long>(prefix[lo]) * a.H + static_cast<long long>(h) * pages +
+             max(0, rem - h * (pages + kItemCost) - kItemCost);
+    };
+    u0 = page_at(span * blockIdx.x);
+    u1 = page_at(span * (blockIdx.x + 1LL));
     if (a.decode) {                                              // rows that see nothing: zeros
       for (int e = blockIdx.x; e < entries; e += gridDim.x) {
         if ((e + 1 < entries ? prefix[e + 1] : total) != prefix[e]) continue;
@@ -351,7 +381,9 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
       complete = c0 == 0 && c1 == it.pages;
       slot = 2 * blockIdx.x + (c0 > 0 ? 0 : 1);
       if (c0 == 0 && !complete)
-        cut = RSplit{1, it.b, it.rb, it.h, it.n, static_cast<int>((item_at + it.pages - 1) / span), {0, 0}};
+        cut = RSplit{1, it.b, it.rb, it.h, it.n,                 // the CTA whose span holds the item's last page
+                     static_cast<int>(((prefix[entry] + static_cast<long long>(kItemCost) * some[entry]) * a.H +
+                                       (it.h + 1LL) * (it.pages + kItemCost) - 1) / span), {0, 0}};
     } else {
       if (whole >= items) break;
       it.h = static_cast<int>(whole % a.H);
@@ -822,10 +854,10 @@ cudaError_t launch_t(const Kv8Attn& a, cudaStream_t s) {
   const bool direct = pages <= static_cast<long long>(most) * cluster;
   const Mode mode = direct ? kDirect : entries <= kMaxEntries ? kSplit : kWhole;
   const size_t fixed = 1024 + kRWarps * (Y::ST * Y::STAGE + sizeof(float) * R * D);
-  const size_t list = sizeof(Kv8Seq) + sizeof(int);
-  const size_t smem = fixed + (mode == kSplit ? list * (entries + 1) : 0);
+  const size_t list = sizeof(Kv8Seq) + 2 * sizeof(int);
+  const size_t smem = fixed + (mode == kSplit ? list * entries : 0);
   static std::atomic<unsigned long long> configured{0};
-  cudaError_t e = smem_attr_once(kv8_rows_kernel<D, NT, F32>, static_cast<int>(fixed + list * (kMaxEntries + 1)), configured);
+  cudaError_t e = smem_attr_once(kv8_rows_kernel<D, NT, F32>, static_cast<int>(fixed + list * kMaxEntries), configured);
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
   const long long blocks = static_cast<long long>(a.num_pages) * a.H;
