@@ -988,7 +988,7 @@ tq_status kv8_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void
   a.err = ctx->tab.err;
   const bool f32 = dtype == TQ_F32;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (kv8_tc_takes(n_new, a.G, ctx->cfg.d, f32, softmax_scale)) return cuda_status(launch_kv8_tc(a, s));
+  if (kv8_tc_takes(n_new, a.G, ctx->cfg.d, f32, softmax_scale)) return cuda_status(launch_kv8_tc(a, ctx->cfg.d, s));
   return cuda_status(launch_kv8_rows(a, ctx->cfg.d, f32, s));
 }
 }  // namespace
@@ -1070,7 +1070,7 @@ extern "C" tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_n
     return TQ_ERR_INVALID_ARG;
   if (!kv8_head_dim(ctx->cfg.d)) return TQ_ERR_UNSUPPORTED;
   *bytes = std::max(kv8_rows_workspace(batch, n_new, Hq / H, H, ctx->cfg.d),
-                    ctx->cfg.d == kD ? kv8_tc_workspace(batch, n_new, Hq / H, H, max_seq_len) : 0);
+                    ctx->cfg.d <= kD ? kv8_tc_workspace(batch, n_new, Hq / H, H, max_seq_len, ctx->cfg.d) : 0);
   return TQ_OK;
 }
 

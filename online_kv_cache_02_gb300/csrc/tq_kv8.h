@@ -94,8 +94,8 @@ bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d)
 // Many query rows on the tensor cores (tq_kv8_tc.cu): whether the call takes
 // that form, its workspace and its launch.
 bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale);
-size_t kv8_tc_workspace(int B, int T, int G, int H, int max_seq_len);
-cudaError_t launch_kv8_tc(const Kv8Attn& a, cudaStream_t s);
+size_t kv8_tc_workspace(int B, int T, int G, int H, int max_seq_len, int d);
+cudaError_t launch_kv8_tc(const Kv8Attn& a, int d, cudaStream_t s);
 
 }  // namespace tq
 

@@ -1,5 +1,5 @@
 // Causal attention of many query rows over the 8-bit paged cache on the tensor
-// cores (tcgen05), bf16 queries, d = 128.
+// cores (tcgen05), bf16 queries, d = 64 or 128.
 //
 // An item is (sequence, KV head, block of 256 query rows r = t G + g); keys go by in
 // tiles of 128 tokens (8 pages).  All items' tiles form one list that is cut into
@@ -41,7 +41,6 @@ namespace {
 
 using namespace tcx;
 
-constexpr int kTD = 128;                  // head dimension
 constexpr int kTRows = 256;               // query rows per item
 constexpr int kTTok = 128;                // tokens per tile
 constexpr int kTPg = kTTok / kPage;       // pages per tile
@@ -53,7 +52,6 @@ constexpr float kMNone = -1.0e30f;
 // largest weight is then 2^3, and fp16 keeps 11 bits down to 2^-17 of it.  M moves when a page's 16 weights sum to more
 // than kFull, below the end of fp16: the largest of them is then 2^11.9 at least, a score above M + kSlack.
 constexpr float kSlack = 4.5f, kLift = 7.0f, kHead = 4.0f, kFull = 61000.0f;
-constexpr int kPartRow = kTD + 4;
 constexpr int kMaxBlocks = 2048;          // (sequence, query block) pairs that the split form lists
 constexpr int kItemCost = 5;              // an item's start and end, in tiles' time
 constexpr int kMinSpan = 2 + kItemCost;   // a CTA's share of the list at least
@@ -67,24 +65,42 @@ struct TileDesc {                         // one tile of the stream, by page
   int full, pad[3];                       // every row of the block sees every token
 };
 
-// shared memory, from a 1024-byte boundary
-constexpr int kOffQ = 0;                              // [A, B][hi, lo][128 rows][128 B]
-constexpr int kOffK = kOffQ + 4 * 16384;              // [stage][128 tokens][128 B]
-constexpr int kOffVr = kOffK + kKSt * 16384;          // [stage][128 tokens][128 B]
-constexpr int kOffV = kOffVr + kVSt * 16384;          // [buffer][2 halves of 64 channels][128 tokens][128 B]
-constexpr int kOffDesc = kOffV + 2 * 32768;
-constexpr int kOffItem = kOffDesc + kDescs * static_cast<int>(sizeof(TileDesc));
-constexpr int kItemMsg = 48;
-constexpr int kOffBar = kOffItem + kDescs * kItemMsg;
+// Shared memory, from a 1024-byte boundary, by head dimension.
+template <int D>
+struct TG {
+  static constexpr int KT = kTTok * D, VT = 2 * KT;    // a tile's codes, and as fp16
+  static constexpr int QX = 128 * 2 * D;               // a half's queries, both parts
+  static constexpr int PART = D + 4;                   // floats of a row's partial
+  static constexpr int Q = 0;                          // [A, B] halves, see qpos
+  static constexpr int K = Q + 2 * QX;                 // [stage][128 tokens][D B]
+  static constexpr int VR = K + kKSt * KT;             // [stage][128 tokens][D B]
+  static constexpr int V = VR + kVSt * KT;             // [buffer][64-channel blocks][128 tokens][128 B]
+  static constexpr int DESC = V + 2 * VT;
+  static constexpr int ITEM = DESC + kDescs * static_cast<int>(sizeof(TileDesc));
+  static constexpr int BAR = ITEM + kDescs * 48;
+  // Piece c (sixteen channels) of part hi (0) or lo (1) of a row, in rows of 128 bytes with the 128-byte swizzle: at
+  // d = 128 the parts have a tile each, at d = 64 a row holds both.
+  __device__ static __forceinline__ uint32_t qpos(int row, int c, int part) {
+    return D == 128 ? static_cast<uint32_t>(part * 16384 + row * 128 + ((c ^ (row & 7)) << 4))
+                    : static_cast<uint32_t>(row * 128 + (((c + 4 * part) ^ (row & 7)) << 4));
+  }
+  // 16-byte piece c of a token's codes as TMA swizzled them.
+  __device__ static __forceinline__ uint32_t vpos(int t, int c) {
+    return static_cast<uint32_t>(t * D + ((c ^ (D == 128 ? t & 7 : (t >> 1) & 3)) << 4));
+  }
+};
 constexpr int kDoneRing = 4;
 enum Bar {
   bKFull = 0, bVFull = bKFull + kKSt, bVEmpty = bVFull + kVSt, bReady = bVEmpty + kVSt, bSFull = bReady + 2,
   bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2, bItem = bQReady + 2, bDesc = bItem + kDescs,
   bDone = bDesc + kDescs, bDrain = bDone + kDoneRing, bCount
 };
-constexpr int kOffTmem = kOffBar + 8 * bCount;
-constexpr int kTSmem = kOffTmem + 16 + 1024;
-static_assert(kTSmem <= 232448, "shared memory per block");
+template <int D>
+constexpr int tmem_at() { return TG<D>::BAR + 8 * bCount; }
+template <int D>
+constexpr int smem_bytes() { return tmem_at<D>() + 16 + 1024; }
+static_assert(smem_bytes<128>() <= 232448, "shared memory per block");
+static_assert(sizeof(TileDesc) % 16 == 0, "items behind the descriptors");
 // tensor-memory columns of half X
 __device__ __forceinline__ constexpr uint32_t col_s(uint32_t X) { return 128u * X; }
 __device__ __forceinline__ constexpr uint32_t col_o(uint32_t X) { return 256u + 128u * X; }
@@ -110,6 +126,19 @@ __device__ __forceinline__ void mma8_scores(uint32_t d, uint64_t qh, uint64_t ql
       "l"(qh), "l"(ql), "l"(k), "r"(idesc)
       : "memory");
 }
+// The same at d = 64: two steps each, the query's parts side by side in a row.
+__device__ __forceinline__ void mma4_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred e, t, f;\n .reg .b64 q1, q2, q3, k1;\n"
+      " add.u64 q1, %1, 2;\n add.u64 q2, %1, 4;\n add.u64 q3, %1, 6;\n add.u64 k1, %2, 2;\n"
+      " setp.ne.b32 t, 1, 0;\n setp.ne.b32 f, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], q1, k1, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], q2, %2, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], q3, k1, %3, t;\n}\n" ::"r"(d),
+      "l"(q), "l"(k), "r"(idesc)
+      : "memory");
+}
 // O (+)= w V: eight steps of 16 tokens (8 columns of weights, 2048 B or 128 descriptor units of values).
 __device__ __forceinline__ void mma8_values(uint32_t d, uint32_t w, uint64_t v, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -132,7 +161,12 @@ __device__ __forceinline__ void mma8_values(uint32_t d, uint32_t w, uint64_t v, 
 }
 // kind::f8f6f4, fp32 accumulate, e4m3 A and B, K-major, M = 128, N = 128
 constexpr uint32_t kIdF8 = (1u << 4) | (static_cast<uint32_t>(kTTok >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
-constexpr uint32_t kIdPV = idesc_f16(kTD) | (1u << 16);          // B MN-major
+// e4m3 rows of D bytes, K-major with a swizzle of their length, in groups of eight
+template <int D>
+__device__ __forceinline__ uint64_t kdesc8(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(8 * D >> 4) << 32) |
+         (1ull << 46) | ((D == 128 ? 2ull : 4ull) << 61);
+}
 // MN-major operand, 128-byte swizzle: token rows of 64 channels, 8-row groups 1024 B apart, channel halves 16 KB apart
 __device__ __forceinline__ uint64_t vdesc(uint32_t saddr) {
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16384 >> 4) << 16) |
@@ -272,16 +306,18 @@ struct TSplit {
   int valid, b, h, qb, p0, rows, last, pad;            // last: the CTA that holds the item's end
 };
 
+template <int D>
 __global__ void __launch_bounds__(kTThreads, 1)
     kv8_tc_kernel(const __grid_constant__ Kv8Attn a, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, int nqb, int split) {
+  using L = TG<D>;
   extern __shared__ __align__(1024) unsigned char sm_raw[];
   unsigned char* sm = sm_raw + ((0u - su32(sm_raw)) & 1023u);
   const uint32_t sb = su32(sm);
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-  auto bar = [&](int i) { return sb + kOffBar + 8u * static_cast<uint32_t>(i); };
-  TileDesc* descs = reinterpret_cast<TileDesc*>(sm + kOffDesc);
-  ItemMsg* item_ring = reinterpret_cast<ItemMsg*>(sm + kOffItem);
+  auto bar = [&](int i) { return sb + L::BAR + 8u * static_cast<uint32_t>(i); };
+  TileDesc* descs = reinterpret_cast<TileDesc*>(sm + L::DESC);
+  ItemMsg* item_ring = reinterpret_cast<ItemMsg*>(sm + L::ITEM);
 
   if (tid == 0) {
     for (int i = 0; i < kKSt; ++i) bar_init(bar(bKFull + i), 1);
@@ -305,7 +341,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 13) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + kOffTmem), "r"(512)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + tmem_at<D>()), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -316,7 +352,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   long long u0 = 0, u1 = 0, span = 1;
   int entry0 = 0, before0 = 0;
   if (split) {
-    int* prefix = reinterpret_cast<int*>(sm + kOffQ);
+    int* prefix = reinterpret_cast<int*>(sm + L::Q);
     int* warp_sum = prefix + kMaxBlocks;
     const int per = (entries + kTThreads - 1) / kTThreads;
     TBlock k;
@@ -359,7 +395,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + kOffTmem);
+  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + tmem_at<D>());
   TSplit* splits = reinterpret_cast<TSplit*>(a.part);              // one per CTA, then the partials' slots
   float* parts = a.part + static_cast<size_t>(gridDim.x) * (sizeof(TSplit) / sizeof(float));
   bool failed = false;
@@ -400,31 +436,30 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const unsigned gr = static_cast<unsigned>(x.qb * kTRows + 128 * X + r), tok = gr / static_cast<unsigned>(a.G);
       w.live = 128 * X + r < x.rows;
       w.p = w.live ? x.p0 + static_cast<int>(tok) : -1;
-      w.at = ((static_cast<long long>(x.b) * a.T + tok) * a.Hq + x.h * a.G + (gr - tok * a.G)) * kTD;
-      // The warp's 32 rows, half a warp per row (a lane per row would ask for 32 lines with each load); the raw 16-byte
+      w.at = ((static_cast<long long>(x.b) * a.T + tok) * a.Hq + x.h * a.G + (gr - tok * a.G)) * D;
+      // The warp's 32 rows, D / 8 lanes per row (a lane per row would ask for 32 lines with each load); the raw 16-byte
       // pieces 2c and 2c + 1 of a row wait where the parts of its channels 16c .. 16c + 15 will stand.
-      const uint32_t qw = sb + kOffQ + X * 32768 + 32 * wq * 128, qh = qw + lane * 128;
+      const uint32_t qx = sb + L::Q + X * L::QX;
       {
+        constexpr int kP = D / 8, kR = 32 / kP;        // pieces per row, rows per load
         const long long where = w.live ? w.at : -1;
-        const int piece = lane & 15;
-        uint4 v4[16];
+        const int piece = lane % kP;
+        uint4 v4[kP];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const long long at = __shfl_sync(0xffffffffu, where, 2 * i + (lane >> 4));
+        for (int i = 0; i < kP; ++i) {
+          const long long at = __shfl_sync(0xffffffffu, where, kR * i + lane / kP);
           v4[i] = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at)[piece]
                           : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int rw = 2 * i + (lane >> 4);
-          sts128(qw + rw * 128 + (piece & 1) * 16384 + (((piece >> 1) ^ (rw & 7)) << 4), v4[i].x, v4[i].y, v4[i].z, v4[i].w);
-        }
+        for (int i = 0; i < kP; ++i)
+          sts128(qx + L::qpos(32 * wq + kR * i + lane / kP, piece >> 1, piece & 1), v4[i].x, v4[i].y, v4[i].z, v4[i].w);
       }
       __syncwarp();
       uint32_t mx2 = 0u;                               // largest magnitudes: bf16 bits order as integers
 #pragma unroll 8
-      for (int i = 0; i < 16; ++i) {
-        const uint4 v = lds128(qh + (i & 1) * 16384 + (((i >> 1) ^ (r & 7)) << 4));
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = lds128(qx + L::qpos(r, i >> 1, i & 1));
         mx2 = __vmaxu2(__vmaxu2(mx2, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
         mx2 = __vmaxu2(__vmaxu2(mx2, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
       }
@@ -435,9 +470,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
       w.rowf = __int_as_float((127 - e) << 23);
       // rolled: a loop that runs once an item, out of the instruction cache otherwise (3.6 us unrolled)
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        const uint32_t pos = qh + static_cast<uint32_t>((c ^ (r & 7)) << 4);
-        const uint4 ua = lds128(pos), ub = lds128(pos + 16384);
+      for (int c = 0; c < D / 16; ++c) {
+        const uint32_t ph = qx + L::qpos(r, c, 0), pl = qx + L::qpos(r, c, 1);
+        const uint4 ua = lds128(ph), ub = lds128(pl);
         const uint32_t u[8] = {ua.x, ua.y, ua.z, ua.w, ub.x, ub.y, ub.z, ub.w};
         uint32_t hi[4], lo[4];
 #pragma unroll
@@ -449,8 +484,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
           hi[k] = h0 | (h1 << 16);
           lo[k] = half2_to_codes(sub_half2(f0, codes_to_half2(h0))) | (half2_to_codes(sub_half2(f1, codes_to_half2(h1))) << 16);
         }
-        sts128(pos, hi[0], hi[1], hi[2], hi[3]);
-        sts128(pos + 16384, lo[0], lo[1], lo[2], lo[3]);
+        sts128(ph, hi[0], hi[1], hi[2], hi[3]);
+        sts128(pl, lo[0], lo[1], lo[2], lo[3]);
       }
       // a row that is not finite: every score NaN, and so the result
       if (mx >= 0x7F80u) w.rowf = __int_as_float(0x7FC00000);
@@ -553,7 +588,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
             if (t > 0) {                               // O of the tiles before (their MMAs have run: S came after)
 #pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
+              for (int c = 0; c < D / 16; ++c) {
                 float o[16];
                 uint32_t u[16];
                 tld16(to + 16u * c, o);
@@ -604,9 +639,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
       ++nO;
       tc_after();
       const float inv = l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
-      float* part = parts + (static_cast<long long>(done_item.slot) * kTRows + 128 * X + r) * kPartRow;
+      float* part = parts + (static_cast<long long>(done_item.slot) * kTRows + 128 * X + r) * L::PART;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < D / 32; ++c) {
         float o[32];
         tld32(to + 32u * c, o);
         if (!done_row.live) continue;
@@ -650,13 +685,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const int j = descs[seq % kDescs].j0[pg] + (t & 15);
         // what no row sees may hold anything: zeros instead
         const bool see = j <= it.pmax && (!a.window || j > it.pmin - a.window || j < a.sinks);
-        const uint32_t src = sb + kOffVr + (seq % kVSt) * 16384 + t * 128;
-        const uint32_t dst = sb + kOffV + (seq & 1) * 32768 + t * 128;
-        uint4 w[8];                                    // every load ahead of the stores
+        const uint32_t src = sb + L::VR + (seq % kVSt) * L::KT;
+        const uint32_t dst = sb + L::V + (seq & 1) * L::VT + t * 128;
+        uint4 w[D / 16];                               // every load ahead of the stores
 #pragma unroll
-        for (int c = 0; c < 8; ++c) w[c] = lds128(src + static_cast<uint32_t>((c ^ (t & 7)) << 4));
+        for (int c = 0; c < D / 16; ++c) w[c] = lds128(src + L::vpos(t, c));
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < D / 16; ++c) {
           if (!see) w[c] = make_uint4(0u, 0u, 0u, 0u);
           const uint32_t o0 = static_cast<uint32_t>((((2 * c) & 7) ^ (t & 7)) << 4),
                          o1 = static_cast<uint32_t>((((2 * c + 1) & 7) ^ (t & 7)) << 4);
@@ -721,8 +756,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
                          end = static_cast<unsigned>(it.qb * kTRows + it.rows - 1) / a.G + 1;
           for (unsigned t = first + lane; t < end; t += 32) {
             const char* q = static_cast<const char*>(a.q) +
-                            2 * ((static_cast<long long>(it.b) * a.T + t) * a.Hq + h * a.G) * kTD;
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q), "r"(2 * kTD * a.G));
+                            2 * ((static_cast<long long>(it.b) * a.T + t) * a.Hq + h * a.G) * D;
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q), "r"(2 * D * a.G));
           }
         }
         const int c0 = t0 * kTPg, c1 = min(it.pages, t1 * kTPg);
@@ -757,7 +792,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           for (int k = 0; k < 4 && c4 + k * kTPg < c1; ++k, ++seq) {
             const bool on = (lane >> 3) == k;
             const int pg = lane & 7;
-            const uint32_t bytes = static_cast<uint32_t>(__popc((there4 >> (8 * k)) & 0xFFu)) * kPage * kTD;
+            const uint32_t bytes = static_cast<uint32_t>(__popc((there4 >> (8 * k)) & 0xFFu)) * kPage * D;
             if (seq >= kKSt && !wait(bDone + (seq - kKSt) % kDoneRing, (seq - kKSt) / kDoneRing)) break;
             TileDesc& d = descs[seq % kDescs];
             if (on) {
@@ -776,7 +811,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             __syncwarp();
             ++nk;
             if (on && cur.blk >= 0)
-              tma_block(sb + kOffK + (seq % kKSt) * 16384 + pg * kPage * kTD, &mk, cur.blk, bar(bKFull + seq % kKSt));
+              tma_block(sb + L::K + (seq % kKSt) * L::KT + pg * kPage * D, &mk, cur.blk, bar(bKFull + seq % kKSt));
             if (seq >= kVSt && !wait(bVEmpty + seq % kVSt, seq / kVSt - 1)) break;
             if (lane == 0) {
               if (bytes) bar_arrive_tx(bar(bVFull + seq % kVSt), bytes);
@@ -785,7 +820,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             __syncwarp();
             ++nv;
             if (on && cur.blk >= 0)
-              tma_block(sb + kOffVr + (seq % kVSt) * 16384 + pg * kPage * kTD, &mv, cur.blk, bar(bVFull + seq % kVSt));
+              tma_block(sb + L::VR + (seq % kVSt) * L::KT + pg * kPage * D, &mv, cur.blk, bar(bVFull + seq % kVSt));
           }
           cur = nxt;
         }
@@ -826,12 +861,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
         two = __all_sync(0xffffffffu, it.rows > 128);
       };
       auto scores = [&](uint32_t X, int s) {
-        const uint32_t q = sb + kOffQ + X * 32768, k = sb + kOffK + (s % kKSt) * 16384;
-        mma8_scores(tmem + col_s(X), sdesc(q), sdesc(q + 16384), sdesc(k), kIdF8);
+        const uint32_t q = sb + L::Q + X * L::QX, k = sb + L::K + (s % kKSt) * L::KT;
+        if (D == 128) mma8_scores(tmem + col_s(X), sdesc(q), sdesc(q + 16384), kdesc8<D>(k), kIdF8);
+        else mma4_scores(tmem + col_s(X), sdesc(q), kdesc8<D>(k), kIdF8);
         mma_commit_warp(bar(bSFull + X));
       };
       auto values = [&](uint32_t X, int s, bool first) {
-        mma8_values(tmem + col_o(X), tmem + col_s(X), vdesc(sb + kOffV + (s & 1) * 32768), kIdPV, first ? 0u : 1u);
+        mma8_values(tmem + col_o(X), tmem + col_s(X), vdesc(sb + L::V + (s & 1) * L::VT), idesc_f16(D) | (1u << 16), first ? 0u : 1u);
       };
       // the first tile of an item: its keys and its queries
       auto first_scores = [&](int s) {
@@ -895,19 +931,21 @@ __global__ void __launch_bounds__(kTThreads, 1)
 }
 
 // Joins the parts of the items that cross spans: 32 rows a block, a warp per row.
+template <int D>
 __global__ void __launch_bounds__(256) kv8_tc_join_kernel(const __grid_constant__ Kv8Attn a, int ctas) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
   pdl_wait();
   const TSplit cut = reinterpret_cast<const TSplit*>(a.part)[c];
   if (!cut.valid) return;
   const float* parts = a.part + static_cast<size_t>(ctas) * (sizeof(TSplit) / sizeof(float));
-  const long long step = static_cast<long long>(kTRows) * kPartRow;
+  constexpr int kPart = TG<D>::PART;
+  const long long step = static_cast<long long>(kTRows) * kPart;
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     const int rr = 32 * blockIdx.y + 8 * i + warp;
     if (rr >= cut.rows) return;
     // the first part is in its CTA's second slot, the others in their CTAs' first
-    auto part = [&](int k) { return parts + (2LL * k + (k == c ? 1 : 0)) * step + static_cast<long long>(rr) * kPartRow; };
+    auto part = [&](int k) { return parts + (2LL * k + (k == c ? 1 : 0)) * step + static_cast<long long>(rr) * kPart; };
     float M = kMNone;
     for (int k = c + lane; k <= cut.last; k += 32) M = fmaxf(M, part(k)[0]);
 #pragma unroll
@@ -919,14 +957,16 @@ __global__ void __launch_bounds__(256) kv8_tc_join_kernel(const __grid_constant_
       const float* p = part(k);
       const float f = ex2(p[0] - M);
       L = fmaf(f, p[1], L);
+      if (4 * lane >= D) continue;
       const float4 x = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
       acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y), acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
     }
+    if (4 * lane >= D) continue;
     const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
     const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
                          y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
     const unsigned gr = static_cast<unsigned>(cut.qb * kTRows + rr), tok = gr / static_cast<unsigned>(a.G);
-    const long long at = ((static_cast<long long>(cut.b) * a.T + tok) * a.Hq + cut.h * a.G + (gr - tok * a.G)) * kTD + 4 * lane;
+    const long long at = ((static_cast<long long>(cut.b) * a.T + tok) * a.Hq + cut.h * a.G + (gr - tok * a.G)) * D + 4 * lane;
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
   }
@@ -983,30 +1023,37 @@ bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d)
 }
 
 bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale) {
-  return d == kTD && !f32 && static_cast<long long>(T) * G > 16 && softmax_scale != 0.0f &&
-         std::fabs(static_cast<double>(softmax_scale)) <= (1.0 + 1e-6) / std::sqrt(static_cast<double>(kTD));
+  return (d == 64 || d == 128) && !f32 && static_cast<long long>(T) * G > 16 && softmax_scale != 0.0f &&
+         std::fabs(static_cast<double>(softmax_scale)) <= (1.0 + 1e-6) / std::sqrt(static_cast<double>(d));
 }
 
-size_t kv8_tc_workspace(int B, int T, int G, int H, int max_seq_len) {
+size_t kv8_tc_workspace(int B, int T, int G, int H, int max_seq_len, int d) {
   const int nqb = query_blocks(T, G);
   if (!splits(B, nqb)) return 16;
   return static_cast<size_t>(ctas_for(B, H, nqb, max_seq_len)) *
-         (sizeof(TSplit) + 2 * sizeof(float) * static_cast<size_t>(kTRows) * kPartRow);
+         (sizeof(TSplit) + 2 * sizeof(float) * static_cast<size_t>(kTRows) * (d + 4));
 }
 
-cudaError_t launch_kv8_tc(const Kv8Attn& a, cudaStream_t s) {
+namespace {
+template <int D>
+cudaError_t launch_t(const Kv8Attn& a, cudaStream_t s) {
   const int nqb = query_blocks(a.T, a.G);
   CUtensorMap mk, mv;
   const long long blocks = static_cast<long long>(a.num_pages) * a.H;
-  if (!kv8_block_map(&mk, a.kc, blocks, kTD) || !kv8_block_map(&mv, a.vc, blocks, kTD)) return cudaErrorInvalidValue;
+  if (!kv8_block_map(&mk, a.kc, blocks, D) || !kv8_block_map(&mv, a.vc, blocks, D)) return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> configured{0};
-  cudaError_t e = smem_attr_once(kv8_tc_kernel, kTSmem, configured);
+  cudaError_t e = smem_attr_once(kv8_tc_kernel<D>, smem_bytes<D>(), configured);
   if (e != cudaSuccess) return e;
   const int ctas = ctas_for(a.B, a.H, nqb, a.max_seq_len);
   const bool split = splits(a.B, nqb);
-  e = launch_pdl(kv8_tc_kernel, dim3(ctas), dim3(kTThreads), kTSmem, s, a, mk, mv, nqb, split ? 1 : 0);
+  e = launch_pdl(kv8_tc_kernel<D>, dim3(ctas), dim3(kTThreads), smem_bytes<D>(), s, a, mk, mv, nqb, split ? 1 : 0);
   if (e != cudaSuccess || !split) return e;
-  return launch_pdl(kv8_tc_join_kernel, dim3(ctas, kTRows / 32), dim3(256), 0, s, a, ctas);
+  return launch_pdl(kv8_tc_join_kernel<D>, dim3(ctas, kTRows / 32), dim3(256), 0, s, a, ctas);
+}
+}  // namespace
+
+cudaError_t launch_kv8_tc(const Kv8Attn& a, int d, cudaStream_t s) {
+  return d == 128 ? launch_t<128>(a, s) : d == 64 ? launch_t<64>(a, s) : cudaErrorInvalidValue;
 }
 
 }  // namespace tq
