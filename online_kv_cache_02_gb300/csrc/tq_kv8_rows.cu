@@ -54,6 +54,10 @@ constexpr int kMaxEntries = 1024;         // (sequence, row block) pairs that th
 //   clusters that leave two thirds of the card free, 48: 1 of 6000 16.5 us (18.7), 2 of 3000 12.7 us (16.9);
 //   clusters that fill it, 32: 16 of 1000 15.4 us (16.5), 7 of 6000 36 us (27).
 constexpr int kDirectOne = 64, kDirectFew = 48, kDirectMany = 32;
+// Weights are 2^(kLift + score - M), M kHead above the largest score met (it seldom moves again): the largest weight is
+// 2^8, and fp16 keeps 11 bits of them down to 2^-22 of it.  M moves once a weight passes kFull, below the end of fp16:
+// that score lies above M + kSlack.
+constexpr float kLift = 11.0f, kHead = 3.0f, kSlack = 4.5f, kFull = 61000.0f;
 enum Mode { kWhole = 0, kSplit = 1, kDirect = 2 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -533,41 +537,53 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
             }
         }
         // ---- weights ----
+        // By the maximum so far, while none passes fp16 (a new maximum costs six shuffles); else the maximum anew.
         uint32_t pf[NT][HL][2];
+        float w[NT][4];
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[nt][i] = exp2_fast(s[nt][i] - (m[nt][i & 1] - evf - kLift));
+            over |= w[nt][i] > kFull || m[nt][i & 1] == -INFINITY;
+          }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float mx = fmaxf(s[nt][c], s[nt][2 + c]) + evf;
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+              if (mx > m[nt][c] + kSlack) {
+                const float mn = mx + kHead, al = exp2_fast(m[nt][c] - mn);
+                l[nt][c] *= al;
+#pragma unroll
+                for (int i = 0; i < Y::MT; ++i) {
+                  o[nt][i][c] *= al;
+                  o[nt][i][2 + c] *= al;
+                }
+                m[nt][c] = mn;
+              }
+              const float base = m[nt][c] == -INFINITY ? 0.0f : m[nt][c] - evf - kLift;
+              w[nt][c] = exp2_fast(s[nt][c] - base);
+              w[nt][2 + c] = exp2_fast(s[nt][2 + c] - base);
+            }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float w[4];
-#pragma unroll
-          for (int cidx = 0; cidx < 2; ++cidx) {
-            float mx = fmaxf(s[nt][cidx], s[nt][2 + cidx]) + evf;
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            const float mn = fmaxf(m[nt][cidx], mx);
-            if (mn > m[nt][cidx]) {
-              const float al = exp2_fast(m[nt][cidx] - mn);
-              l[nt][cidx] *= al;
-#pragma unroll
-              for (int i = 0; i < Y::MT; ++i) {
-                o[nt][i][cidx] *= al;
-                o[nt][i][2 + cidx] *= al;
-              }
-              m[nt][cidx] = mn;
-            }
-            // weights up to 2^15, so that fp16 keeps 11 bits of them down to 2^-29
-            const float base = mn == -INFINITY ? 0.0f : mn - evf - 15.0f;
-            w[cidx] = exp2_fast(s[nt][cidx] - base);
-            w[2 + cidx] = exp2_fast(s[nt][2 + cidx] - base);
-            l[nt][cidx] += (w[cidx] + w[2 + cidx]) * vinv;
-          }
+          l[nt][0] += (w[nt][0] + w[nt][2]) * vinv;
+          l[nt][1] += (w[nt][1] + w[nt][3]) * vinv;
           __half hh[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) hh[i] = __float2half_rn(w[i]);
+          for (int i = 0; i < 4; ++i) hh[i] = __float2half_rn(w[nt][i]);
           pf[nt][0][0] = transpose8(pack(hh[0], hh[1]));
           pf[nt][0][1] = transpose8(pack(hh[2], hh[3]));
           if (F32) {
             __half ll[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ll[i] = __float2half_rn(w[i] - __half2float(hh[i]));
+            for (int i = 0; i < 4; ++i) ll[i] = __float2half_rn(w[nt][i] - __half2float(hh[i]));
             pf[nt][HL - 1][0] = transpose8(pack(ll[0], ll[1]));
             pf[nt][HL - 1][1] = transpose8(pack(ll[2], ll[3]));
           }

@@ -1,4 +1,4 @@
-// Causal attention of many query rows over the 8-bit paged cache on the tensor
+// Attention of many query rows per KV head over the 8-bit paged cache on the tensor
 // cores (tcgen05), bf16 queries, d = 64 or 128.
 //
 // An item is (sequence, KV head, block of 256 query rows r = t G + g); keys go by in
@@ -347,6 +347,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
   }
   pdl_wait();
   pdl_trigger();                                       // the join's launch
+  if (a.decode) {                                      // a sequence that is empty: zeros
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+      if (kv8_seq(a, b).n > 0) continue;
+      uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(b) * a.Hq * D);
+      for (int i = tid; i < a.Hq * (D / 8); i += kTThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
   // the list, cut into equal spans: units before each block (of one head), by a scan in the queries' room
   const int entries = a.B * nqb;
   long long u0 = 0, u1 = 0, span = 1;
