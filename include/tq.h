@@ -401,10 +401,10 @@ typedef struct {
  * written to it so far: the call that writes slot 0 starts a block anew; a
  * later call keeps the scale or raises it, and then rounds the earlier slots'
  * codes again (exact but for the smallest).  Codes are the nearest (ties to
- * even) to the exactly rotated values, whatever the launch.  After a rollback
+ * even) to the values rotated in fp64, whatever the launch.  After a rollback
  * of a sequence, appending at a smaller position is the way to go on.
  * Every block is written by one sequence: two that share a page must not both
- * append to it.  Values that are not finite in fp32 set device status bit 32
+ * append to it (reading shared pages is fine).  Values that are not finite in fp32 set device status bit 32
  * and are stored as 0 (NaN) or as the block's largest code (infinite), without
  * counting for its scale.  Bit 2: a position beyond the block table (the page
  * is skipped) or outside the cos_sin table (the token is skipped).  Bit 64: an
@@ -428,9 +428,14 @@ tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_new, int num
  * page behind the sequence's end, or outside every query's window, may hold
  * any bytes.  Any number of query heads per KV head.  The split of the work
  * follows the lengths on the device; results do not depend on the run.
- * Accuracy at every softmax_scale: fp32 products of exact codes; for fp32 the
- * query and the weights keep 22 bits, for bf16 the query is exact and the
- * weights keep 11.  q, out and workspace are 16-byte aligned. */
+ * Accuracy at every softmax_scale: exact products of codes and queries summed
+ * in fp32, weights to 11 bits (bf16) or 22 (fp32) down to 2^-22 of the largest.
+ * With more than 16 query rows (n_new times heads per KV head) and bf16, d 64
+ * or 128 and |softmax_scale| <= 1/sqrt(d), the tcgen05 form runs: a query
+ * channel is then off by at most 2^-17 of its row's largest, the weights keep
+ * 11 bits down to 2^-17.  NaN codes (which tq_kv8_append never writes) at a
+ * seen position may spoil other rows too.  q, out and workspace are 16-byte
+ * aligned; calls that may overlap on the GPU need a workspace each. */
 tq_status tq_kv8_decode_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* q, tq_dtype dtype, int batch,
                                   int num_q_heads, const int32_t* seq_lens, int max_seq_len, int window, int sinks,
                                   float softmax_scale, void* out, void* workspace, size_t workspace_bytes, void* stream);

@@ -1025,7 +1025,9 @@ extern "C" tq_status tq_kv8_append(const tq_ctx* ctx, const tq_kv8_cache* cache,
   const uintptr_t elem = dtype == TQ_F32 ? 3 : 1;
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(q)) & elem)
     return TQ_ERR_INVALID_ARG;
-  if (static_cast<long long>(batch) * n_new > 0x7FFFFFFFLL || H > 65535 || Hq > 65535) return TQ_ERR_UNSUPPORTED;
+  // in place: a row is read where it is written
+  if (q && q == q_out && q_stride != 0 && q_stride != dq) return TQ_ERR_INVALID_ARG;
+  if (static_cast<long long>(batch) * n_new > (1LL << 30) || H > 65535 || Hq > 65535) return TQ_ERR_UNSUPPORTED;
   st = on_device(ctx);
   if (st != TQ_OK) return st;
   Kv8Append a{};

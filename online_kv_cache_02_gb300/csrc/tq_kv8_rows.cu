@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   bool failed = false;
   const bool split = mode == kSplit;
   pdl_wait();
-  pdl_trigger();                                                 // the join's launch, beside the work
+  if (split) pdl_trigger();                                      // the join's launch, beside the work
   RSplit* records = reinterpret_cast<RSplit*>(a.part);            // one per CTA, then the partials' slots
   float* parts = a.part + static_cast<size_t>(gridDim.x) * (sizeof(RSplit) / sizeof(float));
   RSplit cut{};

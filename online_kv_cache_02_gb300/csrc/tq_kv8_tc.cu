@@ -92,7 +92,7 @@ struct TG {
 constexpr int kDoneRing = 4;
 enum Bar {
   bKFull = 0, bVFull = bKFull + kKSt, bVEmpty = bVFull + kVSt, bReady = bVEmpty + kVSt, bSFull = bReady + 2,
-  bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2, bItem = bQReady + 2, bDesc = bItem + kDescs,
+  bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2, bItem = bQReady + 2, bItemFree = bItem + kDescs, bDesc = bItemFree + kDescs,
   bDone = bDesc + kDescs, bDrain = bDone + kDoneRing, bCount
 };
 template <int D>
@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     for (int i = 0; i < kDoneRing; ++i) bar_init(bar(bDone + i), 1);
     for (int i = 0; i < kDescs; ++i) {
       bar_init(bar(bItem + i), 1);
+      bar_init(bar(bItemFree + i), 13);                // softmax, conversion and MMA warps
       bar_init(bar(bDesc + i), 1);
     }
     bar_init(bar(bDrain), 1);
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  pdl_trigger();                                       // the join's launch
+  if (split) pdl_trigger();                            // the join's launch
   if (a.decode) {                                      // a sequence that is empty: zeros
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
       if (kv8_seq(a, b).n > 0) continue;
@@ -416,6 +417,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
   auto next_item = [&](int n) {
     ItemMsg x{};
     if (wait(bItem + n % kDescs, n / kDescs)) x = item_ring[n % kDescs];
+    __syncwarp();
+    if (lane == 0) bar_arrive(bar(bItemFree + n % kDescs));
     return x;
   };
 
@@ -723,6 +726,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // ---- items, pages, TMA ----------------------------------------------------------------
       int seq = 0, n = 0, nk = 0, nv = 0;              // tiles, and copies issued
       auto publish = [&](const ItemMsg& x) {
+        if (n >= kDescs) (void)wait(bItemFree + n % kDescs, n / kDescs - 1);   // every warp has taken the one before
         if (lane == 0) {
           item_ring[n % kDescs] = x;
           bar_arrive(bar(bItem + n % kDescs));

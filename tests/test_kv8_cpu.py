@@ -133,7 +133,7 @@ def test_nothing_to_do_is_no_error(f):
 @pytest.mark.parametrize("kw", [dict(cache=None), dict(k=None, v=None, q=None), dict(dtype=2), dict(batch=-1),
                                 dict(n_new=-1), dict(hq=0), dict(start=None), dict(q_out=None), dict(q_out=(1 << 20) + 8),
                                 dict(k=(1 << 20) + 1), dict(strides=(511, 0, 0)), dict(strides=(0, -4, 0)),
-                                dict(strides=(0, 0, 1023))])
+                                dict(strides=(0, 0, 1023)), dict(q_out=1 << 20, strides=(0, 0, 2048))])
 def test_append_refuses(f, kw):
     assert _append(f, **kw) == tq.TQ_ERR_INVALID_ARG
 
@@ -177,6 +177,16 @@ def test_attention_refuses_small_workspaces_and_other_head_dims(f):
         assert _append(g) == tq.TQ_ERR_UNSUPPORTED
         assert tq.raw_status("tq_kv8_cache_layout", g.ctx, 4, ctypes.byref(ctypes.c_size_t()), None) == tq.TQ_ERR_UNSUPPORTED
     assert tq.tq_kv8_cache_layout(f.ctx, 4) == (4 * 16 * 128, 16)
+
+
+def test_sizes_beyond_the_kernels_arithmetic_are_refused(f):
+    assert _append(f, batch=2, n_new=(1 << 29) + 1) == tq.TQ_ERR_UNSUPPORTED
+    assert _append(f, cache=_cache(f, num_kv_heads=65536, num_pages=1), k=None, v=None) == tq.TQ_ERR_UNSUPPORTED
+    assert _append(f, cache=_cache(f, num_pages=1 << 29, num_kv_heads=4)) == tq.TQ_ERR_UNSUPPORTED
+    for causal in (False, True):
+        assert _attend(f, causal, cache=_cache(f, num_pages=1 << 29)) == tq.TQ_ERR_UNSUPPORTED
+        assert _attend(f, causal, batch=1 << 20, hq=128, n_new=1) == tq.TQ_ERR_UNSUPPORTED
+        assert _attend(f, causal, cache=_cache(f, max_pages_per_seq=1 << 26), max_len=1 << 30) == tq.TQ_ERR_UNSUPPORTED
 
 
 def test_null_context_is_refused():
