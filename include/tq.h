@@ -403,10 +403,10 @@ typedef struct {
  * codes again (exact but for the smallest).  Codes are the nearest (ties to
  * even) to the values rotated in fp64, whatever the launch.  After a rollback
  * of a sequence, appending at a smaller position is the way to go on.
- * Every block is written by one sequence: two that share a page must not both
- * append to it (reading shared pages is fine).  Values that are not finite in fp32 set device status bit 32
- * and are stored as 0 (NaN) or as the block's largest code (infinite), without
- * counting for its scale.  Bit 2: a position beyond the block table (the page
+ * Every block is written by one sequence, at one place of its table (reading
+ * shared pages is fine).  Values that are not finite in fp32 set device status
+ * bit 32 and are stored as 0 (NaN) or as the block's largest code (infinite),
+ * without counting for its scale.  Bit 2: a position beyond the block table (the page
  * is skipped) or outside the cos_sin table (the token is skipped).  Bit 64: an
  * earlier token's block had no power of two in range as its scale (taken as
  * 2^-100).  Errors as tq_quantize. */
@@ -433,9 +433,13 @@ tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_new, int num
  * With more than 16 query rows (n_new times heads per KV head) and bf16, d 64
  * or 128 and |softmax_scale| <= 1/sqrt(d), the tcgen05 form runs: a query
  * channel is then off by at most 2^-17 of its row's largest, the weights keep
- * 11 bits down to 2^-17.  NaN codes (which tq_kv8_append never writes) at a
- * seen position may spoil other rows too.  q, out and workspace are 16-byte
- * aligned; calls that may overlap on the GPU need a workspace each. */
+ * 11 bits down to 2^-17.  The weights ride on the value scales: of two
+ * blocks of a sequence whose value scales lie more than 2^100 apart (a block of
+ * zeros has 2^-100) the smaller one's weights may be lost.  NaN codes (which
+ * tq_kv8_append never writes) at a seen position may spoil other rows too.
+ * q, out and workspace are 16-byte aligned; calls that may overlap on the GPU
+ * need a workspace each.  batch * n_new * num_q_heads is below 2^27, and
+ * positions below 2^29 (else TQ_ERR_UNSUPPORTED). */
 tq_status tq_kv8_decode_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* q, tq_dtype dtype, int batch,
                                   int num_q_heads, const int32_t* seq_lens, int max_seq_len, int window, int sinks,
                                   float softmax_scale, void* out, void* workspace, size_t workspace_bytes, void* stream);

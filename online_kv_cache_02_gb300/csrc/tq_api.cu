@@ -955,7 +955,7 @@ tq_status kv8_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void
   if (static_cast<long long>(batch) * n_new * Hq >= (1LL << 27)) return TQ_ERR_UNSUPPORTED;
   // positions lie below both: a window or sinks beyond them change nothing (and the kernels' sums stay in 32 bits)
   const long long cap = std::min<long long>(max_seq_len, static_cast<long long>(kPage) * cache->max_pages_per_seq);
-  if (cap > (1LL << 29) || cap * H > 0x7FFFFFFFLL * kPage) return TQ_ERR_UNSUPPORTED;
+  if (cap > (1LL << 29) || (cap / kPage + 64) * H > 0x7FFFFFFFLL) return TQ_ERR_UNSUPPORTED;
   size_t need = 0;
   st = tq_kv8_workspace_size(ctx, batch, n_new, Hq, H, max_seq_len, &need);
   if (st != TQ_OK) return st;

@@ -15,12 +15,11 @@
 //
 // A CTA's warps take its pages in turn and join their (M, l, O) in shared memory
 // at an item's end.  How the pages come to the CTAs:
-//   direct  few pages per item: an item per cluster of 1 to 8 CTAs, joined through
-//           distributed shared memory, one launch;
+//   direct  few pages per item, or too many items to list: an item per cluster of 1 to
+//           8 CTAs, joined through distributed shared memory, one launch;
 //   split   all pages of all items form one list, cut into spans of equal cost, one
 //           per CTA (whatever the sequences' lengths); items that cross spans leave partials
-//           for a second kernel;
-//   whole   too many sequences to list: items in turn.
+//           for a second kernel.
 
 #include "tq_kv8.h"
 #include "tq_tc.cuh"
@@ -58,7 +57,6 @@ constexpr int kDirectOne = 64, kDirectFew = 48, kDirectMany = 32;
 // 2^8, and fp16 keeps 11 bits of them down to 2^-22 of it.  M moves once a weight passes kFull, below the end of fp16:
 // that score lies above M + kSlack.
 constexpr float kLift = 11.0f, kHead = 3.0f, kSlack = 4.5f, kFull = 61000.0f;
-enum Mode { kWhole = 0, kSplit = 1, kDirect = 2 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -160,7 +158,7 @@ __device__ __forceinline__ int block_pages(const Kv8Attn& a, const Kv8Seq& s, in
 
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows_kernel(const __grid_constant__ Kv8Attn a, const __grid_constant__ CUtensorMap mk,
-                                                                const __grid_constant__ CUtensorMap mv, int nrb, int mode,
+                                                                const __grid_constant__ CUtensorMap mv, int nrb, int split,
                                                                 int cluster) {
   using Y = Lay<D>;
   constexpr int R = 8 * NT, HL = F32 ? 2 : 1;
@@ -178,7 +176,6 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
   bool failed = false;
-  const bool split = mode == kSplit;
   pdl_wait();
   if (split) pdl_trigger();                                      // the join's launch, beside the work
   RSplit* records = reinterpret_cast<RSplit*>(a.part);            // one per CTA, then the partials' slots
@@ -294,8 +291,8 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
     item_at = base + static_cast<long long>(it.h) * it.pages;
   }
 
-  const int step = mode == kDirect ? kRWarps * cluster : kRWarps;
-  // The warp's pages: every step-th of the CTA's span (whole and direct form: of an item), counted by k.  A lane looks up one of
+  const int step = kRWarps * cluster;
+  // The warp's pages: every step-th of the CTA's span (direct form: of an item), counted by k.  A lane looks up one of
   // 32 of them: its block, place in the sequence and scales.
   struct PageInfo {
     int blk, page;
@@ -371,9 +368,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   };
   if (split) start();
 
-  const int rank = mode == kDirect ? static_cast<int>(blockIdx.x) % cluster : 0;
-  long long whole = mode == kDirect ? blockIdx.x / cluster : blockIdx.x;   // the item; whole form: items in turn
-  const long long items = static_cast<long long>(entries) * a.H;
+  const int rank = static_cast<int>(blockIdx.x) % cluster;       // in the cluster (split form: 0)
   for (;;) {
     int c0, c1;                                                  // pages of the item that are this CTA's
     bool complete;
@@ -389,12 +384,12 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
                      static_cast<int>(((prefix[entry] + static_cast<long long>(kItemCost) * some[entry]) * a.H +
                                        (it.h + 1LL) * (it.pages + kItemCost) - 1) / span), {0, 0}};
     } else {
-      if (whole >= items) break;
-      it.h = static_cast<int>(whole % a.H);
-      load_entry(static_cast<int>(entries - 1 - whole / a.H));   // the longest rows of a prompt first
+      const int item = static_cast<int>(blockIdx.x) / cluster;
+      it.h = item % a.H;
+      load_entry(entries - 1 - item / a.H);                      // the longest rows of a prompt first
       c0 = 0;
       c1 = it.pages;
-      complete = mode == kWhole || cluster == 1;
+      complete = cluster == 1;
       u0_first = kRWarps * rank;
       u1 = it.pages;
       start();
@@ -691,8 +686,8 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
           store_row(row, ch, acc, L);
         } else {
           // the pages' room serves the direct form (its pages have been read), the workspace the split one
-          float* p = mode == kDirect ? reinterpret_cast<float*>(ring) + row * (D + 4)
-                                     : parts + (static_cast<long long>(slot) * R + row) * (D + 4);
+          float* p = split ? parts + (static_cast<long long>(slot) * R + row) * (D + 4)
+                           : reinterpret_cast<float*>(ring) + row * (D + 4);
           *reinterpret_cast<float4*>(p + 4 + ch) = acc;
           if (ch == 0) {
             p[0] = M;
@@ -701,7 +696,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
         }
       }
       __syncthreads();
-      if (!complete && mode == kDirect) {
+      if (!complete && !split) {
         // ---- join the cluster's CTAs: each takes a share of the rows' channels ------------
         cluster_sync();
         for (int i = rank * 32 * kRWarps + tid; i < rows * D / 4; i += 32 * kRWarps * cluster) {
@@ -722,9 +717,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
         }
         cluster_sync();                                          // nobody leaves before its sums were read
       }
-    } else if (mode == kDirect && rank > 0) {
-      // (an empty sequence: the cluster's first CTA writes)
-    } else if (a.decode && !split && tid < 32) {                 // an empty sequence: zeros
+    } else if (a.decode && !split && rank == 0 && tid < 32) {    // an empty sequence: zeros
       const int dr = min(R, a.G - it.rb * R);
       for (int i = lane; i < dr * D; i += 32) {
         const long long at = (static_cast<long long>(it.b) * a.Hq + it.h * a.G + it.rb * R + i / D) * D + i % D;
@@ -732,11 +725,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
         else static_cast<unsigned short*>(a.out)[at] = 0;
       }
     }
-    if (mode == kDirect) break;
-    if (!split) {
-      whole += gridDim.x;
-      continue;
-    }
+    if (!split) break;
     u0 = item_at + c1;
     if (u0 >= u1) break;
     item_at += it.pages;
@@ -831,8 +820,6 @@ __global__ void __launch_bounds__(512) kv8_join_kernel(const __grid_constant__ K
 int rows_per_block(int T, int G, int d) { return static_cast<long long>(T) * G > 8 && d <= 128 ? 16 : 8; }
 int row_blocks(int T, int G, int R) { return static_cast<int>((static_cast<long long>(T) * G + R - 1) / R); }
 
-
-
 // launch_pdl with thread-block clusters.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster,
@@ -867,24 +854,21 @@ cudaError_t launch_t(const Kv8Attn& a, cudaStream_t s) {
   int cluster = 8;
   while (cluster > 1 && (items * cluster > slots || pages <= cluster / 2 * kRWarps)) cluster /= 2;
   const int most = cluster == 1 ? kDirectOne : 3 * items * cluster <= slots ? kDirectFew : kDirectMany;
-  const bool direct = pages <= static_cast<long long>(most) * cluster;
-  const Mode mode = direct ? kDirect : entries <= kMaxEntries ? kSplit : kWhole;
+  // the list counts pages in 32 bits
+  const bool split = pages > static_cast<long long>(most) * cluster && entries <= kMaxEntries && entries * pages <= 0x7FFFFFFFLL;
   const size_t fixed = 1024 + kRWarps * (Y::ST * Y::STAGE + sizeof(float) * R * D);
   const size_t list = sizeof(Kv8Seq) + 2 * sizeof(int);
-  const size_t smem = fixed + (mode == kSplit ? list * entries : 0);
+  const size_t smem = fixed + (split ? list * entries : 0);
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = smem_attr_once(kv8_rows_kernel<D, NT, F32>, static_cast<int>(fixed + list * kMaxEntries), configured);
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
   const long long blocks = static_cast<long long>(a.num_pages) * a.H;
   if (!kv8_block_map(&mk, a.kc, blocks, D) || !kv8_block_map(&mv, a.vc, blocks, D)) return cudaErrorInvalidValue;
-  if (mode != kSplit) {
-    const unsigned ctas = static_cast<unsigned>(direct ? items * cluster : items);
-    return launch_cluster(kv8_rows_kernel<D, NT, F32>, dim3(ctas), dim3(32 * kRWarps), smem, s, direct ? cluster : 1, a, mk, mv,
-                          static_cast<int>(nrb), static_cast<int>(mode), cluster);
-  }
-  e = launch_pdl(kv8_rows_kernel<D, NT, F32>, dim3(slots), dim3(32 * kRWarps), smem, s, a, mk, mv, static_cast<int>(nrb),
-                 static_cast<int>(mode), 1);
+  if (!split)
+    return launch_cluster(kv8_rows_kernel<D, NT, F32>, dim3(static_cast<unsigned>(items * cluster)), dim3(32 * kRWarps), smem, s,
+                          cluster, a, mk, mv, static_cast<int>(nrb), 0, cluster);
+  e = launch_pdl(kv8_rows_kernel<D, NT, F32>, dim3(slots), dim3(32 * kRWarps), smem, s, a, mk, mv, static_cast<int>(nrb), 1, 1);
   if (e != cudaSuccess) return e;
   return launch_pdl(kv8_join_kernel<D, R, F32>, dim3(slots), dim3(512), 0, s, a, slots);
 }

@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         const int slot = t0 == 0 && t1 == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 ? 0 : 1);
         publish(ItemMsg{1, it.b, h, it.qb, it.p0, it.rows, it.pmin, it.pmax, t1 - t0, slot, {0, 0}});
-        {                                              // the item's queries on their way to L2, token by token
+        if (a.G <= kTRows) {                           // the item's queries on their way to L2, token by token
           const unsigned first = static_cast<unsigned>(it.qb * kTRows) / a.G,
                          end = static_cast<unsigned>(it.qb * kTRows + it.rows - 1) / a.G + 1;
           for (unsigned t = first + lane; t < end; t += 32) {
@@ -986,13 +986,18 @@ __global__ void __launch_bounds__(256) kv8_tc_join_kernel(const __grid_constant_
 int query_blocks(int T, int G) { return static_cast<int>((static_cast<long long>(T) * G + kTRows - 1) / kTRows); }
 
 // CTAs of a call: one per SM, fewer where the list of tiles cannot be that long.
+long long tiles_of(int max_seq_len) { return (static_cast<long long>(max_seq_len) + kTTok - 1) / kTTok + 1; }
 int ctas_for(int B, int H, int nqb, int max_seq_len) {
-  const long long most = static_cast<long long>(B) * H * nqb * ((max_seq_len + kTTok - 1) / kTTok + 1);
+  const long long most = static_cast<long long>(B) * H * nqb * tiles_of(max_seq_len);
   const long long n = (most * (1 + kItemCost) + kMinSpan - 1) / kMinSpan;
   const int sms = kv8_sm_count();
   return static_cast<int>(n < sms ? (n < 1 ? 1 : n) : sms);
 }
-bool splits(int B, int nqb) { return static_cast<long long>(B) * nqb <= kMaxBlocks; }
+// The list holds so many blocks, and counts units in 32 bits.
+bool splits(int B, int nqb, int max_seq_len) {
+  const long long blocks = static_cast<long long>(B) * nqb;
+  return blocks <= kMaxBlocks && blocks * (tiles_of(max_seq_len) + kItemCost) <= 0x7FFFFFFFLL;
+}
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {        // from the driver, looked up once
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -1040,7 +1045,7 @@ bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale) {
 
 size_t kv8_tc_workspace(int B, int T, int G, int H, int max_seq_len, int d) {
   const int nqb = query_blocks(T, G);
-  if (!splits(B, nqb)) return 16;
+  if (!splits(B, nqb, max_seq_len)) return 16;
   return static_cast<size_t>(ctas_for(B, H, nqb, max_seq_len)) *
          (sizeof(TSplit) + 2 * sizeof(float) * static_cast<size_t>(kTRows) * (d + 4));
 }
@@ -1056,7 +1061,7 @@ cudaError_t launch_t(const Kv8Attn& a, cudaStream_t s) {
   cudaError_t e = smem_attr_once(kv8_tc_kernel<D>, smem_bytes<D>(), configured);
   if (e != cudaSuccess) return e;
   const int ctas = ctas_for(a.B, a.H, nqb, a.max_seq_len);
-  const bool split = splits(a.B, nqb);
+  const bool split = splits(a.B, nqb, a.max_seq_len);
   e = launch_pdl(kv8_tc_kernel<D>, dim3(ctas), dim3(kTThreads), smem_bytes<D>(), s, a, mk, mv, nqb, split ? 1 : 0);
   if (e != cudaSuccess || !split) return e;
   return launch_pdl(kv8_tc_join_kernel<D>, dim3(ctas, kTRows / 32), dim3(256), 0, s, a, ctas);

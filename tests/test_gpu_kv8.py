@@ -567,6 +567,92 @@ def test_causal_bad_pages_and_lengths():
     assert np.all(got[0, 70:] == -7) and np.all(got[1] == -7) and not np.any(np.all(got[0, :70] == -7, axis=-1))
 
 
+def test_many_heads_per_kv_head():
+    """More query heads per KV head than a block of query rows, in both forms, with windows and empty sequences."""
+    for dtype, d, hq in (("bf16", 64, 300), ("f32", 64, 37), ("bf16", 128, 260)):
+        _decode_case(np.random.default_rng(35), dtype, d, 1, hq, [20, 0, 333])
+        _decode_case(np.random.default_rng(35), dtype, d, 1, hq, [20, 0, 333], 30, 5)
+    _causal_case(np.random.default_rng(36), "bf16", 64, 1, 300, [100], 3)
+
+
+def test_bounds_on_the_length_far_above_the_lengths():
+    """max_seq_len up to the largest int: the work is not listed (its count passes 32 bits) but taken item by item."""
+    rng = np.random.default_rng(37)
+    lens = [int(x) for x in rng.integers(1, 300, 20)]
+    c = Cache(rng, 20 * 20, 2, 128, 20, 20)
+    for i, n in enumerate(lens):
+        c.clean(rng, i, range(n))
+    c.to_device()
+    q = values(rng, "bf16", 20, 8, 128)
+    for most in (320, 1 << 20, 2 ** 31 - 1):
+        _check(c, _attend(c, q, "bf16", False, lens, max_len=most), q, "bf16", False, lens)
+    q = values(rng, "bf16", 20, 9, 8, 128)
+    starts = [max(n - 9, 0) for n in lens]
+    new = [n - s for n, s in zip(lens, starts)]
+    for most in (320, 2 ** 31 - 1):
+        _check(c, _attend(c, q, "bf16", True, starts, new, max_len=most), q, "bf16", True, starts, new)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_output_on_a_16_byte_boundary(causal):
+    rng = np.random.default_rng(38)
+    c = Cache(rng, 20, 2, 128, 1, 20)
+    c.clean(rng, 0, range(310))
+    c.to_device()
+    q = values(rng, "bf16", 1, 300, 8, 128) if causal else values(rng, "bf16", 1, 8, 128)
+    room = torch.full((q.size + 16,), -7.0, dtype=torch.bfloat16, device=DEV)
+    out = room[8:8 + q.size].view(q.shape)
+    assert out.data_ptr() % 32 == 16
+    got = _attend(c, q, "bf16", causal, [10] if causal else [310], out=out)
+    _check(c, got, q, "bf16", causal, [10] if causal else [310], rows={(0, t) for t in (0, 1, 31, 127, 128, 299)})
+    assert bool((room[:8] == -7).all()) and bool((room[8 + q.size:] == -7).all())
+
+
+def test_pools_beyond_32_bit_offsets():
+    """Codes of 4.4 GB each: a sequence's pages lie at both ends and in the middle."""
+    rng = np.random.default_rng(39)
+    h, d, pages, n = 8, 128, 270000, 330
+    maxp = 21
+    small = Cache(rng, maxp, h, d, 1, maxp)
+    small.clean(rng, 0, range(n))
+    far = np.concatenate([np.arange(7), 131068 + np.arange(7), pages - 7 + np.arange(7)])     # where its pages really are
+    at = torch.from_numpy(far).to(DEV)
+    t = {k: torch.empty(pages, h, 16, d, dtype=torch.uint8, device=DEV) for k in ("kc", "vc")}
+    t.update({k: torch.empty(pages, h, dtype=torch.float32, device=DEV) for k in ("ks", "vs")})
+    for kind in "kv":
+        t[kind + "c"][at] = to_dev(small.codes[kind])
+        t[kind + "s"][at] = to_dev(small.scales[kind])
+    t["bt"] = to_dev(far[small.table].astype(np.int32))
+    small.dev = t
+    small.desc = tq.make_kv8_cache(t["kc"], t["vc"], t["ks"], t["vs"], t["bt"], maxp, pages, h)
+    q = values(rng, "bf16", 1, 32, d)
+    _check(small, _attend(small, q, "bf16", False, [n]), q, "bf16", False, [n])
+    q = values(rng, "bf16", 1, 40, 32, d)
+    _check(small, _attend(small, q, "bf16", True, [n - 40]), q, "bf16", True, [n - 40], rows={(0, 0), (0, 39)})
+    x = values(rng, "bf16", 1, n - 40, h, d)
+    dev = to_dev(x).to(torch.bfloat16)
+    tq.tq_kv8_append(ctx_for(d), small.desc, dev, dev, None, tq.TQ_BF16, 1, n - 40, 0, to_dev(np.asarray([0], np.int32)))
+    torch.cuda.synchronize()
+    for kind in "kv":
+        kv8.append(small.codes[kind], small.scales[kind], small.table[0], 0, x[0].astype(np.float64))
+        assert np.array_equal(t[kind + "c"][at].cpu().numpy(), small.codes[kind])
+        assert np.array_equal(t[kind + "s"][at].cpu().numpy(), small.scales[kind])
+
+
+def test_pages_shared_by_sequences_and_seen_twice():
+    rng = np.random.default_rng(43)
+    c = Cache(rng, 30, 2, 128, 3, 10, nan=False)
+    c.table = np.asarray([[0, 1, 2, 3, 4, 5, 6, 7, 8, 9], [0, 1, 2, 3, 10, 11, 4, 5, 0, 0], [7, 7, 7, 7, 7, 7, 7, 7, 7, 7]], np.int32)
+    for b in range(3):
+        c.clean(rng, b, range(160))
+    c.to_device()
+    for dtype in ("bf16", "f32"):
+        q = values(rng, dtype, 3, 8, 128)
+        _check(c, _attend(c, q, dtype, False, [160, 155, 130]), q, dtype, False, [160, 155, 130])
+        q = values(rng, dtype, 3, 20, 8, 128)
+        _check(c, _attend(c, q, dtype, True, [140, 100, 3]), q, dtype, True, [140, 100, 3])
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
@@ -633,6 +719,79 @@ def test_prompt_then_steps_then_drafts(dtype, d, h, hq, window, sinks):
 
 def test_prompt_then_steps_then_drafts_captured():
     _steps("bf16", 128, 2, 8, 0, 0, graph=True)
+
+
+def test_captured_graphs_share_a_workspace():
+    """A decode step and a drafted step, captured once with one workspace between them and replayed in turn while the
+    lengths on the device grow, with eager calls among them: what each would give alone."""
+    rng = np.random.default_rng(44)
+    h, hq, d, maxp = 2, 16, 128, 400
+    c = Cache(rng, 2 * maxp, h, d, 2, maxp)
+    for b in range(2):
+        c.clean(rng, b, range(16 * maxp))
+    c.to_device()
+    ctx, dt = ctx_for(d), torch.bfloat16
+    q = {1: values(rng, "bf16", 2, 1, hq, d), 4: values(rng, "bf16", 2, 4, hq, d)}
+    dev = {t: to_dev(x).to(dt) for t, x in q.items()}
+    out = {t: torch.empty(2, t, hq, d, dtype=dt, device=DEV) for t in q}
+    n = max(tq.tq_kv8_workspace_size(ctx, 2, t, hq, h, 16 * maxp) for t in q)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+    lens, starts = (torch.zeros(2, dtype=torch.int32, device=DEV) for _ in range(2))
+
+    def call(t, st):
+        if t == 1:
+            tq.tq_kv8_decode_attention(ctx, c.desc, dev[1], tq.TQ_BF16, 2, hq, lens, 16 * maxp, 0, 0, d ** -0.5, out[1], ws, n, st)
+        else:
+            tq.tq_kv8_causal_attention(ctx, c.desc, dev[4], tq.TQ_BF16, 2, 4, hq, starts, None, 16 * maxp, 0, 0, d ** -0.5,
+                                       out[4], ws, n, st)
+
+    graphs, stream = {}, torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for t in q:
+        graphs[t] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[t], stream=stream):
+            call(t, torch.cuda.current_stream())
+    for now in ([6000, 3], [1, 5999], [40, 77], [6070, 6060]):
+        lens.copy_(to_dev(np.asarray(now, np.int32)))
+        starts.copy_(to_dev(np.asarray(now, np.int32)))
+        for _ in range(3):
+            graphs[1].replay()
+            graphs[4].replay()
+        call(1, torch.cuda.current_stream())
+        graphs[4].replay()
+        graphs[1].replay()
+        call(4, torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        _check(c, out[1].float().cpu().numpy(), q[1], "bf16", True, [x - 1 for x in now])
+        _check(c, out[4].float().cpu().numpy(), q[4], "bf16", True, now)
+    assert tq.tq_check_device_status(ctx) == 0
+
+
+@pytest.mark.parametrize("dtype,d,h,hq", [("bf16", 128, 2, 8), ("bf16", 64, 1, 32), ("f32", 128, 2, 8)])
+def test_steps_without_a_wait_between_them(dtype, d, h, hq):
+    """Forty steps of append and attention enqueued one behind the other: each sees the tokens of those before it."""
+    rng = np.random.default_rng(45)
+    n, dt, code = 40, DT[dtype][0], DT[dtype][1]
+    c = Cache(rng, 4, h, d, 1, 4, nan=False)
+    desc = c.to_device()
+    x = {k: values(rng, dtype, n, 1, 1, hh, d) for k, hh in (("k", h), ("v", h), ("q", hq))}
+    dev = {k: to_dev(v).to(dt) for k, v in x.items()}
+    q_rot = torch.empty(n, 1, 1, hq, d, dtype=dt, device=DEV)
+    out = torch.empty(n, 1, hq, d, dtype=dt, device=DEV)
+    at = torch.arange(n + 1, dtype=torch.int32, device=DEV)
+    size = tq.tq_kv8_workspace_size(ctx_for(d), 1, 1, hq, h, 64)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    for i in range(n):
+        tq.tq_kv8_append(ctx_for(d), desc, dev["k"][i], dev["v"][i], dev["q"][i], code, 1, 1, hq, at[i:i + 1], None, None, q_rot[i])
+        tq.tq_kv8_decode_attention(ctx_for(d), desc, q_rot[i], code, 1, hq, at[i + 1:i + 2], 64, 0, 0, d ** -0.5, out[i], ws, size)
+    torch.cuda.synchronize()
+    got = out.float().cpu().numpy()
+    for i in range(n):
+        for kind in "kv":
+            kv8.append(c.codes[kind], c.scales[kind], c.table[0], i, x[kind][i, 0].astype(np.float64))
+        _check(c, got[i], x["q"][i, 0], dtype, False, [i + 1])
+    c.same_as_device()
 
 
 def test_results_repeat_bit_for_bit():
