@@ -23,6 +23,9 @@
 // overlaid by its weights), O of A and B, 512 columns.  Warps 0-3 and 4-7: the
 // softmax of A and B (thread = row), which also split the queries and write the
 // results; 8-11: values to fp16; 12: items, pages and TMA; 13: MMA issue.
+// An item of at most 128 rows (drafted tokens, decode with many heads per KV head) has
+// its rows in both halves: A takes the even tiles, B the odd ones, and A adds B's sums
+// to its own at the item's end, from B's columns of the same lanes.
 // Every wait is bounded; a wait that gives up sets the device error word.
 
 #include "tq_kv8.h"
@@ -45,7 +48,7 @@ constexpr int kTRows = 256;               // query rows per item
 constexpr int kTTok = 128;                // tokens per tile
 constexpr int kTPg = kTTok / kPage;       // pages per tile
 constexpr int kTThreads = 512;
-constexpr int kKSt = 3, kVSt = 2;         // raw K and V stages
+constexpr int kKSt = 3, kVSt = 3;         // raw K and V stages
 constexpr int kDescs = 8;
 constexpr float kMNone = -1.0e30f;
 // Weights are 2^(kLift + score - M).  M is set kHead above the largest score met, so that it seldom moves again: the
@@ -65,7 +68,15 @@ struct TileDesc {                         // one tile of the stream, by page
   int full, pad[3];                       // every row of the block sees every token
 };
 
-// Shared memory, from a 1024-byte boundary, by head dimension.
+constexpr int kDoneRing = 8;
+enum Bar {
+  bKFull = 0, bVFull = bKFull + kKSt, bVEmpty = bVFull + kVSt, bReady = bVEmpty + kVSt, bSFull = bReady + 2,
+  bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2, bItem = bQReady + 2, bItemFree = bItem + kDescs, bDesc = bItemFree + kDescs,
+  bDone = bDesc + kDescs, bJoin = bDone + kDoneRing, bOFree, bDrain, bCount
+};
+
+// Shared memory by head dimension.  It has no room to be moved up to a 1024-byte boundary (the swizzles' period): the
+// kernel's only shared memory starts on one, and the kernel checks that.
 template <int D>
 struct TG {
   static constexpr int KT = kTTok * D, VT = 2 * KT;    // a tile's codes, and as fp16
@@ -78,6 +89,7 @@ struct TG {
   static constexpr int DESC = V + 2 * VT;
   static constexpr int ITEM = DESC + kDescs * static_cast<int>(sizeof(TileDesc));
   static constexpr int BAR = ITEM + kDescs * 48;
+  static constexpr int JOIN = BAR + 8 * ((bCount + 1) & ~1);     // half B's (M, l) of 128 rows
   // Piece c (sixteen channels) of part hi (0) or lo (1) of a row, in rows of 128 bytes with the 128-byte swizzle: at
   // d = 128 the parts have a tile each, at d = 64 a row holds both.
   __device__ static __forceinline__ uint32_t qpos(int row, int c, int part) {
@@ -89,16 +101,10 @@ struct TG {
     return static_cast<uint32_t>(t * D + ((c ^ (D == 128 ? t & 7 : (t >> 1) & 3)) << 4));
   }
 };
-constexpr int kDoneRing = 4;
-enum Bar {
-  bKFull = 0, bVFull = bKFull + kKSt, bVEmpty = bVFull + kVSt, bReady = bVEmpty + kVSt, bSFull = bReady + 2,
-  bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2, bItem = bQReady + 2, bItemFree = bItem + kDescs, bDesc = bItemFree + kDescs,
-  bDone = bDesc + kDescs, bDrain = bDone + kDoneRing, bCount
-};
 template <int D>
-constexpr int tmem_at() { return TG<D>::BAR + 8 * bCount; }
+constexpr int tmem_at() { return TG<D>::JOIN + 1024; }
 template <int D>
-constexpr int smem_bytes() { return tmem_at<D>() + 16 + 1024; }
+constexpr int smem_bytes() { return tmem_at<D>() + 16; }
 static_assert(smem_bytes<128>() <= 232448, "shared memory per block");
 static_assert(sizeof(TileDesc) % 16 == 0, "items behind the descriptors");
 // tensor-memory columns of half X
@@ -312,12 +318,21 @@ __global__ void __launch_bounds__(kTThreads, 1)
                   const __grid_constant__ CUtensorMap mv, int nqb, int split) {
   using L = TG<D>;
   extern __shared__ __align__(1024) unsigned char sm_raw[];
-  unsigned char* sm = sm_raw + ((0u - su32(sm_raw)) & 1023u);
+  unsigned char* sm = sm_raw;
   const uint32_t sb = su32(sm);
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   auto bar = [&](int i) { return sb + L::BAR + 8u * static_cast<uint32_t>(i); };
   TileDesc* descs = reinterpret_cast<TileDesc*>(sm + L::DESC);
   ItemMsg* item_ring = reinterpret_cast<ItemMsg*>(sm + L::ITEM);
+  TSplit* splits = reinterpret_cast<TSplit*>(a.part);              // one per CTA, then the partials' slots
+  if (sb & 1023u) {
+    pdl_wait();
+    if (tid == 0) {
+      atomicOr(a.err, kErrLayout);
+      if (split) splits[blockIdx.x].valid = 0;
+    }
+    return;
+  }
 
   if (tid == 0) {
     for (int i = 0; i < kKSt; ++i) bar_init(bar(bKFull + i), 1);
@@ -333,6 +348,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
       bar_init(bar(bQReady + i), 4);
     }
     for (int i = 0; i < kDoneRing; ++i) bar_init(bar(bDone + i), 1);
+    bar_init(bar(bJoin), 4);
+    bar_init(bar(bOFree), 4);
     for (int i = 0; i < kDescs; ++i) {
       bar_init(bar(bItem + i), 1);
       bar_init(bar(bItemFree + i), 13);                // softmax, conversion and MMA warps
@@ -404,7 +421,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + tmem_at<D>());
-  TSplit* splits = reinterpret_cast<TSplit*>(a.part);              // one per CTA, then the partials' slots
   float* parts = a.part + static_cast<size_t>(gridDim.x) * (sizeof(TSplit) / sizeof(float));
   bool failed = false;
   // a warp's wait for phase `phase` of a barrier; once one gave up, every later one returns at once
@@ -430,7 +446,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const uint32_t ts = trow + col_s(X), to = trow + col_o(X);
     const float sgn = a.scale_log2 < 0.0f ? -1.0f : 1.0f;
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // whole sectors per store
-    int seq = 0, nS = 0, nO = 0;                       // tiles seen, phases of S and of the final O
+    int seq = 0, nS = 0, nO = 0, nJ = 0;               // tiles seen, phases of S, of the final O and of the halves' join
+    float2* join = reinterpret_cast<float2*>(sm + L::JOIN);
     // The row of an item that is this thread's.
     struct Row {
       bool live;
@@ -438,13 +455,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
       long long at;                                    // its element of q and out
       float rowf;
     };
-    auto mine = [&](const ItemMsg& x) { return x.valid && 128 * X < x.rows; };
+    auto mine = [&](const ItemMsg& x) { return x.valid && (X == 0 || x.rows > 128 || x.ntile > 1); };
     // Loads the row and leaves it in shared memory as two e4m3 parts, scaled so that its largest value lies in
     // [128, 256).  The item before has no score MMA left: its last scores were read.
     auto queries = [&](const ItemMsg& x) {
       Row w;
-      const unsigned gr = static_cast<unsigned>(x.qb * kTRows + 128 * X + r), tok = gr / static_cast<unsigned>(a.G);
-      w.live = 128 * X + r < x.rows;
+      const int rx = x.rows > 128 ? 128 * X + r : r;
+      const unsigned gr = static_cast<unsigned>(x.qb * kTRows + rx), tok = gr / static_cast<unsigned>(a.G);
+      w.live = rx < x.rows;
       w.p = w.live ? x.p0 + static_cast<int>(tok) : -1;
       w.at = ((static_cast<long long>(x.b) * a.T + tok) * a.Hq + x.h * a.G + (gr - tok * a.G)) * D;
       // The warp's 32 rows, D / 8 lanes per row (a lane per row would ask for 32 lines with each load); the raw 16-byte
@@ -509,7 +527,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     if (mine(it)) row = queries(it);
     for (int n = 0; it.valid; ++n) {
       const int ntile = it.ntile;
-      if (!mine(it)) {                                 // this half is empty
+      if (!mine(it)) {                                 // one tile of at most 128 rows: nothing for B
         seq += ntile;
         it = next_item(n + 1);
         if (mine(it)) row = queries(it);
@@ -517,8 +535,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
       }
       const float rowf = row.rowf;
       const int p = row.p;
+      const bool turns = it.rows <= 128;               // the halves take the tiles in turn
+      const int t0 = turns ? X : 0, dt = turns ? 2 : 1, seq0 = seq;
       float m = kMNone, l = 0.0f;
-      for (int t = 0; t < ntile; ++t, ++seq) {
+      seq += t0;
+      for (int t = t0; t < ntile; t += dt, seq += dt) {
         if (!wait(bDesc + seq % kDescs, seq / kDescs) || !wait(bSFull + X, nS)) break;
         ++nS;
         tc_after();
@@ -528,7 +549,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         // The tile as it mostly is: every token seen and no score far above the maximum so far.  The weights by the
         // old maximum tell by themselves: a page's sum below kFull means that each fits fp16.  No maximum is taken.
         bool done = false;
-        if (d.full && t > 0) {
+        if (d.full && t > t0) {
           float x[kTTok];
           uint32_t w[kTTok / 2];
           tld32x4(ts, x);
@@ -596,7 +617,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               m = mx + kHead;
               l *= alpha;
             }
-            if (t > 0) {                               // O of the tiles before (their MMAs have run: S came after)
+            if (t > t0) {                              // O of the tiles before (their MMAs have run: S came after)
 #pragma unroll 1
               for (int c = 0; c < D / 16; ++c) {
                 float o[16];
@@ -639,6 +660,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (lane == 0) bar_arrive(bar(bPFull + X));
       }
       if (failed) break;
+      seq = seq0 + ntile;
       // the next item's queries first: its scores then run beside what is left of this one
       const ItemMsg done_item = it;
       const Row done_row = row;
@@ -648,8 +670,41 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (!wait(bODone + X, nO)) break;
       ++nO;
       tc_after();
+      const bool joins = turns && ntile > 1;
+      if (joins) {
+        if (X) {
+          join[r] = make_float2(m, l);
+          tc_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(bar(bJoin));
+          if (!wait(bOFree, nJ++)) break;              // A has read this half's sums: the next item may overwrite them
+          tc_after();
+          continue;
+        }
+        if (!wait(bJoin, nJ++)) break;
+        tc_after();
+        const float2 other = join[r];
+        const float mj = fmaxf(m, other.x);
+        const float fa = ex2(m - mj), fb = ex2(other.x - mj);
+        m = mj;
+        l = fa * l + fb * other.y;
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          float o[16], o2[16];
+          uint32_t u[16];
+          tld16(to + 16u * c, o);
+          tld16(trow + col_o(1) + 16u * c, o2);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(fa * o[k] + fb * o2[k]);
+          tst16(to + 16u * c, u);
+        }
+        tst_wait();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(bOFree));
+      }
       const float inv = l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
-      float* part = parts + (static_cast<long long>(done_item.slot) * kTRows + 128 * X + r) * L::PART;
+      float* part = parts + (static_cast<long long>(done_item.slot) * kTRows + (turns ? 0 : 128 * X) + r) * L::PART;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
@@ -684,11 +739,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
     // ---- values to fp16: thread = token of the tile ----------------------------------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int t = tid - 256, pg = t >> 4;
-    int seq = 0;
+    int seq = 0, keys = 0;                             // tiles, and how many tiles' keys are there
     for (int n = 0;; ++n) {
       const ItemMsg it = next_item(n);
       if (!it.valid) break;
-      const int ntile = it.ntile;
+      const int ntile = it.ntile, ahead = it.rows <= 128 ? 2 : 1, end = seq + ntile;
       for (int i = 0; i < ntile; ++i, ++seq) {
         if (!wait(bVFull + seq % kVSt, seq / kVSt)) break;
         if (seq >= 2 && !wait(bDone + (seq - 2) % kDoneRing, (seq - 2) / kDoneRing)) break;
@@ -714,8 +769,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
         fence_async_smem();
         __syncwarp();
         if (lane == 0) bar_arrive(bar(bVEmpty + seq % kVSt));
-        // the issuing warp's one wait for a tile covers the next tile's keys
-        if (i + 1 < ntile && !wait(bKFull + (seq + 1) % kKSt, (seq + 1) / kKSt)) break;
+        // the issuing warp's one wait for a tile covers the keys of the scores that it issues behind the tile
+        for (; keys <= seq + ahead && keys < end && !failed; ++keys) (void)wait(bKFull + keys % kKSt, keys / kKSt);
+        if (failed) break;
         if (lane == 0) bar_arrive(bar(bReady + (seq & 1)));
       }
       if (failed) break;
@@ -725,6 +781,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
     if (warp == 12) {
       // ---- items, pages, TMA ----------------------------------------------------------------
       int seq = 0, n = 0, nk = 0, nv = 0;              // tiles, and copies issued
+      static_assert(kKSt == 3, "the tiles whose keys are still there");
+      int free0 = 0, free1 = 0, free2 = 0;             // the steps after which the keys of the last three tiles are read
       auto publish = [&](const ItemMsg& x) {
         if (n >= kDescs) (void)wait(bItemFree + n % kDescs, n / kDescs - 1);   // every warp has taken the one before
         if (lane == 0) {
@@ -771,6 +829,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q), "r"(2 * D * a.G));
           }
         }
+        const int ahead = it.rows <= 128 ? 2 : 1;      // a tile's scores are issued so many steps before its values
         const int c0 = t0 * kTPg, c1 = min(it.pages, t1 * kTPg);
         const int* table = a.bt + static_cast<long long>(it.b) * a.maxp;
         // lane i holds page i of four tiles (lanes 8k .. 8k + 7: tile k); the next four tiles' ids and scales are on
@@ -804,7 +863,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const bool on = (lane >> 3) == k;
             const int pg = lane & 7;
             const uint32_t bytes = static_cast<uint32_t>(__popc((there4 >> (8 * k)) & 0xFFu)) * kPage * D;
-            if (seq >= kKSt && !wait(bDone + (seq - kKSt) % kDoneRing, (seq - kKSt) / kDoneRing)) break;
+            if (seq >= kKSt && !wait(bDone + free0 % kDoneRing, free0 / kDoneRing)) break;
+            free0 = free1, free1 = free2;
+            free2 = c4 + k * kTPg >= c0 + ahead * kTPg ? seq - ahead : seq;
             TileDesc& d = descs[seq % kDescs];
             if (on) {
               d.fac[pg] = fabsf(a.scale_log2) * cur.ks;
@@ -885,10 +946,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (!ready(bKFull + s % kKSt, s / kKSt) || !ready(bQReady, nq0++)) return false;
         tc_after();
         scores(0, s);
-        if (two) {
+        if (two || tiles > 1) {
+          const int s1 = two ? s : s + 1;
+          if (!two && !ready(bKFull + s1 % kKSt, s1 / kKSt)) return false;
           if (!ready(bQReady + 1, nq1++)) return false;
           tc_after();
-          scores(1, s);
+          scores(1, s1);
         }
         return true;
       };
@@ -901,7 +964,17 @@ __global__ void __launch_bounds__(kTThreads, 1)
       while (ok && open) {
         const int my_tiles = tiles;
         const bool my_two = two;
-        for (int t = 0; t < my_tiles; ++t, ++seq) {
+        for (int t = 0; t < my_tiles && !my_two; ++t, ++seq) {   // the halves' tiles in turn
+          const uint32_t X = t & 1;
+          ok = ready(bReady + (seq & 1), seq >> 1) && ready(bPFull + X, X ? np1++ : np0++);
+          if (!ok) break;
+          tc_after();
+          values(X, seq, t < 2);
+          if (t + 2 < my_tiles) scores(X, seq + 2);
+          else mma_commit_warp(bar(bODone + X));
+          mma_commit_warp(bar(bDone + seq % kDoneRing));
+        }
+        for (int t = 0; t < my_tiles && my_two; ++t, ++seq) {
           const bool last = t == my_tiles - 1;
           ok = ready(bReady + (seq & 1), seq >> 1) && ready(bPFull, np0++);
           if (!ok) break;
@@ -909,14 +982,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
           values(0, seq, t == 0);
           if (last) mma_commit_warp(bar(bODone));
           else scores(0, seq + 1);
-          if (my_two) {
-            ok = ready(bPFull + 1, np1++);
-            if (!ok) break;
-            tc_after();
-            values(1, seq, t == 0);
-            if (last) mma_commit_warp(bar(bODone + 1));
-            else scores(1, seq + 1);
-          }
+          ok = ready(bPFull + 1, np1++);
+          if (!ok) break;
+          tc_after();
+          values(1, seq, t == 0);
+          if (last) mma_commit_warp(bar(bODone + 1));
+          else scores(1, seq + 1);
           mma_commit_warp(bar(bDone + seq % kDoneRing));   // the tile's keys and values have been read
         }
         if (!ok) break;
