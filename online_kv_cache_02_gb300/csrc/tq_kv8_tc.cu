@@ -22,7 +22,9 @@
 // runs, the tensor cores work on the other.  Tensor memory: S of A and B (each
 // overlaid by its weights), O of A and B, 512 columns.  Warps 0-3 and 4-7: the
 // softmax of A and B (thread = row), which also split the queries and write the
-// results; 8-11: values to fp16; 12: items, pages and TMA; 13: MMA issue.
+// results; 8-11: values to fp16; 12: items, pages and the keys' copies; 13: MMA issue;
+// 14: the values' copies (a copy per page costs its warp about 100 cycles, a tile of
+// keys and values more than the MMAs of twenty rows); 15: queries to L2.
 // An item of at most 128 rows (drafted tokens, decode with many heads per KV head) has
 // its rows in both halves: A takes the even tiles, B the odd ones, and A adds B's sums
 // to its own at the item's end, from B's columns of the same lanes.
@@ -49,7 +51,7 @@ constexpr int kTTok = 128;                // tokens per tile
 constexpr int kTPg = kTTok / kPage;       // pages per tile
 constexpr int kTThreads = 512;
 constexpr int kKSt = 3, kVSt = 3;         // raw K and V stages
-constexpr int kDescs = 8;
+constexpr int kDescs = 8, kItems = 4;     // tiles and items announced ahead
 constexpr float kMNone = -1.0e30f;
 // Weights are 2^(kLift + score - M).  M is set kHead above the largest score met, so that it seldom moves again: the
 // largest weight is then 2^3, and fp16 keeps 11 bits down to 2^-17 of it.  M moves when a page's 16 weights sum to more
@@ -65,13 +67,14 @@ struct TileDesc {                         // one tile of the stream, by page
   float ev[kTPg];                         // value exponent
   float vinv[kTPg];                       // 2^-ev
   int j0[kTPg];                           // first position
+  int blk[kTPg];                          // block of the cache; -1: not there
   int full, pad[3];                       // every row of the block sees every token
 };
 
 constexpr int kDoneRing = 8;
 enum Bar {
   bKFull = 0, bVFull = bKFull + kKSt, bVEmpty = bVFull + kVSt, bReady = bVEmpty + kVSt, bSFull = bReady + 2,
-  bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2, bItem = bQReady + 2, bItemFree = bItem + kDescs, bDesc = bItemFree + kDescs,
+  bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2, bItem = bQReady + 2, bItemFree = bItem + kItems, bDesc = bItemFree + kItems,
   bDone = bDesc + kDescs, bJoin = bDone + kDoneRing, bOFree, bDrain, bCount
 };
 
@@ -88,7 +91,7 @@ struct TG {
   static constexpr int V = VR + kVSt * KT;             // [buffer][64-channel blocks][128 tokens][128 B]
   static constexpr int DESC = V + 2 * VT;
   static constexpr int ITEM = DESC + kDescs * static_cast<int>(sizeof(TileDesc));
-  static constexpr int BAR = ITEM + kDescs * 48;
+  static constexpr int BAR = ITEM + kItems * 48;
   static constexpr int JOIN = BAR + 8 * ((bCount + 1) & ~1);     // half B's (M, l) of 128 rows
   // Piece c (sixteen channels) of part hi (0) or lo (1) of a row, in rows of 128 bytes with the 128-byte swizzle: at
   // d = 128 the parts have a tile each, at d = 64 a row holds both.
@@ -350,10 +353,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
     for (int i = 0; i < kDoneRing; ++i) bar_init(bar(bDone + i), 1);
     bar_init(bar(bJoin), 4);
     bar_init(bar(bOFree), 4);
-    for (int i = 0; i < kDescs; ++i) {
+    for (int i = 0; i < kDescs; ++i) bar_init(bar(bDesc + i), 1);
+    for (int i = 0; i < kItems; ++i) {
       bar_init(bar(bItem + i), 1);
-      bar_init(bar(bItemFree + i), 13);                // softmax, conversion and MMA warps
-      bar_init(bar(bDesc + i), 1);
+      bar_init(bar(bItemFree + i), 15);                // every warp but the one that announces
     }
     bar_init(bar(bDrain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -432,9 +435,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
   // the n-th item of this CTA, from the ring
   auto next_item = [&](int n) {
     ItemMsg x{};
-    if (wait(bItem + n % kDescs, n / kDescs)) x = item_ring[n % kDescs];
+    if (wait(bItem + n % kItems, n / kItems)) x = item_ring[n % kItems];
     __syncwarp();
-    if (lane == 0) bar_arrive(bar(bItemFree + n % kDescs));
+    if (lane == 0) bar_arrive(bar(bItemFree + n % kItems));
     return x;
   };
 
@@ -779,15 +782,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 12) {
-      // ---- items, pages, TMA ----------------------------------------------------------------
-      int seq = 0, n = 0, nk = 0, nv = 0;              // tiles, and copies issued
+      // ---- items, pages, keys -----------------------------------------------------------------
+      int seq = 0, n = 0, nk = 0;                      // tiles, items, and tiles whose copies were issued
       static_assert(kKSt == 3, "the tiles whose keys are still there");
       int free0 = 0, free1 = 0, free2 = 0;             // the steps after which the keys of the last three tiles are read
       auto publish = [&](const ItemMsg& x) {
-        if (n >= kDescs) (void)wait(bItemFree + n % kDescs, n / kDescs - 1);   // every warp has taken the one before
+        if (n >= kItems) (void)wait(bItemFree + n % kItems, n / kItems - 1);   // every warp has taken the one before
         if (lane == 0) {
-          item_ring[n % kDescs] = x;
-          bar_arrive(bar(bItem + n % kDescs));
+          item_ring[n % kItems] = x;
+          bar_arrive(bar(bItem + n % kItems));
         }
         ++n;
       };
@@ -820,15 +823,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         const int slot = t0 == 0 && t1 == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 ? 0 : 1);
         publish(ItemMsg{1, it.b, h, it.qb, it.p0, it.rows, it.pmin, it.pmax, t1 - t0, slot, {0, 0}});
-        if (a.G <= kTRows) {                           // the item's queries on their way to L2, token by token
-          const unsigned first = static_cast<unsigned>(it.qb * kTRows) / a.G,
-                         end = static_cast<unsigned>(it.qb * kTRows + it.rows - 1) / a.G + 1;
-          for (unsigned t = first + lane; t < end; t += 32) {
-            const char* q = static_cast<const char*>(a.q) +
-                            2 * ((static_cast<long long>(it.b) * a.T + t) * a.Hq + h * a.G) * D;
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(q), "r"(2 * D * a.G));
-          }
-        }
         const int ahead = it.rows <= 128 ? 2 : 1;      // a tile's scores are issued so many steps before its values
         const int c0 = t0 * kTPg, c1 = min(it.pages, t1 * kTPg);
         const int* table = a.bt + static_cast<long long>(it.b) * a.maxp;
@@ -872,6 +866,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               d.ev[pg] = static_cast<float>(cur.ev);
               d.vinv[pg] = exp2f(static_cast<float>(-cur.ev));
               d.j0[pg] = cur.j0;
+              d.blk[pg] = cur.blk;
               if (pg == 0) d.full = ((seen4 >> (8 * k)) & 0xFFu) == 0xFFu ? 1 : 0;
             }
             __syncwarp();
@@ -884,15 +879,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
             ++nk;
             if (on && cur.blk >= 0)
               tma_block(sb + L::K + (seq % kKSt) * L::KT + pg * kPage * D, &mk, cur.blk, bar(bKFull + seq % kKSt));
-            if (seq >= kVSt && !wait(bVEmpty + seq % kVSt, seq / kVSt - 1)) break;
-            if (lane == 0) {
-              if (bytes) bar_arrive_tx(bar(bVFull + seq % kVSt), bytes);
-              else bar_arrive(bar(bVFull + seq % kVSt));
-            }
-            __syncwarp();
-            ++nv;
-            if (on && cur.blk >= 0)
-              tma_block(sb + L::VR + (seq % kVSt) * L::KT + pg * kPage * D, &mv, cur.blk, bar(bVFull + seq % kVSt));
           }
           cur = nxt;
         }
@@ -913,7 +899,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // copies still in flight land before the CTA ends
       bool f2 = false;
       for (int s = nk >= kKSt ? nk - kKSt : 0; s < nk; ++s) (void)bar_wait(bar(bKFull + s % kKSt), (s / kKSt) & 1, f2);
-      for (int s = nv >= kVSt ? nv - kVSt : 0; s < nv; ++s) (void)bar_wait(bar(bVFull + s % kVSt), (s / kVSt) & 1, f2);
     } else if (warp == 13) {
       // ---- MMA issue, the warp converged: O += w V of a tile and the next tile's scores, half A, then half B.  The
       // order is strict: left to mix, both halves' MMAs end together, both softmaxes run together and neither overlaps
@@ -1003,6 +988,43 @@ __global__ void __launch_bounds__(kTThreads, 1)
       bool f2 = false;
       (void)bar_wait(bar(bDrain), 0, f2);
       __syncwarp();
+    } else if (warp == 14) {
+      // ---- values ---------------------------------------------------------------------------
+      int seq = 0;
+      for (int n = 0;; ++n) {
+        const ItemMsg it = next_item(n);
+        if (!it.valid) break;
+        const int ntile = it.ntile;
+        for (int i = 0; i < ntile; ++i, ++seq) {
+          if (!wait(bDesc + seq % kDescs, seq / kDescs)) break;
+          const int blk = lane < kTPg ? descs[seq % kDescs].blk[lane] : -1;
+          if (seq >= kVSt && !wait(bVEmpty + seq % kVSt, seq / kVSt - 1)) break;
+          const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, blk >= 0))) * kPage * D;
+          if (lane == 0) {
+            if (bytes) bar_arrive_tx(bar(bVFull + seq % kVSt), bytes);
+            else bar_arrive(bar(bVFull + seq % kVSt));
+          }
+          __syncwarp();
+          if (blk >= 0) tma_block(sb + L::VR + (seq % kVSt) * L::KT + lane * kPage * D, &mv, blk, bar(bVFull + seq % kVSt));
+        }
+        if (failed) break;
+      }
+      // copies still in flight land before the CTA ends
+      bool f2 = false;
+      for (int s = seq >= kVSt ? seq - kVSt : 0; s < seq; ++s) (void)bar_wait(bar(bVFull + s % kVSt), (s / kVSt) & 1, f2);
+    } else {
+      // ---- an item's queries on their way to L2 as soon as it is known ------------------------
+      for (int n = 0;; ++n) {
+        const ItemMsg it = next_item(n);
+        if (!it.valid) break;
+        constexpr int kLines = D / 64;                 // 128-byte lines of a row
+        for (int i = lane; i < it.rows * kLines; i += 32) {
+          const unsigned gr = static_cast<unsigned>(it.qb * kTRows + i / kLines), tok = gr / static_cast<unsigned>(a.G);
+          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
+                                   ((static_cast<long long>(it.b) * a.T + tok) * a.Hq + it.h * a.G + (gr - tok * a.G)) * D;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64 * (i % kLines)));
+        }
+      }
     }
   }
   if (failed && lane == 0) atomicOr(a.err, kErrTimeout);
