@@ -29,6 +29,18 @@
 // its rows in both halves: A takes the even tiles, B the odd ones, and A adds B's sums
 // to its own at the item's end, from B's columns of the same lanes.
 // Every wait is bounded; a wait that gives up sets the device error word.
+//
+// Bound by the tensor cores in the long run of tiles: 2,048 of about 2,200 cycles a
+// tile of 256 rows (two e4m3 products at the rate of one fp16 product, then one fp16
+// product).  Measured, bf16, d = 128, 32 / 8 heads: a prompt of 8,192 tokens 395 us,
+// 1.39 PFLOP/s, 72% of a large bf16 library product's rate; 2 x 1,024 tokens behind
+// 15,000 to 30,000, 475 us, 77%; three prompts of up to 4,000 in a window of 1,024
+// (28 / 4 heads) 165 us, 43%, where an item of nine tiles pays for its queries and its
+// result with the time of four; five drafted tokens of 16 sequences of 2,000 to 8,000,
+// 53 us, 46% of a copy's rate (MMAs of 128 rows of which 20 are there).
+// Slower, each by itself: 64-token tiles in two buffers, sixteen softmax warps, two
+// issuing warps, the queries' copies beside the last tile (from the softmax warps or
+// a warp of their own: code in the tile loop, or a copy slower than four warps').
 
 #include "tq_kv8.h"
 #include "tq_tc.cuh"
@@ -372,7 +384,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
       if (kv8_seq(a, b).n > 0) continue;
       uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(b) * a.Hq * D);
-      for (int i = tid; i < a.Hq * (D / 8); i += kTThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (long long i = tid; i < static_cast<long long>(a.Hq) * (D / 8); i += kTThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
   // the list, cut into equal spans: units before each block (of one head), by a scan in the queries' room
@@ -1131,6 +1143,9 @@ bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d)
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// More rows than a block of the mma.sync form has.  64 sequences of 2,000 to 8,000 tokens: 16 rows 153 us there and 158
+// here (d = 64: 127 and 133), 20 rows 161 us here, two blocks a head there.  A larger scale would make the query's
+// rounding to two e4m3 parts count.
 bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale) {
   return (d == 64 || d == 128) && !f32 && static_cast<long long>(T) * G > 16 && softmax_scale != 0.0f &&
          std::fabs(static_cast<double>(softmax_scale)) <= (1.0 + 1e-6) / std::sqrt(static_cast<double>(d));
