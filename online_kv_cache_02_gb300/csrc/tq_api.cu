@@ -1072,7 +1072,7 @@ extern "C" tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_n
     return TQ_ERR_INVALID_ARG;
   if (!kv8_head_dim(ctx->cfg.d)) return TQ_ERR_UNSUPPORTED;
   *bytes = std::max(kv8_rows_workspace(batch, n_new, Hq / H, H, ctx->cfg.d),
-                    ctx->cfg.d <= kD ? kv8_tc_workspace(batch, n_new, Hq / H, H, max_seq_len, ctx->cfg.d) : 0);
+                    kv8_tc_workspace(batch, n_new, Hq / H, H, max_seq_len, ctx->cfg.d));
   return TQ_OK;
 }
 

@@ -58,12 +58,10 @@ namespace {
 
 using namespace tcx;
 
-constexpr int kTRows = 256;               // query rows per item
 constexpr int kTTok = 128;                // tokens per tile
 constexpr int kTPg = kTTok / kPage;       // pages per tile
 constexpr int kTThreads = 512;
-constexpr int kKSt = 3, kVSt = 3;         // raw K and V stages
-constexpr int kDescs = 8, kItems = 4;     // tiles and items announced ahead
+constexpr int kItems = 4;                 // items announced ahead
 constexpr float kMNone = -1.0e30f;
 // Weights are 2^(kLift + score - M).  M is set kHead above the largest score met, so that it seldom moves again: the
 // largest weight is then 2^3, and fp16 keeps 11 bits down to 2^-17 of it.  M moves when a page's 16 weights sum to more
@@ -84,43 +82,55 @@ struct TileDesc {                         // one tile of the stream, by page
 };
 
 constexpr int kDoneRing = 8;
-enum Bar {
-  bKFull = 0, bVFull = bKFull + kKSt, bVEmpty = bVFull + kVSt, bReady = bVEmpty + kVSt, bSFull = bReady + 2,
-  bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2, bItem = bQReady + 2, bItemFree = bItem + kItems, bDesc = bItemFree + kItems,
-  bDone = bDesc + kDescs, bJoin = bDone + kDoneRing, bOFree, bDrain, bCount
+enum Bar {                                // room for the most stages that a head dimension has
+  bKFull = 0, bKFree = bKFull + 3, bVFull = bKFree + 2, bVEmpty = bVFull + 3, bReady = bVEmpty + 3, bSFull = bReady + 2,
+  bPFull = bSFull + 2, bODone = bPFull + 2, bQReady = bODone + 2, bQFree = bQReady + 2, bItem = bQFree + 1,
+  bItemFree = bItem + kItems, bDesc = bItemFree + kItems, bDone = bDesc + 8, bJoin = bDone + kDoneRing, bOFree, bDrain, bCount
 };
 
 // Shared memory by head dimension.  It has no room to be moved up to a 1024-byte boundary (the swizzles' period): the
 // kernel's only shared memory starts on one, and the kernel checks that.
+// d = 256 (WIDE): an item is 128 rows and one half of the values' channels, the scores of both halves are the same work
+// twice (of 3,072 cycles a tile a third, but queries, keys and values of 256 rows and channels would not fit); the
+// halves A and B share the queries.
 template <int D>
 struct TG {
-  static constexpr int KT = kTTok * D, VT = 2 * KT;    // a tile's codes, and as fp16
-  static constexpr int QX = 128 * 2 * D;               // a half's queries, both parts
-  static constexpr int PART = D + 4;                   // floats of a row's partial
+  static constexpr bool WIDE = D == 256;
+  static constexpr int ROWS = WIDE ? 128 : 256;        // query rows per item
+  static constexpr int DV = WIDE ? 128 : D;            // value channels per item
+  static constexpr int PER = D / DV;                   // items per KV head and block of rows
+  static constexpr int KST = WIDE ? 2 : 3, VST = KST;  // stages of keys and of raw values
+  static constexpr int DESCS = WIDE ? 4 : 8;           // tiles announced ahead
+  static constexpr int KT = kTTok * D, VRT = kTTok * DV, VT = 2 * VRT;   // a tile's keys, values, and values as fp16
+  static constexpr int QX = 128 * 2 * D;               // 128 rows' queries, both parts
+  static constexpr int QB = WIDE ? 0 : QX;             // from half A's queries to half B's
+  static constexpr int PART = DV + 4;                  // floats of a row's partial
   static constexpr int Q = 0;                          // [A, B] halves, see qpos
-  static constexpr int K = Q + 2 * QX;                 // [stage][128 tokens][D B]
-  static constexpr int VR = K + kKSt * KT;             // [stage][128 tokens][D B]
-  static constexpr int V = VR + kVSt * KT;             // [buffer][64-channel blocks][128 tokens][128 B]
+  static constexpr int K = Q + QX + QB;                // [stage][128-channel panels][128 tokens][128 B] (64 at d = 64)
+  static constexpr int VR = K + KST * KT;              // [stage][128 tokens][DV B]
+  static constexpr int V = VR + VST * VRT;             // [buffer][64-channel blocks][128 tokens][128 B]
   static constexpr int DESC = V + 2 * VT;
-  static constexpr int ITEM = DESC + kDescs * static_cast<int>(sizeof(TileDesc));
+  static constexpr int ITEM = DESC + DESCS * static_cast<int>(sizeof(TileDesc));
   static constexpr int BAR = ITEM + kItems * 48;
   static constexpr int JOIN = BAR + 8 * ((bCount + 1) & ~1);     // half B's (M, l) of 128 rows
-  // Piece c (sixteen channels) of part hi (0) or lo (1) of a row, in rows of 128 bytes with the 128-byte swizzle: at
-  // d = 128 the parts have a tile each, at d = 64 a row holds both.
+  static constexpr int ROWF = JOIN + 1024;             // WIDE: the rows' scales, from half A to half B
+  static constexpr int END = ROWF + (WIDE ? 512 : 0);
+  // Piece c (sixteen channels) of part hi (0) or lo (1) of a row, in rows of 128 bytes with the 128-byte swizzle: the
+  // parts have a tile per 128 channels each, at d = 64 a row holds both.
   __device__ static __forceinline__ uint32_t qpos(int row, int c, int part) {
-    return D == 128 ? static_cast<uint32_t>(part * 16384 + row * 128 + ((c ^ (row & 7)) << 4))
-                    : static_cast<uint32_t>(row * 128 + (((c + 4 * part) ^ (row & 7)) << 4));
+    return D == 64 ? static_cast<uint32_t>(row * 128 + (((c + 4 * part) ^ (row & 7)) << 4))
+                   : static_cast<uint32_t>(part * (QX / 2) + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
   }
-  // 16-byte piece c of a token's codes as TMA swizzled them.
+  // 16-byte piece c of a token's value codes as TMA swizzled them.
   __device__ static __forceinline__ uint32_t vpos(int t, int c) {
-    return static_cast<uint32_t>(t * D + ((c ^ (D == 128 ? t & 7 : (t >> 1) & 3)) << 4));
+    return static_cast<uint32_t>(t * DV + ((c ^ (DV == 128 ? t & 7 : (t >> 1) & 3)) << 4));
   }
 };
 template <int D>
-constexpr int tmem_at() { return TG<D>::JOIN + 1024; }
+constexpr int tmem_at() { return TG<D>::END; }
 template <int D>
 constexpr int smem_bytes() { return tmem_at<D>() + 16; }
-static_assert(smem_bytes<128>() <= 232448, "shared memory per block");
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<256>() <= 232448, "shared memory per block");
 static_assert(sizeof(TileDesc) % 16 == 0, "items behind the descriptors");
 // tensor-memory columns of half X
 __device__ __forceinline__ constexpr uint32_t col_s(uint32_t X) { return 128u * X; }
@@ -128,14 +138,15 @@ __device__ __forceinline__ constexpr uint32_t col_o(uint32_t X) { return 256u + 
 
 // Eight MMAs in one statement, one elected lane: the issuing warps share their schedulers with the softmax, so that
 // every instruction between two MMAs counts.  S = Qh Kc^T + Ql Kc^T: four steps of 32 channels (32 B, 2 descriptor
-// units) each.
+// units) each; ACC: on top of what is there.
+template <int ACC>
 __device__ __forceinline__ void mma8_scores(uint32_t d, uint64_t qh, uint64_t ql, uint64_t k, uint32_t idesc) {
   asm volatile(
       "{\n .reg .pred e, t, f;\n .reg .b64 h1, h2, h3, l1, l2, l3, k1, k2, k3;\n"
       " add.u64 h1, %1, 2;\n add.u64 h2, %1, 4;\n add.u64 h3, %1, 6;\n"
       " add.u64 l1, %2, 2;\n add.u64 l2, %2, 4;\n add.u64 l3, %2, 6;\n"
       " add.u64 k1, %3, 2;\n add.u64 k2, %3, 4;\n add.u64 k3, %3, 6;\n"
-      " setp.ne.b32 t, 1, 0;\n setp.ne.b32 f, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " setp.ne.b32 t, 1, 0;\n setp.ne.b32 f, %5, 0;\n elect.sync _|e, 0xffffffff;\n"
       " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %3, %4, f;\n"
       " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], h1, k1, %4, t;\n"
       " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], h2, k2, %4, t;\n"
@@ -144,7 +155,7 @@ __device__ __forceinline__ void mma8_scores(uint32_t d, uint64_t qh, uint64_t ql
       " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], l1, k1, %4, t;\n"
       " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], l2, k2, %4, t;\n"
       " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], l3, k3, %4, t;\n}\n" ::"r"(d),
-      "l"(qh), "l"(ql), "l"(k), "r"(idesc)
+      "l"(qh), "l"(ql), "l"(k), "r"(idesc), "n"(ACC)
       : "memory");
 }
 // The same at d = 64: two steps each, the query's parts side by side in a row.
@@ -193,11 +204,12 @@ __device__ __forceinline__ uint64_t vdesc(uint32_t saddr) {
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16384 >> 4) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
-__device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap* map, int blk, uint32_t bar) {
+// One block's panel of (at most) 128 channels from channel x on.
+__device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap* map, int x, int blk, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(blk), "r"(bar)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(blk), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -294,20 +306,21 @@ __device__ __forceinline__ void stg256(void* p, const uint32_t* v) {   // 32-byt
 
 // A block of query rows of one sequence, and the pages that it sees.
 struct TBlock {
-  int b, qb, p0, rows;                    // sequence, block, the sequence's first query position, rows (<= 256)
+  int b, qb, p0, rows;                    // sequence, block, the sequence's first query position, rows of the block
   int pmin, pmax;
   Kv8Range r;
   int pages;
 };
 // Block `e` of the list (sequence by sequence); its tiles, 0 if there is nothing to do.  In the list an item takes
 // kItemCost units, then one per tile.
+template <int ROWS>
 __device__ __forceinline__ int tc_block(const Kv8Attn& a, int e, int nqb, TBlock& k) {
   k.b = e / nqb;
   k.qb = e - k.b * nqb;
   const Kv8Seq s = kv8_seq(a, k.b);
-  const int rows = s.n * a.G, r0 = k.qb * kTRows;      // the host keeps batch T Hq below 2^27
+  const int rows = s.n * a.G, r0 = k.qb * ROWS;      // the host keeps batch T Hq below 2^27
   k.p0 = s.p0;
-  k.rows = min(rows - r0, kTRows);
+  k.rows = min(rows - r0, ROWS);
   k.pages = 0;
   if (k.rows <= 0) return 0;
   k.pmin = s.p0 + r0 / a.G;
@@ -318,7 +331,7 @@ __device__ __forceinline__ int tc_block(const Kv8Attn& a, int e, int nqb, TBlock
 }
 // What the load warp tells the others of an item: a block, a KV head, and a run of its tiles.
 struct alignas(16) ItemMsg {
-  int valid, b, h, qb;
+  int valid, b, h, qb;                    // h: item of the block (KV head, at d = 256 with a half of the values' channels)
   int p0, rows, pmin, pmax;
   int ntile, slot, pad[2];                // slot: of the workspace for a part of the tiles; -1 for all of them
 };
@@ -350,8 +363,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
   }
 
   if (tid == 0) {
-    for (int i = 0; i < kKSt; ++i) bar_init(bar(bKFull + i), 1);
-    for (int i = 0; i < kVSt; ++i) {
+    for (int i = 0; i < L::KST; ++i) bar_init(bar(bKFull + i), 1);
+    for (int i = 0; i < 2; ++i) bar_init(bar(bKFree + i), 1);
+    bar_init(bar(bQFree), 4);
+    for (int i = 0; i < L::VST; ++i) {
       bar_init(bar(bVFull + i), 1);
       bar_init(bar(bVEmpty + i), 4);
     }
@@ -365,7 +380,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     for (int i = 0; i < kDoneRing; ++i) bar_init(bar(bDone + i), 1);
     bar_init(bar(bJoin), 4);
     bar_init(bar(bOFree), 4);
-    for (int i = 0; i < kDescs; ++i) bar_init(bar(bDesc + i), 1);
+    for (int i = 0; i < L::DESCS; ++i) bar_init(bar(bDesc + i), 1);
     for (int i = 0; i < kItems; ++i) {
       bar_init(bar(bItem + i), 1);
       bar_init(bar(bItemFree + i), 15);                // every warp but the one that announces
@@ -388,7 +403,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
   }
   // the list, cut into equal spans: units before each block (of one head), by a scan in the queries' room
-  const int entries = a.B * nqb;
+  const int entries = a.B * nqb, heads = a.H * L::PER;
   long long u0 = 0, u1 = 0, span = 1;
   int entry0 = 0, before0 = 0;
   if (split) {
@@ -399,7 +414,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     int sum = 0;
     for (int i = 0; i < per && tid * per + i < entries; ++i) {
       prefix[tid * per + i] = sum;
-      const int tiles = tc_block(a, tid * per + i, nqb, k);
+      const int tiles = tc_block<L::ROWS>(a, tid * per + i, nqb, k);
       sum += tiles ? tiles + kItemCost : 0;
     }
     int run = sum;
@@ -417,7 +432,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     for (int i = 0; i < per && tid * per + i < entries; ++i) prefix[tid * per + i] += base;
     __syncthreads();
-    const long long units = static_cast<long long>(total) * a.H;
+    const long long units = static_cast<long long>(total) * heads;
     span = (units + gridDim.x - 1) / gridDim.x;
     span = span < kMinSpan ? kMinSpan : span;
     u0 = span * blockIdx.x < units ? span * blockIdx.x : units;
@@ -425,7 +440,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     int lo = 0, hi = entries - 1;                      // the block that holds u0
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
-      if (static_cast<long long>(prefix[mid]) * a.H <= u0) lo = mid;
+      if (static_cast<long long>(prefix[mid]) * heads <= u0) lo = mid;
       else hi = mid - 1;
     }
     entry0 = lo;
@@ -463,6 +478,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // whole sectors per store
     int seq = 0, nS = 0, nO = 0, nJ = 0;               // tiles seen, phases of S, of the final O and of the halves' join
     float2* join = reinterpret_cast<float2*>(sm + L::JOIN);
+    float* rowf_sm = reinterpret_cast<float*>(sm + L::ROWF);
+    int nF = 0;                                        // phases of the queries' release by half B
     // The row of an item that is this thread's.
     struct Row {
       bool live;
@@ -476,27 +493,33 @@ __global__ void __launch_bounds__(kTThreads, 1)
     auto queries = [&](const ItemMsg& x) {
       Row w;
       const int rx = x.rows > 128 ? 128 * X + r : r;
-      const unsigned gr = static_cast<unsigned>(x.qb * kTRows + rx), tok = gr / static_cast<unsigned>(a.G);
+      const unsigned gr = static_cast<unsigned>(x.qb * L::ROWS + rx), tok = gr / static_cast<unsigned>(a.G);
       w.live = rx < x.rows;
       w.p = w.live ? x.p0 + static_cast<int>(tok) : -1;
-      w.at = ((static_cast<long long>(x.b) * a.T + tok) * a.Hq + x.h * a.G + (gr - tok * a.G)) * D;
+      w.at = ((static_cast<long long>(x.b) * a.T + tok) * a.Hq + x.h / L::PER * a.G + (gr - tok * a.G)) * D;
+      w.rowf = 0.0f;
+      if (L::WIDE && X) return w;                      // half A does the work for both
       // The warp's 32 rows, D / 8 lanes per row (a lane per row would ask for 32 lines with each load); the raw 16-byte
       // pieces 2c and 2c + 1 of a row wait where the parts of its channels 16c .. 16c + 15 will stand.
-      const uint32_t qx = sb + L::Q + X * L::QX;
+      const uint32_t qx = sb + L::Q + X * L::QB;
       {
         constexpr int kP = D / 8, kR = 32 / kP;        // pieces per row, rows per load
         const long long where = w.live ? w.at : -1;
         const int piece = lane % kP;
-        uint4 v4[kP];
+        constexpr int kB = kP < 16 ? kP : 16;          // loads in flight
+#pragma unroll 1
+        for (int i0 = 0; i0 < kP; i0 += kB) {
+          uint4 v4[kB];
 #pragma unroll
-        for (int i = 0; i < kP; ++i) {
-          const long long at = __shfl_sync(0xffffffffu, where, kR * i + lane / kP);
-          v4[i] = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at)[piece]
-                          : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < kB; ++i) {
+            const long long at = __shfl_sync(0xffffffffu, where, kR * (i0 + i) + lane / kP);
+            v4[i] = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at)[piece]
+                            : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int i = 0; i < kB; ++i)
+            sts128(qx + L::qpos(32 * wq + kR * (i0 + i) + lane / kP, piece >> 1, piece & 1), v4[i].x, v4[i].y, v4[i].z, v4[i].w);
         }
-#pragma unroll
-        for (int i = 0; i < kP; ++i)
-          sts128(qx + L::qpos(32 * wq + kR * i + lane / kP, piece >> 1, piece & 1), v4[i].x, v4[i].y, v4[i].z, v4[i].w);
       }
       __syncwarp();
       uint32_t mx2 = 0u;                               // largest magnitudes: bf16 bits order as integers
@@ -532,6 +555,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       }
       // a row that is not finite: every score NaN, and so the result
       if (mx >= 0x7F80u) w.rowf = __int_as_float(0x7FC00000);
+      if (L::WIDE) rowf_sm[r] = w.rowf;
       fence_async_smem();
       __syncwarp();
       if (lane == 0) bar_arrive(bar(bQReady + X));
@@ -548,17 +572,22 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (mine(it)) row = queries(it);
         continue;
       }
-      const float rowf = row.rowf;
+      float rowf = row.rowf;
       const int p = row.p;
       const bool turns = it.rows <= 128;               // the halves take the tiles in turn
       const int t0 = turns ? X : 0, dt = turns ? 2 : 1, seq0 = seq;
       float m = kMNone, l = 0.0f;
       seq += t0;
       for (int t = t0; t < ntile; t += dt, seq += dt) {
-        if (!wait(bDesc + seq % kDescs, seq / kDescs) || !wait(bSFull + X, nS)) break;
+        if (!wait(bDesc + seq % L::DESCS, seq / L::DESCS) || !wait(bSFull + X, nS)) break;
         ++nS;
         tc_after();
-        const TileDesc& d = descs[seq % kDescs];
+        if (L::WIDE && X) {                            // the row's scale is there with the first scores
+          if (t == t0) rowf = rowf_sm[r];
+          __syncwarp();
+          if (lane == 0 && t + dt >= ntile) bar_arrive(bar(bQFree));
+        }
+        const TileDesc& d = descs[seq % L::DESCS];
         // never zero (a hidden score stays -inf), and NaN stays NaN
         auto factor = [&](int pg) { return fmaxf(d.fac[pg] * rowf, 1.2e-38f) + (rowf - rowf); };
         // The tile as it mostly is: every token seen and no score far above the maximum so far.  The weights by the
@@ -634,7 +663,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
             if (t > t0) {                              // O of the tiles before (their MMAs have run: S came after)
 #pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
+              for (int c = 0; c < L::DV / 16; ++c) {
                 float o[16];
                 uint32_t u[16];
                 tld16(to + 16u * c, o);
@@ -680,6 +709,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const ItemMsg done_item = it;
       const Row done_row = row;
       it = next_item(n + 1);
+      if (L::WIDE && X == 0 && ntile > 1 && !wait(bQFree, nF++)) break;     // half B has its last scores too
       if (mine(it)) row = queries(it);
       // ---- the row's result (or partial) ----
       if (!wait(bODone + X, nO)) break;
@@ -704,7 +734,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         m = mj;
         l = fa * l + fb * other.y;
 #pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < L::DV / 16; ++c) {
           float o[16], o2[16];
           uint32_t u[16];
           tld16(to + 16u * c, o);
@@ -719,9 +749,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (lane == 0) bar_arrive(bar(bOFree));
       }
       const float inv = l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
-      float* part = parts + (static_cast<long long>(done_item.slot) * kTRows + (turns ? 0 : 128 * X) + r) * L::PART;
+      float* part = parts + (static_cast<long long>(done_item.slot) * L::ROWS + (turns ? 0 : 128 * X) + r) * L::PART;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < L::DV / 32; ++c) {
         float o[32];
         tld32(to + 32u * c, o);
         if (!done_row.live) continue;
@@ -732,7 +762,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
             w[k] = *reinterpret_cast<const uint32_t*>(&y);
           }
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + done_row.at + 32 * c;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + done_row.at + done_item.h % L::PER * L::DV + 32 * c;
           if (wide) {
             stg256(dst, w);
             stg256(dst + 16, w + 8);
@@ -760,18 +790,18 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (!it.valid) break;
       const int ntile = it.ntile, ahead = it.rows <= 128 ? 2 : 1, end = seq + ntile;
       for (int i = 0; i < ntile; ++i, ++seq) {
-        if (!wait(bVFull + seq % kVSt, seq / kVSt)) break;
+        if (!wait(bVFull + seq % L::VST, seq / L::VST)) break;
         if (seq >= 2 && !wait(bDone + (seq - 2) % kDoneRing, (seq - 2) / kDoneRing)) break;
-        const int j = descs[seq % kDescs].j0[pg] + (t & 15);
+        const int j = descs[seq % L::DESCS].j0[pg] + (t & 15);
         // what no row sees may hold anything: zeros instead
         const bool see = j <= it.pmax && (!a.window || j > it.pmin - a.window || j < a.sinks);
-        const uint32_t src = sb + L::VR + (seq % kVSt) * L::KT;
+        const uint32_t src = sb + L::VR + (seq % L::VST) * L::VRT;
         const uint32_t dst = sb + L::V + (seq & 1) * L::VT + t * 128;
-        uint4 w[D / 16];                               // every load ahead of the stores
+        uint4 w[L::DV / 16];                             // every load ahead of the stores
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) w[c] = lds128(src + L::vpos(t, c));
+        for (int c = 0; c < L::DV / 16; ++c) w[c] = lds128(src + L::vpos(t, c));
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < L::DV / 16; ++c) {
           if (!see) w[c] = make_uint4(0u, 0u, 0u, 0u);
           const uint32_t o0 = static_cast<uint32_t>((((2 * c) & 7) ^ (t & 7)) << 4),
                          o1 = static_cast<uint32_t>((((2 * c + 1) & 7) ^ (t & 7)) << 4);
@@ -783,9 +813,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) bar_arrive(bar(bVEmpty + seq % kVSt));
+        if (lane == 0) bar_arrive(bar(bVEmpty + seq % L::VST));
         // the issuing warp's one wait for a tile covers the keys of the scores that it issues behind the tile
-        for (; keys <= seq + ahead && keys < end && !failed; ++keys) (void)wait(bKFull + keys % kKSt, keys / kKSt);
+        for (; keys <= seq + ahead && keys < end && !failed; ++keys) (void)wait(bKFull + keys % L::KST, keys / L::KST);
         if (failed) break;
         if (lane == 0) bar_arrive(bar(bReady + (seq & 1)));
       }
@@ -796,7 +826,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
     if (warp == 12) {
       // ---- items, pages, keys -----------------------------------------------------------------
       int seq = 0, n = 0, nk = 0;                      // tiles, items, and tiles whose copies were issued
-      static_assert(kKSt == 3, "the tiles whose keys are still there");
       int free0 = 0, free1 = 0, free2 = 0;             // the steps after which the keys of the last three tiles are read
       auto publish = [&](const ItemMsg& x) {
         if (n >= kItems) (void)wait(bItemFree + n % kItems, n / kItems - 1);   // every warp has taken the one before
@@ -808,14 +837,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
       };
       TBlock it;
       TSplit cut{};
-      int e = entry0, h = 0, tiles = split && u0 < u1 ? tc_block(a, e, nqb, it) : 0;
-      long long at = static_cast<long long>(before0) * a.H;          // the item's first unit in the list
+      int e = entry0, h = 0, tiles = split && u0 < u1 ? tc_block<L::ROWS>(a, e, nqb, it) : 0;
+      long long at = static_cast<long long>(before0) * heads;         // the item's first unit in the list
       if (tiles) {
         h = static_cast<int>((u0 - at) / (tiles + kItemCost));
         at += static_cast<long long>(h) * (tiles + kItemCost);
       }
       long long whole = blockIdx.x;                    // not split: whole items in turn, the longest rows first
-      const long long items = static_cast<long long>(entries) * a.H;
+      const long long items = static_cast<long long>(entries) * heads;
       for (;;) {
         int t0 = 0, t1 = 0;                            // the item's tiles that are this CTA's
         if (split) {
@@ -828,8 +857,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
           }
         } else {
           if (whole >= items) break;
-          h = static_cast<int>(whole % a.H);
-          t1 = tiles = tc_block(a, entries - 1 - static_cast<int>(whole / a.H), nqb, it);
+          h = static_cast<int>(whole % heads);
+          t1 = tiles = tc_block<L::ROWS>(a, entries - 1 - static_cast<int>(whole / heads), nqb, it);
           whole += gridDim.x;
           if (!tiles) continue;
         }
@@ -850,7 +879,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const int page = ci < it.r.ns ? ci : ci - it.r.ns + it.r.w0;
             const int pid = table[page];
             if (pid >= 0 && pid < a.num_pages) {
-              x.blk = pid * a.H + h;
+              x.blk = pid * a.H + h / L::PER;
               x.j0 = kPage * page;
               x.ks = a.ks[x.blk];
               x.ev = static_cast<int>((__float_as_uint(a.vs[x.blk]) >> 23) & 0xFF) - 127;
@@ -869,10 +898,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const bool on = (lane >> 3) == k;
             const int pg = lane & 7;
             const uint32_t bytes = static_cast<uint32_t>(__popc((there4 >> (8 * k)) & 0xFFu)) * kPage * D;
-            if (seq >= kKSt && !wait(bDone + free0 % kDoneRing, free0 / kDoneRing)) break;
-            free0 = free1, free1 = free2;
-            free2 = c4 + k * kTPg >= c0 + ahead * kTPg ? seq - ahead : seq;
-            TileDesc& d = descs[seq % kDescs];
+            if (L::WIDE) {
+              if (seq >= 2 && !wait(bKFree + (seq & 1), seq / 2 - 1)) break;
+            } else {
+              if (seq >= 3 && !wait(bDone + free0 % kDoneRing, free0 / kDoneRing)) break;
+              free0 = free1, free1 = free2;
+              free2 = c4 + k * kTPg >= c0 + ahead * kTPg ? seq - ahead : seq;
+            }
+            TileDesc& d = descs[seq % L::DESCS];
             if (on) {
               d.fac[pg] = fabsf(a.scale_log2) * cur.ks;
               d.ev[pg] = static_cast<float>(cur.ev);
@@ -883,14 +916,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
             __syncwarp();
             if (lane == 0) {
-              bar_arrive(bar(bDesc + seq % kDescs));
-              if (bytes) bar_arrive_tx(bar(bKFull + seq % kKSt), bytes);
-              else bar_arrive(bar(bKFull + seq % kKSt));
+              bar_arrive(bar(bDesc + seq % L::DESCS));
+              if (bytes) bar_arrive_tx(bar(bKFull + seq % L::KST), bytes);
+              else bar_arrive(bar(bKFull + seq % L::KST));
             }
             __syncwarp();
             ++nk;
             if (on && cur.blk >= 0)
-              tma_block(sb + L::K + (seq % kKSt) * L::KT + pg * kPage * D, &mk, cur.blk, bar(bKFull + seq % kKSt));
+              tma_block(sb + L::K + (seq % L::KST) * L::KT + pg * kPage * L::DV, &mk, 0, cur.blk, bar(bKFull + seq % L::KST));
           }
           cur = nxt;
         }
@@ -899,9 +932,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
           at += kItemCost + tiles;
           u0 = at;
           if (u0 >= u1) break;
-          if (++h == a.H) {
+          if (++h == heads) {
             h = 0;
-            do tiles = tc_block(a, ++e, nqb, it);
+            do tiles = tc_block<L::ROWS>(a, ++e, nqb, it);
             while (!tiles);
           }
         }
@@ -910,7 +943,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (split && lane == 0) splits[blockIdx.x] = cut;
       // copies still in flight land before the CTA ends
       bool f2 = false;
-      for (int s = nk >= kKSt ? nk - kKSt : 0; s < nk; ++s) (void)bar_wait(bar(bKFull + s % kKSt), (s / kKSt) & 1, f2);
+      for (int s = nk >= L::KST ? nk - L::KST : 0; s < nk; ++s) (void)bar_wait(bar(bKFull + s % L::KST), (s / L::KST) & 1, f2);
     } else if (warp == 13) {
       // ---- MMA issue, the warp converged: O += w V of a tile and the next tile's scores, half A, then half B.  The
       // order is strict: left to mix, both halves' MMAs end together, both softmaxes run together and neither overlaps
@@ -930,23 +963,28 @@ __global__ void __launch_bounds__(kTThreads, 1)
         two = __all_sync(0xffffffffu, it.rows > 128);
       };
       auto scores = [&](uint32_t X, int s) {
-        const uint32_t q = sb + L::Q + X * L::QX, k = sb + L::K + (s % kKSt) * L::KT;
-        if (D == 128) mma8_scores(tmem + col_s(X), sdesc(q), sdesc(q + 16384), kdesc8<D>(k), kIdF8);
-        else mma4_scores(tmem + col_s(X), sdesc(q), kdesc8<D>(k), kIdF8);
+        const uint32_t q = sb + L::Q + X * L::QB, k = sb + L::K + (s % L::KST) * L::KT;
+        if (D == 64) {
+          mma4_scores(tmem + col_s(X), sdesc(q), kdesc8<64>(k), kIdF8);
+        } else {
+          mma8_scores<0>(tmem + col_s(X), sdesc(q), sdesc(q + L::QX / 2), kdesc8<128>(k), kIdF8);
+          if (L::WIDE) mma8_scores<1>(tmem + col_s(X), sdesc(q + 16384), sdesc(q + L::QX / 2 + 16384), kdesc8<128>(k + 16384), kIdF8);
+        }
         mma_commit_warp(bar(bSFull + X));
+        if (L::WIDE) mma_commit_warp(bar(bKFree + (s & 1)));
       };
       auto values = [&](uint32_t X, int s, bool first) {
-        mma8_values(tmem + col_o(X), tmem + col_s(X), vdesc(sb + L::V + (s & 1) * L::VT), idesc_f16(D) | (1u << 16), first ? 0u : 1u);
+        mma8_values(tmem + col_o(X), tmem + col_s(X), vdesc(sb + L::V + (s & 1) * L::VT), idesc_f16(L::DV) | (1u << 16), first ? 0u : 1u);
       };
       // the first tile of an item: its keys and its queries
       auto first_scores = [&](int s) {
-        if (!ready(bKFull + s % kKSt, s / kKSt) || !ready(bQReady, nq0++)) return false;
+        if (!ready(bKFull + s % L::KST, s / L::KST) || !ready(bQReady, nq0++)) return false;
         tc_after();
         scores(0, s);
         if (two || tiles > 1) {
           const int s1 = two ? s : s + 1;
-          if (!two && !ready(bKFull + s1 % kKSt, s1 / kKSt)) return false;
-          if (!ready(bQReady + 1, nq1++)) return false;
+          if (!two && !ready(bKFull + s1 % L::KST, s1 / L::KST)) return false;
+          if (!L::WIDE && !ready(bQReady + 1, nq1++)) return false;
           tc_after();
           scores(1, s1);
         }
@@ -1008,33 +1046,45 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (!it.valid) break;
         const int ntile = it.ntile;
         for (int i = 0; i < ntile; ++i, ++seq) {
-          if (!wait(bDesc + seq % kDescs, seq / kDescs)) break;
-          const int blk = lane < kTPg ? descs[seq % kDescs].blk[lane] : -1;
-          if (seq >= kVSt && !wait(bVEmpty + seq % kVSt, seq / kVSt - 1)) break;
-          const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, blk >= 0))) * kPage * D;
+          if (!wait(bDesc + seq % L::DESCS, seq / L::DESCS)) break;
+          const int blk = lane < kTPg ? descs[seq % L::DESCS].blk[lane] : -1;
+          if (seq >= L::VST && !wait(bVEmpty + seq % L::VST, seq / L::VST - 1)) break;
+          const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, blk >= 0))) * kPage * L::DV;
           if (lane == 0) {
-            if (bytes) bar_arrive_tx(bar(bVFull + seq % kVSt), bytes);
-            else bar_arrive(bar(bVFull + seq % kVSt));
+            if (bytes) bar_arrive_tx(bar(bVFull + seq % L::VST), bytes);
+            else bar_arrive(bar(bVFull + seq % L::VST));
           }
           __syncwarp();
-          if (blk >= 0) tma_block(sb + L::VR + (seq % kVSt) * L::KT + lane * kPage * D, &mv, blk, bar(bVFull + seq % kVSt));
+          if (blk >= 0)
+            tma_block(sb + L::VR + (seq % L::VST) * L::VRT + lane * kPage * L::DV, &mv, it.h % L::PER * L::DV, blk,
+                      bar(bVFull + seq % L::VST));
         }
         if (failed) break;
       }
       // copies still in flight land before the CTA ends
       bool f2 = false;
-      for (int s = seq >= kVSt ? seq - kVSt : 0; s < seq; ++s) (void)bar_wait(bar(bVFull + s % kVSt), (s / kVSt) & 1, f2);
+      for (int s = seq >= L::VST ? seq - L::VST : 0; s < seq; ++s) (void)bar_wait(bar(bVFull + s % L::VST), (s / L::VST) & 1, f2);
     } else {
       // ---- an item's queries on their way to L2 as soon as it is known ------------------------
+      int seq = 0;
       for (int n = 0;; ++n) {
         const ItemMsg it = next_item(n);
         if (!it.valid) break;
         constexpr int kLines = D / 64;                 // 128-byte lines of a row
         for (int i = lane; i < it.rows * kLines; i += 32) {
-          const unsigned gr = static_cast<unsigned>(it.qb * kTRows + i / kLines), tok = gr / static_cast<unsigned>(a.G);
+          const unsigned gr = static_cast<unsigned>(it.qb * L::ROWS + i / kLines), tok = gr / static_cast<unsigned>(a.G);
           const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-                                   ((static_cast<long long>(it.b) * a.T + tok) * a.Hq + it.h * a.G + (gr - tok * a.G)) * D;
+                                   ((static_cast<long long>(it.b) * a.T + tok) * a.Hq + it.h / L::PER * a.G + (gr - tok * a.G)) * D;
           asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64 * (i % kLines)));
+        }
+        if (L::WIDE) {                                 // the keys' upper channels
+          const int ntile = it.ntile;
+          for (int i = 0; i < ntile; ++i, ++seq) {
+            if (!wait(bDesc + seq % L::DESCS, seq / L::DESCS)) break;
+            const int blk = lane < kTPg ? descs[seq % L::DESCS].blk[lane] : -1;
+            if (blk >= 0) tma_block(sb + L::K + (seq & 1) * L::KT + 16384 + lane * kPage * 128, &mk, 128, blk, bar(bKFull + (seq & 1)));
+          }
+          if (failed) break;
         }
       }
     }
@@ -1054,8 +1104,9 @@ __global__ void __launch_bounds__(256) kv8_tc_join_kernel(const __grid_constant_
   const TSplit cut = reinterpret_cast<const TSplit*>(a.part)[c];
   if (!cut.valid) return;
   const float* parts = a.part + static_cast<size_t>(ctas) * (sizeof(TSplit) / sizeof(float));
-  constexpr int kPart = TG<D>::PART;
-  const long long step = static_cast<long long>(kTRows) * kPart;
+  using L = TG<D>;
+  constexpr int kPart = L::PART, DV = L::DV;
+  const long long step = static_cast<long long>(L::ROWS) * kPart;
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     const int rr = 32 * blockIdx.y + 8 * i + warp;
@@ -1073,22 +1124,25 @@ __global__ void __launch_bounds__(256) kv8_tc_join_kernel(const __grid_constant_
       const float* p = part(k);
       const float f = ex2(p[0] - M);
       L = fmaf(f, p[1], L);
-      if (4 * lane >= D) continue;
+      if (4 * lane >= DV) continue;
       const float4 x = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
       acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y), acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
     }
-    if (4 * lane >= D) continue;
+    if (4 * lane >= DV) continue;
     const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
     const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
                          y1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    const unsigned gr = static_cast<unsigned>(cut.qb * kTRows + rr), tok = gr / static_cast<unsigned>(a.G);
-    const long long at = ((static_cast<long long>(cut.b) * a.T + tok) * a.Hq + cut.h * a.G + (gr - tok * a.G)) * D + 4 * lane;
+    const unsigned gr = static_cast<unsigned>(cut.qb * L::ROWS + rr), tok = gr / static_cast<unsigned>(a.G);
+    const long long at = ((static_cast<long long>(cut.b) * a.T + tok) * a.Hq + cut.h / L::PER * a.G + (gr - tok * a.G)) * D +
+                         cut.h % L::PER * DV + 4 * lane;
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
   }
 }
 
-int query_blocks(int T, int G) { return static_cast<int>((static_cast<long long>(T) * G + kTRows - 1) / kTRows); }
+int rows_of(int d) { return d == 256 ? TG<256>::ROWS : TG<128>::ROWS; }
+int items_per_head(int d) { return d == 256 ? TG<256>::PER : 1; }
+int query_blocks(int T, int G, int d) { return static_cast<int>((static_cast<long long>(T) * G + rows_of(d) - 1) / rows_of(d)); }
 
 // CTAs of a call: one per SM, fewer where the list of tiles cannot be that long.
 long long tiles_of(int max_seq_len) { return (static_cast<long long>(max_seq_len) + kTTok - 1) / kTTok + 1; }
@@ -1147,37 +1201,42 @@ bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d)
 // here (d = 64: 127 and 133), 20 rows 161 us here, two blocks a head there.  A larger scale would make the query's
 // rounding to two e4m3 parts count.
 bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale) {
-  return (d == 64 || d == 128) && !f32 && static_cast<long long>(T) * G > 16 && softmax_scale != 0.0f &&
+  return !f32 && static_cast<long long>(T) * G > 16 && softmax_scale != 0.0f &&
          std::fabs(static_cast<double>(softmax_scale)) <= (1.0 + 1e-6) / std::sqrt(static_cast<double>(d));
 }
 
 size_t kv8_tc_workspace(int B, int T, int G, int H, int max_seq_len, int d) {
-  const int nqb = query_blocks(T, G);
+  const int nqb = query_blocks(T, G, d);
   if (!splits(B, nqb, max_seq_len)) return 16;
-  return static_cast<size_t>(ctas_for(B, H, nqb, max_seq_len)) *
-         (sizeof(TSplit) + 2 * sizeof(float) * static_cast<size_t>(kTRows) * (d + 4));
+  return static_cast<size_t>(ctas_for(B, H * items_per_head(d), nqb, max_seq_len)) *
+         (sizeof(TSplit) + 2 * sizeof(float) * static_cast<size_t>(rows_of(d)) * (d / items_per_head(d) + 4));
 }
 
 namespace {
 template <int D>
 cudaError_t launch_t(const Kv8Attn& a, cudaStream_t s) {
-  const int nqb = query_blocks(a.T, a.G);
+  const int nqb = query_blocks(a.T, a.G, D);
   CUtensorMap mk, mv;
   const long long blocks = static_cast<long long>(a.num_pages) * a.H;
   if (!kv8_block_map(&mk, a.kc, blocks, D) || !kv8_block_map(&mv, a.vc, blocks, D)) return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = smem_attr_once(kv8_tc_kernel<D>, smem_bytes<D>(), configured);
   if (e != cudaSuccess) return e;
-  const int ctas = ctas_for(a.B, a.H, nqb, a.max_seq_len);
+  const int ctas = ctas_for(a.B, a.H * TG<D>::PER, nqb, a.max_seq_len);
   const bool split = splits(a.B, nqb, a.max_seq_len);
   e = launch_pdl(kv8_tc_kernel<D>, dim3(ctas), dim3(kTThreads), smem_bytes<D>(), s, a, mk, mv, nqb, split ? 1 : 0);
   if (e != cudaSuccess || !split) return e;
-  return launch_pdl(kv8_tc_join_kernel<D>, dim3(ctas, kTRows / 32), dim3(256), 0, s, a, ctas);
+  return launch_pdl(kv8_tc_join_kernel<D>, dim3(ctas, TG<D>::ROWS / 32), dim3(256), 0, s, a, ctas);
 }
 }  // namespace
 
 cudaError_t launch_kv8_tc(const Kv8Attn& a, int d, cudaStream_t s) {
-  return d == 128 ? launch_t<128>(a, s) : d == 64 ? launch_t<64>(a, s) : cudaErrorInvalidValue;
+  switch (d) {
+    case 64: return launch_t<64>(a, s);
+    case 128: return launch_t<128>(a, s);
+    case 256: return launch_t<256>(a, s);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace tq
