@@ -430,10 +430,10 @@ tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_new, int num
  * follows the lengths on the device; results do not depend on the run.
  * Accuracy at every softmax_scale: exact products of codes and queries summed
  * in fp32, weights to 11 bits (bf16) or 22 (fp32) down to 2^-22 of the largest.
- * With more than 16 query rows (n_new times heads per KV head) and bf16, d 64
- * or 128 and |softmax_scale| <= 1/sqrt(d), the tcgen05 form runs: a query
- * channel is then off by at most 2^-17 of its row's largest, the weights keep
- * 11 bits down to 2^-17.  The weights ride on the value scales: of two
+ * With more than 16 query rows (n_new times heads per KV head), bf16 and
+ * |softmax_scale| <= 1/sqrt(d), the tcgen05 form runs: a query channel is then
+ * off by at most 2^-17 of its row's largest, the weights keep 11 bits down to
+ * 2^-17.  The weights ride on the value scales: of two
  * blocks of a sequence whose value scales lie more than 2^100 apart (a block of
  * zeros has 2^-100) the smaller one's weights may be lost.  NaN codes (which
  * tq_kv8_append never writes) at a seen position may spoil other rows too.

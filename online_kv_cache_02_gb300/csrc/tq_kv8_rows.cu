@@ -1,5 +1,5 @@
 // Attention over the 8-bit paged cache for few query rows (decode, drafted
-// tokens), for fp32 queries and for every head dimension: mma.sync on e4m3
+// tokens), for fp32 queries and for large softmax scales: mma.sync on e4m3
 // codes turned into fp16, which is exact.
 //
 // An item is (sequence, block of R = 8 NT query rows, KV head); its keys are
@@ -27,8 +27,8 @@
 // tokens, 32 / 8 heads, 1.08 GB: 176 us, 6.1 TB/s, 90% of a copy's rate; 64 of 1,024 to
 // 8,192, 28 / 4 heads: 62 us, 4.9 TB/s; a window of 4,096 of 32,768: 35 us; one sequence
 // of 1,000: 9 us.  fp32, d = 64, 7 of 3,001 to 9,001: 25 us.  Weights by a new maximum
-// at every page instead of the one so far: 1 to 6% more.  fp32 prompts and d = 256 run
-// here too, at 55 to 65 TFLOP/s: eight warps an SM wait on their own chains of products.
+// at every page instead of the one so far: 1 to 6% more.  fp32 prompts run here
+// too, at 55 to 65 TFLOP/s: eight warps an SM wait on their own chains of products.
 
 #include "tq_kv8.h"
 #include "tq_tc.cuh"

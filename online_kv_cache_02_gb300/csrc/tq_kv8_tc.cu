@@ -1,5 +1,5 @@
 // Attention of many query rows per KV head over the 8-bit paged cache on the tensor
-// cores (tcgen05), bf16 queries, d = 64 or 128.
+// cores (tcgen05), bf16 queries, d = 64, 128 or 256.
 //
 // An item is (sequence, KV head, block of 256 query rows r = t G + g); keys go by in
 // tiles of 128 tokens (8 pages).  All items' tiles form one list that is cut into
@@ -37,7 +37,8 @@
 // 15,000 to 30,000, 475 us, 77%; three prompts of up to 4,000 in a window of 1,024
 // (28 / 4 heads) 165 us, 43%, where an item of nine tiles pays for its queries and its
 // result with the time of four; five drafted tokens of 16 sequences of 2,000 to 8,000,
-// 53 us, 46% of a copy's rate (MMAs of 128 rows of which 20 are there).
+// 53 us, 46% of a copy's rate (MMAs of 128 rows of which 20 are there).  d = 256, a
+// prompt of 2,048 tokens, 16 / 4 heads: 81 us (mma.sync: 597).
 // Slower, each by itself: 64-token tiles in two buffers, sixteen softmax warps, two
 // issuing warps, the queries' copies beside the last tile (from the softmax warps or
 // a warp of their own: code in the tile loop, or a copy slower than four warps').
@@ -1198,7 +1199,8 @@ bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d)
 }
 
 // More rows than a block of the mma.sync form has.  64 sequences of 2,000 to 8,000 tokens: 16 rows 153 us there and 158
-// here (d = 64: 127 and 133), 20 rows 161 us here, two blocks a head there.  A larger scale would make the query's
+// here (d = 64: 127 and 133), 20 rows 161 us here.  16 sequences, d = 256: 16 rows 100 us there and 106 here, 20 rows
+// 133 and 108, 64 rows 339 and 115.  A larger scale would make the query's
 // rounding to two e4m3 parts count.
 bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale) {
   return !f32 && static_cast<long long>(T) * G > 16 && softmax_scale != 0.0f &&
