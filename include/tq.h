@@ -428,15 +428,16 @@ tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_new, int num
  * page behind the sequence's end, or outside every query's window, may hold
  * any bytes.  Any number of query heads per KV head.  The split of the work
  * follows the lengths on the device; results do not depend on the run.
- * Accuracy at every softmax_scale: exact products of codes and queries summed
- * in fp32, weights to 11 bits (bf16) or 22 (fp32) down to 2^-22 of the largest.
+ * Accuracy at every softmax_scale: products of codes and queries summed in
+ * fp32 (bf16 queries exact, fp32 ones to 22 bits), weights to 11 bits down to
+ * 2^-22 of the largest (bf16) or to 22 bits down to 2^-11 of it (fp32).
  * With more than 16 query rows (n_new times heads per KV head), bf16 and
  * |softmax_scale| <= 1/sqrt(d), the tcgen05 form runs: a query channel is then
  * off by at most 2^-17 of its row's largest, the weights keep 11 bits down to
- * 2^-17.  The weights ride on the value scales: of two
- * blocks of a sequence whose value scales lie more than 2^100 apart (a block of
- * zeros has 2^-100) the smaller one's weights may be lost.  NaN codes (which
- * tq_kv8_append never writes) at a seen position may spoil other rows too.
+ * 2^-17.  The weights ride on the value scales: of two blocks of a sequence
+ * whose value scales lie more than 2^100 apart (a block of zeros has 2^-100)
+ * the smaller one's weights may be lost.  NaN codes (which tq_kv8_append never
+ * writes) at a seen position may spoil other rows too.
  * q, out and workspace are 16-byte aligned; calls that may overlap on the GPU
  * need a workspace each.  batch * n_new * num_q_heads is below 2^27, and
  * positions below 2^29 (else TQ_ERR_UNSUPPORTED). */
