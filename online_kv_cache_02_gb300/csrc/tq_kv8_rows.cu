@@ -608,7 +608,10 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
             }
           }
         }
-        __syncwarp();                                            // the slot has been read: the next page into it
+        // The slot has been read: the next page into it.  The fence orders the reads before the copy, which is another
+        // proxy's: without it they may sink behind it (fp32, 16 rows: now and then a run had a page wrong).
+        tcx::fence_async_smem();
+        __syncwarp();
         issue(Y::ST);
         ++used;
         if ((++k & 31) == 0) {

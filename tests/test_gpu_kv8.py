@@ -810,6 +810,26 @@ def test_results_repeat_bit_for_bit():
     assert np.array_equal(a, _attend(c, q[:, 0], "bf16", False, [4700, 900]))
 
 
+@pytest.mark.parametrize("dtype,d,h,hq,n_new,starts", [("f32", 128, 8, 32, 100, [100, 2000]), ("f32", 64, 8, 32, 50, [1500, 300]),
+                                                       ("f32", 256, 4, 16, 20, [900, 2000]), ("bf16", 128, 8, 32, 4, [9000, 500, 4000]),
+                                                       ("bf16", 256, 4, 8, 3, [5000, 70]), ("bf16", 64, 4, 16, 60, [2000, 100])])
+def test_many_runs_give_the_same_bits(dtype, d, h, hq, n_new, starts):
+    """Copies race with nothing: forty runs, and a sample of rows of each distinct result against the oracle."""
+    rng = np.random.default_rng(46)
+    b = len(starts)
+    maxp = (max(starts) + n_new) // 16 + 2
+    c = Cache(rng, b * maxp, h, d, b, maxp)
+    for i, s in enumerate(starts):
+        c.clean(rng, i, range(s + n_new))
+    c.to_device()
+    q = values(rng, dtype, b, n_new, hq, d)
+    first = _attend(c, q, dtype, True, starts)
+    _check(c, first, q, dtype, True, starts, rows={(i, t) for i in range(b) for t in (0, n_new // 2, n_new - 1)})
+    for _ in range(40):
+        assert np.array_equal(first, _attend(c, q, dtype, True, starts))
+    assert tq.tq_check_device_status(ctx_for(d)) == 0
+
+
 def test_two_streams_at_once():
     """Two calls that overlap on the GPU, each with its own workspace."""
     rng = np.random.default_rng(42)
