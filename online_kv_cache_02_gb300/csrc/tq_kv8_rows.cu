@@ -500,6 +500,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
         float s[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+        float s_lo[F32 ? NT : 1][4] = {}, s_odd[F32 ? NT : 1][4] = {};   // fp32: the low parts, and every other product
         uint32_t kw[2][Y::KW];
 #pragma unroll
         for (int r = 0; r < 2; ++r)
@@ -513,9 +514,16 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
           const uint32_t a0 = half2_of(kw[0][j]), a2 = half2_of(kw[0][j] >> 16);
           const uint32_t a1 = half2_of(kw[1][j]), a3 = half2_of(kw[1][j] >> 16);
 #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(F32 && (j & 1) ? s_odd[F32 ? nt : 0] : s[nt], a0, a1, a2, a3, qf[nt][0][j][0], qf[nt][0][j][1]);
+            if (F32) mma16816(s_lo[F32 ? nt : 0], a0, a1, a2, a3, qf[nt][HL - 1][j][0], qf[nt][HL - 1][j][1]);
+          }
+        }
+        if constexpr (F32) {
+#pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int hl = 0; hl < HL; ++hl) mma16816(s[nt], a0, a1, a2, a3, qf[nt][hl][j][0], qf[nt][hl][j][1]);
+            for (int i = 0; i < 4; ++i) s[nt][i] += s_odd[nt][i] + s_lo[nt][i];
         }
         const int j0 = 16 * page;
         // does every row see the whole page?
@@ -632,12 +640,24 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
           const uint32_t a0 = half2_of(x0), a1 = half2_of(x0 >> 16), a2 = half2_of(y0), a3 = half2_of(y0 >> 16);
           const uint32_t b0 = half2_of(x1), b1 = half2_of(x1 >> 16), b2 = half2_of(y1), b3 = half2_of(y1 >> 16);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (F32) {                                 // a page's sum by itself, added in fp32: the tensor cores' sums are cut, not rounded
+              float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int hl = 0; hl < HL; ++hl) {
-              mma16816(o[nt][2 * w], a0, a1, a2, a3, pf[nt][hl][0], pf[nt][hl][1]);
-              mma16816(o[nt][2 * w + 1], b0, b1, b2, b3, pf[nt][hl][0], pf[nt][hl][1]);
+              for (int hl = HL - 1; hl >= 0; --hl) {
+                mma16816(x, a0, a1, a2, a3, pf[nt][hl][0], pf[nt][hl][1]);
+                mma16816(y, b0, b1, b2, b3, pf[nt][hl][0], pf[nt][hl][1]);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[nt][2 * w][i] += x[i];
+                o[nt][2 * w + 1][i] += y[i];
+              }
+            } else {
+              mma16816(o[nt][2 * w], a0, a1, a2, a3, pf[nt][0][0], pf[nt][0][1]);
+              mma16816(o[nt][2 * w + 1], b0, b1, b2, b3, pf[nt][0][0], pf[nt][0][1]);
             }
+          }
         }
       }
 
