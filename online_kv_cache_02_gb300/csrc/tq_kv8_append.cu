@@ -19,9 +19,10 @@
 // block left room for eight warps an SM.)
 //
 // Bound by the memory and, close behind it, by the instructions of the two passes:
-// 8 x 4,096 tokens of 32 + 8 + 8 heads, bf16, d = 128, 755 MB: 141 us, 5.4 TB/s, 79%
+// 8 x 4,096 tokens of 32 + 8 + 8 heads, bf16, d = 128, 755 MB: 142 us, 5.3 TB/s, 78%
 // of a copy's rate (held in registers 367 us; two CTAs an SM 170 us).  fp32 with
-// three axes, 67 MB: 19 us, of which half is the launch and the last wave.  A single
+// three axes, 67 MB: 19 us (15 in L2), of which half is the launch and the last wave; the same in
+// bf16 12.  A single
 // token of 16 sequences: 5 us on the GPU, the latency of three dependent loads.
 
 #include "tq_kv8.h"
@@ -423,13 +424,14 @@ cudaError_t launch_t(const Kv8Append& a, cudaStream_t s) {
   const int npg = (a.n_new + 2 * kPage - 2) / kPage;
   const long long pages = static_cast<long long>(a.batch) * npg;
   const int tasks = (a.k ? a.H : 0) + (a.v ? a.H : 0) + (a.q ? a.Hq : 0);
-  // a block per warp while one wave of CTAs holds them; more per warp beyond, whose copies overlap the work
+  // A block per warp while one wave of CTAs holds them, two where a warp has room for the next block's copy; more per warp
+  // beyond.  bf16, 8 x 512 tokens: up to two waves 21 us, one 25, four 25; fp32, 3 x 777: 17.6 and 15.1 with one.
   int groups = (tasks + kAWarps - 1) / kAWarps;
   int per = 1;
-  while (per < 8 && pages * ((groups + per - 1) / per) > 3LL * kv8_sm_count()) per *= 2;
+  using S = Stage<D, F32>;
+  while (per < 8 && pages * ((groups + per - 1) / per) > (S::N == 2 ? 6LL : 3LL) * kv8_sm_count()) per *= 2;
   const int tpc = per * kAWarps;
   if (pages > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  using S = Stage<D, F32>;
   constexpr int kStages = kAWarps * S::N * S::BYTES;
   const size_t smem = kStages + sizeof(float) * kPage * static_cast<size_t>(a.rot);
   static std::atomic<unsigned long long> configured{0};
