@@ -31,6 +31,7 @@
 // too, at 55 to 65 TFLOP/s: eight warps an SM wait on their own chains of products.
 
 #include "tq_kv8.h"
+#include "tq_kv8_ring.h"
 #include "tq_tc.cuh"
 
 #include <cuda.h>
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
     for (int i = 0; i < Y::ST; ++i) bar_init(my_bar + 8 * i, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
-  bool failed = false;
+  PageRing<Y::ST> pages_in;                                     // this warp's
   pdl_wait();
   if (split) pdl_trigger();                                      // the join's launch, beside the work
   RSplit* records = reinterpret_cast<RSplit*>(a.part);            // one per CTA, then the partials' slots
@@ -344,16 +345,13 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
     return x;
   };
   PageInfo cur{-1, 0, 0.0f, 0.0f}, nxt = cur;
-  int k = 0, nk = 0;                                             // the warp's pages used, and how many there are
-  uint32_t used = 0;                                             // stages filled so far, by this warp, over all items
-  // page k + ahead of the warp into its ring slot (a page that is not there arrives with no bytes)
-  auto issue = [&](int ahead) {
-    if (k + ahead >= nk) return;
-    const int j = (k & 31) + ahead;
+  // page k + ahead of the warp into a stage (a page that is not there arrives with no bytes)
+  auto send = [&](int ahead, uint32_t st) {
+    const int j = (pages_in.k & 31) + ahead;
     const bool far = j >= 32;
     if (lane == (j & 31)) {
       const int blk = far ? nxt.blk : cur.blk;
-      const uint32_t st = (used + ahead) % Y::ST, bar = my_bar + 8 * st, dst = my_ring + st * Y::STAGE;
+      const uint32_t bar = my_bar + 8 * st, dst = my_ring + st * Y::STAGE;
       if (blk >= 0) {
         bar_arrive_tx(bar, Y::STAGE);
 #pragma unroll
@@ -369,11 +367,22 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   };
   auto start = [&]() {                                           // a new run of pages
     const long long n = u1 - u0_first - warp;
-    k = 0;
-    nk = n > 0 ? static_cast<int>((n + step - 1) / step) : 0;
+    const int nk = n > 0 ? static_cast<int>((n + step - 1) / step) : 0;
     cur = fetch(0);
     nxt = nk > 32 ? fetch(32) : cur;
-    for (int i = 0; i < Y::ST; ++i) issue(i);
+    pages_in.start(nk, send);
+  };
+  auto landed = [&](uint32_t st, uint32_t parity) {
+    bool gave_up = false;
+    return __all_sync(0xffffffffu, bar_wait(my_bar + 8 * st, parity, gave_up)) != 0;
+  };
+  // the page's stage is free for the next one
+  auto pass = [&]() {
+    pages_in.pass(send);
+    if ((pages_in.k & 31) == 0) {
+      cur = nxt;
+      nxt = fetch(pages_in.k + 32);
+    }
   };
   if (split) start();
 
@@ -478,19 +487,14 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
       }
       // list position of the warp's next page, and of the item's end
       const long long seg_end = split ? item_at + c1 : c1;
-      while (k < nk && u0_first + warp + static_cast<long long>(step) * k < seg_end) {
-        const int from = k & 31;
+      while (pages_in.k < pages_in.n && u0_first + warp + static_cast<long long>(step) * pages_in.k < seg_end) {
+        const int from = pages_in.k & 31;
         const int page = __shfl_sync(0xffffffffu, cur.page, from), blk = __shfl_sync(0xffffffffu, cur.blk, from);
         const float kscale = __shfl_sync(0xffffffffu, cur.ks, from), vscale = __shfl_sync(0xffffffffu, cur.vs, from);
-        const uint32_t st = used % Y::ST, kb = my_ring + st * Y::STAGE, vb = kb + Y::BLOCK;
-        if (!__all_sync(0xffffffffu, bar_wait(my_bar + 8 * st, (used / Y::ST) & 1, failed))) failed = true;
-        if (blk < 0 || failed) {                                 // flagged already: the page's tokens are not there
-          issue(Y::ST);
-          ++used;
-          if ((++k & 31) == 0) {
-            cur = nxt;
-            nxt = fetch(k + 32);
-          }
+        const uint32_t kb = my_ring + pages_in.stage() * Y::STAGE, vb = kb + Y::BLOCK;
+        if (!pages_in.land(landed)) break;
+        if (blk < 0) {                                           // flagged already: the page's tokens are not there
+          pass();
           continue;
         }
         const float evf = static_cast<float>(static_cast<int>((__float_as_uint(vscale) >> 23) & 0xFF) - 127);
@@ -620,12 +624,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
         // proxy's: without it they may sink behind it (fp32, 16 rows: now and then a run had a page wrong).
         tcx::fence_async_smem();
         __syncwarp();
-        issue(Y::ST);
-        ++used;
-        if ((++k & 31) == 0) {
-          cur = nxt;
-          nxt = fetch(k + 32);
-        }
+        pass();
         if (live != 0xFFFFu) {                                   // what no row sees may hold anything
 #pragma unroll
           for (int r = 0; r < 4; ++r)
@@ -768,12 +767,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
     }
   }
   if (split && tid == 0) records[blockIdx.x] = cut;
-  // after a wait that gave up, copies may still be on their way: they land before the CTA ends
-  if (failed) {
-    if (lane == 0) atomicOr(a.err, kErrTimeout);
-    bool f2 = false;
-    for (int i = 0; i < Y::ST; ++i) (void)bar_wait(my_bar + 8 * ((used + i) % Y::ST), ((used + i) / Y::ST) & 1, f2);
-  }
+  if (pages_in.failed && lane == 0) atomicOr(a.err, kErrTimeout);
 }
 
 // Joins the parts of the items that cross spans: a block per CTA of the first kernel, 16 / R warps per row.
