@@ -471,6 +471,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
   if (warp < 8) {
     // ---- softmax of half X (thread = row), the queries' split, the results ----------------
+    // Accesses to tensor memory are the whole warp's: behind a branch that only some lanes take they meet again first.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int X = warp >> 2, wq = warp & 3, r = 32 * wq + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * wq) << 16);
@@ -587,6 +588,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if (t == t0) rowf = rowf_sm[r];
           __syncwarp();
           if (lane == 0 && t + dt >= ntile) bar_arrive(bar(bQFree));
+          __syncwarp();
         }
         const TileDesc& d = descs[seq % L::DESCS];
         // never zero (a hidden score stays -inf), and NaN stays NaN
@@ -662,6 +664,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               m = mx + kHead;
               l *= alpha;
             }
+            __syncwarp();
             if (t > t0) {                              // O of the tiles before (their MMAs have run: S came after)
 #pragma unroll 1
               for (int c = 0; c < L::DV / 16; ++c) {
@@ -748,6 +751,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         tc_before();
         __syncwarp();
         if (lane == 0) bar_arrive(bar(bOFree));
+        __syncwarp();
       }
       const float inv = l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
       float* part = parts + (static_cast<long long>(done_item.slot) * L::ROWS + (turns ? 0 : 128 * X) + r) * L::PART;
@@ -755,8 +759,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       for (int c = 0; c < L::DV / 32; ++c) {
         float o[32];
         tld32(to + 32u * c, o);
-        if (!done_row.live) continue;
-        if (done_item.slot < 0) {
+        if (done_row.live && done_item.slot < 0) {
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -772,12 +775,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
             for (int k = 0; k < 4; ++k)
               reinterpret_cast<uint4*>(dst)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
           }
-        } else {
+        } else if (done_row.live) {
           float4* dst = reinterpret_cast<float4*>(part + 4 + 32 * c);
 #pragma unroll
           for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           if (c == 0) *reinterpret_cast<float2*>(part) = make_float2(m, l);
         }
+        __syncwarp();                                  // lanes with no row wait: the loads are the whole warp's
       }
       tc_before();                                     // O is read before the next item's first P is announced
     }
