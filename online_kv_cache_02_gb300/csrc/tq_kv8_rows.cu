@@ -102,8 +102,8 @@ __device__ __forceinline__ void tma_panel(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_sync() {                  // lanes may come to it apart (a loop with a share of the rows)
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
 // Shared-memory address `p` of the cluster's CTA `rank`, and loads from it.
 __device__ __forceinline__ uint32_t map_cluster(uint32_t p, int rank) {
@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
     if ((pages_in.k & 31) == 0) {
       cur = nxt;
       nxt = fetch(pages_in.k + 32);
+      __syncwarp();                                              // MMAs are the whole warp's: its lanes meet first, here and below
     }
   };
   if (split) start();
@@ -586,6 +587,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
               w[nt][c] = exp2_fast(s[nt][c] - base);
               w[nt][2 + c] = exp2_fast(s[nt][2 + c] - base);
             }
+          __syncwarp();
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -631,6 +633,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
             if (!((live >> (2 * t + (r & 1) + 8 * (r >> 1))) & 1u))
 #pragma unroll
               for (int w = 0; w < Y::VW; ++w) vw[r][w] = 0u;
+          __syncwarp();
         }
 #pragma unroll
         for (int w = 0; w < Y::VW; ++w) {

@@ -35,3 +35,14 @@ def test_decode_rows_that_fill_no_warp(d, hq):
     rng = np.random.default_rng(61)
     _decode_case(rng, "bf16", d, 1, hq, [1, 0, 100, 1500])
     _decode_case(rng, "bf16", d, 2, 2 * hq, [5000])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("g", [1, 3, 5, 11])
+def test_decode_short_contexts_with_odd_rows(dtype, d, g):
+    """A cluster's CTAs share out an item's rows: shares that end inside a warp, and CTAs with none."""
+    rng = np.random.default_rng(62)
+    for lens in ([700], [400, 0, 33], [2500]):
+        _decode_case(rng, dtype, d, 1, g, lens)
+    _decode_case(rng, dtype, d, 1, g, [2500], window=300, sinks=3)
