@@ -833,7 +833,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
       int seq = 0, n = 0, nk = 0;                      // tiles, items, and tiles whose copies were issued
       int free0 = 0, free1 = 0, free2 = 0;             // the steps after which the keys of the last three tiles are read
       auto publish = [&](const ItemMsg& x) {
-        if (n >= kItems) (void)wait(bItemFree + n % kItems, n / kItems - 1);   // every warp has taken the one before
+        // Every warp has taken the one before.  If one has not within the limit, its room stays as it is (a message read
+        // half old, half new would send rows anywhere), and the others' waits for this one give up too.
+        if (n >= kItems && !__all_sync(0xffffffffu, wait_short(bar(bItemFree + n % kItems), (n / kItems - 1) & 1))) {
+          failed = true;
+          return;
+        }
         if (lane == 0) {
           item_ring[n % kItems] = x;
           bar_arrive(bar(bItem + n % kItems));
