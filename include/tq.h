@@ -415,7 +415,10 @@ tq_status tq_kv8_append(const tq_ctx* ctx, const tq_kv8_cache* cache, const void
                         const int32_t* new_lens, const tq_rope* rope, void* q_out, long long k_stride,
                         long long v_stride, long long q_stride, void* stream);
 
-/* Workspace bytes of the two attention calls below (decode: n_new = 1). */
+/* Workspace bytes of the two attention calls below (decode: n_new = 1): enough
+ * for either dtype and every softmax_scale, and never less than for a smaller
+ * batch, n_new, num_q_heads or max_seq_len, so that a program sizes one buffer
+ * for its largest calls.  A call refuses only what is too small for itself. */
 tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_new, int num_q_heads, int num_kv_heads,
                                 int max_seq_len, size_t* bytes);
 

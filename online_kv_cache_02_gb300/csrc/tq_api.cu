@@ -956,9 +956,12 @@ tq_status kv8_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void
   // positions lie below both: a window or sinks beyond them change nothing (and the kernels' sums stay in 32 bits)
   const long long cap = std::min<long long>(max_seq_len, static_cast<long long>(kPage) * cache->max_pages_per_seq);
   if (cap > (1LL << 29) || (cap / kPage + 64) * H > 0x7FFFFFFFLL) return TQ_ERR_UNSUPPORTED;
-  size_t need = 0;
-  st = tq_kv8_workspace_size(ctx, batch, n_new, Hq, H, max_seq_len, &need);
-  if (st != TQ_OK) return st;
+  const int d = ctx->cfg.d;
+  const bool f32 = dtype == TQ_F32, tc = kv8_tc_takes(n_new, Hq / H, d, f32, softmax_scale);
+  const size_t need = !tc ? kv8_rows_workspace(n_new, Hq / H, d)
+                      : kv8_tc_splits(batch, n_new, Hq / H, max_seq_len, d)
+                          ? kv8_tc_workspace(batch, n_new, Hq / H, H, max_seq_len, d)
+                          : 0;
   if (workspace_bytes < need) return TQ_ERR_WORKSPACE;
   st = on_device(ctx);
   if (st != TQ_OK) return st;
@@ -986,10 +989,8 @@ tq_status kv8_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.part = static_cast<float*>(workspace);
   a.err = ctx->tab.err;
-  const bool f32 = dtype == TQ_F32;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (kv8_tc_takes(n_new, a.G, ctx->cfg.d, f32, softmax_scale)) return cuda_status(launch_kv8_tc(a, ctx->cfg.d, s));
-  return cuda_status(launch_kv8_rows(a, ctx->cfg.d, f32, s));
+  return cuda_status(tc ? launch_kv8_tc(a, d, s) : launch_kv8_rows(a, d, f32, s));
 }
 }  // namespace
 
@@ -1071,8 +1072,13 @@ extern "C" tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_n
   if (!ctx || !bytes || batch < 0 || n_new < 1 || Hq < 1 || H < 1 || Hq % H || max_seq_len < 0)
     return TQ_ERR_INVALID_ARG;
   if (!kv8_head_dim(ctx->cfg.d)) return TQ_ERR_UNSUPPORTED;
-  *bytes = std::max(kv8_rows_workspace(batch, n_new, Hq / H, H, ctx->cfg.d),
-                    kv8_tc_workspace(batch, n_new, Hq / H, H, max_seq_len, ctx->cfg.d));
+  // What any call of these sizes uses, whatever its dtype and scale, and no less than for smaller sizes: one row counts too
+  // (the blocks of 8 rows of the mma.sync form can take more than those of 16), and so does a tcgen05 call whose list is
+  // too long to be split, though it uses nothing.
+  const int d = ctx->cfg.d, G = Hq / H;
+  size_t n = std::max(kv8_rows_workspace(1, 1, d), kv8_rows_workspace(n_new, G, d));
+  if (static_cast<long long>(n_new) * G > kTcRows) n = std::max(n, kv8_tc_workspace(batch, n_new, G, H, max_seq_len, d));
+  *bytes = n;
   return TQ_OK;
 }
 

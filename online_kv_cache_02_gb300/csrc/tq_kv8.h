@@ -87,13 +87,16 @@ __device__ __forceinline__ Kv8Range kv8_range(int window, int sinks, int pmin, i
 bool kv8_head_dim(int d);
 int kv8_sm_count();                      // of the current device
 cudaError_t launch_kv8_append(const Kv8Append& a, int d, bool f32, cudaStream_t s);
-size_t kv8_rows_workspace(int B, int T, int G, int H, int d);
+size_t kv8_rows_workspace(int T, int G, int d);
 cudaError_t launch_kv8_rows(const Kv8Attn& a, int d, bool f32, cudaStream_t s);
 // TMA map of a cache's blocks: coordinates (channel, token, block), boxes of one block's 128-channel panel.
 bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d);
 // Many query rows on the tensor cores (tq_kv8_tc.cu): whether the call takes
-// that form, its workspace and its launch.
+// that form (it has more than kTcRows query rows per KV head, among others),
+// whether it then uses a workspace, its size and its launch.
+constexpr int kTcRows = 16;
 bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale);
+bool kv8_tc_splits(int B, int T, int G, int max_seq_len, int d);
 size_t kv8_tc_workspace(int B, int T, int G, int H, int max_seq_len, int d);
 cudaError_t launch_kv8_tc(const Kv8Attn& a, int d, cudaStream_t s);
 

@@ -914,9 +914,7 @@ cudaError_t launch_d(const Kv8Attn& a, bool f32, cudaStream_t s) {
 
 bool kv8_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
 
-size_t kv8_rows_workspace(int B, int T, int G, int H, int d) {
-  (void)B;
-  (void)H;
+size_t kv8_rows_workspace(int T, int G, int d) {
   const int R = rows_per_block(T, G, d);
   return static_cast<size_t>(ctas_per_sm(d, R)) * kv8_sm_count() * (sizeof(RSplit) + 2 * sizeof(float) * R * (d + 4));
 }

@@ -1212,13 +1212,14 @@ bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d)
 // 133 and 108, 64 rows 339 and 115.  A larger scale would make the query's
 // rounding to two e4m3 parts count.
 bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale) {
-  return !f32 && static_cast<long long>(T) * G > 16 && softmax_scale != 0.0f &&
+  return !f32 && static_cast<long long>(T) * G > kTcRows && softmax_scale != 0.0f &&
          std::fabs(static_cast<double>(softmax_scale)) <= (1.0 + 1e-6) / std::sqrt(static_cast<double>(d));
 }
 
+bool kv8_tc_splits(int B, int T, int G, int max_seq_len, int d) { return splits(B, query_blocks(T, G, d), max_seq_len); }
+
 size_t kv8_tc_workspace(int B, int T, int G, int H, int max_seq_len, int d) {
   const int nqb = query_blocks(T, G, d);
-  if (!splits(B, nqb, max_seq_len)) return 16;
   return static_cast<size_t>(ctas_for(B, H * items_per_head(d), nqb, max_seq_len)) *
          (sizeof(TSplit) + 2 * sizeof(float) * static_cast<size_t>(rows_of(d)) * (d / items_per_head(d) + 4));
 }
