@@ -939,6 +939,12 @@ tq_status rope_check(const tq_rope* r, int d) {
   return r->num_axes == 1 || sum == r->rot_dim / 2 ? TQ_OK : TQ_ERR_INVALID_ARG;
 }
 
+// Query rows of an attention call: below 2^27, for the kernels' 32-bit sums.  (The product of all three can pass 64 bits.)
+bool kv8_rows_fit(int batch, int n_new, int Hq) {
+  const long long tokens = static_cast<long long>(batch) * n_new;
+  return tokens < (1LL << 27) && tokens * Hq < (1LL << 27);
+}
+
 tq_status kv8_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* q, tq_dtype dtype, int batch, int n_new,
                         int Hq, const int32_t* lens, const int32_t* new_lens, bool decode, int max_seq_len, int window,
                         int sinks, float softmax_scale, void* out, void* workspace, size_t workspace_bytes,
@@ -952,7 +958,7 @@ tq_status kv8_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void
   if (batch == 0) return TQ_OK;
   if (!q || !lens || !out || !workspace || misaligned(q) || misaligned(out) || misaligned(workspace))
     return TQ_ERR_INVALID_ARG;
-  if (static_cast<long long>(batch) * n_new * Hq >= (1LL << 27)) return TQ_ERR_UNSUPPORTED;
+  if (!kv8_rows_fit(batch, n_new, Hq)) return TQ_ERR_UNSUPPORTED;
   // positions lie below both: a window or sinks beyond them change nothing (and the kernels' sums stay in 32 bits)
   const long long cap = std::min<long long>(max_seq_len, static_cast<long long>(kPage) * cache->max_pages_per_seq);
   if (cap > (1LL << 29) || (cap / kPage + 64) * H > 0x7FFFFFFFLL) return TQ_ERR_UNSUPPORTED;
@@ -1071,7 +1077,7 @@ extern "C" tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_n
                                            size_t* bytes) {
   if (!ctx || !bytes || batch < 0 || n_new < 1 || Hq < 1 || H < 1 || Hq % H || max_seq_len < 0)
     return TQ_ERR_INVALID_ARG;
-  if (!kv8_head_dim(ctx->cfg.d)) return TQ_ERR_UNSUPPORTED;
+  if (!kv8_head_dim(ctx->cfg.d) || !kv8_rows_fit(batch, n_new, Hq)) return TQ_ERR_UNSUPPORTED;
   // What any call of these sizes uses, whatever its dtype and scale, and no less than for smaller sizes: one row counts too
   // (the blocks of 8 rows of the mma.sync form can take more than those of 16), and so does a tcgen05 call whose list is
   // too long to be split, though it uses nothing.

@@ -39,3 +39,12 @@ def test_a_call_asks_for_no_workspace_of_a_form_that_it_does_not_take(f):
     assert ask(sixteen, 1000, scale=0.05) == ask(many - 1, 1000, scale=0.05) == tq.TQ_ERR_WORKSPACE
     assert ask(many, 1000, scale=0.05) == tq.TQ_ERR_CUDA
     assert ask(many, 1000, scale=0.05) == ask(many, 8, scale=0.05) == tq.TQ_ERR_CUDA
+
+
+@pytest.mark.parametrize("batch,n_new,hq", [(2 ** 31 - 1, 2 ** 31 - 1, 4), (2 ** 31 - 1, 2 ** 31 - 1, 8), (2 ** 30, 2 ** 30, 16),
+                                            (2 ** 30, 2 ** 31 - 1, 32), (1 << 26, 1, 4), (1, 1 << 26, 4)])
+def test_sizes_whose_product_passes_64_bits_are_refused(f, batch, n_new, hq):
+    n = ctypes.c_size_t()
+    assert tq.raw_status("tq_kv8_workspace_size", f.ctx, batch, n_new, hq, 4, 100, ctypes.byref(n)) == tq.TQ_ERR_UNSUPPORTED
+    for dtype in (0, 1):
+        assert _attend(f, True, batch=batch, n_new=n_new, hq=hq, dtype=dtype, ws_bytes=2 ** 63) == tq.TQ_ERR_UNSUPPORTED
