@@ -90,6 +90,7 @@ __device__ __forceinline__ float exp2_fast(float x) {            // relative err
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float finite_factor(float f) { return fmaxf(fminf(f, 3.4028234e38f), -3.4028234e38f); }
 __device__ __forceinline__ uint32_t pack(__half lo, __half hi) {
   const __half2 h = __halves2half2(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -534,10 +535,14 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
         // does every row see the whole page?
         const bool full = j0 + 15 <= it.pmin && (!a.window || j0 > it.pmax - a.window || j0 + 15 < a.sinks);
         uint32_t live = 0xFFFFu;                                 // tokens that some row sees
+        // The factors first: they cancel where small queries meet large keys, and the sum times one of them could pass fp32.
+        // One that is too large for fp32 leaves zeros zero.
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][i] = s[nt][i] * kscale * rf[nt][i & 1];
+        for (int nt = 0; nt < NT; ++nt) {
+          const float f0 = finite_factor(kscale * rf[nt][0]), f1 = finite_factor(kscale * rf[nt][1]);
+          s[nt][0] *= f0, s[nt][2] *= f0;
+          s[nt][1] *= f1, s[nt][3] *= f1;
+        }
         if (!full) {
           live = 0u;
 #pragma unroll

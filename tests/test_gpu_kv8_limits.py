@@ -46,3 +46,106 @@ def test_decode_short_contexts_with_odd_rows(dtype, d, g):
     for lens in ([700], [400, 0, 33], [2500]):
         _decode_case(rng, dtype, d, 1, g, lens)
     _decode_case(rng, dtype, d, 1, g, [2500], window=300, sinks=3)
+
+
+# ---------------------------------------------------------------------------
+# sizes of values
+# ---------------------------------------------------------------------------
+# (dtype, d, query heads of the one KV head): mma.sync in both types, tcgen05 with the halves in turn and with both halves' rows
+FORMS = [("bf16", 128, 4), ("f32", 128, 4), ("f32", 64, 11), ("bf16", 64, 20), ("bf16", 128, 20), ("bf16", 256, 20),
+         ("bf16", 64, 150), ("bf16", 128, 150), ("bf16", 256, 150)]
+
+
+def _one_head(rng, d, n, pages=None, maxp=None):
+    pages = pages or (n + 15) // 16 + 1
+    c = Cache(rng, pages, 1, d, 1, maxp or pages)
+    c.clean(rng, 0, range(n))
+    return c
+
+
+def _tails(c, x, p, scale):
+    """Per row, what weights below the normal numbers of fp16 add to a bound: half a step of the subnormals is 2^-25, and
+    the largest weight 2^3 at least (tcgen05; 2^8 on mma.sync), so each key's weight is off by 2^-28 of the largest
+    weight times its code."""
+    j = np.arange(p + 1)
+    pg, sl = c.table[0][j // 16], j % 16
+    k = kv8.VALUES[c.codes["k"][pg, 0, sl]] * c.scales["k"][pg, 0].astype(np.float64)[:, None]
+    vc, vs = kv8.VALUES[c.codes["v"][pg, 0, sl]], c.scales["v"][pg, 0].astype(np.float64)
+    out = []
+    for row in x.astype(np.float64):
+        s = (k @ row) * scale
+        w = np.exp(s - s.max())
+        out.append(2.0 ** -28 * (w / w.sum() * vs).max() * np.abs(vc).sum(axis=0))
+    return np.stack(out)
+
+
+def _check_one(c, got, x, dtype, p, two_parts=None):
+    scale = 1.0 / np.sqrt(c.d)
+    want, mag, dots, ksum, n = kv8.attention(x, c.codes["k"], c.scales["k"], c.codes["v"], c.scales["v"], c.table[0], p, 0, 0, scale)
+    two_parts = dtype == "bf16" and len(x) > 16 if two_parts is None else two_parts
+    parts = 2.0 ** -17 * np.abs(x).max(axis=-1) * ksum if two_parts else 0.0
+    tol = _bound(dtype, want, mag, dots, n, c.d, scale, parts) + _tails(c, x, p, scale)
+    err = np.abs(got - want)
+    assert np.all(err <= tol), (float(np.nanmax(err / tol)), int(np.isnan(got).sum()), np.argwhere(~(err <= tol))[:4].tolist())
+
+
+@pytest.mark.parametrize("dtype,d,g", FORMS)
+@pytest.mark.parametrize("n", [100, 310, 5000])
+def test_value_scales_far_apart(dtype, d, g, n):
+    """Value scales 2^-50 to 2^49, queries from 2^-100 to 2^20 and zero: each half of an item and each part of a split one
+    has a maximum of its own."""
+    rng = np.random.default_rng(70)
+    c = _one_head(rng, d, n)
+    c.scales["v"][:] = np.exp2(rng.integers(-50, 50, c.scales["v"].shape))
+    c.scales["k"][:] = np.exp2(rng.integers(-40, -6, c.scales["k"].shape))
+    c.to_device()
+    q = values(rng, dtype, 1, g, d)
+    q[0, 1] *= 2.0 ** -100
+    q[0, 2] *= 2.0 ** 20
+    q[0, 3] = 0
+    q[0, 4::7] *= 2.0 ** 9
+    got = _attend(c, q, dtype, False, [n])
+    assert tq.tq_check_device_status(ctx_for(d)) == 0
+    _check_one(c, got[0], q[0], dtype, n - 1)
+
+
+@pytest.mark.parametrize("dtype,d,g", FORMS)
+def test_blocks_of_zeros_keep_their_weight(dtype, d, g):
+    """Zero values have the smallest scale, 2^-100: their weights count in the sum all the same."""
+    rng = np.random.default_rng(71)
+    c = _one_head(rng, d, 310)
+    zero = c.table[0][[1, 3, 8, 9, 12]]
+    c.codes["v"][zero] = 0
+    c.scales["v"][zero] = 2.0 ** -100
+    c.scales["v"][c.table[0][5]] = 2.0 ** -9
+    c.to_device()
+    q = values(rng, dtype, 1, g, d)
+    _check_one(c, _attend(c, q, dtype, False, [310])[0], q[0], dtype, 309)
+
+
+@pytest.mark.parametrize("dtype,d,g", FORMS)
+def test_tiny_queries_against_huge_keys(dtype, d, g):
+    """Scores of usual size from queries of 2^-106 and keys of 2^111: no product on the way may pass fp32."""
+    rng = np.random.default_rng(72)
+    c = _one_head(rng, d, 310)
+    c.scales["k"][:] = 2.0 ** 106
+    c.scales["k"][c.table[0][::3]] = 2.0 ** 104
+    c.to_device()
+    q = values(rng, dtype, 1, g, d) * np.float32(2.0 ** -106)
+    _check_one(c, _attend(c, q, dtype, False, [310])[0], q[0], dtype, 309)
+
+
+@pytest.mark.parametrize("dtype,d,g", FORMS)
+@pytest.mark.parametrize("n", [60, 310, 5000])
+def test_a_query_that_is_not_finite_spoils_only_its_row(dtype, d, g, n):
+    rng = np.random.default_rng(75)
+    c = _one_head(rng, d, n)
+    c.to_device()
+    q = values(rng, dtype, 1, g, d)
+    bad = {0: np.nan, 2: np.inf, 3: -np.inf, g - 1: np.nan}
+    for r, x in bad.items():
+        q[0, r, (5 + r) % d] = x
+    got = _attend(c, q, dtype, False, [n])
+    assert np.isnan(got[0, list(bad)]).all()
+    keep = [r for r in range(g) if r not in bad]
+    _check_one(c, got[0, keep], q[0, keep], dtype, n - 1, two_parts=dtype == "bf16" and g > 16)
