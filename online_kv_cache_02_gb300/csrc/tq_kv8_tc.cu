@@ -591,8 +591,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
           __syncwarp();
         }
         const TileDesc& d = descs[seq % L::DESCS];
-        // never zero (a hidden score stays -inf), and NaN stays NaN
-        auto factor = [&](int pg) { return fmaxf(d.fac[pg] * rowf, 1.2e-38f) + (rowf - rowf); };
+        // never zero (a hidden score stays -inf) nor infinite (a score of zero stays zero), and NaN stays NaN
+        auto factor = [&](int pg) { return fminf(fmaxf(d.fac[pg] * rowf, 1.2e-38f), 3.4028234e38f) + (rowf - rowf); };
         // The tile as it mostly is: every token seen and no score far above the maximum so far.  The weights by the
         // old maximum tell by themselves: a page's sum below kFull means that each fits fp16.  No maximum is taken.
         bool done = false;

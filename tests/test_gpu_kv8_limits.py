@@ -149,3 +149,26 @@ def test_a_query_that_is_not_finite_spoils_only_its_row(dtype, d, g, n):
     assert np.isnan(got[0, list(bad)]).all()
     keep = [r for r in range(g) if r not in bad]
     _check_one(c, got[0, keep], q[0, keep], dtype, n - 1, two_parts=dtype == "bf16" and g > 16)
+
+
+@pytest.mark.parametrize("dtype,d,g", FORMS)
+def test_keys_of_zeros_beside_huge_ones(dtype, d, g):
+    """Scores beyond fp32 on one side (minus infinity there, weight zero) and exact zeros in the same block."""
+    rng = np.random.default_rng(73)
+    n = 310
+    c = _one_head(rng, d, n)
+    q = np.zeros((1, g, d), np.float32)
+    q[..., 0] = 2.0 ** 20
+    c.codes["k"][:, :, :, 0] = 0x7E                 # the largest code
+    q[..., 0] *= -1
+    c.codes["k"][c.table[0][2], 0, 3] = 0           # three keys of zeros
+    c.codes["k"][c.table[0][11], 0, [0, 15]] = 0
+    c.scales["k"][:] = 2.0 ** 119
+    c.to_device()
+    got = _attend(c, q, dtype, False, [n])
+    v = lambda pg, s: kv8.VALUES[c.codes["v"][c.table[0][pg], 0, s]] * c.scales["v"][c.table[0][pg], 0]  # noqa: E731
+    three = np.stack([v(2, 3), v(11, 0), v(11, 15)]).astype(np.float64)
+    # weights of a third, each off by 2^-11 (bf16; 2^-21), and the output's rounding; subnormal weights: none
+    tol = np.abs(three.mean(0)) * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) + np.abs(three).mean(0) * (
+        (2.0 ** -11 if dtype == "bf16" else 2.0 ** -21) + 2.0 ** -19)
+    assert np.all(np.abs(got[0] - three.mean(0)) <= tol)
