@@ -63,7 +63,7 @@ constexpr int kTTok = 128;                // tokens per tile
 constexpr int kTPg = kTTok / kPage;       // pages per tile
 constexpr int kTThreads = 512;
 constexpr int kItems = 4;                 // items announced ahead
-constexpr float kMNone = -1.0e30f;
+constexpr float kMNone = -3.0e38f;         // a maximum before any score: finite, and below the scores of fp32
 // Weights are 2^(kLift + score - M).  M is set kHead above the largest score met, so that it seldom moves again: the
 // largest weight is then 2^3, and fp16 keeps 11 bits down to 2^-17 of it.  M moves when a page's 16 weights sum to more
 // than kFull, below the end of fp16: the largest of them is then 2^11.9 at least, a score above M + kSlack.

@@ -172,3 +172,20 @@ def test_keys_of_zeros_beside_huge_ones(dtype, d, g):
     tol = np.abs(three.mean(0)) * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) + np.abs(three).mean(0) * (
         (2.0 ** -11 if dtype == "bf16" else 2.0 ** -21) + 2.0 ** -19)
     assert np.all(np.abs(got[0] - three.mean(0)) <= tol)
+
+
+@pytest.mark.parametrize("dtype,d,g", FORMS)
+@pytest.mark.parametrize("best", [0, 17, 140, 309])
+def test_scores_far_below_zero(dtype, d, g, best):
+    """Every score near -2^116 but one at -2^110: that one's value is the result."""
+    rng = np.random.default_rng(74)
+    n = 310
+    c = _one_head(rng, d, n)
+    c.codes["k"][:] = 0x7E
+    c.scales["k"][:] = 2.0 ** 104
+    c.codes["k"][c.table[0][best // 16], 0, best % 16] = 0x4E           # 7 = 448 / 64
+    c.to_device()
+    q = np.full((1, g, d), -(2.0 ** -1), np.float32)
+    got = _attend(c, q, dtype, False, [n])
+    want = kv8.VALUES[c.codes["v"][c.table[0][best // 16], 0, best % 16]] * c.scales["v"][c.table[0][best // 16], 0]
+    assert np.all(np.abs(got[0] - want) <= np.abs(want) * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -22))
