@@ -67,6 +67,10 @@ constexpr int kDirectOne = 64, kDirectFew = 48, kDirectMany = 32;
 // 2^8, and fp16 keeps 11 bits of them down to 2^-22 of it.  M moves once a weight passes kFull, below the end of fp16:
 // that score lies above M + kSlack.
 constexpr float kLift = 11.0f, kHead = 3.0f, kSlack = 4.5f, kFull = 61000.0f;
+// M adds an exponent to a score, which one fp32 number holds up to some size: at scores of 2^27 a weight was 2^16, past
+// fp16, or 0.  A CTA that meets an M beyond kBig does its part of the item once more, without exponents in the weights.
+// (M in two numbers instead, in the page loop: 0.3 to 0.9 us more for every call.)
+constexpr float kBig = 65536.0f;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -480,6 +484,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
         }
       }
       float o[NT][Y::MT][4], m[NT][2], l[NT][2];
+      bool big = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -580,6 +585,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
               for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
               if (mx > m[nt][c] + kSlack) {
                 const float mn = mx + kHead, al = exp2_fast(m[nt][c] - mn);
+                big |= fabsf(mn) > kBig;
                 l[nt][c] *= al;
 #pragma unroll
                 for (int i = 0; i < Y::MT; ++i) {
@@ -686,7 +692,79 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
             *reinterpret_cast<float4*>(sm + (warp * R + row) * D + Y::v_ch(g, w)) =
                 make_float4(o[nt][2 * w][c], o[nt][2 * w][2 + c], o[nt][2 * w + 1][c], o[nt][2 * w + 1][2 + c]);
         }
-      __syncthreads();
+      if (__builtin_expect(__syncthreads_or(big), 0)) {
+        // ---- scores beyond kBig: this part again, a row per warp, the weights by the plain maximum -----------
+        // (as M = maximum + kLift + 8 of the join: the weights are at most 2^-8, the values have their scales)
+        constexpr int kC = D / 32;                               // channels per lane
+        for (int row = warp; row < rows; row += kRWarps) {
+          const int gr = it.rb * R + row, tok = gr / a.G;
+          const long long at = ((static_cast<long long>(it.b) * a.T + tok) * a.Hq + it.h * a.G + (gr - tok * a.G)) * D + kC * lane;
+          float x[kC], mx = 0.0f, top = -INFINITY, sum = 0.0f, acc[kC] = {};
+#pragma unroll
+          for (int i = 0; i < kC; ++i) {
+            x[i] = F32 ? static_cast<const float*>(a.q)[at + i] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at + i]);
+            mx = fmaxf(mx, fabsf(x[i]));
+          }
+          // the row by a power of two, so that no product passes fp32 that the score does not
+          mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+          int e = 14 - (static_cast<int>(__float_as_uint(mx) >> 23) - 127);
+          e = mx > 0.0f && mx <= 3.4028234e38f ? (e > 120 ? 120 : e) : 0;
+#pragma unroll
+          for (int i = 0; i < kC; ++i) x[i] *= __int_as_float((e + 127) << 23);
+          const float rowf = a.scale_log2 * __int_as_float((127 - e) << 23);
+          const int p = it.p0 + tok;
+#pragma unroll 1
+          for (int c = c0; c < c1; ++c) {
+            if (!split && c / kRWarps % cluster != rank) continue;
+            const int page = c < it.r.ns ? c : c - it.r.ns + it.r.w0, pid = a.bt[static_cast<long long>(it.b) * a.maxp + page];
+            if (pid < 0 || pid >= a.num_pages) continue;         // flagged already
+            const long long blk = static_cast<long long>(pid) * a.H + it.h;
+            const float f = finite_factor(a.ks[blk] * rowf), vs = a.vs[blk];
+#pragma unroll 1
+            for (int i = 0; i < kPage; ++i) {
+              const int j = kPage * page + i;
+              if (!(j <= p && (!a.window || j > p - a.window || j < a.sinks))) continue;
+              const long long from = (blk * kPage + i) * D + kC * lane;
+              float kv[2][kC];                                   // the token's codes, of keys and of values
+#pragma unroll
+              for (int n = 0; n < kC; n += 2) {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                  const uint32_t h2 = half2_of(*reinterpret_cast<const unsigned short*>((w ? a.vc : a.kc) + from + n));
+                  const float2 two = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                  kv[w][n] = two.x, kv[w][n + 1] = two.y;
+                }
+              }
+              float dot = 0.0f;
+#pragma unroll
+              for (int n = 0; n < kC; ++n) dot = fmaf(x[n], kv[0][n], dot);
+#pragma unroll
+              for (int n = 16; n > 0; n >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, n);
+              const float score = __fmul_rn(dot, f);
+              if (score > top) {
+                const float al = exp2_fast(top - score);
+                sum *= al;
+#pragma unroll
+                for (int n = 0; n < kC; ++n) acc[n] *= al;
+                top = score;
+              }
+              const float w = score == -INFINITY ? 0.0f : exp2_fast(__fsub_rn(score, top) - 8.0f);
+              sum += w;
+#pragma unroll
+              for (int n = 0; n < kC; ++n) acc[n] = fmaf(w, kv[1][n] * vs, acc[n]);
+            }
+          }
+          if (lane < kRWarps) {
+            s_ml[lane][row][0] = lane ? -INFINITY : top + (kLift + 8.0f);
+            s_ml[lane][row][1] = lane ? 0.0f : sum;
+          }
+#pragma unroll
+          for (int w = 0; w < kRWarps; ++w)
+#pragma unroll
+            for (int n = 0; n < kC; ++n) sm[(w * R + row) * D + kC * lane + n] = w ? 0.0f : acc[n];
+        }
+        __syncthreads();
+      }
       // four channels of one row's result
       auto store_row = [&](int row, int ch, float4 acc, float L) {
         const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;

@@ -189,3 +189,37 @@ def test_scores_far_below_zero(dtype, d, g, best):
     got = _attend(c, q, dtype, False, [n])
     want = kv8.VALUES[c.codes["v"][c.table[0][best // 16], 0, best % 16]] * c.scales["v"][c.table[0][best // 16], 0]
     assert np.all(np.abs(got[0] - want) <= np.abs(want) * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -22))
+
+
+@pytest.mark.parametrize("dtype,d,g", FORMS[:3])
+@pytest.mark.parametrize("n", [60, 310, 5000])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_the_largest_scores_win_at_every_size(dtype, d, g, n, sign):
+    """Scores of 2^12 to 2^110: a few keys share the largest one exactly, every other lies far below.  The result is the
+    mean of those keys' values, whatever the scales of their blocks."""
+    rng = np.random.default_rng(76)
+    for size in (12, 15, 17, 20, 23, 24, 25, 26, 27, 28, 29, 30, 31, 32, 33, 35, 40, 64, 110):
+        c = _one_head(rng, d, n)
+        c.scales["v"][:] = np.exp2(rng.integers(-50, 50, c.scales["v"].shape))
+        step = rng.integers(0, 2, c.scales["k"].shape)
+        c.scales["k"][:] = np.exp2(step + size // 2)
+        best = sorted({int(x) for x in rng.integers(0, n, 4)} | {n - 1})
+        # channel 0 decides: 64 times the smaller scale for the best, half (or, against a negative query, twice) for others
+        for kv in range(n):
+            pg, s = c.table[0][kv // 16], kv % 16
+            v = 64.0 if kv in best else 32.0 if sign > 0 else 128.0
+            c.codes["k"][pg, 0, s, 0] = kv8.e4m3_encode([v / 2.0 ** step[pg, 0]])[0]
+        c.to_device()
+        q = np.zeros((1, g, d), np.float32)
+        q[..., 0] = sign * 2.0 ** (size - size // 2 - 3)
+        got = _attend(c, q, dtype, False, [n])[0]
+        pg, s = c.table[0][np.asarray(best) // 16], np.asarray(best) % 16
+        codes, scales = kv8.VALUES[c.codes["v"][pg, 0, s]], c.scales["v"][pg, 0].astype(np.float64)
+        v = codes * scales[:, None]
+        # each rounding of a weight, of the exponents' sum (2^-21 of the score while one number holds it) and of the
+        # result; weights below the normal ones as in _tails
+        w = (2.0 ** -11 if dtype == "bf16" else 2.0 ** -21) + 2 * 2.0 ** (min(size, 17) + 1 - 21)
+        tol = np.abs(v.mean(0)) * (2.0 ** -8 if dtype == "bf16" else 2.0 ** -24) + np.abs(v).mean(0) * w + (
+            2.0 ** -28 * scales.max() * np.abs(codes).mean(0))
+        err = np.abs(got - v.mean(0))
+        assert np.all(err <= tol), (size, best, float(np.nanmax(err / tol)), int(np.isnan(got).sum()))
