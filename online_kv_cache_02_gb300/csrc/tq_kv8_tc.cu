@@ -68,6 +68,9 @@ constexpr float kMNone = -3.0e38f;         // a maximum before any score: finite
 // largest weight is then 2^3, and fp16 keeps 11 bits down to 2^-17 of it.  M moves when a page's 16 weights sum to more
 // than kFull, below the end of fp16: the largest of them is then 2^11.9 at least, a score above M + kSlack.
 constexpr float kSlack = 4.5f, kLift = 7.0f, kHead = 4.0f, kFull = 61000.0f;
+// M adds an exponent to a score, which one fp32 number holds up to some size (at scores of 2^27 the weights were past fp16
+// or 0).  Beyond kBig a row's M is a score, and an exponent, a whole number in [-96, 123], beside it.
+constexpr float kBig = 65536.0f;
 constexpr int kMaxBlocks = 2048;          // (sequence, query block) pairs that the split form lists
 constexpr int kItemCost = 5;              // an item's start and end, in tiles' time
 constexpr int kMinSpan = 2 + kItemCost;   // a CTA's share of the list at least
@@ -578,7 +581,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const int p = row.p;
       const bool turns = it.rows <= 128;               // the halves take the tiles in turn
       const int t0 = turns ? X : 0, dt = turns ? 2 : 1, seq0 = seq;
-      float m = kMNone, l = 0.0f;
+      float m = kMNone, me = 0.0f, l = 0.0f;           // me: M's exponent where m is beyond kBig, else 0
+      bool bigs = false;                               // a row of the warp has had such an M
       seq += t0;
       for (int t = t0; t < ntile; t += dt, seq += dt) {
         if (!wait(bDesc + seq % L::DESCS, seq / L::DESCS) || !wait(bSFull + X, nS)) break;
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         // The tile as it mostly is: every token seen and no score far above the maximum so far.  The weights by the
         // old maximum tell by themselves: a page's sum below kFull means that each fits fp16.  No maximum is taken.
         bool done = false;
-        if (d.full && t > t0) {
+        if (d.full && t > t0 && !bigs) {
           float x[kTTok];
           uint32_t w[kTTok / 2];
           tld32x4(ts, x);
@@ -631,17 +635,21 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (!done) {                                   // an edge, an item's first tile, or a maximum that moves
           float x[kTTok];
           tld32x4(ts, x);
+          auto seen = [&](int j0) {                    // slots of the page at j0 that the row sees
+            const int hi = p - j0;                                   // up to hi
+            uint32_t see = hi < 0 ? 0u : hi >= 15 ? 0xFFFFu : (2u << hi) - 1u;
+            if (a.window) {
+              const int lo = hi - a.window + 1, sk = a.sinks - j0;   // from lo on, or below sk
+              const uint32_t win = lo <= 0 ? 0xFFFFu : lo > 15 ? 0u : 0xFFFFu << lo;
+              const uint32_t snk = sk <= 0 ? 0u : sk > 15 ? 0xFFFFu : (1u << sk) - 1u;
+              see &= win | snk;
+            }
+            return see;
+          };
           if (!d.full) {
 #pragma unroll
             for (int pg = 0; pg < kTPg; ++pg) {
-              const int j0 = d.j0[pg], hi = p - j0;                  // slots up to hi
-              uint32_t see = hi < 0 ? 0u : hi >= 15 ? 0xFFFFu : (2u << hi) - 1u;
-              if (a.window) {
-                const int lo = hi - a.window + 1, sk = a.sinks - j0; // from lo on, or below sk
-                const uint32_t win = lo <= 0 ? 0xFFFFu : lo > 15 ? 0u : 0xFFFFu << lo;
-                const uint32_t snk = sk <= 0 ? 0u : sk > 15 ? 0xFFFFu : (1u << sk) - 1u;
-                see &= win | snk;
-              }
+              const uint32_t see = seen(d.j0[pg]);
 #pragma unroll
               for (int k = 0; k < 16; ++k) x[16 * pg + k] = (see >> k) & 1u ? x[16 * pg + k] : -INFINITY;
             }
@@ -657,49 +665,107 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
             mx = fmaxf(mx, fmaf(fmaxf(m0, m1), factor(pg), d.ev[pg]));
           }
-          const bool moved = mx > m + kSlack;
-          if (__any_sync(0xffffffffu, moved)) {
-            const float alpha = moved ? ex2(m - (mx + kHead)) : 1.0f;
-            if (moved) {
-              m = mx + kHead;
-              l *= alpha;
+          bool moved = mx > m + kSlack;
+          const bool any = __any_sync(0xffffffffu, moved);
+          if (any && __any_sync(0xffffffffu, moved && fabsf(mx) > kBig)) bigs = true;
+          auto rescale = [&](float alpha) {            // O of the tiles before (their MMAs have run: S came after)
+            l *= alpha;
+            if (t == t0) return;
+#pragma unroll 1
+            for (int c = 0; c < L::DV / 16; ++c) {
+              float o[16];
+              uint32_t u[16];
+              tld16(to + 16u * c, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * alpha);
+              tst16(to + 16u * c, u);
+            }
+          };
+          if (__builtin_expect(!bigs, 1)) {
+            if (any) {
+              const float alpha = moved ? ex2(m - (mx + kHead)) : 1.0f;
+              m = moved ? mx + kHead : m;
+              rescale(alpha);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {              // the weights overlay the scores
+              uint32_t w[16];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const int pg = 2 * c + q;
+                const float f = factor(pg), base = d.ev[pg] - m + kLift;
+                const uint64_t f2 = pack2(f, f), b2 = pack2(base, base);
+                uint64_t s2 = 0ull;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  float y0, y1;
+                  unpack2(fma2(pack2(x[16 * pg + 2 * k], x[16 * pg + 2 * k + 1]), f2, b2), y0, y1);
+                  y0 = ex2(y0);
+                  y1 = ex2(y1);
+                  s2 = add2(s2, pack2(y0, y1));
+                  w[8 * q + k] = half2_bits(y0, y1);
+                }
+                float s0, s1;
+                unpack2(s2, s0, s1);
+                l = fmaf(s0 + s1, d.vinv[pg], l);
+              }
+              tst16(ts + 16u * c, w);
+            }
+          } else {
+            // ---- M in two parts, the weights by differences from it ----
+            // the scores of pages 2c and 2c + 1 again, each rounded: differences are exact where they are small
+            auto scores = [&](int c, float (&y)[32]) {
+              tld32(ts + 32u * c, y);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const int pg = 2 * c + q;
+                const uint32_t see = d.full ? 0xFFFFu : seen(d.j0[pg]);
+                const float f = factor(pg);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) y[16 * q + k] = (see >> k) & 1u ? __fmul_rn(y[16 * q + k], f) : -INFINITY;
+              }
+              __syncwarp();
+            };
+            float y[32], ref = m, top = -INFINITY, alpha = 1.0f;
+#pragma unroll 1
+            for (int c = 0; c < kTPg / 2; ++c) {
+              scores(c, y);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) ref = fmaxf(ref, y[k]);
+            }
+#pragma unroll 1
+            for (int c = 0; c < kTPg / 2; ++c) {
+              scores(c, y);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) top = fmaxf(top, y[k] - ref + d.ev[2 * c + (k >> 4)]);
+            }
+            if (top > m - ref + me + kSlack) {
+              const bool two = fabsf(ref) > kBig;
+              const float mn = two ? ref : ref + (top + kHead), en = two ? ceilf(top + kHead) : 0.0f;
+              alpha = ex2((m - mn) + (me - en));
+              m = mn;
+              me = en;
             }
             __syncwarp();
-            if (t > t0) {                              // O of the tiles before (their MMAs have run: S came after)
+            rescale(alpha);
 #pragma unroll 1
-              for (int c = 0; c < L::DV / 16; ++c) {
-                float o[16];
-                uint32_t u[16];
-                tld16(to + 16u * c, o);
+            for (int c = 0; c < kTPg / 2; ++c) {       // (the weights overlay scores that were read)
+              uint32_t w[16];
+              scores(c, y);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * alpha);
-                tst16(to + 16u * c, u);
+              for (int q = 0; q < 2; ++q) {
+                const float more = d.ev[2 * c + q] - me + kLift;
+                float sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float y0 = ex2(__fsub_rn(y[16 * q + 2 * k], m) + more), y1 = ex2(__fsub_rn(y[16 * q + 2 * k + 1], m) + more);
+                  sum += y0 + y1;
+                  w[8 * q + k] = half2_bits(y0, y1);
+                }
+                l = fmaf(sum, d.vinv[2 * c + q], l);
               }
+              tst16(ts + 16u * c, w);
             }
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {                // the weights overlay the scores
-            uint32_t w[16];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int pg = 2 * c + q;
-              const float f = factor(pg), base = d.ev[pg] - m + kLift;
-              const uint64_t f2 = pack2(f, f), b2 = pack2(base, base);
-              uint64_t s2 = 0ull;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                float y0, y1;
-                unpack2(fma2(pack2(x[16 * pg + 2 * k], x[16 * pg + 2 * k + 1]), f2, b2), y0, y1);
-                y0 = ex2(y0);
-                y1 = ex2(y1);
-                s2 = add2(s2, pack2(y0, y1));
-                w[8 * q + k] = half2_bits(y0, y1);
-              }
-              float s0, s1;
-              unpack2(s2, s0, s1);
-              l = fmaf(s0 + s1, d.vinv[pg], l);
-            }
-            tst16(ts + 16u * c, w);
           }
         }
         tst_wait();
@@ -722,7 +788,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const bool joins = turns && ntile > 1;
       if (joins) {
         if (X) {
-          join[r] = make_float2(m, l);
+          // (m, l); beyond kBig with M's exponent in the last bits of l, which has 15 left
+          join[r] = make_float2(m, fabsf(m) > kBig ? __uint_as_float((__float_as_uint(l) & ~0xFFu) | static_cast<uint32_t>(static_cast<int>(me) + 128)) : l);
           tc_before();
           __syncwarp();
           if (lane == 0) bar_arrive(bar(bJoin));
@@ -733,10 +800,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (!wait(bJoin, nJ++)) break;
         tc_after();
         const float2 other = join[r];
-        const float mj = fmaxf(m, other.x);
-        const float fa = ex2(m - mj), fb = ex2(other.x - mj);
-        m = mj;
-        l = fa * l + fb * other.y;
+        const bool two = fabsf(other.x) > kBig;
+        const float lb = two ? __uint_as_float(__float_as_uint(other.y) & ~0xFFu) : other.y;
+        const float eb = two ? static_cast<float>(static_cast<int>(__float_as_uint(other.y) & 0xFFu) - 128) : 0.0f;
+        const float ref = fmaxf(m, other.x), da = m - ref + me, db = other.x - ref + eb;
+        m = ref;
+        me = fmaxf(da, db);
+        const float fa = ex2(da - me), fb = ex2(db - me);
+        l = fa * l + fb * lb;
 #pragma unroll 1
         for (int c = 0; c < L::DV / 16; ++c) {
           float o[16], o2[16];
@@ -779,7 +850,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           float4* dst = reinterpret_cast<float4*>(part + 4 + 32 * c);
 #pragma unroll
           for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          if (c == 0) *reinterpret_cast<float2*>(part) = make_float2(m, l);
+          if (c == 0) *reinterpret_cast<float4*>(part) = make_float4(m, l, me, 0.0f);
         }
         __syncwarp();                                  // lanes with no row wait: the loads are the whole warp's
       }
@@ -1123,16 +1194,27 @@ __global__ void __launch_bounds__(256) kv8_tc_join_kernel(const __grid_constant_
     if (rr >= cut.rows) return;
     // the first part is in its CTA's second slot, the others in their CTAs' first
     auto part = [&](int k) { return parts + (2LL * k + (k == c ? 1 : 0)) * step + static_cast<long long>(rr) * kPart; };
-    float M = kMNone;
-    for (int k = c + lane; k <= cut.last; k += 32) M = fmaxf(M, part(k)[0]);
+    float M = kMNone, E = 0.0f;                        // the joined M, in its two parts
+    bool two = false;
+    for (int k = c + lane; k <= cut.last; k += 32) {
+      const float4 h = *reinterpret_cast<const float4*>(part(k));
+      M = fmaxf(M, h.x);
+      two |= h.z != 0.0f;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (__any_sync(0xffffffffu, two)) {
+      E = -INFINITY;
+      for (int k = c + lane; k <= cut.last; k += 32) E = fmaxf(E, part(k)[0] - M + part(k)[2]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) E = fmaxf(E, __shfl_xor_sync(0xffffffffu, E, o));
+    }
     float L = 0.0f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = c; k <= cut.last; ++k) {
       const float* p = part(k);
-      const float f = ex2(p[0] - M);
+      const float f = ex2(p[0] - M + p[2] - E);
       L = fmaf(f, p[1], L);
       if (4 * lane >= DV) continue;
       const float4 x = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
