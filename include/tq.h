@@ -441,8 +441,10 @@ tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_new, int num
  * whose value scales lie more than 2^100 apart (a block of zeros has 2^-100)
  * the smaller one's weights may be lost.  NaN codes (which tq_kv8_append never
  * writes) at a seen position may spoil other rows too.
- * q, out and workspace are 16-byte aligned; calls that may overlap on the GPU
- * need a workspace each.  batch * n_new * num_q_heads is below 2^27, and
+ * q, out and workspace are 16-byte aligned; out may be q itself (but not at
+ * d = 256 with more than 16 query rows per KV head: TQ_ERR_INVALID_ARG) and
+ * overlaps it in no other way; calls that may overlap on the GPU need a
+ * workspace each.  batch * n_new * num_q_heads is below 2^27, and
  * positions below 2^29 (else TQ_ERR_UNSUPPORTED). */
 tq_status tq_kv8_decode_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* q, tq_dtype dtype, int batch,
                                   int num_q_heads, const int32_t* seq_lens, int max_seq_len, int window, int sinks,

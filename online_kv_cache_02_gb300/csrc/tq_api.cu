@@ -963,6 +963,8 @@ tq_status kv8_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void
   const long long cap = std::min<long long>(max_seq_len, static_cast<long long>(kPage) * cache->max_pages_per_seq);
   if (cap > (1LL << 29) || (cap / kPage + 64) * H > 0x7FFFFFFFLL) return TQ_ERR_UNSUPPORTED;
   const int d = ctx->cfg.d;
+  // in place: every part of an item reads its queries before a result is written, but at d = 256 a query row has two items
+  if (q == out && d == 256 && static_cast<long long>(n_new) * (Hq / H) > kTcRows) return TQ_ERR_INVALID_ARG;
   const bool f32 = dtype == TQ_F32, tc = kv8_tc_takes(n_new, Hq / H, d, f32, softmax_scale);
   const size_t need = !tc ? kv8_rows_workspace(n_new, Hq / H, d)
                       : kv8_tc_splits(batch, n_new, Hq / H, max_seq_len, d)

@@ -223,3 +223,56 @@ def test_the_largest_scores_win_at_every_size(dtype, d, g, n, sign):
             2.0 ** -28 * scales.max() * np.abs(codes).mean(0))
         err = np.abs(got - v.mean(0))
         assert np.all(err <= tol), (size, best, float(np.nanmax(err / tol)), int(np.isnan(got).sum()))
+
+
+# ---------------------------------------------------------------------------
+# buffers and streams
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,d,h,hq,n_new,starts", [("bf16", 128, 2, 8, 1, [700, 20]), ("bf16", 128, 2, 8, 4, [9000, 40]),
+                                                       ("f32", 64, 2, 4, 30, [500, 3]), ("bf16", 64, 2, 8, 150, [0, 900]),
+                                                       ("bf16", 128, 2, 8, 70, [5000, 1]), ("bf16", 128, 1, 20, 1, [3000]),
+                                                       ("bf16", 256, 2, 8, 4, [2000, 1])])
+def test_results_in_the_queries_place(dtype, d, h, hq, n_new, starts):
+    rng = np.random.default_rng(77)
+    b = len(starts)
+    maxp = (max(starts) + n_new) // 16 + 2
+    c = Cache(rng, b * maxp, h, d, b, maxp)
+    for i, s in enumerate(starts):
+        c.clean(rng, i, range(s + n_new))
+    c.to_device()
+    dt, code = DT[dtype]
+    q = values(rng, dtype, b, n_new, hq, d)
+    n = tq.tq_kv8_workspace_size(ctx_for(d), b, n_new, hq, h, 16 * maxp)
+    ws, at = torch.empty(n, dtype=torch.uint8, device=DEV), to_dev(np.asarray(starts, np.int32))
+    want = _attend(c, q, dtype, True, starts)
+    for _ in range(5):
+        x = to_dev(q).to(dt)
+        tq.tq_kv8_causal_attention(ctx_for(d), c.desc, x, code, b, n_new, hq, at, None, 16 * maxp, 0, 0, d ** -0.5, x, ws, n)
+        torch.cuda.synchronize()
+        assert np.array_equal(x.float().cpu().numpy(), want)
+    _check(c, want, q, dtype, True, starts, rows={(i, t) for i in range(b) for t in (0, n_new - 1)})
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_two_streams_at_once_on_tcgen05(d):
+    """Two calls that overlap on the GPU, items cut over many CTAs, each call with its own workspace."""
+    rng = np.random.default_rng(78)
+    c = Cache(rng, 400, 2, d, 1, 330)
+    c.clean(rng, 0, range(5200))
+    c.to_device()
+    n_new, start = 90, 5000
+    q = values(rng, "bf16", 1, n_new, 8, d)
+    want = _attend(c, q, "bf16", True, [start])
+    ctx, dt = ctx_for(d), torch.bfloat16
+    n = tq.tq_kv8_workspace_size(ctx, 1, n_new, 8, 2, 5280)
+    qd, at = to_dev(q).to(dt), to_dev(np.asarray([start], np.int32))
+    runs = [(torch.cuda.Stream(), torch.empty(n, dtype=torch.uint8, device=DEV), torch.empty(1, n_new, 8, d, dtype=dt, device=DEV))
+            for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, ws, out in runs:
+            tq.tq_kv8_causal_attention(ctx, c.desc, qd, tq.TQ_BF16, 1, n_new, 8, at, None, 5280, 0, 0, d ** -0.5, out, ws, n, st)
+    torch.cuda.synchronize()
+    for _, _, out in runs:
+        assert np.array_equal(out.float().cpu().numpy(), want)
+    _check(c, want, q, "bf16", True, [start], rows={(0, 0), (0, 45), (0, 89)})

@@ -48,3 +48,12 @@ def test_sizes_whose_product_passes_64_bits_are_refused(f, batch, n_new, hq):
     assert tq.raw_status("tq_kv8_workspace_size", f.ctx, batch, n_new, hq, 4, 100, ctypes.byref(n)) == tq.TQ_ERR_UNSUPPORTED
     for dtype in (0, 1):
         assert _attend(f, True, batch=batch, n_new=n_new, hq=hq, dtype=dtype, ws_bytes=2 ** 63) == tq.TQ_ERR_UNSUPPORTED
+
+
+def test_in_place_is_refused_where_a_row_has_two_items(f):
+    g = Fake(256)
+    one = dict(q=1 << 20, out=1 << 20)
+    assert _attend(g, True, n_new=9, **one) == _attend(g, False, hq=4 * 17, **one) == tq.TQ_ERR_INVALID_ARG
+    assert _attend(g, True, n_new=8, **one) == _attend(g, False, hq=4 * 16, **one) == tq.TQ_ERR_CUDA
+    assert _attend(g, True, n_new=9, q=1 << 20, out=1 << 21) == tq.TQ_ERR_CUDA
+    assert _attend(f, True, n_new=9, **one) == _attend(f, False, hq=4 * 17, **one) == tq.TQ_ERR_CUDA
