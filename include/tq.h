@@ -359,7 +359,8 @@ tq_status tq_search_scores(const tq_ctx* ctx, const void* q, tq_dtype dtype, int
  * is one KV head of one page: e4m3 codes [16][d] and one fp32 scale, a power of
  * two 2^e with e in [-100, 119]; the value of a code is code * scale.  Head
  * dimension: the context's d, one of 64, 128, 256 (else TQ_ERR_UNSUPPORTED).
- * Codes are 16-byte aligned; the pages' contents need no initialisation. */
+ * Codes are 16-byte aligned, and every int32 or fp32 array of these calls
+ * 4-byte aligned; the pages' contents need no initialisation. */
 typedef struct {
   void* k_codes;                /* device [num_pages][num_kv_heads][16][d] e4m3 */
   void* v_codes;

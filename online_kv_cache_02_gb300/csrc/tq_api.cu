@@ -906,14 +906,17 @@ extern "C" tq_status tq_search_scores(const tq_ctx* ctx, const void* q, tq_dtype
 // ---------------------------------------------------------------------------
 namespace {
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+// Arrays of int32 and fp32 that the kernels read element by element (null: not there).
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
 
 // The cache descriptor, for calls that touch K and V (or only one of them).
 tq_status kv8_check(const tq_ctx* ctx, const tq_kv8_cache* c, bool need_k, bool need_v) {
   if (!ctx || !c) return TQ_ERR_INVALID_ARG;
   if (!kv8_head_dim(ctx->cfg.d)) return TQ_ERR_UNSUPPORTED;
   if (c->num_kv_heads < 1 || c->max_pages_per_seq < 1 || c->num_pages < 1 || !c->block_table) return TQ_ERR_INVALID_ARG;
-  if (need_k && (!c->k_codes || !c->k_scale || misaligned(c->k_codes))) return TQ_ERR_INVALID_ARG;
-  if (need_v && (!c->v_codes || !c->v_scale || misaligned(c->v_codes))) return TQ_ERR_INVALID_ARG;
+  if (need_k && (!c->k_codes || !c->k_scale || misaligned(c->k_codes) || misaligned4(c->k_scale))) return TQ_ERR_INVALID_ARG;
+  if (need_v && (!c->v_codes || !c->v_scale || misaligned(c->v_codes) || misaligned4(c->v_scale))) return TQ_ERR_INVALID_ARG;
+  if (misaligned4(c->block_table)) return TQ_ERR_INVALID_ARG;
   return static_cast<long long>(c->num_pages) * c->num_kv_heads > 0x7FFFFFFFLL ? TQ_ERR_UNSUPPORTED : TQ_OK;
 }
 
@@ -930,7 +933,7 @@ tq_status rope_check(const tq_rope* r, int d) {
   if (!r->cos_sin || misaligned(r->cos_sin) || r->max_pos < 1) return TQ_ERR_INVALID_ARG;
   if (r->rot_dim < 16 || r->rot_dim > d || r->rot_dim % 16 || (d - r->rot_dim) % 16) return TQ_ERR_INVALID_ARG;
   if (r->interleaved != 0 && r->interleaved != 1) return TQ_ERR_INVALID_ARG;
-  if (r->num_axes < 1 || r->num_axes > 4 || (r->num_axes > 1 && !r->pos)) return TQ_ERR_INVALID_ARG;
+  if (r->num_axes < 1 || r->num_axes > 4 || (r->num_axes > 1 && !r->pos) || misaligned4(r->pos)) return TQ_ERR_INVALID_ARG;
   int sum = 0;
   for (int i = 0; i < r->num_axes; ++i) {
     if (r->section[i] < 0 || r->section[i] > d) return TQ_ERR_INVALID_ARG;
@@ -956,7 +959,8 @@ tq_status kv8_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void
   if (dtype != TQ_BF16 && dtype != TQ_F32) return TQ_ERR_INVALID_ARG;
   if (!std::isfinite(softmax_scale)) return TQ_ERR_INVALID_ARG;
   if (batch == 0) return TQ_OK;
-  if (!q || !lens || !out || !workspace || misaligned(q) || misaligned(out) || misaligned(workspace))
+  if (!q || !lens || !out || !workspace || misaligned(q) || misaligned(out) || misaligned(workspace) || misaligned4(lens) ||
+      misaligned4(new_lens))
     return TQ_ERR_INVALID_ARG;
   if (!kv8_rows_fit(batch, n_new, Hq)) return TQ_ERR_UNSUPPORTED;
   // positions lie below both: a window or sinks beyond them change nothing (and the kernels' sums stay in 32 bits)
@@ -1030,7 +1034,7 @@ extern "C" tq_status tq_kv8_append(const tq_ctx* ctx, const tq_kv8_cache* cache,
     if (st != TQ_OK) return st;
   }
   if (batch == 0 || n_new == 0) return TQ_OK;
-  if (!start_pos) return TQ_ERR_INVALID_ARG;
+  if (!start_pos || misaligned4(start_pos) || misaligned4(new_lens)) return TQ_ERR_INVALID_ARG;
   const uintptr_t elem = dtype == TQ_F32 ? 3 : 1;
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(q)) & elem)
     return TQ_ERR_INVALID_ARG;

@@ -57,3 +57,22 @@ def test_in_place_is_refused_where_a_row_has_two_items(f):
     assert _attend(g, True, n_new=8, **one) == _attend(g, False, hq=4 * 16, **one) == tq.TQ_ERR_CUDA
     assert _attend(g, True, n_new=9, q=1 << 20, out=1 << 21) == tq.TQ_ERR_CUDA
     assert _attend(f, True, n_new=9, **one) == _attend(f, False, hq=4 * 17, **one) == tq.TQ_ERR_CUDA
+
+
+def test_arrays_off_their_elements_boundary_are_refused(f):
+    """int32 and fp32 arrays: a kernel's load from there would end the process's use of the GPU."""
+    odd = (1 << 20) + 2
+    for name in ("k_scale", "v_scale", "block_table"):
+        c = _cache(f, **{name: odd})
+        assert _append(f, cache=c) == _attend(f, False, cache=c) == _attend(f, True, cache=c) == tq.TQ_ERR_INVALID_ARG, name
+    assert _append(f, start=odd) == _attend(f, False, lens=odd) == _attend(f, True, lens=odd) == tq.TQ_ERR_INVALID_ARG
+    assert _append(f, rope=_rope(f, pos=odd)) == tq.TQ_ERR_INVALID_ARG
+    new = lambda at: tq.raw_status("tq_kv8_append", f.ctx, f.cache, f.buf, f.buf, f.buf, 0, 2, 3, 8, f.buf, at, None, f.buf,  # noqa: E731
+                                   0, 0, 0, None)
+    assert new(odd) == tq.TQ_ERR_INVALID_ARG and new(f.buf) == tq.TQ_ERR_CUDA
+    causal = lambda at: tq.raw_status("tq_kv8_causal_attention", f.ctx, f.cache, f.buf, 0, 2, 3, 8, f.buf, at, 100, 0, 0,  # noqa: E731
+                                      ctypes.c_float(0.1), f.buf, f.buf, 1 << 40, None)
+    assert causal(odd) == tq.TQ_ERR_INVALID_ARG
+    assert causal(f.buf) == tq.TQ_ERR_CUDA
+    # of a cache that is only half used, the other half is not looked at
+    assert _append(f, cache=_cache(f, k_scale=odd), k=None) == tq.TQ_ERR_CUDA
