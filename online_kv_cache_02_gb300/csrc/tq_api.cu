@@ -934,12 +934,13 @@ tq_status rope_check(const tq_rope* r, int d) {
   if (r->rot_dim < 16 || r->rot_dim > d || r->rot_dim % 16 || (d - r->rot_dim) % 16) return TQ_ERR_INVALID_ARG;
   if (r->interleaved != 0 && r->interleaved != 1) return TQ_ERR_INVALID_ARG;
   if (r->num_axes < 1 || r->num_axes > 4 || (r->num_axes > 1 && !r->pos) || misaligned4(r->pos)) return TQ_ERR_INVALID_ARG;
+  if (r->num_axes == 1) return TQ_OK;               // its section is not read
   int sum = 0;
   for (int i = 0; i < r->num_axes; ++i) {
     if (r->section[i] < 0 || r->section[i] > d) return TQ_ERR_INVALID_ARG;
     sum += r->section[i];
   }
-  return r->num_axes == 1 || sum == r->rot_dim / 2 ? TQ_OK : TQ_ERR_INVALID_ARG;
+  return sum == r->rot_dim / 2 ? TQ_OK : TQ_ERR_INVALID_ARG;
 }
 
 // Query rows of an attention call: below 2^27, for the kernels' 32-bit sums.  (The product of all three can pass 64 bits.)
@@ -1073,7 +1074,7 @@ extern "C" tq_status tq_kv8_append(const tq_ctx* ctx, const tq_kv8_cache* cache,
     a.axes = rope->num_axes;
     a.pos = rope->pos;
     int end = 0;
-    for (int i = 0; i < a.axes; ++i) a.sec_end[i] = end += rope->section[i];
+    for (int i = 0; i < a.axes && a.axes > 1; ++i) a.sec_end[i] = end += rope->section[i];
   }
   a.err = ctx->tab.err;
   return cuda_status(launch_kv8_append(a, d, dtype == TQ_F32, static_cast<cudaStream_t>(stream)));

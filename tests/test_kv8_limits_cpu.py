@@ -76,3 +76,9 @@ def test_arrays_off_their_elements_boundary_are_refused(f):
     assert causal(f.buf) == tq.TQ_ERR_CUDA
     # of a cache that is only half used, the other half is not looked at
     assert _append(f, cache=_cache(f, k_scale=odd), k=None) == tq.TQ_ERR_CUDA
+
+
+def test_the_section_of_a_single_axis_is_not_read(f):
+    for section in ((-1, 0, 0, 0), (2 ** 31 - 1, -5, 0, 0), (0, 0, 0, 0)):
+        assert _append(f, rope=_rope(f, section=section)) == tq.TQ_ERR_CUDA
+    assert _append(f, rope=_rope(f, num_axes=2, section=(-1, 65, 0, 0), pos=f.buf)) == tq.TQ_ERR_INVALID_ARG
