@@ -8,8 +8,8 @@ import pytest
 
 from oracle import kv8
 
-from .gpu_common import DEV, to_dev, torch, tq, wl
-from .test_gpu_kv8 import DT, Cache, _attend, _bound, _causal_case, _check, _decode_case, _table, ctx_for, values
+from .gpu_common import DEV, to_dev, torch, tq
+from .test_gpu_kv8 import DT, Cache, _append_case, _attend, _bound, _causal_case, _check, _decode_case, ctx_for, values
 
 pytestmark = pytest.mark.gpu
 
@@ -276,3 +276,74 @@ def test_two_streams_at_once_on_tcgen05(d):
     for _, _, out in runs:
         assert np.array_equal(out.float().cpu().numpy(), want)
     _check(c, want, q, "bf16", True, [start], rows={(0, 0), (0, 45), (0, 89)})
+
+
+# ---------------------------------------------------------------------------
+# append: what is stored, where only the flags were looked at
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,d,rot,interleaved", [("f32", 128, 128, False), ("bf16", 128, 128, False), ("f32", 64, 32, True),
+                                                     ("bf16", 256, 240, False), ("f32", 256, 256, True)])
+def test_append_of_pairs_that_are_not_finite(dtype, d, rot, interleaved):
+    """Of a turned pair with an infinity or NaN the infinite halves become the largest code, NaN zero; neither counts for
+    the scale, and every other code is exact."""
+    rng = np.random.default_rng(80)
+    h, n, start = 2, 37, 6
+    x = {"k": values(rng, dtype, 1, n, h, d) * 5, "v": values(rng, dtype, 1, n, h, d), "q": values(rng, dtype, 1, n, 2, d)}
+    for t, head, ch, bad in ((0, 0, 3, np.inf), (3, 1, 5, -np.inf), (9, 0, rot // 2 + 2, np.nan), (10, 1, rot - 1, np.inf),
+                             (25, 0, 0, np.nan), (26, 0, 1, np.inf), (36, 1, rot // 2, -np.inf)):
+        x["k"][0, t, head, ch] = bad
+        x["v"][0, t, head, (ch + 7) % d] = bad
+    x["k"][0, 12, 0, 4] = x["k"][0, 12, 0, 4 + (1 if interleaved else rot // 2)] = np.inf     # both of a pair
+    if rot < d:
+        x["k"][0, 20, 1, d - 1] = np.inf            # a channel that does not turn
+    c = _append_case(rng, dtype, d, h, 2, [start], n, rot=rot, interleaved=interleaved, x=x, kinds="kv", flags=32)
+    for kind in "kv":
+        codes = c.dev[kind + "c"].cpu().numpy()
+        assert not ((codes & 127) == 127).any()     # no NaN code anywhere
+
+
+def test_append_behind_a_scale_that_is_none():
+    """An earlier token's block without a power of two as its scale: taken as 2^-100, so that its codes round to zero, and
+    the new token has the scale that it needs."""
+    rng = np.random.default_rng(81)
+    h, d = 2, 128
+    ctx = ctx_for(d)
+    c = Cache(rng, 3, h, d, 1, 2, nan=False)
+    desc = c.to_device()
+    x = values(rng, "bf16", 1, 1, h, d)
+    dev = to_dev(x).to(torch.bfloat16)
+    page = int(c.table[0, 0])
+    before = c.dev["kc"].cpu().numpy()[page]
+    for bad in (3.0, 0.0, float("nan"), float("inf"), 2.0 ** 120, 2.0 ** -101, -1.0):
+        c.dev["ks"][page] = bad
+        c.dev["kc"][page] = to_dev(before)
+        tq.tq_kv8_append(ctx, desc, dev, None, None, tq.TQ_BF16, 1, 1, 0, to_dev(np.asarray([2], np.int32)))
+        torch.cuda.synchronize()
+        assert tq.tq_check_device_status(ctx) == 64, bad
+        codes, scales = c.dev["kc"].cpu().numpy()[page], c.dev["ks"].cpu().numpy()[page]
+        for head in range(h):
+            e = kv8.block_exponent(np.abs(x[0, 0, head]).max())
+            assert scales[head] == 2.0 ** e
+            assert np.all(kv8.VALUES[codes[head, :2]] == 0)
+            assert np.array_equal(codes[head, 2], kv8.e4m3_encode(x[0, 0, head].astype(np.float64) * 2.0 ** -e))
+            assert np.array_equal(codes[head, 3:], before[head, 3:])
+
+
+@pytest.mark.parametrize("dtype,d,n_new", [("bf16", 128, 100), ("bf16", 64, 100), ("bf16", 256, 100), ("f32", 128, 30), ("bf16", 128, 3)])
+def test_causal_calls_that_are_cut_answer_what_is_left(dtype, d, n_new):
+    """Queries beyond max_seq_len, a padded count that is none and a negative start: the rows that remain are right, and the
+    others stay."""
+    rng = np.random.default_rng(82)
+    c = Cache(rng, 40, 2, d, 3, 13)
+    for b in range(3):
+        c.clean(rng, b, range(200))
+    c.to_device()
+    q = values(rng, dtype, 3, n_new, 8, d)
+    most = 130 + n_new * 7 // 10
+    got = _attend(c, q, dtype, True, [130, -3, 50], lens=[1000, 5, n_new - 1], max_len=most)
+    assert tq.tq_check_device_status(ctx_for(d)) == 4
+    assert np.all(got[1] == -7)
+    keep = [0, 2]
+    sub = Cache.__new__(Cache)
+    sub.__dict__.update(c.__dict__, table=c.table[keep])
+    _check(sub, got[keep], q[keep], dtype, True, [130, 50], [most - 130, n_new - 1])
