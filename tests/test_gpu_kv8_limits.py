@@ -347,3 +347,38 @@ def test_causal_calls_that_are_cut_answer_what_is_left(dtype, d, n_new):
     sub = Cache.__new__(Cache)
     sub.__dict__.update(c.__dict__, table=c.table[keep])
     _check(sub, got[keep], q[keep], dtype, True, [130, 50], [most - 130, n_new - 1])
+
+
+@pytest.mark.parametrize("dtype,d,g,n_new", [("bf16", 128, 4, 3), ("f32", 64, 3, 30), ("f32", 256, 2, 9), ("bf16", 64, 4, 30),
+                                             ("bf16", 128, 4, 30), ("bf16", 256, 4, 30), ("bf16", 64, 4, 100), ("bf16", 128, 4, 100)])
+@pytest.mark.parametrize("window,sinks,start", [(0, 0, 0), (0, 0, 3000), (100, 3, 350), (37, 20, 5)])
+def test_large_scores_behind_masks(dtype, d, g, n_new, window, sinks, start):
+    """Large scores in causal calls with windows, first tokens and rows at different positions: the mean over the visible
+    keys of the largest score."""
+    rng = np.random.default_rng(83)
+    n = start + n_new
+    for size in (17, 27, 60):
+        c = _one_head(rng, d, n)
+        c.scales["v"][:] = np.exp2(rng.integers(-20, 20, c.scales["v"].shape))
+        c.scales["k"][:] = np.exp2(size // 2)
+        c.codes["k"][:, :, :, 0] = kv8.e4m3_encode(rng.choice([32.0, 64.0, 128.0], c.codes["k"].shape[:3]))
+        c.to_device()
+        q = np.zeros((1, n_new, g, d), np.float32)
+        q[..., 0] = rng.choice([-1.0, 1.0], (n_new, g)) * 2.0 ** (size - size // 2 - 2)
+        q[0, 0, 0] = values(rng, dtype, d) * 2.0 ** -(size // 2)           # a row of usual scores among them
+        got = _attend(c, q, dtype, True, [start], window=window, sinks=sinks)
+        assert tq.tq_check_device_status(ctx_for(d)) == 0
+        two_parts = dtype == "bf16" and n_new * g > 16
+        for t in {0, 1, n_new // 2, n_new - 1}:
+            want, mag, dots, ksum, keys = kv8.attention(q[0, t], c.codes["k"], c.scales["k"], c.codes["v"], c.scales["v"], c.table[0],
+                                                        start + t, window, sinks, d ** -0.5)
+            # exact scores but for the first row: no bound on a logit counts beyond 2^17 (where one number holds it)
+            dots = np.where(q[0, t, :, 1] == 0, np.minimum(dots, 2.0 ** 17 * d ** 0.5), dots)
+            parts = np.where(q[0, t, :, 1] == 0, 0.0, 2.0 ** -17 * np.abs(q[0, t]).max(axis=-1) * ksum if two_parts else 0.0)
+            j = np.arange(start + t + 1)
+            j = j[kv8.visible(start + t, j, window, sinks)]
+            pg, sl = c.table[0][j // 16], j % 16
+            tail = 2.0 ** -28 * c.scales["v"][pg, 0].max() * np.abs(kv8.VALUES[c.codes["v"][pg, 0, sl]]).sum(axis=0)
+            tol = _bound(dtype, want, mag, dots, keys, d, d ** -0.5, parts) + tail
+            err = np.abs(got[0, t] - want)
+            assert np.all(err <= tol), (size, t, float(np.nanmax(err / tol)), int(np.isnan(got[0, t]).sum()))
