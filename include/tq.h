@@ -402,13 +402,16 @@ typedef struct {
  * written to it so far: the call that writes slot 0 starts a block anew; a
  * later call keeps the scale or raises it, and then rounds the earlier slots'
  * codes again (exact but for the smallest).  Codes are the nearest (ties to
- * even) to the values rotated in fp64, whatever the launch.  After a rollback
- * of a sequence, appending at a smaller position is the way to go on.
+ * even) to the values rotated in fp64, whatever the launch; q_out is rotated in
+ * fp32 and rounded to `dtype`.  After a rollback of a sequence, appending at a
+ * smaller position is the way to go on.
  * Every block is written by one sequence, at one place of its table (reading
  * shared pages is fine).  Values that are not finite in fp32 set device status
  * bit 32 and are stored as 0 (NaN) or as the block's largest code (infinite),
  * without counting for its scale.  Bit 2: a position beyond the block table (the page
- * is skipped) or outside the cos_sin table (the token is skipped).  Bit 64: an
+ * is skipped) or outside the cos_sin table (the token is skipped).  Bit 4: a
+ * negative start_pos (the sequence is skipped), or new_lens outside 0 .. n_new
+ * (cut to it).  Bit 64: an
  * earlier token's block had no power of two in range as its scale (taken as
  * 2^-100).  Errors as tq_quantize. */
 tq_status tq_kv8_append(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* k, const void* v, const void* q,
@@ -419,7 +422,9 @@ tq_status tq_kv8_append(const tq_ctx* ctx, const tq_kv8_cache* cache, const void
 /* Workspace bytes of the two attention calls below (decode: n_new = 1): enough
  * for either dtype and every softmax_scale, and never less than for a smaller
  * batch, n_new, num_q_heads or max_seq_len, so that a program sizes one buffer
- * for its largest calls.  A call refuses only what is too small for itself. */
+ * for its largest calls.  A call refuses only what is too small for itself (few
+ * rows, fp32 and larger scales use much less).  Sizes beyond the calls' own
+ * limits: TQ_ERR_UNSUPPORTED. */
 tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_new, int num_q_heads, int num_kv_heads,
                                 int max_seq_len, size_t* bytes);
 
@@ -434,11 +439,18 @@ tq_status tq_kv8_workspace_size(const tq_ctx* ctx, int batch, int n_new, int num
  * follows the lengths on the device; results do not depend on the run.
  * Accuracy at every softmax_scale: products of codes and queries summed in
  * fp32 (bf16 queries exact, fp32 ones to 22 bits), weights to 11 bits down to
- * 2^-22 of the largest (bf16) or to 22 bits down to 2^-11 of it (fp32).
+ * 2^-22 of the largest (bf16) or to 22 bits down to 2^-11 of it (fp32).  bf16
+ * results are summed in the tensor cores' fp32, which cut a sum instead of
+ * rounding it; for fp32 inputs a page's sums are added in rounded fp32.
  * With more than 16 query rows (n_new times heads per KV head), bf16 and
  * |softmax_scale| <= 1/sqrt(d), the tcgen05 form runs: a query channel is then
- * off by at most 2^-17 of its row's largest, the weights keep 11 bits down to
- * 2^-17.  The weights ride on the value scales: of two blocks of a sequence
+ * off by at most 2^-17 of its row's largest (or by 2^-130), the weights keep 11
+ * bits down to 2^-17.  fp32 inputs and larger scales take the mma.sync form
+ * with any number of rows, and prompts there take 6 to 9 times as long (d = 128,
+ * 2,048 tokens, 32 / 8 heads: 409 us against 61).  Scores (with the scale and
+ * log2 e) beyond 2^16 are taken again in a slower way, on tcgen05 by tiles and
+ * on mma.sync by a CTA's share of the keys.
+ * The weights ride on the value scales: of two blocks of a sequence
  * whose value scales lie more than 2^100 apart (a block of zeros has 2^-100)
  * the smaller one's weights may be lost.  NaN codes (which tq_kv8_append never
  * writes) at a seen position may spoil other rows too.

@@ -19,11 +19,13 @@
 // block left room for eight warps an SM.)
 //
 // Bound by the memory and, close behind it, by the instructions of the two passes:
-// 8 x 4,096 tokens of 32 + 8 + 8 heads, bf16, d = 128, 755 MB: 142 us, 5.3 TB/s, 78%
-// of a copy's rate (held in registers 367 us; two CTAs an SM 170 us).  fp32 with
-// three axes, 67 MB: 19 us (15 in L2), of which half is the launch and the last wave; the same in
-// bf16 12.  A single
-// token of 16 sequences: 5 us on the GPU, the latency of three dependent loads.
+// 8 x 4,096 tokens of 32 + 8 + 8 heads, bf16, d = 128, 755 MB: 142 us, 5.3 TB/s, 79%
+// of a copy's rate (held in registers 367 us; two CTAs an SM 170 us); d = 64, 378 MB:
+// 83 us, 67%; d = 256, 4 x 4,096 tokens of 16 + 4 + 4, 386 MB: 99 us, 57% (two CTAs an
+// SM, one block in flight a warp).  fp32 with three axes, 3 x 777 tokens of 28 + 4 + 4,
+// 67 MB: 19 us (15 with the inputs in L2), half of it the launch and the last wave; the
+// same in bf16 13.  A single token of 16 sequences: 5 us on the GPU, the latency of
+// three dependent loads.
 
 #include "tq_kv8.h"
 #include "tq_tc.cuh"
@@ -424,8 +426,12 @@ cudaError_t launch_t(const Kv8Append& a, cudaStream_t s) {
   const int npg = (a.n_new + 2 * kPage - 2) / kPage;
   const long long pages = static_cast<long long>(a.batch) * npg;
   const int tasks = (a.k ? a.H : 0) + (a.v ? a.H : 0) + (a.q ? a.Hq : 0);
-  // A block per warp while one wave of CTAs holds them, two where a warp has room for the next block's copy; more per warp
-  // beyond.  bf16, 8 x 512 tokens: up to two waves 21 us, one 25, four 25; fp32, 3 x 777: 17.6 and 15.1 with one.
+  // A block per warp up to three CTAs an SM, six where a warp has room for the next block's copy; more per warp beyond.
+  // That is one wave (two) at d = 64 and 128; at d = 256 an SM holds two CTAs (fp32: one), and it is one and a half (three).
+  // Inputs in L2: bf16, d = 128, 8 x 512 tokens of 32 + 8 + 8 heads: six CTAs an SM 21 us, three 25, twelve 25; fp32,
+  // d = 128, 3 x 777 of 28 + 4 + 4, three axes: three 15.1, six 17.6.  d = 256, 32 + 8 + 8 heads: bf16, 4 x 256: three 15.0,
+  // two 21.0, four 15.0; 16 x 64: three 21.1, two 21.1, four 15.3; fp32, 4 x 256: three 26, one 31, two 26; 3 x 777: three 60,
+  // one 52, two 55.
   int groups = (tasks + kAWarps - 1) / kAWarps;
   int per = 1;
   using S = Stage<D, F32>;

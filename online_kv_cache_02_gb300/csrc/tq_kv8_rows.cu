@@ -22,13 +22,17 @@
 //           for a second kernel.
 //
 // Bound by the memory where contexts are long, by start and end (pages' ids, scales and
-// codes are three dependent loads, the join, the second launch: 9 us of one short
+// codes are three dependent loads, the join, the second launch: 10 us of one short
 // sequence) where they are short.  Measured, bf16, d = 128: 16 sequences of 32,768
-// tokens, 32 / 8 heads, 1.08 GB: 176 us, 6.1 TB/s, 90% of a copy's rate; 64 of 1,024 to
-// 8,192, 28 / 4 heads: 62 us, 4.9 TB/s; a window of 4,096 of 32,768: 35 us; one sequence
-// of 1,000: 9 us.  fp32, d = 64, 7 of 3,001 to 9,001: 25 us.  Weights by a new maximum
-// at every page instead of the one so far: 1 to 6% more.  fp32 prompts run here
-// too, at 55 to 65 TFLOP/s: eight warps an SM wait on their own chains of products.
+// tokens, 32 / 8 heads, 1.08 GB: 177 us, 6.1 TB/s, 89% of a copy's rate (d = 256, 16 / 4
+// heads, 1.08 GB: 173, 92%; d = 64, 32 / 8, 539 MB: 113, 70%: half a page's bytes for the
+// same steps); 64 of 1,024 to 8,192, 28 / 4 heads: 62 us, 4.9 TB/s (d = 64 45, 256 107;
+// fp32 74); a window of 4,096 of 32,768: 35 us; one sequence of 1,000: 10 us.  fp32,
+// d = 64, 7 of 3,001 to 9,001: 25 us.  Weights by a new maximum at every page instead of
+// the one so far: 1 to 6% more.  fp32 prompts run here too (2,048 tokens: d = 64 385 us,
+// 128 560, 256 800 with 16 / 4 heads, 43 to 61 TFLOP/s): eight warps an SM wait on their
+// own chains of products.  So do bf16 prompts with |softmax_scale| above 1/sqrt(d)
+// (2,048 tokens, d = 128: 409 us, on tcgen05 61).
 
 #include "tq_kv8.h"
 #include "tq_kv8_ring.h"
@@ -52,16 +56,22 @@ using tcx::lds64;
 using tcx::su32;
 
 constexpr int kRWarps = 4;
-// An item's start and end (its queries, the join) in pages of a CTA's time: 3.3 us against 0.23 us a page.  Spans are
-// equal in pages and items weighed so: short rows of a prompt would otherwise pile up in the first CTAs (2,048 tokens,
-// d = 64: 0.91 ms, 0.28 so).
+// An item's start and end (its queries, the join) in pages of a CTA's time: spans are equal in pages and items weighed so,
+// since short rows of a prompt would otherwise pile up in the first CTAs.  Decode hardly depends on it (64 sequences of
+// 1,024 .. 8,192, 32 / 8 heads: 8, 12, 16 within 2% at d = 64, 128 and 256, both types); of an fp32 prompt of 2,048 tokens,
+// d = 64, 8 makes 418 us, 12 331, 16 282.
 constexpr int kItemCost = 12;
 constexpr int kMinSpan = 4 + kItemCost;   // a CTA's share at least (a page per warp)
 constexpr int kMaxEntries = 1024;         // (sequence, row block) pairs that the split form lists
-// Pages per CTA up to which the direct form is taken (measured against the split form, bf16, d = 128, 32 / 8 heads):
-//   a CTA per item, 64: 200 sequences of 100 .. 1000 tokens 57 us (split 86), 64 of 1024 .. 8192 125 us (split 64);
-//   clusters that leave two thirds of the card free, 48: 1 of 6000 16.5 us (18.7), 2 of 3000 12.7 us (16.9);
-//   clusters that fill it, 32: 16 of 1000 15.4 us (16.5), 7 of 6000 36 us (27).
+// Pages per CTA up to which the direct form is taken: a CTA per item 64, clusters that leave two thirds of the card free
+// 48, clusters that fill it 32.  Direct and split form, us, 32 / 8 heads, inputs in L2, at bf16 d = 128, 64, 256 and fp32 d = 128:
+//   200 sequences of 100 .. 1,000    55 57   38 44   99 95   66 70
+//   64 of 1,024 .. 8,192            125 106 109 73  223 188 155 125
+//   1 of 6,000                       16 15   14 14   19 20   18 17
+//   2 of 3,000                       12 15   10 14   14 19   14 16
+//   16 of 1,000                      13 17   10 15   17 23   16 20
+//   7 of 6,000                       33 24   18 21   37 42   41 29
+// The rule takes the better one or one within a sixth of it.
 constexpr int kDirectOne = 64, kDirectFew = 48, kDirectMany = 32;
 // Weights are 2^(kLift + score - M), M kHead above the largest score met (it seldom moves again): the largest weight is
 // 2^8, and fp16 keeps 11 bits of them down to 2^-22 of it.  M moves once a weight passes kFull, below the end of fp16:

@@ -30,15 +30,19 @@
 // to its own at the item's end, from B's columns of the same lanes.
 // Every wait is bounded; a wait that gives up sets the device error word.
 //
-// Bound by the tensor cores in the long run of tiles: 2,048 of about 2,200 cycles a
-// tile of 256 rows (two e4m3 products at the rate of one fp16 product, then one fp16
-// product).  Measured, bf16, d = 128, 32 / 8 heads: a prompt of 8,192 tokens 395 us,
-// 1.39 PFLOP/s, 72% of a large bf16 library product's rate; 2 x 1,024 tokens behind
-// 15,000 to 30,000, 475 us, 77%; three prompts of up to 4,000 in a window of 1,024
-// (28 / 4 heads) 165 us, 43%, where an item of nine tiles pays for its queries and its
-// result with the time of four; five drafted tokens of 16 sequences of 2,000 to 8,000,
-// 53 us, 46% of a copy's rate (MMAs of 128 rows of which 20 are there).  d = 256, a
-// prompt of 2,048 tokens, 16 / 4 heads: 81 us (mma.sync: 597).
+// Bound by the tensor cores and the halves' turns behind them: the MMAs of a tile of 256
+// rows take 2,048 cycles (two e4m3 products at the rate of one fp16 product, then one
+// fp16 product), and over a whole call a tile takes 2,920 in a chunk behind a long cache
+// and 3,180 in a prompt of 8,192 tokens (the tensor pipe is active 70% and 64% of the
+// time), items' starts and ends among them.  Measured, bf16, d = 128, 32 / 8 heads: a
+// prompt of 8,192 tokens 402 us, 1.37 PFLOP/s, 71% of a large bf16 library product's
+// rate; 2 x 1,024 tokens behind 15,000 to 30,000, 482 us, 76%; three prompts of up to
+// 4,000 in a window of 1,024 (28 / 4 heads) 167 us, 43%, where an item of nine tiles pays
+// for its queries and its result with the time of four; five drafted tokens of 16
+// sequences of 2,000 to 8,000, 54 us, 45% of a copy's rate (MMAs of 128 rows of which 20
+// are there).  d = 64, 32 / 8 heads, a prompt of 4,096 tokens 119 us, of 8,192 350 (41%:
+// as many weights for half the products).  d = 256, 16 / 4 heads, 2,048 tokens 81 us
+// (mma.sync: 618), 8,192 615 (46%).
 // Slower, each by itself: 64-token tiles in two buffers, sixteen softmax warps, two
 // issuing warps, the queries' copies beside the last tile (from the softmax warps or
 // a warp of their own: code in the tile loop, or a copy slower than four warps').
@@ -1310,10 +1314,10 @@ bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d)
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// More rows than a block of the mma.sync form has.  64 sequences of 2,000 to 8,000 tokens: 16 rows 153 us there and 158
-// here (d = 64: 127 and 133), 20 rows 161 us here.  16 sequences, d = 256: 16 rows 100 us there and 106 here, 20 rows
-// 133 and 108, 64 rows 339 and 115.  A larger scale would make the query's
-// rounding to two e4m3 parts count.
+// More rows than a block of the mma.sync form has.  32 / 8 heads, 64 sequences of 2,000 to 8,000 tokens: 16 rows 157 us
+// there and 158 here (d = 64: 134 and 134), 20 rows 292 and 161 (248 and 137).  16 sequences, d = 256: 16 rows 101 and
+// 104, 20 rows 138 and 106, 64 rows 348 and 113.  A larger scale would make the query's rounding to two e4m3 parts count
+// (and costs: prompts of 2,048 to 4,096 tokens at scale 1, d = 128, 64, 256: 409, 1,048, 618 us on mma.sync, 61, 116, 81 here).
 bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale) {
   return !f32 && static_cast<long long>(T) * G > kTcRows && softmax_scale != 0.0f &&
          std::fabs(static_cast<double>(softmax_scale)) <= (1.0 + 1e-6) / std::sqrt(static_cast<double>(d));
