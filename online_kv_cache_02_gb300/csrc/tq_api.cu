@@ -1,6 +1,8 @@
 // C ABI entry points: context creation, argument checks, launches, status.
 #include "tq_internal.h"
 #include "tq_kv8.h"
+#include "tq_prompt.h"
+#include "tq_read.h"
 
 #include <cuda_runtime.h>
 
@@ -1110,4 +1112,212 @@ extern "C" tq_status tq_kv8_causal_attention(const tq_ctx* ctx, const tq_kv8_cac
                                              void* stream) {
   return kv8_attention(ctx, cache, q, dtype, batch, n_new, Hq, start_pos, new_lens, false, max_seq_len, window, sinks,
                        softmax_scale, out, workspace, workspace_bytes, stream);
+}
+
+extern "C" tq_status tq_kv8_shared_workspace_size(const tq_ctx* ctx, int batch, int Hq, int H, int num_groups, int max_group,
+                                                  int max_seq_len, size_t* bytes) {
+  if (!ctx || !bytes || batch < 0 || Hq < 1 || H < 1 || Hq % H || num_groups < 1 || max_group < 1 || max_seq_len < 0)
+    return TQ_ERR_INVALID_ARG;
+  if (!kv8_head_dim(ctx->cfg.d) || !kv8_rows_fit(batch, 1, Hq) || !kv8_rows_fit(num_groups, max_group, Hq) ||
+      max_seq_len > (1 << 29))
+    return TQ_ERR_UNSUPPORTED;
+  *bytes = kv8_shared_workspace(batch, Hq, H, num_groups, max_group, max_seq_len, ctx->cfg.d);
+  return TQ_OK;
+}
+
+extern "C" tq_status tq_kv8_shared_decode_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* q,
+                                                    tq_dtype dtype, int batch, int Hq, const int32_t* seq_lens,
+                                                    int max_seq_len, int num_groups, const int32_t* group_start,
+                                                    const int32_t* prefix_lens, int max_group, float softmax_scale, void* out,
+                                                    void* workspace, size_t workspace_bytes, void* stream) {
+  tq_status st = kv8_check(ctx, cache, true, true);
+  if (st != TQ_OK) return st;
+  const int H = cache->num_kv_heads, d = ctx->cfg.d;
+  if (batch < 0 || Hq < 1 || Hq % H || max_seq_len < 0 || num_groups < 1 || max_group < 1) return TQ_ERR_INVALID_ARG;
+  if (dtype != TQ_BF16 && dtype != TQ_F32) return TQ_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale)) return TQ_ERR_INVALID_ARG;
+  if (batch == 0) return TQ_OK;
+  if (!q || !seq_lens || !out || !workspace || !group_start || !prefix_lens || misaligned(q) || misaligned(out) ||
+      misaligned(workspace) || misaligned4(seq_lens) || misaligned4(group_start) || misaligned4(prefix_lens))
+    return TQ_ERR_INVALID_ARG;
+  if (!kv8_rows_fit(batch, 1, Hq) || !kv8_rows_fit(num_groups, max_group, Hq)) return TQ_ERR_UNSUPPORTED;
+  const long long cap = std::min<long long>(max_seq_len, static_cast<long long>(kPage) * cache->max_pages_per_seq);
+  if (max_seq_len > (1 << 29) || (cap / kPage + 64) * H > 0x7FFFFFFFLL) return TQ_ERR_UNSUPPORTED;
+  if (workspace_bytes < kv8_shared_workspace(batch, Hq, H, num_groups, max_group, max_seq_len, d)) return TQ_ERR_WORKSPACE;
+  st = on_device(ctx);
+  if (st != TQ_OK) return st;
+  Kv8Attn a{};
+  a.q = q;
+  a.out = out;
+  a.Hq = Hq;
+  a.H = H;
+  a.G = Hq / H;
+  a.lens = seq_lens;
+  a.max_seq_len = max_seq_len;
+  a.bt = cache->block_table;
+  a.maxp = cache->max_pages_per_seq;
+  a.num_pages = cache->num_pages;
+  a.kc = static_cast<const uint8_t*>(cache->k_codes);
+  a.vc = static_cast<const uint8_t*>(cache->v_codes);
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.err = ctx->tab.err;
+  Kv8Share share{};
+  share.batch = batch;
+  share.groups = num_groups;
+  share.max_group = max_group;
+  share.group_start = group_start;
+  share.prefix_lens = prefix_lens;
+  return cuda_status(launch_kv8_shared(a, share, d, dtype == TQ_F32, softmax_scale, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// reading the caches back
+// ---------------------------------------------------------------------------
+namespace {
+// Arguments of both calls; `a` gets what they share.
+tq_status read_check(const tq_ctx* ctx, tq_dtype dtype, int batch, int H, const int32_t* start_pos, const int32_t* lens, int max_len,
+                     const int32_t* block_table, int maxp, int num_pages, void* k_out, void* v_out, const int32_t* first_row,
+                     int total_rows, long long k_stride, long long v_stride, ReadArgs& a) {
+  const long long row = static_cast<long long>(H) * ctx->cfg.d;
+  const int step = dtype == TQ_F32 ? 4 : 8;
+  if (dtype != TQ_BF16 && dtype != TQ_F32) return TQ_ERR_INVALID_ARG;
+  if (batch < 0 || H < 1 || max_len < 0 || maxp < 1 || num_pages < 1 || total_rows < 0) return TQ_ERR_INVALID_ARG;
+  if ((k_stride && (k_stride < row || k_stride % step)) || (v_stride && (v_stride < row || v_stride % step))) return TQ_ERR_INVALID_ARG;
+  if (misaligned(k_out) || misaligned(v_out)) return TQ_ERR_INVALID_ARG;
+  if (batch && max_len && (!start_pos || !lens || !block_table || !first_row || misaligned4(start_pos) || misaligned4(lens) ||
+                           misaligned4(block_table) || misaligned4(first_row)))
+    return TQ_ERR_INVALID_ARG;
+  if (H > 65535 || maxp > (1 << 26) || static_cast<long long>(num_pages) * H > 0x7FFFFFFFLL) return TQ_ERR_UNSUPPORTED;
+  a.batch = batch;
+  a.H = H;
+  a.max_len = max_len;
+  a.total_rows = total_rows;
+  a.start_pos = start_pos;
+  a.lens = lens;
+  a.first_row = first_row;
+  a.bt = block_table;
+  a.maxp = maxp;
+  a.num_pages = num_pages;
+  // a run of max_len tokens that starts at a page's last slot, and no more pages than the table has
+  a.pages = static_cast<int>(std::min<long long>((static_cast<long long>(max_len) + 2 * kPage - 2) / kPage, maxp));
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.k_stride = k_stride ? k_stride : row;
+  a.v_stride = v_stride ? v_stride : row;
+  a.m = ctx->cfg.m;
+  a.kl = ctx->kl;
+  a.vl = ctx->vl;
+  a.tab = ctx->tab;
+  return TQ_OK;
+}
+}  // namespace
+
+extern "C" tq_status tq_dequantize(const tq_ctx* ctx, const void* k_cache, const void* v_cache, tq_dtype dtype, int batch,
+                                   int num_kv_heads, const int32_t* start_pos, const int32_t* lens, int max_len,
+                                   const int32_t* block_table, int max_pages_per_seq, int num_pages, void* k_out, void* v_out,
+                                   const int32_t* first_row, int total_rows, long long k_stride, long long v_stride,
+                                   void* stream) {
+  if (!ctx || (!k_out && !v_out) || (k_out && !k_cache) || (v_out && !v_cache) || misaligned(k_cache) || misaligned(v_cache))
+    return TQ_ERR_INVALID_ARG;
+  ReadArgs a{};
+  tq_status st = read_check(ctx, dtype, batch, num_kv_heads, start_pos, lens, max_len, block_table, max_pages_per_seq, num_pages,
+                            k_out, v_out, first_row, total_rows, k_stride, v_stride, a);
+  if (st != TQ_OK) return st;
+  if (batch == 0 || max_len == 0 || total_rows == 0) return TQ_OK;
+  st = on_device(ctx);
+  if (st != TQ_OK) return st;
+  a.kc = k_out ? static_cast<const uint8_t*>(k_cache) : nullptr;
+  a.vc = v_out ? static_cast<const uint8_t*>(v_cache) : nullptr;
+  a.k_page_bytes = static_cast<long long>(ctx->kl.block_bytes) * num_kv_heads;
+  a.v_page_bytes = static_cast<long long>(ctx->vl.block_bytes) * num_kv_heads;
+  return cuda_status(launch_read(a, ctx->cfg.d, dtype == TQ_F32, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" tq_status tq_kv8_dequantize(const tq_ctx* ctx, const tq_kv8_cache* cache, tq_dtype dtype, int batch,
+                                       const int32_t* start_pos, const int32_t* lens, int max_len, void* k_out, void* v_out,
+                                       const int32_t* first_row, int total_rows, long long k_stride, long long v_stride,
+                                       void* stream) {
+  tq_status st = kv8_check(ctx, cache, k_out != nullptr, v_out != nullptr);
+  if (st != TQ_OK) return st;
+  if (!k_out && !v_out) return TQ_ERR_INVALID_ARG;
+  ReadArgs a{};
+  st = read_check(ctx, dtype, batch, cache->num_kv_heads, start_pos, lens, max_len, cache->block_table, cache->max_pages_per_seq,
+                  cache->num_pages, k_out, v_out, first_row, total_rows, k_stride, v_stride, a);
+  if (st != TQ_OK) return st;
+  if (batch == 0 || max_len == 0 || total_rows == 0) return TQ_OK;
+  st = on_device(ctx);
+  if (st != TQ_OK) return st;
+  a.kc = k_out ? static_cast<const uint8_t*>(cache->k_codes) : nullptr;
+  a.vc = v_out ? static_cast<const uint8_t*>(cache->v_codes) : nullptr;
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  return cuda_status(launch_kv8_read(a, ctx->cfg.d, dtype == TQ_F32, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// attention over packed prompts
+// ---------------------------------------------------------------------------
+extern "C" tq_status tq_prompt_workspace_size(const tq_ctx* ctx, int num_seqs, int max_q_len, int Hq, int H, int max_k_len,
+                                              size_t* bytes) {
+  if (!ctx || !bytes || num_seqs < 0 || max_q_len < 0 || max_k_len < 0 || Hq < 1 || H < 1 || Hq % H) return TQ_ERR_INVALID_ARG;
+  const int d = ctx->cfg.d;
+  *bytes = prompt_simt_workspace(d);
+  return TQ_OK;
+}
+
+extern "C" tq_status tq_prompt_attention(const tq_ctx* ctx, const void* q, const void* k, const void* v, tq_dtype dtype, int num_seqs,
+                                         const int32_t* cu_q, const int32_t* cu_k, int total_q, int total_k, int max_q_len,
+                                         int max_k_len, int Hq, int H, int window, int sinks, float softmax_scale, void* out,
+                                         void* workspace, size_t workspace_bytes, long long q_stride, long long k_stride,
+                                         long long v_stride, void* stream) {
+  if (!ctx || (dtype != TQ_BF16 && dtype != TQ_F32) || num_seqs < 0 || total_q < 0 || total_k < 0 || max_q_len < 0 ||
+      max_k_len < 0 || Hq < 1 || H < 1 || Hq % H || window < 0 || sinks < 0 || !std::isfinite(softmax_scale))
+    return TQ_ERR_INVALID_ARG;
+  const int d = ctx->cfg.d, step = dtype == TQ_F32 ? 4 : 8;
+  const long long dq = static_cast<long long>(Hq) * d, dk = static_cast<long long>(H) * d;
+  if ((q_stride && (q_stride < dq || q_stride % step)) || (k_stride && (k_stride < dk || k_stride % step)) ||
+      (v_stride && (v_stride < dk || v_stride % step)))
+    return TQ_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return TQ_OK;
+  if (!q || !out || !cu_q || !cu_k || !workspace || (total_k && (!k || !v)) || misaligned(q) || misaligned(k) || misaligned(v) ||
+      misaligned(out) || misaligned(workspace) || misaligned4(cu_q) || misaligned4(cu_k))
+    return TQ_ERR_INVALID_ARG;
+  // the kernels' positions and rows are 32-bit
+  if (static_cast<long long>(total_q) * Hq > (1LL << 30) || total_k > (1 << 30) || max_k_len > (1 << 29) || H > 65535) return TQ_ERR_UNSUPPORTED;
+  PromptArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.qs = q_stride ? q_stride : dq;
+  a.ks = k_stride ? k_stride : dk;
+  a.vs = v_stride ? v_stride : dk;
+  // results where inputs are still to be read
+  const size_t e = dtype == TQ_F32 ? 4 : 2;
+  const auto overlaps = [&](const void* p, long long rows, long long stride, long long row) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(out);
+    return rows && x < y + static_cast<size_t>(total_q) * dq * e && y < x + (static_cast<size_t>(rows - 1) * stride + row) * e;
+  };
+  if (overlaps(q, total_q, a.qs, dq) || overlaps(k, total_k, a.ks, dk) || overlaps(v, total_k, a.vs, dk)) return TQ_ERR_INVALID_ARG;
+  a.S = num_seqs;
+  a.total_q = total_q;
+  a.total_k = total_k;
+  a.Hq = Hq;
+  a.H = H;
+  a.G = Hq / H;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.max_q = std::min(max_q_len, total_q);
+  a.max_k = std::min(max_k_len, total_k);
+  a.window = window < a.max_k ? window : 0;            // a window or first tokens beyond every key change nothing
+  a.sinks = std::min(sinks, a.max_k);
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.part = static_cast<float*>(workspace);
+  a.err = ctx->tab.err;
+  if (workspace_bytes < prompt_simt_workspace(d)) return TQ_ERR_WORKSPACE;
+  const tq_status st = on_device(ctx);
+  if (st != TQ_OK) return st;
+  return cuda_status(launch_prompt_simt(a, d, dtype == TQ_F32, static_cast<cudaStream_t>(stream)));
 }

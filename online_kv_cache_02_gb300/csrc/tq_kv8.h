@@ -49,6 +49,59 @@ struct Kv8Attn {
   uint32_t* err;
 };
 
+// Decode of sequences that share a prefix (tq_kv8_shared_decode_attention): groups of sequences one behind the other,
+// whose first pages are the same.  The prefix pass (`tail` 0) takes a group as one sequence of many queries that all see
+// the whole prefix, the tail pass (1) each sequence's pages behind it; both leave their sums, which a last kernel joins.
+struct Kv8SharedSeq {             // what a pass sees of group (or sequence) b
+  int row, n, pages0, pages;      // first query row (of batch) and table, queries, pages [pages0, pages0 + pages)
+  int p;                          // the queries' position
+};
+struct Kv8Share {
+  int tail, batch, groups, max_group;
+  const int32_t *group_start, *prefix_lens;
+  int4* seqs;                     // per sequence, from the prefix pass: prefix pages (0: no prefix), group, the group's first sequence
+  int2* items;                    // tcgen05 form: by block and KV head, the CTAs that hold it (-1: whole, in `state`)
+  float* state;                   // per query row: [items per head][maximum, sum, its exponent, 0, channels]
+};
+__device__ __forceinline__ Kv8SharedSeq kv8_group(const Kv8Attn& a, const Kv8Share& s, int g) {
+  const int r0 = s.group_start[g], r1 = s.group_start[g + 1], len = s.prefix_lens[g];
+  int pages = len < 0 ? 0 : len / kPage;
+  const int cap = min(a.maxp, a.max_seq_len / kPage);
+  if (r0 < 0 || r1 < r0 || r1 > s.batch || r1 - r0 > s.max_group || len < 0 || pages > cap) {
+    atomicOr(a.err, kErrSeqLen);
+    if (!(r0 >= 0 && r1 >= r0 && r1 <= s.batch && r1 - r0 <= s.max_group)) return Kv8SharedSeq{0, 0, 0, 0, -1};
+    pages = min(pages, cap);
+  }
+  return Kv8SharedSeq{r0, pages ? r1 - r0 : 0, 0, pages, kPage * pages - 1};
+}
+// What the tail pass and the join need of each sequence, by all threads of the prefix pass: the group that holds it by a
+// search in the ascending starts.
+__device__ __forceinline__ void kv8_share_seqs(const Kv8Attn& a, const Kv8Share& s) {
+  for (long long b = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; b < s.batch; b += static_cast<long long>(gridDim.x) * blockDim.x) {
+    int lo = 0, hi = s.groups - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (s.group_start[mid] <= b) lo = mid;
+      else hi = mid - 1;
+    }
+    const Kv8SharedSeq g = kv8_group(a, s, lo);
+    const bool in = g.n > 0 && b >= g.row && b - g.row < g.n;
+    if (!in && !(b >= s.group_start[lo] && b < s.group_start[lo + 1])) atomicOr(a.err, kErrSeqLen);   // in no group
+    s.seqs[b] = in ? make_int4(g.pages, lo, g.row, 0) : make_int4(0, 0, 0, 0);
+  }
+}
+__device__ __forceinline__ Kv8SharedSeq kv8_tail(const Kv8Attn& a, const Kv8Share& s, int b) {
+  int len = a.lens[b];
+  const int first = s.seqs[b].x;
+  const long long cap = a.max_seq_len < 16LL * a.maxp ? a.max_seq_len : 16LL * a.maxp;
+  if (len < 0 || len > cap || (len > 0 && len < kPage * first)) {
+    atomicOr(a.err, kErrSeqLen);
+    if (len > cap) len = static_cast<int>(cap);
+  }
+  const int pages = len <= kPage * first ? 0 : (len + kPage - 1) / kPage - first;
+  return Kv8SharedSeq{b, pages ? 1 : 0, first, pages, len - 1};
+}
+
 // A sequence's queries, cut to what its table and max_seq_len hold.
 struct Kv8Seq {
   int p0, n;                      // first query's position, queries
@@ -99,6 +152,20 @@ bool kv8_tc_takes(int T, int G, int d, bool f32, float softmax_scale);
 bool kv8_tc_splits(int B, int T, int G, int max_seq_len, int d);
 size_t kv8_tc_workspace(int B, int T, int G, int H, int max_seq_len, int d);
 cudaError_t launch_kv8_tc(const Kv8Attn& a, int d, cudaStream_t s);
+
+// Decode with shared prefixes (tq_kv8_shared.cu).
+size_t kv8_shared_workspace(int batch, int Hq, int H, int groups, int max_group, int max_seq_len, int d);
+cudaError_t launch_kv8_shared(Kv8Attn a, Kv8Share share, int d, bool f32, float softmax_scale, void* workspace, cudaStream_t s);
+// The passes: with `share` the launches below leave sums in share.state.
+cudaError_t launch_kv8_rows_shared(const Kv8Attn& a, const Kv8Share& share, int d, bool f32, cudaStream_t s);
+cudaError_t launch_kv8_tc_shared(const Kv8Attn& a, const Kv8Share& share, int d, cudaStream_t s);
+struct Kv8TcShape {               // of a tcgen05 call: its items per KV head, rows and channels an item, CTAs and blocks
+  int per, rows, dv, ctas, nqb;
+  size_t records;                 // bytes ahead of the parts
+  float lift;                     // of its weights' exponents
+};
+float kv8_rows_lift();            // of the other form's
+Kv8TcShape kv8_tc_shape(int B, int T, int G, int H, int max_seq_len, int d);
 
 }  // namespace tq
 

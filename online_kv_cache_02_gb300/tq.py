@@ -103,6 +103,16 @@ EXPORTS = {
                                  _SZ, _P], _S),
     "tq_kv8_causal_attention": ([_P, ctypes.POINTER(TQKv8Cache), _P, _I, _I, _I, _I, _P, _P, _I, _I, _I, ctypes.c_float,
                                  _P, _P, _SZ, _P], _S),
+    "tq_kv8_shared_workspace_size": ([_P, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)], _S),
+    "tq_kv8_shared_decode_attention": ([_P, ctypes.POINTER(TQKv8Cache), _P, _I, _I, _I, _P, _I, _I, _P, _P, _I, ctypes.c_float,
+                                        _P, _P, _SZ, _P], _S),
+    "tq_dequantize": ([_P, _P, _P, _I, _I, _I, _P, _P, _I, _P, _I, _I, _P, _P, _P, _I, ctypes.c_longlong,
+                       ctypes.c_longlong, _P], _S),
+    "tq_kv8_dequantize": ([_P, ctypes.POINTER(TQKv8Cache), _I, _I, _P, _P, _I, _P, _P, _P, _I, ctypes.c_longlong,
+                           ctypes.c_longlong, _P], _S),
+    "tq_prompt_workspace_size": ([_P, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)], _S),
+    "tq_prompt_attention": ([_P, _P, _P, _P, _I, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _SZ,
+                             ctypes.c_longlong, ctypes.c_longlong, ctypes.c_longlong, _P], _S),
     "tq_check_device_status": ([_P, ctypes.POINTER(ctypes.c_uint32)], _S),
     "tq_refine_counters": ([_P, ctypes.POINTER(ctypes.c_ulonglong), _I], _S),
     "tq_status_string": ([_S], ctypes.c_char_p),
@@ -396,3 +406,52 @@ def tq_kv8_causal_attention(ctx, cache, q, dtype, batch, n_new, num_q_heads, sta
     _check("tq_kv8_causal_attention", _lib.tq_kv8_causal_attention(
         ctx, cache, _ptr(q), dtype, batch, n_new, num_q_heads, _ptr(start_pos), _ptr(new_lens), max_seq_len, window,
         sinks, softmax_scale, _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def tq_kv8_shared_workspace_size(ctx, batch, num_q_heads, num_kv_heads, num_groups, max_group, max_seq_len):
+    n = _SZ()
+    _check("tq_kv8_shared_workspace_size", _lib.tq_kv8_shared_workspace_size(
+        ctx, batch, num_q_heads, num_kv_heads, num_groups, max_group, max_seq_len, ctypes.byref(n)))
+    return n.value
+
+
+def tq_kv8_shared_decode_attention(ctx, cache, q, dtype, batch, num_q_heads, seq_lens, max_seq_len, num_groups, group_start,
+                                   prefix_lens, max_group, softmax_scale, out, workspace, workspace_bytes, stream=None):
+    """Decode attention over the 8-bit cache of sequences that share a prefix's pages, group by group (see tq.h)."""
+    _check("tq_kv8_shared_decode_attention", _lib.tq_kv8_shared_decode_attention(
+        ctx, cache, _ptr(q), dtype, batch, num_q_heads, _ptr(seq_lens), max_seq_len, num_groups, _ptr(group_start),
+        _ptr(prefix_lens), max_group, softmax_scale, _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def tq_dequantize(ctx, k_cache, v_cache, dtype, batch, num_kv_heads, start_pos, lens, max_len, block_table,
+                  max_pages_per_seq, num_pages, k_out, v_out, first_row, total_rows, k_stride=0, v_stride=0, stream=None):
+    """Read runs of the 2-4-bit cache back into rows, keys and values or one of them (see tq.h); strides in elements."""
+    _check("tq_dequantize", _lib.tq_dequantize(
+        ctx, _ptr(k_cache), _ptr(v_cache), dtype, batch, num_kv_heads, _ptr(start_pos), _ptr(lens), max_len,
+        _ptr(block_table), max_pages_per_seq, num_pages, _ptr(k_out), _ptr(v_out), _ptr(first_row), total_rows, k_stride,
+        v_stride, _stream(stream)))
+
+
+def tq_kv8_dequantize(ctx, cache, dtype, batch, start_pos, lens, max_len, k_out, v_out, first_row, total_rows, k_stride=0,
+                      v_stride=0, stream=None):
+    """Read runs of the 8-bit cache back into rows (see tq.h)."""
+    _check("tq_kv8_dequantize", _lib.tq_kv8_dequantize(
+        ctx, cache, dtype, batch, _ptr(start_pos), _ptr(lens), max_len, _ptr(k_out), _ptr(v_out), _ptr(first_row),
+        total_rows, k_stride, v_stride, _stream(stream)))
+
+
+def tq_prompt_workspace_size(ctx, num_seqs, max_q_len, num_q_heads, num_kv_heads, max_k_len):
+    n = _SZ()
+    _check("tq_prompt_workspace_size", _lib.tq_prompt_workspace_size(ctx, num_seqs, max_q_len, num_q_heads, num_kv_heads,
+                                                                     max_k_len, ctypes.byref(n)))
+    return n.value
+
+
+def tq_prompt_attention(ctx, q, k, v, dtype, num_seqs, cu_q, cu_k, total_q, total_k, max_q_len, max_k_len, num_q_heads,
+                        num_kv_heads, window, sinks, softmax_scale, out, workspace, workspace_bytes, q_stride=0, k_stride=0,
+                        v_stride=0, stream=None):
+    """Causal attention over packed sequences of fresh queries, keys and values (see tq.h); strides in elements per token."""
+    _check("tq_prompt_attention", _lib.tq_prompt_attention(
+        ctx, _ptr(q), _ptr(k), _ptr(v), dtype, num_seqs, _ptr(cu_q), _ptr(cu_k), total_q, total_k, max_q_len, max_k_len,
+        num_q_heads, num_kv_heads, window, sinks, softmax_scale, _ptr(out), _ptr(workspace), workspace_bytes, q_stride,
+        k_stride, v_stride, _stream(stream)))
