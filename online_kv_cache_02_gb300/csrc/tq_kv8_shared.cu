@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(256) kv8_share_join_kernel(const __grid_consta
     const float* p = part(i);
     const float f = exp2_fast(power(i, p) - E);
     L = fmaf(f, p[1], L);
-    if (4 * lane >= DV || f == 0.0f) continue;
+    if (4 * lane >= DV) continue;
     const float4 x = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
     acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y), acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
   }

@@ -6,6 +6,7 @@
 // shared memory, so that a thread's 4 x 4 scores take two 16-byte loads per channel; sums are fp32 throughout.
 // Bound by the FMA pipes and shared-memory loads.
 
+#include "tq_kv8.h"
 #include "tq_prompt.h"
 
 #include <cuda_bf16.h>
@@ -226,7 +227,6 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
     const float* p = part(k);
     const float f = exp2_fast(p[0] - ref + p[2] - E);
     L = fmaf(f, p[1], L);
-    if (f == 0.0f) continue;                           // (a part of nothing that holds NaN or infinities counts by its sum alone)
 #pragma unroll
     for (int i = 0; i < V4; ++i) {
       if (128 * i + 4 * lane >= DV) continue;
@@ -252,13 +252,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
   }
 }
 
-int device_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return 152;
-  return sms;
-}
-int simt_ctas(int d) { return device_sms() * (d > 128 ? 1 : d > 64 ? 1 : 2); }
+int simt_ctas(int d) { return prompt_sms() * (d > 64 ? 1 : 2); }
 
 template <int D>
 cudaError_t launch_t(const PromptArgs& a, bool f32, cudaStream_t s) {
@@ -274,6 +268,8 @@ cudaError_t launch_t(const PromptArgs& a, bool f32, cudaStream_t s) {
   return launch_prompt_join(a, D, f32, ctas, kRows, 1, s);
 }
 }  // namespace
+
+int prompt_sms() { return kv8_sm_count(); }
 
 long long prompt_most_blocks(const PromptArgs& a, int rows) {
   const long long each = (static_cast<long long>(a.max_q) * a.G + rows - 1) / rows;

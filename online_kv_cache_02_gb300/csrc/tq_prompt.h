@@ -279,7 +279,8 @@ bool prompt_splits(const PromptArgs& a, int rows, int tok, int cost);
 // Workspace of either form (whatever the dtype and scale), its CTAs and its launch.
 size_t prompt_simt_workspace(int d);
 cudaError_t launch_prompt_simt(const PromptArgs& a, int d, bool f32, cudaStream_t s);
-bool prompt_tc_takes(int d, bool f32);
+int prompt_sms();                         // of the current device
+bool prompt_tc_takes(const PromptArgs& a, int d, bool f32);
 size_t prompt_tc_workspace(int d);
 cudaError_t launch_prompt_tc(const PromptArgs& a, int d, cudaStream_t s);
 // Joins the parts of split items (PART floats a row: maximum, sum, its exponent, 0, then a run of channels).

@@ -1,0 +1,851 @@
+// Attention over packed prompts on the tensor cores (tcgen05), bf16, d = 64, 128 or 256.
+//
+// An item is (sequence, KV head, block of 256 query rows r = t G + g); keys go by in tiles of 128.  All items' tiles
+// form one list that is cut into equal spans, one per CTA; the parts of an item that crosses spans are joined by a second
+// kernel.  Per tile, with x = scale log2(e) <q, k>:
+//   S = Q K^T              bf16, from tiles that TMA puts in place
+//   w = 2^(x - M)          M the maximum of the row's first tile; bf16 has fp32's range, so that M moves only where a
+//                          tile's weights sum to more than 2^40, and no tile but the first looks for a maximum
+//   O += w V, l += sum w   w as bf16 (off by 2^-8 at most) in tensor memory, V's token rows read MN-major;
+//   out = O / l.
+// Two 128-row halves A and B of the block take turns: while the softmax of one runs, the tensor cores work on the other.
+// Tensor memory: S of A and B (each overlaid by its weights), O of A and B, 512 columns.  An item of at most 128 rows has
+// its rows in both halves: A takes the even tiles, B the odd ones, and A adds B's sums to its own at the item's end.  At
+// d = 256 an item is 128 rows and one half of the values' channels (the scores are the same work twice: queries, keys and
+// values of 256 rows and channels do not fit), in the same turns.
+//
+// A key that a row does not see has weight zero, but zero times an infinity is NaN: the values of tiles that some row does
+// not see in full are looked through before they are multiplied, what is not finite there is taken out, and added to the
+// rows that see it at the end.
+//
+// Warps 0-3 and 4-7: the softmax of A and B (thread = row), the queries, the results; 8: items, the copies of keys and
+// values; 9: MMA issue; 10 and 11: queries to L2, the values of edge tiles.  Every wait is bounded; a wait that gives up
+// sets the device error word.
+
+#include "tq_prompt.h"
+#include "tq_tc.cuh"
+#include "tq_tc_attn.cuh"
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+namespace tq {
+namespace {
+
+using namespace tcx;
+
+constexpr int kTok = 128;                 // keys per tile
+constexpr int kThreads = 384;
+constexpr int kItems = 4;                 // items announced ahead
+constexpr int kItemCost = 5;              // an item's start and end, in tiles' time
+constexpr int kMinSpan = 2 + kItemCost;   // a CTA's share of the list at least
+constexpr float kMNone = -3.0e38f;        // a maximum before any score: finite, and below the scores of fp32
+constexpr float kFull = 1.0995116e12f;    // 2^40: a tile's sum beyond it moves the maximum
+// x - M in one rounding is off by half a step of M against the other tiles' M: beyond 2^16 scores are rounded first, so that
+// small differences of large ones are exact.
+constexpr float kBig = 65536.0f;
+constexpr int kCheckRing = 8;
+
+// Registers: 12 warps start with 168 a thread, and the eight of the softmax take what the others give back.
+constexpr int kRegsMore = 216, kRegsLess = 72;
+static_assert(8 * kRegsMore + 4 * kRegsLess <= 12 * 168, "more registers than the block starts with");
+
+template <int D>
+struct PG {
+  static constexpr bool WIDE = D == 256;
+  static constexpr int ROWS = WIDE ? 128 : 256;        // query rows per item
+  static constexpr int DV = WIDE ? 128 : D;            // value channels per item
+  static constexpr int PER = D / DV;                   // items per KV head and block of rows
+  static constexpr int KCH = D > 128 ? D / 128 : 1;    // pieces of a tile's keys, 128 channels each
+  static constexpr int PIECE = kTok * 2 * (D < 128 ? D : 128);      // bytes of one, and of a tile's values
+  static constexpr int KST = D == 64 ? 5 : D == 128 ? 2 : 3, VST = D == 64 ? 5 : D == 128 ? 3 : 2;
+  static constexpr int QX = 128 * 2 * D;               // 128 rows' queries
+  static constexpr int QB = WIDE ? 0 : QX;             // from half A's queries to half B's
+  static constexpr int PART = DV + 4;                  // floats of a row's partial
+  static constexpr int Q = 0;                          // [A, B][64-channel panels][128 rows][128 B]
+  static constexpr int K = Q + QX + QB;                // [stage][64-channel panels][128 tokens][128 B]
+  static constexpr int V = K + KST * PIECE;
+  static constexpr int ITEM = V + VST * PIECE;
+  static constexpr int BAR = ITEM + kItems * 64;
+};
+enum Bar {
+  bKFull = 0, bKFree = bKFull + 5, bVFull = bKFree + 5, bVFree = bVFull + 5, bVOk = bVFree + 5, bSFull = bVOk + 5, bPFull = bSFull + 2,
+  bODone = bPFull + 2, bQReady = bODone + 2, bItem = bQReady + 2, bItemFree = bItem + kItems, bChecked = bItemFree + kItems,
+  bJoin = bChecked + kCheckRing, bOFree, bQFree, bDrain, bCount
+};
+template <int D>
+struct PS {                                            // behind the barriers
+  static constexpr int JOIN = PG<D>::BAR + 8 * ((bCount + 1) & ~1);      // half B's (M, l) of 128 rows
+  static constexpr int ODD = JOIN + 1024;              // per announced item: values that are not finite in edge tiles
+  static constexpr int TMEM = ODD + 4 * kCheckRing;
+  static constexpr int BYTES = TMEM + 16;
+};
+static_assert(PS<64>::BYTES <= 232448 && PS<128>::BYTES <= 232448 && PS<256>::BYTES <= 232448, "shared memory per block");
+static_assert(PG<64>::ITEM >= 4 * (2 * kPromptList + 64), "the list's room");
+__device__ __forceinline__ constexpr uint32_t col_s(uint32_t X) { return 128u * X; }
+__device__ __forceinline__ constexpr uint32_t col_o(uint32_t X) { return 256u + 128u * X; }
+
+// What the load warp tells the others of an item.
+struct alignas(16) ItemMsg {
+  int valid, h, q0, r0;                   // h: item of the block (KV head, at d = 256 with a half of the values' channels)
+  int rows, p0, pmin, pmax;               // p0: position of the sequence's first query
+  int ntile, t0, slot, k0;                // slot: of the workspace for a part of the tiles; -1 for all of them
+  int ns, w0, pad[2];
+  __device__ __forceinline__ int first_key(int i) const {          // of its i-th tile
+    const int t = t0 + i;
+    return t < ns ? kTok * t : w0 + kTok * (t - ns);
+  }
+  // every row sees every key of the tile from j0 on
+  __device__ __forceinline__ bool full(int j0, int window, int sinks) const {
+    return j0 + kTok - 1 <= pmin && (!window || j0 > pmax - window || j0 + kTok - 1 < sinks);
+  }
+};
+static_assert(sizeof(ItemMsg) == 64, "items in shared memory");
+
+// S = Q K^T, 128 channels (64 at d = 64): steps of 16 channels (32 B, 2 descriptor units), panels of 64 channels 16 KB
+// apart; one statement, one elected lane.
+template <int ACC>
+__device__ __forceinline__ void mma8_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred e, t, f;\n .reg .b64 q1, q2, q3, q4, q5, q6, q7, k1, k2, k3, k4, k5, k6, k7;\n"
+      " add.u64 q1, %1, 2;\n add.u64 q2, %1, 4;\n add.u64 q3, %1, 6;\n add.u64 q4, %1, 1024;\n add.u64 q5, %1, 1026;\n"
+      " add.u64 q6, %1, 1028;\n add.u64 q7, %1, 1030;\n"
+      " add.u64 k1, %2, 2;\n add.u64 k2, %2, 4;\n add.u64 k3, %2, 6;\n add.u64 k4, %2, 1024;\n add.u64 k5, %2, 1026;\n"
+      " add.u64 k6, %2, 1028;\n add.u64 k7, %2, 1030;\n"
+      " setp.ne.b32 t, 1, 0;\n setp.ne.b32 f, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], q1, k1, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], q2, k2, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], q3, k3, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], q4, k4, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], q5, k5, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], q6, k6, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], q7, k7, %3, t;\n}\n" ::"r"(d),
+      "l"(q), "l"(k), "r"(idesc), "n"(ACC)
+      : "memory");
+}
+__device__ __forceinline__ void mma4_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred e, t, f;\n .reg .b64 q1, q2, q3, k1, k2, k3;\n"
+      " add.u64 q1, %1, 2;\n add.u64 q2, %1, 4;\n add.u64 q3, %1, 6;\n add.u64 k1, %2, 2;\n add.u64 k2, %2, 4;\n add.u64 k3, %2, 6;\n"
+      " setp.ne.b32 t, 1, 0;\n setp.ne.b32 f, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], q1, k1, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], q2, k2, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], q3, k3, %3, t;\n}\n" ::"r"(d),
+      "l"(q), "l"(k), "r"(idesc)
+      : "memory");
+}
+// kind::f16 with bf16 A and B, fp32 accumulate, M = 128, N = n
+__host__ __device__ constexpr uint32_t idesc_bf16(int n) { return idesc_f16(n) | (1u << 7) | (1u << 10); }
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int head, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(row), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Whether one of two bf16 values is not finite.
+__device__ __forceinline__ bool odd_pair(uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; }
+__device__ __forceinline__ bool odd_piece(uint4 w) { return odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w); }
+
+// Those of the 32 keys from j0 on that the query at position p sees.
+__device__ __forceinline__ uint32_t seen32(int p, int j0, int window, int sinks) {
+  const int hi = p - j0;                               // up to hi
+  uint32_t see = hi < 0 ? 0u : hi >= 31 ? 0xFFFFFFFFu : (2u << hi) - 1u;
+  if (window) {
+    const int lo = hi - window + 1, sk = sinks - j0;   // from lo on, or below sk
+    const uint32_t win = lo <= 0 ? 0xFFFFFFFFu : lo > 31 ? 0u : 0xFFFFFFFFu << lo;
+    const uint32_t snk = sk <= 0 ? 0u : sk > 31 ? 0xFFFFFFFFu : (1u << sk) - 1u;
+    see &= win | snk;
+  }
+  return see;
+}
+// One tile's weights of a thread's row with a new maximum: scores are rounded before they are compared.  accumulated: O
+// holds tiles before.  Returns M and l.
+template <int DV>
+__device__ __noinline__ float2 careful_tile(uint32_t ts, uint32_t to, int j0, int p, int window, int sinks, float f, bool accumulated,
+                                            float m, float l) {
+  auto scores = [&](int c, float (&y)[32]) {
+    tld32(ts + 32u * c, y);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) y[k] = prompt_sees(p, j0 + 32 * c + k, window, sinks) ? __fmul_rn(y[k], f) : -INFINITY;
+    __syncwarp();
+  };
+  float y[32], mn = m;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    scores(c, y);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) mn = fmaxf(mn, y[k]);
+  }
+  const float alpha = m == mn ? 1.0f : ex2(m - mn);
+  __syncwarp();
+  if (accumulated) rescale_o<DV>(to, alpha);
+  l *= alpha;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {                        // (the weights overlay scores that were read)
+    uint32_t w[16];
+    scores(c, y);
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float y0 = ex2(__fsub_rn(y[2 * k], mn)), y1 = ex2(__fsub_rn(y[2 * k + 1], mn));
+      sum += y0 + y1;
+      w[k] = bf16x2_bits(y0, y1);
+    }
+    l += sum;
+    tst16(ts + 16u * c, w);
+  }
+  return make_float2(mn, l);
+}
+
+// What is not finite among the values that a row sees of an item's edge tiles, added to its O.  `v`: the item's first value
+// channel of the sequence's key 0.
+template <int DV>
+__device__ __noinline__ void add_odd_values(uint32_t to, const __nv_bfloat16* v, long long stride, int t0, int ntile, int ns, int w0, int pmin,
+                                            int pmax, int p, int window, int sinks) {
+  ItemMsg it;
+  it.t0 = t0, it.ns = ns, it.w0 = w0, it.pmin = pmin, it.pmax = pmax;
+#pragma unroll 1
+  for (int c = 0; c < DV / 16; ++c) {
+    float o[16];
+    uint32_t x[16];
+    tld16(to + 16u * c, o);
+#pragma unroll 1
+    for (int t = 0; t < ntile; ++t) {
+      const int j0 = it.first_key(t);
+      if (it.full(j0, window, sinks)) continue;
+#pragma unroll 1
+      for (int j = j0; j < j0 + kTok && j <= pmax; ++j) {
+        const uint4* from = reinterpret_cast<const uint4*>(v + j * stride + 16 * c);
+        const uint4 w[2] = {from[0], from[1]};         // the same for the whole warp
+        if (!odd_piece(w[0]) && !odd_piece(w[1])) continue;
+        const bool see = prompt_sees(p, j, window, sinks);
+        const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float lo = __uint_as_float(u[k] << 16), hi = __uint_as_float(u[k] & 0xFFFF0000u);
+          o[2 * k] += see && !(fabsf(lo) <= 3.4028234e38f) ? lo : 0.0f;
+          o[2 * k + 1] += see && !(fabsf(hi) <= 3.4028234e38f) ? hi : 0.0f;
+        }
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(o[k]);
+    tst16(to + 16u * c, x);
+  }
+  tst_wait();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                     int split) {
+  using L = PG<D>;
+  using P = PS<D>;
+  extern __shared__ __align__(1024) unsigned char sm_raw[];
+  unsigned char* sm = sm_raw;
+  const uint32_t sb = su32(sm);
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  auto bar = [&](int i) { return sb + L::BAR + 8u * static_cast<uint32_t>(i); };
+  ItemMsg* item_ring = reinterpret_cast<ItemMsg*>(sm + L::ITEM);
+  volatile int* odd_of = reinterpret_cast<volatile int*>(sm + P::ODD);
+  PSplit* splits = reinterpret_cast<PSplit*>(a.part);              // one per CTA, then the partials' slots
+  if (sb & 1023u) {                                    // the swizzles' period: the kernel's only shared memory starts on one
+    pdl_wait();
+    if (tid == 0) {
+      atomicOr(a.err, kErrLayout);
+      if (split) splits[blockIdx.x].valid = 0;
+    }
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < L::KST; ++i) {
+      bar_init(bar(bKFull + i), 1);
+      bar_init(bar(bKFree + i), 1);
+    }
+    for (int i = 0; i < L::VST; ++i) {
+      bar_init(bar(bVFull + i), 1);
+      bar_init(bar(bVFree + i), 1);
+      bar_init(bar(bVOk + i), 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bar(bSFull + i), 1);
+      bar_init(bar(bPFull + i), 4);
+      bar_init(bar(bODone + i), 1);
+      bar_init(bar(bQReady + i), 4);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      bar_init(bar(bItem + i), 1);
+      bar_init(bar(bItemFree + i), 11);                // every warp but the one that announces
+    }
+    for (int i = 0; i < kCheckRing; ++i) {
+      bar_init(bar(bChecked + i), 2);
+      odd_of[i] = 0;
+    }
+    bar_init(bar(bJoin), 4);
+    bar_init(bar(bOFree), 4);
+    bar_init(bar(bQFree), 4);
+    bar_init(bar(bDrain), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + P::TMEM), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  if (split) pdl_trigger();                            // the join's launch
+  prompt_zero_rows<__nv_bfloat16>(a, D);
+  PromptSpan span{};
+  if (split) span = prompt_span<L::ROWS, kTok, kItemCost, kThreads>(a, a.H * L::PER, kMinSpan, reinterpret_cast<int*>(sm));
+  fence_async_smem();
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + P::TMEM);
+  float* parts = a.part + static_cast<size_t>(gridDim.x) * (sizeof(PSplit) / sizeof(float));
+  bool failed = false;
+  // a warp's wait for phase `phase` of a barrier; once one gave up, every later one returns at once
+  auto wait = [&](int i, int phase) {
+    if (!failed && __all_sync(0xffffffffu, wait_short(bar(i), phase & 1))) return true;
+    failed = true;
+    return false;
+  };
+  // the n-th item of this CTA, from the ring
+  auto next_item = [&](int n) {
+    ItemMsg x{};
+    if (wait(bItem + n % kItems, n / kItems)) x = item_ring[n % kItems];
+    __syncwarp();
+    if (lane == 0) bar_arrive(bar(bItemFree + n % kItems));
+    return x;
+  };
+
+  if (warp < 8) {
+    // ---- softmax of half X (thread = row), the queries, the results -----------------------
+    // Accesses to tensor memory are the whole warp's: behind a branch that only some lanes take they meet again first.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMore));
+    const int X = warp >> 2, wq = warp & 3, r = 32 * wq + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * wq) << 16);
+    const uint32_t ts = trow + col_s(X), to = trow + col_o(X);
+    const float f = fabsf(a.scale_log2);
+    const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // whole sectors per store
+    int nS = 0, nO = 0, nJ = 0, nF = 0;                // phases of S, of the final O, of the halves' join, of the queries' release
+    float2* join = reinterpret_cast<float2*>(sm + P::JOIN);
+    struct Row {
+      bool live;
+      int p;                                           // position; -1: an absent row sees nothing
+      long long at;                                    // its first element of out
+    };
+    auto mine = [&](const ItemMsg& x) { return x.valid && (X == 0 || x.rows > 128 || x.ntile > 1); };
+    // The row of an item that is this thread's; the warp's 32 rows of queries to shared memory, D / 8 lanes per row (a lane
+    // per row would ask for 32 lines with each load).  The item before has no score MMA left: its last scores were read.
+    auto queries = [&](const ItemMsg& x) {
+      Row w;
+      const int rx = x.rows > 128 ? 128 * X + r : r, gr = x.r0 + rx, tok = gr / a.G, g = gr - tok * a.G, hq = x.h / L::PER * a.G + g;
+      w.live = rx < x.rows;
+      w.p = w.live ? x.p0 + tok : -1;
+      w.at = ((static_cast<long long>(x.q0) + tok) * a.Hq + hq) * D;
+      if (L::WIDE && X) return w;                      // half A does the work for both
+      const uint32_t qx = sb + L::Q + X * L::QB;
+      constexpr int kP = D / 8, kR = 32 / kP;          // 16-byte pieces per row, rows per load
+      constexpr int kB = kP < 16 ? kP : 16;            // loads in flight
+      const long long where = w.live ? (static_cast<long long>(x.q0) + tok) * a.qs + static_cast<long long>(hq) * D : -1;
+      const int piece = lane % kP;
+#pragma unroll 1
+      for (int i0 = 0; i0 < kP; i0 += kB) {
+        uint4 v4[kB];
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+          const long long at = __shfl_sync(0xffffffffu, where, kR * (i0 + i) + lane / kP);
+          v4[i] = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at)[piece] : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+          const int row = 32 * wq + kR * (i0 + i) + lane / kP;
+          sts128(qx + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4), v4[i].x ^ flip, v4[i].y ^ flip, v4[i].z ^ flip,
+                 v4[i].w ^ flip);
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(bQReady + X));
+      return w;
+    };
+    ItemMsg it = next_item(0);
+    Row row{};
+    if (mine(it)) row = queries(it);
+    for (int n = 0; it.valid; ++n) {
+      const int ntile = it.ntile;
+      if (!mine(it)) {                                 // one tile of at most 128 rows: nothing for B
+        it = next_item(n + 1);
+        if (mine(it)) row = queries(it);
+        continue;
+      }
+      const int p = row.p;
+      const bool turns = it.rows <= 128;               // the halves take the tiles in turn
+      const int first = turns ? X : 0, step = turns ? 2 : 1;
+      float m = kMNone, l = 0.0f;
+      bool bigs = false;                               // a row of the warp has had a maximum beyond kBig
+      for (int t = first; t < ntile; t += step) {
+        if (!wait(bSFull + X, nS++)) break;
+        tc_after();
+        if (L::WIDE && X && t + step >= ntile) {       // both halves' queries have been used
+          if (lane == 0) bar_arrive(bar(bQFree));
+          __syncwarp();
+        }
+        const int j0 = it.first_key(t);
+        bool done = false;
+        if (!bigs) {
+          float x[kTok];
+          tld32x4(ts, x);
+          if (!it.full(j0, a.window, a.sinks)) {
+#pragma unroll
+            for (int c = 0; c < kTok; c += 32) {
+              const uint32_t see = seen32(p, j0 + c, a.window, a.sinks);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[c + k] = (see >> k) & 1u ? x[c + k] : -INFINITY;
+            }
+          }
+          if (t == first) {
+            float m0 = x[0], m1 = x[1];
+#pragma unroll
+            for (int c = 2; c < kTok; c += 2) {
+              m0 = fmaxf(m0, x[c]);
+              m1 = fmaxf(m1, x[c + 1]);
+            }
+            m = fmaxf(fmaxf(m0, m1) * f, kMNone);
+          }
+          bigs = __any_sync(0xffffffffu, fabsf(m) > kBig && m > kMNone);
+          if (!bigs) {
+            uint32_t w[kTok / 2];
+            const uint64_t f2 = pack2(f, f), b2 = pack2(-m, -m);
+            uint64_t s2 = 0ull, s3 = 0ull;
+#pragma unroll
+            for (int c = 0; c < kTok; c += 4) {
+              float y0, y1, y2, y3;
+              unpack2(fma2(pack2(x[c], x[c + 1]), f2, b2), y0, y1);
+              unpack2(fma2(pack2(x[c + 2], x[c + 3]), f2, b2), y2, y3);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              y2 = ex2(y2);
+              y3 = ex2(y3);
+              s2 = add2(s2, pack2(y0, y1));
+              s3 = add2(s3, pack2(y2, y3));
+              w[c / 2] = bf16x2_bits(y0, y1);
+              w[c / 2 + 1] = bf16x2_bits(y2, y3);
+            }
+            float s0, s1;
+            unpack2(add2(s2, s3), s0, s1);
+            s0 += s1;
+            if (!__any_sync(0xffffffffu, s0 > kFull)) {
+              l += s0;
+              tst32(ts, *reinterpret_cast<uint32_t(*)[32]>(w));
+              tst32(ts + 32u, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
+              done = true;
+            }
+          }
+        }
+        if (!done) {
+          const float2 next = careful_tile<L::DV>(ts, to, j0, p, a.window, a.sinks, f, t > first, t > first ? m : kMNone, l);
+          m = next.x;
+          l = next.y;
+        }
+        tst_wait();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(bPFull + X));
+      }
+      if (failed) break;
+      // the next item's queries first: its scores then run beside what is left of this one
+      const ItemMsg was = it;
+      const Row done_row = row;
+      it = next_item(n + 1);
+      if (L::WIDE && X == 0 && ntile > 1 && !wait(bQFree, nF++)) break;     // half B has its last scores too
+      if (mine(it)) row = queries(it);
+      // ---- the row's result (or partial) ----
+      if (!wait(bODone + X, nO)) break;
+      ++nO;
+      tc_after();
+      if (turns && ntile > 1) {
+        if (X) {
+          join[r] = make_float2(m, l);
+          tc_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(bar(bJoin));
+          if (!wait(bOFree, nJ++)) break;              // A has read this half's sums: the next item may overwrite them
+          tc_after();
+          continue;
+        }
+        if (!wait(bJoin, nJ++)) break;
+        tc_after();
+        const float2 other = join[r];
+        const float ref = fmaxf(m, other.x);
+        const float fa = ex2(m - ref), fb = ex2(other.x - ref);
+        m = ref;
+        l = fa * l + fb * other.y;
+#pragma unroll 1
+        for (int c = 0; c < L::DV / 16; ++c) {
+          float o[16], o2[16];
+          uint32_t u[16];
+          tld16(to + 16u * c, o);
+          tld16(trow + col_o(1) + 16u * c, o2);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(fa * o[k] + fb * o2[k]);
+          tst16(to + 16u * c, u);
+        }
+        tst_wait();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(bOFree));
+        __syncwarp();
+      }
+      if (!wait(bChecked + n % kCheckRing, n / kCheckRing)) break;
+      const bool odd = __any_sync(0xffffffffu, odd_of[n % kCheckRing] == n + 1);
+      const float inv = prompt_inverse(l, done_row.p);
+      float* part = parts + (static_cast<long long>(was.slot) * L::ROWS + (turns ? 0 : 128 * X) + r) * L::PART;
+      const int ch0 = was.h % L::PER * L::DV;
+      if (__builtin_expect(odd, 0))
+        add_odd_values<L::DV>(to, static_cast<const __nv_bfloat16*>(a.v) + was.k0 * a.vs + static_cast<long long>(was.h / L::PER) * D + ch0, a.vs,
+                              was.t0, ntile, was.ns, was.w0, was.pmin, was.pmax, done_row.p, a.window, a.sinks);
+#pragma unroll 1
+      for (int c = 0; c < L::DV / 32; ++c) {
+        float o[32];
+        tld32(to + 32u * c, o);
+        if (done_row.live && was.slot < 0) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = bf16x2_bits(o[2 * k] * inv, o[2 * k + 1] * inv);
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + done_row.at + ch0 + 32 * c;
+          if (wide) {
+            stg256(dst, w);
+            stg256(dst + 16, w + 8);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(dst)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          }
+        } else if (done_row.live) {
+          float4* dst = reinterpret_cast<float4*>(part + 4 + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          if (c == 0) *reinterpret_cast<float4*>(part) = make_float4(m, l, 0.0f, 0.0f);
+        }
+        __syncwarp();                                  // lanes with no row wait: the loads are the whole warp's
+      }
+      tc_before();                                     // O is read before the next item's first P is announced
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLess));
+    if (warp == 8) {
+      // ---- items, keys, values ----------------------------------------------------------------
+      int n = 0, ck = 0, cv = 0;                       // items, and pieces of keys and tiles of values asked for
+      auto publish = [&](const ItemMsg& x) {
+        // Every warp has taken the one before.  If one has not within the limit, its room stays as it is, and the others'
+        // waits for this one give up too.
+        if (n >= kItems && !__all_sync(0xffffffffu, wait_short(bar(bItemFree + n % kItems), (n / kItems - 1) & 1))) {
+          failed = true;
+          return;
+        }
+        if (lane == 0) {
+          item_ring[n % kItems] = x;
+          bar_arrive(bar(bItem + n % kItems));
+        }
+        ++n;
+      };
+      auto copy = [&](const CUtensorMap* map, uint32_t dst, int ch, int head, int row, uint32_t full) {
+        if (lane == 0) {
+          bar_arrive_tx(full, L::PIECE);
+#pragma unroll
+          for (int i = 0; i < L::PIECE / 16384; ++i) tma_rows(dst + 16384 * i, map, ch + 64 * i, head, row, full);
+        }
+        __syncwarp();
+      };
+      PromptWalk<L::ROWS, kTok, kItemCost> w;
+      w.start(a, span, a.H * L::PER, split != 0);
+      while (!failed && w.next(a, span)) {
+        const PromptBlock& b = w.blk;
+        publish(ItemMsg{1, w.h, b.seq.q0, b.r0, b.rows, b.seq.m - b.seq.n, b.pmin, b.pmax, w.t1 - w.t0, w.t0, w.slot, b.seq.k0, b.ns, b.w0, {0, 0}});
+        const int head = w.h / L::PER, ahead = b.rows <= 128 ? 2 : 1;      // a tile's scores are issued so many steps before its values
+        auto keys = [&](int t) {
+          for (int i = 0; i < L::KCH; ++i, ++ck) {
+            if (ck >= L::KST && !wait(bKFree + ck % L::KST, ck / L::KST - 1)) return;
+            copy(&mk, sb + L::K + (ck % L::KST) * L::PIECE, 128 * i, head, b.seq.k0 + b.first_key<kTok>(t), bar(bKFull + ck % L::KST));
+          }
+        };
+        for (int t = w.t0; t < w.t1 && t < w.t0 + ahead && !failed; ++t) keys(t);
+        for (int t = w.t0; t < w.t1 && !failed; ++t, ++cv) {
+          if (cv >= L::VST && !wait(bVFree + cv % L::VST, cv / L::VST - 1)) break;
+          copy(&mv, sb + L::V + (cv % L::VST) * L::PIECE, w.h % L::PER * L::DV, head, b.seq.k0 + b.first_key<kTok>(t), bar(bVFull + cv % L::VST));
+          if (t + ahead < w.t1) keys(t + ahead);
+        }
+        if (failed) break;
+        w.pass(a, span);
+      }
+      if (!failed) publish(ItemMsg{});
+      if (split && lane == 0) splits[blockIdx.x] = w.cut;
+      // copies still in flight land before the CTA ends
+      bool f2 = false;
+      for (int s = ck >= L::KST ? ck - L::KST : 0; s < ck; ++s) (void)bar_wait(bar(bKFull + s % L::KST), (s / L::KST) & 1, f2);
+      for (int s = cv >= L::VST ? cv - L::VST : 0; s < cv; ++s) (void)bar_wait(bar(bVFull + s % L::VST), (s / L::VST) & 1, f2);
+    } else if (warp == 9) {
+      // ---- MMA issue, the warp converged: O += w V of a tile and the next tile's scores, half A, then half B, in strict
+      // order (left to mix, both halves' MMAs would end together and neither softmax overlap the other) -------------------
+      auto ready = [&](int i, int phase) {             // wait() in few instructions
+        if (__all_sync(0xffffffffu, wait_short(bar(i), phase & 1))) return true;
+        failed = true;
+        return false;
+      };
+      int n = 0, ck = 0, cv = 0;                       // items; pieces of keys whose scores, tiles whose values were issued
+      ItemMsg it = next_item(0);
+      int nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;          // phases of the queries and of the weights
+      int tiles = 0;
+      bool two = false;                                // rows in half B
+      auto open_item = [&]() {
+        tiles = uniform(it.ntile);
+        two = __all_sync(0xffffffffu, it.rows > 128);
+      };
+      // scores of half X with the keys from piece c on
+      auto scores = [&](uint32_t X, int c) {
+        const uint32_t q = sb + L::Q + X * L::QB;
+        auto keys = [&](int i) { return sdesc(sb + L::K + ((c + i) % L::KST) * L::PIECE); };
+        if (D == 64) {
+          mma4_scores(tmem + col_s(X), sdesc(q), keys(0), idesc_bf16(128));
+        } else {
+          mma8_scores<0>(tmem + col_s(X), sdesc(q), keys(0), idesc_bf16(128));
+          if (L::WIDE) mma8_scores<1>(tmem + col_s(X), sdesc(q + 32768), keys(1), idesc_bf16(128));
+        }
+        mma_commit_warp(bar(bSFull + X));
+      };
+      auto keys_there = [&]() {                        // of the next tile's scores
+        for (int i = 0; i < L::KCH; ++i)
+          if (!ready(bKFull + (ck + i) % L::KST, (ck + i) / L::KST)) return false;
+        return true;
+      };
+      auto keys_done = [&]() {
+        for (int i = 0; i < L::KCH; ++i, ++ck) mma_commit_warp(bar(bKFree + ck % L::KST));
+      };
+      auto values = [&](uint32_t X, bool first) {
+        mma8_values(tmem + col_o(X), tmem + col_s(X), vdesc(sb + L::V + (cv % L::VST) * L::PIECE), idesc_bf16(L::DV) | (1u << 16), first ? 0u : 1u);
+      };
+      // the first tiles of an item: their keys and the queries
+      auto first_scores = [&]() {
+        if (!keys_there() || !ready(bQReady, nq0++)) return false;
+        tc_after();
+        scores(0, ck);
+        if (two) {
+          if (!ready(bQReady + 1, nq1++)) return false;
+          tc_after();
+          scores(1, ck);
+          keys_done();
+          return true;
+        }
+        keys_done();
+        if (tiles > 1) {
+          if (!keys_there() || (!L::WIDE && !ready(bQReady + 1, nq1++))) return false;
+          tc_after();
+          scores(1, ck);
+          keys_done();
+        }
+        return true;
+      };
+      bool ok = __all_sync(0xffffffffu, it.valid);
+      bool open = ok;
+      if (ok) {
+        open_item();
+        ok = first_scores();
+      }
+      while (ok && open) {
+        const int my_tiles = tiles;
+        const bool my_two = two;
+        for (int t = 0; t < my_tiles && !my_two; ++t, ++cv) {    // the halves' tiles in turn
+          const uint32_t X = t & 1;
+          ok = ready(bVOk + cv % L::VST, cv / L::VST) && ready(bPFull + X, X ? np1++ : np0++);
+          if (!ok) break;
+          tc_after();
+          values(X, t < 2);
+          mma_commit_warp(bar(bVFree + cv % L::VST));
+          if (t + 2 < my_tiles) {
+            ok = keys_there();
+            if (!ok) break;
+            scores(X, ck);
+            keys_done();
+          } else {
+            mma_commit_warp(bar(bODone + X));
+          }
+        }
+        for (int t = 0; t < my_tiles && my_two; ++t, ++cv) {
+          const bool last = t == my_tiles - 1;
+          ok = ready(bVOk + cv % L::VST, cv / L::VST) && ready(bPFull, np0++);
+          if (!ok) break;
+          tc_after();
+          values(0, t == 0);
+          if (last) {
+            mma_commit_warp(bar(bODone));
+          } else {
+            ok = keys_there();
+            if (!ok) break;
+            scores(0, ck);
+          }
+          ok = ready(bPFull + 1, np1++);
+          if (!ok) break;
+          tc_after();
+          values(1, t == 0);
+          mma_commit_warp(bar(bVFree + cv % L::VST));
+          if (last) {
+            mma_commit_warp(bar(bODone + 1));
+          } else {
+            scores(1, ck);
+            keys_done();
+          }
+        }
+        if (!ok) break;
+        it = next_item(++n);
+        open = __all_sync(0xffffffffu, it.valid);
+        if (failed) ok = false;
+        if (ok && open) {
+          open_item();
+          ok = first_scores();
+        }
+      }
+      mma_commit_warp(bar(bDrain));                    // every MMA issued completes before the CTA ends
+      bool f2 = false;
+      (void)bar_wait(bar(bDrain), 0, f2);
+      __syncwarp();
+    } else {
+      // ---- an item's queries on their way to L2 as soon as it is known; the values of tiles that some row does not see in
+      // full: what is not finite is taken out --------------------------------------------------------------------------
+      const int me = warp - 10;
+      int cv = 0;
+      for (int n = 0;; ++n) {
+        const ItemMsg it = next_item(n);
+        if (!it.valid) break;
+        constexpr int kLines = D / 64;                 // 128-byte lines of a row
+        for (int i = 32 * me + lane; i < it.rows * kLines; i += 64) {
+          const int gr = it.r0 + i / kLines, tok = gr / a.G;
+          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<long long>(it.q0) + tok) * a.qs +
+                                   static_cast<long long>(it.h / L::PER * a.G + (gr - tok * a.G)) * D;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64 * (i % kLines)));
+        }
+        const int ntile = it.ntile;
+        bool any = false;
+        for (int t = 0; t < ntile; ++t, ++cv) {
+          if (!wait(bVFull + cv % L::VST, cv / L::VST)) break;
+          if (!it.full(it.first_key(t), a.window, a.sinks)) {
+            const uint32_t at = sb + L::V + (cv % L::VST) * L::PIECE + me * (L::PIECE / 2) + lane * 16;
+            bool odd = false;
+#pragma unroll 1
+            for (int i = 0; i < L::PIECE / 2; i += 512 * 8) {
+              uint4 v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = lds128(at + i + 512 * k);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (odd_piece(v[k])) {
+                  odd = true;
+                  uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    if ((u[q] & 0x7F80u) == 0x7F80u) u[q] &= 0xFFFF0000u;
+                    if ((u[q] & 0x7F800000u) == 0x7F800000u) u[q] &= 0xFFFFu;
+                  }
+                  sts128(at + i + 512 * k, u[0], u[1], u[2], u[3]);
+                }
+            }
+            if (__any_sync(0xffffffffu, odd)) {
+              any = true;
+              fence_async_smem();
+            }
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(bar(bVOk + cv % L::VST));
+        }
+        if (failed) break;
+        if (lane == 0) {
+          if (any) odd_of[n % kCheckRing] = n + 1;
+          bar_arrive(bar(bChecked + n % kCheckRing));
+        }
+        __syncwarp();
+      }
+    }
+  }
+  if (failed && lane == 0) atomicOr(a.err, kErrTimeout);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {        // from the driver, looked up once
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+// Rows of keys or values: coordinates (channel, head, row), boxes of 64 channels of 128 rows.
+bool rows_map(CUtensorMap* map, const void* p, int d, int heads, long long rows, long long stride) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, 1, kTok};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_t(const PromptArgs& a, cudaStream_t s) {
+  using L = PG<D>;
+  CUtensorMap mk, mv;
+  if (!rows_map(&mk, a.k, D, a.H, a.total_k, a.ks) || !rows_map(&mv, a.v, D, a.H, a.total_k, a.vs)) return cudaErrorInvalidValue;
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = smem_attr_once(prompt_tc_kernel<D>, PS<D>::BYTES, configured);
+  if (e != cudaSuccess) return e;
+  const long long items = prompt_most_blocks(a, L::ROWS) * a.H * L::PER, tiles = a.max_k / kTok + 2 + a.sinks / kTok;
+  // items of few tiles are not cut (and need no join)
+  const bool split = tiles > 4 && prompt_splits(a, L::ROWS, kTok, kItemCost);
+  const int sms = prompt_sms();
+  const long long most = split ? (items * (tiles + kItemCost) + kMinSpan - 1) / kMinSpan : items;
+  const int ctas = static_cast<int>(most < sms ? (most < 1 ? 1 : most) : sms);
+  e = launch_pdl(prompt_tc_kernel<D>, dim3(ctas), dim3(kThreads), PS<D>::BYTES, s, a, mk, mv, split ? 1 : 0);
+  if (e != cudaSuccess || !split) return e;
+  return launch_prompt_join(a, D, false, ctas, L::ROWS, L::PER, s);
+}
+
+}  // namespace
+
+bool prompt_tc_takes(const PromptArgs& a, int d, bool f32) {
+  return !f32 && (d == 64 || d == 128 || d == 256) && a.scale_log2 != 0.0f && a.total_k > 0;
+}
+
+size_t prompt_tc_workspace(int d) {
+  const int rows = d == 256 ? 128 : 256, dv = d == 256 ? 128 : d;
+  return static_cast<size_t>(prompt_sms()) * (sizeof(PSplit) + 2 * sizeof(float) * rows * (dv + 4));
+}
+
+cudaError_t launch_prompt_tc(const PromptArgs& a, int d, cudaStream_t s) {
+  switch (d) {
+    case 64: return launch_t<64>(a, s);
+    case 128: return launch_t<128>(a, s);
+    case 256: return launch_t<256>(a, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace tq
