@@ -55,10 +55,10 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
   if (F32) prompt_zero_rows<float>(a, D);
   else prompt_zero_rows<__nv_bfloat16>(a, D);
   PromptSpan span{};
-  if (split) span = prompt_span<kRows, kTok, kItemCost, kThreads>(a, a.H, kMinSpan, reinterpret_cast<int*>(sm));
+  if (split) span = prompt_span<kTok, kItemCost, kThreads>(a, a.H, kMinSpan, reinterpret_cast<int*>(sm));
   PSplit* splits = reinterpret_cast<PSplit*>(a.part);
   float* parts = a.part + static_cast<size_t>(gridDim.x) * (sizeof(PSplit) / sizeof(float));
-  PromptWalk<kRows, kTok, kItemCost> w;
+  PromptWalk<kTok, kItemCost> w;
   w.start(a, span, a.H, split != 0);
   while (w.next(a, span)) {
     const PromptBlock& b = w.blk;
@@ -260,7 +260,7 @@ cudaError_t launch_t(const PromptArgs& a, bool f32, cudaStream_t s) {
   cudaError_t e = f32 ? smem_attr_once(prompt_simt_kernel<D, true>, SG<D>::BYTES, done32)
                       : smem_attr_once(prompt_simt_kernel<D, false>, SG<D>::BYTES, done16);
   if (e != cudaSuccess) return e;
-  const bool split = prompt_splits(a, kRows, kTok, kItemCost);
+  const bool split = prompt_splits(a, kTok, kItemCost);
   const int ctas = simt_ctas(D);
   e = f32 ? launch_pdl(prompt_simt_kernel<D, true>, dim3(ctas), dim3(kThreads), SG<D>::BYTES, s, a, split ? 1 : 0)
           : launch_pdl(prompt_simt_kernel<D, false>, dim3(ctas), dim3(kThreads), SG<D>::BYTES, s, a, split ? 1 : 0);
@@ -271,12 +271,12 @@ cudaError_t launch_t(const PromptArgs& a, bool f32, cudaStream_t s) {
 
 int prompt_sms() { return kv8_sm_count(); }
 
-long long prompt_most_blocks(const PromptArgs& a, int rows) {
-  const long long each = (static_cast<long long>(a.max_q) * a.G + rows - 1) / rows;
-  return std::min(a.S * each, a.S + static_cast<long long>(a.total_q) * a.G / rows);
+long long prompt_most_blocks(const PromptArgs& a) {
+  const long long each = (static_cast<long long>(a.max_q) * a.G + a.rows - 1) / a.rows;
+  return std::min(a.S * each, a.S + static_cast<long long>(a.total_q) * a.G / a.rows);
 }
-bool prompt_splits(const PromptArgs& a, int rows, int tok, int cost) {
-  const long long blocks = prompt_most_blocks(a, rows);
+bool prompt_splits(const PromptArgs& a, int tok, int cost) {
+  const long long blocks = prompt_most_blocks(a);
   return a.S <= kPromptList && blocks <= kPromptList && blocks * (a.max_k / tok + 2 + a.sinks / tok + cost) <= 0x7FFFFFFFLL;
 }
 
@@ -301,7 +301,9 @@ size_t prompt_simt_workspace(int d) {
   return static_cast<size_t>(simt_ctas(d)) * (sizeof(PSplit) + 2 * sizeof(float) * kRows * (d + 4));
 }
 
-cudaError_t launch_prompt_simt(const PromptArgs& a, int d, bool f32, cudaStream_t s) {
+cudaError_t launch_prompt_simt(const PromptArgs& args, int d, bool f32, cudaStream_t s) {
+  PromptArgs a = args;
+  a.rows = kRows;
   switch (d) {
     case 32: return launch_t<32>(a, f32, s);
     case 64: return launch_t<64>(a, f32, s);

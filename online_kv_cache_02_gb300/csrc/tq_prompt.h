@@ -14,6 +14,7 @@ struct PromptArgs {
   int S, total_q, total_k, Hq, H, G;
   const int32_t *cu_q, *cu_k;             // [S + 1]
   int max_q, max_k;
+  int rows;                               // query rows of a block
   int window, sinks;
   float scale_log2;
   float* part;                            // split items: PSplit per CTA, then [slot][rows][d + 4]
@@ -44,16 +45,15 @@ struct PromptBlock {
   template <int TOK>
   __device__ __forceinline__ int first_key(int tile) const { return tile < ns ? TOK * tile : w0 + TOK * (tile - ns); }
 };
-template <int ROWS>
 __device__ __forceinline__ int prompt_blocks(const PromptArgs& a, const PromptSeq& s) {
-  return static_cast<int>((static_cast<long long>(s.n) * a.G + ROWS - 1) / ROWS);
+  return static_cast<int>((static_cast<long long>(s.n) * a.G + a.rows - 1) / a.rows);
 }
-template <int ROWS, int TOK>
+template <int TOK>
 __device__ __forceinline__ PromptBlock prompt_block(const PromptArgs& a, const PromptSeq& s, int qb) {
   PromptBlock b;
   b.seq = s;
-  b.r0 = qb * ROWS;                       // the host keeps total_q Hq below 2^31
-  b.rows = min(s.n * a.G - b.r0, ROWS);
+  b.r0 = qb * a.rows;                     // the host keeps total_q Hq below 2^31
+  b.rows = min(s.n * a.G - b.r0, a.rows);
   b.pmin = s.m - s.n + b.r0 / a.G;
   b.pmax = s.m - s.n + (b.r0 + b.rows - 1) / a.G;
   b.ns = b.w0 = 0;
@@ -93,7 +93,7 @@ struct PromptSpan {
   long long at;                           // units before it
 };
 // By all THREADS of a block; `room`: kPromptList * 2 + 64 ints of shared memory.
-template <int ROWS, int TOK, int COST, int THREADS>
+template <int TOK, int COST, int THREADS>
 __device__ PromptSpan prompt_span(const PromptArgs& a, int heads, int min_span, int* room) {
   constexpr int WARPS = THREADS / 32;
   int *firsts = room, *units = room + kPromptList, *sums = units + kPromptList;
@@ -121,7 +121,7 @@ __device__ PromptSpan prompt_span(const PromptArgs& a, int heads, int min_span, 
   int sum = 0, blocks = 0;
   for (int i = 0; i < per && tid * per + i < a.S; ++i) {
     firsts[tid * per + i] = sum;
-    sum += prompt_blocks<ROWS>(a, prompt_seq(a, tid * per + i));
+    sum += prompt_blocks(a, prompt_seq(a, tid * per + i));
   }
   int before = scan(sum, blocks);
   for (int i = 0; i < per && tid * per + i < a.S; ++i) firsts[tid * per + i] += before;
@@ -142,7 +142,7 @@ __device__ PromptSpan prompt_span(const PromptArgs& a, int heads, int min_span, 
   for (int i = 0; i < perb && tid * perb + i < blocks; ++i) {
     const int e = tid * perb + i, s = seq_of(e);
     units[e] = sum;
-    const int t = prompt_block<ROWS, TOK>(a, prompt_seq(a, s), e - firsts[s]).tiles();
+    const int t = prompt_block<TOK>(a, prompt_seq(a, s), e - firsts[s]).tiles();
     sum += t ? t + COST : 0;
   }
   before = scan(sum, total);
@@ -172,7 +172,7 @@ __device__ PromptSpan prompt_span(const PromptArgs& a, int heads, int min_span, 
 }
 
 // The items of a CTA in order: parts of the listed ones by its span, or whole items in turn.
-template <int ROWS, int TOK, int COST>
+template <int TOK, int COST>
 struct PromptWalk {
   PromptBlock blk;
   int h, t0, t1, slot;                    // KV head (or item of one); its tiles [t0, t1); workspace slot, -1 for whole items
@@ -203,8 +203,8 @@ struct PromptWalk {
   }
   __device__ __forceinline__ void load(const PromptArgs& a) {
     const PromptSeq q = prompt_seq(a, s);
-    nblk = prompt_blocks<ROWS>(a, q);
-    blk = prompt_block<ROWS, TOK>(a, q, qb);
+    nblk = prompt_blocks(a, q);
+    blk = prompt_block<TOK>(a, q, qb);
     tiles = blk.tiles();
   }
   // The next item with tiles of this CTA; false at the end.
@@ -218,12 +218,12 @@ struct PromptWalk {
             nblk = 0;
             return false;
           }
-          nblk = prompt_blocks<ROWS>(a, prompt_seq(a, s));
+          nblk = prompt_blocks(a, prompt_seq(a, s));
         }
         const int i = static_cast<int>(whole - at);
         qb = nblk - 1 - i / heads;        // a sequence's longest rows first
         h = i % heads;
-        blk = prompt_block<ROWS, TOK>(a, prompt_seq(a, s), qb);
+        blk = prompt_block<TOK>(a, prompt_seq(a, s), qb);
         tiles = blk.tiles();
         if (tiles) break;
       }
@@ -254,7 +254,7 @@ struct PromptWalk {
     do {                                  // (there is one more: units are left)
       if (++qb >= nblk) {
         qb = 0;
-        do nblk = prompt_blocks<ROWS>(a, prompt_seq(a, ++s));
+        do nblk = prompt_blocks(a, prompt_seq(a, ++s));
         while (!nblk);
       }
       load(a);
@@ -273,9 +273,9 @@ __device__ __forceinline__ void prompt_zero_rows(const PromptArgs& a, int d) {
   }
 }
 
-// Blocks of `rows` query rows that a call can have at most, and whether they can be listed.
-long long prompt_most_blocks(const PromptArgs& a, int rows);
-bool prompt_splits(const PromptArgs& a, int rows, int tok, int cost);
+// Blocks that a call can have at most, and whether they can be listed.
+long long prompt_most_blocks(const PromptArgs& a);
+bool prompt_splits(const PromptArgs& a, int tok, int cost);
 // Workspace of either form (whatever the dtype and scale), its CTAs and its launch.
 size_t prompt_simt_workspace(int d);
 cudaError_t launch_prompt_simt(const PromptArgs& a, int d, bool f32, cudaStream_t s);
@@ -283,7 +283,7 @@ int prompt_sms();                         // of the current device
 bool prompt_tc_takes(const PromptArgs& a, int d, bool f32);
 size_t prompt_tc_workspace(int d);
 cudaError_t launch_prompt_tc(const PromptArgs& a, int d, cudaStream_t s);
-// Joins the parts of split items (PART floats a row: maximum, sum, its exponent, 0, then a run of channels).
+// Joins the parts of split items (`rows` of them a slot, PART floats a row: maximum, sum, its exponent, 0, then a run of channels).
 cudaError_t launch_prompt_join(const PromptArgs& a, int d, bool f32, int ctas, int rows, int per, cudaStream_t s);
 
 }  // namespace tq

@@ -1,26 +1,27 @@
 // Attention over packed prompts on the tensor cores (tcgen05), bf16, d = 64, 128 or 256.
 //
-// An item is (sequence, KV head, block of 256 query rows r = t G + g); keys go by in tiles of 128.  All items' tiles
-// form one list that is cut into equal spans, one per CTA; the parts of an item that crosses spans are joined by a second
-// kernel.  Per tile, with x = scale log2(e) <q, k>:
+// An item is (sequence, KV head, block of query rows r = t G + g): whole tokens, two halves A and B of at most 128 rows
+// (TMA brings a half's rows as one box of tokens and heads); keys go by in tiles of 128.  All items' tiles form one list
+// that is cut into equal spans, one per CTA; the parts of an item that crosses spans are joined by a second kernel.  Per
+// tile, with x = scale log2(e) <q, k>:
 //   S = Q K^T              bf16, from tiles that TMA puts in place
 //   w = 2^(x - M)          M the maximum of the row's first tile; bf16 has fp32's range, so that M moves only where a
 //                          tile's weights sum to more than 2^40, and no tile but the first looks for a maximum
 //   O += w V, l += sum w   w as bf16 (off by 2^-8 at most) in tensor memory, V's token rows read MN-major;
 //   out = O / l.
-// Two 128-row halves A and B of the block take turns: while the softmax of one runs, the tensor cores work on the other.
-// Tensor memory: S of A and B (each overlaid by its weights), O of A and B, 512 columns.  An item of at most 128 rows has
-// its rows in both halves: A takes the even tiles, B the odd ones, and A adds B's sums to its own at the item's end.  At
-// d = 256 an item is 128 rows and one half of the values' channels (the scores are the same work twice: queries, keys and
-// values of 256 rows and channels do not fit), in the same turns.
+// The halves take turns: while the softmax of one runs, the tensor cores work on the other.  An item follows the one
+// before like a tile does: its queries are there ahead of time (a ring of halves), and its results are left to warps of
+// their own.  Tensor memory: S of A and B (each overlaid by its weights), O of A and B, 512 columns.  An item that fits one
+// half is in both: A takes the even tiles, B the odd ones, and their sums are added at the end.  At d = 256 an item is one
+// half of rows and one half of the values' channels (the scores are the same work twice: queries, keys and values of 256
+// rows and channels do not fit), in the same turns.
 //
 // A key that a row does not see has weight zero, but zero times an infinity is NaN: the values of tiles that some row does
 // not see in full are looked through before they are multiplied, what is not finite there is taken out, and added to the
 // rows that see it at the end.
 //
-// Warps 0-3 and 4-7: the softmax of A and B (thread = row), the queries, the results; 8: items, the copies of keys and
-// values; 9: MMA issue; 10 and 11: queries to L2, the values of edge tiles.  Every wait is bounded; a wait that gives up
-// sets the device error word.
+// Warps 0-3 and 4-7: the softmax of A and B (thread = row); 8-11: the results; 12: items, the copies; 13: MMA issue; 14
+// and 15: the values of edge tiles.  Every wait is bounded; a wait that gives up sets the device error word.
 
 #include "tq_prompt.h"
 #include "tq_tc.cuh"
@@ -39,48 +40,49 @@ namespace {
 using namespace tcx;
 
 constexpr int kTok = 128;                 // keys per tile
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kItems = 4;                 // items announced ahead
 constexpr int kItemCost = 5;              // an item's start and end, in tiles' time
 constexpr int kMinSpan = 2 + kItemCost;   // a CTA's share of the list at least
 constexpr float kMNone = -3.0e38f;        // a maximum before any score: finite, and below the scores of fp32
 constexpr float kFull = 1.0995116e12f;    // 2^40: a tile's sum beyond it moves the maximum
+constexpr float kAbove = 40.0f;           // or a score so far above it
 // x - M in one rounding is off by half a step of M against the other tiles' M: beyond 2^16 scores are rounded first, so that
 // small differences of large ones are exact.
 constexpr float kBig = 65536.0f;
 constexpr int kCheckRing = 8;
 
-// Registers: 12 warps start with 168 a thread, and the eight of the softmax take what the others give back.
-constexpr int kRegsMore = 216, kRegsLess = 72;
-static_assert(8 * kRegsMore + 4 * kRegsLess <= 12 * 168, "more registers than the block starts with");
+// Registers: 16 warps start with 128 a thread, and the eight of the softmax take what the others give back.
+constexpr int kRegsSoftmax = 184, kRegsResults = 80, kRegsOthers = 64;
+static_assert(8 * kRegsSoftmax + 4 * kRegsResults + 4 * kRegsOthers <= 16 * 128, "more registers than the block starts with");
 
 template <int D>
 struct PG {
   static constexpr bool WIDE = D == 256;
-  static constexpr int ROWS = WIDE ? 128 : 256;        // query rows per item
+  static constexpr int HALVES = WIDE ? 1 : 2;          // of query rows per item
+  static constexpr int ROWS = 128 * HALVES;
   static constexpr int DV = WIDE ? 128 : D;            // value channels per item
   static constexpr int PER = D / DV;                   // items per KV head and block of rows
   static constexpr int KCH = D > 128 ? D / 128 : 1;    // pieces of a tile's keys, 128 channels each
   static constexpr int PIECE = kTok * 2 * (D < 128 ? D : 128);      // bytes of one, and of a tile's values
-  static constexpr int KST = D == 64 ? 5 : D == 128 ? 2 : 3, VST = D == 64 ? 5 : D == 128 ? 3 : 2;
-  static constexpr int QX = 128 * 2 * D;               // 128 rows' queries
-  static constexpr int QB = WIDE ? 0 : QX;             // from half A's queries to half B's
+  static constexpr int QX = 128 * 2 * D;               // a half's queries
+  static constexpr int QST = D == 64 ? 4 : D == 128 ? 3 : 1, KST = D == 64 ? 5 : D == 128 ? 2 : 3, VST = D == 64 ? 5 : 2;
   static constexpr int PART = DV + 4;                  // floats of a row's partial
-  static constexpr int Q = 0;                          // [A, B][64-channel panels][128 rows][128 B]
-  static constexpr int K = Q + QX + QB;                // [stage][64-channel panels][128 tokens][128 B]
+  static constexpr int Q = 0;                          // [stage][64-channel panels][128 rows][128 B]
+  static constexpr int K = Q + QST * QX;               // [stage][64-channel panels][128 tokens][128 B]
   static constexpr int V = K + KST * PIECE;
   static constexpr int ITEM = V + VST * PIECE;
   static constexpr int BAR = ITEM + kItems * 64;
 };
 enum Bar {
-  bKFull = 0, bKFree = bKFull + 5, bVFull = bKFree + 5, bVFree = bVFull + 5, bVOk = bVFree + 5, bSFull = bVOk + 5, bPFull = bSFull + 2,
-  bODone = bPFull + 2, bQReady = bODone + 2, bItem = bQReady + 2, bItemFree = bItem + kItems, bChecked = bItemFree + kItems,
-  bJoin = bChecked + kCheckRing, bOFree, bQFree, bDrain, bCount
+  bQFull = 0, bQFree = bQFull + 4, bKFull = bQFree + 4, bKFree = bKFull + 5, bVFull = bKFree + 5, bVFree = bVFull + 5, bVOk = bVFree + 5,
+  bSFull = bVOk + 5, bPFull = bSFull + 2, bSums = bPFull + 2, bODone = bSums + 2, bOFree = bODone + 2, bItem = bOFree + 2,
+  bItemFree = bItem + kItems, bChecked = bItemFree + kItems, bDrain = bChecked + kCheckRing, bCount
 };
 template <int D>
 struct PS {                                            // behind the barriers
-  static constexpr int JOIN = PG<D>::BAR + 8 * ((bCount + 1) & ~1);      // half B's (M, l) of 128 rows
-  static constexpr int ODD = JOIN + 1024;              // per announced item: values that are not finite in edge tiles
+  static constexpr int SUMS = PG<D>::BAR + 8 * ((bCount + 1) & ~1);      // (M, l) of the halves' rows
+  static constexpr int ODD = SUMS + 2 * 128 * 8;   // per item: values that are not finite in edge tiles
   static constexpr int TMEM = ODD + 4 * kCheckRing;
   static constexpr int BYTES = TMEM + 16;
 };
@@ -250,16 +252,18 @@ __device__ __noinline__ void add_odd_values(uint32_t to, const __nv_bfloat16* v,
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                     int split) {
+    prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, int split) {
   using L = PG<D>;
   using P = PS<D>;
   extern __shared__ __align__(1024) unsigned char sm_raw[];
   unsigned char* sm = sm_raw;
   const uint32_t sb = su32(sm);
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  const int half = a.rows / L::HALVES;                 // rows of a half: whole tokens
   auto bar = [&](int i) { return sb + L::BAR + 8u * static_cast<uint32_t>(i); };
   ItemMsg* item_ring = reinterpret_cast<ItemMsg*>(sm + L::ITEM);
+  float2* sums = reinterpret_cast<float2*>(sm + P::SUMS);
   volatile int* odd_of = reinterpret_cast<volatile int*>(sm + P::ODD);
   PSplit* splits = reinterpret_cast<PSplit*>(a.part);              // one per CTA, then the partials' slots
   if (sb & 1023u) {                                    // the swizzles' period: the kernel's only shared memory starts on one
@@ -271,6 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   if (tid == 0) {
+    for (int i = 0; i < L::QST; ++i) {
+      bar_init(bar(bQFull + i), 1);
+      bar_init(bar(bQFree + i), 1);
+    }
     for (int i = 0; i < L::KST; ++i) {
       bar_init(bar(bKFull + i), 1);
       bar_init(bar(bKFree + i), 1);
@@ -283,24 +291,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       bar_init(bar(bSFull + i), 1);
       bar_init(bar(bPFull + i), 4);
+      bar_init(bar(bSums + i), 4);
       bar_init(bar(bODone + i), 1);
-      bar_init(bar(bQReady + i), 4);
+      bar_init(bar(bOFree + i), 4);
     }
     for (int i = 0; i < kItems; ++i) {
       bar_init(bar(bItem + i), 1);
-      bar_init(bar(bItemFree + i), 11);                // every warp but the one that announces
+      bar_init(bar(bItemFree + i), 15);                // every warp but the one that announces
     }
     for (int i = 0; i < kCheckRing; ++i) {
       bar_init(bar(bChecked + i), 2);
       odd_of[i] = 0;
     }
-    bar_init(bar(bJoin), 4);
-    bar_init(bar(bOFree), 4);
-    bar_init(bar(bQFree), 4);
     bar_init(bar(bDrain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 9) {
+  if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + P::TMEM), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (split) pdl_trigger();                            // the join's launch
   prompt_zero_rows<__nv_bfloat16>(a, D);
   PromptSpan span{};
-  if (split) span = prompt_span<L::ROWS, kTok, kItemCost, kThreads>(a, a.H * L::PER, kMinSpan, reinterpret_cast<int*>(sm));
+  if (split) span = prompt_span<kTok, kItemCost, kThreads>(a, a.H * L::PER, kMinSpan, reinterpret_cast<int*>(sm));
   fence_async_smem();
   tc_before();
   __syncthreads();
@@ -332,129 +338,122 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 8) {
-    // ---- softmax of half X (thread = row), the queries, the results -----------------------
+    // ---- softmax of half X (thread = row) --------------------------------------------------
     // Accesses to tensor memory are the whole warp's: behind a branch that only some lanes take they meet again first.
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMore));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int X = warp >> 2, wq = warp & 3, r = 32 * wq + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * wq) << 16);
     const uint32_t ts = trow + col_s(X), to = trow + col_o(X);
-    const float f = fabsf(a.scale_log2);
-    const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // whole sectors per store
-    int nS = 0, nO = 0, nJ = 0, nF = 0;                // phases of S, of the final O, of the halves' join, of the queries' release
-    float2* join = reinterpret_cast<float2*>(sm + P::JOIN);
-    struct Row {
-      bool live;
-      int p;                                           // position; -1: an absent row sees nothing
-      long long at;                                    // its first element of out
-    };
-    auto mine = [&](const ItemMsg& x) { return x.valid && (X == 0 || x.rows > 128 || x.ntile > 1); };
-    // The row of an item that is this thread's; the warp's 32 rows of queries to shared memory, D / 8 lanes per row (a lane
-    // per row would ask for 32 lines with each load).  The item before has no score MMA left: its last scores were read.
-    auto queries = [&](const ItemMsg& x) {
-      Row w;
-      const int rx = x.rows > 128 ? 128 * X + r : r, gr = x.r0 + rx, tok = gr / a.G, g = gr - tok * a.G, hq = x.h / L::PER * a.G + g;
-      w.live = rx < x.rows;
-      w.p = w.live ? x.p0 + tok : -1;
-      w.at = ((static_cast<long long>(x.q0) + tok) * a.Hq + hq) * D;
-      if (L::WIDE && X) return w;                      // half A does the work for both
-      const uint32_t qx = sb + L::Q + X * L::QB;
-      constexpr int kP = D / 8, kR = 32 / kP;          // 16-byte pieces per row, rows per load
-      constexpr int kB = kP < 16 ? kP : 16;            // loads in flight
-      const long long where = w.live ? (static_cast<long long>(x.q0) + tok) * a.qs + static_cast<long long>(hq) * D : -1;
-      const int piece = lane % kP;
-#pragma unroll 1
-      for (int i0 = 0; i0 < kP; i0 += kB) {
-        uint4 v4[kB];
-#pragma unroll
-        for (int i = 0; i < kB; ++i) {
-          const long long at = __shfl_sync(0xffffffffu, where, kR * (i0 + i) + lane / kP);
-          v4[i] = at >= 0 ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at)[piece] : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < kB; ++i) {
-          const int row = 32 * wq + kR * (i0 + i) + lane / kP;
-          sts128(qx + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4), v4[i].x ^ flip, v4[i].y ^ flip, v4[i].z ^ flip,
-                 v4[i].w ^ flip);
-        }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) bar_arrive(bar(bQReady + X));
-      return w;
-    };
-    ItemMsg it = next_item(0);
-    Row row{};
-    if (mine(it)) row = queries(it);
-    for (int n = 0; it.valid; ++n) {
+    const float f = a.scale_log2;
+    int nS = 0, items = 0;                             // phases of S, items of this half
+    for (int n = 0;; ++n) {
+      const ItemMsg it = next_item(n);
+      if (!it.valid) break;
+      const bool turns = it.rows <= half;              // the halves take the tiles in turn
       const int ntile = it.ntile;
-      if (!mine(it)) {                                 // one tile of at most 128 rows: nothing for B
-        it = next_item(n + 1);
-        if (mine(it)) row = queries(it);
-        continue;
-      }
-      const int p = row.p;
-      const bool turns = it.rows <= 128;               // the halves take the tiles in turn
+      const int rx = turns ? r : half * X + r;
+      const bool live = r < half && rx < it.rows;      // what the other lanes hold is no row, and nobody looks at it
+      const int p = it.p0 + (it.r0 + rx) / a.G;
       const int first = turns ? X : 0, step = turns ? 2 : 1;
       float m = kMNone, l = 0.0f;
       bool bigs = false;                               // a row of the warp has had a maximum beyond kBig
       for (int t = first; t < ntile; t += step) {
         if (!wait(bSFull + X, nS++)) break;
         tc_after();
-        if (L::WIDE && X && t + step >= ntile) {       // both halves' queries have been used
-          if (lane == 0) bar_arrive(bar(bQFree));
-          __syncwarp();
-        }
         const int j0 = it.first_key(t);
+        const bool full = it.full(j0, a.window, a.sinks);
         bool done = false;
-        if (!bigs) {
+        const uint64_t f2 = pack2(f, f);
+        if (!bigs && full && t > first) {              // the tile as it mostly is
           float x[kTok];
+          uint32_t w[kTok / 2];
           tld32x4(ts, x);
-          if (!it.full(j0, a.window, a.sinks)) {
+          const uint64_t b2 = pack2(-m, -m);
+          uint64_t s2 = 0ull, s3 = 0ull;
 #pragma unroll
-            for (int c = 0; c < kTok; c += 32) {
-              const uint32_t see = seen32(p, j0 + c, a.window, a.sinks);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) x[c + k] = (see >> k) & 1u ? x[c + k] : -INFINITY;
-            }
+          for (int c = 0; c < kTok; c += 4) {
+            float y0, y1, y2, y3;
+            unpack2(fma2(pack2(x[c], x[c + 1]), f2, b2), y0, y1);
+            unpack2(fma2(pack2(x[c + 2], x[c + 3]), f2, b2), y2, y3);
+            y0 = ex2(y0);
+            y1 = ex2(y1);
+            y2 = ex2(y2);
+            y3 = ex2(y3);
+            s2 = add2(s2, pack2(y0, y1));
+            s3 = add2(s3, pack2(y2, y3));
+            w[c / 2] = bf16x2_bits(y0, y1);
+            w[c / 2 + 1] = bf16x2_bits(y2, y3);
           }
-          if (t == first) {
+          float s0, s1;
+          unpack2(add2(s2, s3), s0, s1);
+          s0 += s1;
+          if (!__any_sync(0xffffffffu, live && s0 > kFull)) {
+            l += s0;
+            tst32(ts, *reinterpret_cast<uint32_t(*)[32]>(w));
+            tst32(ts + 32u, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
+            done = true;
+          }
+        } else if (!bigs) {
+          // An edge, or an item's first tile: the maximum, then the weights, 32 keys at a time and only those that some row
+          // sees; rolled, since code that runs once or twice an item is out of the instruction cache (unrolled as above:
+          // 2,200 cycles more a tile).
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kTok; c += 32) {
+            const uint32_t see = full ? 0xFFFFFFFFu : seen32(p, j0 + c, a.window, a.sinks);
+            if (!__any_sync(0xffffffffu, see != 0u)) continue;
+            float x[32];
+            tld32(ts + c, x);
+            if (__any_sync(0xffffffffu, see != 0xFFFFFFFFu)) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[k] = (see >> k) & 1u ? x[k] : -INFINITY;
+            }
             float m0 = x[0], m1 = x[1];
 #pragma unroll
-            for (int c = 2; c < kTok; c += 2) {
-              m0 = fmaxf(m0, x[c]);
-              m1 = fmaxf(m1, x[c + 1]);
+            for (int k = 2; k < 32; k += 2) {
+              m0 = fmaxf(m0, x[k]);
+              m1 = fmaxf(m1, x[k + 1]);
             }
-            m = fmaxf(fmaxf(m0, m1) * f, kMNone);
+            top = fmaxf(top, fmaxf(m0, m1));
+            __syncwarp();
           }
-          bigs = __any_sync(0xffffffffu, fabsf(m) > kBig && m > kMNone);
-          if (!bigs) {
-            uint32_t w[kTok / 2];
-            const uint64_t f2 = pack2(f, f), b2 = pack2(-m, -m);
-            uint64_t s2 = 0ull, s3 = 0ull;
+          top *= f;
+          if (t == first) m = fmaxf(top, kMNone);
+          bigs = __any_sync(0xffffffffu, live && fabsf(m) > kBig && m > kMNone);
+          if (!bigs && !__any_sync(0xffffffffu, live && top > m + kAbove)) {
+            const uint64_t b2 = pack2(-m, -m);
+            uint64_t s2 = 0ull;
+#pragma unroll 1
+            for (int c = 0; c < kTok; c += 32) {
+              const uint32_t see = full ? 0xFFFFFFFFu : seen32(p, j0 + c, a.window, a.sinks);
+              uint32_t w[16];
+              if (__any_sync(0xffffffffu, see != 0u)) {
+                float x[32];
+                tld32(ts + c, x);
+                if (__any_sync(0xffffffffu, see != 0xFFFFFFFFu)) {
 #pragma unroll
-            for (int c = 0; c < kTok; c += 4) {
-              float y0, y1, y2, y3;
-              unpack2(fma2(pack2(x[c], x[c + 1]), f2, b2), y0, y1);
-              unpack2(fma2(pack2(x[c + 2], x[c + 3]), f2, b2), y2, y3);
-              y0 = ex2(y0);
-              y1 = ex2(y1);
-              y2 = ex2(y2);
-              y3 = ex2(y3);
-              s2 = add2(s2, pack2(y0, y1));
-              s3 = add2(s3, pack2(y2, y3));
-              w[c / 2] = bf16x2_bits(y0, y1);
-              w[c / 2 + 1] = bf16x2_bits(y2, y3);
+                  for (int k = 0; k < 32; ++k) x[k] = (see >> k) & 1u ? x[k] : -INFINITY;
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  float y0, y1;
+                  unpack2(fma2(pack2(x[2 * k], x[2 * k + 1]), f2, b2), y0, y1);
+                  y0 = ex2(y0);
+                  y1 = ex2(y1);
+                  s2 = add2(s2, pack2(y0, y1));
+                  w[k] = bf16x2_bits(y0, y1);
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) w[k] = 0u;
+              }
+              __syncwarp();
+              tst16(ts + c / 2, w);                    // (over scores that were read)
             }
             float s0, s1;
-            unpack2(add2(s2, s3), s0, s1);
-            s0 += s1;
-            if (!__any_sync(0xffffffffu, s0 > kFull)) {
-              l += s0;
-              tst32(ts, *reinterpret_cast<uint32_t(*)[32]>(w));
-              tst32(ts + 32u, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
-              done = true;
-            }
+            unpack2(s2, s0, s1);
+            l += s0 + s1;
+            done = true;
           }
         }
         if (!done) {
@@ -468,88 +467,117 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) bar_arrive(bar(bPFull + X));
       }
       if (failed) break;
-      // the next item's queries first: its scores then run beside what is left of this one
-      const ItemMsg was = it;
-      const Row done_row = row;
-      it = next_item(n + 1);
-      if (L::WIDE && X == 0 && ntile > 1 && !wait(bQFree, nF++)) break;     // half B has its last scores too
-      if (mine(it)) row = queries(it);
-      // ---- the row's result (or partial) ----
-      if (!wait(bODone + X, nO)) break;
-      ++nO;
-      tc_after();
-      if (turns && ntile > 1) {
-        if (X) {
-          join[r] = make_float2(m, l);
-          tc_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(bar(bJoin));
-          if (!wait(bOFree, nJ++)) break;              // A has read this half's sums: the next item may overwrite them
-          tc_after();
-          continue;
+      if (first >= ntile) continue;                    // one tile in one half: nothing for B
+      if (items > 0 && !wait(bOFree + X, items - 1)) break;      // the sums before were taken
+      ++items;
+      sums[128 * X + r] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(bSums + X));
+    }
+  } else if (warp < 12) {
+    // ---- results (or partials) of both halves, thread = row ---------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsResults));
+    const int wq = warp & 3, r = 32 * wq + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * wq) << 16);
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // whole sectors per store
+    int nO0 = 0, nO1 = 0;                              // items of the halves
+    for (int n = 0; !failed; ++n) {
+      const ItemMsg it = next_item(n);
+      if (!it.valid) break;
+      const bool turns = it.rows <= half, joins = turns && it.ntile > 1;
+      const int ch0 = it.h % L::PER * L::DV, hkv = it.h / L::PER;
+#pragma unroll 1
+      for (int X = 0; X < (turns ? 1 : 2); ++X) {
+        const int rx = half * X + r, gr = it.r0 + rx, tok = gr / a.G, p = it.p0 + tok;
+        const bool live = r < half && rx < it.rows;
+        const uint32_t to = trow + col_o(X);
+        if (!wait(bSums + X, X ? nO1 : nO0) || !wait(bODone + X, X ? nO1 : nO0)) break;
+        if (X) ++nO1;
+        else ++nO0;
+        if (joins) {
+          if (!wait(bSums + 1, nO1) || !wait(bODone + 1, nO1)) break;
+          ++nO1;
         }
-        if (!wait(bJoin, nJ++)) break;
         tc_after();
-        const float2 other = join[r];
-        const float ref = fmaxf(m, other.x);
-        const float fa = ex2(m - ref), fb = ex2(other.x - ref);
-        m = ref;
-        l = fa * l + fb * other.y;
+        const float2 mine = sums[128 * X + r];
+        float m = mine.x, l = mine.y, fa = 1.0f, fb = 0.0f;
+        if (joins) {
+          const float2 other = sums[128 + r];
+          m = fmaxf(mine.x, other.x);
+          fa = ex2(mine.x - m);
+          fb = ex2(other.x - m);
+          l = fa * l + fb * other.y;
+        }
+        if (X == 0 && !wait(bChecked + n % kCheckRing, n / kCheckRing)) break;
+        const bool odd = __any_sync(0xffffffffu, odd_of[n % kCheckRing] == n + 1);
+        if (__builtin_expect(odd, 0)) {
+          if (joins) {                                 // (the sums first)
+#pragma unroll 1
+            for (int c = 0; c < L::DV / 16; ++c) {
+              float o[16], o2[16];
+              uint32_t u[16];
+              tld16(to + 16u * c, o);
+              tld16(trow + col_o(1) + 16u * c, o2);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(fa * o[k] + fb * o2[k]);
+              tst16(to + 16u * c, u);
+            }
+            tst_wait();
+            fa = 1.0f;
+          }
+          add_odd_values<L::DV>(to, static_cast<const __nv_bfloat16*>(a.v) + it.k0 * a.vs + static_cast<long long>(hkv) * D + ch0, a.vs, it.t0,
+                                it.ntile, it.ns, it.w0, it.pmin, it.pmax, p, a.window, a.sinks);
+        }
+        const bool both = joins && !odd;
+        const float inv = it.slot < 0 ? prompt_inverse(l, p) : 1.0f;
+        fa *= inv;
+        fb *= inv;
+        const long long at = ((static_cast<long long>(it.q0) + tok) * a.Hq + hkv * a.G + (gr - tok * a.G)) * D + ch0;
+        float* part = parts + (static_cast<long long>(it.slot) * L::ROWS + rx) * L::PART;
 #pragma unroll 1
         for (int c = 0; c < L::DV / 16; ++c) {
-          float o[16], o2[16];
-          uint32_t u[16];
+          float o[16];
           tld16(to + 16u * c, o);
-          tld16(trow + col_o(1) + 16u * c, o2);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(fa * o[k] + fb * o2[k]);
-          tst16(to + 16u * c, u);
-        }
-        tst_wait();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(bar(bOFree));
-        __syncwarp();
-      }
-      if (!wait(bChecked + n % kCheckRing, n / kCheckRing)) break;
-      const bool odd = __any_sync(0xffffffffu, odd_of[n % kCheckRing] == n + 1);
-      const float inv = prompt_inverse(l, done_row.p);
-      float* part = parts + (static_cast<long long>(was.slot) * L::ROWS + (turns ? 0 : 128 * X) + r) * L::PART;
-      const int ch0 = was.h % L::PER * L::DV;
-      if (__builtin_expect(odd, 0))
-        add_odd_values<L::DV>(to, static_cast<const __nv_bfloat16*>(a.v) + was.k0 * a.vs + static_cast<long long>(was.h / L::PER) * D + ch0, a.vs,
-                              was.t0, ntile, was.ns, was.w0, was.pmin, was.pmax, done_row.p, a.window, a.sinks);
-#pragma unroll 1
-      for (int c = 0; c < L::DV / 32; ++c) {
-        float o[32];
-        tld32(to + 32u * c, o);
-        if (done_row.live && was.slot < 0) {
-          uint32_t w[16];
+          for (int k = 0; k < 16; ++k) o[k] *= fa;
+          if (both) {
+            float o2[16];
+            tld16(trow + col_o(1) + 16u * c, o2);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) w[k] = bf16x2_bits(o[2 * k] * inv, o[2 * k + 1] * inv);
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + done_row.at + ch0 + 32 * c;
-          if (wide) {
-            stg256(dst, w);
-            stg256(dst + 16, w + 8);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(dst)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            for (int k = 0; k < 16; ++k) o[k] = fmaf(fb, o2[k], o[k]);
           }
-        } else if (done_row.live) {
-          float4* dst = reinterpret_cast<float4*>(part + 4 + 32 * c);
+          if (live && it.slot < 0) {
+            uint32_t w[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          if (c == 0) *reinterpret_cast<float4*>(part) = make_float4(m, l, 0.0f, 0.0f);
+            for (int k = 0; k < 8; ++k) w[k] = bf16x2_bits(o[2 * k], o[2 * k + 1]);
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at + 16 * c;
+            if (wide) {
+              stg256(dst, w);
+            } else {
+              reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          } else if (live) {
+            float4* dst = reinterpret_cast<float4*>(part + 4 + 16 * c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            if (c == 0) *reinterpret_cast<float4*>(part) = make_float4(m, l, 0.0f, 0.0f);
+          }
+          __syncwarp();                                // lanes with no row wait: the loads are the whole warp's
         }
-        __syncwarp();                                  // lanes with no row wait: the loads are the whole warp's
+        tc_before();                                   // the next item's products may overwrite what was read
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(bar(bOFree + X));
+          if (joins) bar_arrive(bar(bOFree + 1));
+        }
       }
-      tc_before();                                     // O is read before the next item's first P is announced
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLess));
-    if (warp == 8) {
-      // ---- items, keys, values ----------------------------------------------------------------
-      int n = 0, ck = 0, cv = 0;                       // items, and pieces of keys and tiles of values asked for
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOthers));
+    if (warp == 12) {
+      // ---- items, queries, keys, values -------------------------------------------------------
+      int n = 0, cq = 0, ck = 0, cv = 0;               // items, and halves of queries, pieces of keys and tiles of values asked for
       auto publish = [&](const ItemMsg& x) {
         // Every warp has taken the one before.  If one has not within the limit, its room stays as it is, and the others'
         // waits for this one give up too.
@@ -571,61 +599,88 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      PromptWalk<L::ROWS, kTok, kItemCost> w;
-      w.start(a, span, a.H * L::PER, split != 0);
-      while (!failed && w.next(a, span)) {
+      PromptWalk<kTok, kItemCost> w;
+      auto announce = [&]() {
         const PromptBlock& b = w.blk;
         publish(ItemMsg{1, w.h, b.seq.q0, b.r0, b.rows, b.seq.m - b.seq.n, b.pmin, b.pmax, w.t1 - w.t0, w.t0, w.slot, b.seq.k0, b.ns, b.w0, {0, 0}});
-        const int head = w.h / L::PER, ahead = b.rows <= 128 ? 2 : 1;      // a tile's scores are issued so many steps before its values
+      };
+      w.start(a, span, a.H * L::PER, split != 0);
+      bool more = w.next(a, span);
+      while (!failed && more) {
+        // The item's copies from what is kept of it here: the next one is looked up (and announced) behind the first of them.
+        const PromptBlock b = w.blk;
+        const int wh = w.h, t0 = w.t0, t1 = w.t1;
+        if (n == 0) announce();
+        const int head = wh / L::PER, ahead = b.rows <= half ? 2 : 1;     // a tile's scores are issued so many steps before its values
+        auto queries = [&](int X) {
+          const int st = cq % L::QST;
+          if (cq >= L::QST && !wait(bQFree + st, cq / L::QST - 1)) return;
+          if (lane == 0) {
+            bar_arrive_tx(bar(bQFull + st), static_cast<uint32_t>(half) * 2 * D);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+              tma_rows(sb + L::Q + st * L::QX + 16384 * i, &mq, 64 * i, head * a.G, b.seq.q0 + (b.r0 + X * half) / a.G, bar(bQFull + st));
+          }
+          __syncwarp();
+          ++cq;
+        };
         auto keys = [&](int t) {
           for (int i = 0; i < L::KCH; ++i, ++ck) {
             if (ck >= L::KST && !wait(bKFree + ck % L::KST, ck / L::KST - 1)) return;
             copy(&mk, sb + L::K + (ck % L::KST) * L::PIECE, 128 * i, head, b.seq.k0 + b.first_key<kTok>(t), bar(bKFull + ck % L::KST));
           }
         };
-        for (int t = w.t0; t < w.t1 && t < w.t0 + ahead && !failed; ++t) keys(t);
-        for (int t = w.t0; t < w.t1 && !failed; ++t, ++cv) {
-          if (cv >= L::VST && !wait(bVFree + cv % L::VST, cv / L::VST - 1)) break;
-          copy(&mv, sb + L::V + (cv % L::VST) * L::PIECE, w.h % L::PER * L::DV, head, b.seq.k0 + b.first_key<kTok>(t), bar(bVFull + cv % L::VST));
-          if (t + ahead < w.t1) keys(t + ahead);
+        queries(0);
+        if (!failed) keys(t0);
+        if (ahead == 1) {
+          if (!failed) queries(1);
+        } else if (!failed && t0 + 1 < t1) {
+          keys(t0 + 1);
         }
         if (failed) break;
         w.pass(a, span);
+        more = w.next(a, span);
+        if (more) announce();
+        else publish(ItemMsg{});
+        for (int t = t0; t < t1 && !failed; ++t, ++cv) {
+          if (cv >= L::VST && !wait(bVFree + cv % L::VST, cv / L::VST - 1)) break;
+          copy(&mv, sb + L::V + (cv % L::VST) * L::PIECE, wh % L::PER * L::DV, head, b.seq.k0 + b.first_key<kTok>(t), bar(bVFull + cv % L::VST));
+          if (t + ahead < t1) keys(t + ahead);
+        }
       }
-      if (!failed) publish(ItemMsg{});
+      if (n == 0 && !failed) publish(ItemMsg{});       // no item at all
       if (split && lane == 0) splits[blockIdx.x] = w.cut;
       // copies still in flight land before the CTA ends
       bool f2 = false;
+      for (int s = cq >= L::QST ? cq - L::QST : 0; s < cq; ++s) (void)bar_wait(bar(bQFull + s % L::QST), (s / L::QST) & 1, f2);
       for (int s = ck >= L::KST ? ck - L::KST : 0; s < ck; ++s) (void)bar_wait(bar(bKFull + s % L::KST), (s / L::KST) & 1, f2);
       for (int s = cv >= L::VST ? cv - L::VST : 0; s < cv; ++s) (void)bar_wait(bar(bVFull + s % L::VST), (s / L::VST) & 1, f2);
-    } else if (warp == 9) {
+    } else if (warp == 13) {
       // ---- MMA issue, the warp converged: O += w V of a tile and the next tile's scores, half A, then half B, in strict
-      // order (left to mix, both halves' MMAs would end together and neither softmax overlap the other) -------------------
+      // order (left to mix, both halves' MMAs would end together and neither softmax overlap the other); behind an item's
+      // last tile come the next item's first scores ----------------------------------------------------------------------
       auto ready = [&](int i, int phase) {             // wait() in few instructions
         if (__all_sync(0xffffffffu, wait_short(bar(i), phase & 1))) return true;
         failed = true;
         return false;
       };
-      int n = 0, ck = 0, cv = 0;                       // items; pieces of keys whose scores, tiles whose values were issued
-      ItemMsg it = next_item(0);
-      int nq0 = 0, nq1 = 0, np0 = 0, np1 = 0;          // phases of the queries and of the weights
-      int tiles = 0;
-      bool two = false;                                // rows in half B
-      auto open_item = [&]() {
-        tiles = uniform(it.ntile);
-        two = __all_sync(0xffffffffu, it.rows > 128);
+      int n = 0, cq = 0, ck = 0, cv = 0;               // items taken; halves of queries, pieces of keys, tiles of values used
+      int np0 = 0, np1 = 0, no0 = 0, no1 = 0;          // phases of the weights, and items of the halves (their O)
+      struct Item {
+        int tiles, qa, qb;                             // halves of queries: A's and B's
+        bool open, two;                                // two: rows in half B
       };
-      // scores of half X with the keys from piece c on
-      auto scores = [&](uint32_t X, int c) {
-        const uint32_t q = sb + L::Q + X * L::QB;
-        auto keys = [&](int i) { return sdesc(sb + L::K + ((c + i) % L::KST) * L::PIECE); };
-        if (D == 64) {
-          mma4_scores(tmem + col_s(X), sdesc(q), keys(0), idesc_bf16(128));
-        } else {
-          mma8_scores<0>(tmem + col_s(X), sdesc(q), keys(0), idesc_bf16(128));
-          if (L::WIDE) mma8_scores<1>(tmem + col_s(X), sdesc(q + 32768), keys(1), idesc_bf16(128));
-        }
-        mma_commit_warp(bar(bSFull + X));
+      // The next item; its first scores are started half by half.
+      auto take = [&]() {
+        const ItemMsg x = next_item(n++);
+        Item it;
+        it.open = __all_sync(0xffffffffu, x.valid) && !failed;
+        it.tiles = uniform(it.open ? x.ntile : 0);
+        it.two = __all_sync(0xffffffffu, x.rows > half);
+        it.qa = cq;
+        it.qb = it.two ? cq + 1 : cq;
+        if (it.open) cq += it.two ? 2 : 1;
+        return it;
       };
       auto keys_there = [&]() {                        // of the next tile's scores
         for (int i = 0; i < L::KCH; ++i)
@@ -635,108 +690,117 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto keys_done = [&]() {
         for (int i = 0; i < L::KCH; ++i, ++ck) mma_commit_warp(bar(bKFree + ck % L::KST));
       };
+      // scores of half X with queries qi and the keys from piece ck on
+      auto scores = [&](uint32_t X, int qi, bool last) {
+        const uint32_t q = sb + L::Q + (qi % L::QST) * L::QX;
+        auto keys = [&](int i) { return sdesc(sb + L::K + ((ck + i) % L::KST) * L::PIECE); };
+        if (D == 64) {
+          mma4_scores(tmem + col_s(X), sdesc(q), keys(0), idesc_bf16(128));
+        } else {
+          mma8_scores<0>(tmem + col_s(X), sdesc(q), keys(0), idesc_bf16(128));
+          if (L::WIDE) mma8_scores<1>(tmem + col_s(X), sdesc(q + 32768), keys(1), idesc_bf16(128));
+        }
+        mma_commit_warp(bar(bSFull + X));
+        if (last) mma_commit_warp(bar(bQFree + qi % L::QST));
+      };
       auto values = [&](uint32_t X, bool first) {
         mma8_values(tmem + col_o(X), tmem + col_s(X), vdesc(sb + L::V + (cv % L::VST) * L::PIECE), idesc_bf16(L::DV) | (1u << 16), first ? 0u : 1u);
       };
-      // the first tiles of an item: their keys and the queries
-      auto first_scores = [&]() {
-        if (!keys_there() || !ready(bQReady, nq0++)) return false;
-        tc_after();
-        scores(0, ck);
-        if (two) {
-          if (!ready(bQReady + 1, nq1++)) return false;
+      // An item's first scores of half X (two halves: of one tile; else of the first two tiles).
+      auto begin = [&](const Item& it, uint32_t X) {
+        if (!it.open || (X && !it.two && it.tiles == 1)) return true;
+        if (X && it.two) {
+          if (!ready(bQFull + it.qb % L::QST, it.qb / L::QST)) return false;
           tc_after();
-          scores(1, ck);
+          scores(1, it.qb, it.tiles == 1);
           keys_done();
           return true;
         }
-        keys_done();
-        if (tiles > 1) {
-          if (!keys_there() || (!L::WIDE && !ready(bQReady + 1, nq1++))) return false;
-          tc_after();
-          scores(1, ck);
-          keys_done();
-        }
+        if (!keys_there() || (!X && !ready(bQFull + it.qa % L::QST, it.qa / L::QST))) return false;
+        tc_after();
+        scores(X, it.qa, it.two ? it.tiles == 1 : it.tiles == static_cast<int>(X) + 1);
+        if (!it.two) keys_done();
         return true;
       };
-      bool ok = __all_sync(0xffffffffu, it.valid);
-      bool open = ok;
-      if (ok) {
-        open_item();
-        ok = first_scores();
-      }
-      while (ok && open) {
-        const int my_tiles = tiles;
-        const bool my_two = two;
-        for (int t = 0; t < my_tiles && !my_two; ++t, ++cv) {    // the halves' tiles in turn
-          const uint32_t X = t & 1;
-          ok = ready(bVOk + cv % L::VST, cv / L::VST) && ready(bPFull + X, X ? np1++ : np0++);
-          if (!ok) break;
-          tc_after();
-          values(X, t < 2);
-          mma_commit_warp(bar(bVFree + cv % L::VST));
-          if (t + 2 < my_tiles) {
-            ok = keys_there();
+      // O of half X is free: the item before it was taken from there
+      auto room = [&](uint32_t X) {
+        const int k = X ? no1++ : no0++;
+        return k == 0 || ready(bOFree + X, k - 1);
+      };
+      Item it = take();
+      bool ok = !failed && begin(it, 0) && begin(it, 1);
+      while (ok && it.open) {
+        const int tiles = it.tiles;
+        Item nx{};
+        bool taken = false;
+        if (it.two) {
+          for (int t = 0; t < tiles; ++t, ++cv) {
+            const bool last = t == tiles - 1;
+            ok = ready(bVOk + cv % L::VST, cv / L::VST) && ready(bPFull, np0++) && (t > 0 || room(0));
             if (!ok) break;
-            scores(X, ck);
-            keys_done();
-          } else {
+            tc_after();
+            values(0, t == 0);
+            if (last) {
+              mma_commit_warp(bar(bODone));
+              nx = take();
+              taken = true;
+              ok = !failed && begin(nx, 0);
+            } else {
+              ok = keys_there();
+              if (ok) scores(0, it.qa, t + 2 == tiles);
+            }
+            ok = ok && ready(bPFull + 1, np1++) && (t > 0 || room(1));
+            if (!ok) break;
+            tc_after();
+            values(1, t == 0);
+            mma_commit_warp(bar(bVFree + cv % L::VST));
+            if (last) {
+              mma_commit_warp(bar(bODone + 1));
+              ok = begin(nx, 1);
+            } else {
+              scores(1, it.qb, t + 2 == tiles);
+              keys_done();
+            }
+          }
+        } else {                                       // the halves' tiles in turn
+          for (int t = 0; t < tiles; ++t, ++cv) {
+            const uint32_t X = t & 1;
+            ok = ready(bVOk + cv % L::VST, cv / L::VST) && ready(bPFull + X, X ? np1++ : np0++) && (t > 1 || room(X));
+            if (!ok) break;
+            tc_after();
+            values(X, t < 2);
+            mma_commit_warp(bar(bVFree + cv % L::VST));
+            if (t + 2 < tiles) {
+              ok = keys_there();
+              if (!ok) break;
+              scores(X, it.qa, t + 3 == tiles);
+              keys_done();
+              continue;
+            }
             mma_commit_warp(bar(bODone + X));
+            if (X == 0 && !taken) {                    // half A is free
+              nx = take();
+              taken = true;
+              ok = !failed && begin(nx, 0);
+              if (!ok) break;
+            }
           }
-        }
-        for (int t = 0; t < my_tiles && my_two; ++t, ++cv) {
-          const bool last = t == my_tiles - 1;
-          ok = ready(bVOk + cv % L::VST, cv / L::VST) && ready(bPFull, np0++);
-          if (!ok) break;
-          tc_after();
-          values(0, t == 0);
-          if (last) {
-            mma_commit_warp(bar(bODone));
-          } else {
-            ok = keys_there();
-            if (!ok) break;
-            scores(0, ck);
-          }
-          ok = ready(bPFull + 1, np1++);
-          if (!ok) break;
-          tc_after();
-          values(1, t == 0);
-          mma_commit_warp(bar(bVFree + cv % L::VST));
-          if (last) {
-            mma_commit_warp(bar(bODone + 1));
-          } else {
-            scores(1, ck);
-            keys_done();
-          }
+          if (ok) ok = begin(nx, 1);
         }
         if (!ok) break;
-        it = next_item(++n);
-        open = __all_sync(0xffffffffu, it.valid);
-        if (failed) ok = false;
-        if (ok && open) {
-          open_item();
-          ok = first_scores();
-        }
+        it = nx;
       }
       mma_commit_warp(bar(bDrain));                    // every MMA issued completes before the CTA ends
       bool f2 = false;
       (void)bar_wait(bar(bDrain), 0, f2);
       __syncwarp();
     } else {
-      // ---- an item's queries on their way to L2 as soon as it is known; the values of tiles that some row does not see in
-      // full: what is not finite is taken out --------------------------------------------------------------------------
-      const int me = warp - 10;
+      // ---- the values of tiles that some row does not see in full: what is not finite is taken out ----------------------
+      const int me = warp - 14;
       int cv = 0;
       for (int n = 0;; ++n) {
         const ItemMsg it = next_item(n);
         if (!it.valid) break;
-        constexpr int kLines = D / 64;                 // 128-byte lines of a row
-        for (int i = 32 * me + lane; i < it.rows * kLines; i += 64) {
-          const int gr = it.r0 + i / kLines, tok = gr / a.G;
-          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<long long>(it.q0) + tok) * a.qs +
-                                   static_cast<long long>(it.h / L::PER * a.G + (gr - tok * a.G)) * D;
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64 * (i % kLines)));
-        }
         const int ntile = it.ntile;
         bool any = false;
         for (int t = 0; t < ntile; ++t, ++cv) {
@@ -745,12 +809,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t at = sb + L::V + (cv % L::VST) * L::PIECE + me * (L::PIECE / 2) + lane * 16;
             bool odd = false;
 #pragma unroll 1
-            for (int i = 0; i < L::PIECE / 2; i += 512 * 8) {
-              uint4 v[8];
+            for (int i = 0; i < L::PIECE / 2; i += 512 * 4) {
+              uint4 v[4];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] = lds128(at + i + 512 * k);
+              for (int k = 0; k < 4; ++k) v[k] = lds128(at + i + 512 * k);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
+              for (int k = 0; k < 4; ++k)
                 if (odd_piece(v[k])) {
                   odd = true;
                   uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
@@ -783,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {        // from the driver, looked up once
@@ -797,33 +861,38 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {        // from the driver, looke
   }();
   return fn;
 }
-// Rows of keys or values: coordinates (channel, head, row), boxes of 64 channels of 128 rows.
-bool rows_map(CUtensorMap* map, const void* p, int d, int heads, long long rows, long long stride) {
+// Rows of queries, keys or values: coordinates (channel, head, row), boxes of 64 channels of some heads and rows.
+bool rows_map(CUtensorMap* map, const void* p, int d, int heads, long long rows, long long stride, int box_heads, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
-  const cuuint32_t box[3] = {64, 1, kTok};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
-cudaError_t launch_t(const PromptArgs& a, cudaStream_t s) {
+cudaError_t launch_t(const PromptArgs& args, cudaStream_t s) {
   using L = PG<D>;
-  CUtensorMap mk, mv;
-  if (!rows_map(&mk, a.k, D, a.H, a.total_k, a.ks) || !rows_map(&mv, a.v, D, a.H, a.total_k, a.vs)) return cudaErrorInvalidValue;
+  PromptArgs a = args;
+  const int tokens = 128 / a.G;                        // of a half
+  a.rows = L::HALVES * tokens * a.G;
+  CUtensorMap mq, mk, mv;
+  if (!rows_map(&mq, a.q, D, a.Hq, a.total_q, a.qs, a.G, tokens) || !rows_map(&mk, a.k, D, a.H, a.total_k, a.ks, 1, kTok) ||
+      !rows_map(&mv, a.v, D, a.H, a.total_k, a.vs, 1, kTok))
+    return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = smem_attr_once(prompt_tc_kernel<D>, PS<D>::BYTES, configured);
   if (e != cudaSuccess) return e;
-  const long long items = prompt_most_blocks(a, L::ROWS) * a.H * L::PER, tiles = a.max_k / kTok + 2 + a.sinks / kTok;
+  const long long items = prompt_most_blocks(a) * a.H * L::PER, tiles = a.max_k / kTok + 2 + a.sinks / kTok;
   // items of few tiles are not cut (and need no join)
-  const bool split = tiles > 4 && prompt_splits(a, L::ROWS, kTok, kItemCost);
+  const bool split = tiles > 4 && prompt_splits(a, kTok, kItemCost);
   const int sms = prompt_sms();
   const long long most = split ? (items * (tiles + kItemCost) + kMinSpan - 1) / kMinSpan : items;
   const int ctas = static_cast<int>(most < sms ? (most < 1 ? 1 : most) : sms);
-  e = launch_pdl(prompt_tc_kernel<D>, dim3(ctas), dim3(kThreads), PS<D>::BYTES, s, a, mk, mv, split ? 1 : 0);
+  e = launch_pdl(prompt_tc_kernel<D>, dim3(ctas), dim3(kThreads), PS<D>::BYTES, s, a, mq, mk, mv, split ? 1 : 0);
   if (e != cudaSuccess || !split) return e;
   return launch_prompt_join(a, D, false, ctas, L::ROWS, L::PER, s);
 }
@@ -831,7 +900,7 @@ cudaError_t launch_t(const PromptArgs& a, cudaStream_t s) {
 }  // namespace
 
 bool prompt_tc_takes(const PromptArgs& a, int d, bool f32) {
-  return !f32 && (d == 64 || d == 128 || d == 256) && a.scale_log2 != 0.0f && a.total_k > 0;
+  return !f32 && (d == 64 || d == 128 || d == 256) && a.G <= 128 && a.scale_log2 > 0.0f && a.total_k > 0;
 }
 
 size_t prompt_tc_workspace(int d) {
