@@ -5,8 +5,9 @@
 // that is cut into equal spans, one per CTA; the parts of an item that crosses spans are joined by a second kernel.  Per
 // tile, with x = scale log2(e) <q, k>:
 //   S = Q K^T              bf16, from tiles that TMA puts in place
-//   w = 2^(x - M)          M the maximum of the row's first tile; bf16 has fp32's range, so that M moves only where a
-//                          tile's weights sum to more than 2^40, and no tile but the first looks for a maximum
+//   w = 2^(x - M)          bf16 and fp32 hold the weights whatever M is, within 2^126: M starts as 0, and only a tile whose
+//                          weights sum to more than 2^40, or that leaves a row that sees something with a sum below
+//                          2^-40, looks for a maximum
 //   O += w V, l += sum w   w as bf16 (off by 2^-8 at most) in tensor memory, V's token rows read MN-major;
 //   out = O / l.
 // The halves take turns: while the softmax of one runs, the tensor cores work on the other.  An item follows the one
@@ -44,16 +45,14 @@ constexpr int kThreads = 512;
 constexpr int kItems = 4;                 // items announced ahead
 constexpr int kItemCost = 5;              // an item's start and end, in tiles' time
 constexpr int kMinSpan = 2 + kItemCost;   // a CTA's share of the list at least
-constexpr float kMNone = -3.0e38f;        // a maximum before any score: finite, and below the scores of fp32
-constexpr float kFull = 1.0995116e12f;    // 2^40: a tile's sum beyond it moves the maximum
-constexpr float kAbove = 40.0f;           // or a score so far above it
+constexpr float kFull = 1.0995116e12f, kTiny = 9.0949470e-13f;    // 2^40 and 2^-40: bounds of a row's sum
 // x - M in one rounding is off by half a step of M against the other tiles' M: beyond 2^16 scores are rounded first, so that
 // small differences of large ones are exact.
 constexpr float kBig = 65536.0f;
 constexpr int kCheckRing = 8;
 
 // Registers: 16 warps start with 128 a thread, and the eight of the softmax take what the others give back.
-constexpr int kRegsSoftmax = 184, kRegsResults = 80, kRegsOthers = 64;
+constexpr int kRegsSoftmax = 176, kRegsResults = 80, kRegsOthers = 80;
 static_assert(8 * kRegsSoftmax + 4 * kRegsResults + 4 * kRegsOthers <= 16 * 128, "more registers than the block starts with");
 
 template <int D>
@@ -172,25 +171,28 @@ __device__ __forceinline__ uint32_t seen32(int p, int j0, int window, int sinks)
   }
   return see;
 }
-// One tile's weights of a thread's row with a new maximum: scores are rounded before they are compared.  accumulated: O
-// holds tiles before.  Returns M and l.
+// One tile's weights of a thread's row with a new M, the largest score met; scores are rounded before they are compared.
+// accumulated: O holds tiles before.  Returns M and l.
 template <int DV>
 __device__ __noinline__ float2 careful_tile(uint32_t ts, uint32_t to, int j0, int p, int window, int sinks, float f, bool accumulated,
                                             float m, float l) {
   auto scores = [&](int c, float (&y)[32]) {
     tld32(ts + 32u * c, y);
+    const uint32_t see = seen32(p, j0 + 32 * c, window, sinks);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) y[k] = prompt_sees(p, j0 + 32 * c + k, window, sinks) ? __fmul_rn(y[k], f) : -INFINITY;
+    for (int k = 0; k < 32; ++k) y[k] = (see >> k) & 1u ? __fmul_rn(y[k], f) : -INFINITY;
     __syncwarp();
   };
-  float y[32], mn = m;
+  // of the sum so far: l 2^m, about 2^(m + log2 l), so that alpha l is about 1 at most
+  float y[32], mn = l > 0.0f ? m + log2f(l) : -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     scores(c, y);
 #pragma unroll
     for (int k = 0; k < 32; ++k) mn = fmaxf(mn, y[k]);
   }
-  const float alpha = m == mn ? 1.0f : ex2(m - mn);
+  if (mn == -INFINITY) mn = 0.0f;                      // nothing seen
+  const float alpha = l > 0.0f ? ex2(m - mn) : 1.0f;
   __syncwarp();
   if (accumulated) rescale_o<DV>(to, alpha);
   l *= alpha;
@@ -355,20 +357,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = r < half && rx < it.rows;      // what the other lanes hold is no row, and nobody looks at it
       const int p = it.p0 + (it.r0 + rx) / a.G;
       const int first = turns ? X : 0, step = turns ? 2 : 1;
-      float m = kMNone, l = 0.0f;
-      bool bigs = false;                               // a row of the warp has had a maximum beyond kBig
+      float m = 0.0f, l = 0.0f;
+      bool bigs = false;                               // a row of the warp has had an M beyond kBig
       for (int t = first; t < ntile; t += step) {
         if (!wait(bSFull + X, nS++)) break;
         tc_after();
         const int j0 = it.first_key(t);
-        const bool full = it.full(j0, a.window, a.sinks);
         bool done = false;
-        const uint64_t f2 = pack2(f, f);
-        if (!bigs && full && t > first) {              // the tile as it mostly is
+        if (!bigs) {
           float x[kTok];
           uint32_t w[kTok / 2];
           tld32x4(ts, x);
-          const uint64_t b2 = pack2(-m, -m);
+          bool sees = live;                            // the row sees something of the tile
+          if (!it.full(j0, a.window, a.sinks)) {
+            uint32_t all = 0u;
+#pragma unroll
+            for (int c = 0; c < kTok; c += 32) {
+              const uint32_t see = seen32(p, j0 + c, a.window, a.sinks);
+              all |= see;
+              if (__any_sync(0xffffffffu, see != 0xFFFFFFFFu)) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[c + k] = (see >> k) & 1u ? x[c + k] : -INFINITY;
+              }
+            }
+            sees = live && all != 0u;
+          }
+          const uint64_t f2 = pack2(f, f), b2 = pack2(-m, -m);
           uint64_t s2 = 0ull, s3 = 0ull;
 #pragma unroll
           for (int c = 0; c < kTok; c += 4) {
@@ -387,79 +401,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           float s0, s1;
           unpack2(add2(s2, s3), s0, s1);
           s0 += s1;
-          if (!__any_sync(0xffffffffu, live && s0 > kFull)) {
+          if (!__any_sync(0xffffffffu, sees && (s0 > kFull || l + s0 < kTiny))) {
             l += s0;
             tst32(ts, *reinterpret_cast<uint32_t(*)[32]>(w));
             tst32(ts + 32u, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
             done = true;
           }
-        } else if (!bigs) {
-          // An edge, or an item's first tile: the maximum, then the weights, 32 keys at a time and only those that some row
-          // sees; rolled, since code that runs once or twice an item is out of the instruction cache (unrolled as above:
-          // 2,200 cycles more a tile).
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < kTok; c += 32) {
-            const uint32_t see = full ? 0xFFFFFFFFu : seen32(p, j0 + c, a.window, a.sinks);
-            if (!__any_sync(0xffffffffu, see != 0u)) continue;
-            float x[32];
-            tld32(ts + c, x);
-            if (__any_sync(0xffffffffu, see != 0xFFFFFFFFu)) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = (see >> k) & 1u ? x[k] : -INFINITY;
-            }
-            float m0 = x[0], m1 = x[1];
-#pragma unroll
-            for (int k = 2; k < 32; k += 2) {
-              m0 = fmaxf(m0, x[k]);
-              m1 = fmaxf(m1, x[k + 1]);
-            }
-            top = fmaxf(top, fmaxf(m0, m1));
-            __syncwarp();
-          }
-          top *= f;
-          if (t == first) m = fmaxf(top, kMNone);
-          bigs = __any_sync(0xffffffffu, live && fabsf(m) > kBig && m > kMNone);
-          if (!bigs && !__any_sync(0xffffffffu, live && top > m + kAbove)) {
-            const uint64_t b2 = pack2(-m, -m);
-            uint64_t s2 = 0ull;
-#pragma unroll 1
-            for (int c = 0; c < kTok; c += 32) {
-              const uint32_t see = full ? 0xFFFFFFFFu : seen32(p, j0 + c, a.window, a.sinks);
-              uint32_t w[16];
-              if (__any_sync(0xffffffffu, see != 0u)) {
-                float x[32];
-                tld32(ts + c, x);
-                if (__any_sync(0xffffffffu, see != 0xFFFFFFFFu)) {
-#pragma unroll
-                  for (int k = 0; k < 32; ++k) x[k] = (see >> k) & 1u ? x[k] : -INFINITY;
-                }
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  float y0, y1;
-                  unpack2(fma2(pack2(x[2 * k], x[2 * k + 1]), f2, b2), y0, y1);
-                  y0 = ex2(y0);
-                  y1 = ex2(y1);
-                  s2 = add2(s2, pack2(y0, y1));
-                  w[k] = bf16x2_bits(y0, y1);
-                }
-              } else {
-#pragma unroll
-                for (int k = 0; k < 16; ++k) w[k] = 0u;
-              }
-              __syncwarp();
-              tst16(ts + c / 2, w);                    // (over scores that were read)
-            }
-            float s0, s1;
-            unpack2(s2, s0, s1);
-            l += s0 + s1;
-            done = true;
-          }
         }
         if (!done) {
-          const float2 next = careful_tile<L::DV>(ts, to, j0, p, a.window, a.sinks, f, t > first, t > first ? m : kMNone, l);
+          const float2 next = careful_tile<L::DV>(ts, to, j0, p, a.window, a.sinks, f, t > first, m, l);
           m = next.x;
           l = next.y;
+          bigs = __any_sync(0xffffffffu, live && fabsf(m) > kBig);
         }
         tst_wait();
         tc_before();
@@ -470,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (first >= ntile) continue;                    // one tile in one half: nothing for B
       if (items > 0 && !wait(bOFree + X, items - 1)) break;      // the sums before were taken
       ++items;
-      sums[128 * X + r] = make_float2(m, l);
+      sums[128 * X + r] = make_float2(l == 0.0f ? -INFINITY : m, l);      // M of nothing counts below every other
       __syncwarp();
       if (lane == 0) bar_arrive(bar(bSums + X));
     }
@@ -504,8 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (joins) {
           const float2 other = sums[128 + r];
           m = fmaxf(mine.x, other.x);
-          fa = ex2(mine.x - m);
-          fb = ex2(other.x - m);
+          fa = m == -INFINITY ? 1.0f : ex2(mine.x - m);
+          fb = m == -INFINITY ? 1.0f : ex2(other.x - m);
           l = fa * l + fb * other.y;
         }
         if (X == 0 && !wait(bChecked + n % kCheckRing, n / kCheckRing)) break;
@@ -535,32 +488,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long at = ((static_cast<long long>(it.q0) + tok) * a.Hq + hkv * a.G + (gr - tok * a.G)) * D + ch0;
         float* part = parts + (static_cast<long long>(it.slot) * L::ROWS + rx) * L::PART;
 #pragma unroll 1
-        for (int c = 0; c < L::DV / 16; ++c) {
-          float o[16];
-          tld16(to + 16u * c, o);
+        for (int c = 0; c < L::DV / 32; ++c) {
+          float o[32];
+          tld32(to + 32u * c, o);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] *= fa;
+          for (int k = 0; k < 32; ++k) o[k] *= fa;
           if (both) {
-            float o2[16];
-            tld16(trow + col_o(1) + 16u * c, o2);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = fmaf(fb, o2[k], o[k]);
+            for (int q = 0; q < 2; ++q) {
+              float o2[16];
+              tld16(trow + col_o(1) + 32u * c + 16u * q, o2);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[16 * q + k] = fmaf(fb, o2[k], o[16 * q + k]);
+            }
           }
           if (live && it.slot < 0) {
-            uint32_t w[8];
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = bf16x2_bits(o[2 * k], o[2 * k + 1]);
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at + 16 * c;
+            for (int k = 0; k < 16; ++k) w[k] = bf16x2_bits(o[2 * k], o[2 * k + 1]);
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + at + 32 * c;
             if (wide) {
               stg256(dst, w);
+              stg256(dst + 16, w + 8);
             } else {
-              reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(dst)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
             }
           } else if (live) {
-            float4* dst = reinterpret_cast<float4*>(part + 4 + 16 * c);
+            float4* dst = reinterpret_cast<float4*>(part + 4 + 32 * c);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
             if (c == 0) *reinterpret_cast<float4*>(part) = make_float4(m, l, 0.0f, 0.0f);
           }
           __syncwarp();                                // lanes with no row wait: the loads are the whole warp's
@@ -578,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 12) {
       // ---- items, queries, keys, values -------------------------------------------------------
       int n = 0, cq = 0, ck = 0, cv = 0;               // items, and halves of queries, pieces of keys and tiles of values asked for
+      int q_left = 0, q_head = 0, q_row = 0;           // halves of queries that are still to come, and where they stand
       auto publish = [&](const ItemMsg& x) {
         // Every warp has taken the one before.  If one has not within the limit, its room stays as it is, and the others'
         // waits for this one give up too.
@@ -603,6 +561,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto announce = [&]() {
         const PromptBlock& b = w.blk;
         publish(ItemMsg{1, w.h, b.seq.q0, b.r0, b.rows, b.seq.m - b.seq.n, b.pmin, b.pmax, w.t1 - w.t0, w.t0, w.slot, b.seq.k0, b.ns, b.w0, {0, 0}});
+        q_left = b.rows <= half ? 1 : 2;
+        q_head = w.h / L::PER * a.G;
+        q_row = b.seq.q0 + b.r0 / a.G;
+      };
+      // The halves of queries of the item that was announced last: ahead of time, as soon as a room is free (wait: all of
+      // them now).
+      auto queries = [&](bool now) {
+        for (; q_left > 0 && !failed; --q_left, ++cq, q_row += half / a.G) {
+          const int st = cq % L::QST;
+          if (cq >= L::QST) {
+            if (!now && !__all_sync(0xffffffffu, bar_poll(bar(bQFree + st), (cq / L::QST - 1) & 1))) return;
+            if (now && !wait(bQFree + st, cq / L::QST - 1)) return;
+          }
+          if (lane == 0) {
+            bar_arrive_tx(bar(bQFull + st), static_cast<uint32_t>(half) * 2 * D);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) tma_rows(sb + L::Q + st * L::QX + 16384 * i, &mq, 64 * i, q_head, q_row, bar(bQFull + st));
+          }
+          __syncwarp();
+        }
       };
       w.start(a, span, a.H * L::PER, split != 0);
       bool more = w.next(a, span);
@@ -612,37 +590,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wh = w.h, t0 = w.t0, t1 = w.t1;
         if (n == 0) announce();
         const int head = wh / L::PER, ahead = b.rows <= half ? 2 : 1;     // a tile's scores are issued so many steps before its values
-        auto queries = [&](int X) {
-          const int st = cq % L::QST;
-          if (cq >= L::QST && !wait(bQFree + st, cq / L::QST - 1)) return;
-          if (lane == 0) {
-            bar_arrive_tx(bar(bQFull + st), static_cast<uint32_t>(half) * 2 * D);
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i)
-              tma_rows(sb + L::Q + st * L::QX + 16384 * i, &mq, 64 * i, head * a.G, b.seq.q0 + (b.r0 + X * half) / a.G, bar(bQFull + st));
-          }
-          __syncwarp();
-          ++cq;
-        };
         auto keys = [&](int t) {
           for (int i = 0; i < L::KCH; ++i, ++ck) {
             if (ck >= L::KST && !wait(bKFree + ck % L::KST, ck / L::KST - 1)) return;
             copy(&mk, sb + L::K + (ck % L::KST) * L::PIECE, 128 * i, head, b.seq.k0 + b.first_key<kTok>(t), bar(bKFull + ck % L::KST));
           }
         };
-        queries(0);
-        if (!failed) keys(t0);
-        if (ahead == 1) {
-          if (!failed) queries(1);
-        } else if (!failed && t0 + 1 < t1) {
-          keys(t0 + 1);
-        }
+        // (the queries ahead of the second tile's keys, whose room may come free by the first one's scores)
+        queries(false);
+        keys(t0);
+        if (!failed) queries(true);
+        if (!failed && ahead == 2 && t0 + 1 < t1) keys(t0 + 1);
         if (failed) break;
         w.pass(a, span);
         more = w.next(a, span);
         if (more) announce();
         else publish(ItemMsg{});
         for (int t = t0; t < t1 && !failed; ++t, ++cv) {
+          queries(false);
           if (cv >= L::VST && !wait(bVFree + cv % L::VST, cv / L::VST - 1)) break;
           copy(&mv, sb + L::V + (cv % L::VST) * L::PIECE, wh % L::PER * L::DV, head, b.seq.k0 + b.first_key<kTok>(t), bar(bVFull + cv % L::VST));
           if (t + ahead < t1) keys(t + ahead);
