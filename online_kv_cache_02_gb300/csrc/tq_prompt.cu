@@ -46,20 +46,20 @@ __device__ __forceinline__ bool finite4(float4 x) {
 }
 
 template <int D, bool F32>
-__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_constant__ PromptArgs a, int split) {
+__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_constant__ PromptArgs a, int mode) {
   using L = SG<D>;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   pdl_wait();
-  if (split) pdl_trigger();
+  if (mode == kPromptCut) pdl_trigger();
   if (F32) prompt_zero_rows<float>(a, D);
   else prompt_zero_rows<__nv_bfloat16>(a, D);
   PromptSpan span{};
-  if (split) span = prompt_span<kTok, kItemCost, kThreads>(a, a.H, kMinSpan, reinterpret_cast<int*>(sm));
+  if (mode != kPromptTurns) span = prompt_span<kTok, kItemCost, kThreads>(a, a.H, kMinSpan, reinterpret_cast<int*>(sm));
   PSplit* splits = reinterpret_cast<PSplit*>(a.part);
   float* parts = a.part + static_cast<size_t>(gridDim.x) * (sizeof(PSplit) / sizeof(float));
   PromptWalk<kTok, kItemCost> w;
-  w.start(a, span, a.H, split != 0);
+  w.start(a, span, a.H, mode);
   while (w.next(a, span)) {
     const PromptBlock& b = w.blk;
     // ---- queries, transposed: a warp's lanes take 32 rows of the same channels ------------------
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
     }
     w.pass(a, span);
   }
-  if (split && tid == 0) splits[blockIdx.x] = w.cut;
+  if (mode == kPromptCut && tid == 0) splits[blockIdx.x] = w.cut;
 }
 
 // Joins the parts of the items that cross spans: a warp per row and run of DV channels.  A part's maximum may have an
@@ -260,11 +260,13 @@ cudaError_t launch_t(const PromptArgs& a, bool f32, cudaStream_t s) {
   cudaError_t e = f32 ? smem_attr_once(prompt_simt_kernel<D, true>, SG<D>::BYTES, done32)
                       : smem_attr_once(prompt_simt_kernel<D, false>, SG<D>::BYTES, done16);
   if (e != cudaSuccess) return e;
-  const bool split = prompt_splits(a, kTok, kItemCost);
+  const long long tiles = a.max_k / kTok + 2 + a.sinks / kTok;
+  // items of few tiles are not cut (and need no join)
+  const int mode = !prompt_splits(a, kTok, kItemCost) ? kPromptTurns : tiles > 4 ? kPromptCut : kPromptWhole;
   const int ctas = simt_ctas(D);
-  e = f32 ? launch_pdl(prompt_simt_kernel<D, true>, dim3(ctas), dim3(kThreads), SG<D>::BYTES, s, a, split ? 1 : 0)
-          : launch_pdl(prompt_simt_kernel<D, false>, dim3(ctas), dim3(kThreads), SG<D>::BYTES, s, a, split ? 1 : 0);
-  if (e != cudaSuccess || !split) return e;
+  e = f32 ? launch_pdl(prompt_simt_kernel<D, true>, dim3(ctas), dim3(kThreads), SG<D>::BYTES, s, a, mode)
+          : launch_pdl(prompt_simt_kernel<D, false>, dim3(ctas), dim3(kThreads), SG<D>::BYTES, s, a, mode);
+  if (e != cudaSuccess || mode != kPromptCut) return e;
   return launch_prompt_join(a, D, f32, ctas, kRows, 1, s);
 }
 }  // namespace

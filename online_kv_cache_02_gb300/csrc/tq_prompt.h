@@ -171,18 +171,21 @@ __device__ PromptSpan prompt_span(const PromptArgs& a, int heads, int min_span, 
   return x;
 }
 
-// The items of a CTA in order: parts of the listed ones by its span, or whole items in turn.
+// How the items come to the CTAs: listed ones by equal spans, cut where a span ends (a join follows) or whole, by where they
+// start; or, where there are more than the list holds, whole items in turn.
+enum PromptMode { kPromptCut = 1, kPromptWhole = 2, kPromptTurns = 0 };
+
+// The items of a CTA in order, by whole warps (all of them alike).
 template <int TOK, int COST>
 struct PromptWalk {
   PromptBlock blk;
   int h, t0, t1, slot;                    // KV head (or item of one); its tiles [t0, t1); workspace slot, -1 for whole items
   PSplit cut;                             // the record that this CTA leaves
   long long at, whole;
-  int s, qb, tiles, heads, nblk;
-  bool split;
+  int s, qb, tiles, heads, nblk, mode;
 
-  __device__ __forceinline__ void start(const PromptArgs& a, const PromptSpan& x, int heads_, bool split_) {
-    split = split_;
+  __device__ __forceinline__ void start(const PromptArgs& a, PromptSpan& x, int heads_, int mode_) {
+    mode = mode_;
     heads = heads_;
     cut = PSplit{};
     at = x.at;
@@ -190,16 +193,17 @@ struct PromptWalk {
     qb = x.qb;
     h = 0;
     whole = blockIdx.x;
-    if (split) {
-      if (x.u0 >= x.u1) return;
-      load(a);
-      h = static_cast<int>((x.u0 - at) / (tiles + COST));
-      at += static_cast<long long>(h) * (tiles + COST);
-    } else {
+    if (mode == kPromptTurns) {
       s = -1;
       at = 0;
       nblk = 0;
+      return;
     }
+    if (x.u0 >= x.u1) return;
+    load(a);
+    h = static_cast<int>((x.u0 - at) / (tiles + COST));
+    at += static_cast<long long>(h) * (tiles + COST);
+    if (mode == kPromptWhole && at < x.u0) pass(a, x);   // it is the CTA's before
   }
   __device__ __forceinline__ void load(const PromptArgs& a) {
     const PromptSeq q = prompt_seq(a, s);
@@ -209,16 +213,27 @@ struct PromptWalk {
   }
   // The next item with tiles of this CTA; false at the end.
   __device__ __forceinline__ bool next(const PromptArgs& a, PromptSpan& x) {
-    if (!split) {
+    slot = -1;
+    if (mode == kPromptTurns) {
+      const int lane = threadIdx.x & 31;
       for (;; whole += gridDim.x) {
-        while (whole >= at + static_cast<long long>(nblk) * heads) {
+        while (whole >= at + static_cast<long long>(nblk) * heads) {       // at: items before sequence s
           at += static_cast<long long>(nblk) * heads;
-          if (++s >= a.S) {
-            s = a.S - 1;
-            nblk = 0;
-            return false;
+          nblk = 0;
+          if (s >= a.S - 1) return false;
+          // the 32 sequences behind, a lane each: the one that holds the item, or the last
+          const int mine = s + 1 + lane < a.S ? prompt_blocks(a, prompt_seq(a, s + 1 + lane)) : 0;
+          long long run = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, run, o);
+            run += lane >= o ? v : 0;
           }
-          nblk = prompt_blocks(a, prompt_seq(a, s));
+          const uint32_t there = __ballot_sync(0xffffffffu, whole < at + run * heads);
+          const int k = there ? __ffs(there) - 1 : 31;
+          at += (__shfl_sync(0xffffffffu, run, k) - __shfl_sync(0xffffffffu, mine, k)) * heads;
+          nblk = __shfl_sync(0xffffffffu, mine, k);
+          s = min(s + 1 + k, a.S - 1);
         }
         const int i = static_cast<int>(whole - at);
         qb = nblk - 1 - i / heads;        // a sequence's longest rows first
@@ -230,22 +245,26 @@ struct PromptWalk {
       whole += gridDim.x;
       t0 = 0;
       t1 = tiles;
-      slot = -1;
       return true;
     }
     if (x.u0 >= x.u1) return false;
+    if (mode == kPromptWhole) {
+      t0 = 0;
+      t1 = tiles;
+      return true;
+    }
     t0 = max(0, static_cast<int>(x.u0 - at) - COST);
     t1 = static_cast<int>(min(x.u1 - at - COST, static_cast<long long>(tiles)));
     if (t1 <= t0) return false;           // the span ends before the item's first tile
     if (t0 == 0 && t1 < tiles)
       cut = PSplit{1, blk.seq.q0, blk.r0, blk.rows, h, static_cast<int>((at + COST + tiles - 1) / x.span),
                    blk.seq.m - blk.seq.n, 0};
-    slot = t0 == 0 && t1 == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (t0 ? 0 : 1);
+    if (t0 > 0 || t1 < tiles) slot = 2 * static_cast<int>(blockIdx.x) + (t0 ? 0 : 1);
     return true;
   }
   // Behind an item: where the next one starts.
   __device__ __forceinline__ void pass(const PromptArgs& a, PromptSpan& x) {
-    if (!split) return;
+    if (mode == kPromptTurns) return;
     at += COST + tiles;
     x.u0 = at;
     if (x.u0 >= x.u1) return;

@@ -21,8 +21,8 @@
 // not see in full are looked through before they are multiplied, what is not finite there is taken out, and added to the
 // rows that see it at the end.
 //
-// Warps 0-3 and 4-7: the softmax of A and B (thread = row); 8-11: the results; 12: items, the copies; 13: MMA issue; 14
-// and 15: the values of edge tiles.  Every wait is bounded; a wait that gives up sets the device error word.
+// Warps 0-3 and 4-7: the softmax of A and B (thread = row); 8-11: the results; 12: items, the copies of queries and keys;
+// 13: MMA issue; 14: a look at the values of edge tiles; 15: the values' copies.  Every wait is bounded; a wait that gives up sets the device error word.
 
 #include "tq_prompt.h"
 #include "tq_tc.cuh"
@@ -43,7 +43,7 @@ using namespace tcx;
 constexpr int kTok = 128;                 // keys per tile
 constexpr int kThreads = 512;
 constexpr int kItems = 4;                 // items announced ahead
-constexpr int kItemCost = 5;              // an item's start and end, in tiles' time
+constexpr int kItemCost = 3;              // an item's start and end, in tiles' time
 constexpr int kMinSpan = 2 + kItemCost;   // a CTA's share of the list at least
 constexpr float kFull = 1.0995116e12f, kTiny = 9.0949470e-13f;    // 2^40 and 2^-40: bounds of a row's sum
 // x - M in one rounding is off by half a step of M against the other tiles' M: beyond 2^16 scores are rounded first, so that
@@ -255,7 +255,7 @@ __device__ __noinline__ void add_odd_values(uint32_t to, const __nv_bfloat16* v,
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                     const __grid_constant__ CUtensorMap mv, int split) {
+                     const __grid_constant__ CUtensorMap mv, int mode) {
   using L = PG<D>;
   using P = PS<D>;
   extern __shared__ __align__(1024) unsigned char sm_raw[];
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     if (tid == 0) {
       atomicOr(a.err, kErrLayout);
-      if (split) splits[blockIdx.x].valid = 0;
+      if (mode == kPromptCut) splits[blockIdx.x].valid = 0;
     }
     return;
   }
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < L::VST; ++i) {
       bar_init(bar(bVFull + i), 1);
       bar_init(bar(bVFree + i), 1);
-      bar_init(bar(bVOk + i), 2);
+      bar_init(bar(bVOk + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(bar(bSFull + i), 1);
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(bar(bItemFree + i), 15);                // every warp but the one that announces
     }
     for (int i = 0; i < kCheckRing; ++i) {
-      bar_init(bar(bChecked + i), 2);
+      bar_init(bar(bChecked + i), 1);
       odd_of[i] = 0;
     }
     bar_init(bar(bDrain), 1);
@@ -313,10 +313,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  if (split) pdl_trigger();                            // the join's launch
+  if (mode == kPromptCut) pdl_trigger();                            // the join's launch
   prompt_zero_rows<__nv_bfloat16>(a, D);
   PromptSpan span{};
-  if (split) span = prompt_span<kTok, kItemCost, kThreads>(a, a.H * L::PER, kMinSpan, reinterpret_cast<int*>(sm));
+  if (mode != kPromptTurns) span = prompt_span<kTok, kItemCost, kThreads>(a, a.H * L::PER, kMinSpan, reinterpret_cast<int*>(sm));
   fence_async_smem();
   tc_before();
   __syncthreads();
@@ -337,6 +337,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) bar_arrive(bar(bItemFree + n % kItems));
     return x;
+  };
+
+  // a piece of keys or a tile of values
+  auto copy = [&](const CUtensorMap* map, uint32_t dst, int ch, int head, int row, uint32_t full) {
+    if (lane == 0) {
+      bar_arrive_tx(full, L::PIECE);
+#pragma unroll
+      for (int i = 0; i < L::PIECE / 16384; ++i) tma_rows(dst + 16384 * i, map, ch + 64 * i, head, row, full);
+    }
+    __syncwarp();
   };
 
   if (warp < 8) {
@@ -533,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOthers));
     if (warp == 12) {
-      // ---- items, queries, keys, values -------------------------------------------------------
-      int n = 0, cq = 0, ck = 0, cv = 0;               // items, and halves of queries, pieces of keys and tiles of values asked for
+      // ---- items, queries, keys ---------------------------------------------------------------
+      int n = 0, cq = 0, ck = 0;                       // items, and halves of queries and pieces of keys asked for
       int q_left = 0, q_head = 0, q_row = 0;           // halves of queries that are still to come, and where they stand
       auto publish = [&](const ItemMsg& x) {
         // Every warp has taken the one before.  If one has not within the limit, its room stays as it is, and the others'
@@ -548,14 +558,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           bar_arrive(bar(bItem + n % kItems));
         }
         ++n;
-      };
-      auto copy = [&](const CUtensorMap* map, uint32_t dst, int ch, int head, int row, uint32_t full) {
-        if (lane == 0) {
-          bar_arrive_tx(full, L::PIECE);
-#pragma unroll
-          for (int i = 0; i < L::PIECE / 16384; ++i) tma_rows(dst + 16384 * i, map, ch + 64 * i, head, row, full);
-        }
-        __syncwarp();
       };
       PromptWalk<kTok, kItemCost> w;
       auto announce = [&]() {
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       };
-      w.start(a, span, a.H * L::PER, split != 0);
+      w.start(a, span, a.H * L::PER, mode);
       bool more = w.next(a, span);
       while (!failed && more) {
         // The item's copies from what is kept of it here: the next one is looked up (and announced) behind the first of them.
@@ -606,20 +608,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         more = w.next(a, span);
         if (more) announce();
         else publish(ItemMsg{});
-        for (int t = t0; t < t1 && !failed; ++t, ++cv) {
+        for (int t = t0 + ahead; t < t1 && !failed; ++t) {
           queries(false);
-          if (cv >= L::VST && !wait(bVFree + cv % L::VST, cv / L::VST - 1)) break;
-          copy(&mv, sb + L::V + (cv % L::VST) * L::PIECE, wh % L::PER * L::DV, head, b.seq.k0 + b.first_key<kTok>(t), bar(bVFull + cv % L::VST));
-          if (t + ahead < t1) keys(t + ahead);
+          keys(t);
         }
       }
       if (n == 0 && !failed) publish(ItemMsg{});       // no item at all
-      if (split && lane == 0) splits[blockIdx.x] = w.cut;
+      if (mode == kPromptCut && lane == 0) splits[blockIdx.x] = w.cut;
       // copies still in flight land before the CTA ends
       bool f2 = false;
       for (int s = cq >= L::QST ? cq - L::QST : 0; s < cq; ++s) (void)bar_wait(bar(bQFull + s % L::QST), (s / L::QST) & 1, f2);
       for (int s = ck >= L::KST ? ck - L::KST : 0; s < ck; ++s) (void)bar_wait(bar(bKFull + s % L::KST), (s / L::KST) & 1, f2);
-      for (int s = cv >= L::VST ? cv - L::VST : 0; s < cv; ++s) (void)bar_wait(bar(bVFull + s % L::VST), (s / L::VST) & 1, f2);
     } else if (warp == 13) {
       // ---- MMA issue, the warp converged: O += w V of a tile and the next tile's scores, half A, then half B, in strict
       // order (left to mix, both halves' MMAs would end together and neither softmax overlap the other); behind an item's
@@ -697,19 +696,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && it.open) {
         const int tiles = it.tiles;
         Item nx{};
-        bool taken = false;
         if (it.two) {
           for (int t = 0; t < tiles; ++t, ++cv) {
             const bool last = t == tiles - 1;
+            if (last) nx = take();                     // (ahead of the waits, beside the softmax)
             ok = ready(bVOk + cv % L::VST, cv / L::VST) && ready(bPFull, np0++) && (t > 0 || room(0));
             if (!ok) break;
             tc_after();
             values(0, t == 0);
             if (last) {
               mma_commit_warp(bar(bODone));
-              nx = take();
-              taken = true;
-              ok = !failed && begin(nx, 0);
+              ok = begin(nx, 0);
             } else {
               ok = keys_there();
               if (ok) scores(0, it.qa, t + 2 == tiles);
@@ -730,6 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {                                       // the halves' tiles in turn
           for (int t = 0; t < tiles; ++t, ++cv) {
             const uint32_t X = t & 1;
+            if (X == 0 && t + 2 >= tiles) nx = take(); // half A's last tile
             ok = ready(bVOk + cv % L::VST, cv / L::VST) && ready(bPFull + X, X ? np1++ : np0++) && (t > 1 || room(X));
             if (!ok) break;
             tc_after();
@@ -743,10 +741,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               continue;
             }
             mma_commit_warp(bar(bODone + X));
-            if (X == 0 && !taken) {                    // half A is free
-              nx = take();
-              taken = true;
-              ok = !failed && begin(nx, 0);
+            if (X == 0) {                              // half A is free
+              ok = begin(nx, 0);
               if (!ok) break;
             }
           }
@@ -759,9 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool f2 = false;
       (void)bar_wait(bar(bDrain), 0, f2);
       __syncwarp();
-    } else {
+    } else if (warp == 14) {
       // ---- the values of tiles that some row does not see in full: what is not finite is taken out ----------------------
-      const int me = warp - 14;
       int cv = 0;
       for (int n = 0;; ++n) {
         const ItemMsg it = next_item(n);
@@ -771,28 +766,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < ntile; ++t, ++cv) {
           if (!wait(bVFull + cv % L::VST, cv / L::VST)) break;
           if (!it.full(it.first_key(t), a.window, a.sinks)) {
-            const uint32_t at = sb + L::V + (cv % L::VST) * L::PIECE + me * (L::PIECE / 2) + lane * 16;
-            bool odd = false;
+            const uint32_t at = sb + L::V + (cv % L::VST) * L::PIECE + lane * 16;
+            uint32_t most = 0u;                        // largest magnitudes: bf16 bits order as integers
 #pragma unroll 1
-            for (int i = 0; i < L::PIECE / 2; i += 512 * 4) {
-              uint4 v[4];
+            for (int i = 0; i < L::PIECE; i += 512 * 8) {
+              uint4 v[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) v[k] = lds128(at + i + 512 * k);
+              for (int k = 0; k < 8; ++k) v[k] = lds128(at + i + 512 * k);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (odd_piece(v[k])) {
-                  odd = true;
-                  uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    if ((u[q] & 0x7F80u) == 0x7F80u) u[q] &= 0xFFFF0000u;
-                    if ((u[q] & 0x7F800000u) == 0x7F800000u) u[q] &= 0xFFFFu;
-                  }
-                  sts128(at + i + 512 * k, u[0], u[1], u[2], u[3]);
-                }
+              for (int k = 0; k < 8; ++k) {
+                most = __vmaxu2(__vmaxu2(most, v[k].x & 0x7FFF7FFFu), v[k].y & 0x7FFF7FFFu);
+                most = __vmaxu2(__vmaxu2(most, v[k].z & 0x7FFF7FFFu), v[k].w & 0x7FFF7FFFu);
+              }
             }
-            if (__any_sync(0xffffffffu, odd)) {
+            if (__any_sync(0xffffffffu, odd_pair(most))) {
               any = true;
+#pragma unroll 1
+              for (int i = 0; i < L::PIECE; i += 512) {
+                const uint4 v = lds128(at + i);
+                uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  if ((u[q] & 0x7F80u) == 0x7F80u) u[q] &= 0xFFFF0000u;
+                  if ((u[q] & 0x7F800000u) == 0x7F800000u) u[q] &= 0xFFFFu;
+                }
+                sts128(at + i, u[0], u[1], u[2], u[3]);
+              }
               fence_async_smem();
             }
           }
@@ -806,6 +805,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+    } else {
+      // ---- values ---------------------------------------------------------------------------
+      int cv = 0;
+      for (int n = 0; !failed; ++n) {
+        const ItemMsg it = next_item(n);
+        if (!it.valid) break;
+        const int ntile = it.ntile;
+        for (int t = 0; t < ntile; ++t, ++cv) {
+          if (cv >= L::VST && !wait(bVFree + cv % L::VST, cv / L::VST - 1)) break;
+          copy(&mv, sb + L::V + (cv % L::VST) * L::PIECE, it.h % L::PER * L::DV, it.h / L::PER, it.k0 + it.first_key(t), bar(bVFull + cv % L::VST));
+        }
+      }
+      // copies still in flight land before the CTA ends
+      bool f2 = false;
+      for (int s = cv >= L::VST ? cv - L::VST : 0; s < cv; ++s) (void)bar_wait(bar(bVFull + s % L::VST), (s / L::VST) & 1, f2);
     }
   }
   if (failed && lane == 0) atomicOr(a.err, kErrTimeout);
@@ -853,12 +867,13 @@ cudaError_t launch_t(const PromptArgs& args, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const long long items = prompt_most_blocks(a) * a.H * L::PER, tiles = a.max_k / kTok + 2 + a.sinks / kTok;
   // items of few tiles are not cut (and need no join)
-  const bool split = tiles > 4 && prompt_splits(a, kTok, kItemCost);
+  // (nor are few of them listed: the list takes 4 us)
   const int sms = prompt_sms();
-  const long long most = split ? (items * (tiles + kItemCost) + kMinSpan - 1) / kMinSpan : items;
+  const int mode = !prompt_splits(a, kTok, kItemCost) || (tiles <= 4 && items <= sms) ? kPromptTurns : tiles > 4 ? kPromptCut : kPromptWhole;
+  const long long most = mode == kPromptCut ? (items * (tiles + kItemCost) + kMinSpan - 1) / kMinSpan : items;
   const int ctas = static_cast<int>(most < sms ? (most < 1 ? 1 : most) : sms);
-  e = launch_pdl(prompt_tc_kernel<D>, dim3(ctas), dim3(kThreads), PS<D>::BYTES, s, a, mq, mk, mv, split ? 1 : 0);
-  if (e != cudaSuccess || !split) return e;
+  e = launch_pdl(prompt_tc_kernel<D>, dim3(ctas), dim3(kThreads), PS<D>::BYTES, s, a, mq, mk, mv, mode);
+  if (e != cudaSuccess || mode != kPromptCut) return e;
   return launch_prompt_join(a, D, false, ctas, L::ROWS, L::PER, s);
 }
 
