@@ -277,6 +277,7 @@ extern "C" tq_status tq_create_ex(const tq_config* cfg, tq_ctx** out) {
         sh[swz(p, j, m)] = hi;
         sl[swz(p, j, m)] = to_f16(static_cast<float>(s[p * d + j] - static_cast<double>(from_f16(hi))));
       }
+  std::vector<uint16_t> ah(static_cast<size_t>(m) * d), al(static_cast<size_t>(m) * d);
   std::vector<float> adf(static_cast<size_t>(m) * d * 2), sdf(static_cast<size_t>(m) * d * 2);
   std::vector<float> wt(static_cast<size_t>(d) * (d + m));   // W = [Pi; S Pi], stored transposed
   for (int r = 0; r < d; ++r)
@@ -286,6 +287,11 @@ extern "C" tq_status tq_create_ex(const tq_config* cfg, tq_ctx** out) {
       double acc = 0.0;
       for (int i = 0; i < d; ++i) acc += s[p * d + i] * pi[i * d + k];   // (S Pi)[p][k]
       wt[static_cast<size_t>(k) * (d + m) + d + p] = static_cast<float>(acc);
+      if (d == kD) {
+        const uint16_t h = to_f16(static_cast<float>(acc));
+        ah[swz(p, k, m)] = h;
+        al[swz(p, k, m)] = to_f16(static_cast<float>(acc - static_cast<double>(from_f16(h))));
+      }
       const float hi = static_cast<float>(acc);
       adf[(p * d + k) * 2] = hi;
       adf[(p * d + k) * 2 + 1] = static_cast<float>(acc - static_cast<double>(hi));
@@ -306,7 +312,9 @@ extern "C" tq_status tq_create_ex(const tq_config* cfg, tq_ctx** out) {
   size_t o_sdf = align256(o_adf + sizeof(float) * d * m * 2);
   size_t o_pidf = align256(o_sdf + sizeof(float) * d * m * 2);
   size_t o_wt = align256(o_pidf + sizeof(float) * d * d * 2);
-  size_t o_err = align256(o_wt + sizeof(float) * d * (d + m));
+  size_t o_ah = align256(o_wt + sizeof(float) * d * (d + m));
+  size_t o_al = align256(o_ah + sizeof(uint16_t) * d * m);
+  size_t o_err = align256(o_al + sizeof(uint16_t) * d * m);
   size_t o_cnt = align256(o_err + sizeof(uint32_t));
   size_t total = align256(o_cnt + 2 * sizeof(unsigned long long));
   void* blk = nullptr;
@@ -326,6 +334,8 @@ extern "C" tq_status tq_create_ex(const tq_config* cfg, tq_ctx** out) {
   ctx->tab.pil_sw = reinterpret_cast<unsigned short*>(b + o_pil);
   ctx->tab.sh_sw = reinterpret_cast<unsigned short*>(b + o_sh);
   ctx->tab.sl_sw = reinterpret_cast<unsigned short*>(b + o_sl);
+  ctx->tab.ah_sw = reinterpret_cast<unsigned short*>(b + o_ah);
+  ctx->tab.al_sw = reinterpret_cast<unsigned short*>(b + o_al);
   ctx->tab.a_df = reinterpret_cast<float*>(b + o_adf);
   ctx->tab.s_df = reinterpret_cast<float*>(b + o_sdf);
   ctx->tab.pi_df = reinterpret_cast<float*>(b + o_pidf);
@@ -341,6 +351,8 @@ extern "C" tq_status tq_create_ex(const tq_config* cfg, tq_ctx** out) {
             cudaMemcpy(ctx->tab.pil_sw, pil.data(), 2 * d * d, cudaMemcpyHostToDevice) == cudaSuccess &&
             cudaMemcpy(ctx->tab.sh_sw, sh.data(), 2 * d * m, cudaMemcpyHostToDevice) == cudaSuccess &&
             cudaMemcpy(ctx->tab.sl_sw, sl.data(), 2 * d * m, cudaMemcpyHostToDevice) == cudaSuccess &&
+            cudaMemcpy(ctx->tab.ah_sw, ah.data(), 2 * d * m, cudaMemcpyHostToDevice) == cudaSuccess &&
+            cudaMemcpy(ctx->tab.al_sw, al.data(), 2 * d * m, cudaMemcpyHostToDevice) == cudaSuccess &&
             cudaMemcpy(ctx->tab.pi_df, pidf.data(), sizeof(float) * d * d * 2, cudaMemcpyHostToDevice) == cudaSuccess &&
             cudaMemcpy(ctx->tab.a_df, adf.data(), sizeof(float) * d * m * 2, cudaMemcpyHostToDevice) == cudaSuccess &&
             cudaMemcpy(ctx->tab.s_df, sdf.data(), sizeof(float) * d * m * 2, cudaMemcpyHostToDevice) == cudaSuccess &&
@@ -1232,7 +1244,8 @@ extern "C" tq_status tq_dequantize(const tq_ctx* ctx, const void* k_cache, const
   a.vc = v_out ? static_cast<const uint8_t*>(v_cache) : nullptr;
   a.k_page_bytes = static_cast<long long>(ctx->kl.block_bytes) * num_kv_heads;
   a.v_page_bytes = static_cast<long long>(ctx->vl.block_bytes) * num_kv_heads;
-  return cuda_status(launch_read(a, ctx->cfg.d, dtype == TQ_F32, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(read_tc_takes(a, ctx->cfg.d) ? launch_read_tc(a, dtype == TQ_F32, s) : launch_read(a, ctx->cfg.d, dtype == TQ_F32, s));
 }
 
 extern "C" tq_status tq_kv8_dequantize(const tq_ctx* ctx, const tq_kv8_cache* cache, tq_dtype dtype, int batch,

@@ -81,6 +81,8 @@ struct DeviceTables {
   unsigned short* pil_sw;   // fp16(Pi - pih)
   unsigned short* sh_sw;    // S rounded to fp16, [m rows][128]
   unsigned short* sl_sw;    // fp16(S - sh)
+  unsigned short* ah_sw;    // S Pi rounded to fp16, [m rows][128], and fp16(S Pi - ah)
+  unsigned short* al_sw;
   float* a_df;              // (S Pi) as double-float pairs [m][128][2]
   float* s_df;              // S as double-float pairs [m][128][2]
   float* pi_df;             // Pi as double-float pairs [128][128][2]

@@ -65,6 +65,8 @@ __device__ __forceinline__ ReadPage read_page(const ReadArgs& a, int b, const Re
 }
 
 cudaError_t launch_read(const ReadArgs& a, int d, bool f32, cudaStream_t s);
+bool read_tc_takes(const ReadArgs& a, int d);
+cudaError_t launch_read_tc(const ReadArgs& a, bool f32, cudaStream_t s);
 cudaError_t launch_kv8_read(const ReadArgs& a, int d, bool f32, cudaStream_t s);
 
 }  // namespace tq

@@ -1,0 +1,537 @@
+// Reading the 2-4-bit cache back on the tensor cores (tcgen05), d = m = 128.
+//
+//   k = n16/sqrt(d) (c[code] Pi) + sqrt(pi/2)/m rho16 (s (S Pi)),   v = n16/sqrt(d) (c[code] Pi)
+// for 128 vectors (eight (page, KV head) blocks) at a time: M = 128 vectors, N = 128 channels, K = 128 codes or signs.  Pi
+// and S Pi stand in shared memory in fp16 (the quantize kernels' table read the other way round, MN-major, and one of its
+// own), the left operands are made from the records in registers: a code picks the two bytes of its centroid by prmt, four
+// codes at a time, for any bit width.  bf16 rows take the fp16 tables (2^-11 of each factor, half a step of bf16 being
+// 2^-8).  fp32 rows take centroids and tables in two fp16 parts each; the large products and the small ones are summed
+// apart, since the tensor cores cut their sums instead of rounding them.
+//
+// Warps 0-7: the operands (two lanes a vector); 8-11: the rows (thread = vector); 12: blocks of records by bulk copies;
+// 13: MMA issue.  Every wait is bounded; a wait that gives up sets the device error word.
+
+#include "tq_read.h"
+#include "tq_tc.cuh"
+#include "tq_tc_attn.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+namespace tq {
+namespace {
+
+using namespace tcx;
+
+constexpr int kThreads = 448;
+constexpr int kVec = 128, kBlocks = kVec / kPage;      // vectors and blocks a tile
+constexpr int kOperand = kVec * 256;                   // bytes of a left operand, and of a table
+constexpr int kRecord = kBlocks * 1344;                // room for a tile's blocks: 16 x (64 code bytes, 16 of signs, two norms)
+constexpr int kRecords = 2, kInfos = 4;
+constexpr int kList = 1024;                            // sequences whose pages are listed without gaps
+
+// Shared memory: tables (bf16 rows: Pi, S Pi; fp32: both parts of each), left operands, records, what the rows need.
+template <bool F32>
+struct RG {
+  static constexpr int TABLES = F32 ? 4 : 2, SLOTS = F32 ? 2 : 4, STAGES = F32 ? 1 : 2;       // STAGES of accumulators
+  static constexpr int A = TABLES * kOperand;
+  static constexpr int REC = A + SLOTS * kOperand;
+  static constexpr int INFO = REC + kRecords * kRecord;            // [kInfos][128] {row factors, row}
+  static constexpr int BLK = INFO + kInfos * kVec * 16;            // [kRecords][8] blocks
+  static constexpr int BAR = BLK + kRecords * kBlocks * 16;
+  static constexpr int LIST = BAR + 8 * 24;                        // pages before each sequence, sums of warps
+  static constexpr int TMEM = LIST + 4 * (kList + 16);
+  static constexpr int BYTES = TMEM + 16;
+};
+static_assert(RG<false>::BYTES <= 232448 && RG<true>::BYTES <= 232448, "shared memory per block");
+enum Bar {
+  bRec = 0, bRecFree = bRec + kRecords, bFull = bRecFree + kRecords, bFree = bFull + 4, bDone = bFree + 4, bTaken = bDone + 2,
+  bInfo = bTaken + 2, bTab = bInfo + kInfos, bDrain, bCount
+};
+static_assert(bCount <= 24, "barriers");
+
+struct alignas(16) BlockInfo {
+  int head, slots, row0, pad;             // slots: first | end << 8 (0: nothing); row0: output row of slot 0
+};
+struct alignas(16) RowInfo {
+  float fa, fb;
+  int row, head;                          // row -1: none
+};
+
+// The two bytes of eight centroids (those of the magnitudes for four bits), as prmt takes them.
+struct Bytes {
+  uint32_t lo0, lo1, hi0, hi1;
+};
+__device__ __forceinline__ Bytes table_bytes(const GroupBook& g, bool low) {
+  uint32_t lo[2] = {0u, 0u}, hi[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int code = g.bits == 4 ? 8 + i : i;
+    float x = 0.0f;
+    if (i < (1 << g.bits)) {
+      const __half h = __float2half_rn(g.c[code]);
+      x = low ? g.c[code] - __half2float(h) : g.c[code];
+    }
+    const uint32_t u = __half_as_ushort(__float2half_rn(x));
+    lo[i >> 2] |= (u & 0xFFu) << (8 * (i & 3));
+    hi[i >> 2] |= (u >> 8) << (8 * (i & 3));
+  }
+  return Bytes{lo[0], lo[1], hi[0], hi[1]};
+}
+// Four codes (nibbles of sel, below 8) as two words of fp16 pairs; sign: their signs in bit 3 of the nibbles of raw.
+template <bool SIGN>
+__device__ __forceinline__ void four_codes(const Bytes& t, uint32_t sel, uint32_t raw, uint32_t& a, uint32_t& b) {
+  const uint32_t lo = prmt(t.lo0, t.lo1, sel);
+  uint32_t hi = prmt(t.hi0, t.hi1, sel);
+  if (SIGN) {
+    uint32_t s = raw & 0x8888u;           // to bit 7 of the bytes
+    s = (s | (s << 8)) & 0x00FF00FFu;
+    s = (s << 4 | s << 8) & 0x80808080u;
+    hi ^= s;
+  }
+  a = prmt(lo, hi, 0x5140);
+  b = prmt(lo, hi, 0x7362);
+}
+// Nibbles of the eight codes (BITS below 4) from their stored bits at the low end of x.
+template <int BITS>
+__device__ __forceinline__ uint32_t nibbles(uint32_t x) {
+  if (BITS == 3) {                        // channels 0-5 in nibbles, 6 and 7 in the spare top bits
+    const uint32_t c6 = ((x >> 3) & 1u) | ((x >> 10) & 2u) | ((x >> 17) & 4u), c7 = ((x >> 7) & 1u) | ((x >> 14) & 2u) | ((x >> 21) & 4u);
+    return (x & 0x00777777u) | (c6 << 24) | (c7 << 28);
+  }
+  if (BITS == 2) {
+    x &= 0xFFFFu;
+    x = (x | (x << 8)) & 0x00FF00FFu;
+    x = (x | (x << 4)) & 0x0F0F0F0Fu;
+    return (x | (x << 2)) & 0x33333333u;
+  }
+  x &= 0xFFu;
+  x = (x | (x << 12)) & 0x000F000Fu;
+  x = (x | (x << 6)) & 0x03030303u;
+  return (x | (x << 3)) & 0x11111111u;
+}
+// 32 channels of a row from its stored words at `src`, to the 16-byte pieces 4 blk .. 4 blk + 3 of row r.
+template <int BITS>
+__device__ __forceinline__ void block32(const Bytes& t, uint32_t src, uint32_t dst, int r, int blk) {
+  uint32_t w[BITS];
+#pragma unroll
+  for (int i = 0; i < BITS; ++i) w[i] = lds32(src + 4u * i);
+#pragma unroll
+  for (int o = 0; o < 4; ++o) {           // eight channels
+    constexpr int kB = 8 * BITS;
+    const int at = kB * o / 32, sh = kB * o % 32;
+    uint32_t x = w[at] >> sh;
+    if (sh + kB > 32 && at + 1 < BITS) x |= w[at + 1] << (32 - sh);
+    uint32_t v[4];
+    if (BITS == 4) {
+      const uint32_t m = x & 0x77777777u;
+      four_codes<true>(t, m & 0xFFFFu, x & 0xFFFFu, v[0], v[1]);
+      four_codes<true>(t, m >> 16, x >> 16, v[2], v[3]);
+    } else {
+      const uint32_t n = nibbles<BITS>(x);
+      four_codes<false>(t, n & 0xFFFFu, 0u, v[0], v[1]);
+      four_codes<false>(t, n >> 16, 0u, v[2], v[3]);
+    }
+    sts128(dst + chunk_off(r, 4 * blk + o, kVec), v[0], v[1], v[2], v[3]);
+  }
+}
+// Eight MMAs of one table: rows of 16 codes (2048 B, 128 descriptor units) against 32 B (2 units) of the left operand.
+__device__ __forceinline__ void mma8_table(uint32_t d, uint32_t a, uint32_t table, bool first) {
+  const uint64_t b = vdesc(table);
+#pragma unroll
+  for (int s = 0; s < 8; ++s) mma_ss_warp(d, kdesc(a, kVec, s), b + 128u * s, idesc_f16(kVec) | (1u << 16), first && s == 0 ? 0u : 1u);
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_constant__ ReadArgs a) {
+  using L = RG<F32>;
+  extern __shared__ __align__(1024) unsigned char sm_raw[];
+  unsigned char* sm = sm_raw;
+  const uint32_t sb = su32(sm);
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  auto bar = [&](int i) { return sb + L::BAR + 8u * static_cast<uint32_t>(i); };
+  BlockInfo* blocks = reinterpret_cast<BlockInfo*>(sm + L::BLK);
+  RowInfo* infos = reinterpret_cast<RowInfo*>(sm + L::INFO);
+  if (sb & 1023u) {                                    // the swizzle's period: the kernel's only shared memory starts on one
+    pdl_wait();
+    if (tid == 0) atomicOr(a.tab.err, kErrLayout);
+    return;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kRecords; ++i) {
+      bar_init(bar(bRec + i), 1);
+      bar_init(bar(bRecFree + i), 8);
+    }
+    for (int i = 0; i < L::SLOTS; ++i) {
+      bar_init(bar(bFull + i), 8);
+      bar_init(bar(bFree + i), 1);
+    }
+    for (int i = 0; i < L::STAGES; ++i) {
+      bar_init(bar(bDone + i), 1);
+      bar_init(bar(bTaken + i), 4);
+    }
+    for (int i = 0; i < kInfos; ++i) bar_init(bar(bInfo + i), 4);
+    bar_init(bar(bTab), 1);
+    bar_init(bar(bDrain), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 13) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + L::TMEM), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  __syncthreads();
+  if (warp == 12 && lane == 0) {                       // the tables (no kernel writes them)
+    bar_arrive_tx(bar(bTab), static_cast<uint32_t>(L::TABLES * kOperand));
+    g2s(sb, a.tab.pih_sw, kOperand, bar(bTab));
+    g2s(sb + kOperand, a.tab.ah_sw, kOperand, bar(bTab));
+    if (F32) {
+      g2s(sb + 2 * kOperand, a.tab.pil_sw, kOperand, bar(bTab));
+      g2s(sb + 3 * kOperand, a.tab.al_sw, kOperand, bar(bTab));
+    }
+  }
+  pdl_wait();
+  // pages before each sequence, where there are not too many of them; else `pages` for each
+  const bool listed = a.batch <= kList;
+  int *s_firsts = reinterpret_cast<int*>(sm + L::LIST), *s_sum = s_firsts + kList;
+  int total = 0;
+  if (listed) {
+    constexpr int kPer = (kList + kThreads - 1) / kThreads;
+    int n[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = tid * kPer + i;
+      n[i] = 0;
+      if (b < a.batch) {
+        const ReadRun r = read_run(a, b);
+        if (r.n > 0) n[i] = (r.start + r.n - 1) / kPage - r.start / kPage + 1;
+      }
+      sum += n[i];
+    }
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      run += lane >= o ? v : 0;
+    }
+    if (lane == 31) s_sum[tid >> 5] = run;
+    __syncthreads();
+    run -= sum;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      run += w < (tid >> 5) ? s_sum[w] : 0;
+      total += s_sum[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (tid * kPer + i < a.batch) s_firsts[tid * kPer + i] = run;
+      run += n[i];
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + L::TMEM);
+  // tiles of keys and of values in turn
+  const long long pages = listed ? total : static_cast<long long>(a.batch) * a.pages;
+  const long long per_kind = (pages * a.H + kBlocks - 1) / kBlocks;
+  const int kinds = (a.kc ? 1 : 0) + (a.vc ? 1 : 0);
+  const long long tiles = per_kind * kinds;
+  auto is_key = [&](long long t) { return kinds == 2 ? t % 2 == 0 : a.kc != nullptr; };
+  bool failed = false;
+  auto wait = [&](int i, int phase) {
+    if (!failed && __all_sync(0xffffffffu, wait_short(bar(i), phase & 1))) return true;
+    failed = true;
+    return false;
+  };
+
+  if (warp < 8) {
+    // ---- left operands: row r of the tile, one half of its channels -------------------------------
+    const int r = 16 * warp + (lane >> 1), part = lane & 1;
+    Bytes book[2][F32 ? 2 : 1][2];                     // [kind][part of the centroid][group]
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        book[k][0][g] = table_bytes((k ? a.vl : a.kl).g[g], false);
+        if (F32) book[k][F32 ? 1 : 0][g] = table_bytes((k ? a.vl : a.kl).g[g], true);
+      }
+    int slot = 0, n = 0;                               // operands and tiles
+    for (long long t = blockIdx.x; t < tiles && !failed; t += gridDim.x, ++n) {
+      const bool key = is_key(t);
+      const KindLayout& K = key ? a.kl : a.vl;
+      const int st = n % kRecords;
+      if (!wait(bRec + st, n / kRecords)) break;
+      const uint32_t rec = sb + L::REC + st * kRecord + (r >> 4) * K.block_bytes;
+      const int s = r & 15;
+      if (n >= kInfos && !wait(bInfo + n % kInfos, n / kInfos - 1)) break;
+      if (part == 0) {
+        const BlockInfo b = blocks[st * kBlocks + (r >> 4)];
+        const bool live = s >= (b.slots & 0xFF) && s < (b.slots >> 8);
+        const float n16 = __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(rec + K.off_norm + 2 * s))));
+        const float r16 = K.qjl ? __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(rec + K.off_rnorm + 2 * s)))) : 0.0f;
+        infos[(n % kInfos) * kVec + r] = RowInfo{n16 * (0.08838834764831845f / kPiScale), r16 * (1.2533141373155003f / 128.0f),
+                                                 live ? b.row0 + s : -1, b.head};
+      }
+      auto open = [&]() {                              // the next operand's room
+        return slot < L::SLOTS || wait(bFree + slot % L::SLOTS, slot / L::SLOTS - 1);
+      };
+      auto close = [&]() {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(bFull + slot % L::SLOTS));
+        ++slot;
+      };
+#pragma unroll
+      for (int low = 0; low < (F32 ? 2 : 1); ++low) {
+        if (!open()) break;
+        const uint32_t dst = sb + L::A + (slot % L::SLOTS) * kOperand;
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          const int blk = 2 * part + q, ch = 32 * blk, g = ch < K.split ? 0 : 1, bits = K.g[g].bits;
+          const uint32_t src = rec + s * K.code_bytes + (g ? (K.split * K.g[0].bits + (ch - K.split) * bits) / 8 : ch * bits / 8);
+          const Bytes& x0 = book[0][low][0];
+          const Bytes& x1 = book[0][low][1];
+          const Bytes& y0 = book[1][low][0];
+          const Bytes& y1 = book[1][low][1];
+          const Bytes tb{key ? (g ? x1.lo0 : x0.lo0) : (g ? y1.lo0 : y0.lo0), key ? (g ? x1.lo1 : x0.lo1) : (g ? y1.lo1 : y0.lo1),
+                         key ? (g ? x1.hi0 : x0.hi0) : (g ? y1.hi0 : y0.hi0), key ? (g ? x1.hi1 : x0.hi1) : (g ? y1.hi1 : y0.hi1)};
+          if (bits == 4) block32<4>(tb, src, dst, r, blk);
+          else if (bits == 3) block32<3>(tb, src, dst, r, blk);
+          else if (bits == 2) block32<2>(tb, src, dst, r, blk);
+          else block32<1>(tb, src, dst, r, blk);
+        }
+        close();
+      }
+      if (failed) break;
+      if (key && K.qjl) {
+        if (!open()) break;
+        const uint32_t dst = sb + L::A + (slot % L::SLOTS) * kOperand;
+        const uint32_t src = rec + K.off_signs + 16 * s + 8 * part;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t w = ~lds32(src + 4 * q);      // a set bit is +1
+#pragma unroll
+          for (int o = 0; o < 4; ++o) {
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t x = w >> (8 * o + 2 * k);
+              v[k] = 0x3C003C00u | ((x << 15) & 0x8000u) | ((x << 30) & 0x80000000u);
+            }
+            sts128(dst + chunk_off(r, 8 * part + 4 * q + o, kVec), v[0], v[1], v[2], v[3]);
+          }
+        }
+        close();
+      }
+      fence_async_smem();                              // the next copy into the room comes behind these reads
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(bRecFree + st));
+    }
+  } else if (warp < 12) {
+    // ---- rows ---------------------------------------------------------------------------------
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.k_out) | reinterpret_cast<uintptr_t>(a.v_out)) & 31) == 0 &&
+                      ((a.k_stride | a.v_stride) & 15) == 0;           // whole sectors per store
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    int n = 0;
+    for (long long t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
+      const bool key = is_key(t), two = key && a.kl.qjl;
+      const int st = n % L::STAGES;
+      if (!wait(bDone + st, n / L::STAGES)) break;
+      tc_after();
+      const RowInfo x = infos[(n % kInfos) * kVec + r];
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(bInfo + n % kInfos));
+      const uint32_t acc = trow + 256u * st;
+      void* out = key ? a.k_out : a.v_out;
+      const long long at = static_cast<long long>(x.row) * (key ? a.k_stride : a.v_stride) + static_cast<long long>(x.head) * 128;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        if (F32) {
+          float p[32];
+          tld32(acc + 32u * c, o);
+          tld32(acc + 128u + 32u * c, p);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = (o[k] + p[k]) * x.fa;
+          if (two) {
+            tld32(acc + 256u + 32u * c, p);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = fmaf(p[k], x.fb, o[k]);
+            tld32(acc + 384u + 32u * c, p);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = fmaf(p[k], x.fb, o[k]);
+          }
+          if (x.row >= 0) {
+            float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + at + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+        } else {
+          tld32(acc + 32u * c, o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] *= x.fa;
+          if (two) {
+            float p[32];
+            tld32(acc + 128u + 32u * c, p);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = fmaf(p[k], x.fb, o[k]);
+          }
+          if (x.row >= 0) {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * k], o[2 * k + 1]);
+              w[k] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(out) + at + 32 * c;
+            if (wide) {
+              stg256(to, w);
+              stg256(to + 16, w + 8);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(to)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            }
+          }
+        }
+        __syncwarp();                                  // lanes with no row wait: the loads are the whole warp's
+      }
+      tc_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(bTaken + st));
+    }
+  } else if (warp == 12) {
+    // ---- records: a lane per block, four tiles looked up at once and ahead of time --------------------
+    struct Found {
+      BlockInfo info;
+      const uint8_t* src;
+    };
+    auto look_up = [&](long long t) {                  // block lane % 8 of tile t
+      Found x{BlockInfo{0, 0, 0, 0}, nullptr};
+      const long long g = (kinds == 2 ? t / 2 : t) * kBlocks + (lane & 7), page = g / a.H;
+      if (t >= tiles || page >= pages) return x;
+      const bool key = is_key(t);
+      int b = 0;
+      if (listed) {                                    // the last sequence whose pages start at or before it
+        int lo = 0, hi = a.batch - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) / 2;
+          if (s_firsts[mid] <= page) lo = mid;
+          else hi = mid - 1;
+        }
+        b = lo;
+      } else {
+        b = static_cast<int>(page / a.pages);
+      }
+      const int i = static_cast<int>(page - (listed ? s_firsts[b] : static_cast<long long>(b) * a.pages));
+      x.info.head = static_cast<int>(g - page * a.H);
+      const ReadRun run = read_run(a, b);
+      const ReadPage p = read_page(a, b, run, i);
+      if (p.id >= 0) {
+        x.info.slots = p.s0 | (p.s1 << 8);
+        x.info.row0 = run.row - p.off;
+        x.src = (key ? a.kc : a.vc) + p.id * (key ? a.k_page_bytes : a.v_page_bytes) +
+                static_cast<long long>(x.info.head) * (key ? a.kl : a.vl).block_bytes;
+      }
+      return x;
+    };
+    int n = 0;
+    Found next = look_up(blockIdx.x + static_cast<long long>(lane >> 3) * gridDim.x);
+    for (long long t4 = blockIdx.x; t4 < tiles && !failed; t4 += 4LL * gridDim.x) {
+      const Found cur = next;
+      next = look_up(t4 + static_cast<long long>(4 + (lane >> 3)) * gridDim.x);
+      __syncwarp();
+      for (int k = 0; k < 4 && t4 + static_cast<long long>(k) * gridDim.x < tiles; ++k, ++n) {
+        const KindLayout& K = is_key(t4 + static_cast<long long>(k) * gridDim.x) ? a.kl : a.vl;
+        const int st = n % kRecords;
+        const bool mine = (lane >> 3) == k;
+        if (n >= kRecords && !wait(bRecFree + st, n / kRecords - 1)) break;
+        if (mine) blocks[st * kBlocks + (lane & 7)] = cur.info;
+        const uint32_t there = __ballot_sync(0xffffffffu, mine && cur.src != nullptr);
+        __syncwarp();
+        if (lane == 0) {
+          if (there) bar_arrive_tx(bar(bRec + st), static_cast<uint32_t>(__popc(there) * K.block_bytes));
+          else bar_arrive(bar(bRec + st));
+        }
+        __syncwarp();
+        if (mine && cur.src) g2s(sb + L::REC + st * kRecord + (lane & 7) * K.block_bytes, cur.src, K.block_bytes, bar(bRec + st));
+      }
+    }
+    // copies still in flight land before the CTA ends
+    bool f2 = false;
+    for (int s = n >= kRecords ? n - kRecords : 0; s < n; ++s) (void)bar_wait(bar(bRec + s % kRecords), (s / kRecords) & 1, f2);
+    (void)bar_wait(bar(bTab), 0, f2);
+    __syncwarp();
+  } else {
+    // ---- MMA issue, the warp converged ------------------------------------------------------------
+    int slot = 0, n = 0;
+    bool ok = tiles > blockIdx.x ? wait(bTab, 0) : false;
+    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++n) {
+      const bool two = is_key(t) && a.kl.qjl;
+      const int st = n % L::STAGES;
+      const uint32_t acc = tmem + 256u * st;
+      ok = n < L::STAGES || wait(bTaken + st, n / L::STAGES - 1);
+      if (!ok) break;
+      auto operand = [&]() {                           // the next left operand
+        const int s = slot % L::SLOTS;
+        ok = wait(bFull + s, slot / L::SLOTS);
+        tc_after();
+        return sb + L::A + s * kOperand;
+      };
+      auto done = [&]() {
+        mma_commit_warp(bar(bFree + slot % L::SLOTS));
+        ++slot;
+      };
+      uint32_t x = operand();
+      if (!ok) break;
+      mma8_table(acc, x, sb, true);
+      if (F32) mma8_table(acc + 128u, x, sb + 2 * kOperand, true);
+      done();
+      if (F32) {
+        x = operand();
+        if (!ok) break;
+        mma8_table(acc + 128u, x, sb, false);
+        done();
+      }
+      if (two) {
+        x = operand();
+        if (!ok) break;
+        mma8_table(acc + (F32 ? 256u : 128u), x, sb + kOperand, true);
+        if (F32) mma8_table(acc + 384u, x, sb + 3 * kOperand, true);
+        done();
+      }
+      mma_commit_warp(bar(bDone + st));
+    }
+    mma_commit_warp(bar(bDrain));                      // every MMA issued completes before the CTA ends
+    bool f2 = false;
+    (void)bar_wait(bar(bDrain), 0, f2);
+    __syncwarp();
+  }
+  if (failed && lane == 0) atomicOr(a.tab.err, kErrTimeout);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+template <bool F32>
+cudaError_t launch_t(const ReadArgs& a, cudaStream_t s) {
+  static std::atomic<unsigned long long> configured{0};
+  const cudaError_t e = smem_attr_once(read_tc_kernel<F32>, RG<F32>::BYTES, configured);
+  if (e != cudaSuccess) return e;
+  const long long tiles = (static_cast<long long>(a.batch) * a.pages * a.H + kBlocks - 1) / kBlocks * ((a.kc ? 1 : 0) + (a.vc ? 1 : 0));
+  const dim3 grid(static_cast<unsigned>(std::min<long long>(tiles, kv8_sm_count())));
+  return launch_pdl(read_tc_kernel<F32>, grid, dim3(kThreads), RG<F32>::BYTES, s, a);
+}
+
+}  // namespace
+
+bool read_tc_takes(const ReadArgs& a, int d) {
+  const auto fits = [](const KindLayout& L) { return L.block_bytes * kBlocks <= kRecord; };
+  return d == kD && a.m == kMaxM && fits(a.kl) && fits(a.vl);
+}
+cudaError_t launch_read_tc(const ReadArgs& a, bool f32, cudaStream_t s) { return f32 ? launch_t<true>(a, s) : launch_t<false>(a, s); }
+
+}  // namespace tq
