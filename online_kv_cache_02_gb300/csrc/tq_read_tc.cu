@@ -5,11 +5,11 @@
 // and S Pi stand in shared memory in fp16 (the quantize kernels' table read the other way round, MN-major, and one of its
 // own), the left operands are made from the records in registers: a code picks the two bytes of its centroid by prmt, four
 // codes at a time, for any bit width.  bf16 rows take the fp16 tables (2^-11 of each factor, half a step of bf16 being
-// 2^-8).  fp32 rows take centroids and tables in two fp16 parts each; the large products and the small ones are summed
-// apart, since the tensor cores cut their sums instead of rounding them.
+// 2^-8).  fp32 rows take centroids and tables in two fp16 parts each; the small products are summed ahead of the
+// large ones, since the tensor cores cut a sum instead of rounding it.
 //
-// Warps 0-7: the operands (two lanes a vector); 8-11: the rows (thread = vector); 12: blocks of records by bulk copies;
-// 13: MMA issue.  Every wait is bounded; a wait that gives up sets the device error word.
+// Warps 0-15: the operands, in two groups that take the tiles in turn (two lanes a vector); 16-19: the rows (thread = vector); 20: blocks of records by bulk copies;
+// 21: MMA issue.  Every wait is bounded; a wait that gives up sets the device error word.
 
 #include "tq_read.h"
 #include "tq_tc.cuh"
@@ -26,32 +26,35 @@ namespace {
 
 using namespace tcx;
 
-constexpr int kThreads = 448;
+constexpr int kMakers = 16, kGroup = 8;                // warps that make operands, and of one group
+constexpr int kThreads = 32 * (kMakers + 6);
 constexpr int kVec = 128, kBlocks = kVec / kPage;      // vectors and blocks a tile
 constexpr int kOperand = kVec * 256;                   // bytes of a left operand, and of a table
 constexpr int kRecord = kBlocks * 1344;                // room for a tile's blocks: 16 x (64 code bytes, 16 of signs, two norms)
-constexpr int kRecords = 2, kInfos = 4;
+constexpr int kInfos = 4;
 constexpr int kList = 1024;                            // sequences whose pages are listed without gaps
 
 // Shared memory: tables (bf16 rows: Pi, S Pi; fp32: both parts of each), left operands, records, what the rows need.
 template <bool F32>
 struct RG {
-  static constexpr int TABLES = F32 ? 4 : 2, SLOTS = F32 ? 2 : 4, STAGES = F32 ? 1 : 2;       // STAGES of accumulators
+  static constexpr int TABLES = F32 ? 4 : 2, SLOTS = F32 ? 2 : 3, STAGES = 2;  // STAGES of accumulators
+  static constexpr int RECORDS = F32 ? 2 : 5;
   static constexpr int A = TABLES * kOperand;
   static constexpr int REC = A + SLOTS * kOperand;
-  static constexpr int INFO = REC + kRecords * kRecord;            // [kInfos][128] {row factors, row}
-  static constexpr int BLK = INFO + kInfos * kVec * 16;            // [kRecords][8] blocks
-  static constexpr int BAR = BLK + kRecords * kBlocks * 16;
-  static constexpr int LIST = BAR + 8 * 24;                        // pages before each sequence, sums of warps
-  static constexpr int TMEM = LIST + 4 * (kList + 16);
+  static constexpr int INFO = REC + RECORDS * kRecord;            // [kInfos][128] {row factors, row}
+  static constexpr int BLK = INFO + kInfos * kVec * 16;            // [RECORDS][8] blocks
+  static constexpr int BAR = BLK + RECORDS * kBlocks * 16;
+  static constexpr int BOOK = BAR + 8 * 28;                        // [kind][part of the centroid][group] bytes for prmt
+  static constexpr int LIST = BOOK + 8 * 16;                       // pages before each sequence, sums of warps
+  static constexpr int TMEM = LIST + 4 * (kList + 32);
   static constexpr int BYTES = TMEM + 16;
 };
 static_assert(RG<false>::BYTES <= 232448 && RG<true>::BYTES <= 232448, "shared memory per block");
 enum Bar {
-  bRec = 0, bRecFree = bRec + kRecords, bFull = bRecFree + kRecords, bFree = bFull + 4, bDone = bFree + 4, bTaken = bDone + 2,
+  bRec = 0, bRecFree = bRec + 5, bFull = bRecFree + 5, bFree = bFull + 4, bDone = bFree + 4, bTaken = bDone + 2,
   bInfo = bTaken + 2, bTab = bInfo + kInfos, bDrain, bCount
 };
-static_assert(bCount <= 24, "barriers");
+static_assert(bCount <= 28, "barriers");
 
 struct alignas(16) BlockInfo {
   int head, slots, row0, pad;             // slots: first | end << 8 (0: nothing); row0: output row of slot 0
@@ -161,12 +164,12 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < kRecords; ++i) {
+    for (int i = 0; i < L::RECORDS; ++i) {
       bar_init(bar(bRec + i), 1);
-      bar_init(bar(bRecFree + i), 8);
+      bar_init(bar(bRecFree + i), kGroup);
     }
     for (int i = 0; i < L::SLOTS; ++i) {
-      bar_init(bar(bFull + i), 8);
+      bar_init(bar(bFull + i), kGroup);
       bar_init(bar(bFree + i), 1);
     }
     for (int i = 0; i < L::STAGES; ++i) {
@@ -178,12 +181,12 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
     bar_init(bar(bDrain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 13) {
+  if (warp == kMakers + 5) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + L::TMEM), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   __syncthreads();
-  if (warp == 12 && lane == 0) {                       // the tables (no kernel writes them)
+  if (warp == kMakers + 4 && lane == 0) {                       // the tables (no kernel writes them)
     bar_arrive_tx(bar(bTab), static_cast<uint32_t>(L::TABLES * kOperand));
     g2s(sb, a.tab.pih_sw, kOperand, bar(bTab));
     g2s(sb + kOperand, a.tab.ah_sw, kOperand, bar(bTab));
@@ -191,6 +194,10 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
       g2s(sb + 2 * kOperand, a.tab.pil_sw, kOperand, bar(bTab));
       g2s(sb + 3 * kOperand, a.tab.al_sw, kOperand, bar(bTab));
     }
+  }
+  if (tid < 8) {
+    const Bytes t = table_bytes((tid & 4 ? a.vl : a.kl).g[tid & 1], (tid & 2) != 0);
+    reinterpret_cast<uint4*>(sm + L::BOOK)[tid] = make_uint4(t.lo0, t.lo1, t.hi0, t.hi1);
   }
   pdl_wait();
   // pages before each sequence, where there are not too many of them; else `pages` for each
@@ -233,12 +240,17 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
   __syncthreads();
   tc_after();
   const uint32_t tmem = *reinterpret_cast<const uint32_t*>(sm + L::TMEM);
-  // tiles of keys and of values in turn
+  // The CTA's tiles, two of keys and two of values in turn (a pair for the two groups).
   const long long pages = listed ? total : static_cast<long long>(a.batch) * a.pages;
   const long long per_kind = (pages * a.H + kBlocks - 1) / kBlocks;
   const int kinds = (a.kc ? 1 : 0) + (a.vc ? 1 : 0);
-  const long long tiles = per_kind * kinds;
-  auto is_key = [&](long long t) { return kinds == 2 ? t % 2 == 0 : a.kc != nullptr; };
+  auto is_key = [&](int n) { return kinds == 2 ? (n & 2) == 0 : a.kc != nullptr; };
+  auto tile_of = [&](int n) {                          // of its kind; per_kind or beyond: nothing
+    const int k = kinds == 2 ? (n >> 2) * 2 + (n & 1) : n;
+    return blockIdx.x + static_cast<long long>(k) * gridDim.x;
+  };
+  const int mine_of_kind = per_kind > blockIdx.x ? static_cast<int>((per_kind - blockIdx.x + gridDim.x - 1) / gridDim.x) : 0;
+  const int count = kinds == 2 ? 2 * (mine_of_kind + (mine_of_kind & 1)) : mine_of_kind;     // (a last one may hold nothing)
   bool failed = false;
   auto wait = [&](int i, int phase) {
     if (!failed && __all_sync(0xffffffffu, wait_short(bar(i), phase & 1))) return true;
@@ -246,23 +258,17 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
     return false;
   };
 
-  if (warp < 8) {
-    // ---- left operands: row r of the tile, one half of its channels -------------------------------
-    const int r = 16 * warp + (lane >> 1), part = lane & 1;
-    Bytes book[2][F32 ? 2 : 1][2];                     // [kind][part of the centroid][group]
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        book[k][0][g] = table_bytes((k ? a.vl : a.kl).g[g], false);
-        if (F32) book[k][F32 ? 1 : 0][g] = table_bytes((k ? a.vl : a.kl).g[g], true);
-      }
-    int slot = 0, n = 0;                               // operands and tiles
-    for (long long t = blockIdx.x; t < tiles && !failed; t += gridDim.x, ++n) {
-      const bool key = is_key(t);
+  if (warp < kMakers) {
+    // ---- left operands: row r of the tile, half of its channels (eight rows' pieces of 16 bytes fill the banks) ------------
+    const int group = warp / kGroup, r = 16 * (warp % kGroup) + (lane & 15), part = lane >> 4;
+    int slot = 0;                                      // operands, of both groups
+    auto operands = [&](int n) { return (F32 ? 2 : 1) + (is_key(n) && a.kl.qjl ? 1 : 0); };
+    if (group) slot = count ? operands(0) : 0;
+    for (int n = group; n < count && !failed; n += 2) {
+      const bool key = is_key(n);
       const KindLayout& K = key ? a.kl : a.vl;
-      const int st = n % kRecords;
-      if (!wait(bRec + st, n / kRecords)) break;
+      const int st = n % L::RECORDS;
+      if (!wait(bRec + st, n / L::RECORDS)) break;
       const uint32_t rec = sb + L::REC + st * kRecord + (r >> 4) * K.block_bytes;
       const int s = r & 15;
       if (n >= kInfos && !wait(bInfo + n % kInfos, n / kInfos - 1)) break;
@@ -283,35 +289,34 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
         if (lane == 0) bar_arrive(bar(bFull + slot % L::SLOTS));
         ++slot;
       };
-#pragma unroll
-      for (int low = 0; low < (F32 ? 2 : 1); ++low) {
-        if (!open()) break;
-        const uint32_t dst = sb + L::A + (slot % L::SLOTS) * kOperand;
+      {
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          const int blk = 2 * part + q, ch = 32 * blk, g = ch < K.split ? 0 : 1, bits = K.g[g].bits;
-          const uint32_t src = rec + s * K.code_bytes + (g ? (K.split * K.g[0].bits + (ch - K.split) * bits) / 8 : ch * bits / 8);
-          const Bytes& x0 = book[0][low][0];
-          const Bytes& x1 = book[0][low][1];
-          const Bytes& y0 = book[1][low][0];
-          const Bytes& y1 = book[1][low][1];
-          const Bytes tb{key ? (g ? x1.lo0 : x0.lo0) : (g ? y1.lo0 : y0.lo0), key ? (g ? x1.lo1 : x0.lo1) : (g ? y1.lo1 : y0.lo1),
-                         key ? (g ? x1.hi0 : x0.hi0) : (g ? y1.hi0 : y0.hi0), key ? (g ? x1.hi1 : x0.hi1) : (g ? y1.hi1 : y0.hi1)};
-          if (bits == 4) block32<4>(tb, src, dst, r, blk);
-          else if (bits == 3) block32<3>(tb, src, dst, r, blk);
-          else if (bits == 2) block32<2>(tb, src, dst, r, blk);
-          else block32<1>(tb, src, dst, r, blk);
+        for (int low = F32 ? 1 : 0; low >= 0; --low) {  // (the small products first)
+          if (!open()) break;
+          const uint32_t dst = sb + L::A + (slot % L::SLOTS) * kOperand;
+#pragma unroll 1
+          for (int blk = 2 * part; blk < 2 * part + 2; ++blk) {
+            const int ch = 32 * blk, g = ch < K.split ? 0 : 1, bits = K.g[g].bits;
+            const uint32_t src = rec + s * K.code_bytes + (g ? (K.split * K.g[0].bits + (ch - K.split) * bits) / 8 : ch * bits / 8);
+            const uint4 u = lds128(sb + L::BOOK + 16 * ((key ? 0 : 4) + 2 * low + g));
+            const Bytes tb{u.x, u.y, u.z, u.w};
+            if (bits == 4) block32<4>(tb, src, dst, r, blk);
+            else if (bits == 3) block32<3>(tb, src, dst, r, blk);
+            else if (bits == 2) block32<2>(tb, src, dst, r, blk);
+            else block32<1>(tb, src, dst, r, blk);
+          }
+          __syncwarp();
+          close();
         }
-        close();
       }
       if (failed) break;
       if (key && K.qjl) {
         if (!open()) break;
         const uint32_t dst = sb + L::A + (slot % L::SLOTS) * kOperand;
-        const uint32_t src = rec + K.off_signs + 16 * s + 8 * part;
+        const uint2 two = lds64(rec + K.off_signs + 16 * s + 8 * part);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const uint32_t w = ~lds32(src + 4 * q);      // a set bit is +1
+          const uint32_t w = ~(q ? two.y : two.x);     // a set bit is +1
 #pragma unroll
           for (int o = 0; o < 4; ++o) {
             uint32_t v[4];
@@ -328,16 +333,16 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
       fence_async_smem();                              // the next copy into the room comes behind these reads
       __syncwarp();
       if (lane == 0) bar_arrive(bar(bRecFree + st));
+      if (n + 1 < count) slot += operands(n + 1);      // the other group's
     }
-  } else if (warp < 12) {
+  } else if (warp < kMakers + 4) {
     // ---- rows ---------------------------------------------------------------------------------
     const bool wide = ((reinterpret_cast<uintptr_t>(a.k_out) | reinterpret_cast<uintptr_t>(a.v_out)) & 31) == 0 &&
                       ((a.k_stride | a.v_stride) & 15) == 0;           // whole sectors per store
     const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    int n = 0;
-    for (long long t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
-      const bool key = is_key(t), two = key && a.kl.qjl;
+    for (int n = 0; n < count; ++n) {
+      const bool key = is_key(n), two = key && a.kl.qjl;
       const int st = n % L::STAGES;
       if (!wait(bDone + st, n / L::STAGES)) break;
       tc_after();
@@ -350,35 +355,22 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         float o[32];
-        if (F32) {
+        tld32(acc + 32u * c, o);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] *= x.fa;
+        if (two) {
           float p[32];
-          tld32(acc + 32u * c, o);
           tld32(acc + 128u + 32u * c, p);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = (o[k] + p[k]) * x.fa;
-          if (two) {
-            tld32(acc + 256u + 32u * c, p);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = fmaf(p[k], x.fb, o[k]);
-            tld32(acc + 384u + 32u * c, p);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = fmaf(p[k], x.fb, o[k]);
-          }
+          for (int k = 0; k < 32; ++k) o[k] = fmaf(p[k], x.fb, o[k]);
+        }
+        if (F32) {
           if (x.row >= 0) {
             float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + at + 32 * c);
 #pragma unroll
             for (int k = 0; k < 8; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         } else {
-          tld32(acc + 32u * c, o);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] *= x.fa;
-          if (two) {
-            float p[32];
-            tld32(acc + 128u + 32u * c, p);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = fmaf(p[k], x.fb, o[k]);
-          }
           if (x.row >= 0) {
             uint32_t w[16];
 #pragma unroll
@@ -402,17 +394,17 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) bar_arrive(bar(bTaken + st));
     }
-  } else if (warp == 12) {
+  } else if (warp == kMakers + 4) {
     // ---- records: a lane per block, four tiles looked up at once and ahead of time --------------------
     struct Found {
       BlockInfo info;
       const uint8_t* src;
     };
-    auto look_up = [&](long long t) {                  // block lane % 8 of tile t
+    auto look_up = [&](int m) {                        // block lane % 8 of the CTA's tile m
       Found x{BlockInfo{0, 0, 0, 0}, nullptr};
-      const long long g = (kinds == 2 ? t / 2 : t) * kBlocks + (lane & 7), page = g / a.H;
-      if (t >= tiles || page >= pages) return x;
-      const bool key = is_key(t);
+      const long long g = tile_of(m) * kBlocks + (lane & 7), page = g / a.H;
+      if (m >= count || page >= pages) return x;
+      const bool key = is_key(m);
       int b = 0;
       if (listed) {                                    // the last sequence whose pages start at or before it
         int lo = 0, hi = a.batch - 1;
@@ -438,16 +430,16 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
       return x;
     };
     int n = 0;
-    Found next = look_up(blockIdx.x + static_cast<long long>(lane >> 3) * gridDim.x);
-    for (long long t4 = blockIdx.x; t4 < tiles && !failed; t4 += 4LL * gridDim.x) {
+    Found next = look_up(lane >> 3);
+    while (n < count && !failed) {
       const Found cur = next;
-      next = look_up(t4 + static_cast<long long>(4 + (lane >> 3)) * gridDim.x);
+      next = look_up(n + 4 + (lane >> 3));
       __syncwarp();
-      for (int k = 0; k < 4 && t4 + static_cast<long long>(k) * gridDim.x < tiles; ++k, ++n) {
-        const KindLayout& K = is_key(t4 + static_cast<long long>(k) * gridDim.x) ? a.kl : a.vl;
-        const int st = n % kRecords;
+      for (int k = 0; k < 4 && n < count; ++k, ++n) {
+        const KindLayout& K = is_key(n) ? a.kl : a.vl;
+        const int st = n % L::RECORDS;
         const bool mine = (lane >> 3) == k;
-        if (n >= kRecords && !wait(bRecFree + st, n / kRecords - 1)) break;
+        if (n >= L::RECORDS && !wait(bRecFree + st, n / L::RECORDS - 1)) break;
         if (mine) blocks[st * kBlocks + (lane & 7)] = cur.info;
         const uint32_t there = __ballot_sync(0xffffffffu, mine && cur.src != nullptr);
         __syncwarp();
@@ -461,15 +453,15 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
     }
     // copies still in flight land before the CTA ends
     bool f2 = false;
-    for (int s = n >= kRecords ? n - kRecords : 0; s < n; ++s) (void)bar_wait(bar(bRec + s % kRecords), (s / kRecords) & 1, f2);
+    for (int s = n >= L::RECORDS ? n - L::RECORDS : 0; s < n; ++s) (void)bar_wait(bar(bRec + s % L::RECORDS), (s / L::RECORDS) & 1, f2);
     (void)bar_wait(bar(bTab), 0, f2);
     __syncwarp();
   } else {
     // ---- MMA issue, the warp converged ------------------------------------------------------------
-    int slot = 0, n = 0;
-    bool ok = tiles > blockIdx.x ? wait(bTab, 0) : false;
-    for (long long t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++n) {
-      const bool two = is_key(t) && a.kl.qjl;
+    int slot = 0;
+    bool ok = count ? wait(bTab, 0) : false;
+    for (int n = 0; ok && n < count; ++n) {
+      const bool two = is_key(n) && a.kl.qjl;
       const int st = n % L::STAGES;
       const uint32_t acc = tmem + 256u * st;
       ok = n < L::STAGES || wait(bTaken + st, n / L::STAGES - 1);
@@ -487,19 +479,19 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
       uint32_t x = operand();
       if (!ok) break;
       mma8_table(acc, x, sb, true);
-      if (F32) mma8_table(acc + 128u, x, sb + 2 * kOperand, true);
       done();
-      if (F32) {
+      if (F32) {                                       // (that was the centroids' low part)
         x = operand();
         if (!ok) break;
-        mma8_table(acc + 128u, x, sb, false);
+        mma8_table(acc, x, sb + 2 * kOperand, false);
+        mma8_table(acc, x, sb, false);
         done();
       }
       if (two) {
         x = operand();
         if (!ok) break;
-        mma8_table(acc + (F32 ? 256u : 128u), x, sb + kOperand, true);
-        if (F32) mma8_table(acc + 384u, x, sb + 3 * kOperand, true);
+        if (F32) mma8_table(acc + 128u, x, sb + 3 * kOperand, true);
+        mma8_table(acc + 128u, x, sb + kOperand, !F32);
         done();
       }
       mma_commit_warp(bar(bDone + st));
@@ -513,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  if (warp == kMakers + 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 template <bool F32>
