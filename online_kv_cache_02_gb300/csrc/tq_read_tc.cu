@@ -3,13 +3,16 @@
 //   k = n16/sqrt(d) (c[code] Pi) + sqrt(pi/2)/m rho16 (s (S Pi)),   v = n16/sqrt(d) (c[code] Pi)
 // for 128 vectors (eight (page, KV head) blocks) at a time: M = 128 vectors, N = 128 channels, K = 128 codes or signs.  Pi
 // and S Pi stand in shared memory in fp16 (the quantize kernels' table read the other way round, MN-major, and one of its
-// own), the left operands are made from the records in registers: a code picks the two bytes of its centroid by prmt, four
-// codes at a time, for any bit width.  bf16 rows take the fp16 tables (2^-11 of each factor, half a step of bf16 being
-// 2^-8).  fp32 rows take centroids and tables in two fp16 parts each; the small products are summed ahead of the
-// large ones, since the tensor cores cut a sum instead of rounding it.
+// own); the left operands are made from the records in registers, a code picking the two bytes of its centroid by prmt, four
+// codes at a time, for any bit width, and go to tensor memory (in shared memory they would take half of its bandwidth).
+// bf16 rows take the fp16 tables (2^-11 of each factor, half a step of bf16 being 2^-8), and both products one sum: a row's
+// larger factor is applied at the end, the other operand is scaled by their ratio.  fp32 rows take centroids and tables in
+// two fp16 parts each; the two products are summed apart, the small parts ahead of the large ones, since the tensor cores
+// cut a sum instead of rounding it.  Rows leave through shared memory as bulk copies.
 //
-// Warps 0-15: the operands, in two groups that take the tiles in turn (two lanes a vector); 16-19: the rows (thread = vector); 20: blocks of records by bulk copies;
-// 21: MMA issue.  Every wait is bounded; a wait that gives up sets the device error word.
+// Warps 0-15: the operands, in two groups that take the tiles in turn (thread = vector and half of its channels); 16-19: the
+// rows (thread = vector); 20: blocks of records by bulk copies; 21: MMA issue.  Every wait is bounded; a wait that gives up
+// sets the device error word.
 
 #include "tq_read.h"
 #include "tq_tc.cuh"
@@ -29,25 +32,28 @@ using namespace tcx;
 constexpr int kMakers = 16, kGroup = 8;                // warps that make operands, and of one group
 constexpr int kThreads = 32 * (kMakers + 6);
 constexpr int kVec = 128, kBlocks = kVec / kPage;      // vectors and blocks a tile
-constexpr int kOperand = kVec * 256;                   // bytes of a left operand, and of a table
+constexpr int kTable = 128 * 256;                      // bytes of a table
 constexpr int kRecord = kBlocks * 1344;                // room for a tile's blocks: 16 x (64 code bytes, 16 of signs, two norms)
 constexpr int kInfos = 4;
-constexpr int kList = 1024;                            // sequences whose pages are listed without gaps
+constexpr int kList = 512;                             // sequences whose pages are listed without gaps
 
-// Shared memory: tables (bf16 rows: Pi, S Pi; fp32: both parts of each), left operands, records, what the rows need.
+// Shared memory: tables (bf16 rows: Pi, S Pi; fp32: both parts of each), records, rows on their way out.  Tensor memory:
+// STAGES of accumulators, then four left operands.
 template <bool F32>
 struct RG {
-  static constexpr int TABLES = F32 ? 4 : 2, SLOTS = F32 ? 2 : 3, STAGES = 2;  // STAGES of accumulators
-  static constexpr int RECORDS = F32 ? 2 : 5;
-  static constexpr int A = TABLES * kOperand;
-  static constexpr int REC = A + SLOTS * kOperand;
-  static constexpr int INFO = REC + RECORDS * kRecord;            // [kInfos][128] {row factors, row}
+  static constexpr int TABLES = F32 ? 4 : 2, SLOTS = 4, STAGES = F32 ? 1 : 2, ACC = F32 ? 256 : 128;
+  static constexpr int RECORDS = F32 ? 2 : 5, OUTS = F32 ? 1 : 2;
+  static constexpr int ROW = (F32 ? 512 : 256) + 16;               // bytes from row to row: the banks in turn
+  static constexpr int REC = TABLES * kTable;
+  static constexpr int OUT = REC + RECORDS * kRecord;              // [OUTS][128]
+  static constexpr int INFO = OUT + OUTS * kVec * ROW;             // [kInfos][128] {row factors, row}
   static constexpr int BLK = INFO + kInfos * kVec * 16;            // [RECORDS][8] blocks
   static constexpr int BAR = BLK + RECORDS * kBlocks * 16;
   static constexpr int BOOK = BAR + 8 * 28;                        // [kind][part of the centroid][group] bytes for prmt
   static constexpr int LIST = BOOK + 8 * 16;                       // pages before each sequence, sums of warps
   static constexpr int TMEM = LIST + 4 * (kList + 32);
   static constexpr int BYTES = TMEM + 16;
+  static constexpr uint32_t A = 256;                               // first column of the left operands
 };
 static_assert(RG<false>::BYTES <= 232448 && RG<true>::BYTES <= 232448, "shared memory per block");
 enum Bar {
@@ -116,9 +122,9 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t x) {
   x = (x | (x << 6)) & 0x03030303u;
   return (x | (x << 3)) & 0x11111111u;
 }
-// 32 channels of a row from its stored words at `src`, to the 16-byte pieces 4 blk .. 4 blk + 3 of row r.
+// 32 channels of a row from its stored words at `src`, as fp16 pairs.
 template <int BITS>
-__device__ __forceinline__ void block32(const Bytes& t, uint32_t src, uint32_t dst, int r, int blk) {
+__device__ __forceinline__ void block32(const Bytes& t, uint32_t src, uint32_t* v) {
   uint32_t w[BITS];
 #pragma unroll
   for (int i = 0; i < BITS; ++i) w[i] = lds32(src + 4u * i);
@@ -128,24 +134,31 @@ __device__ __forceinline__ void block32(const Bytes& t, uint32_t src, uint32_t d
     const int at = kB * o / 32, sh = kB * o % 32;
     uint32_t x = w[at] >> sh;
     if (sh + kB > 32 && at + 1 < BITS) x |= w[at + 1] << (32 - sh);
-    uint32_t v[4];
     if (BITS == 4) {
       const uint32_t m = x & 0x77777777u;
-      four_codes<true>(t, m & 0xFFFFu, x & 0xFFFFu, v[0], v[1]);
-      four_codes<true>(t, m >> 16, x >> 16, v[2], v[3]);
+      four_codes<true>(t, m & 0xFFFFu, x & 0xFFFFu, v[4 * o], v[4 * o + 1]);
+      four_codes<true>(t, m >> 16, x >> 16, v[4 * o + 2], v[4 * o + 3]);
     } else {
       const uint32_t n = nibbles<BITS>(x);
-      four_codes<false>(t, n & 0xFFFFu, 0u, v[0], v[1]);
-      four_codes<false>(t, n >> 16, 0u, v[2], v[3]);
+      four_codes<false>(t, n & 0xFFFFu, 0u, v[4 * o], v[4 * o + 1]);
+      four_codes<false>(t, n >> 16, 0u, v[4 * o + 2], v[4 * o + 3]);
     }
-    sts128(dst + chunk_off(r, 4 * blk + o, kVec), v[0], v[1], v[2], v[3]);
   }
 }
-// Eight MMAs of one table: rows of 16 codes (2048 B, 128 descriptor units) against 32 B (2 units) of the left operand.
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, __half2 b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Eight MMAs of one table: rows of 16 codes (2048 B, 128 descriptor units) against 8 columns of the left operand.
 __device__ __forceinline__ void mma8_table(uint32_t d, uint32_t a, uint32_t table, bool first) {
-  const uint64_t b = vdesc(table);
-#pragma unroll
-  for (int s = 0; s < 8; ++s) mma_ss_warp(d, kdesc(a, kVec, s), b + 128u * s, idesc_f16(kVec) | (1u << 16), first && s == 0 ? 0u : 1u);
+  mma8_values(d, a, vdesc(table), idesc_f16(kVec) | (1u << 16), first ? 0u : 1u);
+}
+__device__ __forceinline__ void bulk_row(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void bulk_read() {          // this thread's groups but LEFT have been read from shared memory
+  asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
 }
 
 template <bool F32>
@@ -187,12 +200,12 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
   }
   __syncthreads();
   if (warp == kMakers + 4 && lane == 0) {                       // the tables (no kernel writes them)
-    bar_arrive_tx(bar(bTab), static_cast<uint32_t>(L::TABLES * kOperand));
-    g2s(sb, a.tab.pih_sw, kOperand, bar(bTab));
-    g2s(sb + kOperand, a.tab.ah_sw, kOperand, bar(bTab));
+    bar_arrive_tx(bar(bTab), static_cast<uint32_t>(L::TABLES * kTable));
+    g2s(sb, a.tab.pih_sw, kTable, bar(bTab));
+    g2s(sb + kTable, a.tab.ah_sw, kTable, bar(bTab));
     if (F32) {
-      g2s(sb + 2 * kOperand, a.tab.pil_sw, kOperand, bar(bTab));
-      g2s(sb + 3 * kOperand, a.tab.al_sw, kOperand, bar(bTab));
+      g2s(sb + 2 * kTable, a.tab.pil_sw, kTable, bar(bTab));
+      g2s(sb + 3 * kTable, a.tab.al_sw, kTable, bar(bTab));
     }
   }
   if (tid < 8) {
@@ -259,8 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
   };
 
   if (warp < kMakers) {
-    // ---- left operands: row r of the tile, half of its channels (eight rows' pieces of 16 bytes fill the banks) ------------
-    const int group = warp / kGroup, r = 16 * (warp % kGroup) + (lane & 15), part = lane >> 4;
+    // ---- left operands: row r of the tile, half of its channels --------------------------------------
+    const int group = warp / kGroup, part = (warp >> 2) & 1, r = 32 * (warp & 3) + lane;
+    const uint32_t ta = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + L::A + 32u * part;
     int slot = 0;                                      // operands, of both groups
     auto operands = [&](int n) { return (F32 ? 2 : 1) + (is_key(n) && a.kl.qjl ? 1 : 0); };
     if (group) slot = count ? operands(0) : 0;
@@ -272,63 +286,70 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
       const uint32_t rec = sb + L::REC + st * kRecord + (r >> 4) * K.block_bytes;
       const int s = r & 15;
       if (n >= kInfos && !wait(bInfo + n % kInfos, n / kInfos - 1)) break;
+      const float n16 = __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(rec + K.off_norm + 2 * s))));
+      const float r16 = K.qjl ? __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(rec + K.off_rnorm + 2 * s)))) : 0.0f;
+      const float fa = n16 * (0.08838834764831845f / kPiScale), fb = r16 * (1.2533141373155003f / 128.0f);
+      const float f = F32 ? fa : fmaxf(fabsf(fa), fabsf(fb)), inv = f > 0.0f ? 1.0f / f : 0.0f;
       if (part == 0) {
         const BlockInfo b = blocks[st * kBlocks + (r >> 4)];
         const bool live = s >= (b.slots & 0xFF) && s < (b.slots >> 8);
-        const float n16 = __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(rec + K.off_norm + 2 * s))));
-        const float r16 = K.qjl ? __half2float(__ushort_as_half(static_cast<unsigned short>(lds16(rec + K.off_rnorm + 2 * s)))) : 0.0f;
-        infos[(n % kInfos) * kVec + r] = RowInfo{n16 * (0.08838834764831845f / kPiScale), r16 * (1.2533141373155003f / 128.0f),
-                                                 live ? b.row0 + s : -1, b.head};
+        // (a norm that is not finite spoils its row)
+        infos[(n % kInfos) * kVec + r] = RowInfo{f + (fa - fa) + (fb - fb), fb, live ? b.row0 + s : -1, b.head};
       }
       auto open = [&]() {                              // the next operand's room
-        return slot < L::SLOTS || wait(bFree + slot % L::SLOTS, slot / L::SLOTS - 1);
+        if (slot >= L::SLOTS && !wait(bFree + slot % L::SLOTS, slot / L::SLOTS - 1)) return false;
+        tc_after();
+        return true;
       };
-      auto close = [&]() {
-        fence_async_smem();
+      auto close = [&](const uint32_t (&v)[32]) {
+        tst32(ta + 64u * static_cast<uint32_t>(slot % L::SLOTS), v);
+        tst_wait();
+        tc_before();
         __syncwarp();
         if (lane == 0) bar_arrive(bar(bFull + slot % L::SLOTS));
         ++slot;
       };
-      {
 #pragma unroll 1
-        for (int low = F32 ? 1 : 0; low >= 0; --low) {  // (the small products first)
-          if (!open()) break;
-          const uint32_t dst = sb + L::A + (slot % L::SLOTS) * kOperand;
-#pragma unroll 1
-          for (int blk = 2 * part; blk < 2 * part + 2; ++blk) {
-            const int ch = 32 * blk, g = ch < K.split ? 0 : 1, bits = K.g[g].bits;
-            const uint32_t src = rec + s * K.code_bytes + (g ? (K.split * K.g[0].bits + (ch - K.split) * bits) / 8 : ch * bits / 8);
-            const uint4 u = lds128(sb + L::BOOK + 16 * ((key ? 0 : 4) + 2 * low + g));
-            const Bytes tb{u.x, u.y, u.z, u.w};
-            if (bits == 4) block32<4>(tb, src, dst, r, blk);
-            else if (bits == 3) block32<3>(tb, src, dst, r, blk);
-            else if (bits == 2) block32<2>(tb, src, dst, r, blk);
-            else block32<1>(tb, src, dst, r, blk);
-          }
-          __syncwarp();
-          close();
+      for (int low = F32 ? 1 : 0; low >= 0; --low) {   // (the small products first)
+        uint32_t v[32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int ch = 64 * part + 32 * q, g = ch < K.split ? 0 : 1, bits = K.g[g].bits;
+          const uint32_t src = rec + s * K.code_bytes + (g ? (K.split * K.g[0].bits + (ch - K.split) * bits) / 8 : ch * bits / 8);
+          const uint4 u = lds128(sb + L::BOOK + 16 * ((key ? 0 : 4) + 2 * low + g));
+          const Bytes tb{u.x, u.y, u.z, u.w};
+          if (bits == 4) block32<4>(tb, src, v + 16 * q);
+          else if (bits == 3) block32<3>(tb, src, v + 16 * q);
+          else if (bits == 2) block32<2>(tb, src, v + 16 * q);
+          else block32<1>(tb, src, v + 16 * q);
         }
+        if (!F32 && key && K.qjl) {
+          const __half2 ra = __float2half2_rn(fa * inv);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = mul_half2(v[k], ra);
+        }
+        __syncwarp();
+        if (!open()) break;
+        close(v);
       }
       if (failed) break;
       if (key && K.qjl) {
-        if (!open()) break;
-        const uint32_t dst = sb + L::A + (slot % L::SLOTS) * kOperand;
         const uint2 two = lds64(rec + K.off_signs + 16 * s + 8 * part);
+        const __half2 rb = __float2half2_rn(F32 ? 1.0f : fb * inv);
+        const uint32_t one = *reinterpret_cast<const uint32_t*>(&rb);
+        uint32_t v[32];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const uint32_t w = ~(q ? two.y : two.x);     // a set bit is +1
 #pragma unroll
-          for (int o = 0; o < 4; ++o) {
-            uint32_t v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t x = w >> (8 * o + 2 * k);
-              v[k] = 0x3C003C00u | ((x << 15) & 0x8000u) | ((x << 30) & 0x80000000u);
-            }
-            sts128(dst + chunk_off(r, 8 * part + 4 * q + o, kVec), v[0], v[1], v[2], v[3]);
+          for (int k = 0; k < 16; ++k) {
+            const uint32_t x = w >> (2 * k);
+            v[16 * q + k] = one ^ ((x << 15) & 0x8000u) ^ ((x << 30) & 0x80000000u);
           }
         }
-        close();
+        __syncwarp();
+        if (!open()) break;
+        close(v);
       }
       fence_async_smem();                              // the next copy into the room comes behind these reads
       __syncwarp();
@@ -336,22 +357,20 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
       if (n + 1 < count) slot += operands(n + 1);      // the other group's
     }
   } else if (warp < kMakers + 4) {
-    // ---- rows ---------------------------------------------------------------------------------
-    const bool wide = ((reinterpret_cast<uintptr_t>(a.k_out) | reinterpret_cast<uintptr_t>(a.v_out)) & 31) == 0 &&
-                      ((a.k_stride | a.v_stride) & 15) == 0;           // whole sectors per store
+    // ---- rows: through shared memory, a bulk copy each ---------------------------------------------
     const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     for (int n = 0; n < count; ++n) {
-      const bool key = is_key(n), two = key && a.kl.qjl;
+      const bool key = is_key(n), two = F32 && key && a.kl.qjl;
       const int st = n % L::STAGES;
       if (!wait(bDone + st, n / L::STAGES)) break;
       tc_after();
       const RowInfo x = infos[(n % kInfos) * kVec + r];
       __syncwarp();
       if (lane == 0) bar_arrive(bar(bInfo + n % kInfos));
-      const uint32_t acc = trow + 256u * st;
-      void* out = key ? a.k_out : a.v_out;
-      const long long at = static_cast<long long>(x.row) * (key ? a.k_stride : a.v_stride) + static_cast<long long>(x.head) * 128;
+      const uint32_t acc = trow + static_cast<uint32_t>(L::ACC * st);
+      const uint32_t to = sb + L::OUT + (n % L::OUTS) * (kVec * L::ROW) + r * L::ROW;
+      bulk_read<L::OUTS - 1>();                        // the copy that was there
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         float o[32];
@@ -365,35 +384,32 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
           for (int k = 0; k < 32; ++k) o[k] = fmaf(p[k], x.fb, o[k]);
         }
         if (F32) {
-          if (x.row >= 0) {
-            float4* to = reinterpret_cast<float4*>(static_cast<float*>(out) + at + 32 * c);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) to[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          }
+          for (int k = 0; k < 8; ++k)
+            sts128(to + 128u * c + 16u * k, __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
         } else {
-          if (x.row >= 0) {
-            uint32_t w[16];
+          uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * k], o[2 * k + 1]);
-              w[k] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(out) + at + 32 * c;
-            if (wide) {
-              stg256(to, w);
-              stg256(to + 16, w + 8);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(to)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-            }
+          for (int k = 0; k < 16; ++k) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(o[2 * k], o[2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t*>(&y);
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sts128(to + 64u * c + 16u * k, w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         }
-        __syncwarp();                                  // lanes with no row wait: the loads are the whole warp's
       }
       tc_before();
+      fence_async_smem();
       __syncwarp();
       if (lane == 0) bar_arrive(bar(bTaken + st));
+      if (x.row >= 0) {
+        constexpr int kE = F32 ? 4 : 2;
+        const long long at = static_cast<long long>(x.row) * (key ? a.k_stride : a.v_stride) + static_cast<long long>(x.head) * 128;
+        bulk_row(static_cast<char*>(key ? a.k_out : a.v_out) + at * kE, to, 128 * kE);
+      }
+      __syncwarp();
     }
+    asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (warp == kMakers + 4) {
     // ---- records: a lane per block, four tiles looked up at once and ahead of time --------------------
     struct Found {
@@ -463,14 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
     for (int n = 0; ok && n < count; ++n) {
       const bool two = is_key(n) && a.kl.qjl;
       const int st = n % L::STAGES;
-      const uint32_t acc = tmem + 256u * st;
+      const uint32_t acc = tmem + static_cast<uint32_t>(L::ACC * st);
       ok = n < L::STAGES || wait(bTaken + st, n / L::STAGES - 1);
       if (!ok) break;
       auto operand = [&]() {                           // the next left operand
         const int s = slot % L::SLOTS;
         ok = wait(bFull + s, slot / L::SLOTS);
         tc_after();
-        return sb + L::A + s * kOperand;
+        return tmem + L::A + 64u * static_cast<uint32_t>(s);
       };
       auto done = [&]() {
         mma_commit_warp(bar(bFree + slot % L::SLOTS));
@@ -483,15 +499,15 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
       if (F32) {                                       // (that was the centroids' low part)
         x = operand();
         if (!ok) break;
-        mma8_table(acc, x, sb + 2 * kOperand, false);
+        mma8_table(acc, x, sb + 2 * kTable, false);
         mma8_table(acc, x, sb, false);
         done();
       }
       if (two) {
         x = operand();
         if (!ok) break;
-        if (F32) mma8_table(acc + 128u, x, sb + 3 * kOperand, true);
-        mma8_table(acc + 128u, x, sb + kOperand, !F32);
+        if (F32) mma8_table(acc + 128u, x, sb + 3 * kTable, true);
+        mma8_table(F32 ? acc + 128u : acc, x, sb + kTable, false);
         done();
       }
       mma_commit_warp(bar(bDone + st));
