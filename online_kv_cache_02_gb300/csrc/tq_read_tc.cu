@@ -8,7 +8,7 @@
 // bf16 rows take the fp16 tables (2^-11 of each factor, half a step of bf16 being 2^-8), and both products one sum: a row's
 // larger factor is applied at the end, the other operand is scaled by their ratio.  fp32 rows take centroids and tables in
 // two fp16 parts each; the two products are summed apart, the small parts ahead of the large ones, since the tensor cores
-// cut a sum instead of rounding it.  Rows leave through shared memory as bulk copies.
+// cut a sum instead of rounding it.  Rows leave through shared memory, so that a store takes whole lines.
 //
 // Warps 0-15: the operands, in two groups that take the tiles in turn (thread = vector and half of its channels); 16-19: the
 // rows (thread = vector); 20: blocks of records by bulk copies; 21: MMA issue.  Every wait is bounded; a wait that gives up
@@ -42,14 +42,14 @@ constexpr int kList = 512;                             // sequences whose pages 
 template <bool F32>
 struct RG {
   static constexpr int TABLES = F32 ? 4 : 2, SLOTS = 4, STAGES = F32 ? 1 : 2, ACC = F32 ? 256 : 128;
-  static constexpr int RECORDS = F32 ? 2 : 5, OUTS = F32 ? 1 : 2;
+  static constexpr int RECORDS = F32 ? 2 : 7;
   static constexpr int ROW = (F32 ? 512 : 256) + 16;               // bytes from row to row: the banks in turn
   static constexpr int REC = TABLES * kTable;
-  static constexpr int OUT = REC + RECORDS * kRecord;              // [OUTS][128]
-  static constexpr int INFO = OUT + OUTS * kVec * ROW;             // [kInfos][128] {row factors, row}
+  static constexpr int OUT = REC + RECORDS * kRecord;              // [128]
+  static constexpr int INFO = OUT + kVec * ROW;             // [kInfos][128] {row factors, row}
   static constexpr int BLK = INFO + kInfos * kVec * 16;            // [RECORDS][8] blocks
   static constexpr int BAR = BLK + RECORDS * kBlocks * 16;
-  static constexpr int BOOK = BAR + 8 * 28;                        // [kind][part of the centroid][group] bytes for prmt
+  static constexpr int BOOK = BAR + 8 * 32;                        // [kind][part of the centroid][group] bytes for prmt
   static constexpr int LIST = BOOK + 8 * 16;                       // pages before each sequence, sums of warps
   static constexpr int TMEM = LIST + 4 * (kList + 32);
   static constexpr int BYTES = TMEM + 16;
@@ -57,10 +57,10 @@ struct RG {
 };
 static_assert(RG<false>::BYTES <= 232448 && RG<true>::BYTES <= 232448, "shared memory per block");
 enum Bar {
-  bRec = 0, bRecFree = bRec + 5, bFull = bRecFree + 5, bFree = bFull + 4, bDone = bFree + 4, bTaken = bDone + 2,
+  bRec = 0, bRecFree = bRec + 7, bFull = bRecFree + 7, bFree = bFull + 4, bDone = bFree + 4, bTaken = bDone + 2,
   bInfo = bTaken + 2, bTab = bInfo + kInfos, bDrain, bCount
 };
-static_assert(bCount <= 28, "barriers");
+static_assert(bCount <= 32, "barriers");
 
 struct alignas(16) BlockInfo {
   int head, slots, row0, pad;             // slots: first | end << 8 (0: nothing); row0: output row of slot 0
@@ -153,14 +153,6 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, __half2 b) {
 __device__ __forceinline__ void mma8_table(uint32_t d, uint32_t a, uint32_t table, bool first) {
   mma8_values(d, a, vdesc(table), idesc_f16(kVec) | (1u << 16), first ? 0u : 1u);
 }
-__device__ __forceinline__ void bulk_row(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
-}
-template <int LEFT>
-__device__ __forceinline__ void bulk_read() {          // this thread's groups but LEFT have been read from shared memory
-  asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
-}
-
 template <bool F32>
 __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_constant__ ReadArgs a) {
   using L = RG<F32>;
@@ -357,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
       if (n + 1 < count) slot += operands(n + 1);      // the other group's
     }
   } else if (warp < kMakers + 4) {
-    // ---- rows: through shared memory, a bulk copy each ---------------------------------------------
+    // ---- rows: through shared memory, whole lines a store (32 bytes a lane's row: 1,000 cycles of the store pipe a tile; a
+    // bulk copy a row: 2,600 to issue) -----------------------------------------------------------------
     const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     for (int n = 0; n < count; ++n) {
@@ -369,8 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) bar_arrive(bar(bInfo + n % kInfos));
       const uint32_t acc = trow + static_cast<uint32_t>(L::ACC * st);
-      const uint32_t to = sb + L::OUT + (n % L::OUTS) * (kVec * L::ROW) + r * L::ROW;
-      bulk_read<L::OUTS - 1>();                        // the copy that was there
+      const uint32_t room = sb + L::OUT + 32 * (warp & 3) * L::ROW, to = room + lane * L::ROW;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         float o[32];
@@ -399,17 +391,27 @@ __global__ void __launch_bounds__(kThreads, 1) read_tc_kernel(const __grid_const
         }
       }
       tc_before();
-      fence_async_smem();
       __syncwarp();
       if (lane == 0) bar_arrive(bar(bTaken + st));
-      if (x.row >= 0) {
-        constexpr int kE = F32 ? 4 : 2;
-        const long long at = static_cast<long long>(x.row) * (key ? a.k_stride : a.v_stride) + static_cast<long long>(x.head) * 128;
-        bulk_row(static_cast<char*>(key ? a.k_out : a.v_out) + at * kE, to, 128 * kE);
+      constexpr int kE = F32 ? 4 : 2, kLanes = 8 * kE, kRows = 32 / kLanes;      // lanes a row, rows at once
+      const long long at = x.row < 0 ? -1 : (static_cast<long long>(x.row) * (key ? a.k_stride : a.v_stride) + static_cast<long long>(x.head) * 128) * kE;
+      char* out = static_cast<char*>(key ? a.k_out : a.v_out) + 16 * (lane % kLanes);
+#pragma unroll 1
+      for (int i = 0; i < 32; i += 8 * kRows) {
+        uint4 v[8];
+        long long where[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = i + kRows * k + lane / kLanes;
+          v[k] = lds128(room + row * L::ROW + 16 * (lane % kLanes));
+          where[k] = __shfl_sync(0xffffffffu, at, row);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (where[k] >= 0) *reinterpret_cast<uint4*>(out + where[k]) = v[k];
       }
-      __syncwarp();
+      __syncwarp();                                    // the room has been read
     }
-    asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (warp == kMakers + 4) {
     // ---- records: a lane per block, four tiles looked up at once and ahead of time --------------------
     struct Found {
