@@ -60,7 +60,7 @@ struct Kv8Share {
   int tail, batch, groups, max_group;
   const int32_t *group_start, *prefix_lens;
   int4* seqs;                     // per sequence, from the prefix pass: prefix pages (0: no prefix), group, the group's first sequence
-  int2* items;                    // tcgen05 form: by block and KV head, the CTAs that hold it (-1: whole, in `state`)
+  int2* items;                    // the pass' items, by block of rows and KV head: the CTAs that hold it (-1: whole, in `state`)
   float* state;                   // per query row: [items per head][maximum, sum, its exponent, 0, channels]
 };
 __device__ __forceinline__ Kv8SharedSeq kv8_group(const Kv8Attn& a, const Kv8Share& s, int g) {
@@ -164,7 +164,7 @@ struct Kv8TcShape {               // of a tcgen05 call: its items per KV head, r
   size_t records;                 // bytes ahead of the parts
   float lift;                     // of its weights' exponents
 };
-float kv8_rows_lift();            // of the other form's
+Kv8TcShape kv8_rows_shape(int T, int G, int d);    // the same of the other form
 Kv8TcShape kv8_tc_shape(int B, int T, int G, int H, int max_seq_len, int d);
 
 }  // namespace tq

@@ -459,6 +459,10 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
         cut = RSplit{1, it.b, it.rb, it.h, it.n,                 // the CTA whose span holds the item's last page
                      static_cast<int>(((prefix[entry] + static_cast<long long>(kItemCost) * some[entry]) * a.H +
                                        (it.h + 1LL) * (it.pages + kItemCost) - 1) / span), {0, 0}};
+      if constexpr (SHARED) {                                    // where the join of both passes finds the item
+        if (c0 == 0 && tid == 0)
+          share.items[static_cast<long long>(entry) * a.H + it.h] = complete ? make_int2(-1, -1) : make_int2(static_cast<int>(blockIdx.x), cut.last);
+      }
     } else {
       const int item = static_cast<int>(blockIdx.x) / cluster;
       it.h = item % a.H;
@@ -468,6 +472,9 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
       complete = cluster == 1;
       u0_first = kRWarps * rank;
       u1 = it.pages;
+      if constexpr (SHARED) {
+        if (rank == 0 && tid == 0) share.items[(static_cast<long long>(it.b) * nrb + it.rb) * a.H + it.h] = make_int2(-1, -1);
+      }
       start();
     }
     const int rows = min(R, static_cast<int>(min(static_cast<long long>(R), static_cast<long long>(it.n) * a.G -
@@ -867,6 +874,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
           if (ch == 0) {
             p[0] = M;
             p[1] = L;
+            if constexpr (SHARED) p[2] = 0.0f;                   // (M's exponent, which the tcgen05 form may have)
           }
         }
       }
@@ -915,8 +923,8 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
 }
 
 // Joins the parts of the items that cross spans: a block per CTA of the first kernel, 16 / R warps per row.
-template <int D, int R, bool F32, class Share>
-__global__ void __launch_bounds__(512) kv8_join_kernel(const __grid_constant__ Kv8Attn a, int ctas, const __grid_constant__ Share share) {
+template <int D, int R, bool F32>
+__global__ void __launch_bounds__(512) kv8_join_kernel(const __grid_constant__ Kv8Attn a, int ctas) {
   constexpr int kPer = 16 / R, kV = D >= 128 ? D / 128 : 1;      // warps per row, float4 per lane
   __shared__ float4 s_acc[16][D / 4];
   __shared__ float s_l[16];
@@ -969,18 +977,6 @@ __global__ void __launch_bounds__(512) kv8_join_kernel(const __grid_constant__ K
     }
   }
   if (!live) return;
-  if constexpr (!std::is_same_v<Share, NoShare>) {
-    const int first = share.tail ? cut.b : share.group_start[cut.b];
-    float* x = share.state + ((static_cast<long long>(first) + gr / a.G) * a.Hq + cut.h * a.G + gr % a.G) * StateRow<D>::LEN;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      const int ch = 128 * i + 4 * lane;
-      if (ch >= D) continue;
-      *reinterpret_cast<float4*>(x + StateRow<D>::channel(ch)) = acc[i];
-      if (ch % StateRow<D>::DV == 0) *reinterpret_cast<float4*>(x + StateRow<D>::channel(ch) - 4) = make_float4(M, L, 0.0f, 0.0f);
-    }
-    return;
-  }
   const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
   const long long o = ((static_cast<long long>(cut.b) * a.T + gr / a.G) * a.Hq + cut.h * a.G + gr % a.G) * D;
 #pragma unroll
@@ -1051,8 +1047,8 @@ cudaError_t launch_t(const Kv8Attn& a, const Share& share, cudaStream_t s) {
     return launch_cluster(kv8_rows_kernel<D, NT, F32, Share>, dim3(static_cast<unsigned>(items * cluster)), dim3(32 * kRWarps), smem, s,
                           cluster, a, mk, mv, static_cast<int>(nrb), 0, cluster, share);
   e = launch_pdl(kv8_rows_kernel<D, NT, F32, Share>, dim3(slots), dim3(32 * kRWarps), smem, s, a, mk, mv, static_cast<int>(nrb), 1, 1, share);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kv8_join_kernel<D, R, F32, Share>, dim3(slots), dim3(512), 0, s, a, slots, share);
+  if (e != cudaSuccess || !std::is_same_v<Share, NoShare>) return e;
+  return launch_pdl(kv8_join_kernel<D, R, F32>, dim3(slots), dim3(512), 0, s, a, slots);
 }
 
 template <int D, class Share>

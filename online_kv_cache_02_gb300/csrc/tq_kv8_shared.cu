@@ -18,11 +18,13 @@
 namespace tq {
 namespace {
 
-struct ShareJoin {
-  const float* tail_state;                // (Kv8Share::state is the prefix's)
-  const float* parts;                     // of the prefix's cut items
-  int tc, rows, nqb, heads;               // prefix pass: tcgen05 or not, its blocks and items
-  float prefix_lift, tail_lift;
+// One pass, as the join finds it.
+struct Pass {
+  const float* state;                     // whole items' sums, by query row
+  const float* parts;                     // of the cut ones
+  const int2* items;
+  int rows, nqb, heads, per, part;        // rows a block, blocks, items and items per head; floats of a part's row
+  float lift;
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -31,14 +33,32 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// A query row's parts in one pass: n of them, their rows `step` floats apart (the first by itself).
+struct Parts {
+  const float *first, *rest;
+  long long step;
+  int n;
+  __device__ __forceinline__ const float* at(int i) const { return i ? rest + i * step : first; }
+};
+// Row `r` of group (or sequence) b in the pass; `whole`: where its sums stand if its item is whole.
+template <int DV>
+__device__ __forceinline__ Parts parts_of(const Pass& p, int b, int r, int kv_head, int half, const float* whole) {
+  const int2 who = p.items[(static_cast<long long>(b) * p.nqb + r / p.rows) * p.heads + kv_head * p.per + (p.per > 1 ? half : 0)];
+  if (who.x < 0) return Parts{whole, whole, 0, 1};
+  const long long slot = static_cast<long long>(p.rows) * p.part, row = static_cast<long long>(r % p.rows) * p.part;
+  // the first part is in its CTA's second slot, the others in their CTAs' first
+  return Parts{p.parts + (2LL * who.x + 1) * slot + row, p.parts + 2LL * who.x * slot + row, 2 * slot, who.y - who.x + 1};
+}
+
 // The sums of one query row: their maximum M (a score, and an exponent beside it), l and O = sum of weights
-// 2^(lift + score - M) and of those times the values.
+// 2^(lift + score - M) and of those times the values.  A warp per row (at d = 256 per half of its channels); a lane per part
+// works out the part's weight, then all lanes take a part's channels.
 template <int D, bool F32>
-__global__ void __launch_bounds__(256) kv8_share_join_kernel(const __grid_constant__ Kv8Attn a, const __grid_constant__ Kv8Share share,
-                                                             const __grid_constant__ ShareJoin j) {
+__global__ void __launch_bounds__(128) kv8_share_join_kernel(const __grid_constant__ Kv8Attn a, const __grid_constant__ Kv8Share share,
+                                                             const __grid_constant__ Pass prefix, const __grid_constant__ Pass tails) {
   constexpr int DV = D == 256 ? 128 : D, PER = D / DV, PART = DV + 4;
   const int lane = threadIdx.x & 31;
-  const long long task = blockIdx.x * 8LL + (threadIdx.x >> 5);
+  const long long task = blockIdx.x * 4LL + (threadIdx.x >> 5);
   if (task >= static_cast<long long>(share.batch) * a.Hq * PER) return;
   const long long row = task / PER;
   const int half = static_cast<int>(task % PER), b = static_cast<int>(row / a.Hq), hq = static_cast<int>(row - static_cast<long long>(b) * a.Hq);
@@ -47,48 +67,52 @@ __global__ void __launch_bounds__(256) kv8_share_join_kernel(const __grid_consta
   const int4 seq = share.seqs[b];
   const Kv8SharedSeq tail = kv8_tail(a, share, b);
   const long long at = (row * PER + half) * PART;
-  // the parts: the tail's, then the prefix's
-  const int nt = tail.n > 0 ? 1 : 0;
-  int first = -1, np = 0, rr = 0;
-  if (seq.x > 0) {
-    np = 1;
-    if (j.tc) {
-      const int r = (b - seq.z) * a.G + hq % a.G;
-      rr = r % j.rows;
-      const int2 who = share.items[(static_cast<long long>(seq.y) * j.nqb + r / j.rows) * j.heads + hq / a.G * PER + half];
-      if (who.x >= 0) {
-        first = who.x;
-        np = who.y - who.x + 1;
-      }
-    }
-  }
-  auto part = [&](int i) {
-    if (i < nt) return j.tail_state + at;
-    if (first < 0) return static_cast<const float*>(share.state) + at;
-    const int k = first + i - nt;         // the first part is in its CTA's second slot, the others in their CTAs' first
-    return j.parts + ((2LL * k + (k == first ? 1 : 0)) * j.rows + rr) * PART;
+  Parts pt{nullptr, nullptr, 0, 0}, pp = pt;
+  if (len > 0 && tail.n > 0) pt = parts_of<DV>(tails, b, hq % a.G, hq / a.G, half, tails.state + at);
+  if (len > 0 && seq.x > 0) pp = parts_of<DV>(prefix, seq.y, (b - seq.z) * a.G + hq % a.G, hq / a.G, half, prefix.state + at);
+  const int n = pt.n + pp.n;
+  auto part = [&](int i) { return i < pt.n ? pt.at(i) : pp.at(i - pt.n); };
+  // a part's row holds all channels where the pass has one item a head: this half's stand behind the others
+  auto channels = [&](int i) {
+    const Pass& p = i < pt.n ? tails : prefix;
+    const bool whole = i < pt.n ? pt.step == 0 : pp.step == 0;
+    return part(i) + 4 + (p.per == 1 && !whole ? half * DV : 0) + 4 * lane;
   };
-  const int n = len > 0 ? nt + np : 0;
-  float M = -INFINITY, E = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i)[0]);
+  auto number = [&](int i) {                           // M, l and M's exponent less the lift
+    if (i >= n) return make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    float4 x = *reinterpret_cast<const float4*>(part(i));
+    x.z -= i < pt.n ? tails.lift : prefix.lift;
+    return x;
+  };
+  float M = -INFINITY, E = -INFINITY, L = 0.0f;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, number(i).x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float ref = M == -INFINITY ? 0.0f : M;         // no key, or scores that are all NaN: sums of 0 or NaN
-  auto power = [&](int i, const float* p) { return p[0] - ref + (p[2] - (i < nt ? j.tail_lift : j.prefix_lift)); };
-  for (int i = lane; i < n; i += 32) E = fmaxf(E, power(i, part(i)));
+  for (int i = lane; i < n; i += 32) {
+    const float4 x = number(i);
+    E = fmaxf(E, x.x - ref + x.z);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) E = fmaxf(E, __shfl_xor_sync(0xffffffffu, E, o));
   if (E == -INFINITY) E = 0.0f;
-  float L = 0.0f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* p = part(i);
-    const float f = exp2_fast(power(i, p) - E);
-    L = fmaf(f, p[1], L);
-    if (4 * lane >= DV) continue;
-    const float4 x = *reinterpret_cast<const float4*>(p + 4 + 4 * lane);
-    acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y), acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const float4 x = number(i0 + lane);
+    const float f = exp2_fast(x.x - ref + x.z - E);
+    float sum = f * x.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    L += sum;
+    const int m = min(32, n - i0);
+#pragma unroll 8
+    for (int i = 0; i < m; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      if (4 * lane >= DV) continue;
+      const float4 y = *reinterpret_cast<const float4*>(channels(i0 + i));
+      acc.x = fmaf(fi, y.x, acc.x), acc.y = fmaf(fi, y.y, acc.y), acc.z = fmaf(fi, y.z, acc.z), acc.w = fmaf(fi, y.w, acc.w);
+    }
+    __syncwarp();
   }
   if (4 * lane >= DV) return;
   const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
@@ -105,30 +129,34 @@ __global__ void __launch_bounds__(256) kv8_share_join_kernel(const __grid_consta
 
 // The workspace: sequences, items, the two passes' sums, then each pass' parts (the join reads the prefix's).
 struct Room {
-  size_t items, prefix, tail, pass, rest, total;
+  size_t items, rest_items, prefix, tail, pass, rest, total;
 };
 size_t align16(size_t x) { return (x + 15) & ~static_cast<size_t>(15); }
 Room room(int batch, int Hq, int H, int groups, int max_group, int max_seq_len, int d) {
-  const Kv8TcShape t = kv8_tc_shape(groups, max_group, Hq / H, H, max_seq_len, d);
+  const int G = Hq / H;
+  const Kv8TcShape t = kv8_tc_shape(groups, max_group, G, H, max_seq_len, d);
   const size_t sums = static_cast<size_t>(batch) * Hq * t.per * (t.dv + 4) * sizeof(float);
+  // blocks of the fewest rows that a pass can have, which never fall with larger sizes
+  const auto blocks = [&](int seqs, int T) { return static_cast<size_t>(seqs) * ((static_cast<long long>(T) * G + 7) / 8) * H * t.per * sizeof(int2); };
   Room r;
   r.items = static_cast<size_t>(batch) * sizeof(int4);
-  r.prefix = r.items + align16(static_cast<size_t>(groups) * t.nqb * H * t.per * sizeof(int2));
+  r.rest_items = r.items + align16(blocks(groups, max_group));
+  r.prefix = r.rest_items + align16(blocks(batch, 1));
   r.tail = r.prefix + align16(sums);
   r.pass = r.tail + align16(sums);
   // no less than for smaller sizes: the blocks of 8 rows can take more than those of 16
-  const size_t least = kv8_rows_workspace(1, 1, d), rows = std::max(least, kv8_rows_workspace(max_group, Hq / H, d));
-  r.rest = r.pass + align16(std::max(rows, kv8_tc_workspace(groups, max_group, Hq / H, H, max_seq_len, d)));
-  r.total = r.rest + std::max(least, kv8_rows_workspace(1, Hq / H, d));
+  const size_t least = kv8_rows_workspace(1, 1, d), rows = std::max(least, kv8_rows_workspace(max_group, G, d));
+  r.rest = r.pass + align16(std::max(rows, kv8_tc_workspace(groups, max_group, G, H, max_seq_len, d)));
+  r.total = r.rest + std::max(least, kv8_rows_workspace(1, G, d));
   return r;
 }
 
 template <int D>
-cudaError_t launch_join(const Kv8Attn& a, const Kv8Share& share, const ShareJoin& j, bool f32, cudaStream_t s) {
+cudaError_t launch_join(const Kv8Attn& a, const Kv8Share& share, const Pass& prefix, const Pass& tails, bool f32, cudaStream_t s) {
   const long long tasks = static_cast<long long>(share.batch) * a.Hq * (D == 256 ? 2 : 1);
-  const dim3 grid(static_cast<unsigned>((tasks + 7) / 8));
-  return f32 ? launch_pdl(kv8_share_join_kernel<D, true>, grid, dim3(256), 0, s, a, share, j)
-             : launch_pdl(kv8_share_join_kernel<D, false>, grid, dim3(256), 0, s, a, share, j);
+  const dim3 grid(static_cast<unsigned>((tasks + 3) / 4));
+  return f32 ? launch_pdl(kv8_share_join_kernel<D, true>, grid, dim3(128), 0, s, a, share, prefix, tails)
+             : launch_pdl(kv8_share_join_kernel<D, false>, grid, dim3(128), 0, s, a, share, prefix, tails);
 }
 
 }  // namespace
@@ -152,23 +180,26 @@ cudaError_t launch_kv8_shared(Kv8Attn a, Kv8Share share, int d, bool f32, float 
   const bool tc = kv8_tc_takes(p.T, a.G, d, f32, softmax_scale);
   cudaError_t e = tc ? launch_kv8_tc_shared(p, share, d, s) : launch_kv8_rows_shared(p, share, d, f32, s);
   if (e != cudaSuccess) return e;
-  const Kv8TcShape t = kv8_tc_shape(p.B, p.T, a.G, a.H, a.max_seq_len, d);
-  ShareJoin j{reinterpret_cast<const float*>(ws + r.tail), a.part + t.records / sizeof(float), tc ? 1 : 0, t.rows, t.nqb, a.H * t.per,
-              tc ? t.lift : kv8_rows_lift(), kv8_rows_lift()};
+  const auto pass = [&](const Kv8TcShape& x, const Kv8Share& sh, const float* work) {
+    return Pass{sh.state, work + x.records / sizeof(float), sh.items, x.rows, x.nqb, a.H * x.per, x.per, x.dv + 4, x.lift};
+  };
+  const Pass prefix = pass(tc ? kv8_tc_shape(p.B, p.T, a.G, a.H, a.max_seq_len, d) : kv8_rows_shape(p.T, a.G, d), share, p.part);
   // the tails
   Kv8Share rest = share;
   rest.tail = 1;
   rest.state = reinterpret_cast<float*>(ws + r.tail);
+  rest.items = reinterpret_cast<int2*>(ws + r.rest_items);
   Kv8Attn b = a;
   b.B = share.batch;
   b.T = 1;
   b.part = reinterpret_cast<float*>(ws + r.rest);
   e = launch_kv8_rows_shared(b, rest, d, f32, s);
   if (e != cudaSuccess) return e;
+  const Pass tails = pass(kv8_rows_shape(1, a.G, d), rest, b.part);
   switch (d) {
-    case 64: return launch_join<64>(a, share, j, f32, s);
-    case 128: return launch_join<128>(a, share, j, f32, s);
-    case 256: return launch_join<256>(a, share, j, f32, s);
+    case 64: return launch_join<64>(a, share, prefix, tails, f32, s);
+    case 128: return launch_join<128>(a, share, prefix, tails, f32, s);
+    case 256: return launch_join<256>(a, share, prefix, tails, f32, s);
     default: return cudaErrorInvalidValue;
   }
 }

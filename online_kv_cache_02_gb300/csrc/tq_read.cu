@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 namespace tq {
 namespace {
@@ -119,51 +120,52 @@ __device__ __forceinline__ float4 codes4(uint32_t w) {
   return make_float4(x.x, x.y, y.x, y.y);
 }
 
-// 8-bit cache: a warp per (page, KV head) block of K or V, sixteen codes a lane at a time.
+// 8-bit cache: a warp per (page, KV head), keys and values at once (one look at the tables for both); a lane takes as many
+// codes as make 16 bytes of a row, so that stores are whole lines.
 template <int D, bool F32>
 __global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ ReadArgs a) {
-  constexpr int P = D / 16;                            // 16-byte pieces of a row of codes
+  constexpr int C = F32 ? 4 : 8, STEPS = kPage * D / (32 * C);     // codes a lane at a time, and times
+  using Word = std::conditional_t<F32, uint32_t, uint2>;
   const int lane = threadIdx.x & 31;
   pdl_wait();
-  const long long blocks = 2LL * a.batch * a.pages * a.H;
+  const long long blocks = static_cast<long long>(a.batch) * a.pages * a.H;
   for (long long at = blockIdx.x * 8LL + (threadIdx.x >> 5); at < blocks; at += 8LL * gridDim.x) {
-    const bool key = at % 2 == 0;
-    const long long x = at / 2;
-    const int h = static_cast<int>(x % a.H), i = static_cast<int>(x / a.H % a.pages), b = static_cast<int>(x / a.H / a.pages);
-    const uint8_t* codes = key ? a.kc : a.vc;
-    if (!codes) continue;
+    const long long page = at / a.H;
+    const int h = static_cast<int>(at - page * a.H), b = static_cast<int>(page / a.pages), i = static_cast<int>(page - static_cast<long long>(b) * a.pages);
     const ReadRun run = read_run(a, b);
     const ReadPage pg = read_page(a, b, run, i);
     if (pg.id < 0) continue;
     const long long blk = static_cast<long long>(pg.id) * a.H + h;
-    const float scale = (key ? a.ks : a.vs)[blk];
-    const uint4* src = reinterpret_cast<const uint4*>(codes + blk * kPage * D);
-    void* out = key ? a.k_out : a.v_out;
-    const long long stride = key ? a.k_stride : a.v_stride;
-    uint4 w[P / 2];
+    Word w[2][STEPS];
+    float scale[2];
 #pragma unroll
-    for (int n = 0; n < P / 2; ++n) w[n] = src[32 * n + lane];
+    for (int kind = 0; kind < 2; ++kind) {
+      const uint8_t* codes = kind ? a.vc : a.kc;
+      scale[kind] = codes ? (kind ? a.vs : a.ks)[blk] : 0.0f;
 #pragma unroll
-    for (int n = 0; n < P / 2; ++n) {
-      const int e = 32 * n + lane, s = e / P;
-      if (s < pg.s0 || s >= pg.s1) continue;
-      const uint32_t u[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
-      float4 f[4];
+      for (int n = 0; n < STEPS; ++n)
+        if (codes) w[kind][n] = reinterpret_cast<const Word*>(codes + blk * kPage * D)[32 * n + lane];
+    }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f[q] = codes4(u[q]);
-        f[q].x *= scale, f[q].y *= scale, f[q].z *= scale, f[q].w *= scale;
-      }
-      const long long to = (static_cast<long long>(run.row) + s - pg.off) * stride + h * D + 16 * (e % P);
-      if (F32) {
+    for (int kind = 0; kind < 2; ++kind) {
+      if (!(kind ? a.vc : a.kc)) continue;
+      void* out = kind ? a.v_out : a.k_out;
+      const long long stride = kind ? a.v_stride : a.k_stride;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) reinterpret_cast<float4*>(static_cast<float*>(out) + to)[q] = f[q];
-      } else {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const __nv_bfloat162 y0 = __floats2bfloat162_rn(f[2 * q].x, f[2 * q].y), y1 = __floats2bfloat162_rn(f[2 * q].z, f[2 * q].w),
-                               y2 = __floats2bfloat162_rn(f[2 * q + 1].x, f[2 * q + 1].y), y3 = __floats2bfloat162_rn(f[2 * q + 1].z, f[2 * q + 1].w);
-          reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + to)[q] =
+      for (int n = 0; n < STEPS; ++n) {
+        const int e = C * (32 * n + lane), s = e / D;
+        if (s < pg.s0 || s >= pg.s1) continue;
+        const long long to = (static_cast<long long>(run.row) + s - pg.off) * stride + static_cast<long long>(h) * D + e % D;
+        if constexpr (F32) {
+          float4 f = codes4(w[kind][n]);
+          f.x *= scale[kind], f.y *= scale[kind], f.z *= scale[kind], f.w *= scale[kind];
+          *reinterpret_cast<float4*>(static_cast<float*>(out) + to) = f;
+        } else {
+          const float4 f = codes4(w[kind][n].x), g = codes4(w[kind][n].y);
+          const float c = scale[kind];
+          const __nv_bfloat162 y0 = __floats2bfloat162_rn(f.x * c, f.y * c), y1 = __floats2bfloat162_rn(f.z * c, f.w * c),
+                               y2 = __floats2bfloat162_rn(g.x * c, g.y * c), y3 = __floats2bfloat162_rn(g.z * c, g.w * c);
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + to) =
               make_uint4(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1),
                          *reinterpret_cast<const uint32_t*>(&y2), *reinterpret_cast<const uint32_t*>(&y3));
         }
@@ -182,8 +184,10 @@ cudaError_t launch_read(const ReadArgs& a, int d, bool f32, cudaStream_t s) {
 }
 
 cudaError_t launch_kv8_read(const ReadArgs& a, int d, bool f32, cudaStream_t s) {
-  const long long blocks = 2LL * a.batch * a.pages * a.H;
-  const dim3 grid(static_cast<unsigned>(std::min<long long>((blocks + 7) / 8, 8LL * kv8_sm_count())));
+  const long long blocks = static_cast<long long>(a.batch) * a.pages * a.H;
+  // a (page, head) a warp: handed out by the hardware they end closer together than strides of a resident grid (8 x 16,384
+  // tokens: 122 us, 129 with 8 blocks an SM)
+  const dim3 grid(static_cast<unsigned>(std::min<long long>((blocks + 7) / 8, 1 << 24)));
   auto go = [&](auto k16, auto k32) { return f32 ? launch_pdl(k32, grid, dim3(256), 0, s, a) : launch_pdl(k16, grid, dim3(256), 0, s, a); };
   switch (d) {
     case 64: return go(kv8_read_kernel<64, false>, kv8_read_kernel<64, true>);
