@@ -84,12 +84,20 @@ __global__ void __launch_bounds__(128) kv8_share_join_kernel(const __grid_consta
     x.z -= i < pt.n ? tails.lift : prefix.lift;
     return x;
   };
-  float M = -INFINITY, E = -INFINITY, L = 0.0f;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, number(i).x);
+  // the first parts' numbers and channels at once: what they weigh is worked out while the channels come
+  constexpr int kAhead = 8;
+  const float4 mine = number(lane);
+  float4 y[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    y[i] = i < n && 4 * lane < DV ? *reinterpret_cast<const float4*>(channels(i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = mine.x, E = -INFINITY, L = 0.0f;
+  for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, number(i).x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float ref = M == -INFINITY ? 0.0f : M;         // no key, or scores that are all NaN: sums of 0 or NaN
-  for (int i = lane; i < n; i += 32) {
+  E = mine.x - ref + mine.z;
+  for (int i = lane + 32; i < n; i += 32) {
     const float4 x = number(i);
     E = fmaxf(E, x.x - ref + x.z);
   }
@@ -97,31 +105,40 @@ __global__ void __launch_bounds__(128) kv8_share_join_kernel(const __grid_consta
   for (int o = 16; o > 0; o >>= 1) E = fmaxf(E, __shfl_xor_sync(0xffffffffu, E, o));
   if (E == -INFINITY) E = 0.0f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float f, float4 v) {
+    acc.x = fmaf(f, v.x, acc.x), acc.y = fmaf(f, v.y, acc.y), acc.z = fmaf(f, v.z, acc.z), acc.w = fmaf(f, v.w, acc.w);
+  };
   for (int i0 = 0; i0 < n; i0 += 32) {
-    const float4 x = number(i0 + lane);
+    const float4 x = i0 ? number(i0 + lane) : mine;
     const float f = exp2_fast(x.x - ref + x.z - E);
     float sum = f * x.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     L += sum;
-    const int m = min(32, n - i0);
-#pragma unroll 8
-    for (int i = 0; i < m; ++i) {
-      const float fi = __shfl_sync(0xffffffffu, f, i);
-      if (4 * lane >= DV) continue;
-      const float4 y = *reinterpret_cast<const float4*>(channels(i0 + i));
-      acc.x = fmaf(fi, y.x, acc.x), acc.y = fmaf(fi, y.y, acc.y), acc.z = fmaf(fi, y.z, acc.z), acc.w = fmaf(fi, y.w, acc.w);
+    for (int i = 0; i < min(32, n - i0); i += kAhead) {
+      float4 z[kAhead];                                // the next ones on their way
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int next = i0 + i + kAhead + k;
+        z[k] = next < n && 4 * lane < DV ? *reinterpret_cast<const float4*>(channels(next)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, i + k);
+        if (i0 + i + k < n) add(fk, y[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) y[k] = z[k];
     }
-    __syncwarp();
   }
   if (4 * lane >= DV) return;
   const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
-  const float4 y = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
   const long long to = row * D + half * DV + 4 * lane;
   if (F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = y;
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = o;
   } else {
-    const __nv_bfloat162 y0 = __floats2bfloat162_rn(y.x, y.y), y1 = __floats2bfloat162_rn(y.z, y.w);
+    const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x, o.y), y1 = __floats2bfloat162_rn(o.z, o.w);
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + to) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
   }
