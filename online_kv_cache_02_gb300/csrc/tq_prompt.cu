@@ -1,8 +1,8 @@
 // Attention over packed prompts on CUDA cores: fp32 inputs, and head dimensions that the tensor-core form does not take.
 //
 //   s_j = scale <q, k_j>,  out = sum_j 2^(s_j log2 e - M) v_j / sum_j 2^(s_j log2 e - M),  M the running maximum,
-// over the keys j that the query's position sees.  A CTA takes 64 query rows of a KV head (row r = t G + g, so that a
-// key that is read serves every query head of its group) and 64 keys at a time; keys and queries stand transposed in
+// over the keys j that the query's position sees.  A CTA takes 64 query rows of a KV head, or 16 where no sequence has more
+// (row r = t G + g, so that a key that is read serves every query head of its group) and 64 keys at a time; keys and queries stand transposed in
 // shared memory, so that a thread's 4 x 4 scores take two 16-byte loads per channel; sums are fp32 throughout.
 // Bound by the FMA pipes and shared-memory loads.
 
@@ -17,14 +17,17 @@
 namespace tq {
 namespace {
 
-constexpr int kRows = 64, kTok = 64, kThreads = 256;
+constexpr int kTok = 64, kThreads = 256;
 constexpr int kItemCost = 2;              // an item's start and end, in tiles' time
 constexpr int kMinSpan = 1 + kItemCost;
 constexpr int kLd = 68;                   // floats from channel to channel of the transposed tiles
 
-template <int D>
+// RM: query rows a thread (16 threads side by side hold them all)
+template <int D, int RM>
 struct SG {
-  static constexpr int Q = 0, K = Q + D * kLd, V = K + D * kLd, P = V + kTok * D, END = P + kTok * kLd;   // floats
+  static constexpr int ROWS = 16 * RM, LQ = ROWS + 4;              // LQ: floats from channel to channel of the queries, key to key of the weights
+  // floats; the weights stand where the keys were (with a barrier between), for two blocks an SM up to d = 128
+  static constexpr int Q = 0, K = Q + D * LQ, P = K, V = K + (D > kTok ? D : kTok) * kLd, END = V + kTok * D;
   static constexpr int BYTES = 4 * (END > 2 * kPromptList + 64 ? END : 2 * kPromptList + 64);
 };
 
@@ -45,9 +48,21 @@ __device__ __forceinline__ bool finite4(float4 x) {
   return fabsf(x.x) <= 3.4028234e38f && fabsf(x.y) <= 3.4028234e38f && fabsf(x.z) <= 3.4028234e38f && fabsf(x.w) <= 3.4028234e38f;
 }
 
-template <int D, bool F32>
-__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_constant__ PromptArgs a, int mode) {
-  using L = SG<D>;
+// RM floats of shared memory.
+template <int RM>
+__device__ __forceinline__ void load_rows(const float* p, float (&x)[RM]) {
+  if constexpr (RM == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else {
+    x[0] = *p;
+  }
+}
+
+template <int D, bool F32, int RM>
+__global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) prompt_simt_kernel(const __grid_constant__ PromptArgs a, int mode) {
+  using L = SG<D, RM>;
+  constexpr int kRows = L::ROWS, LQ = L::LQ;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   pdl_wait();
@@ -71,14 +86,14 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
         const int gr = b.r0 + r, tok = gr / a.G, g = gr - tok * a.G;
         x = load4<F32>(a.q, (static_cast<long long>(b.seq.q0) + tok) * a.qs + static_cast<long long>(w.h * a.G + g) * D + c);
       }
-      float* q = sm + L::Q + c * kLd + r;
-      q[0] = x.x, q[kLd] = x.y, q[2 * kLd] = x.z, q[3 * kLd] = x.w;
+      float* q = sm + L::Q + c * LQ + r;
+      q[0] = x.x, q[LQ] = x.y, q[2 * LQ] = x.z, q[3 * LQ] = x.w;
     }
-    int p[4];
-    float m[4], l[4], o[4][D / 16];
+    int p[RM];
+    float m[RM], l[RM], o[RM][D / 16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * ty + i;
+    for (int i = 0; i < RM; ++i) {
+      const int r = RM * ty + i;
       p[i] = r < b.rows ? b.seq.m - b.seq.n + (b.r0 + r) / a.G : -1;
       m[i] = -INFINITY;
       l[i] = 0.0f;
@@ -105,20 +120,21 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
         *reinterpret_cast<float4*>(sm + L::V + r * D + c) = x;
       }
       odd = __syncthreads_or(odd);
-      // ---- scores: rows 4 ty + i, keys 4 tx + k -------------------------------------------------
-      float s[4][4] = {};
+      // ---- scores: rows RM ty + i, keys 4 tx + k -------------------------------------------------
+      float s[RM][4] = {};
 #pragma unroll 8
       for (int c = 0; c < D; ++c) {
-        const float4 q = *reinterpret_cast<const float4*>(sm + L::Q + c * kLd + 4 * ty);
+        float qa[RM];
+        load_rows<RM>(sm + L::Q + c * LQ + RM * ty, qa);
         const float4 k = *reinterpret_cast<const float4*>(sm + L::K + c * kLd + 4 * tx);
-        const float qa[4] = {q.x, q.y, q.z, q.w}, ka[4] = {k.x, k.y, k.z, k.w};
+        const float ka[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RM; ++i)
 #pragma unroll
           for (int n = 0; n < 4; ++n) s[i][n] = fmaf(qa[i], ka[n], s[i][n]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < RM; ++i) {
         float top = -INFINITY;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -141,21 +157,25 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) o[i][c] *= al;
       }
+      __syncthreads();                                 // the keys have been read
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-        *reinterpret_cast<float4*>(sm + L::P + (4 * tx + n) * kLd + 4 * ty) = make_float4(s[0][n], s[1][n], s[2][n], s[3][n]);
+      for (int n = 0; n < 4; ++n) {
+        float* w = sm + L::P + (4 * tx + n) * LQ + RM * ty;
+        if constexpr (RM == 4) *reinterpret_cast<float4*>(w) = make_float4(s[0][n], s[1][n], s[2][n], s[3][n]);
+        else *w = s[0][n];
+      }
       __syncthreads();
       // ---- values: channels 2 tx + 32 c, + 1 -----------------------------------------------------
       auto values = [&](bool masked) {
 #pragma unroll 4
         for (int k = 0; k < kTok; ++k) {
-          const float4 pw = *reinterpret_cast<const float4*>(sm + L::P + k * kLd + 4 * ty);
-          const float pa[4] = {pw.x, pw.y, pw.z, pw.w};
+          float pa[RM];
+          load_rows<RM>(sm + L::P + k * LQ + RM * ty, pa);
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             const float2 v = *reinterpret_cast<const float2*>(sm + L::V + k * D + 2 * tx + 32 * c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < RM; ++i) {
               if (masked && !prompt_sees(p[i], j0 + k, a.window, a.sinks)) continue;
               o[i][2 * c] = fmaf(pa[i], v.x, o[i][2 * c]);
               o[i][2 * c + 1] = fmaf(pa[i], v.y, o[i][2 * c + 1]);
@@ -168,8 +188,8 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const __grid_cons
     }
     // ---- results, or the part's sums ------------------------------------------------------------
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * ty + i;
+    for (int i = 0; i < RM; ++i) {
+      const int r = RM * ty + i;
       if (r >= b.rows) continue;
       const int gr = b.r0 + r, tok = gr / a.G, g = gr - tok * a.G;
       if (w.slot < 0) {
@@ -252,22 +272,30 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
   }
 }
 
-int simt_ctas(int d) { return prompt_sms() * (d > 64 ? 1 : 2); }
+int simt_ctas(int d) { return prompt_sms() * (d > 128 ? 1 : 2); }
 
-template <int D>
+template <int D, int RM>
 cudaError_t launch_t(const PromptArgs& a, bool f32, cudaStream_t s) {
+  using L = SG<D, RM>;
   static std::atomic<unsigned long long> done16{0}, done32{0};
-  cudaError_t e = f32 ? smem_attr_once(prompt_simt_kernel<D, true>, SG<D>::BYTES, done32)
-                      : smem_attr_once(prompt_simt_kernel<D, false>, SG<D>::BYTES, done16);
+  cudaError_t e = f32 ? smem_attr_once(prompt_simt_kernel<D, true, RM>, L::BYTES, done32)
+                      : smem_attr_once(prompt_simt_kernel<D, false, RM>, L::BYTES, done16);
   if (e != cudaSuccess) return e;
   const long long tiles = a.max_k / kTok + 2 + a.sinks / kTok;
   // items of few tiles are not cut (and need no join)
   const int mode = !prompt_splits(a, kTok, kItemCost) ? kPromptTurns : tiles > 4 ? kPromptCut : kPromptWhole;
   const int ctas = simt_ctas(D);
-  e = f32 ? launch_pdl(prompt_simt_kernel<D, true>, dim3(ctas), dim3(kThreads), SG<D>::BYTES, s, a, mode)
-          : launch_pdl(prompt_simt_kernel<D, false>, dim3(ctas), dim3(kThreads), SG<D>::BYTES, s, a, mode);
+  e = f32 ? launch_pdl(prompt_simt_kernel<D, true, RM>, dim3(ctas), dim3(kThreads), L::BYTES, s, a, mode)
+          : launch_pdl(prompt_simt_kernel<D, false, RM>, dim3(ctas), dim3(kThreads), L::BYTES, s, a, mode);
   if (e != cudaSuccess || mode != kPromptCut) return e;
-  return launch_prompt_join(a, D, f32, ctas, kRows, 1, s);
+  return launch_prompt_join(a, D, f32, ctas, L::ROWS, 1, s);
+}
+template <int D>
+cudaError_t launch_d(const PromptArgs& args, bool f32, cudaStream_t s) {
+  PromptArgs a = args;
+  const bool few = static_cast<long long>(a.max_q) * a.G <= 16;
+  a.rows = few ? 16 : 64;
+  return few ? launch_t<D, 1>(a, f32, s) : launch_t<D, 4>(a, f32, s);
 }
 }  // namespace
 
@@ -300,21 +328,19 @@ cudaError_t launch_prompt_join(const PromptArgs& a, int d, bool f32, int ctas, i
 }
 
 size_t prompt_simt_workspace(int d) {
-  return static_cast<size_t>(simt_ctas(d)) * (sizeof(PSplit) + 2 * sizeof(float) * kRows * (d + 4));
+  return static_cast<size_t>(simt_ctas(d)) * (sizeof(PSplit) + 2 * sizeof(float) * 64 * (d + 4));
 }
 
-cudaError_t launch_prompt_simt(const PromptArgs& args, int d, bool f32, cudaStream_t s) {
-  PromptArgs a = args;
-  a.rows = kRows;
+cudaError_t launch_prompt_simt(const PromptArgs& a, int d, bool f32, cudaStream_t s) {
   switch (d) {
-    case 32: return launch_t<32>(a, f32, s);
-    case 64: return launch_t<64>(a, f32, s);
-    case 96: return launch_t<96>(a, f32, s);
-    case 128: return launch_t<128>(a, f32, s);
-    case 160: return launch_t<160>(a, f32, s);
-    case 192: return launch_t<192>(a, f32, s);
-    case 224: return launch_t<224>(a, f32, s);
-    case 256: return launch_t<256>(a, f32, s);
+    case 32: return launch_d<32>(a, f32, s);
+    case 64: return launch_d<64>(a, f32, s);
+    case 96: return launch_d<96>(a, f32, s);
+    case 128: return launch_d<128>(a, f32, s);
+    case 160: return launch_d<160>(a, f32, s);
+    case 192: return launch_d<192>(a, f32, s);
+    case 224: return launch_d<224>(a, f32, s);
+    case 256: return launch_d<256>(a, f32, s);
     default: return cudaErrorInvalidValue;
   }
 }
