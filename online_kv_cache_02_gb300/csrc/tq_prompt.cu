@@ -215,11 +215,10 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) prompt_simt_kernel
   if (mode == kPromptCut && tid == 0) splits[blockIdx.x] = w.cut;
 }
 
-// Joins the parts of the items that cross spans: a warp per row and run of DV channels.  A part's maximum may have an
-// exponent beside it (its third number), which the weights of very large scores need.
-template <int D, int DV, bool F32>
+// Joins the parts of the items that cross spans: a warp per row.
+template <int D, bool F32>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ PromptArgs a, int ctas, int rows) {
-  constexpr int PER = D / DV, PART = DV + 4, V4 = (DV + 127) / 128;
+  constexpr int PART = D + 4, V4 = (D + 127) / 128;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
   pdl_wait();
   const PSplit cut = reinterpret_cast<const PSplit*>(a.part)[c];
@@ -229,15 +228,11 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
   const long long step = static_cast<long long>(rows) * PART;
   // the first part is in its CTA's second slot, the others in their CTAs' first
   auto part = [&](int k) { return parts + (2LL * k + (k == c ? 1 : 0)) * step + static_cast<long long>(rr) * PART; };
-  float M = -INFINITY, E = -INFINITY;
+  float M = -INFINITY;
   for (int k = c + lane; k <= cut.last; k += 32) M = fmaxf(M, part(k)[0]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float ref = M == -INFINITY ? 0.0f : M;         // no key, or scores that are all NaN: sums of 0 or NaN
-  for (int k = c + lane; k <= cut.last; k += 32) E = fmaxf(E, part(k)[0] - ref + part(k)[2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) E = fmaxf(E, __shfl_xor_sync(0xffffffffu, E, o));
-  if (E == -INFINITY) E = 0.0f;
   float L = 0.0f;
   float4 acc[V4];
 #pragma unroll
@@ -245,22 +240,22 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
 #pragma unroll 4
   for (int k = c; k <= cut.last; ++k) {
     const float* p = part(k);
-    const float f = exp2_fast(p[0] - ref + p[2] - E);
+    const float f = exp2_fast(p[0] - ref);
     L = fmaf(f, p[1], L);
 #pragma unroll
     for (int i = 0; i < V4; ++i) {
-      if (128 * i + 4 * lane >= DV) continue;
+      if (128 * i + 4 * lane >= D) continue;
       const float4 x = *reinterpret_cast<const float4*>(p + 4 + 128 * i + 4 * lane);
       acc[i].x = fmaf(f, x.x, acc[i].x), acc[i].y = fmaf(f, x.y, acc[i].y), acc[i].z = fmaf(f, x.z, acc[i].z), acc[i].w = fmaf(f, x.w, acc[i].w);
     }
   }
   const int gr = cut.r0 + rr, tok = gr / a.G, g = gr - tok * a.G;
   const float inv = prompt_inverse(L, cut.p0 + tok);
-  const long long at = ((static_cast<long long>(cut.q0) + tok) * a.Hq + cut.h / PER * a.G + g) * D + cut.h % PER * DV;
+  const long long at = ((static_cast<long long>(cut.q0) + tok) * a.Hq + cut.h * a.G + g) * D;
 #pragma unroll
   for (int i = 0; i < V4; ++i) {
     const int ch = 128 * i + 4 * lane;
-    if (ch >= DV) continue;
+    if (ch >= D) continue;
     const float4 y = make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
     if (F32) {
       *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + ch) = y;
@@ -288,7 +283,7 @@ cudaError_t launch_t(const PromptArgs& a, bool f32, cudaStream_t s) {
   e = f32 ? launch_pdl(prompt_simt_kernel<D, true, RM>, dim3(ctas), dim3(kThreads), L::BYTES, s, a, mode)
           : launch_pdl(prompt_simt_kernel<D, false, RM>, dim3(ctas), dim3(kThreads), L::BYTES, s, a, mode);
   if (e != cudaSuccess || mode != kPromptCut) return e;
-  return launch_prompt_join(a, D, f32, ctas, L::ROWS, 1, s);
+  return launch_prompt_join(a, D, f32, ctas, L::ROWS, s);
 }
 template <int D>
 cudaError_t launch_d(const PromptArgs& args, bool f32, cudaStream_t s) {
@@ -310,19 +305,18 @@ bool prompt_splits(const PromptArgs& a, int tok, int cost) {
   return a.S <= kPromptList && blocks <= kPromptList && blocks * (a.max_k / tok + 2 + a.sinks / tok + cost) <= 0x7FFFFFFFLL;
 }
 
-cudaError_t launch_prompt_join(const PromptArgs& a, int d, bool f32, int ctas, int rows, int per, cudaStream_t s) {
+cudaError_t launch_prompt_join(const PromptArgs& a, int d, bool f32, int ctas, int rows, cudaStream_t s) {
   const dim3 grid(ctas, rows / 8), block(256);
   auto go = [&](auto k16, auto k32) { return f32 ? launch_pdl(k32, grid, block, 0, s, a, ctas, rows) : launch_pdl(k16, grid, block, 0, s, a, ctas, rows); };
-  if (per == 2 && d == 256) return go(prompt_join_kernel<256, 128, false>, prompt_join_kernel<256, 128, true>);
   switch (d) {
-    case 32: return go(prompt_join_kernel<32, 32, false>, prompt_join_kernel<32, 32, true>);
-    case 64: return go(prompt_join_kernel<64, 64, false>, prompt_join_kernel<64, 64, true>);
-    case 96: return go(prompt_join_kernel<96, 96, false>, prompt_join_kernel<96, 96, true>);
-    case 128: return go(prompt_join_kernel<128, 128, false>, prompt_join_kernel<128, 128, true>);
-    case 160: return go(prompt_join_kernel<160, 160, false>, prompt_join_kernel<160, 160, true>);
-    case 192: return go(prompt_join_kernel<192, 192, false>, prompt_join_kernel<192, 192, true>);
-    case 224: return go(prompt_join_kernel<224, 224, false>, prompt_join_kernel<224, 224, true>);
-    case 256: return go(prompt_join_kernel<256, 256, false>, prompt_join_kernel<256, 256, true>);
+    case 32: return go(prompt_join_kernel<32, false>, prompt_join_kernel<32, true>);
+    case 64: return go(prompt_join_kernel<64, false>, prompt_join_kernel<64, true>);
+    case 96: return go(prompt_join_kernel<96, false>, prompt_join_kernel<96, true>);
+    case 128: return go(prompt_join_kernel<128, false>, prompt_join_kernel<128, true>);
+    case 160: return go(prompt_join_kernel<160, false>, prompt_join_kernel<160, true>);
+    case 192: return go(prompt_join_kernel<192, false>, prompt_join_kernel<192, true>);
+    case 224: return go(prompt_join_kernel<224, false>, prompt_join_kernel<224, true>);
+    case 256: return go(prompt_join_kernel<256, false>, prompt_join_kernel<256, true>);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -179,7 +179,7 @@ enum PromptMode { kPromptCut = 1, kPromptWhole = 2, kPromptTurns = 0 };
 template <int TOK, int COST>
 struct PromptWalk {
   PromptBlock blk;
-  int h, t0, t1, slot;                    // KV head (or item of one); its tiles [t0, t1); workspace slot, -1 for whole items
+  int h, t0, t1, slot;                    // KV head; its tiles [t0, t1); workspace slot, -1 for whole items
   PSplit cut;                             // the record that this CTA leaves
   long long at, whole;
   int s, qb, tiles, heads, nblk, mode;
@@ -302,8 +302,8 @@ int prompt_sms();                         // of the current device
 bool prompt_tc_takes(const PromptArgs& a, int d, bool f32);
 size_t prompt_tc_workspace(int d);
 cudaError_t launch_prompt_tc(const PromptArgs& a, int d, cudaStream_t s);
-// Joins the parts of split items (`rows` of them a slot, PART floats a row: maximum, sum, its exponent, 0, then a run of channels).
-cudaError_t launch_prompt_join(const PromptArgs& a, int d, bool f32, int ctas, int rows, int per, cudaStream_t s);
+// Joins the parts of split items (`rows` of them a slot, d + 4 floats a row: maximum, sum, two zeros, then the channels).
+cudaError_t launch_prompt_join(const PromptArgs& a, int d, bool f32, int ctas, int rows, cudaStream_t s);
 
 }  // namespace tq
 

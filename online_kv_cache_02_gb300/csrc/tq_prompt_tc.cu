@@ -6,16 +6,16 @@
 // tile, with x = scale log2(e) <q, k>:
 //   S = Q K^T              bf16, from tiles that TMA puts in place
 //   w = 2^(x - M)          bf16 and fp32 hold the weights whatever M is, within 2^126: M starts as 0, and only a tile whose
-//                          weights sum to more than 2^40, or that leaves a row that sees something with a sum below
-//                          2^-40, looks for a maximum
+//                          weights sum to more than 2^24, or that leaves a row that sees something with a sum below
+//                          2^-24, looks for a maximum
 //   O += w V, l += sum w   w as bf16 (off by 2^-8 at most) in tensor memory, V's token rows read MN-major;
 //   out = O / l.
 // The halves take turns: while the softmax of one runs, the tensor cores work on the other.  An item follows the one
 // before like a tile does: its queries are there ahead of time (a ring of halves), and its results are left to warps of
 // their own.  Tensor memory: S of A and B (each overlaid by its weights), O of A and B, 512 columns.  An item that fits one
-// half is in both: A takes the even tiles, B the odd ones, and their sums are added at the end.  At d = 256 an item is one
-// half of rows and one half of the values' channels (the scores are the same work twice: queries, keys and values of 256
-// rows and channels do not fit), in the same turns.
+// half is in both: A takes the even tiles, B the odd ones, and their sums are added at the end.  At d = 256 every item is
+// one half of rows, in the same turns, and tensor memory has one O of 256 columns, to which both add: M is the row's in
+// both, and a half that moves it does so between the other's products.
 //
 // A key that a row does not see has weight zero, but zero times an infinity is NaN: the values of tiles that some row does
 // not see in full are looked through before they are multiplied, what is not finite there is taken out, and added to the
@@ -45,7 +45,7 @@ constexpr int kThreads = 512;
 constexpr int kItems = 4;                 // items announced ahead
 constexpr int kItemCost = 3;              // an item's start and end, in tiles' time
 constexpr int kMinSpan = 2 + kItemCost;   // a CTA's share of the list at least
-constexpr float kFull = 1.0995116e12f, kTiny = 9.0949470e-13f;    // 2^40 and 2^-40: bounds of a row's sum
+constexpr float kFull = 16777216.0f, kTiny = 5.9604645e-8f;       // 2^24 and 2^-24: bounds of a row's sum
 // x - M in one rounding is off by half a step of M against the other tiles' M: beyond 2^16 scores are rounded first, so that
 // small differences of large ones are exact.
 constexpr float kBig = 65536.0f;
@@ -60,29 +60,30 @@ struct PG {
   static constexpr bool WIDE = D == 256;
   static constexpr int HALVES = WIDE ? 1 : 2;          // of query rows per item
   static constexpr int ROWS = 128 * HALVES;
-  static constexpr int DV = WIDE ? 128 : D;            // value channels per item
-  static constexpr int PER = D / DV;                   // items per KV head and block of rows
+  static constexpr int VCH = WIDE ? 2 : 1, VTOK = kTok / VCH;      // pieces of a tile's values, and their tokens
   static constexpr int KCH = D > 128 ? D / 128 : 1;    // pieces of a tile's keys, 128 channels each
-  static constexpr int PIECE = kTok * 2 * (D < 128 ? D : 128);      // bytes of one, and of a tile's values
+  static constexpr int PIECE = kTok * 2 * (D < 128 ? D : 128);      // bytes of a piece
   static constexpr int QX = 128 * 2 * D;               // a half's queries
-  static constexpr int QST = D == 64 ? 4 : D == 128 ? 3 : 1, KST = D == 64 ? 5 : D == 128 ? 2 : 3, VST = D == 64 ? 5 : 2;
-  static constexpr int PART = DV + 4;                  // floats of a row's partial
+  static constexpr int QST = D == 64 ? 4 : D == 128 ? 3 : 1, KST = D == 64 ? 5 : 2, VST = D == 64 ? 5 : D == 128 ? 2 : 3;
+  static constexpr int PART = D + 4;                   // floats of a row's partial
   static constexpr int Q = 0;                          // [stage][64-channel panels][128 rows][128 B]
   static constexpr int K = Q + QST * QX;               // [stage][64-channel panels][128 tokens][128 B]
-  static constexpr int V = K + KST * PIECE;
+  static constexpr int V = K + KST * PIECE;            // [stage][64-channel panels][VTOK tokens][128 B]
   static constexpr int ITEM = V + VST * PIECE;
   static constexpr int BAR = ITEM + kItems * 64;
 };
 enum Bar {
   bQFull = 0, bQFree = bQFull + 4, bKFull = bQFree + 4, bKFree = bKFull + 5, bVFull = bKFree + 5, bVFree = bVFull + 5, bVOk = bVFree + 5,
-  bSFull = bVOk + 5, bPFull = bSFull + 2, bSums = bPFull + 2, bODone = bSums + 2, bOFree = bODone + 2, bItem = bOFree + 2,
+  bSFull = bVOk + 5, bPFull = bSFull + 2, bProducts = bPFull + 2, bTold = bProducts + 2, bSums = bTold + 4, bODone = bSums + 2, bOFree = bODone + 2, bItem = bOFree + 2,
   bItemFree = bItem + kItems, bChecked = bItemFree + kItems, bDrain = bChecked + kCheckRing, bCount
 };
 template <int D>
 struct PS {                                            // behind the barriers
-  static constexpr int SUMS = PG<D>::BAR + 8 * ((bCount + 1) & ~1);      // (M, l) of the halves' rows
+  static constexpr int SUMS = PG<D>::BAR + 8 * ((bCount + 1) & ~1);      // (M, l) of the halves' rows; d = 256: [l of A, l of B, M of the half
+                                                                         // that ends first, M] of 128 rows
   static constexpr int ODD = SUMS + 2 * 128 * 8;   // per item: values that are not finite in edge tiles
-  static constexpr int TMEM = ODD + 4 * kCheckRing;
+  static constexpr int MOVES = ODD + 4 * kCheckRing;   // d = 256: how often M has moved, by 32 rows: item + 1, times
+  static constexpr int TMEM = MOVES + 32;
   static constexpr int BYTES = TMEM + 16;
 };
 static_assert(PS<64>::BYTES <= 232448 && PS<128>::BYTES <= 232448 && PS<256>::BYTES <= 232448, "shared memory per block");
@@ -92,7 +93,7 @@ __device__ __forceinline__ constexpr uint32_t col_o(uint32_t X) { return 256u + 
 
 // What the load warp tells the others of an item.
 struct alignas(16) ItemMsg {
-  int valid, h, q0, r0;                   // h: item of the block (KV head, at d = 256 with a half of the values' channels)
+  int valid, h, q0, r0;                   // h: KV head
   int rows, p0, pmin, pmax;               // p0: position of the sequence's first query
   int ntile, t0, slot, k0;                // slot: of the workspace for a part of the tiles; -1 for all of them
   int ns, w0, pad[2];
@@ -141,6 +142,20 @@ __device__ __forceinline__ void mma4_scores(uint32_t d, uint64_t q, uint64_t k, 
       "l"(q), "l"(k), "r"(idesc)
       : "memory");
 }
+// O (+)= w V for 64 keys: four steps of 16 (8 columns of weights, 2048 B or 128 descriptor units of values).
+__device__ __forceinline__ void mma4_values(uint32_t d, uint32_t w, uint64_t v, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred e, t, p;\n .reg .b32 w1, w2, w3;\n .reg .b64 v1, v2, v3;\n"
+      " add.u32 w1, %1, 8;\n add.u32 w2, %1, 16;\n add.u32 w3, %1, 24;\n"
+      " add.u64 v1, %2, 128;\n add.u64 v2, %2, 256;\n add.u64 v3, %2, 384;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.ne.b32 t, 1, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [w1], v1, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [w2], v2, %3, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [w3], v3, %3, t;\n}\n" ::"r"(d),
+      "r"(w), "l"(v), "r"(idesc), "r"(acc)
+      : "memory");
+}
 // kind::f16 with bf16 A and B, fp32 accumulate, M = 128, N = n
 __host__ __device__ constexpr uint32_t idesc_bf16(int n) { return idesc_f16(n) | (1u << 7) | (1u << 10); }
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int head, int row, uint32_t bar) {
@@ -172,10 +187,11 @@ __device__ __forceinline__ uint32_t seen32(int p, int j0, int window, int sinks)
   return see;
 }
 // One tile's weights of a thread's row with a new M, the largest score met; scores are rounded before they are compared.
-// accumulated: O holds tiles before.  Returns M and l.
+// accumulated: O holds tiles before, of which the row has seen something (had): M is then the row's reference, only raised
+// where O has another half's sums in it (shared).  Returns M and l.
 template <int DV>
 __device__ __noinline__ float2 careful_tile(uint32_t ts, uint32_t to, int j0, int p, int window, int sinks, float f, bool accumulated,
-                                            float m, float l) {
+                                            float m, float l, bool had, bool shared) {
   auto scores = [&](int c, float (&y)[32]) {
     tld32(ts + 32u * c, y);
     const uint32_t see = seen32(p, j0 + 32 * c, window, sinks);
@@ -184,7 +200,7 @@ __device__ __noinline__ float2 careful_tile(uint32_t ts, uint32_t to, int j0, in
     __syncwarp();
   };
   // of the sum so far: l 2^m, about 2^(m + log2 l), so that alpha l is about 1 at most
-  float y[32], mn = l > 0.0f ? m + log2f(l) : -INFINITY;
+  float y[32], mn = had ? (shared ? m : m + log2f(l)) : -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     scores(c, y);
@@ -192,7 +208,7 @@ __device__ __noinline__ float2 careful_tile(uint32_t ts, uint32_t to, int j0, in
     for (int k = 0; k < 32; ++k) mn = fmaxf(mn, y[k]);
   }
   if (mn == -INFINITY) mn = 0.0f;                      // nothing seen
-  const float alpha = l > 0.0f ? ex2(m - mn) : 1.0f;
+  const float alpha = had ? ex2(m - mn) : 1.0f;
   __syncwarp();
   if (accumulated) rescale_o<DV>(to, alpha);
   l *= alpha;
@@ -293,6 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       bar_init(bar(bSFull + i), 1);
       bar_init(bar(bPFull + i), 4);
+      bar_init(bar(bProducts + i), 1);
+      bar_init(bar(bTold + 2 * i), 4);
+      bar_init(bar(bTold + 2 * i + 1), 4);
       bar_init(bar(bSums + i), 4);
       bar_init(bar(bODone + i), 1);
       bar_init(bar(bOFree + i), 4);
@@ -305,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(bar(bChecked + i), 1);
       odd_of[i] = 0;
     }
+    for (int i = 0; i < 4; ++i) reinterpret_cast<long long*>(sm + P::MOVES)[i] = 0;
     bar_init(bar(bDrain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -316,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (mode == kPromptCut) pdl_trigger();                            // the join's launch
   prompt_zero_rows<__nv_bfloat16>(a, D);
   PromptSpan span{};
-  if (mode != kPromptTurns) span = prompt_span<kTok, kItemCost, kThreads>(a, a.H * L::PER, kMinSpan, reinterpret_cast<int*>(sm));
+  if (mode != kPromptTurns) span = prompt_span<kTok, kItemCost, kThreads>(a, a.H, kMinSpan, reinterpret_cast<int*>(sm));
   fence_async_smem();
   tc_before();
   __syncthreads();
@@ -339,12 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     return x;
   };
 
-  // a piece of keys or a tile of values
-  auto copy = [&](const CUtensorMap* map, uint32_t dst, int ch, int head, int row, uint32_t full) {
+  // a piece of keys or of values, in panels of 64 channels
+  auto copy = [&](const CUtensorMap* map, uint32_t dst, int panel, int ch, int head, int row, uint32_t full) {
     if (lane == 0) {
       bar_arrive_tx(full, L::PIECE);
-#pragma unroll
-      for (int i = 0; i < L::PIECE / 16384; ++i) tma_rows(dst + 16384 * i, map, ch + 64 * i, head, row, full);
+      for (int i = 0; i < L::PIECE / panel; ++i) tma_rows(dst + panel * i, map, ch + 64 * i, head, row, full);
     }
     __syncwarp();
   };
@@ -355,9 +374,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int X = warp >> 2, wq = warp & 3, r = 32 * wq + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * wq) << 16);
-    const uint32_t ts = trow + col_s(X), to = trow + col_o(X);
+    const uint32_t ts = trow + col_s(X), to = trow + col_o(L::WIDE ? 0 : X);
     const float f = a.scale_log2;
-    int nS = 0, items = 0;                             // phases of S, items of this half
+    int nS = 0, items = 0, tiles = 0, other = 0;       // phases of S, items of this half, tiles of it and of the other half
+    volatile float* wide_sums = reinterpret_cast<volatile float*>(sm + P::SUMS);
+    volatile float* moved = wide_sums + 384;
+    volatile long long* moves = reinterpret_cast<volatile long long*>(sm + P::MOVES);
+    int seen_moves = 0;
     for (int n = 0;; ++n) {
       const ItemMsg it = next_item(n);
       if (!it.valid) break;
@@ -369,12 +392,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = turns ? X : 0, step = turns ? 2 : 1;
       float m = 0.0f, l = 0.0f;
       bool bigs = false;                               // a row of the warp has had an M beyond kBig
+      const int before = other;
+      if (L::WIDE) seen_moves = 0;
+      // d = 256: the other half's tile before has its weights.  Two barriers in turn: that half may be one tile further on, at
+      // the next item's first.
+      auto told = [&]() { return wait(bTold + 2 * (X ^ 1) + ((other - 1) & 1), (other - 1) / 2); };
+      // d = 256: to the M that the other half has moved to; false if it has not.
+      auto follow = [&]() {
+        const long long at = moves[wq];
+        const int now = static_cast<int>(at >> 32) == n + 1 ? static_cast<int>(at) : 0;
+        __syncwarp();
+        if (now == seen_moves) return false;
+        seen_moves = now;
+        const float to_m = moved[r];
+        l = l > 0.0f ? l * ex2(m - to_m) : l;
+        m = to_m;
+        bigs = __any_sync(0xffffffffu, live && fabsf(m) > kBig);
+        return true;
+      };
       for (int t = first; t < ntile; t += step) {
         if (!wait(bSFull + X, nS++)) break;
         tc_after();
         const int j0 = it.first_key(t);
+        if (L::WIDE) other = before + (t + X) / 2;     // the other half's tiles up to this one
         bool done = false;
-        if (!bigs) {
+        for (bool again = true; again;) {              // (twice where the other half has moved M meanwhile)
+          again = false;
+          if (bigs) break;
           float x[kTok];
           uint32_t w[kTok / 2];
           tld32x4(ts, x);
@@ -411,6 +455,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           float s0, s1;
           unpack2(add2(s2, s3), s0, s1);
           s0 += s1;
+          if (L::WIDE && t > 0) {
+            // The tile before is the other half's: its weights are there, and M is what they were made with.
+            if (!told()) break;
+            if (follow()) {
+              again = true;
+              continue;
+            }
+          }
           if (!__any_sync(0xffffffffu, sees && (s0 > kFull || l + s0 < kTiny))) {
             l += s0;
             tst32(ts, *reinterpret_cast<uint32_t(*)[32]>(w));
@@ -418,22 +470,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             done = true;
           }
         }
+        if (failed) break;
         if (!done) {
-          const float2 next = careful_tile<L::DV>(ts, to, j0, p, a.window, a.sinks, f, t > first, m, l);
+          if (L::WIDE && t > 0) {                      // O is at rest behind the products of the tile before
+            if (!told() || !wait(bProducts + (X ^ 1), other - 1)) break;
+            tc_after();
+            (void)follow();
+          } else if (L::WIDE && items > 0 && !wait(bOFree, items - 1)) {     // (the item before has M in its results)
+            break;
+          }
+          bool had = l > 0.0f;                         // has the row seen anything?
+          if (L::WIDE)
+            for (int i = 0; i < t && !had; ++i)
+              for (int c = 0; c < kTok; c += 32) had |= seen32(p, it.first_key(i) + c, a.window, a.sinks) != 0u;
+          __syncwarp();
+          const float2 next = careful_tile<D>(ts, to, j0, p, a.window, a.sinks, f, L::WIDE ? t > 0 : t > first, m, l, had, L::WIDE);
           m = next.x;
           l = next.y;
           bigs = __any_sync(0xffffffffu, live && fabsf(m) > kBig);
+          if (L::WIDE) {
+            moved[r] = m;
+            ++seen_moves;
+            __syncwarp();
+            if (lane == 0) moves[wq] = (static_cast<long long>(n + 1) << 32) | seen_moves;
+            __syncwarp();
+          }
         }
         tst_wait();
         tc_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(bar(bPFull + X));
+        if (lane == 0) {
+          bar_arrive(bar(bPFull + X));
+          if (L::WIDE) bar_arrive(bar(bTold + 2 * X + (tiles & 1)));
+        }
+        ++tiles;
       }
       if (failed) break;
+      if (L::WIDE) other = before + (X ? (ntile + 1) / 2 : ntile / 2);
       if (first >= ntile) continue;                    // one tile in one half: nothing for B
       if (items > 0 && !wait(bOFree + X, items - 1)) break;      // the sums before were taken
       ++items;
-      sums[128 * X + r] = make_float2(l == 0.0f ? -INFINITY : m, l);      // M of nothing counts below every other
+      if (L::WIDE) {
+        wide_sums[128 * X + r] = l;
+        wide_sums[(((ntile - 1) & 1) == X ? 384 : 256) + r] = m;
+      } else {
+        sums[128 * X + r] = make_float2(l == 0.0f ? -INFINITY : m, l);       // M of nothing counts below every other
+      }
       __syncwarp();
       if (lane == 0) bar_arrive(bar(bSums + X));
     }
@@ -448,7 +530,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const ItemMsg it = next_item(n);
       if (!it.valid) break;
       const bool turns = it.rows <= half, joins = turns && it.ntile > 1;
-      const int ch0 = it.h % L::PER * L::DV, hkv = it.h / L::PER;
 #pragma unroll 1
       for (int X = 0; X < (turns ? 1 : 2); ++X) {
         const int rx = half * X + r, gr = it.r0 + rx, tok = gr / a.G, p = it.p0 + tok;
@@ -458,13 +539,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (X) ++nO1;
         else ++nO0;
         if (joins) {
-          if (!wait(bSums + 1, nO1) || !wait(bODone + 1, nO1)) break;
+          if (!wait(bSums + 1, nO1) || (!L::WIDE && !wait(bODone + 1, nO1))) break;
           ++nO1;
         }
         tc_after();
-        const float2 mine = sums[128 * X + r];
+        float2 mine = sums[128 * X + r];
+        if (L::WIDE) {                                 // one O, by the M of the half that ends last
+          const float* w = reinterpret_cast<const float*>(sm + P::SUMS);
+          const int last = (it.ntile - 1) & 1;
+          mine = make_float2(w[384 + r], w[128 * last + r]);
+          const float l2 = joins ? w[128 * (last ^ 1) + r] : 0.0f;
+          mine.y += l2 > 0.0f ? l2 * ex2(w[256 + r] - mine.x) : l2;
+        }
         float m = mine.x, l = mine.y, fa = 1.0f, fb = 0.0f;
-        if (joins) {
+        if (joins && !L::WIDE) {
           const float2 other = sums[128 + r];
           m = fmaxf(mine.x, other.x);
           fa = m == -INFINITY ? 1.0f : ex2(mine.x - m);
@@ -474,9 +562,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (X == 0 && !wait(bChecked + n % kCheckRing, n / kCheckRing)) break;
         const bool odd = __any_sync(0xffffffffu, odd_of[n % kCheckRing] == n + 1);
         if (__builtin_expect(odd, 0)) {
-          if (joins) {                                 // (the sums first)
+          if (joins && !L::WIDE) {                     // (the sums first)
 #pragma unroll 1
-            for (int c = 0; c < L::DV / 16; ++c) {
+            for (int c = 0; c < D / 16; ++c) {
               float o[16], o2[16];
               uint32_t u[16];
               tld16(to + 16u * c, o);
@@ -488,17 +576,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             tst_wait();
             fa = 1.0f;
           }
-          add_odd_values<L::DV>(to, static_cast<const __nv_bfloat16*>(a.v) + it.k0 * a.vs + static_cast<long long>(hkv) * D + ch0, a.vs, it.t0,
-                                it.ntile, it.ns, it.w0, it.pmin, it.pmax, p, a.window, a.sinks);
+          add_odd_values<D>(to, static_cast<const __nv_bfloat16*>(a.v) + it.k0 * a.vs + static_cast<long long>(it.h) * D, a.vs, it.t0, it.ntile,
+                            it.ns, it.w0, it.pmin, it.pmax, p, a.window, a.sinks);
         }
-        const bool both = joins && !odd;
+        const bool both = joins && !odd && !L::WIDE;
         const float inv = it.slot < 0 ? prompt_inverse(l, p) : 1.0f;
         fa *= inv;
         fb *= inv;
-        const long long at = ((static_cast<long long>(it.q0) + tok) * a.Hq + hkv * a.G + (gr - tok * a.G)) * D + ch0;
+        const long long at = ((static_cast<long long>(it.q0) + tok) * a.Hq + it.h * a.G + (gr - tok * a.G)) * D;
         float* part = parts + (static_cast<long long>(it.slot) * L::ROWS + rx) * L::PART;
 #pragma unroll 1
-        for (int c = 0; c < L::DV / 32; ++c) {
+        for (int c = 0; c < D / 32; ++c) {
           float o[32];
           tld32(to + 32u * c, o);
 #pragma unroll
@@ -528,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float4* dst = reinterpret_cast<float4*>(part + 4 + 32 * c);
 #pragma unroll
             for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            if (c == 0) *reinterpret_cast<float4*>(part) = make_float4(m, l, 0.0f, 0.0f);
+            if (c == 0) *reinterpret_cast<float4*>(part) = make_float4(l == 0.0f ? -INFINITY : m, l, 0.0f, 0.0f);
           }
           __syncwarp();                                // lanes with no row wait: the loads are the whole warp's
         }
@@ -564,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const PromptBlock& b = w.blk;
         publish(ItemMsg{1, w.h, b.seq.q0, b.r0, b.rows, b.seq.m - b.seq.n, b.pmin, b.pmax, w.t1 - w.t0, w.t0, w.slot, b.seq.k0, b.ns, b.w0, {0, 0}});
         q_left = b.rows <= half ? 1 : 2;
-        q_head = w.h / L::PER * a.G;
+        q_head = w.h * a.G;
         q_row = b.seq.q0 + b.r0 / a.G;
       };
       // The halves of queries of the item that was announced last: ahead of time, as soon as a room is free (wait: all of
@@ -584,18 +672,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       };
-      w.start(a, span, a.H * L::PER, mode);
+      w.start(a, span, a.H, mode);
       bool more = w.next(a, span);
       while (!failed && more) {
         // The item's copies from what is kept of it here: the next one is looked up (and announced) behind the first of them.
         const PromptBlock b = w.blk;
-        const int wh = w.h, t0 = w.t0, t1 = w.t1;
+        const int head = w.h, t0 = w.t0, t1 = w.t1;
         if (n == 0) announce();
-        const int head = wh / L::PER, ahead = b.rows <= half ? 2 : 1;     // a tile's scores are issued so many steps before its values
+        const int ahead = b.rows <= half ? 2 : 1;      // a tile's scores are issued so many steps before its values
         auto keys = [&](int t) {
           for (int i = 0; i < L::KCH; ++i, ++ck) {
             if (ck >= L::KST && !wait(bKFree + ck % L::KST, ck / L::KST - 1)) return;
-            copy(&mk, sb + L::K + (ck % L::KST) * L::PIECE, 128 * i, head, b.seq.k0 + b.first_key<kTok>(t), bar(bKFull + ck % L::KST));
+            copy(&mk, sb + L::K + (ck % L::KST) * L::PIECE, 16384, 128 * i, head, b.seq.k0 + b.first_key<kTok>(t), bar(bKFull + ck % L::KST));
           }
         };
         // (the queries ahead of the second tile's keys, whose room may come free by the first one's scores)
@@ -667,8 +755,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit_warp(bar(bSFull + X));
         if (last) mma_commit_warp(bar(bQFree + qi % L::QST));
       };
+      auto values_there = [&]() { return ready(bVOk + cv % L::VST, cv / L::VST); };
+      auto values_done = [&]() { mma_commit_warp(bar(bVFree + cv % L::VST)); };
+      // O of half X (at d = 256: of both) with a tile's weights; false where a wait gave up
       auto values = [&](uint32_t X, bool first) {
-        mma8_values(tmem + col_o(X), tmem + col_s(X), vdesc(sb + L::V + (cv % L::VST) * L::PIECE), idesc_bf16(L::DV) | (1u << 16), first ? 0u : 1u);
+        if (!L::WIDE) {
+          mma8_values(tmem + col_o(X), tmem + col_s(X), vdesc(sb + L::V + (cv % L::VST) * L::PIECE), idesc_bf16(D) | (1u << 16), first ? 0u : 1u);
+          return true;
+        }
+        // 64 tokens a piece: panels 8 KB apart
+        auto desc = [&]() { return vdesc(sb + L::V + (cv % L::VST) * L::PIECE) - (static_cast<uint64_t>((16384 - 8192) >> 4) << 16); };
+        mma4_values(tmem + col_o(0), tmem + col_s(X), desc(), idesc_bf16(D) | (1u << 16), first ? 0u : 1u);
+        values_done();
+        ++cv;
+        if (!values_there()) return false;
+        tc_after();
+        mma4_values(tmem + col_o(0), tmem + col_s(X) + 32u, desc(), idesc_bf16(D) | (1u << 16), 1u);
+        mma_commit_warp(bar(bProducts + X));
+        return true;
       };
       // An item's first scores of half X (two halves: of one tile; else of the first two tiles).
       auto begin = [&](const Item& it, uint32_t X) {
@@ -700,10 +804,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < tiles; ++t, ++cv) {
             const bool last = t == tiles - 1;
             if (last) nx = take();                     // (ahead of the waits, beside the softmax)
-            ok = ready(bVOk + cv % L::VST, cv / L::VST) && ready(bPFull, np0++) && (t > 0 || room(0));
+            ok = values_there() && ready(bPFull, np0++) && (t > 0 || room(0));
             if (!ok) break;
             tc_after();
-            values(0, t == 0);
+            (void)values(0, t == 0);
             if (last) {
               mma_commit_warp(bar(bODone));
               ok = begin(nx, 0);
@@ -714,8 +818,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && ready(bPFull + 1, np1++) && (t > 0 || room(1));
             if (!ok) break;
             tc_after();
-            values(1, t == 0);
-            mma_commit_warp(bar(bVFree + cv % L::VST));
+            (void)values(1, t == 0);
+            values_done();
             if (last) {
               mma_commit_warp(bar(bODone + 1));
               ok = begin(nx, 1);
@@ -728,11 +832,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < tiles; ++t, ++cv) {
             const uint32_t X = t & 1;
             if (X == 0 && t + 2 >= tiles) nx = take(); // half A's last tile
-            ok = ready(bVOk + cv % L::VST, cv / L::VST) && ready(bPFull + X, X ? np1++ : np0++) && (t > 1 || room(X));
+            ok = values_there() && ready(bPFull + X, X ? np1++ : np0++) && (t > (L::WIDE ? 0 : 1) || room(X));
             if (!ok) break;
             tc_after();
-            values(X, t < 2);
-            mma_commit_warp(bar(bVFree + cv % L::VST));
+            ok = values(X, t < (L::WIDE ? 1 : 2));
+            if (!ok) break;
+            values_done();
             if (t + 2 < tiles) {
               ok = keys_there();
               if (!ok) break;
@@ -740,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               keys_done();
               continue;
             }
-            mma_commit_warp(bar(bODone + X));
+            if (!L::WIDE || t == tiles - 1) mma_commit_warp(bar(bODone + (L::WIDE ? 0 : X)));
             if (X == 0) {                              // half A is free
               ok = begin(nx, 0);
               if (!ok) break;
@@ -763,16 +868,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!it.valid) break;
         const int ntile = it.ntile;
         bool any = false;
-        for (int t = 0; t < ntile; ++t, ++cv) {
+        for (int i = 0; i < ntile * L::VCH; ++i, ++cv) {
           if (!wait(bVFull + cv % L::VST, cv / L::VST)) break;
-          if (!it.full(it.first_key(t), a.window, a.sinks)) {
+          if (!it.full(it.first_key(i / L::VCH), a.window, a.sinks)) {
             const uint32_t at = sb + L::V + (cv % L::VST) * L::PIECE + lane * 16;
             uint32_t most = 0u;                        // largest magnitudes: bf16 bits order as integers
 #pragma unroll 1
-            for (int i = 0; i < L::PIECE; i += 512 * 8) {
+            for (int k0 = 0; k0 < L::PIECE; k0 += 512 * 8) {
               uint4 v[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] = lds128(at + i + 512 * k);
+              for (int k = 0; k < 8; ++k) v[k] = lds128(at + k0 + 512 * k);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 most = __vmaxu2(__vmaxu2(most, v[k].x & 0x7FFF7FFFu), v[k].y & 0x7FFF7FFFu);
@@ -782,15 +887,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (__any_sync(0xffffffffu, odd_pair(most))) {
               any = true;
 #pragma unroll 1
-              for (int i = 0; i < L::PIECE; i += 512) {
-                const uint4 v = lds128(at + i);
+              for (int k0 = 0; k0 < L::PIECE; k0 += 512) {
+                const uint4 v = lds128(at + k0);
                 uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                   if ((u[q] & 0x7F80u) == 0x7F80u) u[q] &= 0xFFFF0000u;
                   if ((u[q] & 0x7F800000u) == 0x7F800000u) u[q] &= 0xFFFFu;
                 }
-                sts128(at + i, u[0], u[1], u[2], u[3]);
+                sts128(at + k0, u[0], u[1], u[2], u[3]);
               }
               fence_async_smem();
             }
@@ -812,10 +917,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const ItemMsg it = next_item(n);
         if (!it.valid) break;
         const int ntile = it.ntile;
-        for (int t = 0; t < ntile; ++t, ++cv) {
-          if (cv >= L::VST && !wait(bVFree + cv % L::VST, cv / L::VST - 1)) break;
-          copy(&mv, sb + L::V + (cv % L::VST) * L::PIECE, it.h % L::PER * L::DV, it.h / L::PER, it.k0 + it.first_key(t), bar(bVFull + cv % L::VST));
-        }
+        for (int t = 0; t < ntile && !failed; ++t)
+          for (int i = 0; i < L::VCH; ++i, ++cv) {
+            if (cv >= L::VST && !wait(bVFree + cv % L::VST, cv / L::VST - 1)) break;
+            copy(&mv, sb + L::V + (cv % L::VST) * L::PIECE, 128 * L::VTOK, 0, it.h, it.k0 + it.first_key(t) + i * L::VTOK, bar(bVFull + cv % L::VST));
+          }
       }
       // copies still in flight land before the CTA ends
       bool f2 = false;
@@ -860,12 +966,12 @@ cudaError_t launch_t(const PromptArgs& args, cudaStream_t s) {
   a.rows = L::HALVES * tokens * a.G;
   CUtensorMap mq, mk, mv;
   if (!rows_map(&mq, a.q, D, a.Hq, a.total_q, a.qs, a.G, tokens) || !rows_map(&mk, a.k, D, a.H, a.total_k, a.ks, 1, kTok) ||
-      !rows_map(&mv, a.v, D, a.H, a.total_k, a.vs, 1, kTok))
+      !rows_map(&mv, a.v, D, a.H, a.total_k, a.vs, 1, L::VTOK))
     return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = smem_attr_once(prompt_tc_kernel<D>, PS<D>::BYTES, configured);
   if (e != cudaSuccess) return e;
-  const long long items = prompt_most_blocks(a) * a.H * L::PER, tiles = a.max_k / kTok + 2 + a.sinks / kTok;
+  const long long items = prompt_most_blocks(a) * a.H, tiles = a.max_k / kTok + 2 + a.sinks / kTok;
   // items of few tiles are not cut (and need no join)
   // (nor are few of them listed: the list takes 4 us)
   const int sms = prompt_sms();
@@ -874,7 +980,7 @@ cudaError_t launch_t(const PromptArgs& args, cudaStream_t s) {
   const int ctas = static_cast<int>(most < sms ? (most < 1 ? 1 : most) : sms);
   e = launch_pdl(prompt_tc_kernel<D>, dim3(ctas), dim3(kThreads), PS<D>::BYTES, s, a, mq, mk, mv, mode);
   if (e != cudaSuccess || mode != kPromptCut) return e;
-  return launch_prompt_join(a, D, false, ctas, L::ROWS, L::PER, s);
+  return launch_prompt_join(a, D, false, ctas, L::ROWS, s);
 }
 
 }  // namespace
@@ -884,8 +990,8 @@ bool prompt_tc_takes(const PromptArgs& a, int d, bool f32) {
 }
 
 size_t prompt_tc_workspace(int d) {
-  const int rows = d == 256 ? 128 : 256, dv = d == 256 ? 128 : d;
-  return static_cast<size_t>(prompt_sms()) * (sizeof(PSplit) + 2 * sizeof(float) * rows * (dv + 4));
+  const int rows = d == 256 ? 128 : 256;
+  return static_cast<size_t>(prompt_sms()) * (sizeof(PSplit) + 2 * sizeof(float) * rows * (d + 4));
 }
 
 cudaError_t launch_prompt_tc(const PromptArgs& a, int d, cudaStream_t s) {
