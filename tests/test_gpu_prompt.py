@@ -287,6 +287,29 @@ def test_large_scores(dtype, d, size):
         assert bool(((out[t].double() - want).abs() <= tol).all()), t
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 128)])
+@pytest.mark.parametrize("kind", ["rising", "falling", "tiles", "rows", "far below", "steps"])
+@pytest.mark.parametrize("new,keys,window", [([700], [700], 0), ([300, 1, 20, 200], [1300, 900, 20, 333], 0), ([260, 70], [1500, 70], 400)])
+def test_maxima_that_move(dtype, d, kind, new, keys, window):
+    """Scores whose size changes along the keys and the rows: hundreds and thousands (in powers of two) up or down from one
+    tile to the next, in one half's tiles and not in the other's, all of them far below zero."""
+    def change(q, k, v):
+        j = torch.arange(k.shape[0], device=DEV)
+        t = torch.arange(q.shape[0], device=DEV)
+        size = {"rising": 1.0 + j / 16, "falling": 80.0 - (j % 1500) / 20, "tiles": torch.where(j // 128 % 2 == 0, 1.0, 60.0),
+                "rows": torch.ones_like(j, dtype=torch.float), "far below": 40.0 + j % 128 / 8,
+                "steps": 2.0 ** (j // 100 % 9).float()}[kind]
+        if kind == "far below":                       # a direction that every key has and every query is against
+            k[:, :, 0], q[:, :, 0] = 0.0, -30.0
+            k += 0.0
+            k[:, :, 0] = size[:, None].to(k.dtype)
+        else:
+            k *= size.to(k.dtype)[:, None, None]
+        if kind == "rows":
+            q *= (2.0 ** (t % 11 - 2).float()).to(q.dtype)[:, None, None]
+    attend(dtype, d, 8, 2, new, keys, window=window, change=change)
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 128)])
 def test_many_sequences_and_blocks(dtype, d):
     """More sequences than the list of spans holds, and more blocks."""
