@@ -12,7 +12,8 @@
 //   out = O / l.
 // The halves take turns: while the softmax of one runs, the tensor cores work on the other.  An item follows the one
 // before like a tile does: its queries are there ahead of time (a ring of halves), and its results are left to warps of
-// their own.  Tensor memory: S of A and B (each overlaid by its weights), O of A and B, 512 columns.  An item that fits one
+// their own.  Tensor memory: S of A and B (each overlaid by its weights), O of A and B, 512 columns; at d = 64, where O takes
+// half of that, S has three rooms in turn and the scores run a half's tile further ahead.  An item that fits one
 // half is in both: A takes the even tiles, B the odd ones, and their sums are added at the end.  At d = 256 every item is
 // one half of rows, in the same turns, and tensor memory has one O of 256 columns, to which both add: M is the row's in
 // both, and a half that moves it does so between the other's products.
@@ -60,6 +61,7 @@ struct PG {
   static constexpr bool WIDE = D == 256;
   static constexpr int HALVES = WIDE ? 1 : 2;          // of query rows per item
   static constexpr int ROWS = 128 * HALVES;
+  static constexpr int SB = D == 64 ? 3 : 2;           // rooms of S, 128 columns each
   static constexpr int VCH = WIDE ? 2 : 1, VTOK = kTok / VCH;      // pieces of a tile's values, and their tokens
   static constexpr int KCH = D > 128 ? D / 128 : 1;    // pieces of a tile's keys, 128 channels each
   static constexpr int PIECE = kTok * 2 * (D < 128 ? D : 128);      // bytes of a piece
@@ -74,7 +76,7 @@ struct PG {
 };
 enum Bar {
   bQFull = 0, bQFree = bQFull + 4, bKFull = bQFree + 4, bKFree = bKFull + 5, bVFull = bKFree + 5, bVFree = bVFull + 5, bVOk = bVFree + 5,
-  bSFull = bVOk + 5, bPFull = bSFull + 2, bProducts = bPFull + 2, bTold = bProducts + 2, bSums = bTold + 4, bODone = bSums + 2, bOFree = bODone + 2, bItem = bOFree + 2,
+  bSFull = bVOk + 5, bPFull = bSFull + 6, bProducts = bPFull + 3, bTold = bProducts + 2, bSums = bTold + 4, bODone = bSums + 2, bOFree = bODone + 2, bItem = bOFree + 2,
   bItemFree = bItem + kItems, bChecked = bItemFree + kItems, bDrain = bChecked + kCheckRing, bCount
 };
 template <int D>
@@ -83,14 +85,30 @@ struct PS {                                            // behind the barriers
                                                                          // that ends first, M] of 128 rows
   static constexpr int ODD = SUMS + 2 * 128 * 8;   // per item: values that are not finite in edge tiles
   static constexpr int MOVES = ODD + 4 * kCheckRing;   // d = 256: how often M has moved, by 32 rows: item + 1, times
-  static constexpr int TMEM = MOVES + 32;
+  static constexpr int QUEUE = MOVES + 32;             // of the MMA warp, four words
+  static constexpr int TMEM = QUEUE + 16;
   static constexpr int BYTES = TMEM + 16;
 };
 static_assert(PS<64>::BYTES <= 232448 && PS<128>::BYTES <= 232448 && PS<256>::BYTES <= 232448, "shared memory per block");
 static_assert(PG<64>::ITEM >= 4 * (2 * kPromptList + 64), "the list's room");
-__device__ __forceinline__ constexpr uint32_t col_s(uint32_t X) { return 128u * X; }
-__device__ __forceinline__ constexpr uint32_t col_o(uint32_t X) { return 256u + 128u * X; }
+template <int D>
+__device__ __forceinline__ constexpr uint32_t col_o(uint32_t X) { return D == 64 ? 384u + 64u * X : D == 128 ? 256u + 128u * X : 256u; }
 
+// A place in a ring of N and its phase: counted where N divides without effort, else kept.
+template <int N>
+struct Ring {
+  static constexpr bool COUNTS = (N & (N - 1)) == 0;
+  int at = 0, turn = 0;
+  __device__ __forceinline__ int place() const { return COUNTS ? at & (N - 1) : at; }
+  __device__ __forceinline__ int phase() const { return COUNTS ? at / N : turn; }
+  __device__ __forceinline__ void next() {
+    ++at;
+    if (!COUNTS && at == N) {
+      at = 0;
+      turn ^= 1;
+    }
+  }
+};
 // What the load warp tells the others of an item.
 struct alignas(16) ItemMsg {
   int valid, h, q0, r0;                   // h: KV head
@@ -307,8 +325,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(bar(bVOk + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(bar(bSFull + i), 1);
-      bar_init(bar(bPFull + i), 4);
       bar_init(bar(bProducts + i), 1);
       bar_init(bar(bTold + 2 * i), 4);
       bar_init(bar(bTold + 2 * i + 1), 4);
@@ -316,6 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(bar(bODone + i), 1);
       bar_init(bar(bOFree + i), 4);
     }
+    for (int i = 0; i < L::SB; ++i) bar_init(bar(bPFull + i), 4);
+    // S of a half's tiles: as many barriers as rooms, in turn.  One that both halves waited on would pass B by while items
+    // have one tile, and one per half would pass A by, whose scores may be three tiles ahead there.
+    for (int i = 0; i < 2 * L::SB; ++i) bar_init(bar(bSFull + i), 1);
     for (int i = 0; i < kItems; ++i) {
       bar_init(bar(bItem + i), 1);
       bar_init(bar(bItemFree + i), 15);                // every warp but the one that announces
@@ -374,9 +394,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int X = warp >> 2, wq = warp & 3, r = 32 * wq + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * wq) << 16);
-    const uint32_t ts = trow + col_s(X), to = trow + col_o(L::WIDE ? 0 : X);
+    const uint32_t to = trow + col_o<D>(X);
     const float f = a.scale_log2;
-    int nS = 0, items = 0, tiles = 0, other = 0;       // phases of S, items of this half, tiles of it and of the other half
+    int unit = 0, items = 0, tiles = 0, other = 0;     // halves' tiles before the item; items of this half, tiles of it and of the other half
     volatile float* wide_sums = reinterpret_cast<volatile float*>(sm + P::SUMS);
     volatile float* moved = wide_sums + 384;
     volatile long long* moves = reinterpret_cast<volatile long long*>(sm + P::MOVES);
@@ -411,7 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       for (int t = first; t < ntile; t += step) {
-        if (!wait(bSFull + X, nS++)) break;
+        const int u = unit + (turns ? t : 2 * t + X), room = u % L::SB;
+        const uint32_t ts = trow + 128u * static_cast<uint32_t>(room);
+        if (!wait(bSFull + X * L::SB + tiles % L::SB, tiles / L::SB)) break;
         tc_after();
         const int j0 = it.first_key(t);
         if (L::WIDE) other = before + (t + X) / 2;     // the other half's tiles up to this one
@@ -478,6 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             (void)follow();
           } else if (L::WIDE && items > 0 && !wait(bOFree, items - 1)) {     // (the item before has M in its results)
             break;
+          } else if (L::SB > 2 && t > first) {         // (with two rooms the scores come behind them)
+            if (!wait(bProducts + X, tiles - 1)) break;
+            tc_after();
           }
           bool had = l > 0.0f;                         // has the row seen anything?
           if (L::WIDE)
@@ -500,12 +525,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_before();
         __syncwarp();
         if (lane == 0) {
-          bar_arrive(bar(bPFull + X));
+          bar_arrive(bar(bPFull + room));
           if (L::WIDE) bar_arrive(bar(bTold + 2 * X + (tiles & 1)));
         }
         ++tiles;
       }
       if (failed) break;
+      unit += turns ? ntile : 2 * ntile;
       if (L::WIDE) other = before + (X ? (ntile + 1) / 2 : ntile / 2);
       if (first >= ntile) continue;                    // one tile in one half: nothing for B
       if (items > 0 && !wait(bOFree + X, items - 1)) break;      // the sums before were taken
@@ -534,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int X = 0; X < (turns ? 1 : 2); ++X) {
         const int rx = half * X + r, gr = it.r0 + rx, tok = gr / a.G, p = it.p0 + tok;
         const bool live = r < half && rx < it.rows;
-        const uint32_t to = trow + col_o(X);
+        const uint32_t to = trow + col_o<D>(X);
         if (!wait(bSums + X, X ? nO1 : nO0) || !wait(bODone + X, X ? nO1 : nO0)) break;
         if (X) ++nO1;
         else ++nO0;
@@ -568,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float o[16], o2[16];
               uint32_t u[16];
               tld16(to + 16u * c, o);
-              tld16(trow + col_o(1) + 16u * c, o2);
+              tld16(trow + col_o<D>(1) + 16u * c, o2);
 #pragma unroll
               for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(fa * o[k] + fb * o2[k]);
               tst16(to + 16u * c, u);
@@ -595,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               float o2[16];
-              tld16(trow + col_o(1) + 32u * c + 16u * q, o2);
+              tld16(trow + col_o<D>(1) + 32u * c + 16u * q, o2);
 #pragma unroll
               for (int k = 0; k < 16; ++k) o[16 * q + k] = fmaf(fb, o2[k], o[16 * q + k]);
             }
@@ -708,153 +734,113 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = cq >= L::QST ? cq - L::QST : 0; s < cq; ++s) (void)bar_wait(bar(bQFull + s % L::QST), (s / L::QST) & 1, f2);
       for (int s = ck >= L::KST ? ck - L::KST : 0; s < ck; ++s) (void)bar_wait(bar(bKFull + s % L::KST), (s / L::KST) & 1, f2);
     } else if (warp == 13) {
-      // ---- MMA issue, the warp converged: O += w V of a tile and the next tile's scores, half A, then half B, in strict
-      // order (left to mix, both halves' MMAs would end together and neither softmax overlap the other); behind an item's
-      // last tile come the next item's first scores ----------------------------------------------------------------------
+      // ---- MMA issue, the warp converged: O += w V of a half's tile, then the scores of a later one, in strict order of the
+      // halves (left to mix, both halves' MMAs would end together and neither softmax overlap the other).  Between a
+      // softmax's end and its next scores stands what this warp executes in between, so that few instructions count: with
+      // a loop per kind of item, a queue in registers and rings by division a d = 64 prompt of 8,192 took 279 us, not 256,
+      // and two dozen d = 128 prompts 341, not 309 -------------------------------------------------------------------------
       auto ready = [&](int i, int phase) {             // wait() in few instructions
         if (__all_sync(0xffffffffu, wait_short(bar(i), phase & 1))) return true;
         failed = true;
         return false;
       };
-      int n = 0, cq = 0, ck = 0, cv = 0;               // items taken; halves of queries, pieces of keys, tiles of values used
-      int np0 = 0, np1 = 0, no0 = 0, no1 = 0;          // phases of the weights, and items of the halves (their O)
-      struct Item {
-        int tiles, qa, qb;                             // halves of queries: A's and B's
-        bool open, two;                                // two: rows in half B
-      };
-      // The next item; its first scores are started half by half.
+      // A unit is a half's tile; units have the rooms of S in turn.  The scores are SB units ahead of the values, over items.
+      int n = 0, no0 = 0, no1 = 0;                     // items taken; items of the halves (their O)
+      Ring<L::QST> queries;                            // halves of queries
+      Ring<L::KST> keys_at;                            // pieces of keys and of values
+      Ring<L::VST> values_at;
+      Ring<L::SB> scores_a, scores_b, weights_at;      // tiles of A, of B; units
+      // items between the scores and the values: 2 * units + two, 0 for the end
+      volatile int* queue = reinterpret_cast<volatile int*>(sm + P::QUEUE);
+      // the scores' item: its units, the next of them, its first half of queries
+      int units = 0, su = 0;
+      Ring<L::QST> qa;
+      bool two = false;                                // rows in half B
       auto take = [&]() {
-        const ItemMsg x = next_item(n++);
-        Item it;
-        it.open = __all_sync(0xffffffffu, x.valid) && !failed;
-        it.tiles = uniform(it.open ? x.ntile : 0);
-        it.two = __all_sync(0xffffffffu, x.rows > half);
-        it.qa = cq;
-        it.qb = it.two ? cq + 1 : cq;
-        if (it.open) cq += it.two ? 2 : 1;
-        return it;
+        const ItemMsg x = next_item(n);
+        const bool open = __all_sync(0xffffffffu, x.valid) && !failed;
+        two = open && __all_sync(0xffffffffu, x.rows > half);
+        units = uniform(open ? (two ? 2 * x.ntile : x.ntile) : 0);
+        su = 0;
+        qa = queries;
+        if (open) queries.next();
+        if (two) queries.next();
+        queue[n % 4] = 2 * units + (two ? 1 : 0);      // (every lane the same)
+        __syncwarp();
+        ++n;
       };
-      auto keys_there = [&]() {                        // of the next tile's scores
-        for (int i = 0; i < L::KCH; ++i)
-          if (!ready(bKFull + (ck + i) % L::KST, (ck + i) / L::KST)) return false;
-        return true;
-      };
-      auto keys_done = [&]() {
-        for (int i = 0; i < L::KCH; ++i, ++ck) mma_commit_warp(bar(bKFree + ck % L::KST));
-      };
-      // scores of half X with queries qi and the keys from piece ck on
-      auto scores = [&](uint32_t X, int qi, bool last) {
-        const uint32_t q = sb + L::Q + (qi % L::QST) * L::QX;
-        auto keys = [&](int i) { return sdesc(sb + L::K + ((ck + i) % L::KST) * L::PIECE); };
+      take();
+      // The scores of the next unit, if there is one.
+      auto scores = [&](uint32_t to) {
+        if (!units) return true;
+        const bool b = su & 1, second = two && b;
+        Ring<L::QST> qi = qa;
+        if (second) qi.next();
+        if (!second)                                   // (a tile's pieces have one phase)
+          for (int i = 0; i < L::KCH; ++i)
+            if (!ready(bKFull + keys_at.place() + i, keys_at.phase())) return false;
+        if (su <= (two ? 1 : 0) && !ready(bQFull + qi.place(), qi.phase())) return false;
+        tc_after();
+        const uint64_t q = sdesc(sb + L::Q + qi.place() * L::QX);
+        auto keys = [&](int i) { return sdesc(sb + L::K + (keys_at.place() + i) * L::PIECE); };
         if (D == 64) {
-          mma4_scores(tmem + col_s(X), sdesc(q), keys(0), idesc_bf16(128));
+          mma4_scores(to, q, keys(0), idesc_bf16(128));
         } else {
-          mma8_scores<0>(tmem + col_s(X), sdesc(q), keys(0), idesc_bf16(128));
-          if (L::WIDE) mma8_scores<1>(tmem + col_s(X), sdesc(q + 32768), keys(1), idesc_bf16(128));
+          mma8_scores<0>(to, q, keys(0), idesc_bf16(128));
+          if (L::WIDE) mma8_scores<1>(to, q + (32768 >> 4), keys(1), idesc_bf16(128));
         }
-        mma_commit_warp(bar(bSFull + X));
-        if (last) mma_commit_warp(bar(bQFree + qi % L::QST));
+        mma_commit_warp(bar(bSFull + (b ? L::SB + scores_b.place() : scores_a.place())));
+        if (b) scores_b.next();
+        else scores_a.next();
+        if (!two || b)
+          for (int i = 0; i < L::KCH; ++i, keys_at.next()) mma_commit_warp(bar(bKFree + keys_at.place()));
+        su += 1;
+        if (su + (two ? 1 : 0) >= units) mma_commit_warp(bar(bQFree + qi.place()));
+        if (su == units) take();
+        return !failed;
       };
-      auto values_there = [&]() { return ready(bVOk + cv % L::VST, cv / L::VST); };
-      auto values_done = [&]() { mma_commit_warp(bar(bVFree + cv % L::VST)); };
-      // O of half X (at d = 256: of both) with a tile's weights; false where a wait gave up
-      auto values = [&](uint32_t X, bool first) {
-        if (!L::WIDE) {
-          mma8_values(tmem + col_o(X), tmem + col_s(X), vdesc(sb + L::V + (cv % L::VST) * L::PIECE), idesc_bf16(D) | (1u << 16), first ? 0u : 1u);
-          return true;
-        }
-        // 64 tokens a piece: panels 8 KB apart
-        auto desc = [&]() { return vdesc(sb + L::V + (cv % L::VST) * L::PIECE) - (static_cast<uint64_t>((16384 - 8192) >> 4) << 16); };
-        mma4_values(tmem + col_o(0), tmem + col_s(X), desc(), idesc_bf16(D) | (1u << 16), first ? 0u : 1u);
-        values_done();
-        ++cv;
-        if (!values_there()) return false;
-        tc_after();
-        mma4_values(tmem + col_o(0), tmem + col_s(X) + 32u, desc(), idesc_bf16(D) | (1u << 16), 1u);
-        mma_commit_warp(bar(bProducts + X));
-        return true;
+      auto values_done = [&]() {
+        mma_commit_warp(bar(bVFree + values_at.place()));
+        values_at.next();
       };
-      // An item's first scores of half X (two halves: of one tile; else of the first two tiles).
-      auto begin = [&](const Item& it, uint32_t X) {
-        if (!it.open || (X && !it.two && it.tiles == 1)) return true;
-        if (X && it.two) {
-          if (!ready(bQFull + it.qb % L::QST, it.qb / L::QST)) return false;
+      auto values_there = [&]() { return ready(bVOk + values_at.place(), values_at.phase()); };
+      bool ok = !failed;
+      for (int i = 0; i < L::SB && ok; ++i) ok = scores(tmem + 128u * i);
+      for (int vn = 0; ok; ++vn) {
+        const int word = uniform(queue[vn % 4]), vunits = word >> 1;
+        const bool vtwo = word & 1;
+        if (!word) break;
+        for (int vu = 0; vu < vunits; ++vu, weights_at.next()) {
+          const uint32_t X = vu & 1;
+          const uint32_t w = tmem + 128u * static_cast<uint32_t>(weights_at.place());
+          if (!(vtwo && X)) ok = values_there();
+          if (ok && vu < (L::WIDE ? 1 : 2)) {          // O of the half is free: the item before it was taken from there
+            const int k = X ? no1++ : no0++;
+            ok = k == 0 || ready(bOFree + X, k - 1);
+          }
+          const uint32_t first = vu < (L::WIDE ? 1 : 2) ? 0u : 1u;
+          const uint64_t v = vdesc(sb + L::V + values_at.place() * L::PIECE);
+          ok = ok && ready(bPFull + weights_at.place(), weights_at.phase());
+          if (!ok) break;
           tc_after();
-          scores(1, it.qb, it.tiles == 1);
-          keys_done();
-          return true;
-        }
-        if (!keys_there() || (!X && !ready(bQFull + it.qa % L::QST, it.qa / L::QST))) return false;
-        tc_after();
-        scores(X, it.qa, it.two ? it.tiles == 1 : it.tiles == static_cast<int>(X) + 1);
-        if (!it.two) keys_done();
-        return true;
-      };
-      // O of half X is free: the item before it was taken from there
-      auto room = [&](uint32_t X) {
-        const int k = X ? no1++ : no0++;
-        return k == 0 || ready(bOFree + X, k - 1);
-      };
-      Item it = take();
-      bool ok = !failed && begin(it, 0) && begin(it, 1);
-      while (ok && it.open) {
-        const int tiles = it.tiles;
-        Item nx{};
-        if (it.two) {
-          for (int t = 0; t < tiles; ++t, ++cv) {
-            const bool last = t == tiles - 1;
-            if (last) nx = take();                     // (ahead of the waits, beside the softmax)
-            ok = values_there() && ready(bPFull, np0++) && (t > 0 || room(0));
-            if (!ok) break;
-            tc_after();
-            (void)values(0, t == 0);
-            if (last) {
-              mma_commit_warp(bar(bODone));
-              ok = begin(nx, 0);
-            } else {
-              ok = keys_there();
-              if (ok) scores(0, it.qa, t + 2 == tiles);
-            }
-            ok = ok && ready(bPFull + 1, np1++) && (t > 0 || room(1));
-            if (!ok) break;
-            tc_after();
-            (void)values(1, t == 0);
+          if (!L::WIDE) {
+            mma8_values(tmem + col_o<D>(X), w, v, idesc_bf16(D) | (1u << 16), first);
+            if (L::SB > 2) mma_commit_warp(bar(bProducts + X));
+          } else {                                     // 64 tokens a piece: panels 8 KB apart
+            auto desc = [&]() { return vdesc(sb + L::V + values_at.place() * L::PIECE) - (static_cast<uint64_t>((16384 - 8192) >> 4) << 16); };
+            mma4_values(tmem + col_o<D>(0), w, desc(), idesc_bf16(D) | (1u << 16), first);
             values_done();
-            if (last) {
-              mma_commit_warp(bar(bODone + 1));
-              ok = begin(nx, 1);
-            } else {
-              scores(1, it.qb, t + 2 == tiles);
-              keys_done();
-            }
-          }
-        } else {                                       // the halves' tiles in turn
-          for (int t = 0; t < tiles; ++t, ++cv) {
-            const uint32_t X = t & 1;
-            if (X == 0 && t + 2 >= tiles) nx = take(); // half A's last tile
-            ok = values_there() && ready(bPFull + X, X ? np1++ : np0++) && (t > (L::WIDE ? 0 : 1) || room(X));
+            ok = values_there();
             if (!ok) break;
             tc_after();
-            ok = values(X, t < (L::WIDE ? 1 : 2));
-            if (!ok) break;
-            values_done();
-            if (t + 2 < tiles) {
-              ok = keys_there();
-              if (!ok) break;
-              scores(X, it.qa, t + 3 == tiles);
-              keys_done();
-              continue;
-            }
-            if (!L::WIDE || t == tiles - 1) mma_commit_warp(bar(bODone + (L::WIDE ? 0 : X)));
-            if (X == 0) {                              // half A is free
-              ok = begin(nx, 0);
-              if (!ok) break;
-            }
+            mma4_values(tmem + col_o<D>(0), w + 32u, desc(), idesc_bf16(D) | (1u << 16), 1u);
+            mma_commit_warp(bar(bProducts + X));
           }
-          if (ok) ok = begin(nx, 1);
+          if (!vtwo || X) values_done();
+          if (L::WIDE ? vu == vunits - 1 : vu + 2 >= vunits) mma_commit_warp(bar(bODone + (L::WIDE ? 0 : X)));
+          ok = scores(w);
+          if (!ok) break;
         }
-        if (!ok) break;
-        it = nx;
       }
       mma_commit_warp(bar(bDrain));                    // every MMA issued completes before the CTA ends
       bool f2 = false;

@@ -320,6 +320,32 @@ def test_many_sequences_and_blocks(dtype, d):
         attend(dtype, 32, 64, 1, [2100, 50], [2100, 50], window=40)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hq,h", [(4, 1), (24, 3)])
+def test_short_and_long_prompts_in_any_order(d, hq, h):
+    """Items of one tile, of several in one half and of two halves follow each other in a block, in every order."""
+    rng = np.random.default_rng(5)
+    new = rng.choice([1, 1, 1, 2, 5, 20, 33, 40, 64, 65, 130], 400).tolist()
+    keys = [n + int(k) for n, k in zip(new, rng.choice([0, 0, 0, 1, 100, 127, 128, 300, 700], 400))]
+    attend("bf16", d, hq, h, new, keys)
+    attend("bf16", d, hq, h, new, keys, window=90, sinks=3)
+    attend("bf16", d, hq, h, [1] * 700 + [90] + [1] * 700, [3] * 700 + [500] + [2] * 700)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_more_sequences_than_the_list(d):
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 6, 2200).tolist()
+    lens[700], lens[1500] = 300, 129
+    attend("bf16", d, 2, 1, lens, [n + (i % 4) for i, n in enumerate(lens)], window=100, sinks=2)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("g", [64, 65, 100, 128, 129])
+def test_many_heads_per_kv_head(d, g):
+    attend("bf16", d, 2 * g, 2, [5, 1, 40], [5, 300, 200])
+
+
 def test_offsets_that_are_none_are_skipped_and_flagged():
     d, h = 128, 2
     ctx = ctx_for(d)

@@ -178,6 +178,57 @@ def test_what_is_out_of_range_is_skipped_and_flagged(dtype):
     tq.tq_destroy(ctx)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("batch", [511, 512, 513, 1500])
+def test_many_sequences(dtype, batch):
+    """As many as the list of pages holds, and more."""
+    ctx, p = config(128, (4, 3), (3, 3))
+    rng = np.random.default_rng(8)
+    pool = Pool(rng, ctx, p, 2, 2 * batch + 3, batch, 2)
+    lens = rng.integers(0, 18, batch)
+    lens[rng.random(batch) < 0.2] = 0
+    lens[-1] = 9
+    starts = rng.integers(0, 32 - lens + 1).tolist()
+    out, first = read(ctx, pool, dtype, starts, lens.tolist())
+    check(pool, dtype, out, starts, lens.tolist(), first)
+    tq.tq_destroy(ctx)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_captured_and_replayed(dtype):
+    """Two reads in graphs, replayed at once on two streams as starts and lengths change."""
+    ctx, p = config(128, (4, 3), (4, 3))
+    pool = Pool(np.random.default_rng(9), ctx, p, 2, 40, 3, 10)
+    dt, code = DT[dtype]
+    starts, lens, first = ints([0, 0, 0]), ints([1, 1, 1]), ints([0, 160, 320])
+    table = to_dev(pool.table)
+    outs, graphs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(2):
+        out = {k: torch.empty(480, 2 * 128, dtype=dt, device=DEV) for k in "kv"}
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tq.tq_dequantize(ctx, pool.dev["k"], pool.dev["v"], code, 3, 2, starts, lens, 160, table, pool.maxp, pool.pages, out["k"], out["v"],
+                             first, 480, stream=torch.cuda.current_stream())
+        outs.append(out)
+        graphs.append(g)
+    for s, n in (([0, 5, 30], [160, 20, 1]), ([100, 0, 3], [0, 33, 150]), ([15, 16, 17], [17, 16, 15])):
+        starts.copy_(ints(s))
+        lens.copy_(ints(n))
+        for out in outs:
+            for x in out.values():
+                x.fill_(-7)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for g, stream in zip(graphs, streams):
+                with torch.cuda.stream(stream):
+                    g.replay()
+        torch.cuda.synchronize()
+        assert tq.tq_check_device_status(ctx) == 0
+        for out in outs:
+            check(pool, dtype, out, s, n, [0, 160, 320])
+    tq.tq_destroy(ctx)
+
+
 @pytest.mark.parametrize("d,bits", [(128, (4, 3)), (64, (3, 3))])
 def test_scores_of_rows_that_were_read_are_the_decodes(d, bits):
     """Quantize, read back, and attend over the rows: the decode's results."""

@@ -252,6 +252,35 @@ def test_results_repeat_bit_for_bit(dtype, d, hq):
         assert torch.equal(b.run(), want)
 
 
+@pytest.mark.parametrize("dtype,d,hq,h", [("bf16", 64, 4, 1), ("bf16", 128, 32, 1), ("f32", 64, 4, 1)])
+def test_many_groups(dtype, d, hq, h):
+    """More groups than the list of spans holds."""
+    rng = np.random.default_rng(13)
+    sizes = rng.integers(1, 3, 2100).tolist()
+    b = Batch(13, d, hq, h, sizes, rng.choice([0, 16, 32, 160], 2100).tolist(), rng.integers(1, 40, sum(sizes)).tolist(), dtype)
+    b.check(b.run(), rows=set(range(0, sum(sizes), 37)) | {sum(sizes) - 1})
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+def test_two_streams_at_once(dtype, d):
+    """A workspace each."""
+    b = Batch(14, d, 8, 2, [9, 4], [2000, 300], [1 + 40 * i for i in range(13)], dtype)
+    want = b.run()
+    ctx = ctx_for(d)
+    max_len = max(b.lens)
+    size = tq.tq_kv8_shared_workspace_size(ctx, 13, 8, 2, 2, 9, max_len)
+    lens, starts, prefix = ints(b.lens), ints(b.starts), ints(b.prefixes)
+    work = [(torch.cuda.Stream(), torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV), torch.zeros_like(b.q)) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for stream, ws, out in work:
+            tq.tq_kv8_shared_decode_attention(ctx, b.cache, b.q, DT[dtype][1], 13, 8, lens, max_len, 2, starts, prefix, 9, d ** -0.5, out, ws, size,
+                                              stream)
+    torch.cuda.synchronize()
+    assert tq.tq_check_device_status(ctx) == 0
+    assert all(torch.equal(out, want) for _, _, out in work)
+
+
 def test_captured_and_replayed():
     """A step in a graph, replayed as lengths, prefixes and groups change, two graphs on one workspace."""
     b = Batch(11, 128, 8, 2, [8, 4], [640, 320], [100 + i for i in range(12)], "bf16")
