@@ -74,25 +74,27 @@ __device__ __forceinline__ Kv8SharedSeq kv8_group(const Kv8Attn& a, const Kv8Sha
   }
   return Kv8SharedSeq{r0, pages ? r1 - r0 : 0, 0, pages, kPage * pages - 1};
 }
-// What the tail pass and the join need of each sequence, by all threads of the prefix pass: the group that holds it by a
-// search in the ascending starts.
-__device__ __forceinline__ void kv8_share_seqs(const Kv8Attn& a, const Kv8Share& s) {
-  for (long long b = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; b < s.batch; b += static_cast<long long>(gridDim.x) * blockDim.x) {
-    int lo = 0, hi = s.groups - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (s.group_start[mid] <= b) lo = mid;
-      else hi = mid - 1;
-    }
-    const Kv8SharedSeq g = kv8_group(a, s, lo);
-    const bool in = g.n > 0 && b >= g.row && b - g.row < g.n;
-    if (!in && !(b >= s.group_start[lo] && b < s.group_start[lo + 1])) atomicOr(a.err, kErrSeqLen);   // in no group
-    s.seqs[b] = in ? make_int4(g.pages, lo, g.row, 0) : make_int4(0, 0, 0, 0);
+// Sequence b as in Kv8Share::seqs: the group that holds it by a search in the ascending starts.
+__device__ __forceinline__ int4 kv8_share_seq(const Kv8Attn& a, const Kv8Share& s, int b) {
+  int lo = 0, hi = s.groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (s.group_start[mid] <= b) lo = mid;
+    else hi = mid - 1;
   }
+  const Kv8SharedSeq g = kv8_group(a, s, lo);
+  const bool in = g.n > 0 && b >= g.row && b - g.row < g.n;
+  if (!in && !(b >= s.group_start[lo] && b < s.group_start[lo + 1])) atomicOr(a.err, kErrSeqLen);   // in no group
+  return in ? make_int4(g.pages, lo, g.row, 0) : make_int4(0, 0, 0, 0);
 }
-__device__ __forceinline__ Kv8SharedSeq kv8_tail(const Kv8Attn& a, const Kv8Share& s, int b) {
+// What the join needs of each sequence, by all threads of the prefix pass.
+__device__ __forceinline__ void kv8_share_seqs(const Kv8Attn& a, const Kv8Share& s) {
+  for (long long b = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; b < s.batch; b += static_cast<long long>(gridDim.x) * blockDim.x)
+    s.seqs[b] = kv8_share_seq(a, s, static_cast<int>(b));
+}
+// The pages of sequence b behind the first ones.
+__device__ __forceinline__ Kv8SharedSeq kv8_tail(const Kv8Attn& a, int b, int first) {
   int len = a.lens[b];
-  const int first = s.seqs[b].x;
   const long long cap = a.max_seq_len < 16LL * a.maxp ? a.max_seq_len : 16LL * a.maxp;
   if (len < 0 || len > cap || (len > 0 && len < kPage * first)) {
     atomicOr(a.err, kErrSeqLen);

@@ -189,7 +189,7 @@ __device__ __forceinline__ int block_pages(const Kv8Attn& a, const Kv8Seq& s, in
 // sequence's tail, where the rows stand, and sums instead of results.
 struct NoShare {};
 __device__ __forceinline__ Kv8Seq seq_of(const Kv8Attn& a, const NoShare&, int b) { return kv8_seq(a, b); }
-__device__ __forceinline__ Kv8SharedSeq seq_of(const Kv8Attn& a, const Kv8Share& s, int b) { return s.tail ? kv8_tail(a, s, b) : kv8_group(a, s, b); }
+__device__ __forceinline__ Kv8SharedSeq seq_of(const Kv8Attn& a, const Kv8Share& s, int b) { return s.tail ? kv8_tail(a, b, kv8_share_seq(a, s, b).x) : kv8_group(a, s, b); }
 __device__ __forceinline__ int block_pages(const Kv8Attn& a, const Kv8SharedSeq& s, int rb, int R, int& pmin, int& pmax, Kv8Range& r) {
   pmin = pmax = s.p;
   r = Kv8Range{0, s.pages0, s.pages};
@@ -241,7 +241,11 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncwarp();
   PageRing<Y::ST> pages_in;                                     // this warp's
-  pdl_wait();
+  // The tail pass needs nothing of the prefix pass, whose blocks have all waited for what came before them when it starts:
+  // it runs beside that pass' last blocks, and waits for it at its end, for the join.
+  bool after = false;
+  if constexpr (SHARED) after = share.tail != 0;
+  if (!after) pdl_wait();
   if (split) pdl_trigger();                                      // the join's launch, beside the work
   if constexpr (SHARED) {
     if (!share.tail) kv8_share_seqs(a, share);
@@ -342,6 +346,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
     }
     if (u0 >= u1) {
       if (tid == 0) records[blockIdx.x].valid = 0;
+      if (after) pdl_wait();
       return;
     }
     int lo = 0, hi = entries - 1;                                // the entry that holds u0
@@ -920,6 +925,7 @@ __global__ void __launch_bounds__(32 * kRWarps, ctas_per_sm(D, 8 * NT)) kv8_rows
   }
   if (split && tid == 0) records[blockIdx.x] = cut;
   if (pages_in.failed && lane == 0) atomicOr(a.err, kErrTimeout);
+  if (after) pdl_wait();
 }
 
 // Joins the parts of the items that cross spans: a block per CTA of the first kernel, 16 / R warps per row.

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(128) kv8_share_join_kernel(const __grid_consta
   pdl_wait();
   const int len = a.lens[b];
   const int4 seq = share.seqs[b];
-  const Kv8SharedSeq tail = kv8_tail(a, share, b);
+  const Kv8SharedSeq tail = kv8_tail(a, b, seq.x);
   const long long at = (row * PER + half) * PART;
   Parts pt{nullptr, nullptr, 0, 0}, pp = pt;
   if (len > 0 && tail.n > 0) pt = parts_of<DV>(tails, b, hq % a.G, hq / a.G, half, tails.state + at);
