@@ -289,6 +289,76 @@ tq_status tq_causal_attention(const tq_ctx* ctx, const void* q, tq_dtype dtype, 
                               const void* k_cache, const void* v_cache, int chunk_tokens, float softmax_scale,
                               float* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Read the 2-4-bit cache back: keys and values as rows, for what attends to
+ * dense tensors (tq_prompt_attention over earlier tokens and a new chunk), and
+ * for checks.  Sequence b's tokens start_pos[b] + t, t < lens[b], go to rows
+ * first_row[b] + t of k_out and v_out: device [total_rows] rows, k_stride and
+ * v_stride elements apart (0: dense) with [num_kv_heads][d] in `dtype` (bf16 or
+ * fp32) each; either may be NULL, and its cache then too.  A token's row is
+ *   Pi^T y,   y_i = n16/sqrt(d) c[code_i],
+ * and of keys with a QJL term + sqrt(pi/2)/m rho16 (S Pi)^T (+-1): the vector
+ * whose inner product with any q is the score that the decode gives q.
+ * Accuracy against that formula, relative to the root of the sum of its terms'
+ * squares: fp32 rows 2^-19; bf16 rows 2^-8 of the element, and 2^-8 of that root
+ * at most (2^-11 a factor, where fp16 tables on tcgen05 form them: d = m = 128).
+ * Rows of no sequence, and what lies between rows that are strides apart, stay
+ * as they were.  Sequences' rows must not overlap.  max_len: no lens[b] is
+ * larger.  Device status bit 1: a page id out of range (its tokens' rows stay as
+ * they were); bit 2: positions beyond the block table (cut off); bit 4: a
+ * negative start, length or first row (nothing is read), a length above max_len
+ * or rows beyond total_rows (cut off).
+ * start_pos, lens, first_row: device int32 [batch].  No workspace.  Caches and
+ * rows are 16-byte aligned, strides multiples of 16 bytes and no smaller than a
+ * row (else TQ_ERR_INVALID_ARG); num_kv_heads is at most 65,535 and num_pages *
+ * num_kv_heads below 2^31 (else TQ_ERR_UNSUPPORTED). */
+tq_status tq_dequantize(const tq_ctx* ctx, const void* k_cache, const void* v_cache, tq_dtype dtype, int batch,
+                        int num_kv_heads, const int32_t* start_pos, const int32_t* lens, int max_len,
+                        const int32_t* block_table, int max_pages_per_seq, int num_pages, void* k_out, void* v_out,
+                        const int32_t* first_row, int total_rows, long long k_stride, long long v_stride, void* stream);
+
+/* Exact causal attention over packed sequences of fresh queries, keys and
+ * values (the prompt's own step, before or beside its append to a cache).
+ * Sequence s has queries cu_q[s] .. cu_q[s + 1] - 1 of q and keys cu_k[s] ..
+ * cu_k[s + 1] - 1 of k and v (device int32 [num_seqs + 1] each); with n queries
+ * and m keys, query t stands at position p = m - n + t (a chunk behind m - n
+ * earlier keys) and sees key j <= p if window = 0, or j > p - window, or
+ * j < sinks.  A query that sees nothing (p < 0) gives zeros.
+ *   out = sum_j w_j v_j / sum_j w_j,   w_j = exp(softmax_scale <q, k_j>)
+ * q: [total_q][num_q_heads][d], k and v: [total_k][num_kv_heads][d] in `dtype`
+ * (bf16 or fp32), consecutive tokens q_stride, k_stride, v_stride elements apart
+ * (0: dense), so that slices of one fused projection can be passed; out: dense
+ * [total_q][num_q_heads][d], overlapping none of them.  d: the context's, any
+ * that a context can have; any number of query heads per KV head.  Rows of q and
+ * out behind the last sequence are neither read nor written.
+ * Keys and values that no query of their block sees may hold anything, and those
+ * that some rows see and others do not spoil only the rows that see them; a
+ * query that is not finite spoils its own row.
+ * max_q_len and max_k_len: no sequence has more.  Offsets that fall, pass
+ * total_q or total_k, or are further apart set device status bit 4; that
+ * sequence's rows stay as they were.  Results do not depend on the run, but in
+ * their last bits on the other sequences of the call (they share its split).
+ * Accuracy: scores and sums in fp32; bf16 weights are rounded to 8 bits (2^-8 of
+ * each at most) for the product with the values, fp32 ones not.  Weights may
+ * reach 2^24 before the division: values beyond 2^100 may overflow.
+ * bf16 at d = 64, 128, 256 with softmax_scale > 0 and up to 128 query heads per
+ * KV head runs on tcgen05; everything else on CUDA cores, where a prompt takes
+ * some 20 to 60 times as long (d = 128, 2,048 tokens, 32 / 8 heads: 1,076 us in
+ * fp32 against 50 in bf16).  Scores that make a tile's weights sum to more than
+ * 2^24, or the first ones of a row to less than 2^-24, take that tile twice.
+ * All pointers but cu_q and cu_k are 16-byte aligned, strides multiples of 16
+ * bytes and no smaller than a token (else TQ_ERR_INVALID_ARG); total_q *
+ * num_q_heads and total_k are at most 2^30, max_k_len 2^29 and num_kv_heads
+ * 65,535 (else TQ_ERR_UNSUPPORTED).  Workspace: tq_prompt_workspace_size, which
+ * never falls as its arguments grow; calls that may overlap on the GPU need one
+ * each. */
+tq_status tq_prompt_workspace_size(const tq_ctx* ctx, int num_seqs, int max_q_len, int num_q_heads, int num_kv_heads,
+                                   int max_k_len, size_t* bytes);
+tq_status tq_prompt_attention(const tq_ctx* ctx, const void* q, const void* k, const void* v, tq_dtype dtype, int num_seqs,
+                              const int32_t* cu_q, const int32_t* cu_k, int total_q, int total_k, int max_q_len,
+                              int max_k_len, int num_q_heads, int num_kv_heads, int window, int sinks, float softmax_scale,
+                              void* out, void* workspace, size_t workspace_bytes, long long q_stride, long long k_stride,
+                              long long v_stride, void* stream);
+
 /* Synchronise the device and report (then clear) the context's device error
  * word: TQ_OK, or TQ_ERR_DEVICE_CHECK with the bits in *flags (may be NULL):
  * 1 = page id out of range, 2 = position beyond the block table,
@@ -474,6 +544,42 @@ tq_status tq_kv8_causal_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, 
                                   int n_new, int num_q_heads, const int32_t* start_pos, const int32_t* new_lens,
                                   int max_seq_len, int window, int sinks, float softmax_scale, void* out,
                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Decode attention of sequences that share a prefix: tq_kv8_decode_attention
+ * (without a window) whose groups' common pages are read once for the group.
+ * Group g is the sequences group_start[g] .. group_start[g + 1] - 1 (device
+ * int32 [num_groups + 1], from 0 to batch, ascending), whose first
+ * prefix_lens[g] / 16 pages (device int32 [num_groups]; whole pages are shared,
+ * a remainder is not) are the same: the table row of its first sequence gives
+ * them, and the others' entries there are not looked at.  Each sequence goes on
+ * with its own pages; seq_lens[b] counts the prefix too and is 0 (an empty
+ * place: zeros) or no smaller than the shared pages.  No group has more than
+ * max_group sequences.  q, out: [batch][num_q_heads][d] in `dtype`; out may be q.
+ * Accuracy as tq_kv8_decode_attention, by the form that the group's rows
+ * (max_group times heads per KV head) take for the prefix and by that of few
+ * rows behind it; their sums are joined in fp32.
+ * Device status bit 4 also: a group_start outside 0 .. batch, falling, or more
+ * than max_group from the next (that group shares nothing), a sequence in no
+ * group (its pages are all its own), a length below the shared pages (counts as
+ * them; a negative one as 0), a prefix beyond the table or max_seq_len (cut).
+ * Limits as tq_kv8_decode_attention, also for num_groups * max_group in place of
+ * batch.  The workspace is sized by tq_kv8_shared_workspace_size, never less
+ * than for smaller sizes.  Three kernels; results do not depend on the run. */
+tq_status tq_kv8_shared_workspace_size(const tq_ctx* ctx, int batch, int num_q_heads, int num_kv_heads, int num_groups,
+                                       int max_group, int max_seq_len, size_t* bytes);
+tq_status tq_kv8_shared_decode_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, const void* q, tq_dtype dtype,
+                                         int batch, int num_q_heads, const int32_t* seq_lens, int max_seq_len,
+                                         int num_groups, const int32_t* group_start, const int32_t* prefix_lens,
+                                         int max_group, float softmax_scale, void* out, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* Read the 8-bit cache back: tq_dequantize's contract over tq_kv8_cache (only
+ * the arrays of what is read need be given).  Values are exact: code * scale in
+ * `dtype` (bf16 holds every code; scales below 2^-117 lose what bf16's smallest
+ * numbers do not hold). */
+tq_status tq_kv8_dequantize(const tq_ctx* ctx, const tq_kv8_cache* cache, tq_dtype dtype, int batch,
+                            const int32_t* start_pos, const int32_t* lens, int max_len, void* k_out, void* v_out,
+                            const int32_t* first_row, int total_rows, long long k_stride, long long v_stride, void* stream);
 
 #ifdef __cplusplus
 }
