@@ -146,7 +146,7 @@ size_t kv8_rows_workspace(int T, int G, int d);
 cudaError_t launch_kv8_rows(const Kv8Attn& a, int d, bool f32, cudaStream_t s);
 // TMA map of a cache's blocks: coordinates (channel, token, block), boxes of one block's 128-channel panel.
 bool kv8_block_map(CUtensorMap* map, const void* codes, long long blocks, int d);
-// Many query rows on the tensor cores (tq_kv8_tc.cu): whether the call takes
+// Many query rows on the tensor cores (tq_kv8_tc.cuh): whether the call takes
 // that form (it has more than kTcRows query rows per KV head, among others),
 // whether it then uses a workspace, its size and its launch.
 constexpr int kTcRows = 16;

@@ -23,7 +23,16 @@
 // rows that see it at the end.
 //
 // Warps 0-3 and 4-7: the softmax of A and B (thread = row); 8-11: the results; 12: items, the copies of queries and keys;
-// 13: MMA issue; 14: a look at the values of edge tiles; 15: the values' copies.  Every wait is bounded; a wait that gives up sets the device error word.
+// 13: MMA issue; 14: a look at the values of edge tiles; 15: the values' copies.  Every wait is bounded; a wait that gives
+// up sets the device error word.
+//
+// What bounds it: a key tile's 2 x 128 rows take 1,024 cycles of the tensor cores at d = 128 (512 at 64) and 1,024 of the
+// exponentials (32 lanes a cycle and SM), which two halves overlap as far as a half's own chain lets them: scores, softmax,
+// weights, values, one behind the other.  A prompt of 8,192 tokens, 32 / 8 heads: d = 128 330 us (1,670 TFLOP/s, tensor
+// pipe 78% of the cycles by its counter), d = 64 256 us (tensor pipe and exponentials 48% each, issue slots 48%), d = 256
+// (16 / 4 heads) 355 us.  Two dozen prompts of up to 2,500 tokens 310 to 340 us, of which the ends of 1,500 items and the join.
+// Slower were an O of its own for each half at d = 256 (every score twice: 552 us) and the softmax in two parts of 64 keys
+// (less code, d = 128: 397 us).
 
 #include "tq_prompt.h"
 #include "tq_tc.cuh"

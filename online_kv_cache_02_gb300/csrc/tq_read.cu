@@ -44,7 +44,8 @@ __device__ __forceinline__ void put(void* out, long long at, float x) {
 }
 
 // Any configuration, on CUDA cores: a block of 128 threads per (page, KV head) block of K or V; its 16 vectors stand in
-// shared memory in the rotated domain, a thread forms one output channel of all of them.
+// shared memory in the rotated domain, a thread forms one output channel of all of them.  Bound by the FMA pipe and the
+// tables' reads from L2 (d = 128, eight sequences of 16,384 tokens, 8 heads: 4,340 us, where the tensor cores take 150).
 template <bool F32>
 __global__ void __launch_bounds__(128) read_generic_kernel(const __grid_constant__ ReadArgs a, int d) {
   __shared__ __align__(16) float y[kDMax + kMaxM][kPage];
@@ -121,7 +122,9 @@ __device__ __forceinline__ float4 codes4(uint32_t w) {
 }
 
 // 8-bit cache: a warp per (page, KV head), keys and values at once (one look at the tables for both); a lane takes as many
-// codes as make 16 bytes of a row, so that stores are whole lines.
+// codes as make 16 bytes of a row, so that stores are whole lines.  Bound by the stores: eight sequences of 16,384 tokens,
+// 8 heads, d = 128, into bf16 rows 121 us (6.7 TB/s, 0.98 of a copy's; with a block per
+// page 150).
 template <int D, bool F32>
 __global__ void __launch_bounds__(256) kv8_read_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int C = F32 ? 4 : 8, STEPS = kPage * D / (32 * C);     // codes a lane at a time, and times
