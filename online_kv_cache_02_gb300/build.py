@@ -15,7 +15,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libtq.so")
 SOURCES = ["tq_api.cu", "tq_quantize.cu", "tq_quantize_tc.cu", "tq_quantize_pipe.cu", "tq_decode.cu", "tq_decode_lut.cu", "tq_noalloc.cu", "tq_search.cu", "tq_search_tc.cu", "tq_causal_tc.cu",
            "tq_generic.cu", "tq_kv8_append.cu", "tq_kv8_rows.cu", "tq_kv8_tc.cu", "tq_kv8_rows_shared.cu", "tq_kv8_tc_shared.cu",
-           "tq_kv8_shared.cu", "tq_read.cu", "tq_read_tc.cu", "tq_prompt.cu", "tq_prompt_tc.cu",
+           "tq_kv8_shared.cu", "tq_read.cu", "tq_read_tc.cu", "tq_prompt.cu", "tq_prompt_tc.cu", "tq_prompt_parts.cu",
            "tq_host.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]

@@ -1276,7 +1276,7 @@ extern "C" tq_status tq_prompt_workspace_size(const tq_ctx* ctx, int num_seqs, i
                                               size_t* bytes) {
   if (!ctx || !bytes || num_seqs < 0 || max_q_len < 0 || max_k_len < 0 || Hq < 1 || H < 1 || Hq % H) return TQ_ERR_INVALID_ARG;
   const int d = ctx->cfg.d;
-  *bytes = std::max(prompt_simt_workspace(d), d == 64 || d == 128 || d == 256 ? prompt_tc_workspace(d) : 0);
+  *bytes = std::max({prompt_simt_workspace(d), prompt_parts_workspace(d), d == 64 || d == 128 || d == 256 ? prompt_tc_workspace(d) : 0});
   return TQ_OK;
 }
 
@@ -1329,10 +1329,10 @@ extern "C" tq_status tq_prompt_attention(const tq_ctx* ctx, const void* q, const
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.part = static_cast<float*>(workspace);
   a.err = ctx->tab.err;
-  const bool f32 = dtype == TQ_F32, tc = prompt_tc_takes(a, d, f32);
-  if (workspace_bytes < (tc ? prompt_tc_workspace(d) : prompt_simt_workspace(d))) return TQ_ERR_WORKSPACE;
+  const bool f32 = dtype == TQ_F32, tc = prompt_tc_takes(a, d, f32), parts = !tc && prompt_parts_takes(a, d);
+  if (workspace_bytes < (tc ? prompt_tc_workspace(d) : parts ? prompt_parts_workspace(d) : prompt_simt_workspace(d))) return TQ_ERR_WORKSPACE;
   const tq_status st = on_device(ctx);
   if (st != TQ_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cuda_status(tc ? launch_prompt_tc(a, d, s) : launch_prompt_simt(a, d, f32, s));
+  return cuda_status(tc ? launch_prompt_tc(a, d, s) : parts ? launch_prompt_parts(a, d, f32, s) : launch_prompt_simt(a, d, f32, s));
 }

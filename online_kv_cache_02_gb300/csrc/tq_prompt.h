@@ -73,6 +73,19 @@ __device__ __forceinline__ bool prompt_sees(int p, int j, int window, int sinks)
   return j <= p && (!window || j > p - window || j < sinks);
 }
 
+// Those of the 32 keys from j0 on that the query at position p sees.
+__device__ __forceinline__ uint32_t prompt_seen32(int p, int j0, int window, int sinks) {
+  const int hi = p - j0;                               // up to hi
+  uint32_t see = hi < 0 ? 0u : hi >= 31 ? 0xFFFFFFFFu : (2u << hi) - 1u;
+  if (window) {
+    const int lo = hi - window + 1, sk = sinks - j0;   // from lo on, or below sk
+    const uint32_t win = lo <= 0 ? 0xFFFFFFFFu : lo > 31 ? 0u : 0xFFFFFFFFu << lo;
+    const uint32_t snk = sk <= 0 ? 0u : sk > 31 ? 0xFFFFFFFFu : (1u << sk) - 1u;
+    see &= win | snk;
+  }
+  return see;
+}
+
 // An item (a block and a KV head) that several CTAs share: its first part ends the span of one CTA, the join finds the
 // others by it.
 struct PSplit {
@@ -302,6 +315,10 @@ int prompt_sms();                         // of the current device
 bool prompt_tc_takes(const PromptArgs& a, int d, bool f32);
 size_t prompt_tc_workspace(int d);
 cudaError_t launch_prompt_tc(const PromptArgs& a, int d, cudaStream_t s);
+// Three bf16 parts on the tensor cores: whether the call's sizes are ones of that form.
+bool prompt_parts_takes(const PromptArgs& a, int d);
+size_t prompt_parts_workspace(int d);
+cudaError_t launch_prompt_parts(const PromptArgs& a, int d, bool f32, cudaStream_t s);
 // Joins the parts of split items (`rows` of them a slot, d + 4 floats a row: maximum, sum, two zeros, then the channels).
 cudaError_t launch_prompt_join(const PromptArgs& a, int d, bool f32, int ctas, int rows, cudaStream_t s);
 

@@ -201,18 +201,6 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
 __device__ __forceinline__ bool odd_pair(uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; }
 __device__ __forceinline__ bool odd_piece(uint4 w) { return odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w); }
 
-// Those of the 32 keys from j0 on that the query at position p sees.
-__device__ __forceinline__ uint32_t seen32(int p, int j0, int window, int sinks) {
-  const int hi = p - j0;                               // up to hi
-  uint32_t see = hi < 0 ? 0u : hi >= 31 ? 0xFFFFFFFFu : (2u << hi) - 1u;
-  if (window) {
-    const int lo = hi - window + 1, sk = sinks - j0;   // from lo on, or below sk
-    const uint32_t win = lo <= 0 ? 0xFFFFFFFFu : lo > 31 ? 0u : 0xFFFFFFFFu << lo;
-    const uint32_t snk = sk <= 0 ? 0u : sk > 31 ? 0xFFFFFFFFu : (1u << sk) - 1u;
-    see &= win | snk;
-  }
-  return see;
-}
 // One tile's weights of a thread's row with a new M, the largest score met; scores are rounded before they are compared.
 // accumulated: O holds tiles before, of which the row has seen something (had): M is then the row's reference, only raised
 // where O has another half's sums in it (shared).  Returns M and l.
@@ -221,7 +209,7 @@ __device__ __noinline__ float2 careful_tile(uint32_t ts, uint32_t to, int j0, in
                                             float m, float l, bool had, bool shared) {
   auto scores = [&](int c, float (&y)[32]) {
     tld32(ts + 32u * c, y);
-    const uint32_t see = seen32(p, j0 + 32 * c, window, sinks);
+    const uint32_t see = prompt_seen32(p, j0 + 32 * c, window, sinks);
 #pragma unroll
     for (int k = 0; k < 32; ++k) y[k] = (see >> k) & 1u ? __fmul_rn(y[k], f) : -INFINITY;
     __syncwarp();
@@ -458,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t all = 0u;
 #pragma unroll
             for (int c = 0; c < kTok; c += 32) {
-              const uint32_t see = seen32(p, j0 + c, a.window, a.sinks);
+              const uint32_t see = prompt_seen32(p, j0 + c, a.window, a.sinks);
               all |= see;
               if (__any_sync(0xffffffffu, see != 0xFFFFFFFFu)) {
 #pragma unroll
@@ -516,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool had = l > 0.0f;                         // has the row seen anything?
           if (L::WIDE)
             for (int i = 0; i < t && !had; ++i)
-              for (int c = 0; c < kTok; c += 32) had |= seen32(p, it.first_key(i) + c, a.window, a.sinks) != 0u;
+              for (int c = 0; c < kTok; c += 32) had |= prompt_seen32(p, it.first_key(i) + c, a.window, a.sinks) != 0u;
           __syncwarp();
           const float2 next = careful_tile<D>(ts, to, j0, p, a.window, a.sinks, f, L::WIDE ? t > 0 : t > first, m, l, had, L::WIDE);
           m = next.x;
