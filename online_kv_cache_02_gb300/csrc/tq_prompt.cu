@@ -1,11 +1,12 @@
-// Attention over packed prompts on CUDA cores: fp32 inputs, and head dimensions that the tensor-core form does not take.
+// Attention over packed prompts on CUDA cores: the head dimensions that neither tensor-core form takes, and fp32 calls of
+// few rows and keys.
 //
 //   s_j = scale <q, k_j>,  out = sum_j 2^(s_j log2 e - M) v_j / sum_j 2^(s_j log2 e - M),  M the running maximum,
 // over the keys j that the query's position sees.  A CTA takes 64 query rows of a KV head, or 16 where no sequence has more
 // (row r = t G + g, so that a key that is read serves every query head of its group) and 64 keys at a time; keys and queries stand transposed in
 // shared memory, so that a thread's 4 x 4 scores take two 16-byte loads per channel; sums are fp32 throughout.
-// Bound by the FMA pipes and the shared-memory loads that feed them (32 TFLOP/s; 2,048 tokens, 32 / 8 heads, d = 128, fp32:
-// 1,076 us).  Two blocks an SM, the weights where the keys were: three prompts of up to 1,111 tokens 293 us, with one block 380.
+// Bound by the FMA pipes and the shared-memory loads that feed them (27 to 32 TFLOP/s; 2,048 tokens, 16 / 4 heads, d = 256,
+// fp32: 1,253 us).  Two blocks an SM up to d = 128, the weights where the keys were: by a quarter faster than one.
 
 #include "tq_kv8.h"
 #include "tq_prompt.h"

@@ -1,5 +1,6 @@
 // Attention over packed prompts (tq_prompt_attention): arguments, the sequences' blocks of query rows and the tiles of
-// keys that they see, shared by the CUDA-core form (tq_prompt.cu) and the tensor-core form (tq_prompt_tc.cu).
+// keys that they see, shared by the tensor-core forms (tq_prompt_tc.cu for bf16, tq_prompt_parts.cu to fp32's accuracy) and
+// the CUDA-core form (tq_prompt.cu).
 #ifndef TQ_PROMPT_H_
 #define TQ_PROMPT_H_
 

@@ -14,6 +14,11 @@
 // Warps 0-3: softmax (thread = row); 4-7: O and results; 8-11: keys, from memory to parts in shared memory; 12-15: values;
 // both: queries; 16: MMA issue, a tile's scores ahead of the values before.  Every warp walks the list of items by itself.
 // Every wait is bounded; a wait that gives up sets the device error word.
+//
+// Bound by shared memory (480 KB a tile, of which the scores' products read the queries 48 times: 2.1 us at 128 B a cycle;
+// the MMAs by themselves 1.7) and by the chain from rows in memory to parts, scores, weights and products: 3.9 us a tile.
+// Two thousand tokens, 32 / 8 heads, d = 128, fp32: 257 us (134 TFLOP/s; CUDA cores 1,076), three prompts of up to 1,111 tokens
+// 90 (293).  Slower were 16 warps for keys and values (274) and both at once by eight (356), fewer pieces in flight (279).
 
 #include "tq_kv8.h"
 #include "tq_prompt.h"
@@ -483,8 +488,10 @@ cudaError_t launch_t(const PromptArgs& args, cudaStream_t s) {
 
 }  // namespace
 
+// All sizes but a tile of keys for a few rows, which is latency alone (4 tokens, 4 heads per KV head: 14 us, CUDA cores 11);
+// from there on this form is ahead (5 tokens 14 us against 17; eight single tokens behind 4,000 keys 130 against 230, fp32).
 bool prompt_parts_takes(const PromptArgs& a, int d) {
-  return (d == 64 || d == 128) && static_cast<long long>(a.max_q) * a.G > 16;
+  return (d == 64 || d == 128) && (a.max_k > kTok || static_cast<long long>(a.max_q) * a.G > 16);
 }
 size_t prompt_parts_workspace(int d) {
   return static_cast<size_t>(prompt_sms()) * (sizeof(PSplit) + 2 * sizeof(float) * kRows * (d + 4));
