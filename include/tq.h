@@ -339,14 +339,15 @@ tq_status tq_dequantize(const tq_ctx* ctx, const void* k_cache, const void* v_ca
  * their last bits on the other sequences of the call (they share its split).
  * Accuracy: scores and sums in fp32; bf16 weights are rounded to 8 bits (2^-8 of
  * each at most) for the product with the values, fp32 ones not; fp32 products
- * to 2^-23 of each.  bf16 weights may reach 2^24 before the division: values
- * beyond 2^100 may overflow.
+ * to 2^-23 of each.  The division is the last step: values beyond 2^99 may
+ * overflow in the sums.
  * bf16 at d = 64, 128, 256 with softmax_scale > 0 and up to 128 query heads per
  * KV head runs on tcgen05, and so does the rest at d = 64 and 128, fp32 as three
  * bf16 parts (d = 128, 2,048 tokens, 32 / 8 heads: bf16 50 us, fp32 257); other
  * head dimensions, and fp32 or such scales at d = 256, run on CUDA cores (d =
- * 256, 16 / 4 heads: 1,253 us).  In bf16, scores that make a tile's weights sum to more than
- * 2^24, or the first ones of a row to less than 2^-24, take that tile twice.
+ * 256, 16 / 4 heads: 1,253 us).  In bf16, scores that make a tile's weights sum
+ * to more than 2^24, or the first ones of a row to less than 2^-24, take that
+ * tile twice.
  * All pointers but cu_q and cu_k are 16-byte aligned, strides multiples of 16
  * bytes and no smaller than a token (else TQ_ERR_INVALID_ARG); total_q *
  * num_q_heads and total_k are at most 2^30, max_k_len 2^29 and num_kv_heads

@@ -63,8 +63,9 @@ def reference(q, k, v, window, sinks, scale, weight_step):
             size = w @ vs.abs()
         else:                               # a value that some rows see and others do not
             sr = seen[any_seen]
-            o = torch.stack([(torch.where(sr[i][:, None], vs, 0.0) * w[i][:, None]).sum(0) for i in range(len(w))])
-            size = o.abs()
+            each = [torch.where(sr[i][:, None], vs, 0.0) * w[i][:, None] for i in range(len(w))]
+            o = torch.stack([x.sum(0) for x in each])
+            size = torch.stack([x.abs().sum(0) for x in each])              # A, not the sum's size: its terms cancel
         rough = 8 * math.sqrt(d) * 2.0 ** -24 * (torch.sqrt((q[:, a] ** 2) @ (ks ** 2).T) + s.abs()) * abs(scale)
         rough = rough + 2.0 ** -22 * (s * scale).abs()
         e = torch.where(seen, rough, 0.0).amax(1)[any_seen][:, None]
@@ -338,6 +339,46 @@ def test_more_sequences_than_the_list(d):
     lens = rng.integers(0, 6, 2200).tolist()
     lens[700], lens[1500] = 300, 129
     attend("bf16", d, 2, 1, lens, [n + (i % 4) for i, n in enumerate(lens)], window=100, sinks=2)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp32_of_many_sequences(d):
+    """More than the list holds, prompts of one tile and of several in turn."""
+    rng = np.random.default_rng(6)
+    new = rng.integers(0, 5, 2200).tolist()
+    new[300], new[900] = 150, 64
+    attend("f32", d, 2, 1, new, [n + (i % 70) for i, n in enumerate(new)])
+    new = rng.choice([1, 2, 30, 64, 65, 129], 150).tolist()
+    attend("f32", d, 4, 2, new, [n + int(k) for n, k in zip(new, rng.choice([0, 63, 64, 200, 900], 150))], window=130, sinks=2)
+
+
+@pytest.mark.parametrize("dtype,d,scale", [("f32", 128, None), ("f32", 64, 0.01), ("bf16", 128, -0.01)])
+def test_sums_of_one_sign(dtype, d, scale):
+    """Long sums of values, and scores, that do not cancel."""
+    def change(q, k, v):
+        v.abs_().add_(1.0)
+        q.abs_()
+        k.abs_().mul_(0.25)
+    attend(dtype, d, 4, 2, [70, 3], [6000, 2500], scale=scale, change=change)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -60, 2.0 ** 60, 2.0 ** 99])
+def test_fp32_sizes(size):
+    """Values of any size, queries and keys whose sizes cancel in the scores."""
+    def change(q, k, v):
+        q.mul_(size)
+        k.div_(size)
+        v.mul_(size)
+    attend("f32", 128, 4, 2, [130, 17], [300, 900], change=change)
+
+
+@pytest.mark.parametrize("dtype,d,scale", [("f32", 64, None), ("bf16", 64, -0.05), ("bf16", 128, -0.05)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_values_that_are_not_finite_spoil_only_who_sees_them(dtype, d, scale, bad):
+    def change(q, k, v):
+        v[5, 0, 3] = v[120, 1, 7] = v[199, 0, 0] = bad
+    attend(dtype, d, 4, 2, [200], [200], scale=scale, change=change)
+    attend(dtype, d, 4, 2, [200], [200], scale=scale, change=change, window=40)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
