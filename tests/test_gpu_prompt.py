@@ -419,20 +419,23 @@ def test_results_repeat_bit_for_bit(dtype, d):
     assert all(torch.equal(o, outs[0]) for o in outs)
 
 
-def test_captured_and_replayed_with_new_inputs():
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_captured_and_replayed_with_new_inputs(dtype):
     """Two graphs that share a workspace, replayed with other inputs, offsets among them."""
+    dt, code = DT[dtype]
+    step = 2.0 ** -8 if dtype == "bf16" else 0.0
     d, hq, h, n = 128, 8, 2, 400
     ctx = ctx_for(d)
-    bufs = [torch.zeros(n, x, d, dtype=torch.bfloat16, device=DEV) for x in (hq, h, h)]
+    bufs = [torch.zeros(n, x, d, dtype=dt, device=DEV) for x in (hq, h, h)]
     cu = ints([0, 0, 0])
     ws_n = tq.tq_prompt_workspace_size(ctx, 2, n, hq, h, n)
     ws = torch.zeros(ws_n, dtype=torch.uint8, device=DEV)
-    outs = [torch.zeros(n, hq, d, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    outs = [torch.zeros(n, hq, d, dtype=dt, device=DEV) for _ in range(2)]
     graphs = []
     for window, out in zip((0, 50), outs):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            tq.tq_prompt_attention(ctx, *bufs, tq.TQ_BF16, 2, cu, cu, n, n, n, n, hq, h, window, 0, 0.1, out, ws, ws_n,
+            tq.tq_prompt_attention(ctx, *bufs, code, 2, cu, cu, n, n, n, n, hq, h, window, 0, 0.1, out, ws, ws_n,
                                    stream=torch.cuda.current_stream())
         graphs.append(g)
     for seed, offsets in ((1, [0, 100, 400]), (2, [0, 399, 400]), (3, [0, 0, 350])):
@@ -445,35 +448,38 @@ def test_captured_and_replayed_with_new_inputs():
         torch.cuda.synchronize()
         for window, out in zip((0, 50), outs):
             for a, b in zip(offsets[:-1], offsets[1:]):
-                want, bound = reference(*(x[a:b].double() for x in bufs), window, 0, 0.1, 2.0 ** -8)
-                assert bool(((out[a:b].double() - want).abs() <= bound + 2.0 ** -8 * (want.abs() + bound)).all())
+                want, bound = reference(*(x[a:b].double() for x in bufs), window, 0, 0.1, step)
+                assert bool(((out[a:b].double() - want).abs() <= bound + torch.finfo(dt).eps / 2 * (want.abs() + bound)).all())
     assert tq.tq_check_device_status(ctx) == 0
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_two_streams_at_once(dtype):
+    dt, code = DT[dtype]
+    step = 2.0 ** -8 if dtype == "bf16" else 0.0
     d, hq, h, n = 128, 8, 2, 500
     ctx = ctx_for(d)
     ws_n = tq.tq_prompt_workspace_size(ctx, 1, n, hq, h, n)
     sets = []
     for seed in (1, 2):
         gen = torch.Generator(device=DEV).manual_seed(seed)
-        sets.append([torch.randn(n, x, d, generator=gen, device=DEV).bfloat16() for x in (hq, h, h)] +
-                    [torch.zeros(n, hq, d, dtype=torch.bfloat16, device=DEV), torch.zeros(ws_n, dtype=torch.uint8, device=DEV), torch.cuda.Stream()])
+        sets.append([torch.randn(n, x, d, generator=gen, device=DEV).to(dt) for x in (hq, h, h)] +
+                    [torch.zeros(n, hq, d, dtype=dt, device=DEV), torch.zeros(ws_n, dtype=torch.uint8, device=DEV), torch.cuda.Stream()])
     cu = ints([0, n])
     want = []
     for rounds in (1, 8):
         torch.cuda.synchronize()
         for _ in range(rounds):
             for q, k, v, out, ws, s in sets:
-                tq.tq_prompt_attention(ctx, q, k, v, tq.TQ_BF16, 1, cu, cu, n, n, n, n, hq, h, 0, 0, 0.1, out, ws, ws_n, stream=s)
+                tq.tq_prompt_attention(ctx, q, k, v, code, 1, cu, cu, n, n, n, n, hq, h, 0, 0, 0.1, out, ws, ws_n, stream=s)
             if rounds == 1:
                 torch.cuda.synchronize()
         torch.cuda.synchronize()
         want.append([x[3].clone() for x in sets])
     assert all(torch.equal(a, b) for a, b in zip(*want))
     for q, k, v, out, ws, s in sets:
-        r, bound = reference(q.double(), k.double(), v.double(), 0, 0, 0.1, 2.0 ** -8)
-        assert bool(((out.double() - r).abs() <= bound + 2.0 ** -8 * (r.abs() + bound)).all())
+        r, bound = reference(q.double(), k.double(), v.double(), 0, 0, 0.1, step)
+        assert bool(((out.double() - r).abs() <= bound + torch.finfo(dt).eps / 2 * (r.abs() + bound)).all())
 
 
 def test_rows_beyond_32_bit_offsets():
