@@ -290,9 +290,14 @@ cudaError_t launch_t(const PromptArgs& a, bool f32, cudaStream_t s) {
 template <int D>
 cudaError_t launch_d(const PromptArgs& args, bool f32, cudaStream_t s) {
   PromptArgs a = args;
-  const bool few = static_cast<long long>(a.max_q) * a.G <= 16;
-  a.rows = few ? 16 : 64;
-  return few ? launch_t<D, 1>(a, f32, s) : launch_t<D, 4>(a, f32, s);
+  a.rows = 16;
+  if constexpr (D != 64 && D != 128) {                 // (there only a few rows come here)
+    if (static_cast<long long>(a.max_q) * a.G > 16) {
+      a.rows = 64;
+      return launch_t<D, 4>(a, f32, s);
+    }
+  }
+  return launch_t<D, 1>(a, f32, s);
 }
 }  // namespace
 
