@@ -272,8 +272,11 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
 int simt_ctas(int d) { return prompt_sms() * (d > 128 ? 1 : 2); }
 
 template <int D, int RM>
-cudaError_t launch_t(const PromptArgs& a, bool f32, cudaStream_t s) {
+cudaError_t launch_t(const PromptArgs& args, bool f32, cudaStream_t s) {
   using L = SG<D, RM>;
+  PromptArgs a = args;
+  a.rows = L::ROWS;
+  a.most = prompt_list_room(a);
   static std::atomic<unsigned long long> done16{0}, done32{0};
   cudaError_t e = f32 ? smem_attr_once(prompt_simt_kernel<D, true, RM>, L::BYTES, done32)
                       : smem_attr_once(prompt_simt_kernel<D, false, RM>, L::BYTES, done16);
@@ -288,14 +291,9 @@ cudaError_t launch_t(const PromptArgs& a, bool f32, cudaStream_t s) {
   return launch_prompt_join(a, D, f32, ctas, L::ROWS, s);
 }
 template <int D>
-cudaError_t launch_d(const PromptArgs& args, bool f32, cudaStream_t s) {
-  PromptArgs a = args;
-  a.rows = 16;
+cudaError_t launch_d(const PromptArgs& a, bool f32, cudaStream_t s) {
   if constexpr (D != 64 && D != 128) {                 // (there only a few rows come here)
-    if (static_cast<long long>(a.max_q) * a.G > 16) {
-      a.rows = 64;
-      return launch_t<D, 4>(a, f32, s);
-    }
+    if (static_cast<long long>(a.max_q) * a.G > 16) return launch_t<D, 4>(a, f32, s);
   }
   return launch_t<D, 1>(a, f32, s);
 }
@@ -303,10 +301,6 @@ cudaError_t launch_d(const PromptArgs& args, bool f32, cudaStream_t s) {
 
 int prompt_sms() { return kv8_sm_count(); }
 
-long long prompt_most_blocks(const PromptArgs& a) {
-  const long long each = (static_cast<long long>(a.max_q) * a.G + a.rows - 1) / a.rows;
-  return std::min(a.S * each, a.S + static_cast<long long>(a.total_q) * a.G / a.rows);
-}
 bool prompt_splits(const PromptArgs& a, int tok, int cost) {
   const long long blocks = prompt_most_blocks(a);
   return a.S <= kPromptList && blocks <= kPromptList && blocks * (a.max_k / tok + 2 + a.sinks / tok + cost) <= 0x7FFFFFFFLL;

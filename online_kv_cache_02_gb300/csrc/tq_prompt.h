@@ -5,6 +5,7 @@
 #define TQ_PROMPT_H_
 
 #include "tq_internal.h"
+#include "tq_prompt_list.h"
 
 namespace tq {
 
@@ -16,6 +17,7 @@ struct PromptArgs {
   const int32_t *cu_q, *cu_k;             // [S + 1]
   int max_q, max_k;
   int rows;                               // query rows of a block
+  int most;                               // blocks that the list takes
   int window, sinks;
   float scale_log2;
   float* part;                            // split items: PSplit per CTA, then [slot][rows][d + 4]
@@ -28,7 +30,7 @@ struct PromptSeq {
 };
 __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs& a, int s) {
   const int q0 = a.cu_q[s], q1 = a.cu_q[s + 1], k0 = a.cu_k[s], k1 = a.cu_k[s + 1];
-  if (q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k || q1 - q0 > a.max_q || k1 - k0 > a.max_k) {
+  if (!prompt_pair(q0, q1, a.total_q, a.max_q) || !prompt_pair(k0, k1, a.total_k, a.max_k)) {
     atomicOr(a.err, kErrSeqLen);
     return PromptSeq{0, 0, 0, 0};
   }
@@ -46,9 +48,7 @@ struct PromptBlock {
   template <int TOK>
   __device__ __forceinline__ int first_key(int tile) const { return tile < ns ? TOK * tile : w0 + TOK * (tile - ns); }
 };
-__device__ __forceinline__ int prompt_blocks(const PromptArgs& a, const PromptSeq& s) {
-  return static_cast<int>((static_cast<long long>(s.n) * a.G + a.rows - 1) / a.rows);
-}
+__device__ __forceinline__ int prompt_blocks(const PromptArgs& a, const PromptSeq& s) { return prompt_blocks(s.n, a.G, a.rows); }
 template <int TOK>
 __device__ __forceinline__ PromptBlock prompt_block(const PromptArgs& a, const PromptSeq& s, int qb) {
   PromptBlock b;
@@ -97,8 +97,6 @@ __device__ __forceinline__ float prompt_inverse(float l, int p) {
   return l > 0.0f ? 1.0f / l : l == 0.0f && p < 0 ? 0.0f : __int_as_float(0x7FC00000);
 }
 
-constexpr int kPromptList = 2048;         // blocks and sequences that the split form lists
-
 // The CTA's place in the list of all items' tiles, cut into spans of equal cost: an item takes COST units, then one per
 // tile; the blocks stand sequence by sequence, each for all its `heads`.
 struct PromptSpan {
@@ -135,13 +133,18 @@ __device__ PromptSpan prompt_span(const PromptArgs& a, int heads, int min_span, 
   int sum = 0, blocks = 0;
   for (int i = 0; i < per && tid * per + i < a.S; ++i) {
     firsts[tid * per + i] = sum;
-    sum += prompt_blocks(a, prompt_seq(a, tid * per + i));
+    sum += prompt_counted(prompt_blocks(a, prompt_seq(a, tid * per + i)), a.most);
   }
   int before = scan(sum, blocks);
   for (int i = 0; i < per && tid * per + i < a.S; ++i) firsts[tid * per + i] += before;
   __syncthreads();
+  const int seqs = prompt_taken(firsts, a.S, blocks, a.most);
+  if (seqs < a.S) {                       // more blocks than the rows of the call have: the same rows again
+    blocks = firsts[seqs];
+    if (tid == 0) atomicOr(a.err, kErrSeqLen);
+  }
   auto seq_of = [&](int e) {              // the last sequence whose first block is at or before e
-    int lo = 0, hi = a.S - 1;
+    int lo = 0, hi = seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
       if (firsts[mid] <= e) lo = mid;
@@ -284,7 +287,7 @@ struct PromptWalk {
     if (x.u0 >= x.u1) return;
     if (++h < heads) return;
     h = 0;
-    do {                                  // (there is one more: units are left)
+    do {                                  // (there is one more: units are left, and only listed blocks have units)
       if (++qb >= nblk) {
         qb = 0;
         do nblk = prompt_blocks(a, prompt_seq(a, ++s));
@@ -306,9 +309,13 @@ __device__ __forceinline__ void prompt_zero_rows(const PromptArgs& a, int d) {
   }
 }
 
-// Blocks that a call can have at most, and whether they can be listed.
-long long prompt_most_blocks(const PromptArgs& a);
+// Blocks that a call can have at most (by its sizes alone), and whether they can be listed.
+inline long long prompt_most_blocks(const PromptArgs& a) { return prompt_most_blocks(a.S, a.max_q, a.total_q, a.G, a.rows); }
 bool prompt_splits(const PromptArgs& a, int tok, int cost);
+inline int prompt_list_room(const PromptArgs& a) {
+  const long long most = prompt_most_blocks(a);
+  return most < kPromptList ? static_cast<int>(most) : kPromptList;
+}
 // Workspace of either form (whatever the dtype and scale), its CTAs and its launch.
 size_t prompt_simt_workspace(int d);
 cudaError_t launch_prompt_simt(const PromptArgs& a, int d, bool f32, cudaStream_t s);

@@ -472,6 +472,7 @@ template <int D, bool F32>
 cudaError_t launch_t(const PromptArgs& args, cudaStream_t s) {
   PromptArgs a = args;
   a.rows = kRows;
+  a.most = prompt_list_room(a);
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = smem_attr_once(prompt_parts_kernel<D, F32>, PB<D, F32>::BYTES, configured);
   if (e != cudaSuccess) return e;

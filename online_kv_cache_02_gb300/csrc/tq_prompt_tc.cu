@@ -947,6 +947,7 @@ cudaError_t launch_t(const PromptArgs& args, cudaStream_t s) {
   PromptArgs a = args;
   const int tokens = 128 / a.G;                        // of a half
   a.rows = L::HALVES * tokens * a.G;
+  a.most = prompt_list_room(a);
   CUtensorMap mq, mk, mv;
   if (!rows_map(&mq, a.q, D, a.Hq, a.total_q, a.qs, a.G, tokens) || !rows_map(&mk, a.k, D, a.H, a.total_k, a.ks, 1, kTok) ||
       !rows_map(&mv, a.v, D, a.H, a.total_k, a.vs, 1, L::VTOK))

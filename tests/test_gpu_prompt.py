@@ -413,6 +413,49 @@ def test_offsets_that_are_none_are_skipped_and_flagged():
     assert flags == 4 and torch.equal(out[:60], good[:60]) and bool((out[60:] == -7).all())
 
 
+# a form each: tcgen05, three parts on tcgen05 (fp32, and bf16 at a scale below 0), CUDA cores; with the query rows of a block
+FORMS = [("bf16", 64, None, 256), ("bf16", 128, None, 256), ("bf16", 256, None, 128), ("f32", 64, None, 128), ("f32", 128, None, 128),
+         ("bf16", 128, -0.05, 128), ("f32", 96, None, 64), ("bf16", 96, None, 64), ("f32", 256, None, 64)]
+
+
+def by_offsets(dtype, d, scale, cu_q, cu_k, total, hq=4, h=1, max_q=None, max_k=None, seed=0, flags=4):
+    """A call with any offsets: its inputs and what it leaves of an output of -7."""
+    dt, code = DT[dtype]
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    q, k, v = (torch.randn(total, x, d, generator=gen, device=DEV).to(dt) for x in (hq, h, h))
+    ctx, max_q, max_k = ctx_for(d), total if max_q is None else max_q, total if max_k is None else max_k
+    size = tq.tq_prompt_workspace_size(ctx, len(cu_q) - 1, max_q, hq, h, max_k)
+    ws, out = torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV), torch.full_like(q, -7.0)
+    tq.tq_prompt_attention(ctx, q, k, v, code, len(cu_q) - 1, ints(cu_q), ints(cu_k), total, total, max_q, max_k, hq, h, 0, 0,
+                           1 / math.sqrt(d) if scale is None else scale, out, ws, size)
+    torch.cuda.synchronize()
+    assert tq.tq_check_device_status(ctx) == flags
+    return q, k, v, out
+
+
+def near(dtype, d, scale, q, k, v, got):
+    want, bound = reference(q.double(), k.double(), v.double(), 0, 0, 1 / math.sqrt(d) if scale is None else scale, 2.0 ** -8 if dtype == "bf16" else 0.0)
+    return bool(((got.double() - want).abs() <= bound + torch.finfo(got.dtype).eps / 2 * (want.abs() + bound)).all())
+
+
+@pytest.mark.parametrize("dtype,d,scale,rows", FORMS)
+def test_offsets_that_fall_again_and_again(dtype, d, scale, rows):
+    """The same rows in every second pair of offsets: more blocks than rows of that number make."""
+    n = 700
+    q, k, v, out = by_offsets(dtype, d, scale, [0, n] * 40, [0, n] * 40, n + 9)
+    assert near(dtype, d, scale, q[:n], k[:n], v[:n], out[:n]) and bool((out[n:] == -7).all())
+
+
+@pytest.mark.parametrize("dtype,d,scale,rows", FORMS[:-1])
+def test_offsets_that_fall_behind_many_blocks(dtype, d, scale, rows):
+    """Twice the rows that the list of 2,048 blocks takes once: the second time they are left out."""
+    n = 1560 * rows // 4
+    q, k, v, out = by_offsets(dtype, d, scale, [0, n, 0, n], [0, n, 0, n], n + 9)
+    for at in (0, n // 2, n - 40):
+        assert near(dtype, d, scale, q[at:at + 40], k[:at + 40], v[:at + 40], out[at:at + 40])
+    assert not bool((out[:n] == -7).all(-1).any()) and bool((out[n:] == -7).all())
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 128)])
 def test_results_repeat_bit_for_bit(dtype, d):
     outs = [attend(dtype, d, 8, 2, [300, 1, 45], [1300, 2000, 45], repeat=3) for _ in range(4)]
