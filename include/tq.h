@@ -565,7 +565,8 @@ tq_status tq_kv8_causal_attention(const tq_ctx* ctx, const tq_kv8_cache* cache, 
  * (max_group times heads per KV head) take for the prefix and by that of few
  * rows behind it; their sums are joined in fp32.
  * Device status bit 4 also: a group_start outside 0 .. batch, falling, or more
- * than max_group from the next (that group shares nothing), a sequence in no
+ * than max_group from the next (that group shares nothing, nor do groups around
+ * a fall that have a sequence in common, but for one), a sequence in no
  * group (its pages are all its own), a length below the shared pages (counts as
  * them; a negative one as 0), a prefix beyond the table or max_seq_len (cut).
  * Limits as tq_kv8_decode_attention, also for num_groups * max_group in place of

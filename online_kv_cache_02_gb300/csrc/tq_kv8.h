@@ -63,25 +63,44 @@ struct Kv8Share {
   int2* items;                    // the pass' items, by block of rows and KV head: the CTAs that hold it (-1: whole, in `state`)
   float* state;                   // per query row: [items per head][maximum, sum, its exponent, 0, channels]
 };
-__device__ __forceinline__ Kv8SharedSeq kv8_group(const Kv8Attn& a, const Kv8Share& s, int g) {
-  const int r0 = s.group_start[g], r1 = s.group_start[g + 1], len = s.prefix_lens[g];
-  int pages = len < 0 ? 0 : len / kPage;
-  const int cap = min(a.maxp, a.max_seq_len / kPage);
-  if (r0 < 0 || r1 < r0 || r1 > s.batch || r1 - r0 > s.max_group || len < 0 || pages > cap) {
-    atomicOr(a.err, kErrSeqLen);
-    if (!(r0 >= 0 && r1 >= r0 && r1 <= s.batch && r1 - r0 <= s.max_group)) return Kv8SharedSeq{0, 0, 0, 0, -1};
-    pages = min(pages, cap);
-  }
-  return Kv8SharedSeq{r0, pages ? r1 - r0 : 0, 0, pages, kPage * pages - 1};
-}
-// Sequence b as in Kv8Share::seqs: the group that holds it by a search in the ascending starts.
-__device__ __forceinline__ int4 kv8_share_seq(const Kv8Attn& a, const Kv8Share& s, int b) {
+// The group of sequence b by bisection of the starts.
+__device__ __forceinline__ int kv8_group_of(const Kv8Share& s, int b) {
   int lo = 0, hi = s.groups - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
     if (s.group_start[mid] <= b) lo = mid;
     else hi = mid - 1;
   }
+  return lo;
+}
+// Where starts fall, a sequence can be in two groups.  Bisection leads each sequence to one of them, and never a later sequence
+// to an earlier group, whatever the starts are: a group that it finds from its first and from its last sequence it finds from
+// all of them, and such groups have no sequence in common.  The others share nothing.  Whether it finds group g from all of
+// r0 .. r1 - 1: the places that it looks at follow from g.
+__device__ __forceinline__ bool kv8_group_found(const Kv8Share& s, int g, int r0, int r1) {
+  bool found = true;
+  int lo = 0, hi = s.groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2, start = s.group_start[mid];
+    found &= mid <= g ? start <= r0 : start >= r1;
+    if (mid <= g) lo = mid;
+    else hi = mid - 1;
+  }
+  return found;
+}
+__device__ __forceinline__ Kv8SharedSeq kv8_group(const Kv8Attn& a, const Kv8Share& s, int g) {
+  const int r0 = s.group_start[g], r1 = s.group_start[g + 1], len = s.prefix_lens[g];
+  const bool list = r0 >= 0 && r1 >= r0 && r1 <= s.batch && r1 - r0 <= s.max_group &&
+                    (r1 == r0 || kv8_group_found(s, g, r0, r1));
+  const int cap = min(a.maxp, a.max_seq_len / kPage), pages = len < 0 ? 0 : len / kPage;
+  if (!list || len < 0 || pages > cap) atomicOr(a.err, kErrSeqLen);
+  if (!list) return Kv8SharedSeq{0, 0, 0, 0, -1};
+  const int taken = min(pages, cap);
+  return Kv8SharedSeq{r0, taken ? r1 - r0 : 0, 0, taken, kPage * taken - 1};
+}
+// Sequence b as in Kv8Share::seqs.
+__device__ __forceinline__ int4 kv8_share_seq(const Kv8Attn& a, const Kv8Share& s, int b) {
+  const int lo = kv8_group_of(s, b);
   const Kv8SharedSeq g = kv8_group(a, s, lo);
   const bool in = g.n > 0 && b >= g.row && b - g.row < g.n;
   if (!in && !(b >= s.group_start[lo] && b < s.group_start[lo + 1])) atomicOr(a.err, kErrSeqLen);   // in no group

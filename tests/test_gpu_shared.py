@@ -237,6 +237,18 @@ def test_what_is_out_of_range_is_flagged():
         b.check(got)
 
 
+@pytest.mark.parametrize("dtype,d,hq", [("bf16", 128, 8), ("f32", 64, 8), ("bf16", 256, 4)])
+def test_groups_that_overlap_share_nothing_twice(dtype, d, hq):
+    """Starts that fall put sequences into two groups: one of them at most shares its pages, and every result is right."""
+    b = Batch(15, d, hq, 2, [6, 0, 6], [320, 0, 160], [20 + i for i in range(12)], dtype)
+    for starts, prefixes in (([0, 6, 0, 6], [320, 0, 160]), ([0, 6, 0, 6], [160, 0, 320]), ([0, 6, 2, 12], [320, 0, 0])):
+        for _ in range(5):
+            b.check(b.run(starts=starts, prefix_lens=prefixes, flags=4))
+    b = Batch(16, d, hq, 2, [8, 0, 8], [320, 0, 160], [20 + i for i in range(16)], dtype)
+    for _ in range(5):
+        b.check(b.run(starts=[0, 8, 4, 8], prefix_lens=[320, 0, 160], flags=4))
+
+
 def test_prefix_beyond_the_table_is_cut():
     b = Batch(9, 128, 8, 2, [6], [320], [20 + i for i in range(6)], "bf16")
     got = b.run(prefix_lens=[1 << 30], flags=4)          # to the 21 whole pages of the longest sequence, all of the first's
