@@ -13,6 +13,7 @@
 // 1,000 to 6,000 tokens 37 us, most of it three kernels' starts and the chains of their first loads.
 
 #include "tq_kv8.h"
+#include "tq_kv8_parts.h"
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -28,6 +29,7 @@ struct Pass {
   const float* parts;                     // of the cut ones
   const int2* items;
   int rows, nqb, heads, per, part;        // rows a block, blocks, items and items per head; floats of a part's row
+  int ctas;                               // that can hold parts
   float lift;
 };
 
@@ -44,14 +46,15 @@ struct Parts {
   int n;
   __device__ __forceinline__ const float* at(int i) const { return i ? rest + i * step : first; }
 };
-// Row `r` of group (or sequence) b in the pass; `whole`: where its sums stand if its item is whole.
+// Row `r` of group (or sequence) b in the pass; `whole`: where its sums stand if its item is whole.  An item that the pass did
+// not come to has no parts.
 template <int DV>
 __device__ __forceinline__ Parts parts_of(const Pass& p, int b, int r, int kv_head, int half, const float* whole) {
   const int2 who = p.items[(static_cast<long long>(b) * p.nqb + r / p.rows) * p.heads + kv_head * p.per + (p.per > 1 ? half : 0)];
   if (who.x < 0) return Parts{whole, whole, 0, 1};
   const long long slot = static_cast<long long>(p.rows) * p.part, row = static_cast<long long>(r % p.rows) * p.part;
   // the first part is in its CTA's second slot, the others in their CTAs' first
-  return Parts{p.parts + (2LL * who.x + 1) * slot + row, p.parts + 2LL * who.x * slot + row, 2 * slot, who.y - who.x + 1};
+  return Parts{p.parts + (2LL * who.x + 1) * slot + row, p.parts + 2LL * who.x * slot + row, 2 * slot, kv8_item_parts(who.x, who.y, p.ctas)};
 }
 
 // The sums of one query row: their maximum M (a score, and an exponent beside it), l and O = sum of weights
@@ -202,7 +205,7 @@ cudaError_t launch_kv8_shared(Kv8Attn a, Kv8Share share, int d, bool f32, float 
   cudaError_t e = tc ? launch_kv8_tc_shared(p, share, d, s) : launch_kv8_rows_shared(p, share, d, f32, s);
   if (e != cudaSuccess) return e;
   const auto pass = [&](const Kv8TcShape& x, const Kv8Share& sh, const float* work) {
-    return Pass{sh.state, work + x.records / sizeof(float), sh.items, x.rows, x.nqb, a.H * x.per, x.per, x.dv + 4, x.lift};
+    return Pass{sh.state, work + x.records / sizeof(float), sh.items, x.rows, x.nqb, a.H * x.per, x.per, x.dv + 4, x.ctas, x.lift};
   };
   const Pass prefix = pass(tc ? kv8_tc_shape(p.B, p.T, a.G, a.H, a.max_seq_len, d) : kv8_rows_shape(p.T, a.G, d), share, p.part);
   // the tails

@@ -369,6 +369,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       atomicOr(a.err, kErrLayout);
       if (split) splits[blockIdx.x].valid = 0;
     }
+    if constexpr (SHARED) kv8_share_seqs(a, share);    // (the join looks at them)
     return;
   }
 

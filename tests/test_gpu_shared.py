@@ -249,6 +249,18 @@ def test_groups_that_overlap_share_nothing_twice(dtype, d, hq):
         b.check(b.run(starts=[0, 8, 4, 8], prefix_lens=[320, 0, 160], flags=4))
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64), ("bf16", 256)])
+def test_a_workspace_may_hold_anything(dtype, d):
+    """Also what looks like the records of other items."""
+    b = Batch(17, d, 8, 2, [9, 1, 20], [3000, 0, 500], [1 + 40 * i for i in range(30)], dtype)
+    want = b.run()
+    b.check(want)
+    for fill in (0, 1, 0x7F, None):
+        size = 1 << 26
+        ws = torch.randint(0, 256, (size,), dtype=torch.uint8, device=DEV) if fill is None else torch.full((size,), fill, dtype=torch.uint8, device=DEV)
+        assert torch.equal(b.run(ws=ws), want)
+
+
 def test_prefix_beyond_the_table_is_cut():
     b = Batch(9, 128, 8, 2, [6], [320], [20 + i for i in range(6)], "bf16")
     got = b.run(prefix_lens=[1 << 30], flags=4)          # to the 21 whole pages of the longest sequence, all of the first's
