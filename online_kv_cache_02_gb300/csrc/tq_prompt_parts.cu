@@ -1,9 +1,10 @@
 // Attention over packed prompts on the tensor cores (tcgen05) to fp32's accuracy, d = 64 or 128: fp32 inputs, and bf16 ones
 // that the bf16 form does not take.
 //
-// An fp32 number is the sum of three bf16 ones, its bits 8 at a time (cut off, so that each part and each remainder is exact
-// and no part overflows).  Of the products of two such sums the six largest count: what is left out is below 2^-23 of the
-// product.  Per block of 128 query rows (row r = t G + g) of a KV head and 64 keys:
+// An fp32 number is the sum of three bf16 ones, each the nearest to what the ones before leave (the first no larger than the
+// largest), so that the remainders are exact.  The second and third are at most 2^-8 and 2^-17 of the number's power of two:
+// of the products of two such sums the six largest count, and what is left out is 2^-24 of the product at most, to either side
+// (parts cut off instead of rounded leave out up to 2^-21, always toward zero).  Per block of 128 query rows (row r = t G + g) of a KV head and 64 keys:
 //   S = Q K^T                 six products (bf16 inputs: one), the small ones first: the tensor cores cut a sum instead of
 //                             rounding it, and the large product's few steps are the ones that count
 //   w = 2^(x - M)             fp32, M the running maximum
@@ -85,11 +86,15 @@ __device__ __forceinline__ void load8(const void* p, long long at, float (&x)[8]
   }
 }
 __device__ __forceinline__ bool is_odd(float x) { return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u; }
-// The upper halves of a and b as a pair of bf16, and what they leave.
-__device__ __forceinline__ uint32_t cut_pair(float& a, float& b) {
-  const uint32_t u = __float_as_uint(a), v = __float_as_uint(b), w = prmt(u, v, 0x7632);
-  a = __fsub_rn(a, __uint_as_float(u & 0xFFFF0000u));
-  b = __fsub_rn(b, __uint_as_float(v & 0xFFFF0000u));
+// The next parts of a and b as a pair of bf16, and what they leave.  FIRST: of numbers that may be beyond the largest bf16
+// (infinity is one in the second part then).
+template <bool FIRST>
+__device__ __forceinline__ uint32_t part_pair(float& a, float& b) {
+  uint32_t w;
+  if (FIRST) asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+  a = __fsub_rn(a, __uint_as_float(w << 16));
+  b = __fsub_rn(b, __uint_as_float(w & 0xFFFF0000u));
   return w;
 }
 // 16 bytes of each part at `at`.
@@ -99,7 +104,7 @@ __device__ __forceinline__ void put_parts(uint32_t at, int bytes, float (&x)[8])
   for (int p = 0; p < PARTS; ++p) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = cut_pair(x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) w[i] = p == 0 ? part_pair<PARTS == 3>(x[2 * i], x[2 * i + 1]) : part_pair<false>(x[2 * i], x[2 * i + 1]);
     sts128(at + p * bytes, w[0], w[1], w[2], w[3]);
   }
 }
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_parts_kernel(const __grid_
           for (int i = 0; i < 3; ++i) {
             uint32_t u[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) u[k] = cut_pair(y[c + 2 * k], y[c + 2 * k + 1]);
+            for (int k = 0; k < 16; ++k) u[k] = part_pair<false>(y[c + 2 * k], y[c + 2 * k + 1]);
             tst16(trow + kColP + 32u * i + c / 2, u);
           }
         alphas[kRows * (T % kSlots) + tid] = al;

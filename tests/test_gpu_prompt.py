@@ -362,6 +362,62 @@ def test_sums_of_one_sign(dtype, d, scale):
     attend(dtype, d, 4, 2, [70, 3], [6000, 2500], scale=scale, change=change)
 
 
+def two_keys(d, q, k, v, scale):
+    """Single queries (of many heads) that see two keys each, fp32 on both sides."""
+    s, hq = q.shape[:2]
+    ctx = ctx_for(d)
+    q, k, v = (torch.from_numpy(x).to(DEV) for x in (q, k, v))
+    size = tq.tq_prompt_workspace_size(ctx, s, 1, hq, 1, 2)
+    ws, out = torch.zeros(size, dtype=torch.uint8, device=DEV), torch.empty_like(q)
+    tq.tq_prompt_attention(ctx, q, k, v, tq.TQ_F32, s, ints(range(s + 1)), ints(range(0, 2 * s + 1, 2)), s, 2 * s, 1, 2, hq, 1, 0, 0, scale,
+                           out, ws, size)
+    torch.cuda.synchronize()
+    assert tq.tq_check_device_status(ctx) == 0
+    return out.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp32_products_keep_24_bits(d):
+    """Scores of one product each, of numbers whose parts are as large as parts can be, against a score that is exact: what the
+    two weights show of the difference.  Counted: 2^-24 of the product for what six products of parts leave out, a cut of the
+    sum twice (2^-23), and both scores' scaling (2^-24 each); the exponentials and the rest 2^-20 of the result."""
+    rng = np.random.default_rng(11)
+    s, hq, big = 64, 20, 2.0 ** 13
+    low = [(1 << 16) - 1, 1 << 16, 0x7FFF, 0x8000, 0xFFFF, 0x17FFF, 0x18000, 0x1FFFF, 0xFF7F, 0x7F80]
+    pick = lambda *shape: ((1 << 23) + (rng.integers(0, 64, shape) << 17) * (rng.random(shape) < 0.5) + rng.choice(low, shape)) / 2.0 ** 23  # noqa: E731
+    a, b = pick(s, hq), pick(s, 1)
+    a[:8], b[:8] = 1 + 2.0 ** -7 - 2.0 ** -23, 1 + 2.0 ** -7 - 2.0 ** -23
+    q, k, v = (np.zeros((n, h, d), np.float32) for n, h in ((s, hq), (2 * s, 1), (2 * s, 1)))
+    c = (a * b * big).astype(np.float32)
+    q[:, :, 0], q[:, :, 1] = a * big, c
+    k[::2, 0, 0], k[1::2, 0, 1] = b[:, 0], 1.0
+    v[::2] = 1.0
+    scale = math.log(2.0)
+    f = float(np.float32(scale) * np.float32(1.4426950408889634))
+    got = two_keys(d, q, k, v, scale)
+    apart = f * (a * b * big - c.astype(np.float64))
+    tol = f * a * b * big * (0.5 + 2 + 1) * 2.0 ** -23
+    lo, hi = (1 / (1 + np.exp2(-(apart + x))) for x in (-tol, tol))
+    assert np.all(got >= lo[..., None] * (1 - 2.0 ** -20)) and np.all(got <= hi[..., None] * (1 + 2.0 ** -20))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp32_keys_beyond_the_largest_bf16_number(d):
+    """Finite ones: two scores that are exact and equal, so that the values' mean comes out, and a value that size alone."""
+    most = np.array([0x7F7FFFFF, 0x7F7F8000, 0x7F7F7FFF, 0x7F7FC001], np.uint32).view(np.float32)
+    s, hq = len(most), 20
+    q, k, v = (np.zeros((n, h, d), np.float32) for n, h in ((s, hq), (2 * s, 1), (2 * s, 1)))
+    q[:, :, 0], q[:, :, 1] = 2.0 ** -114, most[:, None] * np.float32(2.0 ** -114)
+    k[::2, 0, 0], k[1::2, 0, 1] = most, 1.0
+    v[::2], v[1::2] = 3.0, 1.0
+    got = two_keys(d, q, k, v, 1.0)
+    assert np.abs(got - 2.0).max() <= 2.0 ** -20
+    v[1::2, 0, :] = np.where(np.arange(d) % 2, most[:, None], -most[:, None])
+    k[::2], k[1::2, 0, 1] = 0.0, 1.0                                # (the other key's weight is nothing)
+    got = two_keys(d, q, k, v, 1.0)
+    assert np.array_equal(got, np.broadcast_to(v[1::2].astype(np.float64), got.shape))
+
+
 @pytest.mark.parametrize("size", [2.0 ** -60, 2.0 ** 60, 2.0 ** 99])
 def test_fp32_sizes(size):
     """Values of any size, queries and keys whose sizes cancel in the scores."""
