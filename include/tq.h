@@ -336,9 +336,9 @@ tq_status tq_dequantize(const tq_ctx* ctx, const void* k_cache, const void* v_ca
  * max_q_len and max_k_len: no sequence has more.  Offsets that fall, pass
  * total_q or total_k, or are further apart set device status bit 4; that
  * sequence's rows stay as they were.  (Around a fall, rows may be in two
- * sequences: they get the results of either, element by element; and the last
- * sequences of a list whose pairs make many more blocks of rows than total_q
- * rows can may be left out.)  Otherwise results do not depend on the run, but in
+ * sequences: they get the results of either, element by element; and where the
+ * pairs make more blocks of rows than one list takes, and than total_q rows can,
+ * the last sequences are left out.)  Otherwise results do not depend on the run, but in
  * their last bits on the other sequences of the call (they share its split).
  * Accuracy: scores and sums in fp32; bf16 weights are rounded to 8 bits (2^-8 of
  * each at most) for the product with the values, fp32 ones not; fp32 products

@@ -276,14 +276,14 @@ cudaError_t launch_t(const PromptArgs& args, bool f32, cudaStream_t s) {
   using L = SG<D, RM>;
   PromptArgs a = args;
   a.rows = L::ROWS;
-  a.most = prompt_list_room(a);
+  a.most = prompt_list_room(a, kTok, kItemCost);
   static std::atomic<unsigned long long> done16{0}, done32{0};
   cudaError_t e = f32 ? smem_attr_once(prompt_simt_kernel<D, true, RM>, L::BYTES, done32)
                       : smem_attr_once(prompt_simt_kernel<D, false, RM>, L::BYTES, done16);
   if (e != cudaSuccess) return e;
   const long long tiles = a.max_k / kTok + 2 + a.sinks / kTok;
   // items of few tiles are not cut (and need no join)
-  const int mode = !prompt_splits(a, kTok, kItemCost) ? kPromptTurns : tiles > 4 ? kPromptCut : kPromptWhole;
+  const int mode = !prompt_splits(a) ? kPromptTurns : tiles > 4 ? kPromptCut : kPromptWhole;
   const int ctas = simt_ctas(D);
   e = f32 ? launch_pdl(prompt_simt_kernel<D, true, RM>, dim3(ctas), dim3(kThreads), L::BYTES, s, a, mode)
           : launch_pdl(prompt_simt_kernel<D, false, RM>, dim3(ctas), dim3(kThreads), L::BYTES, s, a, mode);
@@ -300,11 +300,6 @@ cudaError_t launch_d(const PromptArgs& a, bool f32, cudaStream_t s) {
 }  // namespace
 
 int prompt_sms() { return kv8_sm_count(); }
-
-bool prompt_splits(const PromptArgs& a, int tok, int cost) {
-  const long long blocks = prompt_most_blocks(a);
-  return a.S <= kPromptList && blocks <= kPromptList && blocks * (a.max_k / tok + 2 + a.sinks / tok + cost) <= 0x7FFFFFFFLL;
-}
 
 cudaError_t launch_prompt_join(const PromptArgs& a, int d, bool f32, int ctas, int rows, cudaStream_t s) {
   const dim3 grid(ctas, rows / 8), block(256);

@@ -139,7 +139,7 @@ __device__ PromptSpan prompt_span(const PromptArgs& a, int heads, int min_span, 
   for (int i = 0; i < per && tid * per + i < a.S; ++i) firsts[tid * per + i] += before;
   __syncthreads();
   const int seqs = prompt_taken(firsts, a.S, blocks, a.most);
-  if (seqs < a.S) {                       // more blocks than the rows of the call have: the same rows again
+  if (seqs < a.S) {                       // more blocks than ascending offsets have: the same rows again
     blocks = firsts[seqs];
     if (tid == 0) atomicOr(a.err, kErrSeqLen);
   }
@@ -311,11 +311,8 @@ __device__ __forceinline__ void prompt_zero_rows(const PromptArgs& a, int d) {
 
 // Blocks that a call can have at most (by its sizes alone), and whether they can be listed.
 inline long long prompt_most_blocks(const PromptArgs& a) { return prompt_most_blocks(a.S, a.max_q, a.total_q, a.G, a.rows); }
-bool prompt_splits(const PromptArgs& a, int tok, int cost);
-inline int prompt_list_room(const PromptArgs& a) {
-  const long long most = prompt_most_blocks(a);
-  return most < kPromptList ? static_cast<int>(most) : kPromptList;
-}
+inline int prompt_list_room(const PromptArgs& a, int tok, int cost) { return prompt_list_room(a.max_k / tok + 2LL + a.sinks / tok + cost); }
+inline bool prompt_splits(const PromptArgs& a) { return a.S <= kPromptList && prompt_most_blocks(a) <= a.most; }
 // Workspace of either form (whatever the dtype and scale), its CTAs and its launch.
 size_t prompt_simt_workspace(int d);
 cudaError_t launch_prompt_simt(const PromptArgs& a, int d, bool f32, cudaStream_t s);

@@ -23,10 +23,15 @@ TQ_LIST_FN long long prompt_most_blocks(int S, int max_q, int total_q, int G, in
   const long long each = S * static_cast<long long>(prompt_blocks(max_q, G, rows)), whole = S + static_cast<long long>(total_q) * G / rows;
   return each < whole ? each : whole;
 }
-// In offsets that fall the pairs around the falling one can be the same rows again, as often as there are pairs: the list
-// counts a sequence as one block too many where it has more than `most`, so that no sum passes 31 bits, and takes the
-// sequences from the first on for as long as they have `most` blocks together.  firsts: blocks before each of S sequences;
-// total: of all of them.  With offsets that ascend these are always all S.
+// Blocks that the list takes: its places, and no more than make 31 bits of units, a block taking `units` at most.
+TQ_LIST_FN int prompt_list_room(long long units) {
+  const long long n = 0x7FFFFFFFLL / units;
+  return n < kPromptList ? static_cast<int>(n) : kPromptList;
+}
+// In offsets that fall the pairs around the falling one can be the same rows again, as often as there are pairs, and pass the
+// bound above.  The list counts a sequence as one block too many where it has more than `most` (the list's room), so that no
+// sum passes 31 bits, and takes the sequences from the first on for as long as they have `most` blocks together.  firsts:
+// blocks before each of S sequences; total: of all of them.
 TQ_LIST_FN int prompt_counted(int blocks, int most) { return blocks <= most ? blocks : most + 1; }
 TQ_LIST_FN int prompt_taken(const int* firsts, int S, int total, int most) {
   if (total <= most) return S;

@@ -477,14 +477,14 @@ template <int D, bool F32>
 cudaError_t launch_t(const PromptArgs& args, cudaStream_t s) {
   PromptArgs a = args;
   a.rows = kRows;
-  a.most = prompt_list_room(a);
+  a.most = prompt_list_room(a, kTok, kItemCost);
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = smem_attr_once(prompt_parts_kernel<D, F32>, PB<D, F32>::BYTES, configured);
   if (e != cudaSuccess) return e;
   const long long items = prompt_most_blocks(a) * a.H, tiles = a.max_k / kTok + 2 + a.sinks / kTok;
   const int sms = prompt_sms();
   // items of few tiles are not cut (and need no join)
-  const int mode = !prompt_splits(a, kTok, kItemCost) ? kPromptTurns : tiles > 4 ? kPromptCut : kPromptWhole;
+  const int mode = !prompt_splits(a) ? kPromptTurns : tiles > 4 ? kPromptCut : kPromptWhole;
   const long long most = mode == kPromptCut ? (items * (tiles + kItemCost) + kMinSpan - 1) / kMinSpan : items;
   const int ctas = static_cast<int>(most < sms ? (most < 1 ? 1 : most) : sms);
   e = launch_pdl(prompt_parts_kernel<D, F32>, dim3(ctas), dim3(kThreads), PB<D, F32>::BYTES, s, a, mode);

@@ -947,7 +947,7 @@ cudaError_t launch_t(const PromptArgs& args, cudaStream_t s) {
   PromptArgs a = args;
   const int tokens = 128 / a.G;                        // of a half
   a.rows = L::HALVES * tokens * a.G;
-  a.most = prompt_list_room(a);
+  a.most = prompt_list_room(a, kTok, kItemCost);
   CUtensorMap mq, mk, mv;
   if (!rows_map(&mq, a.q, D, a.Hq, a.total_q, a.qs, a.G, tokens) || !rows_map(&mk, a.k, D, a.H, a.total_k, a.ks, 1, kTok) ||
       !rows_map(&mv, a.v, D, a.H, a.total_k, a.vs, 1, L::VTOK))
@@ -959,7 +959,7 @@ cudaError_t launch_t(const PromptArgs& args, cudaStream_t s) {
   // items of few tiles are not cut (and need no join)
   // (nor are few of them listed: the list takes 4 us)
   const int sms = prompt_sms();
-  const int mode = !prompt_splits(a, kTok, kItemCost) || (tiles <= 4 && items <= sms) ? kPromptTurns : tiles > 4 ? kPromptCut : kPromptWhole;
+  const int mode = !prompt_splits(a) || (tiles <= 4 && items <= sms) ? kPromptTurns : tiles > 4 ? kPromptCut : kPromptWhole;
   const long long most = mode == kPromptCut ? (items * (tiles + kItemCost) + kMinSpan - 1) / kMinSpan : items;
   const int ctas = static_cast<int>(most < sms ? (most < 1 ? 1 : most) : sms);
   e = launch_pdl(prompt_tc_kernel<D>, dim3(ctas), dim3(kThreads), PS<D>::BYTES, s, a, mq, mk, mv, mode);

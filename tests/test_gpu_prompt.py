@@ -512,6 +512,32 @@ def test_offsets_that_fall_behind_many_blocks(dtype, d, scale, rows):
     assert not bool((out[:n] == -7).all(-1).any()) and bool((out[n:] == -7).all())
 
 
+@pytest.mark.parametrize("dtype,d,scale,rows", FORMS)
+@pytest.mark.parametrize("cu_q,cu_k,max_q,max_k,left", [
+    ([0, 600, 400, 2000], [0, 600, 1500, 2000], 2000, 2000, [1]),             # falls: rows 400 .. 599 are the third sequence's, too
+    ([0, 600, 1500, 2001], [0, 600, 1500, 2000], 2000, 2000, [2]),
+    ([0, 600, 1500, 2000], [0, 600, 1500, 1 << 30], 2000, 2000, [2]),
+    ([-5, 600, 1500, 2000], [0, 600, 1500, 2000], 2000, 2000, [0]),
+    ([0, 600, 1500, 2000], [-(1 << 31), 600, 1500, 2000], 2000, 2000, [0]),
+    ([0, 600, 1500, 2000], [0, 600, 300, 2000], 2000, 2000, [1]),
+    ([0, 600, 1500, 2000], [0, 600, 1500, 2000], 700, 2000, [1]),
+    ([0, 600, 1500, 2000], [0, 600, 1500, 2000], 2000, 599, [0, 1]),
+    ([3000, 2000, 1000, -7], [0, 600, 1500, 2000], 2000, 2000, [0, 1, 2])])
+def test_offsets_that_are_none_among_cut_items(dtype, d, scale, rows, cu_q, cu_k, max_q, max_k, left):
+    """Lists that are cut into spans: what is no sequence is left as it was, the others are right."""
+    q, k, v, out = by_offsets(dtype, d, scale, cu_q, cu_k, 2000, 4, 2, max_q, max_k, seed=3)
+    taken = [(cu_q[s], cu_q[s + 1], cu_k[s], cu_k[s + 1]) for s in range(3) if s not in left]
+    owners = torch.zeros(2000, dtype=torch.int32, device=DEV)
+    for a, b, *_ in taken:
+        owners[a:b] += 1
+    for a, b, c, e in taken:
+        want, bound = reference(q[a:b].double(), k[c:e].double(), v[c:e].double(), 0, 0, 1 / math.sqrt(d) if scale is None else scale,
+                                2.0 ** -8 if dtype == "bf16" else 0.0)
+        bound = bound + torch.finfo(out.dtype).eps / 2 * (want.abs() + bound)
+        assert bool(((out[a:b].double() - want).abs() <= bound)[owners[a:b] == 1].all())
+    assert bool((out[owners == 0] == -7).all())
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 128)])
 def test_results_repeat_bit_for_bit(dtype, d):
     outs = [attend(dtype, d, 8, 2, [300, 1, 45], [1300, 2000, 45], repeat=3) for _ in range(4)]

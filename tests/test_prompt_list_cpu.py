@@ -35,14 +35,14 @@ struct Count {
   }
 
 // As the host and then each block of the kernels count.
-Count count(const std::vector<int>& cu, int total, int max_q, int G, int rows) {
+Count count(const std::vector<int>& cu, int total, int max_q, int G, int rows, long long units = 100) {
   const int S = static_cast<int>(cu.size()) - 1;
   Count c{};
   max_q = std::min(max_q, total);
   const long long bound = prompt_most_blocks(S, max_q, total, G, rows);
-  c.lists = S <= kPromptList && bound <= kPromptList;
+  const int most = prompt_list_room(units);
+  c.lists = S <= kPromptList && bound <= most;
   if (!c.lists) return c;
-  const int most = static_cast<int>(bound);
   std::vector<int> firsts(S), exact(S);
   long long sum = 0;
   bool ascends = true;
@@ -59,7 +59,7 @@ Count count(const std::vector<int>& cu, int total, int max_q, int G, int rows) {
   c.taken = prompt_taken(firsts.data(), S, static_cast<int>(sum), most);
   NEED(c.taken >= 0 && c.taken <= S);
   c.blocks = c.taken < S ? firsts[c.taken] : static_cast<int>(sum);
-  NEED(c.blocks <= most && c.blocks <= kPromptList);                    // places in the list
+  NEED(c.blocks <= kPromptList && c.blocks * units <= INT_MAX);         // places in the list, and their units
   long long listed = 0;
   for (int s = 0; s < c.taken; ++s) {
     NEED(firsts[s] == listed);                                          // as they are without the limit
@@ -103,7 +103,7 @@ int main() {
     if (kind == 2)
       for (int& x : cu)
         if (rng() % 8 == 0) x = static_cast<int>(rng());
-    const Count c = count(cu, total, max_q, G, rows);
+    const Count c = count(cu, total, max_q, G, rows, 5 + rng() % (1 << rng() % 24));
     listed += c.lists;
     cut += c.lists && c.taken < S;
   }
