@@ -36,7 +36,7 @@ __device__ __forceinline__ ReadRun read_run(const ReadArgs& a, int b) {
     n = n < 0 || start < 0 || row < 0 ? 0 : a.max_len;
   }
   const long long room = static_cast<long long>(kPage) * a.maxp - start;
-  if (n > room) {
+  if (n > 0 && n > room) {                            // (nothing is read of a start beyond the table with a length of 0)
     bad |= kErrBlock;
     n = room > 0 ? static_cast<int>(room) : 0;
   }

@@ -324,6 +324,24 @@ def test_kv8_what_is_out_of_range_is_skipped_and_flagged():
     tq.tq_destroy(ctx)
 
 
+@pytest.mark.parametrize("eight", [False, True])
+def test_a_length_of_zero_reads_nothing_wherever_it_starts(eight):
+    """(A negative start is flagged all the same.)"""
+    rng = np.random.default_rng(10)
+    for starts, flags in (([1 << 20, 3], 0), ([81, 3], 0), ([2 ** 31 - 1, 3], 0), ([-1, 3], 4)):
+        if eight:
+            ctx = tq.tq_create(128, 3, 128, 0)
+            cache = _kv8(rng, 128, 2, 20, 2, 5)[3]
+            out = _kv8_read(ctx, cache, "f32", 2, 128, starts, [0, 5], [0, 0], 5, 5, flags=flags)
+            assert not bool((out["k"][:5] == -7).any()) and bool((out["k"][5:] == -7).all())
+        else:
+            ctx, p = config(128, (4, 3), (4, 3))
+            pool = Pool(rng, ctx, p, 2, 20, 2, 5)
+            out, first = read(ctx, pool, "f32", starts, [0, 5], flags=flags)
+            check(pool, "f32", out, starts, [0, 5], first)
+        tq.tq_destroy(ctx)
+
+
 def test_reads_beyond_32_bit_offsets():
     """Pages and rows whose elements lie beyond 2^31."""
     d, h, pages = 128, 8, (1 << 17) + 999
