@@ -259,6 +259,24 @@ def test_scores_of_rows_that_were_read_are_the_decodes(d, bits):
     tq.tq_destroy(ctx)
 
 
+@pytest.mark.parametrize("d,m,k_bits,v_bits,qjl", [(128, 128, (4, 3), (4, 3), True), (128, 128, (3, 3), (2, 2), True), (128, 128, (4, 4), (1, 1), False),
+                                                   (64, 64, (4, 3), (3, 2), True), (128, 64, (4, 3), (4, 3), True), (256, 128, (3, 3), (4, 3), True)])
+def test_bf16_rows_within_the_stated_bounds(d, m, k_bits, v_bits, qjl):
+    """2^-8 of the root of the terms' squares and 2^-8 of the element where fp16 tables form them (d = m = 128), elsewhere the
+    fp32 rows' bound and half a step of bf16."""
+    ctx, p = config(d, k_bits, v_bits, m=m, qjl=qjl)
+    pool = Pool(np.random.default_rng(14), ctx, p, 3, 60, 2, 30)
+    lens, h = [470, 333], 3
+    out, first = read(ctx, pool, "bf16", [0, 5], lens)
+    for kind in "kv":
+        got = out[kind].double().cpu().numpy()
+        for b, (s, n, f) in enumerate(zip([0, 5], lens, first)):
+            want, root = pool.values(kind, b, range(s, s + n))
+            over = (np.abs(got[f:f + n].reshape(n, h, d) - want)) / (root * (2.0 ** -8 if d == m == 128 else 2.0 ** -19) + 2.0 ** -8 * np.abs(want) + 1e-30)
+            assert float(over.max()) <= 1.0, (kind, float(over.max()))
+    tq.tq_destroy(ctx)
+
+
 # ---------------------------------------------------------------------------
 # the 8-bit cache
 # ---------------------------------------------------------------------------
