@@ -4,7 +4,8 @@
 // An fp32 number is the sum of three bf16 ones, each the nearest to what the ones before leave (the first no larger than the
 // largest), so that the remainders are exact.  The second and third are at most 2^-8 and 2^-17 of the number's power of two:
 // of the products of two such sums the six largest count, and what is left out is 2^-24 of the product at most, to either side
-// (parts cut off instead of rounded leave out up to 2^-21, always toward zero).  Per block of 128 query rows (row r = t G + g) of a KV head and 64 keys:
+// (parts cut off instead of rounded leave out up to 2^-21, always toward zero).  Per block of 128 query rows (row r = t G + g)
+// of a KV head and 64 keys:
 //   S = Q K^T                 six products (bf16 inputs: one), the small ones first: the tensor cores cut a sum instead of
 //                             rounding it, and the large product's few steps are the ones that count
 //   w = 2^(x - M)             fp32, M the running maximum
@@ -16,10 +17,13 @@
 // both: queries; 16: MMA issue, a tile's scores ahead of the values before.  Every warp walks the list of items by itself.
 // Every wait is bounded; a wait that gives up sets the device error word.
 //
-// Bound by shared memory (480 KB a tile, of which the scores' products read the queries 48 times: 2.1 us at 128 B a cycle;
-// the MMAs by themselves 1.7) and by the chain from rows in memory to parts, scores, weights and products: 3.9 us a tile.
-// Two thousand tokens, 32 / 8 heads, d = 128, fp32: 257 us (134 TFLOP/s; CUDA cores 1,076), three prompts of up to 1,111 tokens
-// 90 (293).  Slower were 16 warps for keys and values (274) and both at once by eight (356), fewer pieces in flight (279).
+// Bound by the chain from rows in memory to parts, scores, weights and products: 3.9 us a tile, of which the MMAs take 1.7 and
+// their operands 2.1 of shared memory by arithmetic (480 KB, the queries being read 48 times, at 128 B a cycle).  By counters
+// (three prompts of up to 1,111 tokens) no unit is busy for more than a third of the time: issue slots 37%, integer pipe 34%,
+// tensor pipe 27%; 6.6 stalls an issue wait for loads.
+// Two thousand tokens, 32 / 8 heads, fp32: d = 128 256 us (134 TFLOP/s; CUDA cores 1,076), d = 64 172; three prompts of up to
+// 1,111 tokens 96 (293); eight single tokens behind 4,000 keys 126 (their bytes take 38).  Slower were 16 warps for keys and
+// values (274) and both at once by eight (356), fewer pieces in flight (279).
 
 #include "tq_kv8.h"
 #include "tq_prompt.h"
@@ -495,7 +499,7 @@ cudaError_t launch_t(const PromptArgs& args, cudaStream_t s) {
 }  // namespace
 
 // All sizes but a tile of keys for a few rows, which is latency alone (4 tokens, 4 heads per KV head: 14 us, CUDA cores 11);
-// from there on this form is ahead (5 tokens 14 us against 17; eight single tokens behind 4,000 keys 130 against 230, fp32).
+// from there on this form is ahead (5 tokens 14 us against 17; eight single tokens behind 4,000 keys 126 against 230, fp32).
 bool prompt_parts_takes(const PromptArgs& a, int d) {
   return (d == 64 || d == 128) && (a.max_k > kTok || static_cast<long long>(a.max_q) * a.G > 16);
 }

@@ -28,9 +28,10 @@
 //
 // What bounds it: a key tile's 2 x 128 rows take 1,024 cycles of the tensor cores at d = 128 (512 at 64) and 1,024 of the
 // exponentials (32 lanes a cycle and SM), which two halves overlap as far as a half's own chain lets them: scores, softmax,
-// weights, values, one behind the other.  A prompt of 8,192 tokens, 32 / 8 heads: d = 128 330 us (1,670 TFLOP/s, tensor
-// pipe 78% of the cycles by its counter), d = 64 256 us (tensor pipe and exponentials 48% each, issue slots 48%), d = 256
-// (16 / 4 heads) 355 us.  Two dozen prompts of up to 2,500 tokens 310 to 340 us, of which the ends of 1,500 items and the join.
+// weights, values, one behind the other.  A prompt of 8,192 tokens, 32 / 8 heads: d = 128 330 us in a burst (1,670 TFLOP/s,
+// tensor pipe 78% of the cycles by its counter) and 363 in a long series, where power lowers the clock (1,515), d = 64 256 us
+// (tensor pipe and exponentials 48% each, issue slots 48%), d = 256 (16 / 4 heads) 355 us.  Two dozen prompts of up to 2,500
+// tokens 329 to 343 us, of which the ends of 3,408 items and the join.
 // Slower were an O of its own for each half at d = 256 (every score twice: 552 us) and the softmax in two parts of 64 keys
 // (less code, d = 128: 397 us).
 
@@ -53,7 +54,9 @@ using namespace tcx;
 constexpr int kTok = 128;                 // keys per tile
 constexpr int kThreads = 512;
 constexpr int kItems = 4;                 // items announced ahead
-constexpr int kItemCost = 3;              // an item's start and end, in tiles' time
+// An item's start and end, in tiles' time.  1, 2, 3, 4: windows of 1,024 at d = 64 133, 129, 128, 130 us, chunks at d = 256 275,
+// 276, 277, 279, two dozen prompts at d = 128 334, 333, 342, 341.
+constexpr int kItemCost = 3;
 constexpr int kMinSpan = 2 + kItemCost;   // a CTA's share of the list at least
 constexpr float kFull = 16777216.0f, kTiny = 5.9604645e-8f;       // 2^24 and 2^-24: bounds of a row's sum
 // x - M in one rounding is off by half a step of M against the other tiles' M: beyond 2^16 scores are rounded first, so that
@@ -735,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // halves (left to mix, both halves' MMAs would end together and neither softmax overlap the other).  Between a
       // softmax's end and its next scores stands what this warp executes in between, so that few instructions count: with
       // a loop per kind of item, a queue in registers and rings by division a d = 64 prompt of 8,192 took 279 us, not 256,
-      // and two dozen d = 128 prompts 341, not 309 -------------------------------------------------------------------------
+      // and two dozen d = 128 prompts 341, not 309 (in a burst) -------------------------------------------------------------------------
       auto ready = [&](int i, int phase) {             // wait() in few instructions
         if (__all_sync(0xffffffffu, wait_short(bar(i), phase & 1))) return true;
         failed = true;

@@ -15,10 +15,11 @@
 // sets the device error word.
 //
 // Bound by the operands' making, then by the rows' stores.  Eight sequences of 16,384 tokens, 8 heads, 3.5-bit keys and
-// values into bf16 rows: 150 us (4.5 TB/s of rows and records; on CUDA cores 4,340), 8,192 tokens each into fp32 rows 150.
+// values into bf16 rows: 150 us (4.5 TB/s of rows and records; on CUDA cores 4,340), 8,192 tokens each into fp32 rows 150.  By
+// counters: integer pipe 63% and issue slots 64% of the cycles (the operands), shared memory 52%, DRAM 51%, tensor pipe 29%.
 // Left operands through shared memory took its bandwidth from the tables; rows by bulk copies of a lane each took 2,600
-// cycles to issue.  Some dozen pages a sequence: 17 us, most of them the tables' way into shared memory (on CUDA cores
-// 72).
+// cycles to issue.  Some dozen pages a sequence: 17 us (on CUDA cores 72): the tables' way into shared memory and the list of pages
+// (5.5 stalls an issue at barriers), ahead of a tile or two a CTA.
 
 #include "tq_read.h"
 #include "tq_tc.cuh"
