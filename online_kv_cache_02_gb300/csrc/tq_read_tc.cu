@@ -8,7 +8,9 @@
 // bf16 rows take the fp16 tables (2^-11 of each factor, half a step of bf16 being 2^-8), and both products one sum: a row's
 // larger factor is applied at the end, the other operand is scaled by their ratio.  fp32 rows take centroids and tables in
 // two fp16 parts each; the two products are summed apart, the small parts ahead of the large ones, since the tensor cores
-// cut a sum instead of rounding it.  Rows leave through shared memory, so that a store takes whole lines.
+// cut a sum instead of rounding it: by up to 2^-23 of what it is at each of the large product's eight steps, 2^-20 of an element
+// (2-bit values whose elements are four times the root of their terms' squares are off by 1.3 times 2^-19 of that root, all toward
+// zero).  Rows leave through shared memory, so that a store takes whole lines.
 //
 // Warps 0-15: the operands, in two groups that take the tiles in turn (thread = vector and half of its channels); 16-19: the
 // rows (thread = vector); 20: blocks of records by bulk copies; 21: MMA issue.  Every wait is bounded; a wait that gives up

@@ -277,6 +277,25 @@ def test_bf16_rows_within_the_stated_bounds(d, m, k_bits, v_bits, qjl):
     tq.tq_destroy(ctx)
 
 
+@pytest.mark.parametrize("k_bits,v_bits,split", [((3, 3), (2, 2), 0), ((4, 3), (3, 2), 64), ((4, 4), (1, 1), 64)])
+def test_fp32_rows_within_the_stated_bounds(k_bits, v_bits, split):
+    """Half a million elements, some of them several times the root of their terms' squares: 2^-19 of that root, and 2^-20 of the
+    element for the tensor cores' cut sums."""
+    ctx, p = config(128, k_bits, v_bits, split=split)
+    pool = Pool(np.random.default_rng(5), ctx, p, 8, 42, 2, 20)
+    out, first = read(ctx, pool, "f32", [0, 0], [320, 320])
+    most = 0.0
+    for kind in "kv":
+        got = out[kind].double().cpu().numpy()
+        for b in range(2):
+            want, root = pool.values(kind, b, range(320))
+            most = max(most, float((np.abs(want) / (root + 1e-30)).max()))
+            tol = root * 2.0 ** -19 + np.abs(want) * (2.0 ** -20 + 2.0 ** -24)
+            assert np.all(np.abs(got[first[b]:first[b] + 320].reshape(want.shape) - want) <= tol), kind
+    assert most > 3.5
+    tq.tq_destroy(ctx)
+
+
 # ---------------------------------------------------------------------------
 # the 8-bit cache
 # ---------------------------------------------------------------------------
